@@ -22,13 +22,17 @@ CLO_DEC_HIT, CLO_DEC_MISS, CLO_DEC_PERSIST = 0, 1, 2
  CLO_DBG_STEP_BYTES) = range(1, 14)
 STEP_HIST = 4096
 CLO_SET_DROP_FLAG_LAYER, CLO_SET_WAIT_TIMEOUT_NS = 1, 2
+CLO_ROPE_SCALING = {"none": 0, "linear": 1, "bands": 2, "yarn": 3}
+CLO_ROPE_MAX_PAIRS = 64
 
 _STATUS_NAMES = {0: "CLO_OK", 1: "CLO_ERR_INVALID", 2: "CLO_ERR_OOM", 3: "CLO_ERR_CUDA", 4: "CLO_ERR_TIMEOUT",
                  5: "CLO_ERR_STATE", 6: "CLO_ERR_CAPACITY", 7: "CLO_ERR_DEVICE"}
 
 EXPORTED = ["clo_config_default", "clo_init", "clo_destroy", "clo_append_kv", "clo_append_step", "clo_decode_step",
             "clo_decode_layer",
-            "clo_sync", "clo_stats", "clo_last_error", "clo_debug_get", "clo_set", "clo_sparse_attention_noalloc"]
+            "clo_sync", "clo_stats", "clo_last_error", "clo_debug_get", "clo_set", "clo_sparse_attention_noalloc",
+            "clo_rope_config_default", "clo_rope_plan_init", "clo_rope", "clo_paged_append", "clo_paged_read",
+            "clo_paged_attention"]
 
 
 class CLOError(RuntimeError):
@@ -75,6 +79,49 @@ class clo_stats_t(ctypes.Structure):
         return {n: getattr(self, n) for n, _ in self._fields_}
 
 
+class clo_rope_config(ctypes.Structure):
+    _fields_ = [
+        ("rot_dim", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("theta", ctypes.c_double),
+        ("scaling", ctypes.c_int32),
+        ("factor", ctypes.c_double),
+        ("low_freq", ctypes.c_double),
+        ("high_freq", ctypes.c_double),
+        ("beta_fast", ctypes.c_double),
+        ("beta_slow", ctypes.c_double),
+        ("original_max", ctypes.c_int64),
+        ("magnitude", ctypes.c_double),
+    ]
+
+
+class clo_rope_plan(ctypes.Structure):
+    _fields_ = [
+        ("turn", ctypes.c_uint64 * CLO_ROPE_MAX_PAIRS),
+        ("magnitude", ctypes.c_float),
+        ("rot_dim", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("ready", ctypes.c_int32),
+    ]
+
+
+class clo_rows(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("stride_token", ctypes.c_int64), ("stride_head", ctypes.c_int64)]
+
+
+class clo_paged_cache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_pages", "v_pages", "k_scales", "v_scales")] + \
+        [(n, ctypes.c_int64) for n in ("n_pages", "k_stride_page", "k_stride_head", "k_stride_token", "v_stride_page",
+                                       "v_stride_head", "v_stride_token")] + \
+        [(n, ctypes.c_int32) for n in ("n_kv_heads", "head_dim", "page_size", "kv_bits")]
+
+
+class clo_paged_batch(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q_starts", "kv_lens", "block_table")] + \
+        [("table_stride", ctypes.c_int64)] + \
+        [(n, ctypes.c_int32) for n in ("max_pages", "batch", "total_q", "max_q")]
+
+
 _lib = None
 
 
@@ -113,6 +160,18 @@ def load_library(path: str = LIB_PATH):
     lib.clo_set.argtypes = [vp, i32, i64]
     lib.clo_sparse_attention_noalloc.restype = ctypes.c_int
     lib.clo_sparse_attention_noalloc.argtypes = [vp, vp, vp, i32, i32, i32, i64, vp]
+    lib.clo_rope_config_default.restype = None
+    lib.clo_rope_config_default.argtypes = [vp]
+    lib.clo_rope_plan_init.restype = ctypes.c_int
+    lib.clo_rope_plan_init.argtypes = [vp, vp]
+    lib.clo_rope.restype = ctypes.c_int
+    lib.clo_rope.argtypes = [vp, vp, vp, vp, i64, i32, i32, i32, vp]
+    lib.clo_paged_append.restype = ctypes.c_int
+    lib.clo_paged_append.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, vp]
+    lib.clo_paged_read.restype = ctypes.c_int
+    lib.clo_paged_read.argtypes = [vp, vp, vp, vp, vp]
+    lib.clo_paged_attention.restype = ctypes.c_int
+    lib.clo_paged_attention.argtypes = [vp, vp, vp, vp, i32, ctypes.c_float, i32, i32, vp]
     _lib = lib
     return lib
 
@@ -236,6 +295,262 @@ def clo_sparse_attention_noalloc(q, rows, out, n_groups: int, group_size: int, h
     op, _ = _ptr(out)
     _check(load_library().clo_sparse_attention_noalloc(qp, rp, op, int(n_groups), int(group_size), int(head_dim),
                                                        int(k), stream), "clo_sparse_attention_noalloc")
+
+
+# ----------------------------------------------------------------------------- rotary positions, paged cache
+def clo_rope_config_default() -> clo_rope_config:
+    cfg = clo_rope_config()
+    load_library().clo_rope_config_default(ctypes.byref(cfg))
+    return cfg
+
+
+def clo_rope_plan_init(cfg: clo_rope_config | None = None, **fields) -> clo_rope_plan:
+    """Plan of a rotation: from a config, or from its fields (scaling by name: "none", "linear",
+    "bands", "yarn").  The plan holds plain values and may serve any number of calls."""
+    if cfg is None:
+        cfg = clo_rope_config_default()
+        for name, value in fields.items():
+            if name not in _ROPE_FIELDS:
+                raise TypeError(f"clo_rope_config has no field {name!r}")
+            if name == "scaling" and isinstance(value, str):
+                if value not in CLO_ROPE_SCALING:
+                    raise ValueError(f"unknown scaling {value!r}; known: {sorted(CLO_ROPE_SCALING)}")
+                value = CLO_ROPE_SCALING[value]
+            setattr(cfg, name, int(value) if name == "interleaved" else value)
+    plan = clo_rope_plan()
+    _check(load_library().clo_rope_plan_init(ctypes.byref(cfg), ctypes.byref(plan)), "clo_rope_plan_init")
+    return plan
+
+
+_ROPE_FIELDS = {n for n, _ in clo_rope_config._fields_}
+
+
+def _device_of(t, name: str) -> int:
+    """Index of the current device, after checking that t is a tensor on it."""
+    import torch
+
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    dev = torch.cuda.current_device()
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on the current device")
+    return dev
+
+
+def _rows(t, name: str, dev: int, shape=None) -> clo_rows:
+    """A bf16 [n_tokens][n_heads][head_dim] tensor (any strides but the last) as the library takes it."""
+    import torch
+
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on the current device")
+    if t.dtype is not torch.bfloat16:
+        raise ValueError(f"{name} has dtype {t.dtype}; expected torch.bfloat16")
+    if t.dim() != 3 or (shape is not None and tuple(t.shape) != shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}; expected {shape or '[n_tokens][n_heads][head_dim]'}")
+    st, sh, sd = t.stride()
+    if sd != 1 and t.shape[2] > 1:
+        raise ValueError(f"{name} must be contiguous along head_dim")
+    return clo_rows(t.data_ptr(), st, sh)
+
+
+def _refuse_folded(t, name: str) -> None:
+    """Refuses an output whose rows lie on one another (expanded tensors)."""
+    if any(st == 0 and n > 1 for st, n in zip(t.stride(), t.shape)):
+        raise ValueError(f"{name} is written and must not be an expanded tensor")
+
+
+def _index(t, name: str, dev: int, dtype, numel=None):
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on the current device")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}; expected {dtype}")
+    if t.dim() != 1 or not t.is_contiguous() or (numel is not None and t.numel() != numel):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}; expected a contiguous vector of {numel}")
+    return t.data_ptr()
+
+
+def _stream_of(stream, dev: int):
+    """A stream's handle; None is torch's current stream, an integer is passed through."""
+    import torch
+
+    if stream is None:
+        return torch.cuda.current_stream(dev).cuda_stream
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def clo_rope(plan: clo_rope_plan, x, positions, out=None, transpose: bool = False, stream=None):
+    """Rotates bf16 rows [n_tokens][n_heads][head_dim] by int64 positions [n_tokens] (see include/clo.h).
+
+    out: rows of the same shape, x itself for in place, or None for new ones.  transpose applies the
+    transposed rotation, which takes the gradient of the output to that of x.  Returns out."""
+    import torch
+
+    dev = _device_of(x, "x")
+    xr = _rows(x, "x", dev)
+    if out is None:
+        out = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+    else:
+        _refuse_folded(out, "out")
+    yr = _rows(out, "out", dev, tuple(x.shape))
+    n, h, d = x.shape
+    pp = _index(positions, "positions", dev, torch.int64, n)
+    _check(load_library().clo_rope(ctypes.byref(plan), ctypes.byref(xr), ctypes.byref(yr), pp, n, h, d, int(bool(transpose)),
+                                   _stream_of(stream, dev)), "clo_rope")
+    return out
+
+
+class PagedCache:
+    """K/V pages in HBM (see include/clo.h): the caller's tensors, and the calls on them.
+
+    k_pages, v_pages: [n_pages][n_kv_heads][page_size][head_dim], bf16 or float8_e4m3fn, any strides that are
+    multiples of 16 bytes with head_dim contiguous (pages laid out token by token: pass
+    ``pages.transpose(1, 2)``).  8-bit pages come with contiguous fp32 scales [n_pages][n_kv_heads].
+
+    The calls take the batch as q_starts int32 [batch + 1], kv_lens int32 [batch] (the call's tokens included)
+    and block_table int32 [batch][max_pages]; max_q is the most rows that a sequence has (default: all
+    rows of the call, which is right for one sequence; a step of single tokens passes 1).  stream None is
+    torch's current stream."""
+
+    def __init__(self, k_pages, v_pages, k_scales=None, v_scales=None):
+        import torch
+
+        self.device = _device_of(k_pages, "k_pages")
+        _device_of(v_pages, "v_pages")
+        if k_pages.dtype not in (torch.bfloat16, torch.float8_e4m3fn) or v_pages.dtype is not k_pages.dtype:
+            raise ValueError(f"pages have dtypes {k_pages.dtype}, {v_pages.dtype}; expected bfloat16 or float8_e4m3fn for both")
+        if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
+            raise ValueError(f"pages have shapes {tuple(k_pages.shape)}, {tuple(v_pages.shape)}; expected "
+                             "[n_pages][n_kv_heads][page_size][head_dim] for both")
+        if k_pages.stride(3) != 1 or v_pages.stride(3) != 1:
+            raise ValueError("pages must be contiguous along head_dim")
+        n, h, s, d = k_pages.shape
+        bits = 16 if k_pages.dtype is torch.bfloat16 else 8
+        for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
+            if (t is None) != (bits == 16):
+                raise ValueError("8-bit pages come with k_scales and v_scales, bf16 pages without")
+            if t is not None:
+                _device_of(t, name)
+                if t.dtype is not torch.float32 or tuple(t.shape) != (n, h) or not t.is_contiguous():
+                    raise ValueError(f"{name} must be a contiguous fp32 tensor of shape {(n, h)}")
+        self.k_pages, self.v_pages, self.k_scales, self.v_scales = k_pages, v_pages, k_scales, v_scales
+        self.n_pages, self.n_kv_heads, self.page_size, self.head_dim, self.kv_bits = n, h, s, d, bits
+        self._c = clo_paged_cache(k_pages.data_ptr(), v_pages.data_ptr(), None if k_scales is None else k_scales.data_ptr(),
+                                  None if v_scales is None else v_scales.data_ptr(), n, *k_pages.stride()[:3],
+                                  *v_pages.stride()[:3], h, d, s, bits)
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def create(cls, n_pages: int, n_kv_heads: int, page_size: int, head_dim: int, kv_bits: int = 16, device=None):
+        """A cache of new pages (their contents are undefined until they are appended to)."""
+        import torch
+
+        if kv_bits not in (16, 8):
+            raise ValueError("kv_bits must be 16 or 8")
+        device = torch.device("cuda", torch.cuda.current_device()) if device is None else device
+        shape = (n_pages, n_kv_heads, page_size, head_dim)
+        if kv_bits == 16:
+            return cls(*(torch.empty(shape, dtype=torch.bfloat16, device=device) for _ in range(2)))
+        return cls(*(torch.empty(shape, dtype=torch.float8_e4m3fn, device=device) for _ in range(2)),
+                   *(torch.ones((n_pages, n_kv_heads), dtype=torch.float32, device=device) for _ in range(2)))
+
+    def _batch(self, dev, q_starts, kv_lens, block_table, total: int, max_q) -> clo_paged_batch:
+        import torch
+
+        if dev != self.device:
+            raise ValueError(f"the cache is on device {self.device}, the call's rows on {dev}")
+        batch = kv_lens.shape[0]
+        if block_table.get_device() != dev or block_table.dtype is not torch.int32 or block_table.dim() != 2 or \
+                block_table.shape[0] != batch or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+            raise ValueError(f"block_table must be an int32 CUDA tensor [{batch}][max_pages] on the current device with "
+                             "contiguous rows")
+        return clo_paged_batch(_index(q_starts, "q_starts", dev, torch.int32, batch + 1),
+                               _index(kv_lens, "kv_lens", dev, torch.int32, batch), block_table.data_ptr(),
+                               block_table.stride(0), block_table.shape[1], batch, total, total if max_q is None else max_q)
+
+    def append(self, k, v, q_starts, kv_lens, block_table, rope: clo_rope_plan | None = None, positions=None, q=None,
+               q_out=None, max_q=None, stream=None):
+        """clo_paged_append: k, v bf16 [total][n_kv_heads][head_dim] into the pages, k rotated by rope; with
+        q, returns the rotated queries (q_out, or new rows)."""
+        import torch
+
+        dev = _device_of(k, "k")
+        total = k.shape[0]
+        kr = _rows(k, "k", dev, (total, self.n_kv_heads, self.head_dim))
+        vr = _rows(v, "v", dev, (total, self.n_kv_heads, self.head_dim))
+        b = self._batch(dev, q_starts, kv_lens, block_table, total, max_q)
+        qr = yr = None
+        heads = 0
+        if q is not None:
+            if q.dim() != 3:
+                raise ValueError("q must be [total][n_q_heads][head_dim]")
+            heads = q.shape[1]
+            if q_out is None:
+                q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+            else:
+                _refuse_folded(q_out, "q_out")
+            qr = ctypes.byref(_rows(q, "q", dev, (total, heads, self.head_dim)))
+            yr = ctypes.byref(_rows(q_out, "q_out", dev, (total, heads, self.head_dim)))
+        elif q_out is not None:
+            raise ValueError("q_out without q")
+        _check(load_library().clo_paged_append(
+            self._ref, ctypes.byref(b), None if rope is None else ctypes.byref(rope),
+            None if positions is None else _index(positions, "positions", dev, torch.int64, total), ctypes.byref(kr),
+            ctypes.byref(vr), qr, yr, heads, _stream_of(stream, dev)), "clo_paged_append")
+        return q_out
+
+    def read(self, q_starts, kv_lens, block_table, total: int, k_out=None, v_out=None, max_q=None, stream=None):
+        """clo_paged_read: the batch's last tokens as bf16 (k, v), each [total][n_kv_heads][head_dim]."""
+        import torch
+
+        dev = _device_of(kv_lens, "kv_lens")
+        shape = (int(total), self.n_kv_heads, self.head_dim)
+        outs = []
+        for name, t in (("k_out", k_out), ("v_out", v_out)):
+            if t is None:
+                t = torch.empty(shape, dtype=torch.bfloat16, device=kv_lens.device)
+            else:
+                _refuse_folded(t, name)
+            outs.append((t, _rows(t, name, dev, shape)))
+        b = self._batch(dev, q_starts, kv_lens, block_table, int(total), max_q)
+        _check(load_library().clo_paged_read(self._ref, ctypes.byref(b), ctypes.byref(outs[0][1]), ctypes.byref(outs[1][1]),
+                                             _stream_of(stream, dev)), "clo_paged_read")
+        return outs[0][0], outs[1][0]
+
+    def attention(self, q, q_starts, kv_lens, block_table, out=None, max_q=None, softmax_scale: float = 0.0, window: int = 0,
+                  sinks: int = 0, stream=None):
+        """clo_paged_attention: q bf16 [total][n_q_heads][head_dim] over the pages; returns out (or new rows)."""
+        import torch
+
+        dev = _device_of(q, "q")
+        qr = _rows(q, "q", dev)
+        total, heads, d = q.shape
+        if d != self.head_dim:
+            raise ValueError(f"q has head_dim {d}; the cache has {self.head_dim}")
+        if out is None:
+            out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        else:
+            _refuse_folded(out, "out")
+        orow = _rows(out, "out", dev, (total, heads, d))
+        b = self._batch(dev, q_starts, kv_lens, block_table, total, max_q)
+        _check(load_library().clo_paged_attention(self._ref, ctypes.byref(b), ctypes.byref(qr), ctypes.byref(orow), heads,
+                                                  softmax_scale, window, sinks, _stream_of(stream, dev)),
+               "clo_paged_attention")
+        return out
+
+
+def clo_paged_append(cache: PagedCache, *args, **kwargs):
+    """PagedCache.append under the C name."""
+    return cache.append(*args, **kwargs)
+
+
+def clo_paged_read(cache: PagedCache, *args, **kwargs):
+    """PagedCache.read under the C name."""
+    return cache.read(*args, **kwargs)
+
+
+def clo_paged_attention(cache: PagedCache, *args, **kwargs):
+    """PagedCache.attention under the C name."""
+    return cache.attention(*args, **kwargs)
 
 
 # ----------------------------------------------------------------------------- convenience

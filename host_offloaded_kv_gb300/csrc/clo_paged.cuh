@@ -1,0 +1,168 @@
+// Shared parts of the paged-cache operators: kernel parameters, the phase of a rotary pair,
+// e4m3 conversion and the addressing of a ragged batch.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "clo.h"
+#include "clo_internal.cuh"
+
+namespace clo {
+
+constexpr float kE4m3Max = 448.f;
+constexpr int kMinScaleExp = -64;
+constexpr float kMinScale = 1e-30f;   // smallest page scale that a reader uses
+constexpr int kMaxGroup = 16;         // query heads per kv head
+constexpr int64_t kMaxPagedTokens = int64_t(1) << 30;
+
+// One of K or V: pages, scales (8-bit pages) and strides in elements.
+struct PagedSide {
+  char* pages;
+  float* scales;
+  int64_t stride_page, stride_head, stride_token;
+};
+
+struct PagedParams {
+  PagedSide side[2];  // K, V
+  const int32_t* q_starts;
+  const int32_t* kv_lens;
+  const int32_t* table;
+  int64_t table_stride;
+  int32_t n_pages;
+  int32_t max_pages;
+  int32_t batch;
+  int32_t total_q;
+  int32_t max_q;
+  int32_t n_kv_heads;
+  int32_t page_size;
+  int32_t page_shift;
+};
+
+// Rows [first, first + n) of the call's tensors belong to sequence b; row i has position pos0 + i.
+struct SeqRows {
+  int first, n, pos0, kv_len;
+};
+
+// The device-side lengths, clamped to the sizes that the host vouches for.
+__device__ __forceinline__ SeqRows seq_rows(const PagedParams& p, int b) {
+  SeqRows s;
+  int a = __ldg(p.q_starts + b), e = __ldg(p.q_starts + b + 1);
+  a = min(max(a, 0), p.total_q);
+  e = min(max(e, a), p.total_q);
+  s.first = a;
+  s.n = e - a;
+  s.kv_len = min(max(__ldg(p.kv_lens + b), -(1 << 30)), 1 << 30);
+  s.pos0 = s.kv_len - s.n;
+  s.n = min(s.n, p.max_q);
+  s.kv_len = min(max(s.kv_len, 0), p.max_pages << p.page_shift);
+  return s;
+}
+
+// Page of a position, or -1 where there is none.
+__device__ __forceinline__ int page_of(const PagedParams& p, int b, int logical) {
+  if (logical < 0 || logical >= p.max_pages) return -1;
+  const int id = __ldg(p.table + (int64_t)b * p.table_stride + logical);
+  return (unsigned)id < (unsigned)p.n_pages ? id : -1;
+}
+
+// Sequence of row t by the whole warp: the number of sequences that end at or before t.
+__device__ __forceinline__ int seq_of_row(const PagedParams& p, int t, int lane) {
+  int b = 0;
+  for (int c = 0; c < p.batch; c += 32) {
+    const bool done = c + lane < p.batch && __ldg(p.q_starts + c + lane + 1) <= t;
+    const unsigned m = __ballot_sync(0xffffffffu, done);
+    b += __popc(m);
+    if (m != 0xffffffffu) break;
+  }
+  return b;
+}
+
+// cos and sin of position * turn: the product modulo 2^64 is the angle as a fraction of a turn, so far
+// positions lose nothing.  Its top 23 bits go to the hardware sine and cosine, whose absolute error on
+// [-pi, pi] is below 2^-21; both are far below the half ulp (2^-9) of the bf16 results.
+__device__ __forceinline__ float2 rope_cos_sin(int64_t pos, uint64_t turn, float magnitude) {
+  const uint32_t lo = (uint32_t)turn, hi = (uint32_t)(turn >> 32);
+  const uint32_t plo = (uint32_t)pos, phi = (uint32_t)((uint64_t)pos >> 32);
+  const uint32_t frac = __umulhi(plo, lo) + plo * hi + phi * lo + 0x80000000u;
+  const float a = (__uint_as_float(0x3f800000u | (frac >> 9)) - 1.5f) * 6.283185307179586f;
+  return make_float2(__cosf(a) * magnitude, __sinf(a) * magnitude);
+}
+
+__device__ __forceinline__ void unpack8(const uint4 v, float* x) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint4 pack8(const float* x) {
+  return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+}
+
+// Two e4m3 codes of (lo, hi): nearest, ties to even, beyond +-448 (infinities too) to +-448, NaN stays.
+__device__ __forceinline__ uint32_t pack_e4m3(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint2 pack8_e4m3(const float* x) {
+  return make_uint2(pack_e4m3(x[0], x[1]) | pack_e4m3(x[2], x[3]) << 16, pack_e4m3(x[4], x[5]) | pack_e4m3(x[6], x[7]) << 16);
+}
+// Two codes as an fp16 pair (exact: e4m3 is a subset of fp16).
+__device__ __forceinline__ uint32_t e4m3_to_f16x2(uint32_t two) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(r) : "r"(two));
+  return r;
+}
+__device__ __forceinline__ float2 e4m3_to_f32x2(uint32_t two) {
+  const uint32_t h = e4m3_to_f16x2(two);
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// A sequence's visible tokens for a row at position `pos` are [0, sink_end) and [lo, hi).
+struct Visible {
+  int sink_end, lo, hi;
+};
+__device__ __forceinline__ Visible visible_of(int pos, int kv_len, int window, int sinks) {
+  Visible v;
+  v.hi = min(pos + 1, kv_len);
+  v.lo = window > 0 && pos >= window ? pos - window + 1 : 0;
+  v.sink_end = min(window > 0 ? sinks : 0, min(v.lo, v.hi));
+  return v;
+}
+
+struct AttendParams {
+  PagedParams c;
+  const uint16_t* q;
+  uint16_t* out;
+  int64_t q_token, q_head, o_token, o_head;
+  int32_t group;      // query heads per kv head
+  int32_t n_q_heads;
+  int32_t window, sinks;
+  float scale_log2;   // softmax scale * log2(e)
+};
+
+// Checks a cache and a batch and fills the kernels' view of them; null or what is wrong.
+const char* paged_params(const clo_paged_cache* c, const clo_paged_batch* b, PagedParams* p);
+
+// Records a CUDA-side or argument error as the calling thread's error text.
+clo_status paged_fail(clo_status st, const char* fmt, ...);
+
+cudaError_t launch_paged_attention(const AttendParams& p, int head_dim, int kv_bits, cudaStream_t st);
+
+}  // namespace clo

@@ -309,6 +309,161 @@ CLO_API clo_status clo_set(clo_ctx* ctx, int32_t key, int64_t value);
 CLO_API clo_status clo_sparse_attention_noalloc(const void* q, const void* rows, float* out, int32_t n_groups,
                                                 int32_t group_size, int32_t head_dim, int64_t k, void* stream);
 
+/* ---- rotary positions, and a paged K/V cache that stays in HBM ----------------------------------
+ * The calls above keep the K/V of every sequence in host memory and take queries and
+ * keys that carry their positions already.  The calls below are what a model needs
+ * around them: the rotation of queries and keys by their positions, and a cache in
+ * HBM pages with its own attention, for sequences and layers that need no offloading
+ * (short contexts, layers with a sliding window, prompts).  clo_paged_read turns a
+ * paged range back into the bf16 rows that clo_append_kv takes.  They have no context:
+ * all memory is the caller's, nothing is allocated, no workspace is kept between
+ * calls, and calls on different streams or in different captured graphs share
+ * nothing but the buffers that they are given.
+ *
+ * Common conventions
+ *   - All pointers are device pointers of the current device unless marked host; work
+ *     is enqueued on `stream` (cudaStream_t, NULL = the legacy default stream), the
+ *     call returns at once and may be captured into a graph.
+ *   - Strides count elements; the innermost dimension is contiguous.  A stride may be
+ *     negative or zero only where nothing is written.
+ *   - Values that the host cannot see (lengths, page numbers) are checked on the device:
+ *     what would lie outside the given sizes is skipped, never accessed. */
+
+/* A [n_tokens][n_heads][head_dim] view of bf16 rows. */
+typedef struct clo_rows {
+  void* ptr;
+  int64_t stride_token; /* elements */
+  int64_t stride_head;
+} clo_rows;
+
+enum { CLO_ROPE_NONE = 0, CLO_ROPE_LINEAR = 1, CLO_ROPE_BANDS = 2, CLO_ROPE_YARN = 3 };
+#define CLO_ROPE_MAX_PAIRS 64
+
+/* Rotary positions: pair i of the first rot_dim elements of a head is rotated by the angle
+ * position * f_i, f_i = theta^(-2i / rot_dim) before scaling; the rest is copied.
+ *   scaling CLO_ROPE_NONE    f_i
+ *           CLO_ROPE_LINEAR  f_i / factor
+ *           CLO_ROPE_BANDS   n_i = original_max f_i / 2 pi turns over the original context;
+ *                            w = clamp((n_i - low_freq) / (high_freq - low_freq), 0, 1);
+ *                            w f_i + (1 - w) f_i / factor
+ *           CLO_ROPE_YARN    pair indices lo = max(0, floor(c(beta_fast))), hi = min(rot_dim - 1,
+ *                            ceil(c(beta_slow))), c(n) = rot_dim ln(original_max / (2 pi n)) / (2 ln theta);
+ *                            w = 1 - clamp((i - lo) / max(hi - lo, 0.001), 0, 1), as above;
+ *                            magnitude 0.1 ln(factor) + 1 unless given. */
+typedef struct clo_rope_config {
+  int32_t rot_dim;     /* even, 2 .. 2 * CLO_ROPE_MAX_PAIRS */
+  int32_t interleaved; /* nonzero: pairs (2i, 2i + 1); 0: pairs (i, i + rot_dim / 2) */
+  double theta;        /* > 1; default 10000 */
+  int32_t scaling;     /* CLO_ROPE_*; default none */
+  double factor;       /* >= 1; default 1 */
+  double low_freq, high_freq;  /* bands: low < high; default 1, 4 */
+  double beta_fast, beta_slow; /* yarn: fast > slow > 0; default 32, 1 */
+  int64_t original_max;        /* bands, yarn: original context length, >= 1 */
+  double magnitude;            /* factor on the rotated elements; 0 (default) = by the scaling */
+} clo_rope_config;
+
+/* What the kernels take (plain values, kept by the caller; fill it with clo_rope_plan_init):
+ * turn[i] = f_i / 2 pi turns per position as a 64-bit binary fraction, so that
+ * position * turn[i] modulo 2^64 is the angle, exact at any position. */
+typedef struct clo_rope_plan {
+  uint64_t turn[CLO_ROPE_MAX_PAIRS];
+  float magnitude;
+  int32_t rot_dim;
+  int32_t interleaved;
+  int32_t ready; /* set by clo_rope_plan_init */
+} clo_rope_plan;
+
+CLO_API void clo_rope_config_default(clo_rope_config* cfg);
+/* Host only, no CUDA call.  Errors: CLO_ERR_INVALID (cfg, plan or a value out of range). */
+CLO_API clo_status clo_rope_plan_init(const clo_rope_config* cfg, clo_rope_plan* plan);
+
+/* y = magnitude * R(position) x on the rotated elements, rounded once from fp32 to bf16; the
+ * other elements are copied.  transpose != 0 applies magnitude * R(position)^T: the gradient
+ * of the call.  x and y may be the same rows (same strides); other overlap is not allowed.
+ * positions: int64 [n_tokens], any value.  head_dim: even, rot_dim <= head_dim <= 1024.
+ * n_tokens or n_heads 0: nothing to do.  Any strides and 2-byte alignment are taken; rows
+ * on 16-byte boundaries with rot_dim and head_dim multiples of 16 move in 16-byte words.
+ * Errors: CLO_ERR_INVALID, CLO_ERR_CUDA. */
+CLO_API clo_status clo_rope(const clo_rope_plan* plan, const clo_rows* x, const clo_rows* y, const int64_t* positions,
+                            int64_t n_tokens, int32_t n_heads, int32_t head_dim, int32_t transpose, void* stream);
+
+/* A paged cache: page p, kv head h, slot t is the row at
+ * pages + p * stride_page + h * stride_head + t * stride_token, for K and for V.
+ * kv_bits 16: bf16.  kv_bits 8: e4m3 codes, value = code * scale[p][h], one fp32 scale per page
+ * and kv head, separate for K and V.  The scales that clo_paged_append writes are powers
+ * of two, so values are exact in bf16; clo_paged_attention and clo_paged_read take any positive
+ * finite scales (below 1e-30: taken as 1e-30).
+ * Base addresses on 16-byte boundaries, strides multiples of 16 bytes and > 0. */
+typedef struct clo_paged_cache {
+  void* k_pages;
+  void* v_pages;
+  float* k_scales; /* fp32 [n_pages][n_kv_heads], contiguous; kv_bits 8 only */
+  float* v_scales;
+  int64_t n_pages; /* 1 .. 2^31 - 1 */
+  int64_t k_stride_page, k_stride_head, k_stride_token; /* elements */
+  int64_t v_stride_page, v_stride_head, v_stride_token;
+  int32_t n_kv_heads;
+  int32_t head_dim;  /* 64 or 128 */
+  int32_t page_size; /* tokens: 16, 32, 64 or 128 */
+  int32_t kv_bits;   /* 16 or 8 */
+} clo_paged_cache;
+
+/* A ragged batch: sequence b has kv_lens[b] tokens in the cache, the call's own included, and its
+ * last q_starts[b + 1] - q_starts[b] tokens are rows q_starts[b] .. of the call's tensors: row i
+ * of n has position kv_lens[b] - n + i.  Token j of sequence b is in slot j % page_size of page
+ * block_table[b][j / page_size].  A page number outside [0, n_pages) marks a page that is not
+ * there (a window has moved past it): its tokens are not written, read as zeros and not
+ * attended to.  Tokens at positions < 0 or >= max_pages * page_size are treated likewise. */
+typedef struct clo_paged_batch {
+  const int32_t* q_starts;    /* [batch + 1], ascending from 0, q_starts[batch] <= total_q */
+  const int32_t* kv_lens;     /* [batch] */
+  const int32_t* block_table; /* [batch][max_pages], rows table_stride apart */
+  int64_t table_stride;
+  int32_t max_pages;          /* max_pages * page_size < 2^30 */
+  int32_t batch;              /* 0 .. 65535 */
+  int32_t total_q;            /* rows of the call's tensors, 0 .. 2^30 */
+  int32_t max_q;              /* the most rows that a sequence has (rows beyond it are left out) */
+} clo_paged_batch;
+
+/* Append: writes the rows of k and v ([total_q][n_kv_heads][head_dim]) to their slots, k rotated by plan
+ * (NULL: as it is) at `positions` (int64 [total_q]; NULL: the rows' positions in the cache), rounded once
+ * from fp32.  With q and q_out ([total_q][n_q_heads][head_dim], both or neither; in place allowed), q is
+ * rotated into q_out in the same launch.  Slots other than the new tokens' are left as they are, but:
+ * kv_bits 8: a page whose slot 0 is written gets the scale 2^e, e >= -64 the smallest with
+ * max |x| <= 448 * 2^e over the finite new values of the page and head; a page that holds earlier
+ * tokens gets the larger of this and its scale, and where that grows the earlier tokens' codes are
+ * rescaled (exact unless they fall below 2^-6 * scale).  Infinities become +-448 * scale, NaN stays.
+ * A page may be written for one sequence only in a call.  Rows on 16-byte boundaries, strides multiples of 8
+ * elements, rot_dim a multiple of 16.
+ * Errors: CLO_ERR_INVALID, CLO_ERR_CUDA. */
+CLO_API clo_status clo_paged_append(const clo_paged_cache* cache, const clo_paged_batch* batch, const clo_rope_plan* plan,
+                                    const int64_t* positions, const clo_rows* k, const clo_rows* v, const clo_rows* q,
+                                    const clo_rows* q_out, int32_t n_q_heads, void* stream);
+
+/* Read back: the batch's rows as bf16 (code * scale, rounded once) into k_out and v_out
+ * [total_q][n_kv_heads][head_dim]; rows as for clo_paged_append.  A whole sequence is read with
+ * q_starts = {0, n}, kv_lens = {n}, and goes to the host pool with clo_append_kv(..., src_is_device = 1).
+ * Errors: CLO_ERR_INVALID, CLO_ERR_CUDA. */
+CLO_API clo_status clo_paged_read(const clo_paged_cache* cache, const clo_paged_batch* batch, const clo_rows* k_out,
+                                  const clo_rows* v_out, void* stream);
+
+/* Attention of the batch's query rows over the cache:
+ *   out = sum_j p_j V_j, p = softmax over the visible j of softmax_scale * q . K_j,
+ * q and out bf16 [total_q][n_q_heads][head_dim]; scores, maxima and sums in fp32, weights rounded to
+ * the type of the product (bf16 for bf16 pages, fp16 for 8-bit pages), out rounded once.
+ * Token j is visible to the row at position p iff j <= p, j < kv_lens[b], its page is there, and
+ * window == 0 or j > p - window or j < sinks: the last `window` tokens (the row's own included) and
+ * the first `sinks`.  Rows that see no token, or whose scores are all -infinity, are zeros; what an
+ * invisible token holds (NaN, infinity, memory never written) changes nothing.
+ * n_q_heads: a multiple of n_kv_heads, at most 16 per kv head; head h reads kv head h / group.
+ * softmax_scale 0: 1 / sqrt(head_dim).  window, sinks >= 0 (sinks without a window have no effect).
+ * Rows as for clo_paged_append; out must not overlap q.
+ * Rows past q_starts[batch] are left as they are.
+ * Errors: CLO_ERR_INVALID, CLO_ERR_CUDA. */
+CLO_API clo_status clo_paged_attention(const clo_paged_cache* cache, const clo_paged_batch* batch, const clo_rows* q,
+                                       const clo_rows* out, int32_t n_q_heads, float softmax_scale, int32_t window,
+                                       int32_t sinks, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
