@@ -2,6 +2,7 @@
 // e4m3 conversion and the addressing of a ragged batch.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -162,6 +163,58 @@ const char* paged_params(const clo_paged_cache* c, const clo_paged_batch* b, Pag
 
 // Records a CUDA-side or argument error as the calling thread's error text.
 clo_status paged_fail(clo_status st, const char* fmt, ...);
+
+// ---------------------------------------------------------------------------- TMA
+// Tensor maps of K and V as [page][head][slot][element] with boxes of `rows` slots and one swizzle span (128
+// bytes, or the whole row where that is 64) of elements.
+struct PageMaps {
+  CUtensorMap side[2];
+};
+// Null, or what failed.
+const char* make_page_maps(const PagedParams& c, int head_dim, int kv_bits, int rows, PageMaps* maps);
+
+// One box to shared memory; pages outside the map read as zeros.
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int element, int slot, int head, int page, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(map), "r"(element), "r"(slot), "r"(head), "r"(page), "r"(bar)
+      : "memory");
+}
+
+// Bounded wait: false after about two seconds, which no copy or product takes.
+__device__ __forceinline__ bool mbar_wait_limited(uint64_t* bar, uint32_t parity) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (true) {
+    for (int i = 0; i < 64; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (global_timer_ns() - t0 > 2000000000ull) return false;
+  }
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float ld_cluster_f32(uint32_t smem_addr, uint32_t rank) {
+  float v;
+  asm volatile(
+      "{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
+      : "=f"(v)
+      : "r"(smem_addr), "r"(rank)
+      : "memory");
+  return v;
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
 cudaError_t launch_paged_attention(const AttendParams& p, int head_dim, int kv_bits, cudaStream_t st);
 
