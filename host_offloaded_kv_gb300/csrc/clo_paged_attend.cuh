@@ -1,0 +1,89 @@
+// Device parts shared by the two attention kernels over paged caches.
+#pragma once
+
+#include "clo_paged.cuh"
+
+namespace clo {
+
+// One row by one warp: lane i holds elements i * D / 32 and on.  Right for every input; no speed.
+template <int D, int BITS>
+__device__ void attend_row(const AttendParams& a, int b, const SeqRows& s, int row, int head, int lane) {
+  constexpr int E = D / 32;
+  const PagedParams& p = a.c;
+  const int kvh = head / a.group, pos = s.pos0 + row;
+  const int64_t t = s.first + row;
+  const Visible v = visible_of(pos, s.kv_len, a.window, a.sinks);
+  float q[E], acc[E], m = -INFINITY, l = 0.f;
+  const uint16_t* qp = a.q + t * a.q_token + (int64_t)head * a.q_head;
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    q[i] = bf16_bits_to_f32(qp[lane * E + i]);
+    acc[i] = 0.f;
+  }
+  auto value = [&](int side, int page, int slot, int e) {
+    const PagedSide& sd = p.side[side];
+    const int64_t at = (int64_t)page * sd.stride_page + (int64_t)kvh * sd.stride_head + (int64_t)slot * sd.stride_token + e;
+    if (BITS == 16) return bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(sd.pages)[at]);
+    return e4m3_to_f32x2(reinterpret_cast<const uint8_t*>(sd.pages)[at]).x *
+           fmaxf(sd.scales[(int64_t)page * p.n_kv_heads + kvh], kMinScale);
+  };
+  int j = v.sink_end > 0 ? 0 : v.lo;
+  for (; j < v.hi; j = j + 1 == v.sink_end ? v.lo : j + 1) {
+    const int page = page_of(p, b, j >> p.page_shift);
+    if (page < 0) continue;
+    const int slot = j & (p.page_size - 1);
+    float d = 0.f;
+#pragma unroll
+    for (int i = 0; i < E; ++i) d = fmaf(q[i], value(0, page, slot, lane * E + i), d);
+    const float sc = warp_sum(d) * a.scale_log2;
+    const float mn = fmaxf(m, sc);
+    const float keep = m == mn ? 1.f : exp2f(m - mn);
+    const float w = mn == -INFINITY ? 0.f : exp2f(sc - mn);
+    l = l * keep + w;
+#pragma unroll
+    for (int i = 0; i < E; ++i) acc[i] = acc[i] * keep + w * value(1, page, slot, lane * E + i);
+    m = mn;
+  }
+  uint16_t* o = a.out + t * a.o_token + (int64_t)head * a.o_head;
+#pragma unroll
+  for (int i = 0; i < E; ++i) o[lane * E + i] = (uint16_t)pack_bf16(l == 0.f ? 0.f : acc[i] / l, 0.f);
+}
+
+// Shared-memory address of 16-byte chunk `chunk` of row `row` in a tile of `rows` rows as TMA's swizzle left it.
+template <int SPAN>
+__device__ __forceinline__ uint32_t swizzled(uint32_t base, int rows, int row, int chunk) {
+  constexpr int kChunks = SPAN / 16;
+  const int c = chunk % kChunks;
+  const int x = SPAN == 128 ? c ^ (row & 7) : c ^ ((row >> 1) & 3);
+  return base + chunk / kChunks * rows * SPAN + row * SPAN + x * 16;
+}
+
+// True if one of the two 16-bit values is an infinity or NaN.
+template <int BITS>
+__device__ __forceinline__ bool not_finite2(uint32_t x) {
+  constexpr uint32_t E = BITS == 16 ? 0x7f80u : 0x7c00u;
+  return (x & E) == E || ((x >> 16) & E) == E;
+}
+
+// The tiles that some row of a unit sees: [0, sink_tiles) and [first, first + rest).
+struct TileList {
+  int sink_tiles, first, rest;
+  __device__ __forceinline__ int count() const { return sink_tiles + rest; }
+  __device__ __forceinline__ int at(int k) const { return k < sink_tiles ? k : first + k - sink_tiles; }
+};
+__device__ __forceinline__ TileList tiles_of(int pos_first, int pos_last, int kv_len, int window, int sinks, int tokens) {
+  const Visible a = visible_of(pos_first, kv_len, window, sinks), z = visible_of(pos_last, kv_len, window, sinks);
+  TileList t;
+  t.sink_tiles = t.first = t.rest = 0;
+  if (z.hi <= 0) return t;
+  // a sink token that the first row sees through its window lies in the second range
+  const int sink_end = window > 0 ? min(min(sinks, a.lo), z.hi) : 0;
+  t.sink_tiles = (sink_end + tokens - 1) / tokens;
+  t.first = max(a.lo / tokens, t.sink_tiles);
+  t.rest = max((z.hi + tokens - 1) / tokens - t.first, 0);
+  return t;
+}
+
+cudaError_t launch_attend_many(const AttendParams& a, int head_dim, int kv_bits, cudaStream_t st);
+
+}  // namespace clo

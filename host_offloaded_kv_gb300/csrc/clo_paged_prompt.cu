@@ -1,0 +1,685 @@
+// Attention of many rows per kv head over a paged cache: prompts, chunks of prompts, several drafted tokens.
+//
+// A block takes kTiles tiles of 128 rows of one (sequence, kv head) - consecutive query tokens times the group's
+// heads, so that a K or V tile of 128 tokens serves every head of the group - and walks the tiles of tokens that its
+// rows see.  Both products run on tcgen05: S = Q K^T from shared memory into TMEM, O += P V with P in TMEM (over the
+// columns of S that it came from) and O in TMEM.  One thread owns a row of S: its maximum and sum need no exchange.
+//
+//   warps 0-3, 4-7   softmax of row tile 0, 1 (TMEM lanes are tied to a warp's place in its group of four)
+//   warp 8           TMA: pages -> ring of operand tiles, K(0) K(1) V(0) K(2) V(1) ...
+//   warp 9           MMA issue: PV of one row tile, then S of the next token tile, alternating between the row tiles, so that
+//                    one tile's products run under the other's softmax
+//   warps 10, 11     bf16 pages: V of the tiles at a mask's edge: rows that hold an infinity or NaN are cleared (see below)
+//   warps 12-15      8-bit pages only: codes -> fp16 operand tiles
+//
+// The accumulator is rescaled only when a row's maximum has grown by more than 2^8 (weights stay below 2^8 times
+// the largest so far; exact in the end, as sum and accumulator share the reference).
+//
+// A masked weight is zero, but zero times NaN is not: V rows that hold an infinity or NaN are cleared in the operand tile
+// wherever not every row sees the token.  If some row does see such a token, the block's rows are
+// computed again one by one.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "clo_paged_attend.cuh"
+
+namespace clo {
+namespace {
+
+constexpr int kTok = 128;    // tokens per tile
+constexpr int kRows = 128;   // rows per row tile
+constexpr int kMeta = 8;     // token tiles whose page data is kept
+constexpr float kGrow = 8.f;
+
+// ---------------------------------------------------------------------------- tcgen05
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+#define CLO_R4(x, i) "=r"(x[i]), "=r"(x[i + 1]), "=r"(x[i + 2]), "=r"(x[i + 3])
+#define CLO_I4(x, i) "r"(x[i]), "r"(x[i + 1]), "r"(x[i + 2]), "r"(x[i + 3])
+__device__ __forceinline__ void tc_ld32(uint32_t addr, uint32_t* x) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : CLO_R4(x, 0), CLO_R4(x, 4), CLO_R4(x, 8), CLO_R4(x, 12), CLO_R4(x, 16), CLO_R4(x, 20), CLO_R4(x, 24), CLO_R4(x, 28)
+      : "r"(addr));
+}
+#define CLO_RW4(x, i) "+r"(x[i]), "+r"(x[i + 1]), "+r"(x[i + 2]), "+r"(x[i + 3])
+// Ties 32 loaded registers to this point of the program: nothing that uses them moves above it.
+__device__ __forceinline__ void tie32(uint32_t* x) {
+  asm volatile("" : CLO_RW4(x, 0), CLO_RW4(x, 4), CLO_RW4(x, 8), CLO_RW4(x, 12), CLO_RW4(x, 16), CLO_RW4(x, 20), CLO_RW4(x, 24), CLO_RW4(x, 28));
+}
+// Waits for this thread's TMEM loads, of which x[0 .. 32 * N) are the results.
+template <int N>
+__device__ __forceinline__ void tc_wait_ld(uint32_t* x) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) tie32(x + 32 * i);
+}
+__device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t* x) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::CLO_I4(x, 0),
+      CLO_I4(x, 4), CLO_I4(x, 8), CLO_I4(x, 12), CLO_I4(x, 16), CLO_I4(x, 20), CLO_I4(x, 24), CLO_I4(x, 28), "r"(addr)
+      : "memory");
+}
+
+// Operand tiles are [span of 64 elements][128 rows][128 bytes] with the 128-byte swizzle.  K-major (Q, K): rows are rows, 8-row
+// groups 1024 bytes apart.  MN-major (V): a row is a token (the K side), its 64 elements the N side; spans 16 KB apart.
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t leading, uint32_t stride) {
+  return (uint64_t)((addr >> 4) & 0x3fffu) | (uint64_t)(leading >> 4) << 16 | (uint64_t)(stride >> 4) << 32 | 1ull << 46 | 2ull << 61;
+}
+__host__ __device__ constexpr uint32_t mma_shape(bool bf16, int n, bool mn_major_b) {
+  return 1u << 4 | (bf16 ? 1u : 0u) << 7 | (bf16 ? 1u : 0u) << 10 | (mn_major_b ? 1u : 0u) << 16 | (uint32_t)(n / 8) << 17 | (uint32_t)(kRows / 16) << 24;
+}
+
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+template <int D, int BITS>
+struct Cfg {
+  static constexpr int kSpans = D / 64;                       // 64-element spans of an operand row
+  static constexpr int kTileBytes = kTok * D * 2;             // an operand tile
+  static constexpr int kQBytes = kRows * D * 2;
+  static constexpr int kSlots = BITS == 16 ? 4 : 3;
+  static constexpr int kRawBytes = BITS == 16 ? 0 : kTok * D;
+  static constexpr int kRaw = BITS == 16 ? 0 : 3;
+  static constexpr int kThreads = BITS == 16 ? 384 : 512;
+  static constexpr int kPartRow = D + 4;                       // floats per row of a joined block's accumulator
+  static constexpr int smem(int tiles) { return tiles * kQBytes + kSlots * kTileBytes + kRaw * kRawBytes + 1024; }
+};
+
+struct Shared {
+  uint64_t full[4], empty[4];      // operand tiles: filled (TMA or converters), products done
+  uint64_t checked[4];             // bf16: operand tiles looked over
+  uint64_t raw_full[4], raw_empty[4];
+  uint64_t s_full[2], p_ready[2];
+  uint64_t done;                   // every product
+  uint64_t meta[kMeta];
+  float scale[kMeta][2][8];
+  uint32_t there[kMeta];
+  uint32_t tmem;
+  int odd, failed;
+  float m[2][kRows], l[2][kRows];
+};
+
+// Bounded wait; once one has given up, the others follow at once.
+__device__ __forceinline__ bool wait(Shared& sh, uint64_t* bar, uint32_t parity) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (true) {
+    for (int i = 0; i < 64; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (*reinterpret_cast<volatile int*>(&sh.failed)) return false;
+    if (global_timer_ns() - t0 > 2000000000ull) {
+      *reinterpret_cast<volatile int*>(&sh.failed) = 1;
+      return false;
+    }
+  }
+}
+
+template <int D, int BITS, int TILES>
+__global__ void __launch_bounds__(Cfg<D, BITS>::kThreads, 1) k_attend_many(const AttendParams a, const __grid_constant__ PageMaps maps, int q_blocks,
+                                                                              int splits) {
+  using C = Cfg<D, BITS>;
+  constexpr int SLOTS = C::kSlots;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(16) Shared sh;
+
+  const PagedParams& p = a.c;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // the last rows first: they see the most tokens
+  const int unit = blockIdx.x / splits, rank = blockIdx.x % splits;
+  const int kvh = unit % p.n_kv_heads, qb = q_blocks - 1 - unit / p.n_kv_heads, b = blockIdx.y;
+  const SeqRows s = seq_rows(p, b);
+  const int rows = s.n * a.group, row0 = qb * TILES * kRows;
+  if (row0 >= rows) return;  // the whole cluster
+  const int row_end = min(rows, row0 + TILES * kRows);
+  const int pos_first = s.pos0 + row0 / a.group, pos_last = s.pos0 + (row_end - 1) / a.group;
+  const TileList tl = tiles_of(pos_first, pos_last, s.kv_len, a.window, a.sinks, kTok);
+  const int all = tl.count();
+  const int t_begin = (int)((int64_t)all * rank / splits), n = (int)((int64_t)all * (rank + 1) / splits) - t_begin;
+
+  const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t q_smem = smem, ring = smem + TILES * C::kQBytes, raw = ring + SLOTS * C::kTileBytes;
+  uint8_t* const generic = smem_raw + (smem - smem_u32(smem_raw));
+
+  if (tid == 0) {
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&sh.full[i], BITS == 16 ? 1 : 128);
+      mbar_init(&sh.empty[i], 1);
+      mbar_init(&sh.checked[i], 64);
+      mbar_init(&sh.raw_full[i], 1);
+      mbar_init(&sh.raw_empty[i], 128);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_ready[i], 128);
+    }
+    mbar_init(&sh.done, 1);
+    for (int i = 0; i < kMeta; ++i) mbar_init(&sh.meta[i], 1);
+    sh.odd = 0;
+    sh.failed = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh.tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+
+  // Q rows into operand tiles, a row per softmax thread.  8-bit pages: fp16, each row scaled by a power of two that
+  // puts its largest finite element into [2^14, 2^15).
+  float fac = a.scale_log2;
+  const int tile = warp >> 2, my_row = row0 + (tile < TILES ? tile : 0) * kRows + (tid & 127);
+  const bool row_ok = warp < 4 * TILES && my_row < rows;
+  if (warp < 4 * TILES) {
+    const uint16_t* src = a.q + (int64_t)(s.first + my_row / a.group) * a.q_token + (int64_t)(kvh * a.group + my_row % a.group) * a.q_head;
+    const int r = tid & 127;
+    float down = 1.f;
+    if (BITS == 8 && row_ok) {
+      float mx = 0.f;
+      for (int c = 0; c < D / 8; ++c) {
+        float x[8];
+        unpack8(__ldg(reinterpret_cast<const uint4*>(src) + c), x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fabsf(x[i]) < INFINITY ? fabsf(x[i]) : 0.f);
+      }
+      const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127 - 14, -100), 112);
+      down = __uint_as_float((uint32_t)(127 - e) << 23);
+      fac *= __uint_as_float((uint32_t)(127 + e) << 23);
+    }
+#pragma unroll 4
+    for (int c = 0; c < D / 8; ++c) {
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (row_ok) v = __ldg(reinterpret_cast<const uint4*>(src) + c);
+      if (BITS == 8) {
+        float x[8];
+        unpack8(v, x);
+        v = make_uint4(pack_f16(x[0] * down, x[1] * down), pack_f16(x[2] * down, x[3] * down), pack_f16(x[4] * down, x[5] * down), pack_f16(x[6] * down, x[7] * down));
+      }
+      *reinterpret_cast<uint4*>(generic + (swizzled<128>(q_smem + tile * C::kQBytes, kRows, r, c) - smem)) = v;
+    }
+    fence_proxy_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  constexpr uint32_t kS[2] = {0, 128}, kO[2] = {256, 384};
+
+  // Operand tiles in ring order: e = 0 is K(0), e = 2 j + 1 is K(j + 1), e = 2 j + 2 is V(j), without K(n).
+  // Position of K(j) and V(j):
+  auto at_k = [&](int j) { return j == 0 ? 0 : 2 * j - 1; };
+  auto at_v = [&](int j) { return 2 * j + 2 - (j + 1 >= n ? 1 : 0); };
+  // and back: element e is a V tile?  which token tile?
+  auto is_v = [&](int e) { return e > 0 && ((e & 1) == 0 || e == 2 * n - 1); };
+  auto tile_of = [&](int e) { return !is_v(e) ? (e + 1) / 2 : e == 2 * n - 1 ? n - 1 : e / 2 - 1; };
+
+  if (warp < 8) {
+    // ------------------------------------------------------------------------ softmax
+    if (BITS == 16) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+    float ref = -INFINITY, l = 0.f;
+    const int t = warp >> 2;
+    bool ok = true;
+    if (t < TILES) {
+      constexpr float kOff = BITS == 16 ? 0.f : 7.f;  // weights of 8-bit pages: up to 2^15 with kGrow, fp16 down to 2^-31
+      const uint32_t lane_off = (uint32_t)(warp & 3) * 32u << 16;
+      const uint32_t s_addr = tmem + lane_off + kS[t], o_addr = tmem + lane_off + kO[t];
+      // the tile's first and last row bound what "every row sees" means; rows past the end follow the last one
+      const int rf = min(row0 + t * kRows, rows - 1), rl = min(row0 + t * kRows + kRows - 1, rows - 1);
+      const Visible vf = visible_of(s.pos0 + rf / a.group, s.kv_len, a.window, a.sinks);
+      const Visible vl = visible_of(s.pos0 + rl / a.group, s.kv_len, a.window, a.sinks);
+      const Visible v = visible_of(s.pos0 + min(my_row, rows - 1) / a.group, s.kv_len, a.window, a.sinks);
+      for (int j = 0; j < n; ++j) {
+        const int j0 = tl.at(t_begin + j) * kTok;
+        const int slot = j % kMeta;
+        ok = wait(sh, &sh.meta[slot], (j / kMeta) & 1) && wait(sh, &sh.s_full[t], j & 1);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t x[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tc_ld32(s_addr + 32 * c, x + 32 * c);
+        tc_wait_ld<4>(x);
+        const uint32_t there = sh.there[slot];
+        const bool whole = there == 0xffu && j0 + kTok <= vf.hi && (j0 >= vl.lo || j0 + kTok <= (a.window > 0 ? a.sinks : 0));
+        if (!whole) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            // bits of the columns 32 c .. 32 c + 31 that this row sees
+            const int base = j0 + 32 * c;
+            auto below = [&](int end) { return end - base >= 32 ? 0xffffffffu : end <= base ? 0u : (1u << (end - base)) - 1u; };
+            uint32_t see = (below(v.hi) & ~below(v.lo)) | below(v.sink_end);
+            if (!(there >> (2 * c) & 1u)) see &= 0xffff0000u;
+            if (!(there >> (2 * c + 1) & 1u)) see &= 0x0000ffffu;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!(see >> i & 1u)) x[32 * c + i] = 0xff800000u;
+          }
+        }
+        float ks[BITS == 8 ? 8 : 1], vs[BITS == 8 ? 8 : 1];
+        float mx = -INFINITY;
+        if (BITS == 8) {
+#pragma unroll
+          for (int g = 0; g < 8; ++g) {
+            ks[g] = fmaxf(sh.scale[slot][0][g], kMinScale) * fac;
+            vs[g] = fmaxf(sh.scale[slot][1][g], kMinScale);
+            const uint64_t f2 = pack2(ks[g], ks[g]);
+            const float lv = __log2f(vs[g]);
+            const uint64_t l2 = pack2(lv, lv);
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+              const float2 y = unpack2(fma2(pack2(__uint_as_float(x[16 * g + i]), __uint_as_float(x[16 * g + i + 1])), f2, l2));
+              x[16 * g + i] = __float_as_uint(y.x);
+              x[16 * g + i + 1] = __float_as_uint(y.y);
+              mx = fmaxf(mx, fmaxf(y.x, y.y));
+            }
+          }
+        } else {
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int i = 0; i < 128; i += 8)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) m4[c] = fmaxf(m4[c], fmaxf(__uint_as_float(x[i + 2 * c]), __uint_as_float(x[i + 2 * c + 1])));
+          mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * fac;
+        }
+        const bool grow = mx > ref + kGrow;
+        if (__any_sync(0xffffffffu, grow)) {
+          const float f = grow ? (ref == -INFINITY ? 0.f : exp2_fast(ref - mx)) : 1.f;
+          if (grow) ref = mx;
+          l *= f;
+          if (j > 0) {
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tc_ld32(o_addr + 32 * c, o);
+              tc_wait_ld<1>(o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tc_st32(o_addr + 32 * c, o);
+            }
+          }
+        }
+        const float sub = ref == -INFINITY ? 0.f : kOff - ref;
+        const uint64_t sub2 = pack2(sub, sub), fac2 = pack2(fac, fac);
+        uint64_t sum2[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t w[32];
+#pragma unroll
+          for (int i = 0; i < 64; i += 2) {
+            const int c = 64 * h + i;
+            const uint64_t x2 = pack2(__uint_as_float(x[c]), __uint_as_float(x[c + 1]));
+            float2 y = unpack2(BITS == 8 ? add2(x2, sub2) : fma2(x2, fac2, sub2));
+            y.x = exp2_fast(y.x);
+            y.y = exp2_fast(y.y);
+            sum2[(i >> 1) & 3] = add2(sum2[(i >> 1) & 3], pack2(y.x, y.y));
+            // weights in the products' type: bf16 next to bf16 V, fp16 next to 8-bit V
+            w[i >> 1] = BITS == 16 ? pack_bf16(y.x, y.y) : pack_f16(y.x, y.y);
+            if (BITS == 8 && (c & 15) == 14) {
+              const float2 q = unpack2(add2(add2(sum2[0], sum2[1]), add2(sum2[2], sum2[3])));
+              l = fmaf(q.x + q.y, __frcp_rn(vs[c >> 4]), l);
+              sum2[0] = sum2[1] = sum2[2] = sum2[3] = 0;
+            }
+          }
+          tc_st32(s_addr + 32 * h, w);
+        }
+        if (BITS == 16) {
+          const float2 q = unpack2(add2(add2(sum2[0], sum2[1]), add2(sum2[2], sum2[3])));
+          l += q.x + q.y;
+        }
+        tc_wait_st();
+        tc_fence_before();
+        mbar_arrive(&sh.p_ready[t]);
+      }
+      // the row tile's last product; where the accumulators go to shared memory, the other row tile's too
+      if (ok && n > 0) ok = splits == 1 ? wait(sh, &sh.s_full[t], n & 1) : wait(sh, &sh.done, 0);
+      ok = __all_sync(0xffffffffu, ok);
+      tc_fence_after();
+      if (n > 0) {
+        // the reference of the weights as the join sees it
+        ref = ref == -INFINITY ? ref : ref - kOff;
+      }
+      if (!ok) l = __int_as_float(0x7fffffff);
+      const bool direct = splits == 1;
+      uint16_t* dst = a.out + (int64_t)(s.first + my_row / a.group) * a.o_token + (int64_t)(kvh * a.group + my_row % a.group) * a.o_head;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      float* part = reinterpret_cast<float*>(generic) + (t * kRows + (tid & 127)) * C::kPartRow;
+      if (!direct) {
+        sh.m[t][tid & 127] = ref;
+        sh.l[t][tid & 127] = l;
+      }
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        if (n > 0) {
+          tc_ld32(o_addr + 32 * c, o);
+          tc_wait_ld<1>(o);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = 0u;
+        }
+        if (!direct) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) *reinterpret_cast<uint4*>(part + 32 * c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+        } else if (row_ok) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 8) {
+            float y[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = l == 0.f ? 0.f : __uint_as_float(o[i + e]) * inv;
+            *reinterpret_cast<uint4*>(dst + 32 * c + i) = pack8(y);
+          }
+        }
+      }
+      tc_fence_before();
+    }
+  } else {
+    if (BITS == 16) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if (warp == 8) {
+      // ---------------------------------------------------------------------- TMA
+      auto page_for = [&](int j) {
+        return lane < 8 && j < n ? page_of(p, b, (tl.at(t_begin + j) * kTok + lane * 16) >> p.page_shift) : -1;
+      };
+      const int box = min(p.page_size, kTok);
+      constexpr int kSpan = BITS == 16 ? 128 : (D < 128 ? D : 128);  // bytes of a page row in one box
+      constexpr int kBoxSpans = D * BITS / 8 / kSpan;
+      constexpr int kBuf = BITS == 16 ? C::kSlots : C::kRaw;
+      bool ok = true;
+      auto load = [&](int side, int j, int e, int page) {
+        const int buf = e % kBuf;
+        uint64_t* full = BITS == 16 ? &sh.full[buf] : &sh.raw_full[buf];
+        uint64_t* empty = BITS == 16 ? &sh.empty[buf] : &sh.raw_empty[buf];
+        if (e >= kBuf) ok = wait(sh, empty, (e / kBuf - 1) & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) return;
+        if (side == 0) {
+          const int slot = j % kMeta;
+          const unsigned there = __ballot_sync(0xffffffffu, page >= 0);
+          if (lane == 0) sh.there[slot] = there;
+          if (BITS == 8 && lane < 8) {
+            const int64_t at = (int64_t)max(page, 0) * p.n_kv_heads + kvh;
+            sh.scale[slot][0][lane] = __ldg(p.side[0].scales + at);
+            sh.scale[slot][1][lane] = __ldg(p.side[1].scales + at);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.meta[slot]);
+        }
+        if (lane == 0) mbar_arrive_expect_tx(full, BITS == 16 ? C::kTileBytes : C::kRawBytes);
+        __syncwarp();
+        const int tok = lane * 16;
+        if (lane < 8 && tok % box == 0) {
+          const uint32_t dst = (BITS == 16 ? ring + buf * C::kTileBytes : raw + buf * C::kRawBytes) + tok * kSpan;
+          const int slot = (tl.at(t_begin + j) * kTok + tok) & (p.page_size - 1);
+#pragma unroll
+          for (int h = 0; h < kBoxSpans; ++h)
+            tma_box(dst + h * kTok * kSpan, &maps.side[side], h * (kSpan * 8 / BITS), slot, kvh, page, smem_u32(full));
+        }
+        __syncwarp();
+      };
+      int page_k = page_for(0), page_v = page_k, page_next = page_for(1);
+      if (n > 0) load(0, 0, 0, page_k);
+      for (int j = 0; j < n && ok; ++j) {
+        page_k = page_next;
+        page_next = page_for(j + 2);
+        if (j + 1 < n) load(0, j + 1, at_k(j + 1), page_k);
+        if (ok) load(1, j, at_v(j), page_v);
+        page_v = page_k;
+      }
+      if (!ok)  // copies in flight land before the block leaves
+        for (int i = 0; i < kBuf; ++i)
+          for (int ph = 0; ph < 2; ++ph) mbar_wait_limited(BITS == 16 ? &sh.full[i] : &sh.raw_full[i], ph);
+    } else if (warp == 9) {
+      // ---------------------------------------------------------------------- MMA issue
+      if (lane == 0) {
+        constexpr uint32_t kShapeS = mma_shape(BITS == 16, kTok, false), kShapeO = mma_shape(BITS == 16, D, true);
+        auto score = [&](int t, int e) {
+          const uint32_t qa = q_smem + t * C::kQBytes, ka = ring + e % SLOTS * C::kTileBytes;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = kk / 4 * (kTok * 128) + kk % 4 * 32;
+            tc_mma_ss(tmem + kS[t], operand(qa + off, 16, 1024), operand(ka + off, 16, 1024), kShapeS, kk > 0);
+          }
+        };
+        auto ready = [&](int e) { return wait(sh, &sh.full[e % SLOTS], (e / SLOTS) & 1); };
+        bool ok = n > 0 && ready(0);
+        if (ok) {
+          tc_fence_after();
+          for (int t = 0; t < TILES; ++t) {
+            score(t, 0);
+            tc_commit(&sh.s_full[t]);
+          }
+          tc_commit(&sh.empty[0]);
+        }
+        for (int j = 0; j < n && ok; ++j) {
+          const int ek = at_k(j + 1), ev = at_v(j);
+          if (j + 1 < n) ok = ready(ek);
+          ok = ok && ready(ev);
+          if (ok && BITS == 16) ok = wait(sh, &sh.checked[ev % SLOTS], (ev / SLOTS) & 1);
+          for (int t = 0; t < TILES && ok; ++t) {
+            ok = wait(sh, &sh.p_ready[t], j & 1);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t va = ring + ev % SLOTS * C::kTileBytes;
+#pragma unroll
+            for (int kk = 0; kk < kTok / 16; ++kk)
+              tc_mma_ts(tmem + kO[t], tmem + kS[t] + kk * 8, operand(va + kk * 2048, kTok * 128, 1024), kShapeO, j > 0 || kk > 0);
+            if (j + 1 < n) score(t, ek);
+            tc_commit(&sh.s_full[t]);
+          }
+          if (ok) {
+            tc_commit(&sh.empty[ev % SLOTS]);
+            if (j + 1 < n) tc_commit(&sh.empty[ek % SLOTS]);
+          }
+        }
+        if (ok) tc_commit(&sh.done);
+      }
+      __syncwarp();
+    } else if (BITS == 16 ? warp >= 10 : warp >= 12) {
+      // ---------------------------------------------------------------------- V at a mask's edge; 8-bit codes -> fp16
+      const Visible vf = visible_of(pos_first, s.kv_len, a.window, a.sinks), vl = visible_of(pos_last, s.kv_len, a.window, a.sinks);
+      auto edge = [&](int j) {
+        const int j0 = tl.at(t_begin + j) * kTok;
+        return !(j0 + kTok <= vf.hi && (j0 >= vl.lo || j0 + kTok <= (a.window > 0 ? a.sinks : 0)));
+      };
+      auto seen = [&](int tok) { return tok < vl.hi && (tok >= vf.lo || tok < (a.window > 0 ? a.sinks : 0)); };
+      bool ok = true;
+      if constexpr (BITS == 16) {
+        const int th = tid - 320;
+        for (int e = 0; e < 2 * n && ok; ++e) {
+          const int j = tile_of(e), slot = e % SLOTS;
+          ok = wait(sh, &sh.full[slot], (e / SLOTS) & 1);
+          if (ok && is_v(e) && edge(j)) {
+            const int j0 = tl.at(t_begin + j) * kTok;
+            for (int r = th; r < kTok; r += 64) {
+              uint8_t* row = generic + (ring - smem) + slot * C::kTileBytes + r * 128;
+              bool bad = false;
+              for (int c = 0; c < C::kSpans * 8; ++c) {
+                const uint4 w = *reinterpret_cast<const uint4*>(row + (c >> 3) * (kTok * 128) + (c & 7) * 16);
+                bad |= not_finite2<16>(w.x) || not_finite2<16>(w.y) || not_finite2<16>(w.z) || not_finite2<16>(w.w);
+              }
+              if (bad) {
+                if (seen(j0 + r)) sh.odd = 1;
+                for (int c = 0; c < C::kSpans * 8; ++c) *reinterpret_cast<uint4*>(row + (c >> 3) * (kTok * 128) + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+              }
+            }
+            fence_proxy_async_smem();
+          }
+          mbar_arrive(&sh.checked[slot]);
+        }
+      } else {
+        const int th = tid - 384;
+        constexpr int kChunks = D / 16;   // 16-byte chunks of a code row
+        for (int e = 0; e < 2 * n && ok; ++e) {
+          const int j = tile_of(e);
+          const int buf = e % C::kRaw, slot = e % SLOTS;
+          ok = wait(sh, &sh.raw_full[buf], (e / C::kRaw) & 1);
+          if (ok && e >= SLOTS) ok = wait(sh, &sh.empty[slot], (e / SLOTS - 1) & 1);
+          if (!ok) break;
+          const bool look = is_v(e) && edge(j);
+          const int j0 = tl.at(t_begin + j) * kTok;
+          const uint32_t src = raw + buf * C::kRawBytes, dst = ring + slot * C::kTileBytes;
+#pragma unroll 2
+          for (int i = th; i < kTok * kChunks; i += 128) {
+            const int r = i / kChunks, c = i % kChunks;
+            uint4 w = *reinterpret_cast<const uint4*>(generic + (swizzled<(D < 128 ? 64 : 128)>(src, kTok, r, c) - smem));
+            if (look) {
+              // NaN codes are 0x7f and 0xff; the chunk that holds one is cleared
+              uint32_t nan = 0;
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const uint32_t y = q == 0 ? w.x : q == 1 ? w.y : q == 2 ? w.z : w.w;
+                nan |= __vcmpeq4(y & 0x7f7f7f7fu, 0x7f7f7f7fu);
+              }
+              if (nan) {
+                if (seen(j0 + r)) sh.odd = 1;
+                w = make_uint4(0, 0, 0, 0);
+              }
+            }
+            const uint4 lo = make_uint4(e4m3_to_f16x2(w.x & 0xffffu), e4m3_to_f16x2(w.x >> 16), e4m3_to_f16x2(w.y & 0xffffu), e4m3_to_f16x2(w.y >> 16));
+            const uint4 hi = make_uint4(e4m3_to_f16x2(w.z & 0xffffu), e4m3_to_f16x2(w.z >> 16), e4m3_to_f16x2(w.w & 0xffffu), e4m3_to_f16x2(w.w >> 16));
+            // the upper half of a row's threads store their second chunk first: eight lanes then cover all banks
+            const bool swap = c >= kChunks / 2;
+            *reinterpret_cast<uint4*>(generic + (swizzled<128>(dst, kTok, r, 2 * c + (swap ? 1 : 0)) - smem)) = swap ? hi : lo;
+            *reinterpret_cast<uint4*>(generic + (swizzled<128>(dst, kTok, r, 2 * c + (swap ? 0 : 1)) - smem)) = swap ? lo : hi;
+          }
+          fence_proxy_async_smem();
+          mbar_arrive(&sh.full[slot]);
+          mbar_arrive(&sh.raw_empty[buf]);
+        }
+      }
+    }
+  }
+  __syncwarp();
+  __syncthreads();
+  if (splits > 1) cluster_sync();
+  if (warp == 9) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
+  bool slow = false;
+  for (int r = 0; r < splits; ++r) slow |= (splits > 1 ? __float_as_int(ld_cluster_f32(smem_u32(&sh.odd), r)) : sh.odd) != 0;
+  if (warp < 8) {
+    if (slow) {
+      for (int r = row0 + rank * 8 + warp; r < row_end; r += splits * 8)
+        attend_row<D, BITS>(a, b, s, r / a.group, kvh * a.group + r % a.group, lane);
+    } else if (splits > 1) {
+      // join the blocks of the cluster: a warp per row
+      for (int r = rank * 8 + warp; r < row_end - row0; r += splits * 8) {
+        float mx = -INFINITY;
+        for (int c = 0; c < splits; ++c) mx = fmaxf(mx, ld_cluster_f32(smem_u32(&sh.m[0][0] + r), c));
+        float sum = 0.f, o[D / 32];
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
+        for (int c = 0; c < splits; ++c) {
+          const float mc = ld_cluster_f32(smem_u32(&sh.m[0][0] + r), c);
+          const float f = mc == mx ? 1.f : exp2_fast(mc - mx);
+          sum += ld_cluster_f32(smem_u32(&sh.l[0][0] + r), c) * f;
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i)
+            o[i] = fmaf(ld_cluster_f32(smem + (r * C::kPartRow + lane * (D / 32) + i) * 4, c), f, o[i]);
+        }
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const int gr = row0 + r;
+        uint16_t* dst = a.out + (int64_t)(s.first + gr / a.group) * a.o_token + (int64_t)(kvh * a.group + gr % a.group) * a.o_head + lane * (D / 32);
+#pragma unroll
+        for (int i = 0; i < D / 32; i += 2) *reinterpret_cast<uint32_t*>(dst + i) = sum == 0.f ? 0u : pack_bf16(o[i] * inv, o[i + 1] * inv);
+      }
+    }
+  }
+  if (splits > 1) {
+    __syncwarp();
+    cluster_sync();  // no block leaves while another reads its shared memory
+  }
+}
+
+template <int D, int BITS, int TILES>
+cudaError_t launch(const AttendParams& a, cudaStream_t st) {
+  using C = Cfg<D, BITS>;
+  PageMaps maps;
+  if (make_page_maps(a.c, D, BITS, std::min(a.c.page_size, kTok), &maps)) return cudaErrorInvalidValue;
+  auto* f = k_attend_many<D, BITS, TILES>;
+  // a cluster's blocks keep their accumulators where Q and the ring were
+  const int join = TILES * kRows * C::kPartRow * 4 + 1024;
+  const int smem = std::max(C::smem(TILES), join);
+  cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const int64_t rows = (int64_t)a.c.max_q * a.group;
+  const int64_t q_blocks = (rows + TILES * kRows - 1) / (TILES * kRows);
+  const int64_t blocks = q_blocks * a.c.n_kv_heads * a.c.batch;
+  int64_t tokens = (int64_t)a.c.max_pages << a.c.page_shift;
+  if (a.window > 0) tokens = std::min<int64_t>(tokens, (int64_t)a.window + TILES * kRows / a.group + a.sinks + 2 * kTok);
+  int splits = 1;
+  while (splits < 8 && 2 * splits * blocks <= 152 && splits * 4 * kTok <= tokens) splits *= 2;
+  cudaLaunchConfig_t cfg{};
+  if (splits * q_blocks * a.c.n_kv_heads > 0x7fffffff || rows > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  cfg.gridDim = dim3((unsigned)(splits * q_blocks * a.c.n_kv_heads), a.c.batch);
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = splits;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, f, a, maps, (int)q_blocks, splits);
+}
+
+template <int D, int BITS>
+cudaError_t launch_rows(const AttendParams& a, cudaStream_t st) {
+  return (int64_t)a.c.max_q * a.group <= kRows ? launch<D, BITS, 1>(a, st) : launch<D, BITS, 2>(a, st);
+}
+
+}  // namespace
+
+cudaError_t launch_attend_many(const AttendParams& a, int head_dim, int kv_bits, cudaStream_t st) {
+  if (head_dim == 128) return kv_bits == 16 ? launch_rows<128, 16>(a, st) : launch_rows<128, 8>(a, st);
+  return kv_bits == 16 ? launch_rows<64, 16>(a, st) : launch_rows<64, 8>(a, st);
+}
+
+}  // namespace clo
