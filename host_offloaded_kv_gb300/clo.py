@@ -325,28 +325,51 @@ def clo_rope_plan_init(cfg: clo_rope_config | None = None, **fields) -> clo_rope
 _ROPE_FIELDS = {n for n, _ in clo_rope_config._fields_}
 
 
-def _device_of(t, name: str) -> int:
-    """Index of the current device, after checking that t is a tensor on it."""
-    import torch
+# The calls below run once per layer and step, so their checks are straight-line: what is right costs a few attribute
+# reads, what is wrong is named by the slower functions.  torch is imported with the first of them.
+torch = None
+_BF16 = None
 
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+
+def _load_torch() -> None:
+    global torch, _BF16
+    import torch as module
+
+    module.cuda.current_device()  # raises where there is no GPU
+    torch, _BF16 = module, module.bfloat16
+
+
+def _tensor_fault(t, name: str, dev: int) -> None:
+    import torch as module
+
+    if not isinstance(t, module.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    dev = torch.cuda.current_device()
     if t.get_device() != dev:
         raise ValueError(f"{name} is on {t.device}, not on the current device")
+
+
+def _device_of(t, name: str) -> int:
+    """Index of the current device, after checking that t is a tensor on it."""
+    if torch is None:
+        import torch as module
+
+        if not isinstance(t, module.Tensor) or not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        _load_torch()
+    dev = torch._C._cuda_getDevice()
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        _tensor_fault(t, name, dev)
     return dev
 
 
 def _rows(t, name: str, dev: int, shape=None) -> clo_rows:
     """A bf16 [n_tokens][n_heads][head_dim] tensor (any strides but the last) as the library takes it."""
-    import torch
-
     if not isinstance(t, torch.Tensor) or t.get_device() != dev:
-        raise ValueError(f"{name} must be a CUDA tensor on the current device")
-    if t.dtype is not torch.bfloat16:
+        _tensor_fault(t, name, dev)
+    if t.dtype is not _BF16:
         raise ValueError(f"{name} has dtype {t.dtype}; expected torch.bfloat16")
-    if t.dim() != 3 or (shape is not None and tuple(t.shape) != shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}; expected {shape or '[n_tokens][n_heads][head_dim]'}")
+    if t.dim() != 3 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}; expected {tuple(shape) if shape else '[n_tokens][n_heads][head_dim]'}")
     st, sh, sd = t.stride()
     if sd != 1 and t.shape[2] > 1:
         raise ValueError(f"{name} must be contiguous along head_dim")
@@ -359,22 +382,20 @@ def _refuse_folded(t, name: str) -> None:
         raise ValueError(f"{name} is written and must not be an expanded tensor")
 
 
-def _index(t, name: str, dev: int, dtype, numel=None):
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be a CUDA tensor on the current device")
+def _index(t, name: str, dev: int, dtype, numel: int):
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        _tensor_fault(t, name, dev)
     if t.dtype is not dtype:
         raise ValueError(f"{name} has dtype {t.dtype}; expected {dtype}")
-    if t.dim() != 1 or not t.is_contiguous() or (numel is not None and t.numel() != numel):
+    if t.dim() != 1 or t.shape[0] != numel or (numel > 1 and t.stride(0) != 1):
         raise ValueError(f"{name} has shape {tuple(t.shape)}; expected a contiguous vector of {numel}")
     return t.data_ptr()
 
 
 def _stream_of(stream, dev: int):
     """A stream's handle; None is torch's current stream, an integer is passed through."""
-    import torch
-
     if stream is None:
-        return torch.cuda.current_stream(dev).cuda_stream
+        return torch._C._cuda_getCurrentRawStream(dev)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -383,19 +404,18 @@ def clo_rope(plan: clo_rope_plan, x, positions, out=None, transpose: bool = Fals
 
     out: rows of the same shape, x itself for in place, or None for new ones.  transpose applies the
     transposed rotation, which takes the gradient of the output to that of x.  Returns out."""
-    import torch
-
     dev = _device_of(x, "x")
     xr = _rows(x, "x", dev)
     if out is None:
-        out = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+        out = torch.empty_like(x)
     else:
         _refuse_folded(out, "out")
-    yr = _rows(out, "out", dev, tuple(x.shape))
-    n, h, d = x.shape
-    pp = _index(positions, "positions", dev, torch.int64, n)
-    _check(load_library().clo_rope(ctypes.byref(plan), ctypes.byref(xr), ctypes.byref(yr), pp, n, h, d, int(bool(transpose)),
-                                   _stream_of(stream, dev)), "clo_rope")
+    n, h, d = shape = x.shape
+    status = (_lib or load_library()).clo_rope(
+        ctypes.byref(plan), ctypes.byref(xr), ctypes.byref(_rows(out, "out", dev, shape)),
+        _index(positions, "positions", dev, torch.int64, n), n, h, d, 1 if transpose else 0, _stream_of(stream, dev))
+    if status:
+        _check(status, "clo_rope")
     return out
 
 
@@ -412,8 +432,7 @@ class PagedCache:
     torch's current stream."""
 
     def __init__(self, k_pages, v_pages, k_scales=None, v_scales=None):
-        import torch
-
+        load_library()
         self.device = _device_of(k_pages, "k_pages")
         _device_of(v_pages, "v_pages")
         if k_pages.dtype not in (torch.bfloat16, torch.float8_e4m3fn) or v_pages.dtype is not k_pages.dtype:
@@ -442,10 +461,10 @@ class PagedCache:
     @classmethod
     def create(cls, n_pages: int, n_kv_heads: int, page_size: int, head_dim: int, kv_bits: int = 16, device=None):
         """A cache of new pages (their contents are undefined until they are appended to)."""
-        import torch
-
         if kv_bits not in (16, 8):
             raise ValueError("kv_bits must be 16 or 8")
+        if torch is None:
+            _load_torch()
         device = torch.device("cuda", torch.cuda.current_device()) if device is None else device
         shape = (n_pages, n_kv_heads, page_size, head_dim)
         if kv_bits == 16:
@@ -454,87 +473,91 @@ class PagedCache:
                    *(torch.ones((n_pages, n_kv_heads), dtype=torch.float32, device=device) for _ in range(2)))
 
     def _batch(self, dev, q_starts, kv_lens, block_table, total: int, max_q) -> clo_paged_batch:
-        import torch
-
         if dev != self.device:
             raise ValueError(f"the cache is on device {self.device}, the call's rows on {dev}")
-        batch = kv_lens.shape[0]
-        if block_table.get_device() != dev or block_table.dtype is not torch.int32 or block_table.dim() != 2 or \
-                block_table.shape[0] != batch or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
-            raise ValueError(f"block_table must be an int32 CUDA tensor [{batch}][max_pages] on the current device with "
-                             "contiguous rows")
-        return clo_paged_batch(_index(q_starts, "q_starts", dev, torch.int32, batch + 1),
-                               _index(kv_lens, "kv_lens", dev, torch.int32, batch), block_table.data_ptr(),
-                               block_table.stride(0), block_table.shape[1], batch, total, total if max_q is None else max_q)
+        if not isinstance(kv_lens, torch.Tensor) or not isinstance(block_table, torch.Tensor):
+            raise ValueError("kv_lens and block_table must be CUDA tensors")
+        int32 = torch.int32
+        batch = kv_lens.numel()
+        if block_table.get_device() != dev or block_table.dtype is not int32 or block_table.dim() != 2:
+            raise ValueError(f"block_table must be an int32 CUDA tensor [{batch}][max_pages] on the current device")
+        rows, width = block_table.shape
+        stride, inner = block_table.stride()
+        if rows != batch or (inner != 1 and width > 1):
+            raise ValueError(f"block_table must have {batch} contiguous rows")
+        return clo_paged_batch(_index(q_starts, "q_starts", dev, int32, batch + 1), _index(kv_lens, "kv_lens", dev, int32, batch),
+                               block_table.data_ptr(), stride, width, batch, total, total if max_q is None else max_q)
 
     def append(self, k, v, q_starts, kv_lens, block_table, rope: clo_rope_plan | None = None, positions=None, q=None,
                q_out=None, max_q=None, stream=None):
         """clo_paged_append: k, v bf16 [total][n_kv_heads][head_dim] into the pages, k rotated by rope; with
         q, returns the rotated queries (q_out, or new rows)."""
-        import torch
-
         dev = _device_of(k, "k")
+        byref = ctypes.byref
         total = k.shape[0]
-        kr = _rows(k, "k", dev, (total, self.n_kv_heads, self.head_dim))
-        vr = _rows(v, "v", dev, (total, self.n_kv_heads, self.head_dim))
+        shape = (total, self.n_kv_heads, self.head_dim)
+        kr = _rows(k, "k", dev, shape)
+        vr = _rows(v, "v", dev, shape)
         b = self._batch(dev, q_starts, kv_lens, block_table, total, max_q)
         qr = yr = None
         heads = 0
         if q is not None:
-            if q.dim() != 3:
-                raise ValueError("q must be [total][n_q_heads][head_dim]")
-            heads = q.shape[1]
+            qr = _rows(q, "q", dev)
+            shape = q.shape
+            heads = shape[1]
+            if shape[0] != total or shape[2] != self.head_dim:
+                raise ValueError(f"q has shape {tuple(shape)}; expected [{total}][n_q_heads][{self.head_dim}]")
             if q_out is None:
-                q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+                q_out = torch.empty_like(q)
             else:
                 _refuse_folded(q_out, "q_out")
-            qr = ctypes.byref(_rows(q, "q", dev, (total, heads, self.head_dim)))
-            yr = ctypes.byref(_rows(q_out, "q_out", dev, (total, heads, self.head_dim)))
+            qr, yr = byref(qr), byref(_rows(q_out, "q_out", dev, shape))
         elif q_out is not None:
             raise ValueError("q_out without q")
-        _check(load_library().clo_paged_append(
-            self._ref, ctypes.byref(b), None if rope is None else ctypes.byref(rope),
-            None if positions is None else _index(positions, "positions", dev, torch.int64, total), ctypes.byref(kr),
-            ctypes.byref(vr), qr, yr, heads, _stream_of(stream, dev)), "clo_paged_append")
+        status = _lib.clo_paged_append(
+            self._ref, byref(b), None if rope is None else byref(rope),
+            None if positions is None else _index(positions, "positions", dev, torch.int64, total), byref(kr), byref(vr),
+            qr, yr, heads, _stream_of(stream, dev))
+        if status:
+            _check(status, "clo_paged_append")
         return q_out
 
     def read(self, q_starts, kv_lens, block_table, total: int, k_out=None, v_out=None, max_q=None, stream=None):
         """clo_paged_read: the batch's last tokens as bf16 (k, v), each [total][n_kv_heads][head_dim]."""
-        import torch
-
         dev = _device_of(kv_lens, "kv_lens")
-        shape = (int(total), self.n_kv_heads, self.head_dim)
-        outs = []
-        for name, t in (("k_out", k_out), ("v_out", v_out)):
-            if t is None:
-                t = torch.empty(shape, dtype=torch.bfloat16, device=kv_lens.device)
-            else:
-                _refuse_folded(t, name)
-            outs.append((t, _rows(t, name, dev, shape)))
-        b = self._batch(dev, q_starts, kv_lens, block_table, int(total), max_q)
-        _check(load_library().clo_paged_read(self._ref, ctypes.byref(b), ctypes.byref(outs[0][1]), ctypes.byref(outs[1][1]),
-                                             _stream_of(stream, dev)), "clo_paged_read")
-        return outs[0][0], outs[1][0]
+        shape = (total, self.n_kv_heads, self.head_dim)
+        if k_out is None:
+            k_out = torch.empty(shape, dtype=_BF16, device=kv_lens.device)
+        else:
+            _refuse_folded(k_out, "k_out")
+        if v_out is None:
+            v_out = torch.empty(shape, dtype=_BF16, device=kv_lens.device)
+        else:
+            _refuse_folded(v_out, "v_out")
+        b = self._batch(dev, q_starts, kv_lens, block_table, total, max_q)
+        status = _lib.clo_paged_read(self._ref, ctypes.byref(b), ctypes.byref(_rows(k_out, "k_out", dev, shape)),
+                                     ctypes.byref(_rows(v_out, "v_out", dev, shape)), _stream_of(stream, dev))
+        if status:
+            _check(status, "clo_paged_read")
+        return k_out, v_out
 
     def attention(self, q, q_starts, kv_lens, block_table, out=None, max_q=None, softmax_scale: float = 0.0, window: int = 0,
                   sinks: int = 0, stream=None):
         """clo_paged_attention: q bf16 [total][n_q_heads][head_dim] over the pages; returns out (or new rows)."""
-        import torch
-
         dev = _device_of(q, "q")
         qr = _rows(q, "q", dev)
-        total, heads, d = q.shape
+        total, heads, d = shape = q.shape
         if d != self.head_dim:
             raise ValueError(f"q has head_dim {d}; the cache has {self.head_dim}")
         if out is None:
-            out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+            out = torch.empty_like(q)
         else:
             _refuse_folded(out, "out")
-        orow = _rows(out, "out", dev, (total, heads, d))
         b = self._batch(dev, q_starts, kv_lens, block_table, total, max_q)
-        _check(load_library().clo_paged_attention(self._ref, ctypes.byref(b), ctypes.byref(qr), ctypes.byref(orow), heads,
-                                                  softmax_scale, window, sinks, _stream_of(stream, dev)),
-               "clo_paged_attention")
+        status = _lib.clo_paged_attention(self._ref, ctypes.byref(b), ctypes.byref(qr), ctypes.byref(_rows(out, "out", dev, shape)),
+                                          heads, softmax_scale, window, sinks, _stream_of(stream, dev))
+        if status:
+            _check(status, "clo_paged_attention")
         return out
 
 

@@ -82,14 +82,16 @@ __device__ __forceinline__ int seq_of_row(const PagedParams& p, int t, int lane)
 }
 
 // cos and sin of position * turn: the product modulo 2^64 is the angle as a fraction of a turn, so far
-// positions lose nothing.  Its top 23 bits go to the hardware sine and cosine, whose absolute error on
-// [-pi, pi] is below 2^-21; both are far below the half ulp (2^-9) of the bf16 results.
+// positions lose nothing.  Its upper 32 bits, as half turns in [-1, 1), go through one rounding to fp32.
 __device__ __forceinline__ float2 rope_cos_sin(int64_t pos, uint64_t turn, float magnitude) {
   const uint32_t lo = (uint32_t)turn, hi = (uint32_t)(turn >> 32);
   const uint32_t plo = (uint32_t)pos, phi = (uint32_t)((uint64_t)pos >> 32);
-  const uint32_t frac = __umulhi(plo, lo) + plo * hi + phi * lo + 0x80000000u;
-  const float a = (__uint_as_float(0x3f800000u | (frac >> 9)) - 1.5f) * 6.283185307179586f;
-  return make_float2(__cosf(a) * magnitude, __sinf(a) * magnitude);
+  const uint32_t frac = __umulhi(plo, lo) + plo * hi + phi * lo;
+  float2 r;
+  sincospif((float)(int32_t)frac * 4.656612873077393e-10f, &r.y, &r.x);
+  r.x *= magnitude;
+  r.y *= magnitude;
+  return r;
 }
 
 __device__ __forceinline__ void unpack8(const uint4 v, float* x) {

@@ -1,6 +1,8 @@
 // Device parts shared by the two attention kernels over paged caches.
 #pragma once
 
+#include <atomic>
+
 #include "clo_paged.cuh"
 
 namespace clo {
@@ -65,6 +67,15 @@ __device__ __forceinline__ bool not_finite2(uint32_t x) {
   return (x & E) == E || ((x >> 16) & E) == E;
 }
 
+template <int BITS>
+__device__ __forceinline__ bool not_finite16(const uint4 w) {
+  if (BITS == 16) return not_finite2<16>(w.x) || not_finite2<16>(w.y) || not_finite2<16>(w.z) || not_finite2<16>(w.w);
+  uint32_t nan = 0;  // codes 0x7f and 0xff
+#pragma unroll
+  for (int i = 0; i < 4; ++i) nan |= __vcmpeq4((i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w) & 0x7f7f7f7fu, 0x7f7f7f7fu);
+  return nan != 0;
+}
+
 // The tiles that some row of a unit sees: [0, sink_tiles) and [first, first + rest).
 struct TileList {
   int sink_tiles, first, rest;
@@ -84,6 +95,30 @@ __device__ __forceinline__ TileList tiles_of(int pos_first, int pos_last, int kv
   return t;
 }
 
+constexpr int kSms = 152;  // GB300
+
+// Sets a kernel's shared-memory size and cluster limit, once per device (`prepared`: a bit each).
+cudaError_t prepare_kernel(const void* f, int smem, std::atomic<uint64_t>* prepared);
+
+// One launch; clusters of `cluster` blocks along x where that is more than one.
+template <typename... Params, typename... Args>
+cudaError_t launch_cluster(void (*f)(Params...), dim3 grid, int threads, int smem, int cluster, cudaStream_t st, const Args&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = cluster;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = cluster > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, f, args...);
+}
+
+cudaError_t launch_attend_few_bf16(const AttendParams& a, int head_dim, int rows, cudaStream_t st);
+cudaError_t launch_attend_few_e4m3(const AttendParams& a, int head_dim, int rows, cudaStream_t st);
 cudaError_t launch_attend_many(const AttendParams& a, int head_dim, int kv_bits, cudaStream_t st);
 
 }  // namespace clo

@@ -15,502 +15,6 @@
 namespace clo {
 namespace {
 
-constexpr int kThreads = 128;
-
-
-// ---------------------------------------------------------------------------- few rows per kv head
-// Decode: the rows of a (sequence, kv head) unit, at most 8 * NT of them, read every visible K and V row once, so HBM
-// bounds the kernel and the products run on mma.sync m16n8k16 fragments: S^T = K Q^T (16 tokens by 8 rows), O^T = V^T P^T
-// (16 elements by 8 rows), which waste none of the 16-wide side on absent rows; the weights pass from one product to the next
-// with movmatrix.
-//
-// Each warp owns a ring of kStages 8 KB stages (16 tokens of bf16 K and V rows of 128, 64 tokens of 8-bit rows of 64) that its
-// lanes fill with TMA boxes, so no warp waits for another before the end.  The tiles of a unit go round the warps of
-// a cluster of 1 to 16 blocks; warps join through shared memory, blocks through distributed shared memory: one launch, no
-// workspace, a fixed order of sums.
-constexpr int kWarps = kThreads / 32;
-constexpr int kStages = 3;
-constexpr int kStageBytes = 8192;
-
-template <int D, int BITS>
-struct Tile {
-  static constexpr int kRowBytes = D * BITS / 8;
-  static constexpr int kSpan = kRowBytes < 128 ? kRowBytes : 128;  // bytes of a row in one swizzled block
-  static constexpr int kSpans = kRowBytes / kSpan;
-  static constexpr int kTokens = kStageBytes / (2 * kRowBytes);
-  static constexpr int kM = kTokens / 16;
-  static constexpr int kSideBytes = kTokens * kRowBytes;
-};
-
-__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t* r) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-}
-__device__ __forceinline__ void ldsm4_trans(uint32_t addr, uint32_t* r) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-}
-__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
-  uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-  return y;
-}
-template <int BITS>
-__device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
-  if (BITS == 16)
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  else
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-template <int D, int BITS, int NT>
-__global__ void __launch_bounds__(kThreads) k_attend_few(const AttendParams a, const __grid_constant__ PageMaps maps) {
-  using T = Tile<D, BITS>;
-  constexpr int TOK = T::kTokens, KM = T::kM, KD = D / 16, ROWS = 8 * NT;
-  constexpr float kOff = BITS == 16 ? 0.f : 14.f;  // weights up to 2^14: fp16 holds them down to 2^-38 of the largest
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t s_full[kWarps][kStages];
-  __shared__ __align__(16) float s_scale[kWarps][kStages][2][4];
-  __shared__ uint32_t s_there[kWarps][kStages];
-  __shared__ float s_m[kWarps][ROWS], s_l[kWarps][ROWS];
-  __shared__ float s_cm[ROWS], s_cl[ROWS];
-  __shared__ int s_odd;
-
-  const PagedParams& p = a.c;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
-  const int kvh = blockIdx.y, b = blockIdx.z;
-  const SeqRows s = seq_rows(p, b);
-  const int rows = s.n * a.group;
-  if (rows == 0) return;  // the whole cluster
-  const int splits = gridDim.x, rank = splits > 1 ? (int)cluster_rank() : 0;
-
-  const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t ring = smem + warp * kStages * kStageBytes;
-  if (tid == 0) s_odd = 0;
-  if (lane == 0) {
-#pragma unroll
-    for (int i = 0; i < kStages; ++i) mbar_init(&s_full[warp][i], 1);
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-  }
-  __syncthreads();
-
-  const TileList tl = tiles_of(s.pos0, s.pos0 + s.n - 1, s.kv_len, a.window, a.sinks, TOK);
-  const int stride = splits * kWarps, k0 = rank * kWarps + warp, n_tiles = tl.count();
-
-  // Page of 16-token group `lane` of tile k, for the lanes below KM (the others: -1).
-  auto page_for = [&](int k) {
-    return lane < KM && k < n_tiles ? page_of(p, b, (tl.at(k) * TOK + lane * 16) >> p.page_shift) : -1;
-  };
-  auto issue = [&](int k, int page, int st) {
-    const unsigned there = __ballot_sync(0xffffffffu, page >= 0);
-    if (lane == 0) {
-      s_there[warp][st] = there;
-      mbar_arrive_expect_tx(&s_full[warp][st], kStageBytes);
-    }
-    __syncwarp();
-    if (lane < KM) {
-      if (BITS == 8 && page >= 0) {
-        const int64_t at = (int64_t)page * p.n_kv_heads + kvh;
-#pragma unroll
-        for (int side = 0; side < 2; ++side)
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(&s_scale[warp][st][side][lane])), "l"(p.side[side].scales + at) : "memory");
-      }
-      const int box = min(p.page_size, TOK);
-      const int tok = lane * 16;
-      if (tok % box == 0) {
-        const int slot = (tl.at(k) * TOK + tok) & (p.page_size - 1);
-#pragma unroll
-        for (int side = 0; side < 2; ++side)
-#pragma unroll
-          for (int h = 0; h < T::kSpans; ++h)
-            tma_box(ring + st * kStageBytes + side * T::kSideBytes + h * TOK * T::kSpan + tok * T::kSpan, &maps.side[side],
-                    h * (T::kSpan * 8 / BITS), slot, kvh, page, smem_u32(&s_full[warp][st]));
-      }
-    }
-    if (BITS == 8) cp_async_commit();
-  };
-
-  int page_next[kStages];
-#pragma unroll
-  for (int i = 0; i < kStages; ++i) page_next[i] = page_for(k0 + i * stride);
-#pragma unroll
-  for (int i = 0; i < kStages; ++i) {
-    if (k0 + i * stride < n_tiles) issue(k0 + i * stride, page_next[i], i);
-    else if (BITS == 8) cp_async_commit();
-  }
-  int page_ahead = page_for(k0 + kStages * stride);
-
-  // Q^T fragments: column (row of the unit) nt * 8 + g.  bf16: elements kk * 16 + 2 t4 + {0, 1} and + 8.  8-bit pages: the lane's
-  // four codes of a 16-element chunk are neighbours, so elements kk * 16 + 4 t4 + {0, 1} and {2, 3}; q in fp16, scaled by
-  // a power of two that puts the row's largest finite element into [2^14, 2^15).
-  uint32_t qf[NT][KD][2];
-  float fac[NT][2];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int r = nt * 8 + g;
-    const uint16_t* qp = a.q + (int64_t)(s.first + r / a.group) * a.q_token + (int64_t)(kvh * a.group + r % a.group) * a.q_head;
-    float row_fac = a.scale_log2;
-    if (BITS == 16) {
-#pragma unroll
-      for (int kk = 0; kk < KD; ++kk) {
-        qf[nt][kk][0] = r < rows ? *reinterpret_cast<const uint32_t*>(qp + kk * 16 + 2 * t4) : 0u;
-        qf[nt][kk][1] = r < rows ? *reinterpret_cast<const uint32_t*>(qp + kk * 16 + 2 * t4 + 8) : 0u;
-      }
-    } else {
-      uint2 raw[KD];
-      float mx = 0.f;
-#pragma unroll
-      for (int kk = 0; kk < KD; ++kk) {
-        raw[kk] = r < rows ? *reinterpret_cast<const uint2*>(qp + kk * 16 + 4 * t4) : make_uint2(0u, 0u);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t w = i < 2 ? raw[kk].x : raw[kk].y;
-          const float v = fabsf(__uint_as_float(i & 1 ? w & 0xffff0000u : w << 16));
-          mx = fmaxf(mx, v < INFINITY ? v : 0.f);
-        }
-      }
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127 - 14, -100), 112);
-      const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-      row_fac *= __uint_as_float((uint32_t)(127 + e) << 23);
-#pragma unroll
-      for (int kk = 0; kk < KD; ++kk) {
-        qf[nt][kk][0] = pack_f16(__uint_as_float(raw[kk].x << 16) * down, __uint_as_float(raw[kk].x & 0xffff0000u) * down);
-        qf[nt][kk][1] = pack_f16(__uint_as_float(raw[kk].y << 16) * down, __uint_as_float(raw[kk].y & 0xffff0000u) * down);
-      }
-    }
-    fac[nt][0] = __shfl_sync(0xffffffffu, row_fac, 8 * t4);
-    fac[nt][1] = __shfl_sync(0xffffffffu, row_fac, 8 * t4 + 4);
-  }
-
-  float acc[KD][NT][4], m[NT][2], l[NT][2];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      m[nt][i] = -INFINITY;
-      l[nt][i] = 0.f;
-    }
-#pragma unroll
-    for (int dt = 0; dt < KD; ++dt)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[dt][nt][i] = 0.f;
-  }
-  const Visible va = visible_of(s.pos0, s.kv_len, a.window, a.sinks);
-  const Visible vz = visible_of(s.pos0 + s.n - 1, s.kv_len, a.window, a.sinks);
-  bool odd = false, ok = true;
-  int st = 0;
-  uint32_t phase = 0;
-
-  for (int k = k0; k < n_tiles; k += stride) {
-    if (BITS == 8) cp_async_wait<kStages - 1>();
-    __syncwarp();
-    ok = mbar_wait_limited(&s_full[warp][st], phase);
-    if (!__all_sync(0xffffffffu, ok)) {
-      ok = false;
-      break;
-    }
-    const uint32_t kb = ring + st * kStageBytes, vb = kb + T::kSideBytes;
-    const int j0 = tl.at(k) * TOK;
-    const uint32_t there = s_there[warp][st];
-    // every row sees the whole tile
-    const bool whole = there == (1u << KM) - 1u && j0 + TOK <= va.hi && (j0 >= vz.lo || j0 + TOK <= (a.window > 0 ? a.sinks : 0));
-
-    float sc[KM][NT][4];
-#pragma unroll
-    for (int mt = 0; mt < KM; ++mt) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sc[mt][nt][i] = 0.f;
-      if (BITS == 16) {
-#pragma unroll
-        for (int kk = 0; kk < KD; ++kk) {
-          uint32_t f[4];
-          ldsm4(swizzled<T::kSpan>(kb, TOK, mt * 16 + (lane & 15), kk * 2 + (lane >> 4)), f);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma16816<BITS>(sc[mt][nt], f, qf[nt][kk][0], qf[nt][kk][1]);
-        }
-      } else {
-#pragma unroll
-        for (int kk = 0; kk < KD; kk += 2) {
-          uint32_t r[4];
-          ldsm4(swizzled<T::kSpan>(kb, TOK, mt * 16 + (lane & 15), kk + (lane >> 4)), r);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t f[4] = {e4m3_to_f16x2(r[2 * i] & 0xffffu), e4m3_to_f16x2(r[2 * i + 1] & 0xffffu), e4m3_to_f16x2(r[2 * i] >> 16),
-                                   e4m3_to_f16x2(r[2 * i + 1] >> 16)};
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma16816<BITS>(sc[mt][nt], f, qf[nt][kk + i][0], qf[nt][kk + i][1]);
-          }
-        }
-      }
-    }
-
-    // Scores in log2 units.  8-bit pages: the page's V scale joins the exponent, so that the weights times the codes keep the
-    // accumulator in range, and leaves the sum by its reciprocal.
-    float inv_vs[KM];
-#pragma unroll
-    for (int mt = 0; mt < KM; ++mt) {
-      float ks = 1.f, lvs = 0.f;
-      inv_vs[mt] = 1.f;
-      if (BITS == 8) {
-        ks = fmaxf(s_scale[warp][st][0][mt], kMinScale);
-        const float vs = fmaxf(s_scale[warp][st][1][mt], kMinScale);
-        lvs = __log2f(vs);
-        inv_vs[mt] = __frcp_rn(vs);
-      }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float f = fac[nt][i & 1] * ks;
-          sc[mt][nt][i] = BITS == 8 ? fmaf(sc[mt][nt][i], f, lvs) : sc[mt][nt][i] * f;
-          if (!whole) {
-            const int j = j0 + mt * 16 + g + (i >> 1) * 8;
-            const int pos = s.pos0 + (nt * 8 + 2 * t4 + (i & 1)) / a.group;
-            const bool see = (there >> mt & 1u) && j <= pos && j < s.kv_len && (a.window == 0 || j > pos - a.window || j < a.sinks);
-            if (!see) sc[mt][nt][i] = -INFINITY;
-          }
-        }
-    }
-    uint32_t pf[KM][NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float keep[2], ref[2];
-      bool moved = false;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float mx = sc[0][nt][i];
-#pragma unroll
-        for (int mt = 0; mt < KM; ++mt) mx = fmaxf(mx, fmaxf(sc[mt][nt][i], sc[mt][nt][i + 2]));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-        const float mn = fmaxf(m[nt][i], mx);
-        moved |= mn != m[nt][i];
-        keep[i] = m[nt][i] == mn ? 1.f : exp2_fast(m[nt][i] - mn);
-        m[nt][i] = mn;
-        ref[i] = mn == -INFINITY ? 0.f : mn - kOff;
-      }
-      if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) l[nt][i] *= keep[i];
-#pragma unroll
-        for (int dt = 0; dt < KD; ++dt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[dt][nt][i] *= keep[i & 1];
-      }
-#pragma unroll
-      for (int mt = 0; mt < KM; ++mt) {
-        float w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          w[i] = exp2_fast(sc[mt][nt][i] - ref[i & 1]);
-          l[nt][i & 1] = BITS == 8 ? fmaf(w[i], inv_vs[mt], l[nt][i & 1]) : l[nt][i & 1] + w[i];
-        }
-        // weights in the products' type: bf16 next to bf16 V, fp16 next to 8-bit V (three bits more, and V is exact in it)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t two = BITS == 16 ? pack_bf16(w[2 * i], w[2 * i + 1]) : pack_f16(w[2 * i], w[2 * i + 1]);
-          pf[mt][nt][i] = transpose8x8(two);
-        }
-      }
-    }
-
-#pragma unroll
-    for (int mt = 0; mt < KM; ++mt) {
-      // V of tokens that no row sees is cleared: its weight is zero, but zero times NaN is not
-      uint32_t see[2] = {0xffffffffu, 0xffffffffu};
-      if (!whole) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int j = j0 + mt * 16 + 2 * t4 + (i & 1) + (i >> 1) * 8;
-          const bool any = (there >> mt & 1u) && j < vz.hi && (j >= va.lo || j < (a.window > 0 ? a.sinks : 0));
-          if (!any) see[i >> 1] &= i & 1 ? 0x0000ffffu : 0xffff0000u;
-        }
-      }
-#pragma unroll
-      for (int dt = 0; dt < KD; ++dt) {
-        uint32_t f[4];
-        if (BITS == 16) {
-          ldsm4_trans(swizzled<T::kSpan>(vb, TOK, mt * 16 + (lane & 7) + (lane >> 4) * 8, dt * 2 + (lane >> 3 & 1)), f);
-        } else {
-          // two chunks per load; a lane's pairs of elements 2 g, 2 g + 1 of two tokens become rows g and g + 8
-          uint32_t r[4];
-          ldsm4_trans(swizzled<T::kSpan>(vb, TOK, mt * 16 + (lane & 15), (dt & ~1) + (lane >> 4)), r);
-          const uint32_t x = __byte_perm(r[(dt & 1) * 2], 0u, 0x3120), y = __byte_perm(r[(dt & 1) * 2 + 1], 0u, 0x3120);
-          f[0] = e4m3_to_f16x2(x & 0xffffu);
-          f[1] = e4m3_to_f16x2(x >> 16);
-          f[2] = e4m3_to_f16x2(y & 0xffffu);
-          f[3] = e4m3_to_f16x2(y >> 16);
-        }
-        if (!whole) {
-          f[0] &= see[0];
-          f[1] &= see[0];
-          f[2] &= see[1];
-          f[3] &= see[1];
-          if (s.n > 1) odd |= not_finite2<BITS>(f[0]) || not_finite2<BITS>(f[1]) || not_finite2<BITS>(f[2]) || not_finite2<BITS>(f[3]);
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma16816<BITS>(acc[dt][nt], f, pf[mt][nt][0], pf[mt][nt][1]);
-      }
-    }
-    // refill the stage
-    __syncwarp();
-    const int kn = k + kStages * stride;
-    if (kn < n_tiles) {
-      fence_proxy_async_smem();
-      issue(kn, page_ahead, st);
-      page_ahead = page_for(kn + stride);
-    } else if (BITS == 8) {
-      cp_async_commit();
-    }
-    if (++st == kStages) {
-      st = 0;
-      phase ^= 1u;
-    }
-  }
-  if (BITS == 8) cp_async_wait<0>();
-  // A wait that gave up (a copy lost): the rows become NaN.  The copies in flight get the same limit again.
-  if (!ok) {
-    for (int i = 0; i < kStages; ++i) mbar_wait_limited(&s_full[warp][i], phase);
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) l[nt][i] = __int_as_float(0x7fffffff);
-  }
-
-  // Join the warps: every warp's accumulator in its own ring.
-  float* part = reinterpret_cast<float*>(smem_raw + (smem - smem_u32(smem_raw)));
-  constexpr int kPart = kStages * kStageBytes / 4;
-  if (__any_sync(0xffffffffu, odd) && lane == 0) s_odd = 1;
-  __syncwarp();
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float v = l[nt][i];
-      v += __shfl_xor_sync(0xffffffffu, v, 4);
-      v += __shfl_xor_sync(0xffffffffu, v, 8);
-      v += __shfl_xor_sync(0xffffffffu, v, 16);
-      const int r = nt * 8 + 2 * t4 + i;
-      if (g == 0) {
-        s_m[warp][r] = m[nt][i];
-        s_l[warp][r] = v;
-      }
-#pragma unroll
-      for (int dt = 0; dt < KD; ++dt)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int e = dt * 16 + (BITS == 16 ? g + 8 * h : 2 * g + h);
-          part[warp * kPart + r * (D + 4) + e] = acc[dt][nt][i + 2 * h];
-        }
-    }
-  __syncthreads();
-  if (tid < ROWS) {
-    float mx = -INFINITY, sum = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, s_m[w][tid]);
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float f = s_m[w][tid] == mx ? 1.f : exp2_fast(s_m[w][tid] - mx);
-      sum += s_l[w][tid] * f;
-      s_m[w][tid] = f;
-    }
-    s_cm[tid] = mx;
-    s_cl[tid] = sum;
-  }
-  __syncthreads();
-  for (int e = tid; e < rows * D; e += kThreads) {
-    const int r = e / D, at = r * (D + 4) + e % D;
-    float v = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) v += part[w * kPart + at] * s_m[w][r];
-    part[at] = v;
-  }
-  if (splits > 1)
-    cluster_sync();
-  else
-    __syncthreads();
-
-  // Join the blocks: each writes its share of the rows' elements.
-  bool slow = false;
-  for (int r = 0; r < splits; ++r)
-    slow |= (splits > 1 ? __float_as_int(ld_cluster_f32(smem_u32(&s_odd), r)) : s_odd) != 0;
-  if (!slow) {
-    for (int e = rank * kThreads + tid; e < rows * (D / 2); e += splits * kThreads) {
-      const int r = e / (D / 2), d2 = e % (D / 2) * 2;
-      float o[2], sum;
-      if (splits == 1) {
-        sum = s_cl[r];
-        o[0] = part[r * (D + 4) + d2];
-        o[1] = part[r * (D + 4) + d2 + 1];
-      } else {
-        float mx = -INFINITY;
-        for (int c = 0; c < splits; ++c) mx = fmaxf(mx, ld_cluster_f32(smem_u32(&s_cm[r]), c));
-        sum = o[0] = o[1] = 0.f;
-        for (int c = 0; c < splits; ++c) {
-          const float mc = ld_cluster_f32(smem_u32(&s_cm[r]), c);
-          const float f = mc == mx ? 1.f : exp2_fast(mc - mx);
-          sum += ld_cluster_f32(smem_u32(&s_cl[r]), c) * f;
-          o[0] += ld_cluster_f32(smem_u32(part + r * (D + 4) + d2), c) * f;
-          o[1] += ld_cluster_f32(smem_u32(part + r * (D + 4) + d2 + 1), c) * f;
-        }
-      }
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      uint16_t* op = a.out + (int64_t)(s.first + r / a.group) * a.o_token + (int64_t)(kvh * a.group + r % a.group) * a.o_head + d2;
-      *reinterpret_cast<uint32_t*>(op) = sum == 0.f ? 0u : pack_bf16(o[0] * inv, o[1] * inv);
-    }
-  } else {
-    // an infinity or NaN in V that some rows see and others do not: row by row
-    for (int r = rank * kWarps + warp; r < rows; r += splits * kWarps)
-      attend_row<D, BITS>(a, b, s, r / a.group, kvh * a.group + r % a.group, lane);
-  }
-  if (splits > 1) cluster_sync();  // no block leaves while another reads its shared memory
-}
-
-template <int D, int BITS, int NT>
-cudaError_t launch_few(const AttendParams& a, cudaStream_t st) {
-  using T = Tile<D, BITS>;
-  PageMaps maps;
-  if (make_page_maps(a.c, D, BITS, min(a.c.page_size, T::kTokens), &maps)) return cudaErrorInvalidValue;
-  auto* f = k_attend_few<D, BITS, NT>;
-  constexpr int smem = kWarps * kStages * kStageBytes + 1024;
-  cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e != cudaSuccess) return e;
-  // Blocks per unit: enough to fill the GPU, no more than the tiles that a unit can have.
-  const int64_t units = (int64_t)a.c.batch * a.c.n_kv_heads;
-  int64_t tokens = (int64_t)a.c.max_pages << a.c.page_shift;
-  if (a.window > 0) tokens = std::min<int64_t>(tokens, (int64_t)a.window + a.c.max_q + a.sinks + 2 * T::kTokens);
-  int splits = 1;
-  while (splits < 16 && splits * units < 304 && splits * kWarps * T::kTokens < tokens) splits *= 2;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(splits, a.c.n_kv_heads, a.c.batch);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = splits;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, f, a, maps);
-}
-
-template <int D, int BITS>
-cudaError_t launch_any(const AttendParams& a, cudaStream_t st) {
-  const int rows = a.c.max_q * a.group;  // at most, per sequence and kv head
-  if (rows <= 8) return launch_few<D, BITS, 1>(a, st);
-  if (rows <= 16) return launch_few<D, BITS, 2>(a, st);
-  return launch_attend_many(a, D, BITS, st);
-}
 
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
                               const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -533,6 +37,18 @@ EncodeFn tensor_map_encoder() {
 
 }  // namespace
 
+cudaError_t prepare_kernel(const void* f, int smem, std::atomic<uint64_t>* prepared) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+  if (prepared->load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) prepared->fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
 const char* make_page_maps(const PagedParams& c, int head_dim, int kv_bits, int rows, PageMaps* maps) {
   EncodeFn encode = tensor_map_encoder();
   if (!encode) return "no tensor map encoder in the driver";
@@ -551,8 +67,9 @@ const char* make_page_maps(const PagedParams& c, int head_dim, int kv_bits, int 
 }
 
 cudaError_t launch_paged_attention(const AttendParams& a, int head_dim, int kv_bits, cudaStream_t st) {
-  if (head_dim == 128) return kv_bits == 16 ? launch_any<128, 16>(a, st) : launch_any<128, 8>(a, st);
-  return kv_bits == 16 ? launch_any<64, 16>(a, st) : launch_any<64, 8>(a, st);
+  const int64_t rows = (int64_t)a.c.max_q * a.group;  // at most, per sequence and kv head
+  if (rows > 32) return launch_attend_many(a, head_dim, kv_bits, st);
+  return kv_bits == 16 ? launch_attend_few_bf16(a, head_dim, (int)rows, st) : launch_attend_few_e4m3(a, head_dim, (int)rows, st);
 }
 
 }  // namespace clo

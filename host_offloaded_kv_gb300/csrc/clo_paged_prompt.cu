@@ -117,7 +117,6 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 
 template <int D, int BITS>
 struct Cfg {
-  static constexpr int kSpans = D / 64;                       // 64-element spans of an operand row
   static constexpr int kTileBytes = kTok * D * 2;             // an operand tile
   static constexpr int kQBytes = kRows * D * 2;
   static constexpr int kSlots = BITS == 16 ? 4 : 3;
@@ -538,13 +537,13 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::kThreads, 1) k_attend_many(const
             for (int r = th; r < kTok; r += 64) {
               uint8_t* row = generic + (ring - smem) + slot * C::kTileBytes + r * 128;
               bool bad = false;
-              for (int c = 0; c < C::kSpans * 8; ++c) {
+              for (int c = 0; c < D / 8; ++c) {
                 const uint4 w = *reinterpret_cast<const uint4*>(row + (c >> 3) * (kTok * 128) + (c & 7) * 16);
-                bad |= not_finite2<16>(w.x) || not_finite2<16>(w.y) || not_finite2<16>(w.z) || not_finite2<16>(w.w);
+                bad |= not_finite16<16>(w);
               }
               if (bad) {
                 if (seen(j0 + r)) sh.odd = 1;
-                for (int c = 0; c < C::kSpans * 8; ++c) *reinterpret_cast<uint4*>(row + (c >> 3) * (kTok * 128) + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+                for (int c = 0; c < D / 8; ++c) *reinterpret_cast<uint4*>(row + (c >> 3) * (kTok * 128) + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
               }
             }
             fence_proxy_async_smem();
@@ -569,13 +568,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::kThreads, 1) k_attend_many(const
             uint4 w = *reinterpret_cast<const uint4*>(generic + (swizzled<(D < 128 ? 64 : 128)>(src, kTok, r, c) - smem));
             if (look) {
               // NaN codes are 0x7f and 0xff; the chunk that holds one is cleared
-              uint32_t nan = 0;
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const uint32_t y = q == 0 ? w.x : q == 1 ? w.y : q == 2 ? w.z : w.w;
-                nan |= __vcmpeq4(y & 0x7f7f7f7fu, 0x7f7f7f7fu);
-              }
-              if (nan) {
+              if (not_finite16<8>(w)) {
                 if (seen(j0 + r)) sh.odd = 1;
                 w = make_uint4(0, 0, 0, 0);
               }
@@ -646,7 +639,8 @@ cudaError_t launch(const AttendParams& a, cudaStream_t st) {
   // a cluster's blocks keep their accumulators where Q and the ring were
   const int join = TILES * kRows * C::kPartRow * 4 + 1024;
   const int smem = std::max(C::smem(TILES), join);
-  cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> prepared{0};
+  const cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(f), smem, &prepared);
   if (e != cudaSuccess) return e;
   const int64_t rows = (int64_t)a.c.max_q * a.group;
   const int64_t q_blocks = (rows + TILES * kRows - 1) / (TILES * kRows);
@@ -654,20 +648,9 @@ cudaError_t launch(const AttendParams& a, cudaStream_t st) {
   int64_t tokens = (int64_t)a.c.max_pages << a.c.page_shift;
   if (a.window > 0) tokens = std::min<int64_t>(tokens, (int64_t)a.window + TILES * kRows / a.group + a.sinks + 2 * kTok);
   int splits = 1;
-  while (splits < 8 && 2 * splits * blocks <= 152 && splits * 4 * kTok <= tokens) splits *= 2;
-  cudaLaunchConfig_t cfg{};
+  while (splits < 8 && 2 * splits * blocks <= kSms && splits * 4 * kTok <= tokens) splits *= 2;
   if (splits * q_blocks * a.c.n_kv_heads > 0x7fffffff || rows > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  cfg.gridDim = dim3((unsigned)(splits * q_blocks * a.c.n_kv_heads), a.c.batch);
-  cfg.blockDim = dim3(C::kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = splits;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, f, a, maps, (int)q_blocks, splits);
+  return launch_cluster(f, dim3((unsigned)(splits * q_blocks * a.c.n_kv_heads), a.c.batch), C::kThreads, smem, splits, st, a, maps, (int)q_blocks, splits);
 }
 
 template <int D, int BITS>
