@@ -32,7 +32,7 @@ EXPORTED = ["clo_config_default", "clo_init", "clo_destroy", "clo_append_kv", "c
             "clo_decode_layer",
             "clo_sync", "clo_stats", "clo_last_error", "clo_debug_get", "clo_set", "clo_sparse_attention_noalloc",
             "clo_rope_config_default", "clo_rope_plan_init", "clo_rope", "clo_paged_append", "clo_paged_read",
-            "clo_paged_attention"]
+            "clo_paged_attention", "clo_paged_attention_workspace"]
 
 
 class CLOError(RuntimeError):
@@ -171,7 +171,9 @@ def load_library(path: str = LIB_PATH):
     lib.clo_paged_read.restype = ctypes.c_int
     lib.clo_paged_read.argtypes = [vp, vp, vp, vp, vp]
     lib.clo_paged_attention.restype = ctypes.c_int
-    lib.clo_paged_attention.argtypes = [vp, vp, vp, vp, i32, ctypes.c_float, i32, i32, vp]
+    lib.clo_paged_attention.argtypes = [vp, vp, vp, vp, i32, ctypes.c_float, i32, i32, vp, i64, vp]
+    lib.clo_paged_attention_workspace.restype = ctypes.c_int
+    lib.clo_paged_attention_workspace.argtypes = [vp, vp, i32, i32, i32, ctypes.POINTER(i64)]
     _lib = lib
     return lib
 
@@ -419,6 +421,9 @@ def clo_rope(plan: clo_rope_plan, x, positions, out=None, transpose: bool = Fals
     return out
 
 
+_WORKSPACE_TOKENS = 4096  # no shorter sequence makes clo_paged_attention ask for a workspace
+
+
 class PagedCache:
     """K/V pages in HBM (see include/clo.h): the caller's tensors, and the calls on them.
 
@@ -541,9 +546,23 @@ class PagedCache:
             _check(status, "clo_paged_read")
         return k_out, v_out
 
+    def _workspace(self, b: clo_paged_batch, heads: int, window: int, sinks: int) -> int:
+        size = ctypes.c_int64()
+        _check(_lib.clo_paged_attention_workspace(self._ref, ctypes.byref(b), heads, window, sinks, ctypes.byref(size)),
+               "clo_paged_attention_workspace")
+        return size.value
+
+    def attention_workspace(self, n_q_heads: int, batch: int, total: int, max_pages: int, max_q=None, window: int = 0,
+                            sinks: int = 0) -> int:
+        """Bytes of workspace that attention of these sizes uses (0: none)."""
+        b = clo_paged_batch(1 << 20, 1 << 20, 1 << 20, max_pages, max_pages, batch, total, total if max_q is None else max_q)
+        return self._workspace(b, n_q_heads, window, sinks)
+
     def attention(self, q, q_starts, kv_lens, block_table, out=None, max_q=None, softmax_scale: float = 0.0, window: int = 0,
-                  sinks: int = 0, stream=None):
-        """clo_paged_attention: q bf16 [total][n_q_heads][head_dim] over the pages; returns out (or new rows)."""
+                  sinks: int = 0, workspace=None, stream=None):
+        """clo_paged_attention: q bf16 [total][n_q_heads][head_dim] over the pages; returns out (or new rows).
+
+        workspace: uint8 tensor of attention_workspace() bytes, or None: allocated where the sizes ask for one."""
         dev = _device_of(q, "q")
         qr = _rows(q, "q", dev)
         total, heads, d = shape = q.shape
@@ -554,11 +573,27 @@ class PagedCache:
         else:
             _refuse_folded(out, "out")
         b = self._batch(dev, q_starts, kv_lens, block_table, total, max_q)
+        work, size = None, 0
+        if workspace is None and b.max_pages * self.page_size >= _WORKSPACE_TOKENS:
+            size = self._workspace(b, heads, window, sinks)
+            if size:
+                workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+                if stream is not None:  # not the allocator's stream: it has to know who uses the memory
+                    handle = _stream_of(stream, dev)
+                    workspace.record_stream(torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev))
+        if workspace is not None:
+            size = workspace.numel()
+            work = _index(workspace, "workspace", dev, torch.uint8, size)
         status = _lib.clo_paged_attention(self._ref, ctypes.byref(b), ctypes.byref(qr), ctypes.byref(_rows(out, "out", dev, shape)),
-                                          heads, softmax_scale, window, sinks, _stream_of(stream, dev))
+                                          heads, softmax_scale, window, sinks, work, size, _stream_of(stream, dev))
         if status:
             _check(status, "clo_paged_attention")
         return out
+
+
+def clo_paged_attention_workspace(cache: PagedCache, *args, **kwargs) -> int:
+    """PagedCache.attention_workspace under the C name."""
+    return cache.attention_workspace(*args, **kwargs)
 
 
 def clo_paged_append(cache: PagedCache, *args, **kwargs):

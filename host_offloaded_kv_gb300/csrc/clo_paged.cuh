@@ -158,6 +158,9 @@ struct AttendParams {
   int32_t n_q_heads;
   int32_t window, sinks;
   float scale_log2;   // softmax scale * log2(e)
+  int32_t part_rows;  // rows per (sequence, kv head), at most
+  float* part;        // the caller's workspace, or null
+  int64_t part_bytes;
 };
 
 // Checks a cache and a batch and fills the kernels' view of them; null or what is wrong.
@@ -218,6 +221,5 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-cudaError_t launch_paged_attention(const AttendParams& p, int head_dim, int kv_bits, cudaStream_t st);
 
 }  // namespace clo

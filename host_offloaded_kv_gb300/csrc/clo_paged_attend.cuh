@@ -117,8 +117,25 @@ cudaError_t launch_cluster(void (*f)(Params...), dim3 grid, int threads, int sme
   return cudaLaunchKernelEx(&cfg, f, args...);
 }
 
-cudaError_t launch_attend_few_bf16(const AttendParams& a, int head_dim, int rows, cudaStream_t st);
-cudaError_t launch_attend_few_e4m3(const AttendParams& a, int head_dim, int rows, cudaStream_t st);
+// A launch that may begin while the stream's previous kernel drains; the kernel waits for it (griddepcontrol.wait).
+template <typename... Params, typename... Args>
+cudaError_t launch_after(void (*f)(Params...), dim3 grid, int threads, cudaStream_t st, const Args&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, f, args...);
+}
+
+cudaError_t launch_attend_few_bf16(const AttendParams& a, int head_dim, cudaStream_t st);
+cudaError_t launch_attend_few_e4m3(const AttendParams& a, int head_dim, cudaStream_t st);
+int64_t attend_few_bf16_bytes(const AttendParams& a, int head_dim);
+int64_t attend_few_e4m3_bytes(const AttendParams& a, int head_dim);
 cudaError_t launch_attend_many(const AttendParams& a, int head_dim, int kv_bits, cudaStream_t st);
 
 }  // namespace clo

@@ -66,27 +66,50 @@ const char* make_page_maps(const PagedParams& c, int head_dim, int kv_bits, int 
   return nullptr;
 }
 
-cudaError_t launch_paged_attention(const AttendParams& a, int head_dim, int kv_bits, cudaStream_t st) {
-  const int64_t rows = (int64_t)a.c.max_q * a.group;  // at most, per sequence and kv head
-  if (rows > 32) return launch_attend_many(a, head_dim, kv_bits, st);
-  return kv_bits == 16 ? launch_attend_few_bf16(a, head_dim, (int)rows, st) : launch_attend_few_e4m3(a, head_dim, (int)rows, st);
-}
-
 }  // namespace clo
 
 using namespace clo;
 
+// The kernels' view of a call, or what is wrong with it.
+static const char* attend_params(const clo_paged_cache* cache, const clo_paged_batch* batch, int32_t n_q_heads, int32_t window, int32_t sinks,
+                                 AttendParams* a) {
+  if (const char* f = paged_params(cache, batch, &a->c)) return f;
+  const int hkv = cache->n_kv_heads;
+  if (n_q_heads < 1 || n_q_heads % hkv || n_q_heads / hkv > kMaxGroup) return "n_q_heads must be a multiple of n_kv_heads, at most 16 per kv head";
+  if (window < 0 || sinks < 0) return "window and sinks must not be negative";
+  a->n_q_heads = n_q_heads;
+  a->group = n_q_heads / hkv;
+  a->window = window;
+  a->sinks = sinks;
+  const int64_t rows = (int64_t)a->c.max_q * a->group;
+  a->part_rows = (int32_t)std::min<int64_t>(rows, 0x7fffffff);
+  return nullptr;
+}
+
+// Up to this many rows per kv head go to the decode kernel, more to the tcgen05 kernel.
+constexpr int kFewRows = 32;
+
+extern "C" CLO_API clo_status clo_paged_attention_workspace(const clo_paged_cache* cache, const clo_paged_batch* batch, int32_t n_q_heads,
+                                                            int32_t window, int32_t sinks, int64_t* bytes) {
+  const char* who = "clo_paged_attention_workspace";
+  AttendParams a{};
+  if (!bytes) return paged_fail(CLO_ERR_INVALID, "%s: null pointer", who);
+  *bytes = 0;
+  if (const char* f = attend_params(cache, batch, n_q_heads, window, sinks, &a)) return paged_fail(CLO_ERR_INVALID, "%s: %s", who, f);
+  if (a.c.batch == 0 || a.c.total_q == 0 || a.c.max_q == 0 || a.part_rows > kFewRows) return CLO_OK;
+  *bytes = cache->kv_bits == 16 ? attend_few_bf16_bytes(a, cache->head_dim) : attend_few_e4m3_bytes(a, cache->head_dim);
+  return CLO_OK;
+}
+
 extern "C" CLO_API clo_status clo_paged_attention(const clo_paged_cache* cache, const clo_paged_batch* batch, const clo_rows* q,
                                                   const clo_rows* out, int32_t n_q_heads, float softmax_scale, int32_t window,
-                                                  int32_t sinks, void* stream) {
+                                                  int32_t sinks, void* workspace, int64_t workspace_bytes, void* stream) {
   const char* who = "clo_paged_attention";
   AttendParams a{};
-  if (const char* f = paged_params(cache, batch, &a.c)) return paged_fail(CLO_ERR_INVALID, "%s: %s", who, f);
-  const int hkv = cache->n_kv_heads;
-  if (n_q_heads < 1 || n_q_heads % hkv || n_q_heads / hkv > kMaxGroup)
-    return paged_fail(CLO_ERR_INVALID, "%s: n_q_heads must be a multiple of n_kv_heads, at most %d per kv head", who, kMaxGroup);
-  if (window < 0 || sinks < 0) return paged_fail(CLO_ERR_INVALID, "%s: window and sinks must not be negative", who);
+  if (const char* f = attend_params(cache, batch, n_q_heads, window, sinks, &a)) return paged_fail(CLO_ERR_INVALID, "%s: %s", who, f);
   if (!std::isfinite(softmax_scale) || softmax_scale < 0.f) return paged_fail(CLO_ERR_INVALID, "%s: softmax_scale must be >= 0", who);
+  if (workspace_bytes < 0 || (reinterpret_cast<uintptr_t>(workspace) & 15u))
+    return paged_fail(CLO_ERR_INVALID, "%s: workspace must be 16-byte aligned, its size not negative", who);
   if (batch->batch == 0 || batch->total_q == 0 || a.c.max_q == 0) return CLO_OK;
   for (const clo_rows* r : {q, out}) {
     if (!r || !r->ptr) return paged_fail(CLO_ERR_INVALID, "%s: null pointer", who);
@@ -100,12 +123,15 @@ extern "C" CLO_API clo_status clo_paged_attention(const clo_paged_cache* cache, 
   a.q_head = q->stride_head;
   a.o_token = out->stride_token;
   a.o_head = out->stride_head;
-  a.n_q_heads = n_q_heads;
-  a.group = n_q_heads / hkv;
-  a.window = window;
-  a.sinks = sinks;
   a.scale_log2 = (softmax_scale > 0.f ? softmax_scale : 1.f / std::sqrt((float)cache->head_dim)) * 1.4426950408889634f;
-  const cudaError_t e = launch_paged_attention(a, cache->head_dim, cache->kv_bits, static_cast<cudaStream_t>(stream));
+  a.part = static_cast<float*>(workspace);
+  a.part_bytes = workspace ? workspace_bytes : 0;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (a.part_rows > kFewRows)
+    e = launch_attend_many(a, cache->head_dim, cache->kv_bits, st);
+  else
+    e = cache->kv_bits == 16 ? launch_attend_few_bf16(a, cache->head_dim, st) : launch_attend_few_e4m3(a, cache->head_dim, st);
   if (e != cudaSuccess) return paged_fail(CLO_ERR_CUDA, "%s: launch: %s", who, cudaGetErrorString(e));
   return CLO_OK;
 }

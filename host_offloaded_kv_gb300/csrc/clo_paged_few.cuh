@@ -15,17 +15,20 @@ namespace {
 //
 // Each warp owns a ring of kStages 8 KB stages (16 tokens of bf16 K and V rows of 128, 64 tokens of 8-bit rows of 64) that its
 // lanes fill with TMA boxes, so no warp waits for another before the end.  The tiles of a unit go round the warps of
-// a cluster of 1 to 16 blocks; warps join through shared memory, blocks through distributed shared memory: one launch, no
-// workspace, a fixed order of sums.
+// a unit's 1 to 16 blocks, a cluster; warps join through shared memory, blocks through distributed shared memory: one launch, no
+// workspace, a fixed order of sums.  Where the units are so few that 16 blocks each leave SMs idle, the blocks are no cluster:
+// they leave their sums in the caller's workspace, and a second kernel joins them.
 constexpr int kStageBytes = 8192;
 
-// Blocks of 4 warps, several to an SM; where the units are so few that their clusters cannot cover the SMs with those, blocks
-// of 12 warps that fill one.  8-bit pages take more instructions per byte, so more warps with fewer stages each.
-template <int BITS, int NT, int WARPS>
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+
+// 8-bit pages take more instructions per byte, so more warps with fewer stages each: three blocks to an SM, else two.
+template <int BITS, int NT>
 struct FewShape {
-  static constexpr int kStages = WARPS == 4 && (BITS == 16 || NT > 2) ? 3 : 2;
-  static constexpr int kRing = kStages * kStageBytes;  // per warp
-  static constexpr int kSmem = WARPS * kRing + 1024;
+  static constexpr int kStages = BITS == 16 || NT > 2 ? 3 : 2;
+  static constexpr int kSmem = kWarps * kStages * kStageBytes + 1024;
+  static constexpr int kBlocks = kStages == 2 ? 3 : 2;  // per SM
 };
 
 template <int D, int BITS>
@@ -61,10 +64,10 @@ __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <int D, int BITS, int NT, int WARPS>
-__global__ void __launch_bounds__(WARPS * 32) k_attend_few(const AttendParams a, const __grid_constant__ PageMaps maps) {
+template <int D, int BITS, int NT>
+__global__ void __launch_bounds__(kThreads) k_attend_few(const AttendParams a, const __grid_constant__ PageMaps maps) {
   using T = Tile<D, BITS>;
-  constexpr int kWarps = WARPS, kThreads = WARPS * 32, kStages = FewShape<BITS, NT, WARPS>::kStages;
+  constexpr int kStages = FewShape<BITS, NT>::kStages;
   constexpr int TOK = T::kTokens, KM = T::kM, KD = D / 16, ROWS = 8 * NT;
   constexpr float kOff = BITS == 16 ? 0.f : 14.f;  // weights up to 2^14: fp16 holds them down to 2^-38 of the largest
   extern __shared__ uint8_t smem_raw[];
@@ -81,7 +84,7 @@ __global__ void __launch_bounds__(WARPS * 32) k_attend_few(const AttendParams a,
   const SeqRows s = seq_rows(p, b);
   const int rows = s.n * a.group;
   if (rows == 0) return;  // the whole cluster
-  const int splits = gridDim.x, rank = splits > 1 ? (int)cluster_rank() : 0;
+  const int splits = gridDim.x, rank = blockIdx.x;
 
   const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t ring = smem + warp * kStages * kStageBytes;
@@ -437,6 +440,17 @@ __global__ void __launch_bounds__(WARPS * 32) k_attend_few(const AttendParams a,
     for (int w = 0; w < kWarps; ++w) v += part[w * kPart + at] * s_m[w][r];
     part[at] = v;
   }
+  if (a.part) {
+    __syncthreads();
+    // [unit][split][row]: D elements, maximum, sum, whether V held an infinity or NaN that only some rows see
+    float* dst = a.part + (((int64_t)b * p.n_kv_heads + kvh) * splits + rank) * a.part_rows * (D + 4);
+    for (int e = tid; e < rows * (D / 4); e += kThreads) {
+      const int r = e / (D / 4), q4 = e % (D / 4) * 4;
+      *reinterpret_cast<float4*>(dst + r * (D + 4) + q4) = *reinterpret_cast<const float4*>(part + r * (D + 4) + q4);
+    }
+    if (tid < rows) *reinterpret_cast<float4*>(dst + tid * (D + 4) + D) = make_float4(s_cm[tid], s_cl[tid], s_odd ? 1.f : 0.f, 0.f);
+    return;
+  }
   if (splits > 1)
     cluster_sync();
   else
@@ -497,32 +511,109 @@ __global__ void __launch_bounds__(WARPS * 32) k_attend_few(const AttendParams a,
   if (splits > 1) cluster_sync();  // no block leaves while another reads its shared memory
 }
 
-template <int D, int BITS, int NT, int WARPS>
-cudaError_t launch_few(const AttendParams& a, int splits, cudaStream_t st) {
-  using T = Tile<D, BITS>;
-  PageMaps maps;
-  if (make_page_maps(a.c, D, BITS, std::min(a.c.page_size, T::kTokens), &maps)) return cudaErrorInvalidValue;
-  auto* f = k_attend_few<D, BITS, NT, WARPS>;
-  constexpr int smem = FewShape<BITS, NT, WARPS>::kSmem;
-  static std::atomic<uint64_t> prepared{0};
-  const cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(f), smem, &prepared);
-  if (e != cudaSuccess) return e;
-  return launch_cluster(f, dim3(splits, a.c.n_kv_heads, a.c.batch), WARPS * 32, smem, splits, st, a, maps);
+// Joins the blocks of a unit: a block per row of a unit, a thread per element and eighth of the splits.
+template <int D, int BITS>
+__global__ void __launch_bounds__(8 * D) k_attend_join(const AttendParams a, int splits) {
+  __shared__ float s_o[8][D], s_l[8];
+  const PagedParams& p = a.c;
+  const int kvh = blockIdx.y, b = blockIdx.z, r = blockIdx.x;
+  const int part = threadIdx.x / D, d = threadIdx.x % D;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const SeqRows s = seq_rows(p, b);
+  if (r >= s.n * a.group) return;
+  const float* src = a.part + (((int64_t)b * p.n_kv_heads + kvh) * splits * a.part_rows + r) * (D + 4);
+  const int64_t step = (int64_t)a.part_rows * (D + 4);
+  float mx = -INFINITY;
+  bool odd = false;
+#pragma unroll 4
+  for (int c = part; c < splits; c += 8) {
+    const float4 t = *reinterpret_cast<const float4*>(src + c * step + D);
+    mx = fmaxf(mx, t.x);
+    odd |= t.z != 0.f;
+  }
+  if (d == 0) s_l[part] = mx;
+  odd = __syncthreads_or(odd) != 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) mx = fmaxf(mx, s_l[i]);
+  __syncthreads();
+  if (odd) {  // the whole block
+    if (threadIdx.x < 32) attend_row<D, BITS>(a, b, s, r / a.group, kvh * a.group + r % a.group, threadIdx.x);
+    return;
+  }
+  float o = 0.f, l = 0.f;
+#pragma unroll 4
+  for (int c = part; c < splits; c += 8) {
+    const float m = src[c * step + D];
+    const float f = m == mx ? 1.f : exp2_fast(m - mx);
+    l = fmaf(src[c * step + D + 1], f, l);
+    o = fmaf(src[c * step + d], f, o);
+  }
+  s_o[part][d] = o;
+  if (d == 0) s_l[part] = l;
+  __syncthreads();
+  if (part != 0) return;
+  o = l = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    o += s_o[i][d];
+    l += s_l[i];
+  }
+  a.out[(int64_t)(s.first + r / a.group) * a.o_token + (int64_t)(kvh * a.group + r % a.group) * a.o_head + d] =
+      (uint16_t)pack_bf16(l == 0.f ? 0.f : o / l, 0.f);
 }
+
+struct FewPlan {
+  int splits;
+  int64_t bytes;  // of workspace; 0: clusters
+};
 
 // Blocks per unit: enough to fill the GPU, no more than leaves each warp two tiles of the longest sequence.
 template <int D, int BITS, int NT>
-cudaError_t launch_few_rows(const AttendParams& a, cudaStream_t st) {
+FewPlan plan_few(const AttendParams& a) {
   using T = Tile<D, BITS>;
   const int64_t units = (int64_t)a.c.batch * a.c.n_kv_heads;
   int64_t tokens = (int64_t)a.c.max_pages << a.c.page_shift;
   if (a.window > 0) tokens = std::min<int64_t>(tokens, (int64_t)a.window + a.c.max_q + a.sinks + 2 * T::kTokens);
-  if constexpr (NT <= 2) {
-    if (units * 16 <= kSms && tokens >= 2 * 16 * 12 * T::kTokens) return launch_few<D, BITS, NT, 12>(a, 16, st);
-  }
+  const int64_t most = tokens / (2 * kWarps * T::kTokens), fill = FewShape<BITS, NT>::kBlocks * kSms / units;
+  const int64_t want = std::min(most, fill);
+  if (want > 16 && tokens >= 4096) return {(int)want, want * units * a.part_rows * (D + 4) * 4};
   int splits = 1;
-  while (splits < 16 && splits * units < 2 * kSms && 4 * splits * 4 * T::kTokens <= tokens) splits *= 2;
-  return launch_few<D, BITS, NT, 4>(a, splits, st);
+  while (splits < 16 && splits * units < 2 * kSms && 2 * splits <= most) splits *= 2;
+  return {splits, 0};
+}
+
+template <int D, int BITS, int NT>
+cudaError_t few_rows(AttendParams a, FewPlan* plan, cudaStream_t st) {
+  using T = Tile<D, BITS>;
+  FewPlan pl = plan_few<D, BITS, NT>(a);
+  if (plan) {
+    *plan = pl;
+    return cudaSuccess;
+  }
+  if (pl.bytes > a.part_bytes) pl = {16, 0};  // no workspace
+  if (!pl.bytes) a.part = nullptr;
+  PageMaps maps;
+  if (make_page_maps(a.c, D, BITS, std::min(a.c.page_size, T::kTokens), &maps)) return cudaErrorInvalidValue;
+  auto* f = k_attend_few<D, BITS, NT>;
+  constexpr int smem = FewShape<BITS, NT>::kSmem;
+  static std::atomic<uint64_t> prepared{0};
+  cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(f), smem, &prepared);
+  if (e != cudaSuccess) return e;
+  e = launch_cluster(f, dim3(pl.splits, a.c.n_kv_heads, a.c.batch), kThreads, smem, a.part ? 1 : pl.splits, st, a, maps);
+  if (e != cudaSuccess || !a.part) return e;
+  return launch_after(k_attend_join<D, BITS>, dim3(a.part_rows, a.c.n_kv_heads, a.c.batch), 8 * D, st, a, pl.splits);
+}
+
+// Runs the call, or (plan) says what it would take.
+template <int BITS>
+cudaError_t few(const AttendParams& a, int head_dim, FewPlan* plan, cudaStream_t st) {
+  const int rows = a.part_rows;
+  if (head_dim == 128) {
+    if (rows <= 8) return few_rows<128, BITS, 1>(a, plan, st);
+    return rows <= 16 ? few_rows<128, BITS, 2>(a, plan, st) : few_rows<128, BITS, 4>(a, plan, st);
+  }
+  if (rows <= 8) return few_rows<64, BITS, 1>(a, plan, st);
+  return rows <= 16 ? few_rows<64, BITS, 2>(a, plan, st) : few_rows<64, BITS, 4>(a, plan, st);
 }
 
 }  // namespace

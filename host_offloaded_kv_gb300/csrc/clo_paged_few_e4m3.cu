@@ -3,13 +3,12 @@
 
 namespace clo {
 
-cudaError_t launch_attend_few_e4m3(const AttendParams& a, int head_dim, int rows, cudaStream_t st) {
-  if (head_dim == 128) {
-    if (rows <= 8) return launch_few_rows<128, 8, 1>(a, st);
-    return rows <= 16 ? launch_few_rows<128, 8, 2>(a, st) : launch_few_rows<128, 8, 4>(a, st);
-  }
-  if (rows <= 8) return launch_few_rows<64, 8, 1>(a, st);
-  return rows <= 16 ? launch_few_rows<64, 8, 2>(a, st) : launch_few_rows<64, 8, 4>(a, st);
+cudaError_t launch_attend_few_e4m3(const AttendParams& a, int head_dim, cudaStream_t st) { return few<8>(a, head_dim, nullptr, st); }
+
+int64_t attend_few_e4m3_bytes(const AttendParams& a, int head_dim) {
+  FewPlan p{};
+  few<8>(a, head_dim, &p, nullptr);
+  return p.bytes;
 }
 
 }  // namespace clo

@@ -316,7 +316,7 @@ CLO_API clo_status clo_sparse_attention_noalloc(const void* q, const void* rows,
  * HBM pages with its own attention, for sequences and layers that need no offloading
  * (short contexts, layers with a sliding window, prompts).  clo_paged_read turns a
  * paged range back into the bf16 rows that clo_append_kv takes.  They have no context:
- * all memory is the caller's, nothing is allocated, no workspace is kept between
+ * all memory is the caller's, nothing is allocated, nothing is kept between
  * calls, and calls on different streams or in different captured graphs share
  * nothing but the buffers that they are given.
  *
@@ -459,10 +459,17 @@ CLO_API clo_status clo_paged_read(const clo_paged_cache* cache, const clo_paged_
  * softmax_scale 0: 1 / sqrt(head_dim).  window, sinks >= 0 (sinks without a window have no effect).
  * Rows as for clo_paged_append; out must not overlap q.
  * Rows past q_starts[batch] are left as they are.
+ * workspace: device memory, 16-byte aligned, of the size that clo_paged_attention_workspace gives (it may
+ * hold anything, and is free again when the call's work is done); calls that may overlap need one each.
+ * NULL or less than that: the call works without, on fewer SMs (it matters for few long sequences).
  * Errors: CLO_ERR_INVALID, CLO_ERR_CUDA. */
 CLO_API clo_status clo_paged_attention(const clo_paged_cache* cache, const clo_paged_batch* batch, const clo_rows* q,
                                        const clo_rows* out, int32_t n_q_heads, float softmax_scale, int32_t window,
-                                       int32_t sinks, void* stream);
+                                       int32_t sinks, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace for a call of these sizes (0: none); host only, no CUDA call. */
+CLO_API clo_status clo_paged_attention_workspace(const clo_paged_cache* cache, const clo_paged_batch* batch, int32_t n_q_heads,
+                                                 int32_t window, int32_t sinks, int64_t* bytes);
 
 #ifdef __cplusplus
 }

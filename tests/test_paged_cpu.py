@@ -108,7 +108,7 @@ def test_paged_calls_refuse(clo, call):
     lib = clo.load_library()
     plan = clo.clo_rope_plan_init(rot_dim=128)
 
-    def run(c=None, b=None, k=None, v=None, plan=plan, q=None, q_out=None, hq=4, scale=0.0, window=0, sinks=0, pos=None):
+    def run(c=None, b=None, k=None, v=None, plan=plan, q=None, q_out=None, hq=4, scale=0.0, window=0, sinks=0, pos=None, work=None):
         c, b = ctypes.byref(c or _cache(clo)), ctypes.byref(b or _batch(clo))
         k, v = ctypes.byref(k or _rows(clo)), ctypes.byref(v or _rows(clo, 0x20000))
         opt = lambda r: None if r is None else ctypes.byref(r)  # noqa: E731
@@ -116,7 +116,7 @@ def test_paged_calls_refuse(clo, call):
             return lib.clo_paged_append(c, b, opt(plan), pos, k, v, opt(q), opt(q_out), hq, None)
         if call == "read":
             return lib.clo_paged_read(c, b, k, v, None)
-        return lib.clo_paged_attention(c, b, k, v, hq, scale, window, sinks, None)
+        return lib.clo_paged_attention(c, b, k, v, hq, scale, window, sinks, work, 0, None)
 
     bad = [dict(c=_cache(clo, **kw)) for kw in CACHE_FAULTS] + [dict(b=_batch(clo, **kw)) for kw in BATCH_FAULTS]
     bad += [dict(k=_rows(clo, 0x10008)), dict(v=_rows(clo, 0x20000, token=1028)), dict(k=_rows(clo, None)), dict(v=_rows(clo, 0x20000, head=100))]
@@ -129,7 +129,7 @@ def test_paged_calls_refuse(clo, call):
                 dict(q=r, q_out=_rows(clo, 0x50002)), dict(pos=0x30004)]
     if call == "attention":
         bad += [dict(hq=0), dict(hq=3), dict(hq=34), dict(scale=float("nan")), dict(scale=-1.0), dict(window=-1), dict(sinks=-1),
-                dict(v=_rows(clo))]
+                dict(v=_rows(clo)), dict(work=0x4008)]
     for kw in bad:
         assert run(**kw) == clo.CLO_ERR_INVALID, kw
         assert clo.clo_last_error().startswith("clo_paged_" + call), kw
