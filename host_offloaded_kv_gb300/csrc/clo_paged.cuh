@@ -186,15 +186,41 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, in
       : "memory");
 }
 
-// Bounded wait: false after about two seconds, which no copy or product takes.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// One try that may suspend the thread for up to 20 us, so that waiting warps leave the issue slots to working ones.
+__device__ __forceinline__ bool mbar_try_wait_long(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
+      : "memory");
+  return ok != 0;
+}
+
+// Bounded wait: false after about two seconds, which no copy or product takes.  The clock is read only after
+// many tries (reading it takes longer than most waits).
 __device__ __forceinline__ bool mbar_wait_limited(uint64_t* bar, uint32_t parity) {
-  if (mbar_try_wait(bar, parity)) return true;
+  if (mbar_test(bar, parity)) return true;
+  for (int i = 0; i < 64; ++i)
+    if (mbar_try_wait_long(bar, parity)) return true;
   const uint64_t t0 = global_timer_ns();
-  while (true) {
-    for (int i = 0; i < 64; ++i)
-      if (mbar_try_wait(bar, parity)) return true;
-    if (global_timer_ns() - t0 > 2000000000ull) return false;
-  }
+  while (global_timer_ns() - t0 < 2000000000ull)
+    if (mbar_try_wait_long(bar, parity)) return true;
+  return false;
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {

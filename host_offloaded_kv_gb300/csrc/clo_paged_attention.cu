@@ -87,7 +87,7 @@ static const char* attend_params(const clo_paged_cache* cache, const clo_paged_b
 }
 
 // Up to this many rows per kv head go to the decode kernel, more to the tcgen05 kernel.
-constexpr int kFewRows = 32;
+constexpr int kFewRows = 16;
 
 extern "C" CLO_API clo_status clo_paged_attention_workspace(const clo_paged_cache* cache, const clo_paged_batch* batch, int32_t n_q_heads,
                                                             int32_t window, int32_t sinks, int64_t* bytes) {

@@ -26,7 +26,7 @@ constexpr int kThreads = kWarps * 32;
 // 8-bit pages take more instructions per byte, so more warps with fewer stages each: three blocks to an SM, else two.
 template <int BITS, int NT>
 struct FewShape {
-  static constexpr int kStages = BITS == 16 || NT > 2 ? 3 : 2;
+  static constexpr int kStages = BITS == 16 ? 3 : 2;
   static constexpr int kSmem = kWarps * kStages * kStageBytes + 1024;
   static constexpr int kBlocks = kStages == 2 ? 3 : 2;  // per SM
 };
@@ -610,10 +610,10 @@ cudaError_t few(const AttendParams& a, int head_dim, FewPlan* plan, cudaStream_t
   const int rows = a.part_rows;
   if (head_dim == 128) {
     if (rows <= 8) return few_rows<128, BITS, 1>(a, plan, st);
-    return rows <= 16 ? few_rows<128, BITS, 2>(a, plan, st) : few_rows<128, BITS, 4>(a, plan, st);
+    return few_rows<128, BITS, 2>(a, plan, st);
   }
   if (rows <= 8) return few_rows<64, BITS, 1>(a, plan, st);
-  return rows <= 16 ? few_rows<64, BITS, 2>(a, plan, st) : few_rows<64, BITS, 4>(a, plan, st);
+  return few_rows<64, BITS, 2>(a, plan, st);
 }
 
 }  // namespace

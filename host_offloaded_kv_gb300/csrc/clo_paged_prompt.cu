@@ -5,19 +5,21 @@
 // rows see.  Both products run on tcgen05: S = Q K^T from shared memory into TMEM, O += P V with P in TMEM (over the
 // columns of S that it came from) and O in TMEM.  One thread owns a row of S: its maximum and sum need no exchange.
 //
-//   warps 0-3, 4-7   softmax of row tile 0, 1 (TMEM lanes are tied to a warp's place in its group of four)
+// Two lanes of work run against each other, so that one's products fill the time of the other's softmax: with two row
+// tiles, a lane is a row tile; with one (at most 128 rows), lane 0 takes the even token tiles and lane 1 the odd ones, and
+// their sums are joined at the end.
+//
+//   warps 0-3, 4-7   softmax of lane 0, 1 (TMEM rows are tied to a warp's place in its group of four)
 //   warp 8           TMA: pages -> ring of operand tiles, K(0) K(1) V(0) K(2) V(1) ...
-//   warp 9           MMA issue: PV of one row tile, then S of the next token tile, alternating between the row tiles, so that
-//                    one tile's products run under the other's softmax
-//   warps 10, 11     bf16 pages: V of the tiles at a mask's edge: rows that hold an infinity or NaN are cleared (see below)
+//   warp 9           MMA issue: P V of a token tile, then S of the lane's next one, the lanes in turn
+//   warp 11          bf16 pages: V of the tiles at a mask's edge is looked over (see below)
 //   warps 12-15      8-bit pages only: codes -> fp16 operand tiles
 //
 // The accumulator is rescaled only when a row's maximum has grown by more than 2^8 (weights stay below 2^8 times
 // the largest so far; exact in the end, as sum and accumulator share the reference).
 //
-// A masked weight is zero, but zero times NaN is not: V rows that hold an infinity or NaN are cleared in the operand tile
-// wherever not every row sees the token.  If some row does see such a token, the block's rows are
-// computed again one by one.
+// A masked weight is zero, but zero times NaN is not: infinities and NaN in V are cleared in the operand tile wherever not every
+// row sees the token.  If some row does see such a token, the block's rows are computed again one by one.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -29,28 +31,38 @@ namespace {
 
 constexpr int kTok = 128;    // tokens per tile
 constexpr int kRows = 128;   // rows per row tile
-constexpr int kMeta = 8;     // token tiles whose page data is kept
+constexpr int kMeta = 16;    // token tiles whose page data is kept: more than the ring runs ahead
 constexpr float kGrow = 8.f;
 
 // ---------------------------------------------------------------------------- tcgen05
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tc_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+// Issue by one elected thread of a converged warp (`leader` is nonzero in it): what the warp computes for an
+// instruction stays in uniform registers, which the instruction wants.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r;
 }
-__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void tc_commit(uint64_t* bar, uint32_t leader) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)), "r"(leader)
       : "memory");
 }
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add, uint32_t leader) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add, uint32_t leader) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add), "r"(leader)
       : "memory");
 }
 #define CLO_R4(x, i) "=r"(x[i]), "=r"(x[i + 1]), "=r"(x[i + 2]), "=r"(x[i + 3])
@@ -115,24 +127,27 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-template <int D, int BITS>
+template <int D, int BITS, int TILES>
 struct Cfg {
   static constexpr int kTileBytes = kTok * D * 2;             // an operand tile
   static constexpr int kQBytes = kRows * D * 2;
-  static constexpr int kSlots = BITS == 16 ? 4 : 3;
+  // operand tiles of the ring, and 8-bit tiles on their way into it: what fits next to Q
+  static constexpr int kSlots = BITS == 16 ? (D == 64 ? 8 : TILES == 2 ? 4 : 5) : (D == 64 ? 6 : TILES == 2 ? 3 : 4);
+  static constexpr int kRaw = BITS == 16 ? 0 : D == 64 ? 6 : 3;
   static constexpr int kRawBytes = BITS == 16 ? 0 : kTok * D;
-  static constexpr int kRaw = BITS == 16 ? 0 : 3;
   static constexpr int kThreads = BITS == 16 ? 384 : 512;
-  static constexpr int kPartRow = D + 4;                       // floats per row of a joined block's accumulator
-  static constexpr int smem(int tiles) { return tiles * kQBytes + kSlots * kTileBytes + kRaw * kRawBytes + 1024; }
+  static constexpr int kPartRow = D + 4;                       // floats per row of an accumulator to be joined
+  static constexpr int kSmem = TILES * kQBytes + kSlots * kTileBytes + kRaw * kRawBytes;
+  static constexpr int kJoin = 2 * kRows * kPartRow * 4;       // over Q and the ring, when they are done with
+  static constexpr int kBytes = (kSmem > kJoin ? kSmem : kJoin) + 1024;
 };
 
 struct Shared {
-  uint64_t full[4], empty[4];      // operand tiles: filled (TMA or converters), products done
-  uint64_t checked[4];             // bf16: operand tiles looked over
-  uint64_t raw_full[4], raw_empty[4];
-  uint64_t s_full[2], p_ready[2];
-  uint64_t done;                   // every product
+  uint64_t full[8], empty[8];      // operand tiles: filled (TMA or converters), products done
+  uint64_t checked[8];             // bf16: V at a mask's edge looked over
+  uint64_t raw_full[8], raw_empty[8];
+  uint64_t s_full[2], p_ready[2];  // per lane
+  uint64_t done;                   // every product of both lanes
   uint64_t meta[kMeta];
   float scale[kMeta][2][8];
   uint32_t there[kMeta];
@@ -141,31 +156,29 @@ struct Shared {
   float m[2][kRows], l[2][kRows];
 };
 
-// Bounded wait; once one has given up, the others follow at once.
+// Bounded wait (two seconds, see mbar_wait_limited); once one has given up, the others follow.
 __device__ __forceinline__ bool wait(Shared& sh, uint64_t* bar, uint32_t parity) {
-  if (mbar_try_wait(bar, parity)) return true;
+  if (mbar_test(bar, parity)) return true;
+  for (int i = 0; i < 64; ++i)
+    if (mbar_try_wait_long(bar, parity)) return true;
   const uint64_t t0 = global_timer_ns();
-  while (true) {
-    for (int i = 0; i < 64; ++i)
-      if (mbar_try_wait(bar, parity)) return true;
-    if (*reinterpret_cast<volatile int*>(&sh.failed)) return false;
-    if (global_timer_ns() - t0 > 2000000000ull) {
-      *reinterpret_cast<volatile int*>(&sh.failed) = 1;
-      return false;
-    }
+  while (*reinterpret_cast<volatile int*>(&sh.failed) == 0) {
+    if (mbar_try_wait_long(bar, parity)) return true;
+    if (global_timer_ns() - t0 > 2000000000ull) *reinterpret_cast<volatile int*>(&sh.failed) = 1;
   }
+  return false;
 }
 
 template <int D, int BITS, int TILES>
-__global__ void __launch_bounds__(Cfg<D, BITS>::kThreads, 1) k_attend_many(const AttendParams a, const __grid_constant__ PageMaps maps, int q_blocks,
+__global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_many(const AttendParams a, const __grid_constant__ PageMaps maps, int q_blocks,
                                                                               int splits) {
-  using C = Cfg<D, BITS>;
+  using C = Cfg<D, BITS, TILES>;
   constexpr int SLOTS = C::kSlots;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(16) Shared sh;
 
   const PagedParams& p = a.c;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   // the last rows first: they see the most tokens
   const int unit = blockIdx.x / splits, rank = blockIdx.x % splits;
   const int kvh = unit % p.n_kv_heads, qb = q_blocks - 1 - unit / p.n_kv_heads, b = blockIdx.y;
@@ -183,10 +196,10 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::kThreads, 1) k_attend_many(const
   uint8_t* const generic = smem_raw + (smem - smem_u32(smem_raw));
 
   if (tid == 0) {
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 8; ++i) {
       mbar_init(&sh.full[i], BITS == 16 ? 1 : 128);
-      mbar_init(&sh.empty[i], 1);
-      mbar_init(&sh.checked[i], 64);
+      mbar_init(&sh.empty[i], BITS == 16 ? 2 : 1);  // products; bf16: the look-over
+      mbar_init(&sh.checked[i], 32);
       mbar_init(&sh.raw_full[i], 1);
       mbar_init(&sh.raw_empty[i], 128);
     }
@@ -209,9 +222,10 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::kThreads, 1) k_attend_many(const
   // Q rows into operand tiles, a row per softmax thread.  8-bit pages: fp16, each row scaled by a power of two that
   // puts its largest finite element into [2^14, 2^15).
   float fac = a.scale_log2;
-  const int tile = warp >> 2, my_row = row0 + (tile < TILES ? tile : 0) * kRows + (tid & 127);
-  const bool row_ok = warp < 4 * TILES && my_row < rows;
-  if (warp < 4 * TILES) {
+  const int lane_of_work = (warp >> 2) & 1, my_tile = TILES == 2 ? lane_of_work : 0;
+  const int my_row = row0 + my_tile * kRows + (tid & 127);
+  const bool row_ok = warp < 8 && my_row < rows;
+  if (warp < 8) {
     const uint16_t* src = a.q + (int64_t)(s.first + my_row / a.group) * a.q_token + (int64_t)(kvh * a.group + my_row % a.group) * a.q_head;
     const int r = tid & 127;
     float down = 1.f;
@@ -227,6 +241,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::kThreads, 1) k_attend_many(const
       down = __uint_as_float((uint32_t)(127 - e) << 23);
       fac *= __uint_as_float((uint32_t)(127 + e) << 23);
     }
+    if (TILES == 2 || warp < 4)
 #pragma unroll 4
     for (int c = 0; c < D / 8; ++c) {
       uint4 v = make_uint4(0, 0, 0, 0);
@@ -236,7 +251,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::kThreads, 1) k_attend_many(const
         unpack8(v, x);
         v = make_uint4(pack_f16(x[0] * down, x[1] * down), pack_f16(x[2] * down, x[3] * down), pack_f16(x[4] * down, x[5] * down), pack_f16(x[6] * down, x[7] * down));
       }
-      *reinterpret_cast<uint4*>(generic + (swizzled<128>(q_smem + tile * C::kQBytes, kRows, r, c) - smem)) = v;
+      *reinterpret_cast<uint4*>(generic + (swizzled<128>(q_smem + my_tile * C::kQBytes, kRows, r, c) - smem)) = v;
     }
     fence_proxy_async_smem();
   }
@@ -254,26 +269,37 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::kThreads, 1) k_attend_many(const
   auto is_v = [&](int e) { return e > 0 && ((e & 1) == 0 || e == 2 * n - 1); };
   auto tile_of = [&](int e) { return !is_v(e) ? (e + 1) / 2 : e == 2 * n - 1 ? n - 1 : e / 2 - 1; };
 
+  // Lane t takes token tiles first_of(t), + kStep, ...: count_of(t) of them.
+  constexpr int kStep = TILES == 2 ? 1 : 2;
+  auto first_of = [&](int t) { return TILES == 2 ? 0 : t; };
+  auto count_of = [&](int t) { return TILES == 2 ? n : (n + 1 - t) / 2; };
+  const Visible blk_f = visible_of(pos_first, s.kv_len, a.window, a.sinks), blk_l = visible_of(pos_last, s.kv_len, a.window, a.sinks);
+  // some row does not see all of the token tile (by position: missing pages read as zeros)
+  auto edge = [&](int j) {
+    const int j0 = tl.at(t_begin + j) * kTok;
+    return !(j0 + kTok <= blk_f.hi && (j0 >= blk_l.lo || j0 + kTok <= (a.window > 0 ? a.sinks : 0)));
+  };
+
   if (warp < 8) {
     // ------------------------------------------------------------------------ softmax
     if (BITS == 16) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     else asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
     float ref = -INFINITY, l = 0.f;
-    const int t = warp >> 2;
+    const int t = lane_of_work, mine = count_of(t);
     bool ok = true;
-    if (t < TILES) {
+    {
       constexpr float kOff = BITS == 16 ? 0.f : 7.f;  // weights of 8-bit pages: up to 2^15 with kGrow, fp16 down to 2^-31
       const uint32_t lane_off = (uint32_t)(warp & 3) * 32u << 16;
       const uint32_t s_addr = tmem + lane_off + kS[t], o_addr = tmem + lane_off + kO[t];
       // the tile's first and last row bound what "every row sees" means; rows past the end follow the last one
-      const int rf = min(row0 + t * kRows, rows - 1), rl = min(row0 + t * kRows + kRows - 1, rows - 1);
+      const int rf = min(row0 + my_tile * kRows, rows - 1), rl = min(row0 + my_tile * kRows + kRows - 1, rows - 1);
       const Visible vf = visible_of(s.pos0 + rf / a.group, s.kv_len, a.window, a.sinks);
       const Visible vl = visible_of(s.pos0 + rl / a.group, s.kv_len, a.window, a.sinks);
       const Visible v = visible_of(s.pos0 + min(my_row, rows - 1) / a.group, s.kv_len, a.window, a.sinks);
-      for (int j = 0; j < n; ++j) {
-        const int j0 = tl.at(t_begin + j) * kTok;
+      for (int i = 0; i < mine; ++i) {
+        const int j = first_of(t) + i * kStep, j0 = tl.at(t_begin + j) * kTok;
         const int slot = j % kMeta;
-        ok = wait(sh, &sh.meta[slot], (j / kMeta) & 1) && wait(sh, &sh.s_full[t], j & 1);
+        ok = wait(sh, &sh.meta[slot], (j / kMeta) & 1) && wait(sh, &sh.s_full[t], i & 1);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
@@ -330,7 +356,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::kThreads, 1) k_attend_many(const
           const float f = grow ? (ref == -INFINITY ? 0.f : exp2_fast(ref - mx)) : 1.f;
           if (grow) ref = mx;
           l *= f;
-          if (j > 0) {
+          if (i > 0) {
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
               uint32_t o[32];
@@ -374,16 +400,12 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::kThreads, 1) k_attend_many(const
         tc_fence_before();
         mbar_arrive(&sh.p_ready[t]);
       }
-      // the row tile's last product; where the accumulators go to shared memory, the other row tile's too
-      if (ok && n > 0) ok = splits == 1 ? wait(sh, &sh.s_full[t], n & 1) : wait(sh, &sh.done, 0);
+      // the lane's last product; where the accumulators go to shared memory, every product
+      const bool direct = TILES == 2 && splits == 1;
+      if (ok) ok = direct ? mine == 0 || wait(sh, &sh.s_full[t], mine & 1) : wait(sh, &sh.done, 0);
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
-      if (n > 0) {
-        // the reference of the weights as the join sees it
-        ref = ref == -INFINITY ? ref : ref - kOff;
-      }
       if (!ok) l = __int_as_float(0x7fffffff);
-      const bool direct = splits == 1;
       uint16_t* dst = a.out + (int64_t)(s.first + my_row / a.group) * a.o_token + (int64_t)(kvh * a.group + my_row % a.group) * a.o_head;
       const float inv = l == 0.f ? 0.f : 1.f / l;
       float* part = reinterpret_cast<float*>(generic) + (t * kRows + (tid & 127)) * C::kPartRow;
@@ -394,7 +416,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::kThreads, 1) k_attend_many(const
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
-        if (n > 0) {
+        if (mine > 0) {
           tc_ld32(o_addr + 32 * c, o);
           tc_wait_ld<1>(o);
         } else {
@@ -474,81 +496,91 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::kThreads, 1) k_attend_many(const
           for (int ph = 0; ph < 2; ++ph) mbar_wait_limited(BITS == 16 ? &sh.full[i] : &sh.raw_full[i], ph);
     } else if (warp == 9) {
       // ---------------------------------------------------------------------- MMA issue
-      if (lane == 0) {
-        constexpr uint32_t kShapeS = mma_shape(BITS == 16, kTok, false), kShapeO = mma_shape(BITS == 16, D, true);
-        auto score = [&](int t, int e) {
-          const uint32_t qa = q_smem + t * C::kQBytes, ka = ring + e % SLOTS * C::kTileBytes;
+      constexpr uint32_t kShapeS = mma_shape(BITS == 16, kTok, false), kShapeO = mma_shape(BITS == 16, D, true);
+      const uint32_t leader = elect_one();
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint64_t q_desc = operand(__shfl_sync(0xffffffffu, q_smem, 0), 16, 1024);
+      const uint32_t ring_u = __shfl_sync(0xffffffffu, ring, 0);
+      auto score = [&](int t, int slot) {
+        const uint64_t qd = q_desc + (TILES == 2 ? t * (C::kQBytes >> 4) : 0);
+        const uint64_t kd = operand(__shfl_sync(0xffffffffu, ring_u + slot * C::kTileBytes, 0), 16, 1024);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = kk / 4 * (kTok * 128) + kk % 4 * 32;
-            tc_mma_ss(tmem + kS[t], operand(qa + off, 16, 1024), operand(ka + off, 16, 1024), kShapeS, kk > 0);
-          }
-        };
-        auto ready = [&](int e) { return wait(sh, &sh.full[e % SLOTS], (e / SLOTS) & 1); };
-        bool ok = n > 0 && ready(0);
-        if (ok) {
-          tc_fence_after();
-          for (int t = 0; t < TILES; ++t) {
-            score(t, 0);
-            tc_commit(&sh.s_full[t]);
-          }
-          tc_commit(&sh.empty[0]);
+        for (int kk = 0; kk < D / 16; ++kk) {
+          constexpr int kHalf = kTok * 128 >> 4;
+          const int off = kk / 4 * kHalf + kk % 4 * 2;
+          tc_mma_ss(tm + 128 * t, qd + off, kd + off, kShapeS, kk > 0, leader);
         }
-        for (int j = 0; j < n && ok; ++j) {
-          const int ek = at_k(j + 1), ev = at_v(j);
-          if (j + 1 < n) ok = ready(ek);
-          ok = ok && ready(ev);
-          if (ok && BITS == 16) ok = wait(sh, &sh.checked[ev % SLOTS], (ev / SLOTS) & 1);
-          for (int t = 0; t < TILES && ok; ++t) {
-            ok = wait(sh, &sh.p_ready[t], j & 1);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t va = ring + ev % SLOTS * C::kTileBytes;
-#pragma unroll
-            for (int kk = 0; kk < kTok / 16; ++kk)
-              tc_mma_ts(tmem + kO[t], tmem + kS[t] + kk * 8, operand(va + kk * 2048, kTok * 128, 1024), kShapeO, j > 0 || kk > 0);
-            if (j + 1 < n) score(t, ek);
-            tc_commit(&sh.s_full[t]);
-          }
-          if (ok) {
-            tc_commit(&sh.empty[ev % SLOTS]);
-            if (j + 1 < n) tc_commit(&sh.empty[ek % SLOTS]);
-          }
-        }
-        if (ok) tc_commit(&sh.done);
-      }
-      __syncwarp();
-    } else if (BITS == 16 ? warp >= 10 : warp >= 12) {
-      // ---------------------------------------------------------------------- V at a mask's edge; 8-bit codes -> fp16
-      const Visible vf = visible_of(pos_first, s.kv_len, a.window, a.sinks), vl = visible_of(pos_last, s.kv_len, a.window, a.sinks);
-      auto edge = [&](int j) {
-        const int j0 = tl.at(t_begin + j) * kTok;
-        return !(j0 + kTok <= vf.hi && (j0 >= vl.lo || j0 + kTok <= (a.window > 0 ? a.sinks : 0)));
       };
-      auto seen = [&](int tok) { return tok < vl.hi && (tok >= vf.lo || tok < (a.window > 0 ? a.sinks : 0)); };
+      auto values = [&](int t, int slot, bool add) {
+        const uint64_t vd = operand(__shfl_sync(0xffffffffu, ring_u + slot * C::kTileBytes, 0), kTok * 128, 1024);
+#pragma unroll
+        for (int kk = 0; kk < kTok / 16; ++kk)
+          tc_mma_ts(tm + 256 + 128 * t, tm + 128 * t + kk * 8, vd + kk * (2048 >> 4), kShapeO, add || kk > 0, leader);
+      };
+      auto ready = [&](int e) { return wait(sh, &sh.full[e % SLOTS], (e / SLOTS) & 1); };
+      uint32_t checked = 0;  // phase of each slot's `checked`
+      bool ok = true;
+      for (int t = 0; t < 2 && ok; ++t) {
+        if (count_of(t) == 0) break;
+        const int e = at_k(first_of(t));
+        ok = ready(e);
+        if (!ok) break;
+        tc_fence_after();
+        score(t, e % SLOTS);
+        tc_commit(&sh.s_full[t], leader);
+        if (TILES == 1 || t == 1) tc_commit(&sh.empty[e % SLOTS], leader);
+      }
+      for (int j = 0; j < n && ok; ++j) {
+        const int ev = at_v(j), vslot = ev % SLOTS;
+        const bool next = j + kStep < n;
+        const int ek = next ? at_k(j + kStep) : 0, kslot = ek % SLOTS;
+        ok = ready(ev) && (!next || ready(ek));
+        if (BITS == 16 && ok && edge(j)) {
+          ok = wait(sh, &sh.checked[vslot], checked >> vslot & 1u);
+          checked ^= 1u << vslot;
+        }
+#pragma unroll
+        for (int u = 0; u < TILES; ++u) {
+          const int t = TILES == 2 ? u : j & 1;
+          ok = ok && wait(sh, &sh.p_ready[t], (TILES == 2 ? j : j >> 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          values(t, vslot, TILES == 2 ? j > 0 : j > 1);
+          if (next) score(t, kslot);
+          tc_commit(&sh.s_full[t], leader);
+        }
+        if (ok) {
+          tc_commit(&sh.empty[vslot], leader);
+          if (next) tc_commit(&sh.empty[kslot], leader);
+        }
+      }
+      if (ok && n > 0) tc_commit(&sh.done, leader);
+      else if (leader) mbar_arrive(&sh.done);
+      __syncwarp();
+    } else if (BITS == 16 ? warp == 11 : warp >= 12) {
+      // ---------------------------------------------------------------------- V at a mask's edge; 8-bit codes -> fp16
+      auto seen = [&](int tok) { return tok < blk_l.hi && (tok >= blk_f.lo || tok < (a.window > 0 ? a.sinks : 0)); };
       bool ok = true;
       if constexpr (BITS == 16) {
-        const int th = tid - 320;
-        for (int e = 0; e < 2 * n && ok; ++e) {
-          const int j = tile_of(e), slot = e % SLOTS;
+        for (int e = 0; e < 2 * n; ++e) {
+          const int slot = e % SLOTS, j = tile_of(e);
           ok = wait(sh, &sh.full[slot], (e / SLOTS) & 1);
-          if (ok && is_v(e) && edge(j)) {
+          if (!ok) break;
+          if (is_v(e) && edge(j)) {
             const int j0 = tl.at(t_begin + j) * kTok;
-            for (int r = th; r < kTok; r += 64) {
-              uint8_t* row = generic + (ring - smem) + slot * C::kTileBytes + r * 128;
-              bool bad = false;
-              for (int c = 0; c < D / 8; ++c) {
-                const uint4 w = *reinterpret_cast<const uint4*>(row + (c >> 3) * (kTok * 128) + (c & 7) * 16);
-                bad |= not_finite16<16>(w);
-              }
-              if (bad) {
-                if (seen(j0 + r)) sh.odd = 1;
-                for (int c = 0; c < D / 8; ++c) *reinterpret_cast<uint4*>(row + (c >> 3) * (kTok * 128) + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+#pragma unroll 4
+            for (int i = lane; i < kTok * D / 8; i += 32) {
+              uint4* at = reinterpret_cast<uint4*>(generic + (ring - smem) + slot * C::kTileBytes) + i;
+              if (not_finite16<16>(*at)) {
+                if (seen(j0 + i / 8 % kTok)) sh.odd = 1;
+                *at = make_uint4(0, 0, 0, 0);
               }
             }
             fence_proxy_async_smem();
+            mbar_arrive(&sh.checked[slot]);
           }
-          mbar_arrive(&sh.checked[slot]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.empty[slot]);
         }
       } else {
         const int th = tid - 384;
@@ -600,21 +632,22 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::kThreads, 1) k_attend_many(const
     if (slow) {
       for (int r = row0 + rank * 8 + warp; r < row_end; r += splits * 8)
         attend_row<D, BITS>(a, b, s, r / a.group, kvh * a.group + r % a.group, lane);
-    } else if (splits > 1) {
-      // join the blocks of the cluster: a warp per row
+    } else if (TILES == 1 || splits > 1) {
+      // join the blocks of the cluster and, with one row tile, their lanes: a warp per row
+      constexpr int kSets = TILES == 2 ? 1 : 2;
       for (int r = rank * 8 + warp; r < row_end - row0; r += splits * 8) {
-        float mx = -INFINITY;
-        for (int c = 0; c < splits; ++c) mx = fmaxf(mx, ld_cluster_f32(smem_u32(&sh.m[0][0] + r), c));
-        float sum = 0.f, o[D / 32];
+        float mx = -INFINITY, sum = 0.f, o[D / 32];
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
-        for (int c = 0; c < splits; ++c) {
-          const float mc = ld_cluster_f32(smem_u32(&sh.m[0][0] + r), c);
+        for (int c = 0; c < splits * kSets; ++c) mx = fmaxf(mx, ld_cluster_f32(smem_u32(&sh.m[0][0] + c % kSets * kRows + r), c / kSets));
+        for (int c = 0; c < splits * kSets; ++c) {
+          const int at = c % kSets * kRows + r, from = c / kSets;
+          const float mc = ld_cluster_f32(smem_u32(&sh.m[0][0] + at), from);
           const float f = mc == mx ? 1.f : exp2_fast(mc - mx);
-          sum += ld_cluster_f32(smem_u32(&sh.l[0][0] + r), c) * f;
+          sum = fmaf(ld_cluster_f32(smem_u32(&sh.l[0][0] + at), from), f, sum);
 #pragma unroll
           for (int i = 0; i < D / 32; ++i)
-            o[i] = fmaf(ld_cluster_f32(smem + (r * C::kPartRow + lane * (D / 32) + i) * 4, c), f, o[i]);
+            o[i] = fmaf(ld_cluster_f32(smem + (at * C::kPartRow + lane * (D / 32) + i) * 4, from), f, o[i]);
         }
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
         const int gr = row0 + r;
@@ -632,25 +665,25 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::kThreads, 1) k_attend_many(const
 
 template <int D, int BITS, int TILES>
 cudaError_t launch(const AttendParams& a, cudaStream_t st) {
-  using C = Cfg<D, BITS>;
+  using C = Cfg<D, BITS, TILES>;
   PageMaps maps;
   if (make_page_maps(a.c, D, BITS, std::min(a.c.page_size, kTok), &maps)) return cudaErrorInvalidValue;
   auto* f = k_attend_many<D, BITS, TILES>;
-  // a cluster's blocks keep their accumulators where Q and the ring were
-  const int join = TILES * kRows * C::kPartRow * 4 + 1024;
-  const int smem = std::max(C::smem(TILES), join);
   static std::atomic<uint64_t> prepared{0};
-  const cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(f), smem, &prepared);
+  const cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(f), C::kBytes, &prepared);
   if (e != cudaSuccess) return e;
   const int64_t rows = (int64_t)a.c.max_q * a.group;
   const int64_t q_blocks = (rows + TILES * kRows - 1) / (TILES * kRows);
   const int64_t blocks = q_blocks * a.c.n_kv_heads * a.c.batch;
   int64_t tokens = (int64_t)a.c.max_pages << a.c.page_shift;
   if (a.window > 0) tokens = std::min<int64_t>(tokens, (int64_t)a.window + TILES * kRows / a.group + a.sinks + 2 * kTok);
+  // Few rows: the tokens are split until there are blocks for every SM; several sequences, whose lengths may differ, until
+  // each SM has about three.
+  const int64_t want = a.c.batch > 1 && TILES == 1 ? 3 * kSms : kSms;
   int splits = 1;
-  while (splits < 8 && 2 * splits * blocks <= kSms && splits * 4 * kTok <= tokens) splits *= 2;
+  while (splits < 8 && 2 * splits * blocks <= want && splits * 8 * kTok <= tokens) splits *= 2;
   if (splits * q_blocks * a.c.n_kv_heads > 0x7fffffff || rows > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  return launch_cluster(f, dim3((unsigned)(splits * q_blocks * a.c.n_kv_heads), a.c.batch), C::kThreads, smem, splits, st, a, maps, (int)q_blocks, splits);
+  return launch_cluster(f, dim3((unsigned)(splits * q_blocks * a.c.n_kv_heads), a.c.batch), C::kThreads, C::kBytes, splits, st, a, maps, (int)q_blocks, splits);
 }
 
 template <int D, int BITS>
