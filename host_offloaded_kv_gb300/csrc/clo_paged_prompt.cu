@@ -12,14 +12,15 @@
 //   warps 0-3, 4-7   softmax of lane 0, 1 (TMEM rows are tied to a warp's place in its group of four)
 //   warp 8           TMA: pages -> ring of operand tiles, K(0) K(1) V(0) K(2) V(1) ...
 //   warp 9           MMA issue: P V of a token tile, then S of the lane's next one, the lanes in turn
-//   warp 11          bf16 pages: V of the tiles at a mask's edge is looked over (see below)
+//   warp 10          bf16 pages: V behind the last token that any row sees is cleared
 //   warps 12-15      8-bit pages only: codes -> fp16 operand tiles
 //
 // The accumulator is rescaled only when a row's maximum has grown by more than 2^8 (weights stay below 2^8 times
 // the largest so far; exact in the end, as sum and accumulator share the reference).
 //
-// A masked weight is zero, but zero times NaN is not: infinities and NaN in V are cleared in the operand tile wherever not every
-// row sees the token.  If some row does see such a token, the block's rows are computed again one by one.
+// A masked weight is zero, but zero times NaN is not.  V behind the last visible token (a page's end, where memory may never
+// have been written) is cleared in the operand tile; rows that end with an infinity or NaN all the same, because V has one
+// where they do not look, or where they do, are computed again one by one.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -144,16 +145,16 @@ struct Cfg {
 
 struct Shared {
   uint64_t full[8], empty[8];      // operand tiles: filled (TMA or converters), products done
-  uint64_t checked[8];             // bf16: V at a mask's edge looked over
+  uint64_t tail, q_ready;          // bf16: the last V tile, before its end is cleared; Q
   uint64_t raw_full[8], raw_empty[8];
-  uint64_t s_full[2], p_ready[2];  // per lane
+  uint64_t s_full[2], p_half[2], p_ready[2];  // per lane: scores; weights of the first 64 tokens, of all
   uint64_t done;                   // every product of both lanes
   uint64_t meta[kMeta];
-  float scale[kMeta][2][8];
+  float scale[kMeta][3][8];        // K scale, log2 of the V scale, its reciprocal
   uint32_t there[kMeta];
   uint32_t tmem;
-  int odd, failed;
-  float m[2][kRows], l[2][kRows];
+  int failed;
+  float m[2][kRows], l[2][kRows], fac[2][kRows];
 };
 
 // Bounded wait (two seconds, see mbar_wait_limited); once one has given up, the others follow.
@@ -198,18 +199,19 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
   if (tid == 0) {
     for (int i = 0; i < 8; ++i) {
       mbar_init(&sh.full[i], BITS == 16 ? 1 : 128);
-      mbar_init(&sh.empty[i], BITS == 16 ? 2 : 1);  // products; bf16: the look-over
-      mbar_init(&sh.checked[i], 32);
+      mbar_init(&sh.empty[i], 1);
       mbar_init(&sh.raw_full[i], 1);
       mbar_init(&sh.raw_empty[i], 128);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_half[i], 128);
       mbar_init(&sh.p_ready[i], 128);
     }
     mbar_init(&sh.done, 1);
+    mbar_init(&sh.tail, 1);
+    mbar_init(&sh.q_ready, 256);
     for (int i = 0; i < kMeta; ++i) mbar_init(&sh.meta[i], 1);
-    sh.odd = 0;
     sh.failed = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -219,42 +221,6 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
 
-  // Q rows into operand tiles, a row per softmax thread.  8-bit pages: fp16, each row scaled by a power of two that
-  // puts its largest finite element into [2^14, 2^15).
-  float fac = a.scale_log2;
-  const int lane_of_work = (warp >> 2) & 1, my_tile = TILES == 2 ? lane_of_work : 0;
-  const int my_row = row0 + my_tile * kRows + (tid & 127);
-  const bool row_ok = warp < 8 && my_row < rows;
-  if (warp < 8) {
-    const uint16_t* src = a.q + (int64_t)(s.first + my_row / a.group) * a.q_token + (int64_t)(kvh * a.group + my_row % a.group) * a.q_head;
-    const int r = tid & 127;
-    float down = 1.f;
-    if (BITS == 8 && row_ok) {
-      float mx = 0.f;
-      for (int c = 0; c < D / 8; ++c) {
-        float x[8];
-        unpack8(__ldg(reinterpret_cast<const uint4*>(src) + c), x);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fabsf(x[i]) < INFINITY ? fabsf(x[i]) : 0.f);
-      }
-      const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127 - 14, -100), 112);
-      down = __uint_as_float((uint32_t)(127 - e) << 23);
-      fac *= __uint_as_float((uint32_t)(127 + e) << 23);
-    }
-    if (TILES == 2 || warp < 4)
-#pragma unroll 4
-    for (int c = 0; c < D / 8; ++c) {
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (row_ok) v = __ldg(reinterpret_cast<const uint4*>(src) + c);
-      if (BITS == 8) {
-        float x[8];
-        unpack8(v, x);
-        v = make_uint4(pack_f16(x[0] * down, x[1] * down), pack_f16(x[2] * down, x[3] * down), pack_f16(x[4] * down, x[5] * down), pack_f16(x[6] * down, x[7] * down));
-      }
-      *reinterpret_cast<uint4*>(generic + (swizzled<128>(q_smem + my_tile * C::kQBytes, kRows, r, c) - smem)) = v;
-    }
-    fence_proxy_async_smem();
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -274,19 +240,54 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
   auto first_of = [&](int t) { return TILES == 2 ? 0 : t; };
   auto count_of = [&](int t) { return TILES == 2 ? n : (n + 1 - t) / 2; };
   const Visible blk_f = visible_of(pos_first, s.kv_len, a.window, a.sinks), blk_l = visible_of(pos_last, s.kv_len, a.window, a.sinks);
-  // some row does not see all of the token tile (by position: missing pages read as zeros)
-  auto edge = [&](int j) {
-    const int j0 = tl.at(t_begin + j) * kTok;
-    return !(j0 + kTok <= blk_f.hi && (j0 >= blk_l.lo || j0 + kTok <= (a.window > 0 ? a.sinks : 0)));
-  };
+  // the last token tile holds tokens that no row sees
+  const bool tail = n > 0 && (tl.at(t_begin + n - 1) + 1) * kTok > blk_l.hi;
 
   if (warp < 8) {
     // ------------------------------------------------------------------------ softmax
     if (BITS == 16) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    else asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    // Q rows into operand tiles, D / 8 threads per row.  8-bit pages: fp16, each row scaled by a power of two that puts its
+    // largest finite element into [2^14, 2^15).
+    {
+      constexpr int kLanes = D / 8, kStepRows = 256 / kLanes, kIters = TILES * kRows / kStepRows, kBatch = kIters < 8 ? kIters : 8;
+      const int c = tid % kLanes;
+#pragma unroll 1
+      for (int i0 = 0; i0 < kIters; i0 += kBatch) {
+        uint4 v[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int gr = row0 + (i0 + i) * kStepRows + tid / kLanes;
+          v[i] = make_uint4(0, 0, 0, 0);
+          if (gr < rows) v[i] = __ldg(reinterpret_cast<const uint4*>(a.q + (int64_t)(s.first + gr / a.group) * a.q_token + (int64_t)(kvh * a.group + gr % a.group) * a.q_head) + c);
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int r = (i0 + i) * kStepRows + tid / kLanes;
+          if (BITS == 8) {
+            float x[8], mx = 0.f;
+            unpack8(v[i], x);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) mx = fmaxf(mx, fabsf(x[k]) < INFINITY ? fabsf(x[k]) : 0.f);
+#pragma unroll
+            for (int o = kLanes / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127 - 14, -100), 112);
+            const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+            if (c == 0) sh.fac[r / kRows][r % kRows] = a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
+            v[i] = make_uint4(pack_f16(x[0] * down, x[1] * down), pack_f16(x[2] * down, x[3] * down), pack_f16(x[4] * down, x[5] * down), pack_f16(x[6] * down, x[7] * down));
+          }
+          *reinterpret_cast<uint4*>(generic + (swizzled<128>(q_smem + r / kRows * C::kQBytes, kRows, r % kRows, c) - smem)) = v[i];
+        }
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&sh.q_ready);
+    }
     float ref = -INFINITY, l = 0.f;
-    const int t = lane_of_work, mine = count_of(t);
-    bool ok = true;
+    const int t = warp >> 2, mine = count_of(t), my_tile = TILES == 2 ? t : 0;
+    const int my_row = row0 + my_tile * kRows + (tid & 127);
+    const bool row_ok = my_row < rows;
+    bool ok = __all_sync(0xffffffffu, wait(sh, &sh.q_ready, 0));
+    const float fac = BITS == 8 ? sh.fac[my_tile][tid & 127] : a.scale_log2;
     {
       constexpr float kOff = BITS == 16 ? 0.f : 7.f;  // weights of 8-bit pages: up to 2^15 with kGrow, fp16 down to 2^-31
       const uint32_t lane_off = (uint32_t)(warp & 3) * 32u << 16;
@@ -296,7 +297,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
       const Visible vf = visible_of(s.pos0 + rf / a.group, s.kv_len, a.window, a.sinks);
       const Visible vl = visible_of(s.pos0 + rl / a.group, s.kv_len, a.window, a.sinks);
       const Visible v = visible_of(s.pos0 + min(my_row, rows - 1) / a.group, s.kv_len, a.window, a.sinks);
-      for (int i = 0; i < mine; ++i) {
+      for (int i = 0; i < mine && ok; ++i) {
         const int j = first_of(t) + i * kStep, j0 = tl.at(t_begin + j) * kTok;
         const int slot = j % kMeta;
         ok = wait(sh, &sh.meta[slot], (j / kMeta) & 1) && wait(sh, &sh.s_full[t], i & 1);
@@ -325,16 +326,12 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
               if (!(see >> i & 1u)) x[32 * c + i] = 0xff800000u;
           }
         }
-        float ks[BITS == 8 ? 8 : 1], vs[BITS == 8 ? 8 : 1];
         float mx = -INFINITY;
         if (BITS == 8) {
 #pragma unroll
           for (int g = 0; g < 8; ++g) {
-            ks[g] = fmaxf(sh.scale[slot][0][g], kMinScale) * fac;
-            vs[g] = fmaxf(sh.scale[slot][1][g], kMinScale);
-            const uint64_t f2 = pack2(ks[g], ks[g]);
-            const float lv = __log2f(vs[g]);
-            const uint64_t l2 = pack2(lv, lv);
+            const float ks = sh.scale[slot][0][g] * fac, lv = sh.scale[slot][1][g];
+            const uint64_t f2 = pack2(ks, ks), l2 = pack2(lv, lv);
 #pragma unroll
             for (int i = 0; i < 16; i += 2) {
               const float2 y = unpack2(fma2(pack2(__uint_as_float(x[16 * g + i]), __uint_as_float(x[16 * g + i + 1])), f2, l2));
@@ -386,11 +383,16 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
             w[i >> 1] = BITS == 16 ? pack_bf16(y.x, y.y) : pack_f16(y.x, y.y);
             if (BITS == 8 && (c & 15) == 14) {
               const float2 q = unpack2(add2(add2(sum2[0], sum2[1]), add2(sum2[2], sum2[3])));
-              l = fmaf(q.x + q.y, __frcp_rn(vs[c >> 4]), l);
+              l = fmaf(q.x + q.y, sh.scale[slot][2][c >> 4], l);
               sum2[0] = sum2[1] = sum2[2] = sum2[3] = 0;
             }
           }
           tc_st32(s_addr + 32 * h, w);
+          if (h == 0) {
+            tc_wait_st();
+            tc_fence_before();
+            mbar_arrive(&sh.p_half[t]);
+          }
         }
         if (BITS == 16) {
           const float2 q = unpack2(add2(add2(sum2[0], sum2[1]), add2(sum2[2], sum2[3])));
@@ -406,13 +408,13 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
       if (!ok) l = __int_as_float(0x7fffffff);
-      uint16_t* dst = a.out + (int64_t)(s.first + my_row / a.group) * a.o_token + (int64_t)(kvh * a.group + my_row % a.group) * a.o_head;
       const float inv = l == 0.f ? 0.f : 1.f / l;
       float* part = reinterpret_cast<float*>(generic) + (t * kRows + (tid & 127)) * C::kPartRow;
       if (!direct) {
         sh.m[t][tid & 127] = ref;
         sh.l[t][tid & 127] = l;
       }
+      float odd = l * 0.f;  // NaN if anything in the row is no finite number
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
@@ -426,21 +428,42 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
         if (!direct) {
 #pragma unroll
           for (int i = 0; i < 32; i += 4) *reinterpret_cast<uint4*>(part + 32 * c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-        } else if (row_ok) {
+        } else {
+          // through the row tile's Q, which is done with, so that rows leave in whole lines
 #pragma unroll
           for (int i = 0; i < 32; i += 8) {
             float y[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = l == 0.f ? 0.f : __uint_as_float(o[i + e]) * inv;
-            *reinterpret_cast<uint4*>(dst + 32 * c + i) = pack8(y);
+            for (int e = 0; e < 8; ++e) {
+              odd = fmaf(__uint_as_float(o[i + e]), 0.f, odd);
+              y[e] = l == 0.f ? 0.f : __uint_as_float(o[i + e]) * inv;
+            }
+            *reinterpret_cast<uint4*>(generic + (swizzled<128>(q_smem + my_tile * C::kQBytes, kRows, tid & 127, 4 * c + i / 8) - smem)) = pack8(y);
           }
+        }
+      }
+      if (direct) {
+        __syncwarp();
+        constexpr int kLanes = D / 8;
+#pragma unroll 4
+        for (int i = 0; i < kLanes; ++i) {
+          const int r = (warp & 3) * 32 + i * (32 / kLanes) + lane / kLanes, gr = row0 + my_tile * kRows + r;
+          if (gr < rows)
+            *(reinterpret_cast<uint4*>(a.out + (int64_t)(s.first + gr / a.group) * a.o_token + (int64_t)(kvh * a.group + gr % a.group) * a.o_head) + lane % kLanes) =
+                *reinterpret_cast<const uint4*>(generic + (swizzled<128>(q_smem + my_tile * C::kQBytes, kRows, r, lane % kLanes) - smem));
+        }
+        __syncwarp();
+        unsigned again = __ballot_sync(0xffffffffu, row_ok && odd != 0.f);
+        for (; again; again &= again - 1) {
+          const int gr = row0 + my_tile * kRows + (warp & 3) * 32 + __ffs(again) - 1;
+          attend_row<D, BITS>(a, b, s, gr / a.group, kvh * a.group + gr % a.group, lane);
         }
       }
       tc_fence_before();
     }
   } else {
     if (BITS == 16) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-    else asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == 8) {
       // ---------------------------------------------------------------------- TMA
       auto page_for = [&](int j) {
@@ -453,23 +476,11 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
       bool ok = true;
       auto load = [&](int side, int j, int e, int page) {
         const int buf = e % kBuf;
-        uint64_t* full = BITS == 16 ? &sh.full[buf] : &sh.raw_full[buf];
+        uint64_t* full = BITS == 16 ? (tail && side == 1 && j == n - 1 ? &sh.tail : &sh.full[buf]) : &sh.raw_full[buf];
         uint64_t* empty = BITS == 16 ? &sh.empty[buf] : &sh.raw_empty[buf];
         if (e >= kBuf) ok = wait(sh, empty, (e / kBuf - 1) & 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) return;
-        if (side == 0) {
-          const int slot = j % kMeta;
-          const unsigned there = __ballot_sync(0xffffffffu, page >= 0);
-          if (lane == 0) sh.there[slot] = there;
-          if (BITS == 8 && lane < 8) {
-            const int64_t at = (int64_t)max(page, 0) * p.n_kv_heads + kvh;
-            sh.scale[slot][0][lane] = __ldg(p.side[0].scales + at);
-            sh.scale[slot][1][lane] = __ldg(p.side[1].scales + at);
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.meta[slot]);
-        }
         if (lane == 0) mbar_arrive_expect_tx(full, BITS == 16 ? C::kTileBytes : C::kRawBytes);
         __syncwarp();
         const int tok = lane * 16;
@@ -482,14 +493,42 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
         }
         __syncwarp();
       };
-      int page_k = page_for(0), page_v = page_k, page_next = page_for(1);
-      if (n > 0) load(0, 0, 0, page_k);
+      // pages are looked up two tiles ahead, their scales one, so that no load waits for another
+      float2 scale = make_float2(1.f, 1.f);
+      auto scale_for = [&](int page) {
+        if (BITS == 8 && page >= 0) {
+          const int64_t at = (int64_t)page * p.n_kv_heads + kvh;
+          scale = make_float2(__ldg(p.side[0].scales + at), __ldg(p.side[1].scales + at));
+        }
+      };
+      auto tell = [&](int j, int page, float2 sc) {
+        const int slot = j % kMeta;
+        const unsigned there = __ballot_sync(0xffffffffu, page >= 0);
+        if (lane == 0) sh.there[slot] = there;
+        if (BITS == 8 && lane < 8) {
+          const float vs = fmaxf(sc.y, kMinScale);
+          sh.scale[slot][0][lane] = fmaxf(sc.x, kMinScale);
+          sh.scale[slot][1][lane] = __log2f(vs);
+          sh.scale[slot][2][lane] = __frcp_rn(vs);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.meta[slot]);
+      };
+      int page_v = page_for(0), page_k = page_for(1), page_next = page_for(2);
+      if (n > 0) load(0, 0, 0, page_v);
+      scale_for(page_v);
+      if (n > 0) tell(0, page_v, scale);
+      scale_for(page_k);
       for (int j = 0; j < n && ok; ++j) {
-        page_k = page_next;
-        page_next = page_for(j + 2);
+        const float2 sc = scale;
+        const int page_far = page_for(j + 3);
         if (j + 1 < n) load(0, j + 1, at_k(j + 1), page_k);
+        scale_for(page_next);
         if (ok) load(1, j, at_v(j), page_v);
+        if (ok && j + 1 < n) tell(j + 1, page_k, sc);
         page_v = page_k;
+        page_k = page_next;
+        page_next = page_far;
       }
       if (!ok)  // copies in flight land before the block leaves
         for (int i = 0; i < kBuf; ++i)
@@ -511,15 +550,14 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
           tc_mma_ss(tm + 128 * t, qd + off, kd + off, kShapeS, kk > 0, leader);
         }
       };
-      auto values = [&](int t, int slot, bool add) {
+      auto values = [&](int t, int slot, bool add, int from) {
         const uint64_t vd = operand(__shfl_sync(0xffffffffu, ring_u + slot * C::kTileBytes, 0), kTok * 128, 1024);
 #pragma unroll
-        for (int kk = 0; kk < kTok / 16; ++kk)
+        for (int kk = from; kk < from + kTok / 32; ++kk)
           tc_mma_ts(tm + 256 + 128 * t, tm + 128 * t + kk * 8, vd + kk * (2048 >> 4), kShapeO, add || kk > 0, leader);
       };
       auto ready = [&](int e) { return wait(sh, &sh.full[e % SLOTS], (e / SLOTS) & 1); };
-      uint32_t checked = 0;  // phase of each slot's `checked`
-      bool ok = true;
+      bool ok = wait(sh, &sh.q_ready, 0);
       for (int t = 0; t < 2 && ok; ++t) {
         if (count_of(t) == 0) break;
         const int e = at_k(first_of(t));
@@ -535,17 +573,18 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
         const bool next = j + kStep < n;
         const int ek = next ? at_k(j + kStep) : 0, kslot = ek % SLOTS;
         ok = ready(ev) && (!next || ready(ek));
-        if (BITS == 16 && ok && edge(j)) {
-          ok = wait(sh, &sh.checked[vslot], checked >> vslot & 1u);
-          checked ^= 1u << vslot;
-        }
 #pragma unroll
         for (int u = 0; u < TILES; ++u) {
           const int t = TILES == 2 ? u : j & 1;
-          ok = ok && wait(sh, &sh.p_ready[t], (TILES == 2 ? j : j >> 1) & 1);
+          const uint32_t phase = (TILES == 2 ? j : j >> 1) & 1;
+          ok = ok && wait(sh, &sh.p_half[t], phase);
           if (!ok) break;
           tc_fence_after();
-          values(t, vslot, TILES == 2 ? j > 0 : j > 1);
+          values(t, vslot, TILES == 2 ? j > 0 : j > 1, 0);
+          ok = wait(sh, &sh.p_ready[t], phase);
+          if (!ok) break;
+          tc_fence_after();
+          values(t, vslot, true, kTok / 32);
           if (next) score(t, kslot);
           tc_commit(&sh.s_full[t], leader);
         }
@@ -557,60 +596,50 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
       if (ok && n > 0) tc_commit(&sh.done, leader);
       else if (leader) mbar_arrive(&sh.done);
       __syncwarp();
-    } else if (BITS == 16 ? warp == 11 : warp >= 12) {
-      // ---------------------------------------------------------------------- V at a mask's edge; 8-bit codes -> fp16
-      auto seen = [&](int tok) { return tok < blk_l.hi && (tok >= blk_f.lo || tok < (a.window > 0 ? a.sinks : 0)); };
-      bool ok = true;
+    } else if (BITS == 16 ? warp == 10 && tail : warp >= 12) {
       if constexpr (BITS == 16) {
-        for (int e = 0; e < 2 * n; ++e) {
-          const int slot = e % SLOTS, j = tile_of(e);
-          ok = wait(sh, &sh.full[slot], (e / SLOTS) & 1);
-          if (!ok) break;
-          if (is_v(e) && edge(j)) {
-            const int j0 = tl.at(t_begin + j) * kTok;
-#pragma unroll 4
-            for (int i = lane; i < kTok * D / 8; i += 32) {
-              uint4* at = reinterpret_cast<uint4*>(generic + (ring - smem) + slot * C::kTileBytes) + i;
-              if (not_finite16<16>(*at)) {
-                if (seen(j0 + i / 8 % kTok)) sh.odd = 1;
-                *at = make_uint4(0, 0, 0, 0);
-              }
-            }
-            fence_proxy_async_smem();
-            mbar_arrive(&sh.checked[slot]);
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.empty[slot]);
+        // ------------------------------------------------------------------ the last V tile's end
+        const int e = 2 * n - 1, slot = e % SLOTS, from = blk_l.hi - tl.at(t_begin + n - 1) * kTok;  // first token that no row sees
+        if (wait(sh, &sh.tail, 0)) {
+          for (int h = 0; h < D / 64; ++h)
+            for (int i = from * 8 + lane; i < kTok * 8; i += 32)
+              *(reinterpret_cast<uint4*>(generic + (ring - smem) + slot * C::kTileBytes + h * kTok * 128) + i) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.full[slot]);
       } else {
+        // ------------------------------------------------------------------ 8-bit codes -> fp16
         const int th = tid - 384;
-        constexpr int kChunks = D / 16;   // 16-byte chunks of a code row
+        constexpr int kChunks = D / 16, kIters = kTok * kChunks / 128, kBatch = 4;  // 16-byte chunks of a code row; per thread
+        bool ok = true;
         for (int e = 0; e < 2 * n && ok; ++e) {
           const int j = tile_of(e);
           const int buf = e % C::kRaw, slot = e % SLOTS;
           ok = wait(sh, &sh.raw_full[buf], (e / C::kRaw) & 1);
           if (ok && e >= SLOTS) ok = wait(sh, &sh.empty[slot], (e / SLOTS - 1) & 1);
           if (!ok) break;
-          const bool look = is_v(e) && edge(j);
-          const int j0 = tl.at(t_begin + j) * kTok;
+          const int rows_seen = is_v(e) ? blk_l.hi - tl.at(t_begin + j) * kTok : kTok;
           const uint32_t src = raw + buf * C::kRawBytes, dst = ring + slot * C::kTileBytes;
-#pragma unroll 2
-          for (int i = th; i < kTok * kChunks; i += 128) {
-            const int r = i / kChunks, c = i % kChunks;
-            uint4 w = *reinterpret_cast<const uint4*>(generic + (swizzled<(D < 128 ? 64 : 128)>(src, kTok, r, c) - smem));
-            if (look) {
-              // NaN codes are 0x7f and 0xff; the chunk that holds one is cleared
-              if (not_finite16<8>(w)) {
-                if (seen(j0 + r)) sh.odd = 1;
-                w = make_uint4(0, 0, 0, 0);
-              }
+#pragma unroll
+          for (int i0 = 0; i0 < kIters; i0 += kBatch) {
+            uint4 w[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+              const int at = th + (i0 + i) * 128, r = at / kChunks;
+              w[i] = *reinterpret_cast<const uint4*>(generic + (swizzled<(D < 128 ? 64 : 128)>(src, kTok, r, at % kChunks) - smem));
+              if (r >= rows_seen) w[i] = make_uint4(0, 0, 0, 0);
             }
-            const uint4 lo = make_uint4(e4m3_to_f16x2(w.x & 0xffffu), e4m3_to_f16x2(w.x >> 16), e4m3_to_f16x2(w.y & 0xffffu), e4m3_to_f16x2(w.y >> 16));
-            const uint4 hi = make_uint4(e4m3_to_f16x2(w.z & 0xffffu), e4m3_to_f16x2(w.z >> 16), e4m3_to_f16x2(w.w & 0xffffu), e4m3_to_f16x2(w.w >> 16));
-            // the upper half of a row's threads store their second chunk first: eight lanes then cover all banks
-            const bool swap = c >= kChunks / 2;
-            *reinterpret_cast<uint4*>(generic + (swizzled<128>(dst, kTok, r, 2 * c + (swap ? 1 : 0)) - smem)) = swap ? hi : lo;
-            *reinterpret_cast<uint4*>(generic + (swizzled<128>(dst, kTok, r, 2 * c + (swap ? 0 : 1)) - smem)) = swap ? lo : hi;
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+              const int at = th + (i0 + i) * 128, r = at / kChunks, c = at % kChunks;
+              const uint4 lo = make_uint4(e4m3_to_f16x2(w[i].x & 0xffffu), e4m3_to_f16x2(w[i].x >> 16), e4m3_to_f16x2(w[i].y & 0xffffu), e4m3_to_f16x2(w[i].y >> 16));
+              const uint4 hi = make_uint4(e4m3_to_f16x2(w[i].z & 0xffffu), e4m3_to_f16x2(w[i].z >> 16), e4m3_to_f16x2(w[i].w & 0xffffu), e4m3_to_f16x2(w[i].w >> 16));
+              // the upper half of a row's threads store their second chunk first: eight lanes then cover all banks
+              const bool swap = c >= kChunks / 2;
+              *reinterpret_cast<uint4*>(generic + (swizzled<128>(dst, kTok, r, 2 * c + (swap ? 1 : 0)) - smem)) = swap ? hi : lo;
+              *reinterpret_cast<uint4*>(generic + (swizzled<128>(dst, kTok, r, 2 * c + (swap ? 0 : 1)) - smem)) = swap ? lo : hi;
+            }
           }
           fence_proxy_async_smem();
           mbar_arrive(&sh.full[slot]);
@@ -626,35 +655,35 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }
-  bool slow = false;
-  for (int r = 0; r < splits; ++r) slow |= (splits > 1 ? __float_as_int(ld_cluster_f32(smem_u32(&sh.odd), r)) : sh.odd) != 0;
-  if (warp < 8) {
-    if (slow) {
-      for (int r = row0 + rank * 8 + warp; r < row_end; r += splits * 8)
-        attend_row<D, BITS>(a, b, s, r / a.group, kvh * a.group + r % a.group, lane);
-    } else if (TILES == 1 || splits > 1) {
-      // join the blocks of the cluster and, with one row tile, their lanes: a warp per row
-      constexpr int kSets = TILES == 2 ? 1 : 2;
-      for (int r = rank * 8 + warp; r < row_end - row0; r += splits * 8) {
-        float mx = -INFINITY, sum = 0.f, o[D / 32];
+  if (warp < 8 && (TILES == 1 || splits > 1)) {
+    // join the blocks of the cluster and, with one row tile, their lanes: a warp per row
+    constexpr int kSets = TILES == 2 ? 1 : 2;
+    for (int r = rank * 8 + warp; r < row_end - row0; r += splits * 8) {
+      float mx = -INFINITY, sum = 0.f, o[D / 32];
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
-        for (int c = 0; c < splits * kSets; ++c) mx = fmaxf(mx, ld_cluster_f32(smem_u32(&sh.m[0][0] + c % kSets * kRows + r), c / kSets));
-        for (int c = 0; c < splits * kSets; ++c) {
-          const int at = c % kSets * kRows + r, from = c / kSets;
-          const float mc = ld_cluster_f32(smem_u32(&sh.m[0][0] + at), from);
-          const float f = mc == mx ? 1.f : exp2_fast(mc - mx);
-          sum = fmaf(ld_cluster_f32(smem_u32(&sh.l[0][0] + at), from), f, sum);
+      for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
+      for (int c = 0; c < splits * kSets; ++c) mx = fmaxf(mx, ld_cluster_f32(smem_u32(&sh.m[0][0] + c % kSets * kRows + r), c / kSets));
+      for (int c = 0; c < splits * kSets; ++c) {
+        const int at = c % kSets * kRows + r, from = c / kSets;
+        const float mc = ld_cluster_f32(smem_u32(&sh.m[0][0] + at), from);
+        const float f = mc == mx ? 1.f : exp2_fast(mc - mx);
+        sum = fmaf(ld_cluster_f32(smem_u32(&sh.l[0][0] + at), from), f, sum);
 #pragma unroll
-          for (int i = 0; i < D / 32; ++i)
-            o[i] = fmaf(ld_cluster_f32(smem + (at * C::kPartRow + lane * (D / 32) + i) * 4, from), f, o[i]);
-        }
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const int gr = row0 + r;
-        uint16_t* dst = a.out + (int64_t)(s.first + gr / a.group) * a.o_token + (int64_t)(kvh * a.group + gr % a.group) * a.o_head + lane * (D / 32);
-#pragma unroll
-        for (int i = 0; i < D / 32; i += 2) *reinterpret_cast<uint32_t*>(dst + i) = sum == 0.f ? 0u : pack_bf16(o[i] * inv, o[i + 1] * inv);
+        for (int i = 0; i < D / 32; ++i)
+          o[i] = fmaf(ld_cluster_f32(smem + (at * C::kPartRow + lane * (D / 32) + i) * 4, from), f, o[i]);
       }
+      const int gr = row0 + r;
+      float odd = sum * 0.f;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) odd = fmaf(o[i], 0.f, odd);
+      if (__any_sync(0xffffffffu, odd != 0.f)) {
+        attend_row<D, BITS>(a, b, s, gr / a.group, kvh * a.group + gr % a.group, lane);
+        continue;
+      }
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      uint16_t* dst = a.out + (int64_t)(s.first + gr / a.group) * a.o_token + (int64_t)(kvh * a.group + gr % a.group) * a.o_head + lane * (D / 32);
+#pragma unroll
+      for (int i = 0; i < D / 32; i += 2) *reinterpret_cast<uint32_t*>(dst + i) = sum == 0.f ? 0u : pack_bf16(o[i] * inv, o[i + 1] * inv);
     }
   }
   if (splits > 1) {
