@@ -155,6 +155,7 @@ struct AttendParams {
   uint16_t* out;
   int64_t q_token, q_head, o_token, o_head;
   int32_t group;      // query heads per kv head
+  uint32_t group_inv; // ceil(2^32 / group)
   int32_t n_q_heads;
   int32_t window, sinks;
   float scale_log2;   // softmax scale * log2(e)
@@ -162,6 +163,16 @@ struct AttendParams {
   float* part;        // the caller's workspace, or null
   int64_t part_bytes;
 };
+
+// Row of a unit -> query token, for rows below 2^28 (group <= 16: the product's excess stays below one part in `group`).
+__device__ __forceinline__ int token_of_row(const AttendParams& a, int row) {
+  return a.group == 1 ? row : (int)__umulhi((uint32_t)row, a.group_inv);
+}
+// Offset of a unit's row in q-like rows with these strides.
+__device__ __forceinline__ int64_t row_offset(const AttendParams& a, int first, int kvh, int row, int64_t stride_token, int64_t stride_head) {
+  const int t = token_of_row(a, row);
+  return (int64_t)(first + t) * stride_token + (int64_t)(kvh * a.group + row - t * a.group) * stride_head;
+}
 
 // Checks a cache and a batch and fills the kernels' view of them; null or what is wrong.
 const char* paged_params(const clo_paged_cache* c, const clo_paged_batch* b, PagedParams* p);

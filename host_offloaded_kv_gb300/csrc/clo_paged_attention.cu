@@ -79,10 +79,12 @@ static const char* attend_params(const clo_paged_cache* cache, const clo_paged_b
   if (window < 0 || sinks < 0) return "window and sinks must not be negative";
   a->n_q_heads = n_q_heads;
   a->group = n_q_heads / hkv;
+  a->group_inv = (uint32_t)(((uint64_t(1) << 32) + a->group - 1) / a->group);
   a->window = window;
   a->sinks = sinks;
   const int64_t rows = (int64_t)a->c.max_q * a->group;
-  a->part_rows = (int32_t)std::min<int64_t>(rows, 0x7fffffff);
+  if (rows >= int64_t(1) << 28) return "max_q times the heads per kv head must be below 2^28";
+  a->part_rows = (int32_t)rows;
   return nullptr;
 }
 

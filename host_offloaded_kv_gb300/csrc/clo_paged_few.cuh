@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kThreads) k_attend_few(const AttendParams a, c
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const int r = nt * 8 + g;
-    const uint16_t* qp = a.q + (int64_t)(s.first + r / a.group) * a.q_token + (int64_t)(kvh * a.group + r % a.group) * a.q_head;
+    const uint16_t* qp = a.q + row_offset(a, s.first, kvh, r, a.q_token, a.q_head);
     float row_fac = a.scale_log2;
     if (BITS == 16) {
 #pragma unroll
@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(kThreads) k_attend_few(const AttendParams a, c
           sc[mt][nt][i] = BITS == 8 ? fmaf(sc[mt][nt][i], f, lvs) : sc[mt][nt][i] * f;
           if (!whole) {
             const int j = j0 + mt * 16 + g + (i >> 1) * 8;
-            const int pos = s.pos0 + (nt * 8 + 2 * t4 + (i & 1)) / a.group;
+            const int pos = s.pos0 + token_of_row(a, nt * 8 + 2 * t4 + (i & 1));
             const bool see = (there >> mt & 1u) && j <= pos && j < s.kv_len && (a.window == 0 || j > pos - a.window || j < a.sinks);
             if (!see) sc[mt][nt][i] = -INFINITY;
           }
@@ -458,7 +458,7 @@ __global__ void __launch_bounds__(kThreads) k_attend_few(const AttendParams a, c
 
   // Join the blocks: each writes its share of the rows' elements.
   auto store = [&](int r, int d2, float sum, float x, float y) {
-    uint16_t* op = a.out + (int64_t)(s.first + r / a.group) * a.o_token + (int64_t)(kvh * a.group + r % a.group) * a.o_head + d2;
+    uint16_t* op = a.out + row_offset(a, s.first, kvh, r, a.o_token, a.o_head) + d2;
     *reinterpret_cast<uint32_t*>(op) = sum == 0.f ? 0u : pack_bf16(x, y);
   };
   bool slow = false;
@@ -558,7 +558,7 @@ __global__ void __launch_bounds__(8 * D) k_attend_join(const AttendParams a, int
     o += s_o[i][d];
     l += s_l[i];
   }
-  a.out[(int64_t)(s.first + r / a.group) * a.o_token + (int64_t)(kvh * a.group + r % a.group) * a.o_head + d] =
+  a.out[row_offset(a, s.first, kvh, r, a.o_token, a.o_head) + d] =
       (uint16_t)pack_bf16(l == 0.f ? 0.f : o / l, 0.f);
 }
 

@@ -133,9 +133,9 @@ struct Cfg {
   static constexpr int kTileBytes = kTok * D * 2;             // an operand tile
   static constexpr int kQBytes = kRows * D * 2;
   // operand tiles of the ring, and 8-bit tiles on their way into it: what fits next to Q
-  static constexpr int kSlots = BITS == 16 ? (D == 64 ? 8 : TILES == 2 ? 4 : 5) : (D == 64 ? 6 : TILES == 2 ? 3 : 4);
-  static constexpr int kRaw = BITS == 16 ? 0 : D == 64 ? 6 : 3;
-  static constexpr int kRawBytes = BITS == 16 ? 0 : kTok * D;
+  static constexpr int kSlots = BITS == 16 ? (D == 64 ? 8 : TILES == 2 ? 4 : 5) : (D == 64 ? 6 : 4);
+  static constexpr int kRaw = BITS == 16 ? 0 : D == 64 ? 12 : TILES == 2 ? 3 : 6;  // halves of 64 tokens
+  static constexpr int kRawBytes = BITS == 16 ? 0 : kTok * D / 2;
   static constexpr int kThreads = BITS == 16 ? 384 : 512;
   static constexpr int kPartRow = D + 4;                       // floats per row of an accumulator to be joined
   static constexpr int kSmem = TILES * kQBytes + kSlots * kTileBytes + kRaw * kRawBytes;
@@ -146,7 +146,7 @@ struct Cfg {
 struct Shared {
   uint64_t full[8], empty[8];      // operand tiles: filled (TMA or converters), products done
   uint64_t tail, q_ready;          // bf16: the last V tile, before its end is cleared; Q
-  uint64_t raw_full[8], raw_empty[8];
+  uint64_t raw_full[12], raw_empty[12];  // 8-bit pages: halves of tiles on their way
   uint64_t s_full[2], p_half[2], p_ready[2];  // per lane: scores; weights of the first 64 tokens, of all
   uint64_t done;                   // every product of both lanes
   uint64_t meta[kMeta];
@@ -198,8 +198,10 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
 
   if (tid == 0) {
     for (int i = 0; i < 8; ++i) {
-      mbar_init(&sh.full[i], BITS == 16 ? 1 : 128);
+      mbar_init(&sh.full[i], BITS == 16 ? 1 : 2 * 128);
       mbar_init(&sh.empty[i], 1);
+    }
+    for (int i = 0; i < 12; ++i) {
       mbar_init(&sh.raw_full[i], 1);
       mbar_init(&sh.raw_empty[i], 128);
     }
@@ -245,38 +247,38 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
 
   if (warp < 8) {
     // ------------------------------------------------------------------------ softmax
-    if (BITS == 16) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    else asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     // Q rows into operand tiles, D / 8 threads per row.  8-bit pages: fp16, each row scaled by a power of two that puts its
     // largest finite element into [2^14, 2^15).
     {
-      constexpr int kLanes = D / 8, kStepRows = 256 / kLanes, kIters = TILES * kRows / kStepRows, kBatch = kIters < 8 ? kIters : 8;
+      constexpr int kLanes = D / 8, kStepRows = 256 / kLanes, kIters = TILES * kRows / kStepRows;
       const int c = tid % kLanes;
 #pragma unroll 1
-      for (int i0 = 0; i0 < kIters; i0 += kBatch) {
-        uint4 v[kBatch];
+      for (int i = 0; i < kIters; ++i) {
+        const int r = i * kStepRows + tid / kLanes, gr = row0 + r;
+        uint8_t* to = generic + (swizzled<128>(q_smem + r / kRows * C::kQBytes, kRows, r % kRows, c) - smem);
+        if (gr < rows)
+          cp_async16(to, a.q + row_offset(a, s.first, kvh, gr, a.q_token, a.q_head) + c * 8);
+        else
+          *reinterpret_cast<uint4*>(to) = make_uint4(0, 0, 0, 0);
+      }
+      cp_async_commit();
+      cp_async_wait<0>();
+      if (BITS == 8) {
+        __syncwarp();
+#pragma unroll 1
+        for (int i = 0; i < kIters; ++i) {
+          const int r = i * kStepRows + tid / kLanes;
+          uint4* at = reinterpret_cast<uint4*>(generic + (swizzled<128>(q_smem + r / kRows * C::kQBytes, kRows, r % kRows, c) - smem));
+          float x[8], mx = 0.f;
+          unpack8(*at, x);
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int gr = row0 + (i0 + i) * kStepRows + tid / kLanes;
-          v[i] = make_uint4(0, 0, 0, 0);
-          if (gr < rows) v[i] = __ldg(reinterpret_cast<const uint4*>(a.q + (int64_t)(s.first + gr / a.group) * a.q_token + (int64_t)(kvh * a.group + gr % a.group) * a.q_head) + c);
-        }
+          for (int k = 0; k < 8; ++k) mx = fmaxf(mx, fabsf(x[k]) < INFINITY ? fabsf(x[k]) : 0.f);
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int r = (i0 + i) * kStepRows + tid / kLanes;
-          if (BITS == 8) {
-            float x[8], mx = 0.f;
-            unpack8(v[i], x);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) mx = fmaxf(mx, fabsf(x[k]) < INFINITY ? fabsf(x[k]) : 0.f);
-#pragma unroll
-            for (int o = kLanes / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127 - 14, -100), 112);
-            const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-            if (c == 0) sh.fac[r / kRows][r % kRows] = a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
-            v[i] = make_uint4(pack_f16(x[0] * down, x[1] * down), pack_f16(x[2] * down, x[3] * down), pack_f16(x[4] * down, x[5] * down), pack_f16(x[6] * down, x[7] * down));
-          }
-          *reinterpret_cast<uint4*>(generic + (swizzled<128>(q_smem + r / kRows * C::kQBytes, kRows, r % kRows, c) - smem)) = v[i];
+          for (int o = kLanes / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+          const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127 - 14, -100), 112);
+          const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+          if (c == 0) sh.fac[r / kRows][r % kRows] = a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
+          *at = make_uint4(pack_f16(x[0] * down, x[1] * down), pack_f16(x[2] * down, x[3] * down), pack_f16(x[4] * down, x[5] * down), pack_f16(x[6] * down, x[7] * down));
         }
       }
       fence_proxy_async_smem();
@@ -306,15 +308,17 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
           break;
         }
         tc_fence_after();
-        uint32_t x[128];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tc_ld32(s_addr + 32 * c, x + 32 * c);
-        tc_wait_ld<4>(x);
         const uint32_t there = sh.there[slot];
         const bool whole = there == 0xffu && j0 + kTok <= vf.hi && (j0 >= vl.lo || j0 + kTok <= (a.window > 0 ? a.sinks : 0));
-        if (!whole) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
+        // Scores stay in TMEM and pass through registers in parts, twice: for the maximum, then for the weights, which go over
+        // columns already read.  (Code of a whole row's 128 scores does not fit the instruction cache beside the other roles'.)
+        float mx = -INFINITY;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t x[32];
+          tc_ld32(s_addr + 32 * c, x);
+          tc_wait_ld<1>(x);
+          if (!whole) {
             // bits of the columns 32 c .. 32 c + 31 that this row sees
             const int base = j0 + 32 * c;
             auto below = [&](int end) { return end - base >= 32 ? 0xffffffffu : end <= base ? 0u : (1u << (end - base)) - 1u; };
@@ -322,85 +326,77 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
             if (!(there >> (2 * c) & 1u)) see &= 0xffff0000u;
             if (!(there >> (2 * c + 1) & 1u)) see &= 0x0000ffffu;
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (!(see >> i & 1u)) x[32 * c + i] = 0xff800000u;
+            for (int k = 0; k < 32; ++k)
+              if (!(see >> k & 1u)) x[k] = 0xff800000u;
+            tc_st32(s_addr + 32 * c, x);
           }
-        }
-        float mx = -INFINITY;
-        if (BITS == 8) {
+          float m2[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-          for (int g = 0; g < 8; ++g) {
-            const float ks = sh.scale[slot][0][g] * fac, lv = sh.scale[slot][1][g];
-            const uint64_t f2 = pack2(ks, ks), l2 = pack2(lv, lv);
+          for (int k = 0; k < 32; k += 4)
 #pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-              const float2 y = unpack2(fma2(pack2(__uint_as_float(x[16 * g + i]), __uint_as_float(x[16 * g + i + 1])), f2, l2));
-              x[16 * g + i] = __float_as_uint(y.x);
-              x[16 * g + i + 1] = __float_as_uint(y.y);
-              mx = fmaxf(mx, fmaxf(y.x, y.y));
+            for (int h = 0; h < 2; ++h) {
+              const int at = BITS == 8 ? 16 * h + k / 2 : k + 2 * h;  // 8-bit pages: a maximum per 16 tokens, which share a scale
+              m2[h] = fmaxf(m2[h], fmaxf(__uint_as_float(x[at]), __uint_as_float(x[at + 1])));
             }
+          if (BITS == 8) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) m2[h] = fmaf(m2[h], fmaxf(sh.scale[slot][0][2 * c + h] * fac, 1e-37f), sh.scale[slot][1][2 * c + h]);
           }
-        } else {
-          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int i = 0; i < 128; i += 8)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) m4[c] = fmaxf(m4[c], fmaxf(__uint_as_float(x[i + 2 * c]), __uint_as_float(x[i + 2 * c + 1])));
-          mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * fac;
+          mx = fmaxf(mx, fmaxf(m2[0], m2[1]));
         }
+        if (BITS == 16) mx *= fac;
+        if (!whole) tc_wait_st();
         const bool grow = mx > ref + kGrow;
         if (__any_sync(0xffffffffu, grow)) {
           const float f = grow ? (ref == -INFINITY ? 0.f : exp2_fast(ref - mx)) : 1.f;
           if (grow) ref = mx;
           l *= f;
           if (i > 0) {
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
               uint32_t o[32];
               tc_ld32(o_addr + 32 * c, o);
               tc_wait_ld<1>(o);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
               tc_st32(o_addr + 32 * c, o);
             }
           }
         }
         const float sub = ref == -INFINITY ? 0.f : kOff - ref;
-        const uint64_t sub2 = pack2(sub, sub), fac2 = pack2(fac, fac);
-        uint64_t sum2[4] = {0, 0, 0, 0};
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          uint32_t x[64], w[32];
+          tc_ld32(s_addr + 64 * half, x);
+          tc_ld32(s_addr + 64 * half + 32, x + 32);
+          tc_wait_ld<2>(x);
+          uint64_t sum2[2] = {0, 0};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t w[32];
+          for (int h = 0; h < 4; ++h) {
+            // 16 tokens: one page, one set of scales
+            const int at = 4 * half + h;
+            const float mul = BITS == 8 ? fmaxf(sh.scale[slot][0][at] * fac, 1e-37f) : fac, add = BITS == 8 ? sh.scale[slot][1][at] + sub : sub;
+            const uint64_t mul2 = pack2(mul, mul), add_2 = pack2(add, add);
 #pragma unroll
-          for (int i = 0; i < 64; i += 2) {
-            const int c = 64 * h + i;
-            const uint64_t x2 = pack2(__uint_as_float(x[c]), __uint_as_float(x[c + 1]));
-            float2 y = unpack2(BITS == 8 ? add2(x2, sub2) : fma2(x2, fac2, sub2));
-            y.x = exp2_fast(y.x);
-            y.y = exp2_fast(y.y);
-            sum2[(i >> 1) & 3] = add2(sum2[(i >> 1) & 3], pack2(y.x, y.y));
-            // weights in the products' type: bf16 next to bf16 V, fp16 next to 8-bit V
-            w[i >> 1] = BITS == 16 ? pack_bf16(y.x, y.y) : pack_f16(y.x, y.y);
-            if (BITS == 8 && (c & 15) == 14) {
-              const float2 q = unpack2(add2(add2(sum2[0], sum2[1]), add2(sum2[2], sum2[3])));
-              l = fmaf(q.x + q.y, sh.scale[slot][2][c >> 4], l);
-              sum2[0] = sum2[1] = sum2[2] = sum2[3] = 0;
+            for (int k = 0; k < 16; k += 2) {
+              float2 y = unpack2(fma2(pack2(__uint_as_float(x[16 * h + k]), __uint_as_float(x[16 * h + k + 1])), mul2, add_2));
+              y.x = exp2_fast(y.x);
+              y.y = exp2_fast(y.y);
+              sum2[(k >> 1) & 1] = add2(sum2[(k >> 1) & 1], pack2(y.x, y.y));
+              // weights in the products' type: bf16 next to bf16 V, fp16 next to 8-bit V
+              w[8 * h + k / 2] = BITS == 16 ? pack_bf16(y.x, y.y) : pack_f16(y.x, y.y);
+            }
+            if (BITS == 8 || h == 3) {
+              const float2 q = unpack2(add2(sum2[0], sum2[1]));
+              l = BITS == 8 ? fmaf(q.x + q.y, sh.scale[slot][2][at], l) : l + (q.x + q.y);
+              sum2[0] = sum2[1] = 0;
             }
           }
-          tc_st32(s_addr + 32 * h, w);
-          if (h == 0) {
-            tc_wait_st();
-            tc_fence_before();
-            mbar_arrive(&sh.p_half[t]);
-          }
+          tc_st32(s_addr + 32 * half, w);
+          tc_wait_st();
+          tc_fence_before();
+          mbar_arrive(half == 0 ? &sh.p_half[t] : &sh.p_ready[t]);
         }
-        if (BITS == 16) {
-          const float2 q = unpack2(add2(add2(sum2[0], sum2[1]), add2(sum2[2], sum2[3])));
-          l += q.x + q.y;
-        }
-        tc_wait_st();
-        tc_fence_before();
-        mbar_arrive(&sh.p_ready[t]);
       }
       // the lane's last product; where the accumulators go to shared memory, every product
       const bool direct = TILES == 2 && splits == 1;
@@ -415,7 +411,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
         sh.l[t][tid & 127] = l;
       }
       float odd = l * 0.f;  // NaN if anything in the row is no finite number
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
         if (mine > 0) {
@@ -445,11 +441,11 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
       if (direct) {
         __syncwarp();
         constexpr int kLanes = D / 8;
-#pragma unroll 4
+#pragma unroll 2
         for (int i = 0; i < kLanes; ++i) {
           const int r = (warp & 3) * 32 + i * (32 / kLanes) + lane / kLanes, gr = row0 + my_tile * kRows + r;
           if (gr < rows)
-            *(reinterpret_cast<uint4*>(a.out + (int64_t)(s.first + gr / a.group) * a.o_token + (int64_t)(kvh * a.group + gr % a.group) * a.o_head) + lane % kLanes) =
+            *(reinterpret_cast<uint4*>(a.out + row_offset(a, s.first, kvh, gr, a.o_token, a.o_head)) + lane % kLanes) =
                 *reinterpret_cast<const uint4*>(generic + (swizzled<128>(q_smem + my_tile * C::kQBytes, kRows, r, lane % kLanes) - smem));
         }
         __syncwarp();
@@ -462,36 +458,38 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
       tc_fence_before();
     }
   } else {
-    if (BITS == 16) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-    else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == 8) {
       // ---------------------------------------------------------------------- TMA
       auto page_for = [&](int j) {
         return lane < 8 && j < n ? page_of(p, b, (tl.at(t_begin + j) * kTok + lane * 16) >> p.page_shift) : -1;
       };
-      const int box = min(p.page_size, kTok);
       constexpr int kSpan = BITS == 16 ? 128 : (D < 128 ? D : 128);  // bytes of a page row in one box
       constexpr int kBoxSpans = D * BITS / 8 / kSpan;
       constexpr int kBuf = BITS == 16 ? C::kSlots : C::kRaw;
+      constexpr int kParts = BITS == 16 ? 1 : 2, kPartTok = kTok / kParts;
+      const int box = min(p.page_size, kPartTok);
       bool ok = true;
       auto load = [&](int side, int j, int e, int page) {
-        const int buf = e % kBuf;
-        uint64_t* full = BITS == 16 ? (tail && side == 1 && j == n - 1 ? &sh.tail : &sh.full[buf]) : &sh.raw_full[buf];
-        uint64_t* empty = BITS == 16 ? &sh.empty[buf] : &sh.raw_empty[buf];
-        if (e >= kBuf) ok = wait(sh, empty, (e / kBuf - 1) & 1);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) return;
-        if (lane == 0) mbar_arrive_expect_tx(full, BITS == 16 ? C::kTileBytes : C::kRawBytes);
-        __syncwarp();
-        const int tok = lane * 16;
-        if (lane < 8 && tok % box == 0) {
-          const uint32_t dst = (BITS == 16 ? ring + buf * C::kTileBytes : raw + buf * C::kRawBytes) + tok * kSpan;
-          const int slot = (tl.at(t_begin + j) * kTok + tok) & (p.page_size - 1);
 #pragma unroll
-          for (int h = 0; h < kBoxSpans; ++h)
-            tma_box(dst + h * kTok * kSpan, &maps.side[side], h * (kSpan * 8 / BITS), slot, kvh, page, smem_u32(full));
+        for (int h = 0; h < kParts; ++h) {
+          const int x = e * kParts + h, buf = x % kBuf;
+          uint64_t* full = BITS == 16 ? (tail && side == 1 && j == n - 1 ? &sh.tail : &sh.full[buf]) : &sh.raw_full[buf];
+          uint64_t* empty = BITS == 16 ? &sh.empty[buf] : &sh.raw_empty[buf];
+          if (x >= kBuf) ok = wait(sh, empty, (x / kBuf - 1) & 1);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) return;
+          if (lane == 0) mbar_arrive_expect_tx(full, BITS == 16 ? C::kTileBytes : C::kRawBytes);
+          __syncwarp();
+          const int tok = lane * 16, in_part = tok - h * kPartTok;
+          if (in_part >= 0 && in_part < kPartTok && tok % box == 0) {
+            const uint32_t dst = (BITS == 16 ? ring + buf * C::kTileBytes : raw + buf * C::kRawBytes) + in_part * kSpan;
+            const int slot = (tl.at(t_begin + j) * kTok + tok) & (p.page_size - 1);
+#pragma unroll
+            for (int w = 0; w < kBoxSpans; ++w)
+              tma_box(dst + w * kTok * kSpan, &maps.side[side], w * (kSpan * 8 / BITS), slot, kvh, page, smem_u32(full));
+          }
+          __syncwarp();
         }
-        __syncwarp();
       };
       // pages are looked up two tiles ahead, their scales one, so that no load waits for another
       float2 scale = make_float2(1.f, 1.f);
@@ -568,11 +566,15 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
         tc_commit(&sh.s_full[t], leader);
         if (TILES == 1 || t == 1) tc_commit(&sh.empty[e % SLOTS], leader);
       }
+      // V of tile j and K of the lane's next tile; looked at ahead of time, between two products' issue, where a wait
+      // costs nothing
+      auto seen = [&](int e) { return mbar_test(&sh.full[e % SLOTS], (e / SLOTS) & 1); };
+      bool ahead = false;
       for (int j = 0; j < n && ok; ++j) {
         const int ev = at_v(j), vslot = ev % SLOTS;
         const bool next = j + kStep < n;
         const int ek = next ? at_k(j + kStep) : 0, kslot = ek % SLOTS;
-        ok = ready(ev) && (!next || ready(ek));
+        if (!ahead) ok = ready(ev) && (!next || ready(ek));
 #pragma unroll
         for (int u = 0; u < TILES; ++u) {
           const int t = TILES == 2 ? u : j & 1;
@@ -585,13 +587,14 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
           if (!ok) break;
           tc_fence_after();
           values(t, vslot, true, kTok / 32);
+          if (u == TILES - 1) {
+            tc_commit(&sh.empty[vslot], leader);
+            ahead = __all_sync(0xffffffffu, j + 1 < n && seen(at_v(j + 1)) && (j + 1 + kStep >= n || seen(at_k(j + 1 + kStep))));
+          }
           if (next) score(t, kslot);
           tc_commit(&sh.s_full[t], leader);
         }
-        if (ok) {
-          tc_commit(&sh.empty[vslot], leader);
-          if (next) tc_commit(&sh.empty[kslot], leader);
-        }
+        if (ok && next) tc_commit(&sh.empty[kslot], leader);
       }
       if (ok && n > 0) tc_commit(&sh.done, leader);
       else if (leader) mbar_arrive(&sh.done);
@@ -610,40 +613,48 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
         if (lane == 0) mbar_arrive(&sh.full[slot]);
       } else {
         // ------------------------------------------------------------------ 8-bit codes -> fp16
-        const int th = tid - 384;
-        constexpr int kChunks = D / 16, kIters = kTok * kChunks / 128, kBatch = 4;  // 16-byte chunks of a code row; per thread
+        // A warp takes 16 rows of a half tile, a quarter of it 4 neighbouring chunks of two rows that differ in bits 0 and 2: then
+        // neither the reads nor the writes of the swizzled tiles meet in a bank.
+        constexpr int kHalves = D / 64, kPer = 2 * kHalves;  // 16-byte chunks of codes per thread and half tile
+        const int w4 = warp - 12, pair = lane >> 3, r8 = lane & 4 ? pair ^ 5 : pair;
+        uint32_t from[kPer], to[kPer];  // offsets in the half tile and in the operand tile's half
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const int r = w4 * 16 + i / kHalves * 8 + r8, h = i % kHalves, c = h * 4 + (lane & 3);
+          from[i] = swizzled<(D < 128 ? 64 : 128)>(0, kTok, r, c);
+          to[i] = h * kTok * 128 + r * 128 + (((2 * (lane & 3)) ^ (r & 7)) << 4);
+        }
         bool ok = true;
         for (int e = 0; e < 2 * n && ok; ++e) {
-          const int j = tile_of(e);
-          const int buf = e % C::kRaw, slot = e % SLOTS;
-          ok = wait(sh, &sh.raw_full[buf], (e / C::kRaw) & 1);
-          if (ok && e >= SLOTS) ok = wait(sh, &sh.empty[slot], (e / SLOTS - 1) & 1);
-          if (!ok) break;
-          const int rows_seen = is_v(e) ? blk_l.hi - tl.at(t_begin + j) * kTok : kTok;
-          const uint32_t src = raw + buf * C::kRawBytes, dst = ring + slot * C::kTileBytes;
+          const int slot = e % SLOTS;
+          if (e >= SLOTS) ok = wait(sh, &sh.empty[slot], (e / SLOTS - 1) & 1);
+          const int seen = is_v(e) ? blk_l.hi - tl.at(t_begin + tile_of(e)) * kTok : kTok;  // tokens that some row sees
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+            const int x = 2 * e + half, buf = x % C::kRaw;
+            ok = ok && wait(sh, &sh.raw_full[buf], (x / C::kRaw) & 1);
+            if (!ok) break;
+            const uint8_t* src = generic + (raw - smem) + buf * C::kRawBytes;
+            uint8_t* dst = generic + (ring - smem) + slot * C::kTileBytes + half * 64 * 128;
+            uint4 w[kPer];
 #pragma unroll
-          for (int i0 = 0; i0 < kIters; i0 += kBatch) {
-            uint4 w[kBatch];
+            for (int i = 0; i < kPer; ++i) w[i] = *reinterpret_cast<const uint4*>(src + from[i]);
+            mbar_arrive(&sh.raw_empty[buf]);
+            if (seen < kTok) {
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-              const int at = th + (i0 + i) * 128, r = at / kChunks;
-              w[i] = *reinterpret_cast<const uint4*>(generic + (swizzled<(D < 128 ? 64 : 128)>(src, kTok, r, at % kChunks) - smem));
-              if (r >= rows_seen) w[i] = make_uint4(0, 0, 0, 0);
+              for (int i = 0; i < kPer; ++i)
+                if (half * 64 + w4 * 16 + i / kHalves * 8 + r8 >= seen) w[i] = make_uint4(0, 0, 0, 0);
             }
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-              const int at = th + (i0 + i) * 128, r = at / kChunks, c = at % kChunks;
-              const uint4 lo = make_uint4(e4m3_to_f16x2(w[i].x & 0xffffu), e4m3_to_f16x2(w[i].x >> 16), e4m3_to_f16x2(w[i].y & 0xffffu), e4m3_to_f16x2(w[i].y >> 16));
-              const uint4 hi = make_uint4(e4m3_to_f16x2(w[i].z & 0xffffu), e4m3_to_f16x2(w[i].z >> 16), e4m3_to_f16x2(w[i].w & 0xffffu), e4m3_to_f16x2(w[i].w >> 16));
-              // the upper half of a row's threads store their second chunk first: eight lanes then cover all banks
-              const bool swap = c >= kChunks / 2;
-              *reinterpret_cast<uint4*>(generic + (swizzled<128>(dst, kTok, r, 2 * c + (swap ? 1 : 0)) - smem)) = swap ? hi : lo;
-              *reinterpret_cast<uint4*>(generic + (swizzled<128>(dst, kTok, r, 2 * c + (swap ? 0 : 1)) - smem)) = swap ? lo : hi;
+            for (int i = 0; i < kPer; ++i) {
+              *reinterpret_cast<uint4*>(dst + to[i]) =
+                  make_uint4(e4m3_to_f16x2(w[i].x & 0xffffu), e4m3_to_f16x2(w[i].x >> 16), e4m3_to_f16x2(w[i].y & 0xffffu), e4m3_to_f16x2(w[i].y >> 16));
+              *reinterpret_cast<uint4*>(dst + (to[i] ^ 16)) =
+                  make_uint4(e4m3_to_f16x2(w[i].z & 0xffffu), e4m3_to_f16x2(w[i].z >> 16), e4m3_to_f16x2(w[i].w & 0xffffu), e4m3_to_f16x2(w[i].w >> 16));
             }
+            fence_proxy_async_smem();
+            mbar_arrive(&sh.full[slot]);
           }
-          fence_proxy_async_smem();
-          mbar_arrive(&sh.full[slot]);
-          mbar_arrive(&sh.raw_empty[buf]);
         }
       }
     }
@@ -681,7 +692,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
         continue;
       }
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      uint16_t* dst = a.out + (int64_t)(s.first + gr / a.group) * a.o_token + (int64_t)(kvh * a.group + gr % a.group) * a.o_head + lane * (D / 32);
+      uint16_t* dst = a.out + row_offset(a, s.first, kvh, gr, a.o_token, a.o_head) + lane * (D / 32);
 #pragma unroll
       for (int i = 0; i < D / 32; i += 2) *reinterpret_cast<uint32_t*>(dst + i) = sum == 0.f ? 0u : pack_bf16(o[i] * inv, o[i + 1] * inv);
     }
@@ -696,7 +707,7 @@ template <int D, int BITS, int TILES>
 cudaError_t launch(const AttendParams& a, cudaStream_t st) {
   using C = Cfg<D, BITS, TILES>;
   PageMaps maps;
-  if (make_page_maps(a.c, D, BITS, std::min(a.c.page_size, kTok), &maps)) return cudaErrorInvalidValue;
+  if (make_page_maps(a.c, D, BITS, std::min(a.c.page_size, BITS == 16 ? kTok : kTok / 2), &maps)) return cudaErrorInvalidValue;
   auto* f = k_attend_many<D, BITS, TILES>;
   static std::atomic<uint64_t> prepared{0};
   const cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(f), C::kBytes, &prepared);
