@@ -132,6 +132,10 @@ __device__ __forceinline__ uint32_t e4m3_to_f16x2(uint32_t two) {
   asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(r) : "r"(two));
   return r;
 }
+// Four codes as two fp16 pairs.
+__device__ __forceinline__ void e4m3_to_f16x4(uint32_t four, uint32_t* lo, uint32_t* hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}" : "=r"(*lo), "=r"(*hi) : "r"(four));
+}
 __device__ __forceinline__ float2 e4m3_to_f32x2(uint32_t two) {
   const uint32_t h = e4m3_to_f16x2(two);
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
@@ -189,7 +193,15 @@ struct PageMaps {
 // Null, or what failed.
 const char* make_page_maps(const PagedParams& c, int head_dim, int kv_bits, int rows, PageMaps* maps);
 
-// One box to shared memory; pages outside the map read as zeros.
+// Nonzero in one thread of a converged warp.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r;
+}
+
+// One box to shared memory; pages outside the map read as zeros.  The instruction takes its operands from uniform registers: lanes that
+// issue boxes of their own run one after the other, some 180 cycles each, so one thread issues all of a tile's.
 __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int element, int slot, int head, int page, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),

@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(kThreads) k_attend_few(const AttendParams a, c
   __shared__ int s_odd;
 
   const PagedParams& p = a.c;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, g = lane >> 2, t4 = lane & 3;
   const int kvh = blockIdx.y, b = blockIdx.z;
   const SeqRows s = seq_rows(p, b);
   const int rows = s.n * a.group;
@@ -107,30 +107,32 @@ __global__ void __launch_bounds__(kThreads) k_attend_few(const AttendParams a, c
   };
   auto issue = [&](int k, int page, int st) {
     const unsigned there = __ballot_sync(0xffffffffu, page >= 0);
-    if (lane == 0) {
+    if (BITS == 8 && page >= 0) {  // lanes below KM
+      const int64_t at = (int64_t)page * p.n_kv_heads + kvh;
+#pragma unroll
+      for (int side = 0; side < 2; ++side)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(&s_scale[warp][st][side][lane])), "l"(p.side[side].scales + at) : "memory");
+    }
+    const int box = min(p.page_size, TOK), first = tl.at(k) * TOK;
+    const uint32_t dst = ring + st * kStageBytes, bar = smem_u32(&s_full[warp][st]);
+    int id[KM];
+#pragma unroll
+    for (int g = 0; g < KM; ++g) id[g] = __shfl_sync(0xffffffffu, page, g);
+    if (elect_one()) {
       s_there[warp][st] = there;
       mbar_arrive_expect_tx(&s_full[warp][st], kStageBytes);
+#pragma unroll
+      for (int g = 0; g < KM; ++g)
+        if (g * 16 % box == 0) {
+#pragma unroll
+          for (int side = 0; side < 2; ++side)
+#pragma unroll
+            for (int h = 0; h < T::kSpans; ++h)
+              tma_box(dst + side * T::kSideBytes + h * TOK * T::kSpan + g * 16 * T::kSpan, &maps.side[side], h * (T::kSpan * 8 / BITS),
+                      (first + g * 16) & (p.page_size - 1), kvh, id[g], bar);
+        }
     }
     __syncwarp();
-    if (lane < KM) {
-      if (BITS == 8 && page >= 0) {
-        const int64_t at = (int64_t)page * p.n_kv_heads + kvh;
-#pragma unroll
-        for (int side = 0; side < 2; ++side)
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(&s_scale[warp][st][side][lane])), "l"(p.side[side].scales + at) : "memory");
-      }
-      const int box = min(p.page_size, TOK);
-      const int tok = lane * 16;
-      if (tok % box == 0) {
-        const int slot = (tl.at(k) * TOK + tok) & (p.page_size - 1);
-#pragma unroll
-        for (int side = 0; side < 2; ++side)
-#pragma unroll
-          for (int h = 0; h < T::kSpans; ++h)
-            tma_box(ring + st * kStageBytes + side * T::kSideBytes + h * TOK * T::kSpan + tok * T::kSpan, &maps.side[side],
-                    h * (T::kSpan * 8 / BITS), slot, kvh, page, smem_u32(&s_full[warp][st]));
-      }
-    }
     if (BITS == 8) cp_async_commit();
   };
 
@@ -260,8 +262,9 @@ __global__ void __launch_bounds__(kThreads) k_attend_few(const AttendParams a, c
           ldsm4(swizzled<T::kSpan>(kb, TOK, mt * 16 + (lane & 15), kk + (lane >> 4)), r);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const uint32_t f[4] = {e4m3_to_f16x2(r[2 * i] & 0xffffu), e4m3_to_f16x2(r[2 * i + 1] & 0xffffu), e4m3_to_f16x2(r[2 * i] >> 16),
-                                   e4m3_to_f16x2(r[2 * i + 1] >> 16)};
+            uint32_t f[4];
+            e4m3_to_f16x4(r[2 * i], &f[0], &f[2]);
+            e4m3_to_f16x4(r[2 * i + 1], &f[1], &f[3]);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) mma16816<BITS>(sc[mt][nt], f, qf[nt][kk + i][0], qf[nt][kk + i][1]);
           }
@@ -359,7 +362,9 @@ __global__ void __launch_bounds__(kThreads) k_attend_few(const AttendParams a, c
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const uint32_t x = __byte_perm(r[2 * i], 0u, 0x3120), y = __byte_perm(r[2 * i + 1], 0u, 0x3120);
-            const uint32_t f[4] = {e4m3_to_f16x2(x & 0xffffu), e4m3_to_f16x2(x >> 16), e4m3_to_f16x2(y & 0xffffu), e4m3_to_f16x2(y >> 16)};
+            uint32_t f[4];
+            e4m3_to_f16x4(x, &f[0], &f[1]);
+            e4m3_to_f16x4(y, &f[2], &f[3]);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) mma16816<BITS>(acc[dt + i][nt], f, pf[mt][nt][0], pf[mt][nt][1]);
           }

@@ -10,7 +10,7 @@
 // their sums are joined at the end.
 //
 //   warps 0-3, 4-7   softmax of lane 0, 1 (TMEM rows are tied to a warp's place in its group of four)
-//   warp 8           TMA: pages -> ring of operand tiles, K(0) K(1) V(0) K(2) V(1) ...
+//   warps 8, 11      TMA of K and of V: pages -> ring of operand tiles, K(0) K(1) V(0) K(2) V(1) ...
 //   warp 9           MMA issue: P V of a token tile, then S of the lane's next one, the lanes in turn
 //   warp 10          bf16 pages: V behind the last token that any row sees is cleared
 //   warps 12-15      8-bit pages only: codes -> fp16 operand tiles
@@ -32,20 +32,12 @@ namespace {
 
 constexpr int kTok = 128;    // tokens per tile
 constexpr int kRows = 128;   // rows per row tile
-constexpr int kMeta = 16;    // token tiles whose page data is kept: more than the ring runs ahead
 constexpr float kGrow = 8.f;
 
 // ---------------------------------------------------------------------------- tcgen05
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-// Issue by one elected thread of a converged warp (`leader` is nonzero in it): what the warp computes for an
-// instruction stays in uniform registers, which the instruction wants.
-__device__ __forceinline__ uint32_t elect_one() {
-  uint32_t r;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-  return r;
-}
 __device__ __forceinline__ void tc_commit(uint64_t* bar, uint32_t leader) {
   asm volatile(
       "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
@@ -134,31 +126,35 @@ struct Cfg {
   static constexpr int kQBytes = kRows * D * 2;
   // operand tiles of the ring, and 8-bit tiles on their way into it: what fits next to Q
   static constexpr int kSlots = BITS == 16 ? (D == 64 ? 8 : TILES == 2 ? 4 : 5) : (D == 64 ? 6 : 4);
-  static constexpr int kRaw = BITS == 16 ? 0 : D == 64 ? 12 : TILES == 2 ? 3 : 6;  // halves of 64 tokens
+  static constexpr int kRaw = BITS == 16 ? 0 : D == 64 ? 12 : TILES == 2 ? 4 : 6;  // halves of 64 tokens
   static constexpr int kRawBytes = BITS == 16 ? 0 : kTok * D / 2;
+  static constexpr int kMeta = D == 64 ? 16 : 8;  // token tiles whose page data is kept: more than the ring runs ahead
   static constexpr int kThreads = BITS == 16 ? 384 : 512;
   static constexpr int kPartRow = D + 4;                       // floats per row of an accumulator to be joined
   static constexpr int kSmem = TILES * kQBytes + kSlots * kTileBytes + kRaw * kRawBytes;
-  static constexpr int kJoin = 2 * kRows * kPartRow * 4;       // over Q and the ring, when they are done with
+  // accumulators to be joined, their maxima and sums: over Q and the ring, when they are done with
+  static constexpr int kMax = 2 * kRows * kPartRow * 4, kSum = kMax + 2 * kRows * 4, kJoin = kSum + 2 * kRows * 4;
   static constexpr int kBytes = (kSmem > kJoin ? kSmem : kJoin) + 1024;
 };
 
+template <int META>
 struct Shared {
   uint64_t full[8], empty[8];      // operand tiles: filled (TMA or converters), products done
   uint64_t tail, q_ready;          // bf16: the last V tile, before its end is cleared; Q
   uint64_t raw_full[12], raw_empty[12];  // 8-bit pages: halves of tiles on their way
   uint64_t s_full[2], p_half[2], p_ready[2];  // per lane: scores; weights of the first 64 tokens, of all
   uint64_t done;                   // every product of both lanes
-  uint64_t meta[kMeta];
-  float scale[kMeta][3][8];        // K scale, log2 of the V scale, its reciprocal
-  uint32_t there[kMeta];
+  uint64_t meta[META];
+  float scale[META][3][8];        // K scale, log2 of the V scale, its reciprocal
+  uint32_t there[META];
   uint32_t tmem;
   int failed;
-  float m[2][kRows], l[2][kRows], fac[2][kRows];
+  int8_t q_exp[2][kRows];          // 8-bit pages: q rows are scaled by 2^-q_exp
 };
 
 // Bounded wait (two seconds, see mbar_wait_limited); once one has given up, the others follow.
-__device__ __forceinline__ bool wait(Shared& sh, uint64_t* bar, uint32_t parity) {
+template <typename S>
+__device__ __forceinline__ bool wait(S& sh, uint64_t* bar, uint32_t parity) {
   if (mbar_test(bar, parity)) return true;
   for (int i = 0; i < 64; ++i)
     if (mbar_try_wait_long(bar, parity)) return true;
@@ -176,7 +172,8 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
   using C = Cfg<D, BITS, TILES>;
   constexpr int SLOTS = C::kSlots;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(16) Shared sh;
+  constexpr int kMeta = C::kMeta;
+  __shared__ __align__(16) Shared<kMeta> sh;
 
   const PagedParams& p = a.c;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -277,7 +274,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
           for (int o = kLanes / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
           const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127 - 14, -100), 112);
           const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-          if (c == 0) sh.fac[r / kRows][r % kRows] = a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
+          if (c == 0) sh.q_exp[r / kRows][r % kRows] = (int8_t)e;
           *at = make_uint4(pack_f16(x[0] * down, x[1] * down), pack_f16(x[2] * down, x[3] * down), pack_f16(x[4] * down, x[5] * down), pack_f16(x[6] * down, x[7] * down));
         }
       }
@@ -289,7 +286,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
     const int my_row = row0 + my_tile * kRows + (tid & 127);
     const bool row_ok = my_row < rows;
     bool ok = __all_sync(0xffffffffu, wait(sh, &sh.q_ready, 0));
-    const float fac = BITS == 8 ? sh.fac[my_tile][tid & 127] : a.scale_log2;
+    const float fac = BITS == 8 ? a.scale_log2 * __uint_as_float((uint32_t)(127 + sh.q_exp[my_tile][tid & 127]) << 23) : a.scale_log2;
     {
       constexpr float kOff = BITS == 16 ? 0.f : 7.f;  // weights of 8-bit pages: up to 2^15 with kGrow, fp16 down to 2^-31
       const uint32_t lane_off = (uint32_t)(warp & 3) * 32u << 16;
@@ -310,39 +307,41 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
         tc_fence_after();
         const uint32_t there = sh.there[slot];
         const bool whole = there == 0xffu && j0 + kTok <= vf.hi && (j0 >= vl.lo || j0 + kTok <= (a.window > 0 ? a.sinks : 0));
-        // Scores stay in TMEM and pass through registers in parts, twice: for the maximum, then for the weights, which go over
+        // Scores stay in TMEM and pass through registers by halves, twice: for the maximum, then for the weights, which go over
         // columns already read.  (Code of a whole row's 128 scores does not fit the instruction cache beside the other roles'.)
+        uint32_t x[64];
         float mx = -INFINITY;
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          uint32_t x[32];
-          tc_ld32(s_addr + 32 * c, x);
-          tc_wait_ld<1>(x);
+        for (int half = 1; half >= 0; --half) {  // the first half last: it stays in registers for its weights
+          tc_ld32(s_addr + 64 * half, x);
+          tc_ld32(s_addr + 64 * half + 32, x + 32);
+          tc_wait_ld<2>(x);
           if (!whole) {
-            // bits of the columns 32 c .. 32 c + 31 that this row sees
-            const int base = j0 + 32 * c;
-            auto below = [&](int end) { return end - base >= 32 ? 0xffffffffu : end <= base ? 0u : (1u << (end - base)) - 1u; };
-            uint32_t see = (below(v.hi) & ~below(v.lo)) | below(v.sink_end);
-            if (!(there >> (2 * c) & 1u)) see &= 0xffff0000u;
-            if (!(there >> (2 * c + 1) & 1u)) see &= 0x0000ffffu;
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (!(see >> k & 1u)) x[k] = 0xff800000u;
-            tc_st32(s_addr + 32 * c, x);
-          }
-          float m2[2] = {-INFINITY, -INFINITY};
+            for (int c = 0; c < 2; ++c) {
+              // bits of 32 columns that this row sees
+              const int base = j0 + 64 * half + 32 * c;
+              auto below = [&](int end) { return end - base >= 32 ? 0xffffffffu : end <= base ? 0u : (1u << (end - base)) - 1u; };
+              uint32_t see = (below(v.hi) & ~below(v.lo)) | below(v.sink_end);
+              const uint32_t pages = there >> (4 * half + 2 * c);
+              if (!(pages & 1u)) see &= 0xffff0000u;
+              if (!(pages & 2u)) see &= 0x0000ffffu;
 #pragma unroll
-          for (int k = 0; k < 32; k += 4)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int at = BITS == 8 ? 16 * h + k / 2 : k + 2 * h;  // 8-bit pages: a maximum per 16 tokens, which share a scale
-              m2[h] = fmaxf(m2[h], fmaxf(__uint_as_float(x[at]), __uint_as_float(x[at + 1])));
+              for (int k = 0; k < 32; ++k)
+                if (!(see >> k & 1u)) x[32 * c + k] = 0xff800000u;
+              tc_st32(s_addr + 64 * half + 32 * c, x + 32 * c);
             }
+          }
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // per 16 tokens, which share a page's scales
+#pragma unroll
+          for (int k = 0; k < 16; k += 2)
+#pragma unroll
+            for (int h = 0; h < 4; ++h) m4[h] = fmaxf(m4[h], fmaxf(__uint_as_float(x[16 * h + k]), __uint_as_float(x[16 * h + k + 1])));
           if (BITS == 8) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) m2[h] = fmaf(m2[h], fmaxf(sh.scale[slot][0][2 * c + h] * fac, 1e-37f), sh.scale[slot][1][2 * c + h]);
+            for (int h = 0; h < 4; ++h) m4[h] = fmaf(m4[h], fmaxf(sh.scale[slot][0][4 * half + h] * fac, 1e-37f), sh.scale[slot][1][4 * half + h]);
           }
-          mx = fmaxf(mx, fmaxf(m2[0], m2[1]));
+          mx = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
         }
         if (BITS == 16) mx *= fac;
         if (!whole) tc_wait_st();
@@ -366,10 +365,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
         const float sub = ref == -INFINITY ? 0.f : kOff - ref;
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
-          uint32_t x[64], w[32];
-          tc_ld32(s_addr + 64 * half, x);
-          tc_ld32(s_addr + 64 * half + 32, x + 32);
-          tc_wait_ld<2>(x);
+          uint32_t w[32];
           uint64_t sum2[2] = {0, 0};
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
@@ -393,9 +389,14 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
             }
           }
           tc_st32(s_addr + 32 * half, w);
+          if (half == 0) {
+            tc_ld32(s_addr + 64, x);
+            tc_ld32(s_addr + 96, x + 32);
+          }
           tc_wait_st();
           tc_fence_before();
           mbar_arrive(half == 0 ? &sh.p_half[t] : &sh.p_ready[t]);
+          if (half == 0) tc_wait_ld<2>(x);
         }
       }
       // the lane's last product; where the accumulators go to shared memory, every product
@@ -407,8 +408,8 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
       const float inv = l == 0.f ? 0.f : 1.f / l;
       float* part = reinterpret_cast<float*>(generic) + (t * kRows + (tid & 127)) * C::kPartRow;
       if (!direct) {
-        sh.m[t][tid & 127] = ref;
-        sh.l[t][tid & 127] = l;
+        *reinterpret_cast<float*>(generic + C::kMax + (t * kRows + (tid & 127)) * 4) = ref;
+        *reinterpret_cast<float*>(generic + C::kSum + (t * kRows + (tid & 127)) * 4) = l;
       }
       float odd = l * 0.f;  // NaN if anything in the row is no finite number
 #pragma unroll 1
@@ -458,79 +459,83 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
       tc_fence_before();
     }
   } else {
-    if (warp == 8) {
-      // ---------------------------------------------------------------------- TMA
-      auto page_for = [&](int j) {
-        return lane < 8 && j < n ? page_of(p, b, (tl.at(t_begin + j) * kTok + lane * 16) >> p.page_shift) : -1;
-      };
+    if (warp == 8 || warp == 11) {
+      // ---------------------------------------------------------------------- TMA: K and page data; V
+      const int side = warp == 8 ? 0 : 1;
       constexpr int kSpan = BITS == 16 ? 128 : (D < 128 ? D : 128);  // bytes of a page row in one box
       constexpr int kBoxSpans = D * BITS / 8 / kSpan;
       constexpr int kBuf = BITS == 16 ? C::kSlots : C::kRaw;
       constexpr int kParts = BITS == 16 ? 1 : 2, kPartTok = kTok / kParts;
       const int box = min(p.page_size, kPartTok);
+      // Pages of four tiles at a time, a lane per 16 tokens, looked up two batches ahead and their scales one, so that no load waits for
+      // another.
+      auto pages_of = [&](int batch) {
+        const int j = 4 * batch + (lane >> 3);
+        return j < n ? page_of(p, b, (tl.at(t_begin + j) * kTok + (lane & 7) * 16) >> p.page_shift) : -1;
+      };
+      auto scales_of = [&](int page) {
+        float2 sc = make_float2(1.f, 1.f);
+        if (BITS == 8 && side == 0 && page >= 0) {
+          const int64_t at = (int64_t)page * p.n_kv_heads + kvh;
+          sc = make_float2(__ldg(p.side[0].scales + at), __ldg(p.side[1].scales + at));
+        }
+        return sc;
+      };
+      int page0 = pages_of(0), page1 = pages_of(1), page2 = pages_of(2);
+      float2 scale0 = scales_of(page0), scale1 = scales_of(page1);
       bool ok = true;
-      auto load = [&](int side, int j, int e, int page) {
+      for (int j = 0; j < n && ok; ++j) {
+        const int q = j & 3, e = side == 0 ? at_k(j) : at_v(j);
+        if (q == 0 && j > 0) {
+          page0 = page1;
+          page1 = page2;
+          page2 = pages_of((j >> 2) + 2);
+          scale0 = scale1;
+          scale1 = scales_of(page1);
+        }
 #pragma unroll
         for (int h = 0; h < kParts; ++h) {
           const int x = e * kParts + h, buf = x % kBuf;
           uint64_t* full = BITS == 16 ? (tail && side == 1 && j == n - 1 ? &sh.tail : &sh.full[buf]) : &sh.raw_full[buf];
           uint64_t* empty = BITS == 16 ? &sh.empty[buf] : &sh.raw_empty[buf];
+          int id[kPartTok / 16];
+#pragma unroll
+          for (int g = 0; g < kPartTok / 16; ++g) id[g] = __shfl_sync(0xffffffffu, page0, 8 * q + h * (kPartTok / 16) + g);
           if (x >= kBuf) ok = wait(sh, empty, (x / kBuf - 1) & 1);
           ok = __all_sync(0xffffffffu, ok);
-          if (!ok) return;
-          if (lane == 0) mbar_arrive_expect_tx(full, BITS == 16 ? C::kTileBytes : C::kRawBytes);
-          __syncwarp();
-          const int tok = lane * 16, in_part = tok - h * kPartTok;
-          if (in_part >= 0 && in_part < kPartTok && tok % box == 0) {
-            const uint32_t dst = (BITS == 16 ? ring + buf * C::kTileBytes : raw + buf * C::kRawBytes) + in_part * kSpan;
-            const int slot = (tl.at(t_begin + j) * kTok + tok) & (p.page_size - 1);
+          if (!ok) break;
+          if (elect_one()) {
+            const uint32_t dst = BITS == 16 ? ring + buf * C::kTileBytes : raw + buf * C::kRawBytes, bar = smem_u32(full);
+            const int slot0 = tl.at(t_begin + j) * kTok + h * kPartTok;
+            mbar_arrive_expect_tx(full, BITS == 16 ? C::kTileBytes : C::kRawBytes);
 #pragma unroll
-            for (int w = 0; w < kBoxSpans; ++w)
-              tma_box(dst + w * kTok * kSpan, &maps.side[side], w * (kSpan * 8 / BITS), slot, kvh, page, smem_u32(full));
+            for (int g = 0; g < kPartTok / 16; ++g)
+              if (g * 16 % box == 0) {
+#pragma unroll
+                for (int w = 0; w < kBoxSpans; ++w)
+                  tma_box(dst + g * 16 * kSpan + w * kTok * kSpan, &maps.side[side], w * (kSpan * 8 / BITS), (slot0 + g * 16) & (p.page_size - 1), kvh, id[g], bar);
+              }
           }
           __syncwarp();
         }
-      };
-      // pages are looked up two tiles ahead, their scales one, so that no load waits for another
-      float2 scale = make_float2(1.f, 1.f);
-      auto scale_for = [&](int page) {
-        if (BITS == 8 && page >= 0) {
-          const int64_t at = (int64_t)page * p.n_kv_heads + kvh;
-          scale = make_float2(__ldg(p.side[0].scales + at), __ldg(p.side[1].scales + at));
+        if (ok && side == 0) {  // which 16-token groups are there, and their scales
+          const int slot = j % kMeta;
+          const unsigned there = __ballot_sync(0xffffffffu, page0 >= 0) >> (8 * q) & 0xffu;
+          if (lane == 0) sh.there[slot] = there;
+          if (BITS == 8 && lane >> 3 == q) {
+            const float vs = fmaxf(scale0.y, kMinScale);
+            sh.scale[slot][0][lane & 7] = fmaxf(scale0.x, kMinScale);
+            sh.scale[slot][1][lane & 7] = __log2f(vs);
+            sh.scale[slot][2][lane & 7] = __frcp_rn(vs);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.meta[slot]);
         }
-      };
-      auto tell = [&](int j, int page, float2 sc) {
-        const int slot = j % kMeta;
-        const unsigned there = __ballot_sync(0xffffffffu, page >= 0);
-        if (lane == 0) sh.there[slot] = there;
-        if (BITS == 8 && lane < 8) {
-          const float vs = fmaxf(sc.y, kMinScale);
-          sh.scale[slot][0][lane] = fmaxf(sc.x, kMinScale);
-          sh.scale[slot][1][lane] = __log2f(vs);
-          sh.scale[slot][2][lane] = __frcp_rn(vs);
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.meta[slot]);
-      };
-      int page_v = page_for(0), page_k = page_for(1), page_next = page_for(2);
-      if (n > 0) load(0, 0, 0, page_v);
-      scale_for(page_v);
-      if (n > 0) tell(0, page_v, scale);
-      scale_for(page_k);
-      for (int j = 0; j < n && ok; ++j) {
-        const float2 sc = scale;
-        const int page_far = page_for(j + 3);
-        if (j + 1 < n) load(0, j + 1, at_k(j + 1), page_k);
-        scale_for(page_next);
-        if (ok) load(1, j, at_v(j), page_v);
-        if (ok && j + 1 < n) tell(j + 1, page_k, sc);
-        page_v = page_k;
-        page_k = page_next;
-        page_next = page_far;
       }
-      if (!ok)  // copies in flight land before the block leaves
+      if (!ok) {  // copies in flight land before the block leaves
         for (int i = 0; i < kBuf; ++i)
           for (int ph = 0; ph < 2; ++ph) mbar_wait_limited(BITS == 16 ? &sh.full[i] : &sh.raw_full[i], ph);
+      }
     } else if (warp == 9) {
       // ---------------------------------------------------------------------- MMA issue
       constexpr uint32_t kShapeS = mma_shape(BITS == 16, kTok, false), kShapeO = mma_shape(BITS == 16, D, true);
@@ -647,10 +652,13 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
             }
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
-              *reinterpret_cast<uint4*>(dst + to[i]) =
-                  make_uint4(e4m3_to_f16x2(w[i].x & 0xffffu), e4m3_to_f16x2(w[i].x >> 16), e4m3_to_f16x2(w[i].y & 0xffffu), e4m3_to_f16x2(w[i].y >> 16));
-              *reinterpret_cast<uint4*>(dst + (to[i] ^ 16)) =
-                  make_uint4(e4m3_to_f16x2(w[i].z & 0xffffu), e4m3_to_f16x2(w[i].z >> 16), e4m3_to_f16x2(w[i].w & 0xffffu), e4m3_to_f16x2(w[i].w >> 16));
+              uint4 lo, hi;
+              e4m3_to_f16x4(w[i].x, &lo.x, &lo.y);
+              e4m3_to_f16x4(w[i].y, &lo.z, &lo.w);
+              e4m3_to_f16x4(w[i].z, &hi.x, &hi.y);
+              e4m3_to_f16x4(w[i].w, &hi.z, &hi.w);
+              *reinterpret_cast<uint4*>(dst + to[i]) = lo;
+              *reinterpret_cast<uint4*>(dst + (to[i] ^ 16)) = hi;
             }
             fence_proxy_async_smem();
             mbar_arrive(&sh.full[slot]);
@@ -673,12 +681,12 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
       float mx = -INFINITY, sum = 0.f, o[D / 32];
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
-      for (int c = 0; c < splits * kSets; ++c) mx = fmaxf(mx, ld_cluster_f32(smem_u32(&sh.m[0][0] + c % kSets * kRows + r), c / kSets));
+      for (int c = 0; c < splits * kSets; ++c) mx = fmaxf(mx, ld_cluster_f32(smem + C::kMax + (c % kSets * kRows + r) * 4, c / kSets));
       for (int c = 0; c < splits * kSets; ++c) {
         const int at = c % kSets * kRows + r, from = c / kSets;
-        const float mc = ld_cluster_f32(smem_u32(&sh.m[0][0] + at), from);
+        const float mc = ld_cluster_f32(smem + C::kMax + at * 4, from);
         const float f = mc == mx ? 1.f : exp2_fast(mc - mx);
-        sum = fmaf(ld_cluster_f32(smem_u32(&sh.l[0][0] + at), from), f, sum);
+        sum = fmaf(ld_cluster_f32(smem + C::kSum + at * 4, from), f, sum);
 #pragma unroll
         for (int i = 0; i < D / 32; ++i)
           o[i] = fmaf(ld_cluster_f32(smem + (at * C::kPartRow + lane * (D / 32) + i) * 4, from), f, o[i]);
