@@ -330,24 +330,17 @@ _ROPE_FIELDS = {n for n, _ in clo_rope_config._fields_}
 # The calls below run once per layer and step, so their checks are straight-line: what is right costs a few attribute
 # reads, what is wrong is named by the slower functions.  torch is imported with the first of them.
 torch = None
-_BF16 = None
+_BF16 = _INT32 = _INT64 = None
+_byref = ctypes.byref
 
 
 def _load_torch() -> None:
-    global torch, _BF16
+    global torch, _BF16, _INT32, _INT64
     import torch as module
 
     module.cuda.current_device()  # raises where there is no GPU
-    torch, _BF16 = module, module.bfloat16
-
-
-def _tensor_fault(t, name: str, dev: int) -> None:
-    import torch as module
-
-    if not isinstance(t, module.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on {t.device}, not on the current device")
+    load_library()
+    torch, _BF16, _INT32, _INT64 = module, module.bfloat16, module.int32, module.int64
 
 
 def _device_of(t, name: str) -> int:
@@ -360,22 +353,39 @@ def _device_of(t, name: str) -> int:
         _load_torch()
     dev = torch._C._cuda_getDevice()
     if not isinstance(t, torch.Tensor) or t.get_device() != dev:
-        _tensor_fault(t, name, dev)
+        _tensor_fault(t, name, dev, None)
     return dev
 
 
-def _rows(t, name: str, dev: int, shape=None) -> clo_rows:
+def _tensor_fault(t, name: str, dev: int, dtype) -> None:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on the current device")
+    if dtype is not None and t.dtype is not dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}; expected {dtype}")
+
+
+def _rows(t, name: str, dev: int, shape) -> clo_rows:
     """A bf16 [n_tokens][n_heads][head_dim] tensor (any strides but the last) as the library takes it."""
-    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
-        _tensor_fault(t, name, dev)
-    if t.dtype is not _BF16:
-        raise ValueError(f"{name} has dtype {t.dtype}; expected torch.bfloat16")
-    if t.dim() != 3 or (shape is not None and t.shape != shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}; expected {tuple(shape) if shape else '[n_tokens][n_heads][head_dim]'}")
+    if not isinstance(t, torch.Tensor) or t.dtype is not _BF16 or t.get_device() != dev:
+        _tensor_fault(t, name, dev, _BF16)
+    if t.shape != shape or len(shape) != 3:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}; expected {tuple(shape) if len(shape) == 3 else '[n_tokens][n_heads][head_dim]'}")
     st, sh, sd = t.stride()
-    if sd != 1 and t.shape[2] > 1:
+    if sd != 1 and shape[2] > 1:
         raise ValueError(f"{name} must be contiguous along head_dim")
     return clo_rows(t.data_ptr(), st, sh)
+
+
+def _new_rows(like):
+    """New rows of the shape of `like`, and as the library takes them."""
+    t = torch.empty_like(like)
+    st, sh, sd = t.stride()
+    if sd != 1:  # the layout of a transposed view
+        t = torch.empty(like.shape, dtype=_BF16, device=like.device)
+        st, sh, _ = t.stride()
+    return t, clo_rows(t.data_ptr(), st, sh)
 
 
 def _refuse_folded(t, name: str) -> None:
@@ -385,11 +395,9 @@ def _refuse_folded(t, name: str) -> None:
 
 
 def _index(t, name: str, dev: int, dtype, numel: int):
-    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
-        _tensor_fault(t, name, dev)
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} has dtype {t.dtype}; expected {dtype}")
-    if t.dim() != 1 or t.shape[0] != numel or (numel > 1 and t.stride(0) != 1):
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev:
+        _tensor_fault(t, name, dev, dtype)
+    if t.numel() != numel or not t.is_contiguous():
         raise ValueError(f"{name} has shape {tuple(t.shape)}; expected a contiguous vector of {numel}")
     return t.data_ptr()
 
@@ -407,21 +415,22 @@ def clo_rope(plan: clo_rope_plan, x, positions, out=None, transpose: bool = Fals
     out: rows of the same shape, x itself for in place, or None for new ones.  transpose applies the
     transposed rotation, which takes the gradient of the output to that of x.  Returns out."""
     dev = _device_of(x, "x")
-    xr = _rows(x, "x", dev)
+    shape = x.shape
+    xr = _rows(x, "x", dev, shape)
+    n, h, d = shape
     if out is None:
-        out = torch.empty_like(x)
+        out, yr = _new_rows(x)
     else:
         _refuse_folded(out, "out")
-    n, h, d = shape = x.shape
-    status = (_lib or load_library()).clo_rope(
-        ctypes.byref(plan), ctypes.byref(xr), ctypes.byref(_rows(out, "out", dev, shape)),
-        _index(positions, "positions", dev, torch.int64, n), n, h, d, 1 if transpose else 0, _stream_of(stream, dev))
+        yr = _rows(out, "out", dev, shape)
+    status = _lib.clo_rope(_byref(plan), _byref(xr), _byref(yr), _index(positions, "positions", dev, _INT64, n), n, h, d,
+                           1 if transpose else 0, _stream_of(stream, dev))
     if status:
         _check(status, "clo_rope")
     return out
 
 
-_WORKSPACE_TOKENS = 4096  # no shorter sequence makes clo_paged_attention ask for a workspace
+_WORKSPACE_TOKENS = 4096  # no shorter table makes clo_paged_attention ask for a workspace
 
 
 class PagedCache:
@@ -480,17 +489,15 @@ class PagedCache:
     def _batch(self, dev, q_starts, kv_lens, block_table, total: int, max_q) -> clo_paged_batch:
         if dev != self.device:
             raise ValueError(f"the cache is on device {self.device}, the call's rows on {dev}")
-        if not isinstance(kv_lens, torch.Tensor) or not isinstance(block_table, torch.Tensor):
-            raise ValueError("kv_lens and block_table must be CUDA tensors")
-        int32 = torch.int32
-        batch = kv_lens.numel()
-        if block_table.get_device() != dev or block_table.dtype is not int32 or block_table.dim() != 2:
-            raise ValueError(f"block_table must be an int32 CUDA tensor [{batch}][max_pages] on the current device")
-        rows, width = block_table.shape
+        if not isinstance(block_table, torch.Tensor) or block_table.dtype is not _INT32 or block_table.get_device() != dev:
+            _tensor_fault(block_table, "block_table", dev, _INT32)
+        if block_table.dim() != 2:
+            raise ValueError(f"block_table has shape {tuple(block_table.shape)}; expected [batch][max_pages]")
+        batch, width = block_table.shape
         stride, inner = block_table.stride()
-        if rows != batch or (inner != 1 and width > 1):
-            raise ValueError(f"block_table must have {batch} contiguous rows")
-        return clo_paged_batch(_index(q_starts, "q_starts", dev, int32, batch + 1), _index(kv_lens, "kv_lens", dev, int32, batch),
+        if inner != 1 and width > 1:
+            raise ValueError("block_table must have contiguous rows")
+        return clo_paged_batch(_index(q_starts, "q_starts", dev, _INT32, batch + 1), _index(kv_lens, "kv_lens", dev, _INT32, batch),
                                block_table.data_ptr(), stride, width, batch, total, total if max_q is None else max_q)
 
     def append(self, k, v, q_starts, kv_lens, block_table, rope: clo_rope_plan | None = None, positions=None, q=None,
@@ -498,7 +505,6 @@ class PagedCache:
         """clo_paged_append: k, v bf16 [total][n_kv_heads][head_dim] into the pages, k rotated by rope; with
         q, returns the rotated queries (q_out, or new rows)."""
         dev = _device_of(k, "k")
-        byref = ctypes.byref
         total = k.shape[0]
         shape = (total, self.n_kv_heads, self.head_dim)
         kr = _rows(k, "k", dev, shape)
@@ -507,21 +513,22 @@ class PagedCache:
         qr = yr = None
         heads = 0
         if q is not None:
-            qr = _rows(q, "q", dev)
             shape = q.shape
+            qr = _byref(_rows(q, "q", dev, shape))
             heads = shape[1]
             if shape[0] != total or shape[2] != self.head_dim:
                 raise ValueError(f"q has shape {tuple(shape)}; expected [{total}][n_q_heads][{self.head_dim}]")
             if q_out is None:
-                q_out = torch.empty_like(q)
+                q_out, yr = _new_rows(q)
             else:
                 _refuse_folded(q_out, "q_out")
-            qr, yr = byref(qr), byref(_rows(q_out, "q_out", dev, shape))
+                yr = _rows(q_out, "q_out", dev, shape)
+            yr = _byref(yr)
         elif q_out is not None:
             raise ValueError("q_out without q")
         status = _lib.clo_paged_append(
-            self._ref, byref(b), None if rope is None else byref(rope),
-            None if positions is None else _index(positions, "positions", dev, torch.int64, total), byref(kr), byref(vr),
+            self._ref, _byref(b), None if rope is None else _byref(rope),
+            None if positions is None else _index(positions, "positions", dev, _INT64, total), _byref(kr), _byref(vr),
             qr, yr, heads, _stream_of(stream, dev))
         if status:
             _check(status, "clo_paged_append")
@@ -533,15 +540,17 @@ class PagedCache:
         shape = (total, self.n_kv_heads, self.head_dim)
         if k_out is None:
             k_out = torch.empty(shape, dtype=_BF16, device=kv_lens.device)
+            kr = clo_rows(k_out.data_ptr(), shape[1] * shape[2], shape[2])
         else:
             _refuse_folded(k_out, "k_out")
+            kr = _rows(k_out, "k_out", dev, shape)
         if v_out is None:
-            v_out = torch.empty(shape, dtype=_BF16, device=kv_lens.device)
+            v_out, vr = _new_rows(k_out)
         else:
             _refuse_folded(v_out, "v_out")
+            vr = _rows(v_out, "v_out", dev, shape)
         b = self._batch(dev, q_starts, kv_lens, block_table, total, max_q)
-        status = _lib.clo_paged_read(self._ref, ctypes.byref(b), ctypes.byref(_rows(k_out, "k_out", dev, shape)),
-                                     ctypes.byref(_rows(v_out, "v_out", dev, shape)), _stream_of(stream, dev))
+        status = _lib.clo_paged_read(self._ref, _byref(b), _byref(kr), _byref(vr), _stream_of(stream, dev))
         if status:
             _check(status, "clo_paged_read")
         return k_out, v_out
@@ -564,14 +573,16 @@ class PagedCache:
 
         workspace: uint8 tensor of attention_workspace() bytes, or None: allocated where the sizes ask for one."""
         dev = _device_of(q, "q")
-        qr = _rows(q, "q", dev)
-        total, heads, d = shape = q.shape
+        shape = q.shape
+        qr = _rows(q, "q", dev, shape)
+        total, heads, d = shape
         if d != self.head_dim:
             raise ValueError(f"q has head_dim {d}; the cache has {self.head_dim}")
         if out is None:
-            out = torch.empty_like(q)
+            out, orow = _new_rows(q)
         else:
             _refuse_folded(out, "out")
+            orow = _rows(out, "out", dev, shape)
         b = self._batch(dev, q_starts, kv_lens, block_table, total, max_q)
         work, size = None, 0
         if workspace is None and b.max_pages * self.page_size >= _WORKSPACE_TOKENS:
@@ -584,8 +595,8 @@ class PagedCache:
         if workspace is not None:
             size = workspace.numel()
             work = _index(workspace, "workspace", dev, torch.uint8, size)
-        status = _lib.clo_paged_attention(self._ref, ctypes.byref(b), ctypes.byref(qr), ctypes.byref(_rows(out, "out", dev, shape)),
-                                          heads, softmax_scale, window, sinks, work, size, _stream_of(stream, dev))
+        status = _lib.clo_paged_attention(self._ref, _byref(b), _byref(qr), _byref(orow), heads, softmax_scale, window, sinks, work,
+                                          size, _stream_of(stream, dev))
         if status:
             _check(status, "clo_paged_attention")
         return out
