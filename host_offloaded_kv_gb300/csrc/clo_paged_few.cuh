@@ -583,7 +583,8 @@ FewPlan plan_few(const AttendParams& a) {
   const int64_t want = std::min(most, fill);
   if (want > 16 && tokens >= 4096) return {(int)want, want * units * a.part_rows * (D + 4) * 4};
   int splits = 1;
-  while (splits < 16 && splits * units < 2 * kSms && 2 * splits <= most) splits *= 2;
+  // (twice the blocks, at 8 sequences of 32K: 167 us for 161 in bf16, 117 for 98 in e4m3; at 4 of 2000: 25 for 12)
+  while (splits < 16 && splits * units < kSms && 2 * splits <= most) splits *= 2;
   return {splits, 0};
 }
 

@@ -8,6 +8,7 @@
 // its unit while its warp walks over rows.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -33,7 +34,7 @@ clo_status paged_fail(clo_status st, const char* fmt, ...) {
 
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
 struct Rope {
@@ -50,8 +51,14 @@ struct Unit {
   float magnitude;
 };
 
+// The plan's turns in shared memory: lanes read their units' with wide loads, where the parameter space would serve one address at a time.
+__device__ __forceinline__ void stage_turns(const Rope& r, uint64_t* s_turn) {
+  if (threadIdx.x < CLO_ROPE_MAX_PAIRS) s_turn[threadIdx.x] = r.plan.turn[threadIdx.x];
+  __syncthreads();
+}
+
 template <int D>
-__device__ __forceinline__ Unit<D> unit_of_lane(const Rope& r, int u) {
+__device__ __forceinline__ Unit<D> unit_of_lane(const Rope& r, const uint64_t* s_turn, int u) {
   Unit<D> x;
   const int rot = r.plan.rot_dim;
   x.rotate = u * 16 < rot;
@@ -66,7 +73,11 @@ __device__ __forceinline__ Unit<D> unit_of_lane(const Rope& r, int u) {
   }
   if (x.rotate) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x.turn[i] = r.plan.turn[u * 8 + i];
+    for (int i = 0; i < 8; i += 2) {
+      const ulonglong2 t = *reinterpret_cast<const ulonglong2*>(s_turn + u * 8 + i);
+      x.turn[i] = t.x;
+      x.turn[i + 1] = t.y;
+    }
   }
   return x;
 }
@@ -112,20 +123,18 @@ struct Rows {
 };
 
 // ---------------------------------------------------------------------------- rows of one token
-// A warp takes one token and up to kRowIters rounds of its heads: the cosines and sines of a lane's
-// unit are computed once for all of them.
-constexpr int kRowIters = 4;
-
-template <int D>
-__device__ __forceinline__ void rotate_heads(const Rope& r, const Rows& x, const Rows& y, int64_t token, int64_t pos,
+// A warp takes one token and up to ITERS rounds of its heads: the cosines and sines of a lane's unit are computed
+// once for all of them.
+template <int D, int ITERS>
+__device__ __forceinline__ void rotate_heads(const Rope& r, const uint64_t* s_turn, const Rows& x, const Rows& y, int64_t token, int64_t pos,
                                              int head0, int n_heads, int lane) {
   constexpr int kLanes = D / 16, kRows = 32 / kLanes;
-  const Unit<D> u = unit_of_lane<D>(r, lane % kLanes);
+  const Unit<D> u = unit_of_lane<D>(r, s_turn, lane % kLanes);
   const uint16_t* src = x.p + token * x.token;
   uint16_t* dst = y.p + token * y.token;
-  uint4 va[kRowIters], vb[kRowIters];
+  uint4 va[ITERS], vb[ITERS];
 #pragma unroll
-  for (int i = 0; i < kRowIters; ++i) {
+  for (int i = 0; i < ITERS; ++i) {
     const int h = head0 + i * kRows + lane / kLanes;
     if (h < n_heads) {
       va[i] = *reinterpret_cast<const uint4*>(src + (int64_t)h * x.head + u.a);
@@ -135,7 +144,7 @@ __device__ __forceinline__ void rotate_heads(const Rope& r, const Rows& x, const
   CosSin c;
   if (u.rotate) c = cos_sin_of<D>(u, pos, r.transpose);
 #pragma unroll
-  for (int i = 0; i < kRowIters; ++i) {
+  for (int i = 0; i < ITERS; ++i) {
     const int h = head0 + i * kRows + lane / kLanes;
     if (h < n_heads) {
       if (u.rotate) {
@@ -152,14 +161,21 @@ __device__ __forceinline__ void rotate_heads(const Rope& r, const Rows& x, const
   }
 }
 
+// Rounds of heads per warp: many for long calls, where the sines count, few for short ones, where the latency does.
+constexpr int kLongIters = 8, kShortIters = 2;
+constexpr int64_t kLongTokens = 8 * 152;  // a warp per SM and slot of eight
 template <int D>
+__host__ __device__ constexpr int heads_per_warp(int iters) { return iters * 32 / (D / 16); }
+
+template <int D, int ITERS>
 __global__ void __launch_bounds__(kThreads) k_rope(const Rope r, const Rows x, const Rows y, const int64_t* __restrict__ positions,
                                                    int64_t n_tokens, int n_heads, int chunks) {
-  constexpr int kHeads = kRowIters * 32 / (D / 16);
+  __shared__ __align__(16) uint64_t s_turn[CLO_ROPE_MAX_PAIRS];
+  stage_turns(r, s_turn);
   const int64_t job = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
   const int64_t t = job / chunks;
   if (t >= n_tokens) return;
-  rotate_heads<D>(r, x, y, t, positions[t], (int)(job % chunks) * kHeads, n_heads, threadIdx.x & 31);
+  rotate_heads<D, ITERS>(r, s_turn, x, y, t, positions[t], (int)(job % chunks) * heads_per_warp<D>(ITERS), n_heads, threadIdx.x & 31);
 }
 
 // Any strides, alignment, rot_dim and head_dim: one pair, or one copied element, per thread and step.
@@ -233,10 +249,14 @@ __device__ __forceinline__ bool item_of(const PagedParams& p, int item, int lane
   return false;
 }
 
-// Rows of one job: (touched page, kv head, K or V).  kPer warps share a job; kPer > 1: the block is the job.
+// One job: (touched page, kv head, K or V), by kPer warps.  A lane holds kUnits units (16 elements of a row each) in registers from
+// the load to the store, so that rows are read and rotated once also where the page's scale comes in between; kPer warps
+// hold the most rows that a page can get from the call.
+constexpr int kUnits = 4;
+
 template <int D, int BITS, int kPer>
-__device__ __forceinline__ void write_page(const AppendParams& a, int item, int head, int side, int part, int lane,
-                                           float* s_red) {
+__device__ __forceinline__ void write_page(const AppendParams& a, const uint64_t* s_turn, int item, int head, int side, int part, int lane, float* s_red,
+                                           int group) {
   const PagedParams& p = a.c;
   int b, logical;
   SeqRows s;
@@ -248,55 +268,56 @@ __device__ __forceinline__ void write_page(const AppendParams& a, int item, int 
   const int lo = max(max(s.pos0, 0), base), hi = min(s.pos0 + s.n, base + p.page_size);
   const PagedSide& sd = p.side[side];
   const Rows& in = a.in[side];
-  Unit<D> u = unit_of_lane<D>(a.rope, lane % kLanes);
+  Unit<D> u = unit_of_lane<D>(a.rope, s_turn, lane % kLanes);
   const bool rotate = side == 0 && u.rotate;
   if (side == 1) {
     u.a = (lane % kLanes) * 16;
     u.b = u.a + 8;
   }
   char* dst0 = sd.pages + ((int64_t)page * sd.stride_page + (int64_t)head * sd.stride_head) * (BITS / 8);
-  const int r0 = part * kRows + lane / kLanes;
+  const int first = lo + part * kRows + lane / kLanes;  // this lane's rows: first, + kPer * kRows, ...
 
-  auto load = [&](int pos, float* f) {
-    const int64_t t = s.first + (pos - s.pos0);
-    const uint16_t* src = in.p + t * in.token + (int64_t)head * in.head;
-    unpack8(__ldg(reinterpret_cast<const uint4*>(src + u.a)), f);
-    unpack8(__ldg(reinterpret_cast<const uint4*>(src + u.b)), f + 8);
-    if (rotate) {
-      const int64_t at = a.positions ? __ldg(a.positions + t) : pos;
-      rotate_unit<D>(u, cos_sin_of<D>(u, at, 0), f);
-    }
-  };
-
-  if (BITS == 16) {
-#pragma unroll 2
-    for (int pos = lo + r0; pos < hi; pos += kPer * kRows) {
-      float f[16];
-      load(pos, f);
-      char* dst = dst0 + (int64_t)(pos - base) * sd.stride_token * 2;
-      *reinterpret_cast<uint4*>(dst + u.a * 2) = pack8(f);
-      *reinterpret_cast<uint4*>(dst + u.b * 2) = pack8(f + 8);
-    }
-    return;
-  }
-  // 8 bits: the largest finite magnitude first, then the codes (the rows come from L1 the second time)
-  float amax = 0.f;
-#pragma unroll 2
-  for (int pos = lo + r0; pos < hi; pos += kPer * kRows) {
-    float f[16];
-    load(pos, f);
+  uint4 va[kUnits], vb[kUnits];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float m = fabsf(f[i]);
-      amax = fmaxf(amax, m < INFINITY ? m : 0.f);
+  for (int i = 0; i < kUnits; ++i) {
+    const int pos = first + i * kPer * kRows;
+    if (pos < hi) {
+      const uint16_t* src = in.p + (int64_t)(s.first + (pos - s.pos0)) * in.token + (int64_t)head * in.head;
+      va[i] = __ldg(reinterpret_cast<const uint4*>(src + u.a));
+      vb[i] = __ldg(reinterpret_cast<const uint4*>(src + u.b));
     }
   }
+  float f[kUnits][16], amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    const int pos = first + i * kPer * kRows;
+    if (pos < hi) {
+      unpack8(va[i], f[i]);
+      unpack8(vb[i], f[i] + 8);
+      if (rotate) {
+        const int64_t at = a.positions ? __ldg(a.positions + s.first + (pos - s.pos0)) : pos;
+        rotate_unit<D>(u, cos_sin_of<D>(u, at, 0), f[i]);
+      }
+      if (BITS == 16) {
+        char* dst = dst0 + (int64_t)(pos - base) * sd.stride_token * 2;
+        *reinterpret_cast<uint4*>(dst + u.a * 2) = pack8(f[i]);
+        *reinterpret_cast<uint4*>(dst + u.b * 2) = pack8(f[i] + 8);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const float m = fabsf(f[i][k]);
+          amax = fmaxf(amax, m < INFINITY ? m : 0.f);
+        }
+      }
+    }
+  }
+  if (BITS == 16) return;
   amax = warp_max(amax);
   if (kPer > 1) {
-    if (lane == 0) s_red[part] = amax;
-    __syncthreads();
+    if (lane == 0) s_red[group * kPer + part] = amax;
+    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(kPer * 32) : "memory");
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) amax = fmaxf(amax, s_red[i]);
+    for (int i = 0; i < kPer; ++i) amax = fmaxf(amax, s_red[group * kPer + i]);
   }
   // smallest e with amax <= 1.75 * 2^(8 + e), from the bits of amax
   const int bits = __float_as_int(amax);
@@ -325,34 +346,38 @@ __device__ __forceinline__ void write_page(const AppendParams& a, int item, int 
     }
   }
   const float inv = 1.f / scale;
-#pragma unroll 2
-  for (int pos = lo + r0; pos < hi; pos += kPer * kRows) {
-    float f[16];
-    load(pos, f);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) f[i] *= inv;
-    char* dst = dst0 + (int64_t)(pos - base) * sd.stride_token;
-    *reinterpret_cast<uint2*>(dst + u.a) = pack8_e4m3(f);
-    *reinterpret_cast<uint2*>(dst + u.b) = pack8_e4m3(f + 8);
+  for (int i = 0; i < kUnits; ++i) {
+    const int pos = first + i * kPer * kRows;
+    if (pos < hi) {
+#pragma unroll
+      for (int k = 0; k < 16; ++k) f[i][k] *= inv;
+      char* dst = dst0 + (int64_t)(pos - base) * sd.stride_token;
+      *reinterpret_cast<uint2*>(dst + u.a) = pack8_e4m3(f[i]);
+      *reinterpret_cast<uint2*>(dst + u.b) = pack8_e4m3(f[i] + 8);
+    }
   }
-  if (kPer > 1) __syncthreads();  // every warp has read the old scale
+  // every warp has read the old scale
+  if (kPer > 1) asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(kPer * 32) : "memory");
   __syncwarp();
   if (part == 0 && lane == 0) *sp = scale;
 }
 
 template <int D, int BITS, int kPer>
 __global__ void __launch_bounds__(kThreads) k_paged_append(const AppendParams a) {
+  __shared__ __align__(16) uint64_t s_turn[CLO_ROPE_MAX_PAIRS];
   __shared__ float s_red[kWarps];
+  stage_turns(a.rope, s_turn);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if ((int)blockIdx.x < a.kv_blocks) {
     const int64_t job = (int64_t)blockIdx.x * (kWarps / kPer) + warp / kPer;
     const int heads = a.c.n_kv_heads;
     const int64_t item = job / (2 * heads);
     if (item >= a.items) return;
-    write_page<D, BITS, kPer>(a, (int)item, (int)(job % heads), (int)(job / heads & 1), warp % kPer, lane, s_red);
+    write_page<D, BITS, kPer>(a, s_turn, (int)item, (int)(job % heads), (int)(job / heads & 1), warp % kPer, lane, s_red, warp / kPer);
     return;
   }
-  constexpr int kHeads = kRowIters * 32 / (D / 16);
+  constexpr int kIters = kPer == 1 ? kShortIters : kLongIters;
   const int64_t job = (int64_t)((int)blockIdx.x - a.kv_blocks) * kWarps + warp;
   const int64_t t = job / a.q_chunks;
   if (t >= a.c.total_q) return;
@@ -360,7 +385,7 @@ __global__ void __launch_bounds__(kThreads) k_paged_append(const AppendParams a)
   if (b >= a.c.batch) return;
   const SeqRows s = seq_rows(a.c, b);
   const int64_t pos = a.positions ? __ldg(a.positions + t) : (int64_t)s.pos0 + (t - s.first);
-  rotate_heads<D>(a.rope, a.q, a.q_out, t, pos, (int)(job % a.q_chunks) * kHeads, a.n_q_heads, lane);
+  rotate_heads<D, kIters>(a.rope, s_turn, a.q, a.q_out, t, pos, (int)(job % a.q_chunks) * heads_per_warp<D>(kIters), a.n_q_heads, lane);
 }
 
 // ---------------------------------------------------------------------------- read-back
@@ -553,14 +578,14 @@ extern "C" CLO_API clo_status clo_rope(const clo_rope_plan* plan, const clo_rows
   Rope r{*plan, transpose != 0};
   const bool vec = !rows_fault(x, true) && !rows_fault(y, true) && plan->rot_dim % 16 == 0 && (head_dim == 64 || head_dim == 128);
   if (vec) {
-    const int per = kRowIters * 32 / (head_dim / 16);  // heads per warp
+    const int iters = n_tokens >= kLongTokens ? kLongIters : kShortIters;
+    const int per = iters * 32 / (head_dim / 16);  // heads per warp
     const int chunks = (n_heads + per - 1) / per;
     const int64_t blocks = (n_tokens * chunks + kWarps - 1) / kWarps;
     if (blocks > 0x7fffffff) return paged_fail(CLO_ERR_INVALID, "%s: too many rows for one call", who);
-    if (head_dim == 128)
-      k_rope<128><<<(unsigned)blocks, kThreads, 0, st>>>(r, rows_of(x), rows_of(y), positions, n_tokens, n_heads, chunks);
-    else
-      k_rope<64><<<(unsigned)blocks, kThreads, 0, st>>>(r, rows_of(x), rows_of(y), positions, n_tokens, n_heads, chunks);
+    auto* f = head_dim == 128 ? (iters == kLongIters ? k_rope<128, kLongIters> : k_rope<128, kShortIters>)
+                              : (iters == kLongIters ? k_rope<64, kLongIters> : k_rope<64, kShortIters>);
+    f<<<(unsigned)blocks, kThreads, 0, st>>>(r, rows_of(x), rows_of(y), positions, n_tokens, n_heads, chunks);
   } else {
     const int64_t pairs = n_tokens * n_heads * (head_dim - plan->rot_dim / 2);
     const int64_t blocks = (pairs + kThreads - 1) / kThreads;
@@ -572,11 +597,9 @@ extern "C" CLO_API clo_status clo_rope(const clo_rope_plan* plan, const clo_rows
 }
 
 template <int D, int BITS>
-static void launch_append(const AppendParams& a, int64_t blocks, bool wide, cudaStream_t st) {
-  if (wide)
-    k_paged_append<D, BITS, kWarps><<<(unsigned)blocks, kThreads, 0, st>>>(a);
-  else
-    k_paged_append<D, BITS, 1><<<(unsigned)blocks, kThreads, 0, st>>>(a);
+static void launch_append(const AppendParams& a, int64_t blocks, int per, cudaStream_t st) {
+  auto* f = per == 1 ? k_paged_append<D, BITS, 1> : per == 2 ? k_paged_append<D, BITS, 2> : per == 4 ? k_paged_append<D, BITS, 4> : k_paged_append<D, BITS, 8>;
+  f<<<(unsigned)blocks, kThreads, 0, st>>>(a);
 }
 
 extern "C" CLO_API clo_status clo_paged_append(const clo_paged_cache* cache, const clo_paged_batch* batch, const clo_rope_plan* plan,
@@ -610,18 +633,18 @@ extern "C" CLO_API clo_status clo_paged_append(const clo_paged_cache* cache, con
   int64_t items = t / a.c.page_size + 2 * (int64_t)a.c.batch;
   if (items > t) items = t;
   a.items = (int32_t)items;
-  // Single-token steps: a warp per job.  Longer appends: a block per job, so that a page's rows move in fewer
-  // dependent rounds.
-  const bool wide = a.c.max_q >= 16;
+  // Warps per job: as many as hold the most rows that a page can get (a single token: one).
+  const int rows = std::min(a.c.page_size, a.c.max_q), units = rows * (cache->head_dim / 16);
+  const int per = units <= 32 * kUnits ? 1 : units <= 64 * kUnits ? 2 : units <= 128 * kUnits ? 4 : 8;
   const int64_t jobs = items * 2 * a.c.n_kv_heads;
-  const int64_t kv_blocks = wide ? jobs : (jobs + kWarps - 1) / kWarps;
+  const int64_t kv_blocks = (jobs * per + kWarps - 1) / kWarps;
   int64_t q_blocks = 0;
   if (q) {
-    const int per = kRowIters * 32 / (cache->head_dim / 16);
+    const int heads = (per == 1 ? kShortIters : kLongIters) * 32 / (cache->head_dim / 16);  // per warp
     a.q = rows_of(q);
     a.q_out = rows_of(q_out);
     a.n_q_heads = n_q_heads;
-    a.q_chunks = (n_q_heads + per - 1) / per;
+    a.q_chunks = (n_q_heads + heads - 1) / heads;
     q_blocks = (t * a.q_chunks + kWarps - 1) / kWarps;
   }
   if (kv_blocks + q_blocks > 0x7fffffff) return paged_fail(CLO_ERR_INVALID, "%s: too many rows for one call", who);
@@ -629,11 +652,11 @@ extern "C" CLO_API clo_status clo_paged_append(const clo_paged_cache* cache, con
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int64_t blocks = kv_blocks + q_blocks;
   if (cache->head_dim == 128) {
-    if (cache->kv_bits == 16) launch_append<128, 16>(a, blocks, wide, st);
-    else launch_append<128, 8>(a, blocks, wide, st);
+    if (cache->kv_bits == 16) launch_append<128, 16>(a, blocks, per, st);
+    else launch_append<128, 8>(a, blocks, per, st);
   } else {
-    if (cache->kv_bits == 16) launch_append<64, 16>(a, blocks, wide, st);
-    else launch_append<64, 8>(a, blocks, wide, st);
+    if (cache->kv_bits == 16) launch_append<64, 16>(a, blocks, per, st);
+    else launch_append<64, 8>(a, blocks, per, st);
   }
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return paged_fail(CLO_ERR_CUDA, "%s: launch: %s", who, cudaGetErrorString(e));
