@@ -430,7 +430,7 @@ def clo_rope(plan: clo_rope_plan, x, positions, out=None, transpose: bool = Fals
     return out
 
 
-_WORKSPACE_TOKENS = 4096  # no shorter table makes clo_paged_attention ask for a workspace
+_WORKSPACE_TOKENS = 2048  # a workspace for shorter tables would gain nothing that it costs
 
 
 class PagedCache:
@@ -585,7 +585,7 @@ class PagedCache:
             orow = _rows(out, "out", dev, shape)
         b = self._batch(dev, q_starts, kv_lens, block_table, total, max_q)
         work, size = None, 0
-        if workspace is None and b.max_pages * self.page_size >= _WORKSPACE_TOKENS:
+        if workspace is None and (total >= 512 or b.max_pages * self.page_size >= _WORKSPACE_TOKENS):
             size = self._workspace(b, heads, window, sinks)
             if size:
                 workspace = torch.empty(size, dtype=torch.uint8, device=q.device)

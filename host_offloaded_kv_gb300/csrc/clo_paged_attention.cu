@@ -98,8 +98,11 @@ extern "C" CLO_API clo_status clo_paged_attention_workspace(const clo_paged_cach
   if (!bytes) return paged_fail(CLO_ERR_INVALID, "%s: null pointer", who);
   *bytes = 0;
   if (const char* f = attend_params(cache, batch, n_q_heads, window, sinks, &a)) return paged_fail(CLO_ERR_INVALID, "%s: %s", who, f);
-  if (a.c.batch == 0 || a.c.total_q == 0 || a.c.max_q == 0 || a.part_rows > kFewRows) return CLO_OK;
-  *bytes = cache->kv_bits == 16 ? attend_few_bf16_bytes(a, cache->head_dim) : attend_few_e4m3_bytes(a, cache->head_dim);
+  if (a.c.batch == 0 || a.c.total_q == 0 || a.c.max_q == 0) return CLO_OK;
+  if (a.part_rows > kFewRows)
+    *bytes = attend_many_bytes(a, cache->head_dim);
+  else
+    *bytes = cache->kv_bits == 16 ? attend_few_bf16_bytes(a, cache->head_dim) : attend_few_e4m3_bytes(a, cache->head_dim);
   return CLO_OK;
 }
 

@@ -1,9 +1,14 @@
 // Attention of many rows per kv head over a paged cache: prompts, chunks of prompts, several drafted tokens.
 //
-// A block takes kTiles tiles of 128 rows of one (sequence, kv head) - consecutive query tokens times the group's
-// heads, so that a K or V tile of 128 tokens serves every head of the group - and walks the tiles of tokens that its
-// rows see.  Both products run on tcgen05: S = Q K^T from shared memory into TMEM, O += P V with P in TMEM (over the
+// A unit is one or two tiles of 128 rows of one (sequence, kv head) - consecutive query tokens times the group's
+// heads, so that a K or V tile of 128 tokens serves every head of the group - with the tiles of tokens that its rows see.
+// Both products run on tcgen05: S = Q K^T from shared memory into TMEM, O += P V with P in TMEM (over the
 // columns of S that it came from) and O in TMEM.  One thread owns a row of S: its maximum and sum need no exchange.
+//
+// The grid is one block per SM.  All units' token tiles, laid end to end (a unit counts kUnitCost more), are cut into equal shares, so
+// that ragged batches and causal prompts load the SMs alike and the fill of a block's next unit hides behind the current one's
+// end.  Units that a cut meets leave their sums in the caller's workspace and are joined by a second kernel; without a workspace, or
+// where a share would be short, units stay whole.
 //
 // Two lanes of work run against each other, so that one's products fill the time of the other's softmax: with two row
 // tiles, a lane is a row tile; with one (at most 128 rows), lane 0 takes the even token tiles and lane 1 the odd ones, and
@@ -33,6 +38,8 @@ namespace {
 constexpr int kTok = 128;    // tokens per tile
 constexpr int kRows = 128;   // rows per row tile
 constexpr float kGrow = 8.f;
+constexpr int kUnitCost = 2;   // what a unit costs beside its token tiles, in tiles
+constexpr int kMinShare = 8;   // no cuts below this share per block: joining costs about as much as four tiles
 
 // ---------------------------------------------------------------------------- tcgen05
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -126,29 +133,29 @@ struct Cfg {
   static constexpr int kQBytes = kRows * D * 2;
   // operand tiles of the ring, and 8-bit tiles on their way into it: what fits next to Q
   static constexpr int kSlots = BITS == 16 ? (D == 64 ? 8 : TILES == 2 ? 4 : 5) : (D == 64 ? 6 : 4);
-  static constexpr int kRaw = BITS == 16 ? 0 : D == 64 ? 12 : TILES == 2 ? 4 : 6;  // halves of 64 tokens
+  static constexpr int kRawSide = BITS == 16 ? 0 : D == 64 ? 6 : TILES == 2 ? 2 : 3;  // halves of 64 tokens, for K and for V
+  static constexpr int kRaw = 2 * kRawSide;
   static constexpr int kRawBytes = BITS == 16 ? 0 : kTok * D / 2;
   static constexpr int kMeta = D == 64 ? 16 : 8;  // token tiles whose page data is kept: more than the ring runs ahead
   static constexpr int kThreads = BITS == 16 ? 384 : 512;
-  static constexpr int kPartRow = D + 4;                       // floats per row of an accumulator to be joined
-  static constexpr int kSmem = TILES * kQBytes + kSlots * kTileBytes + kRaw * kRawBytes;
-  // accumulators to be joined, their maxima and sums: over Q and the ring, when they are done with
-  static constexpr int kMax = 2 * kRows * kPartRow * 4, kSum = kMax + 2 * kRows * 4, kJoin = kSum + 2 * kRows * 4;
-  static constexpr int kBytes = (kSmem > kJoin ? kSmem : kJoin) + 1024;
+  static constexpr int kBytes = TILES * kQBytes + kSlots * kTileBytes + kRaw * kRawBytes + 1024;
 };
 
-template <int META>
+template <int META, int TILES>
 struct Shared {
   uint64_t full[8], empty[8];      // operand tiles: filled (TMA or converters), products done
-  uint64_t tail, q_ready;          // bf16: the last V tile, before its end is cleared; Q
+  uint64_t tail[8], q_ready;       // bf16: a V tile whose end is yet to be cleared; Q
   uint64_t raw_full[12], raw_empty[12];  // 8-bit pages: halves of tiles on their way
   uint64_t s_full[2], p_half[2], p_ready[2];  // per lane: scores; weights of the first 64 tokens, of all
-  uint64_t done;                   // every product of both lanes
   uint64_t meta[META];
   float scale[META][3][8];        // K scale, log2 of the V scale, its reciprocal
   uint32_t there[META];
   uint32_t tmem;
   int failed;
+  int64_t first, last, total;      // the block's share of the units' costs, [first, last) of total
+  int64_t base;                    // where the first unit of the share begins
+  int start[3];                    // that unit: sequence, block of rows, kv head
+  float join_m[TILES == 1 ? kRows : 1], join_l[TILES == 1 ? kRows : 1];  // lane 1's maxima and sums
   int8_t q_exp[2][kRows];          // 8-bit pages: q rows are scaled by 2^-q_exp
 };
 
@@ -166,28 +173,197 @@ __device__ __forceinline__ bool wait(S& sh, uint64_t* bar, uint32_t parity) {
   return false;
 }
 
+// A unit and the block's part of it.
+struct Unit {
+  SeqRows s;
+  int b, qb, kvh;
+  int rows, row0, row_end;  // the sequence's rows, and the unit's [row0, row_end) of them
+  int pos_first, pos_last;
+  TileList tl;
+  int all;                  // token tiles of the unit
+  int t_begin, n;           // the block's part
+};
+
+template <int TILES>
+__device__ __forceinline__ void set_rows(const AttendParams& a, Unit* u) {
+  u->row0 = u->qb * TILES * kRows;
+  u->row_end = min(u->rows, u->row0 + TILES * kRows);
+  u->pos_first = u->s.pos0 + token_of_row(a, u->row0);
+  u->pos_last = u->s.pos0 + token_of_row(a, u->row_end - 1);
+  u->tl = tiles_of(u->pos_first, u->pos_last, u->s.kv_len, a.window, a.sinks, kTok);
+  u->all = u->tl.count();
+}
+template <int TILES>
+__device__ __forceinline__ bool set_seq(const AttendParams& a, int b, Unit* u) {
+  u->b = b;
+  u->s = seq_rows(a.c, b);
+  u->rows = u->s.n * a.group;
+  u->qb = (u->rows + TILES * kRows - 1) / (TILES * kRows) - 1;  // the last rows first: they see the most tokens
+  u->kvh = 0;
+  if (u->rows == 0) return false;
+  set_rows<TILES>(a, u);
+  return true;
+}
+// The next unit in the order sequence, block of rows from the last, kv head; false past the last one.
+template <int TILES>
+__device__ __forceinline__ bool next_unit(const AttendParams& a, Unit* u) {
+  if (++u->kvh < a.c.n_kv_heads) return true;
+  u->kvh = 0;
+  if (u->qb > 0) {
+    --u->qb;
+    set_rows<TILES>(a, u);
+    return true;
+  }
+  for (int b = u->b + 1; b < a.c.batch; ++b)
+    if (set_seq<TILES>(a, b, u)) return true;
+  return false;
+}
+
+// Cost of a sequence's units for one kv head: by one lane, or by a warp's lanes over its blocks of rows.
+template <int TILES>
+__device__ __forceinline__ int64_t seq_cost(const AttendParams& a, const SeqRows& s, int lane, int lanes) {
+  Unit u;
+  u.s = s;
+  u.rows = s.n * a.group;
+  const int blocks = (u.rows + TILES * kRows - 1) / (TILES * kRows);
+  int64_t c = 0;
+  for (u.qb = lane; u.qb < blocks; u.qb += lanes) {
+    set_rows<TILES>(a, &u);
+    c += u.all + kUnitCost;
+  }
+  return c;
+}
+__device__ __forceinline__ int64_t warp_sum64(int64_t v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ SeqRows shfl_seq(const SeqRows& s, int from) {
+  SeqRows r;
+  r.first = __shfl_sync(0xffffffffu, s.first, from);
+  r.n = __shfl_sync(0xffffffffu, s.n, from);
+  r.pos0 = __shfl_sync(0xffffffffu, s.pos0, from);
+  r.kv_len = __shfl_sync(0xffffffffu, s.kv_len, from);
+  return r;
+}
+
+// The block's share and the unit that it begins in, by one warp.
+template <int TILES, typename S>
+__device__ void find_share(const AttendParams& a, int lane, S& sh) {
+  const PagedParams& p = a.c;
+  const int heads = p.n_kv_heads;
+  int64_t total = 0, share = 0;
+  // pass 0 adds everything up, pass 1 stops at the sequence that holds the share's begin
+  for (int pass = 0; pass < 2; ++pass) {
+    int64_t before = 0;
+    int found = -1;
+    for (int c = 0; c < p.batch && found < 0; c += 32) {
+      SeqRows mine{};
+      if (c + lane < p.batch) mine = seq_rows(p, c + lane);
+      const int count = min(32, p.batch - c), blocks = (mine.n * a.group + TILES * kRows - 1) / (TILES * kRows);
+      const bool many = __any_sync(0xffffffffu, blocks > 8);
+      int64_t cost = 0;  // of this lane's sequence
+      if (many) {
+        for (int i = 0; i < count; ++i) {
+          const int64_t x = warp_sum64(seq_cost<TILES>(a, shfl_seq(mine, i), lane, 32));
+          if (lane == i) cost = x;
+        }
+      } else {
+        cost = seq_cost<TILES>(a, mine, 0, 1);
+      }
+      cost *= heads;
+      if (pass == 0) {
+        total += warp_sum64(cost);
+        continue;
+      }
+      int64_t incl = cost;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      const unsigned m = __ballot_sync(0xffffffffu, before + incl > share);
+      if (m) {
+        const int l = __ffs(m) - 1;
+        found = c + l;
+        before += __shfl_sync(0xffffffffu, incl - cost, l);
+        // the block of rows: the lanes step through them from the last
+        const SeqRows s = shfl_seq(mine, l);
+        Unit u;
+        u.s = s;
+        u.rows = s.n * a.group;
+        const int nb = (u.rows + TILES * kRows - 1) / (TILES * kRows);
+        for (int q = 0; q < nb; q += 32) {
+          int64_t x = 0;
+          if (q + lane < nb) {
+            u.qb = nb - 1 - q - lane;
+            set_rows<TILES>(a, &u);
+            x = (int64_t)(u.all + kUnitCost) * heads;
+          }
+          int64_t upto = x;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += v;
+          }
+          const unsigned w = __ballot_sync(0xffffffffu, before + upto > share);
+          if (w) {
+            const int k = __ffs(w) - 1;
+            const int64_t each = __shfl_sync(0xffffffffu, x, k) / heads;
+            before += __shfl_sync(0xffffffffu, upto - x, k);
+            if (lane == 0) {
+              const int64_t h = (share - before) / each;
+              sh.start[0] = found;
+              sh.start[1] = nb - 1 - q - k;
+              sh.start[2] = (int)h;
+              sh.base = before + h * each;
+            }
+            break;
+          }
+          before += __shfl_sync(0xffffffffu, upto, 31);
+        }
+      } else {
+        before += __shfl_sync(0xffffffffu, incl, 31);
+      }
+    }
+    if (pass == 0) {
+      share = total * blockIdx.x / gridDim.x;
+      if (lane == 0) {
+        sh.first = share;
+        sh.last = total * (blockIdx.x + 1) / gridDim.x;
+        sh.total = total;
+        sh.base = total;  // an empty share finds nothing
+      }
+      __syncwarp();
+      if (total * (blockIdx.x + 1) / gridDim.x == share) return;
+    }
+  }
+}
+
+// Workspace: a record per block, then two parts per block (slot 0: a unit that it ends or passes through, slot 1: one that it begins),
+// each [row][D elements, maximum, sum, -, -].
+struct PartRecord {
+  int valid, b, qb, kvh;
+  int last;  // the unit's parts are this block's slot 1 and slot 0 of the following ones up to `last`
+  int pad[3];
+};
+constexpr int kRecordBytes = 8192;
+static_assert(kSms * sizeof(PartRecord) <= kRecordBytes, "records fit");
+__host__ __device__ constexpr int64_t part_floats(int d, int tiles) { return (int64_t)tiles * kRows * (d + 4); }
+__device__ __forceinline__ float* part_of(const AttendParams& a, int block, int slot, int d, int tiles) {
+  return a.part + kRecordBytes / 4 + (2 * (int64_t)block + slot) * part_floats(d, tiles);
+}
+
 template <int D, int BITS, int TILES>
-__global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_many(const AttendParams a, const __grid_constant__ PageMaps maps, int q_blocks,
-                                                                              int splits) {
+__global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_many(const AttendParams a, const __grid_constant__ PageMaps maps) {
   using C = Cfg<D, BITS, TILES>;
   constexpr int SLOTS = C::kSlots;
   extern __shared__ uint8_t smem_raw[];
   constexpr int kMeta = C::kMeta;
-  __shared__ __align__(16) Shared<kMeta> sh;
+  __shared__ __align__(16) Shared<kMeta, TILES> sh;
 
   const PagedParams& p = a.c;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-  // the last rows first: they see the most tokens
-  const int unit = blockIdx.x / splits, rank = blockIdx.x % splits;
-  const int kvh = unit % p.n_kv_heads, qb = q_blocks - 1 - unit / p.n_kv_heads, b = blockIdx.y;
-  const SeqRows s = seq_rows(p, b);
-  const int rows = s.n * a.group, row0 = qb * TILES * kRows;
-  if (row0 >= rows) return;  // the whole cluster
-  const int row_end = min(rows, row0 + TILES * kRows);
-  const int pos_first = s.pos0 + row0 / a.group, pos_last = s.pos0 + (row_end - 1) / a.group;
-  const TileList tl = tiles_of(pos_first, pos_last, s.kv_len, a.window, a.sinks, kTok);
-  const int all = tl.count();
-  const int t_begin = (int)((int64_t)all * rank / splits), n = (int)((int64_t)all * (rank + 1) / splits) - t_begin;
 
   const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t q_smem = smem, ring = smem + TILES * C::kQBytes, raw = ring + SLOTS * C::kTileBytes;
@@ -197,6 +373,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
     for (int i = 0; i < 8; ++i) {
       mbar_init(&sh.full[i], BITS == 16 ? 1 : 2 * 128);
       mbar_init(&sh.empty[i], 1);
+      mbar_init(&sh.tail[i], 1);
     }
     for (int i = 0; i < 12; ++i) {
       mbar_init(&sh.raw_full[i], 1);
@@ -207,8 +384,6 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
       mbar_init(&sh.p_half[i], 128);
       mbar_init(&sh.p_ready[i], 128);
     }
-    mbar_init(&sh.done, 1);
-    mbar_init(&sh.tail, 1);
     mbar_init(&sh.q_ready, 256);
     for (int i = 0; i < kMeta; ++i) mbar_init(&sh.meta[i], 1);
     sh.failed = 0;
@@ -220,33 +395,81 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
 
+  if (warp == 0) find_share<TILES>(a, lane, sh);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
   constexpr uint32_t kS[2] = {0, 128}, kO[2] = {256, 384};
 
-  // Operand tiles in ring order: e = 0 is K(0), e = 2 j + 1 is K(j + 1), e = 2 j + 2 is V(j), without K(n).
-  // Position of K(j) and V(j):
-  auto at_k = [&](int j) { return j == 0 ? 0 : 2 * j - 1; };
-  auto at_v = [&](int j) { return 2 * j + 2 - (j + 1 >= n ? 1 : 0); };
-  // and back: element e is a V tile?  which token tile?
-  auto is_v = [&](int e) { return e > 0 && ((e & 1) == 0 || e == 2 * n - 1); };
-  auto tile_of = [&](int e) { return !is_v(e) ? (e + 1) / 2 : e == 2 * n - 1 ? n - 1 : e / 2 - 1; };
+  // The block's walk over its units; every role takes it by itself.  `visit` is called with each unit that the block has a part of.
+  const bool cuts = a.part != nullptr && sh.total >= (int64_t)kMinShare * gridDim.x;
+  auto walk = [&](auto&& visit) {
+    int64_t base = sh.base;
+    const int64_t first = sh.first, last = sh.last;
+    if (base >= last) return;
+    Unit u;
+    set_seq<TILES>(a, sh.start[0], &u);
+    u.qb = sh.start[1];
+    u.kvh = sh.start[2];
+    set_rows<TILES>(a, &u);
+    while (true) {
+      const int64_t end = base + u.all + kUnitCost;
+      bool part = base >= first;  // the unit begins in the share: whole units, and those without a token, go by that alone
+      u.t_begin = 0;
+      u.n = u.all;
+      if (cuts && u.all > 0) {
+        u.t_begin = base >= first ? 0 : max((int)(first - base) - kUnitCost, 0);
+        u.n = (end <= last ? u.all : max((int)(last - base) - kUnitCost, 0)) - u.t_begin;
+        part = u.n > 0;
+      }
+      if (part && !visit(u, base)) return;
+      base = end;
+      if (base >= last || !next_unit<TILES>(a, &u)) return;
+    }
+  };
 
-  // Lane t takes token tiles first_of(t), + kStep, ...: count_of(t) of them.
+  // Operand tiles of a unit in ring order: e = 0 is K(0), e = 2 j + 1 is K(j + 1), e = 2 j + 2 is V(j), without K(n); the ring's count
+  // runs on from unit to unit.  Lane t takes token tiles first_of(t), + kStep, ...
+  auto at_k = [](int j) { return j == 0 ? 0 : 2 * j - 1; };
+  auto at_v = [](int j, int n) { return 2 * j + 2 - (j + 1 >= n ? 1 : 0); };
   constexpr int kStep = TILES == 2 ? 1 : 2;
-  auto first_of = [&](int t) { return TILES == 2 ? 0 : t; };
-  auto count_of = [&](int t) { return TILES == 2 ? n : (n + 1 - t) / 2; };
-  const Visible blk_f = visible_of(pos_first, s.kv_len, a.window, a.sinks), blk_l = visible_of(pos_last, s.kv_len, a.window, a.sinks);
-  // the last token tile holds tokens that no row sees
-  const bool tail = n > 0 && (tl.at(t_begin + n - 1) + 1) * kTok > blk_l.hi;
+  auto first_of = [](int t) { return TILES == 2 ? 0 : t; };
+  auto count_of = [](int t, int n) { return TILES == 2 ? n : (n + 1 - t) / 2; };
+  // the unit's last tile, if the part has it, holds tokens that no row sees
+  auto tail_of = [&](const Unit& u) {
+    return u.n > 0 && (u.tl.at(u.t_begin + u.n - 1) + 1) * kTok > visible_of(u.pos_last, u.s.kv_len, a.window, a.sinks).hi;
+  };
 
   if (warp < 8) {
     // ------------------------------------------------------------------------ softmax
+    constexpr float kOff = BITS == 16 ? 0.f : 7.f;  // weights of 8-bit pages: up to 2^15 with kGrow, fp16 down to 2^-31
+    const int t = warp >> 2, my_tile = TILES == 2 ? t : 0;
+    const uint32_t lane_off = (uint32_t)(warp & 3) * 32u << 16;
+    const uint32_t s_addr = tmem + lane_off + kS[t], o_addr = tmem + lane_off + kO[t];
+    uint32_t q_phase = 0, s_phase = 0;
+    int tiles_done = 0;
+    bool ok = true;
+    PartRecord record{};
+    walk([&](const Unit& u, int64_t base) {
+    const SeqRows& s = u.s;
+    const int n = u.n, row0 = u.row0, rows = u.rows, kvh = u.kvh, mine = count_of(t, n);
+    const bool full = n == u.all;
+    if (!full && u.t_begin == 0) {
+      record.valid = 1;
+      record.b = u.b;
+      record.qb = u.qb;
+      record.kvh = kvh;
+      const int64_t end = base + u.all + kUnitCost;
+      int c = (int)min(end * gridDim.x / sh.total, (int64_t)gridDim.x - 1);
+      while (sh.total * c / gridDim.x >= end) --c;
+      while (sh.total * (c + 1) / gridDim.x < end) ++c;
+      record.last = c;
+    }
     // Q rows into operand tiles, D / 8 threads per row.  8-bit pages: fp16, each row scaled by a power of two that puts its
     // largest finite element into [2^14, 2^15).
-    {
+    if (n > 0) asm volatile("bar.sync 1, 256;" ::: "memory");  // both lanes have left the last unit's Q
+    if (n > 0 && ok) {
       constexpr int kLanes = D / 8, kStepRows = 256 / kLanes, kIters = TILES * kRows / kStepRows;
       const int c = tid % kLanes;
 #pragma unroll 1
@@ -282,24 +505,24 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
       mbar_arrive(&sh.q_ready);
     }
     float ref = -INFINITY, l = 0.f;
-    const int t = warp >> 2, mine = count_of(t), my_tile = TILES == 2 ? t : 0;
     const int my_row = row0 + my_tile * kRows + (tid & 127);
     const bool row_ok = my_row < rows;
-    bool ok = __all_sync(0xffffffffu, wait(sh, &sh.q_ready, 0));
+    if (n > 0) {
+      ok = ok && __all_sync(0xffffffffu, wait(sh, &sh.q_ready, q_phase));
+      q_phase ^= 1u;
+    }
     const float fac = BITS == 8 ? a.scale_log2 * __uint_as_float((uint32_t)(127 + sh.q_exp[my_tile][tid & 127]) << 23) : a.scale_log2;
     {
-      constexpr float kOff = BITS == 16 ? 0.f : 7.f;  // weights of 8-bit pages: up to 2^15 with kGrow, fp16 down to 2^-31
-      const uint32_t lane_off = (uint32_t)(warp & 3) * 32u << 16;
-      const uint32_t s_addr = tmem + lane_off + kS[t], o_addr = tmem + lane_off + kO[t];
       // the tile's first and last row bound what "every row sees" means; rows past the end follow the last one
       const int rf = min(row0 + my_tile * kRows, rows - 1), rl = min(row0 + my_tile * kRows + kRows - 1, rows - 1);
       const Visible vf = visible_of(s.pos0 + rf / a.group, s.kv_len, a.window, a.sinks);
       const Visible vl = visible_of(s.pos0 + rl / a.group, s.kv_len, a.window, a.sinks);
       const Visible v = visible_of(s.pos0 + min(my_row, rows - 1) / a.group, s.kv_len, a.window, a.sinks);
       for (int i = 0; i < mine && ok; ++i) {
-        const int j = first_of(t) + i * kStep, j0 = tl.at(t_begin + j) * kTok;
-        const int slot = j % kMeta;
-        ok = wait(sh, &sh.meta[slot], (j / kMeta) & 1) && wait(sh, &sh.s_full[t], i & 1);
+        const int j = first_of(t) + i * kStep, j0 = u.tl.at(u.t_begin + j) * kTok;
+        const int slot = (tiles_done + j) % kMeta;
+        ok = wait(sh, &sh.meta[slot], ((tiles_done + j) / kMeta) & 1) && wait(sh, &sh.s_full[t], s_phase);
+        s_phase ^= 1u;
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
@@ -399,79 +622,121 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
           if (half == 0) tc_wait_ld<2>(x);
         }
       }
-      // the lane's last product; where the accumulators go to shared memory, every product
-      const bool direct = TILES == 2 && splits == 1;
-      if (ok) ok = direct ? mine == 0 || wait(sh, &sh.s_full[t], mine & 1) : wait(sh, &sh.done, 0);
-      ok = __all_sync(0xffffffffu, ok);
+      // the lane's last product
+      if (mine > 0) {
+        ok = ok && __all_sync(0xffffffffu, wait(sh, &sh.s_full[t], s_phase));
+        s_phase ^= 1u;
+      }
       tc_fence_after();
       if (!ok) l = __int_as_float(0x7fffffff);
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      float* part = reinterpret_cast<float*>(generic) + (t * kRows + (tid & 127)) * C::kPartRow;
-      if (!direct) {
-        *reinterpret_cast<float*>(generic + C::kMax + (t * kRows + (tid & 127)) * 4) = ref;
-        *reinterpret_cast<float*>(generic + C::kSum + (t * kRows + (tid & 127)) * 4) = l;
-      }
-      float odd = l * 0.f;  // NaN if anything in the row is no finite number
-#pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t o[32];
-        if (mine > 0) {
-          tc_ld32(o_addr + 32 * c, o);
-          tc_wait_ld<1>(o);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = 0u;
+      if (TILES == 1) {
+        // lane 1's sums join lane 0's: its accumulator lies in the same TMEM rows
+        if (TILES == 1 && t == 1) {
+          sh.join_m[tid & 127] = ref;
+          sh.join_l[tid & 127] = l;
+          tc_fence_before();
         }
-        if (!direct) {
+        asm volatile("bar.sync 2, 256;" ::: "memory");
+        tc_fence_after();
+      }
+      if (TILES == 2 || t == 0) {
+        float f0 = 1.f, f1 = 0.f;
+        const bool both = TILES == 1 && count_of(1, n) > 0;
+        if (both) {
+          const float m1 = sh.join_m[tid & 127], mx = fmaxf(ref, m1);
+          f0 = ref == mx ? 1.f : exp2_fast(ref - mx);
+          f1 = m1 == mx ? 1.f : exp2_fast(m1 - mx);
+          l = l * f0 + sh.join_l[tid & 127] * f1;
+          ref = mx;
+        }
+        const float inv = full ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+        float* part = nullptr;
+        if (!full) {
+          part = part_of(a, blockIdx.x, u.t_begin == 0 ? 1 : 0, D, TILES) + (int64_t)(my_tile * kRows + (tid & 127)) * (D + 4);
+          *reinterpret_cast<float2*>(part + D) = make_float2(ref, l);
+        }
+        float odd = l * 0.f;  // NaN if anything in the row is no finite number
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          if (mine > 0) {
+            tc_ld32(o_addr + 32 * c, o);
+            tc_wait_ld<1>(o);
+          } else {
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) *reinterpret_cast<uint4*>(part + 32 * c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-        } else {
-          // through the row tile's Q, which is done with, so that rows leave in whole lines
+            for (int i = 0; i < 32; ++i) o[i] = 0u;
+          }
+          if (both) {
+            uint32_t o1[32];
+            tc_ld32(o_addr + 128 + 32 * c, o1);
+            tc_wait_ld<1>(o1);
 #pragma unroll
-          for (int i = 0; i < 32; i += 8) {
-            float y[8];
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f0 + __uint_as_float(o1[i]) * f1);
+          }
+          if (!full) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              odd = fmaf(__uint_as_float(o[i + e]), 0.f, odd);
-              y[e] = l == 0.f ? 0.f : __uint_as_float(o[i + e]) * inv;
+            for (int i = 0; i < 32; i += 4) *reinterpret_cast<uint4*>(part + 32 * c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          } else {
+            // through the row tile's Q, which is done with, so that rows leave in whole lines
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+              float y[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                odd = fmaf(__uint_as_float(o[i + e]), 0.f, odd);
+                y[e] = l == 0.f ? 0.f : __uint_as_float(o[i + e]) * inv;
+              }
+              *reinterpret_cast<uint4*>(generic + (swizzled<128>(q_smem + my_tile * C::kQBytes, kRows, tid & 127, 4 * c + i / 8) - smem)) = pack8(y);
             }
-            *reinterpret_cast<uint4*>(generic + (swizzled<128>(q_smem + my_tile * C::kQBytes, kRows, tid & 127, 4 * c + i / 8) - smem)) = pack8(y);
+          }
+        }
+        if (full) {
+          __syncwarp();
+          constexpr int kLanes = D / 8;
+#pragma unroll 2
+          for (int i = 0; i < kLanes; ++i) {
+            const int r = (warp & 3) * 32 + i * (32 / kLanes) + lane / kLanes, gr = row0 + my_tile * kRows + r;
+            if (gr < rows)
+              *(reinterpret_cast<uint4*>(a.out + row_offset(a, s.first, kvh, gr, a.o_token, a.o_head)) + lane % kLanes) =
+                  *reinterpret_cast<const uint4*>(generic + (swizzled<128>(q_smem + my_tile * C::kQBytes, kRows, r, lane % kLanes) - smem));
+          }
+          __syncwarp();
+          unsigned again = __ballot_sync(0xffffffffu, row_ok && odd != 0.f);
+          for (; again; again &= again - 1) {
+            const int gr = row0 + my_tile * kRows + (warp & 3) * 32 + __ffs(again) - 1;
+            attend_row<D, BITS>(a, u.b, s, gr / a.group, kvh * a.group + gr % a.group, lane);
           }
         }
       }
-      if (direct) {
-        __syncwarp();
-        constexpr int kLanes = D / 8;
-#pragma unroll 2
-        for (int i = 0; i < kLanes; ++i) {
-          const int r = (warp & 3) * 32 + i * (32 / kLanes) + lane / kLanes, gr = row0 + my_tile * kRows + r;
-          if (gr < rows)
-            *(reinterpret_cast<uint4*>(a.out + row_offset(a, s.first, kvh, gr, a.o_token, a.o_head)) + lane % kLanes) =
-                *reinterpret_cast<const uint4*>(generic + (swizzled<128>(q_smem + my_tile * C::kQBytes, kRows, r, lane % kLanes) - smem));
-        }
-        __syncwarp();
-        unsigned again = __ballot_sync(0xffffffffu, row_ok && odd != 0.f);
-        for (; again; again &= again - 1) {
-          const int gr = row0 + my_tile * kRows + (warp & 3) * 32 + __ffs(again) - 1;
-          attend_row<D, BITS>(a, b, s, gr / a.group, kvh * a.group + gr % a.group, lane);
-        }
-      }
       tc_fence_before();
+      tiles_done += n;
     }
+    return true;
+    });
+    if (tid == 0 && a.part) *(reinterpret_cast<PartRecord*>(a.part) + blockIdx.x) = record;
   } else {
     if (warp == 8 || warp == 11) {
       // ---------------------------------------------------------------------- TMA: K and page data; V
       const int side = warp == 8 ? 0 : 1;
       constexpr int kSpan = BITS == 16 ? 128 : (D < 128 ? D : 128);  // bytes of a page row in one box
       constexpr int kBoxSpans = D * BITS / 8 / kSpan;
-      constexpr int kBuf = BITS == 16 ? C::kSlots : C::kRaw;
+      // The ring of operand tiles (16 bits), or the side's own ring of half tiles.  Two warps may fill one ring in turns only if it holds
+      // three elements or more: the parity of an earlier use than the one waited for must not be met (K jumps three places from
+      // unit to unit).
+      static_assert(C::kSlots >= 3, "see above");
+      constexpr int kBuf = BITS == 16 ? C::kSlots : C::kRawSide;
       constexpr int kParts = BITS == 16 ? 1 : 2, kPartTok = kTok / kParts;
       const int box = min(p.page_size, kPartTok);
+      int e_base = 0, tiles_done = 0;
+      bool ok = true;
+      walk([&](const Unit& u, int64_t) {
+      const int n = u.n, b = u.b, kvh = u.kvh;
+      const bool tail = tail_of(u);
       // Pages of four tiles at a time, a lane per 16 tokens, looked up two batches ahead and their scales one, so that no load waits for
       // another.
       auto pages_of = [&](int batch) {
         const int j = 4 * batch + (lane >> 3);
-        return j < n ? page_of(p, b, (tl.at(t_begin + j) * kTok + (lane & 7) * 16) >> p.page_shift) : -1;
+        return j < n ? page_of(p, b, (u.tl.at(u.t_begin + j) * kTok + (lane & 7) * 16) >> p.page_shift) : -1;
       };
       auto scales_of = [&](int page) {
         float2 sc = make_float2(1.f, 1.f);
@@ -483,9 +748,8 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
       };
       int page0 = pages_of(0), page1 = pages_of(1), page2 = pages_of(2);
       float2 scale0 = scales_of(page0), scale1 = scales_of(page1);
-      bool ok = true;
       for (int j = 0; j < n && ok; ++j) {
-        const int q = j & 3, e = side == 0 ? at_k(j) : at_v(j);
+        const int q = j & 3, e = e_base + (side == 0 ? at_k(j) : at_v(j, n));
         if (q == 0 && j > 0) {
           page0 = page1;
           page1 = page2;
@@ -495,18 +759,18 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
         }
 #pragma unroll
         for (int h = 0; h < kParts; ++h) {
-          const int x = e * kParts + h, buf = x % kBuf;
-          uint64_t* full = BITS == 16 ? (tail && side == 1 && j == n - 1 ? &sh.tail : &sh.full[buf]) : &sh.raw_full[buf];
+          const int x = BITS == 16 ? e : 2 * (tiles_done + j) + h, use = x / kBuf, buf = BITS == 16 ? x % kBuf : side * kBuf + x % kBuf;
+          uint64_t* full = BITS == 16 ? (tail && side == 1 && j == n - 1 ? &sh.tail[buf] : &sh.full[buf]) : &sh.raw_full[buf];
           uint64_t* empty = BITS == 16 ? &sh.empty[buf] : &sh.raw_empty[buf];
           int id[kPartTok / 16];
 #pragma unroll
           for (int g = 0; g < kPartTok / 16; ++g) id[g] = __shfl_sync(0xffffffffu, page0, 8 * q + h * (kPartTok / 16) + g);
-          if (x >= kBuf) ok = wait(sh, empty, (x / kBuf - 1) & 1);
+          if (use > 0) ok = wait(sh, empty, (use - 1) & 1);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           if (elect_one()) {
             const uint32_t dst = BITS == 16 ? ring + buf * C::kTileBytes : raw + buf * C::kRawBytes, bar = smem_u32(full);
-            const int slot0 = tl.at(t_begin + j) * kTok + h * kPartTok;
+            const int slot0 = u.tl.at(u.t_begin + j) * kTok + h * kPartTok;
             mbar_arrive_expect_tx(full, BITS == 16 ? C::kTileBytes : C::kRawBytes);
 #pragma unroll
             for (int g = 0; g < kPartTok / 16; ++g)
@@ -519,7 +783,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
           __syncwarp();
         }
         if (ok && side == 0) {  // which 16-token groups are there, and their scales
-          const int slot = j % kMeta;
+          const int slot = (tiles_done + j) % kMeta;
           const unsigned there = __ballot_sync(0xffffffffu, page0 >= 0) >> (8 * q) & 0xffu;
           if (lane == 0) sh.there[slot] = there;
           if (BITS == 8 && lane >> 3 == q) {
@@ -532,9 +796,13 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
           if (lane == 0) mbar_arrive(&sh.meta[slot]);
         }
       }
+      e_base += 2 * n;
+      tiles_done += n;
+      return ok;
+      });
       if (!ok) {  // copies in flight land before the block leaves
         for (int i = 0; i < kBuf; ++i)
-          for (int ph = 0; ph < 2; ++ph) mbar_wait_limited(BITS == 16 ? &sh.full[i] : &sh.raw_full[i], ph);
+          for (int ph = 0; ph < 2; ++ph) mbar_wait_limited(BITS == 16 ? &sh.full[i] : &sh.raw_full[side * kBuf + i], ph);
       }
     } else if (warp == 9) {
       // ---------------------------------------------------------------------- MMA issue
@@ -560,62 +828,84 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
           tc_mma_ts(tm + 256 + 128 * t, tm + 128 * t + kk * 8, vd + kk * (2048 >> 4), kShapeO, add || kk > 0, leader);
       };
       auto ready = [&](int e) { return wait(sh, &sh.full[e % SLOTS], (e / SLOTS) & 1); };
-      bool ok = wait(sh, &sh.q_ready, 0);
-      for (int t = 0; t < 2 && ok; ++t) {
-        if (count_of(t) == 0) break;
-        const int e = at_k(first_of(t));
-        ok = ready(e);
-        if (!ok) break;
-        tc_fence_after();
-        score(t, e % SLOTS);
-        tc_commit(&sh.s_full[t], leader);
-        if (TILES == 1 || t == 1) tc_commit(&sh.empty[e % SLOTS], leader);
-      }
-      // V of tile j and K of the lane's next tile; looked at ahead of time, between two products' issue, where a wait
-      // costs nothing
       auto seen = [&](int e) { return mbar_test(&sh.full[e % SLOTS], (e / SLOTS) & 1); };
-      bool ahead = false;
-      for (int j = 0; j < n && ok; ++j) {
-        const int ev = at_v(j), vslot = ev % SLOTS;
-        const bool next = j + kStep < n;
-        const int ek = next ? at_k(j + kStep) : 0, kslot = ek % SLOTS;
-        if (!ahead) ok = ready(ev) && (!next || ready(ek));
-#pragma unroll
-        for (int u = 0; u < TILES; ++u) {
-          const int t = TILES == 2 ? u : j & 1;
-          const uint32_t phase = (TILES == 2 ? j : j >> 1) & 1;
-          ok = ok && wait(sh, &sh.p_half[t], phase);
+      uint32_t q_phase = 0, p_phase = 0;  // p_phase: a bit per lane
+      int e_base = 0;
+      walk([&](const Unit& u, int64_t) {
+        const int n = u.n;
+        if (n == 0) return true;
+        bool ok = wait(sh, &sh.q_ready, q_phase);
+        q_phase ^= 1u;
+        for (int t = 0; t < 2 && ok; ++t) {
+          if (count_of(t, n) == 0) break;
+          const int e = e_base + at_k(first_of(t));
+          ok = ready(e);
           if (!ok) break;
           tc_fence_after();
-          values(t, vslot, TILES == 2 ? j > 0 : j > 1, 0);
-          ok = wait(sh, &sh.p_ready[t], phase);
-          if (!ok) break;
-          tc_fence_after();
-          values(t, vslot, true, kTok / 32);
-          if (u == TILES - 1) {
-            tc_commit(&sh.empty[vslot], leader);
-            ahead = __all_sync(0xffffffffu, j + 1 < n && seen(at_v(j + 1)) && (j + 1 + kStep >= n || seen(at_k(j + 1 + kStep))));
-          }
-          if (next) score(t, kslot);
+          score(t, e % SLOTS);
           tc_commit(&sh.s_full[t], leader);
+          if (TILES == 1 || t == 1) tc_commit(&sh.empty[e % SLOTS], leader);
         }
-        if (ok && next) tc_commit(&sh.empty[kslot], leader);
-      }
-      if (ok && n > 0) tc_commit(&sh.done, leader);
-      else if (leader) mbar_arrive(&sh.done);
+        // V of tile j and K of the lane's next tile; looked at ahead of time, between two products' issue, where a wait
+        // costs nothing
+        bool ahead = false;
+        for (int j = 0; j < n && ok; ++j) {
+          const int ev = e_base + at_v(j, n), vslot = ev % SLOTS;
+          const bool next = j + kStep < n;
+          const int ek = next ? e_base + at_k(j + kStep) : 0, kslot = ek % SLOTS;
+          if (!ahead) ok = ready(ev) && (!next || ready(ek));
+#pragma unroll
+          for (int v = 0; v < TILES; ++v) {
+            const int t = TILES == 2 ? v : j & 1;
+            const uint32_t phase = p_phase >> t & 1u;
+            p_phase ^= 1u << t;
+            ok = ok && wait(sh, &sh.p_half[t], phase);
+            if (!ok) break;
+            tc_fence_after();
+            values(t, vslot, TILES == 2 ? j > 0 : j > 1, 0);
+            ok = wait(sh, &sh.p_ready[t], phase);
+            if (!ok) break;
+            tc_fence_after();
+            values(t, vslot, true, kTok / 32);
+            if (v == TILES - 1) {
+              tc_commit(&sh.empty[vslot], leader);
+              ahead = __all_sync(0xffffffffu, j + 1 < n && seen(e_base + at_v(j + 1, n)) && (j + 1 + kStep >= n || seen(e_base + at_k(j + 1 + kStep))));
+            }
+            if (next) score(t, kslot);
+            tc_commit(&sh.s_full[t], leader);
+          }
+          if (ok && next) tc_commit(&sh.empty[kslot], leader);
+        }
+        e_base += 2 * n;
+        return ok;
+      });
       __syncwarp();
-    } else if (BITS == 16 ? warp == 10 && tail : warp >= 12) {
+    } else if (BITS == 16 ? warp == 10 : warp >= 12) {
       if constexpr (BITS == 16) {
         // ------------------------------------------------------------------ the last V tile's end
-        const int e = 2 * n - 1, slot = e % SLOTS, from = blk_l.hi - tl.at(t_begin + n - 1) * kTok;  // first token that no row sees
-        if (wait(sh, &sh.tail, 0)) {
-          for (int h = 0; h < D / 64; ++h)
-            for (int i = from * 8 + lane; i < kTok * 8; i += 32)
-              *(reinterpret_cast<uint4*>(generic + (ring - smem) + slot * C::kTileBytes + h * kTok * 128) + i) = make_uint4(0, 0, 0, 0);
-          fence_proxy_async_smem();
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.full[slot]);
+        uint32_t phase = 0;  // a bit per slot
+        int e_base = 0;
+        walk([&](const Unit& u, int64_t) {
+          const int n = u.n;
+          if (tail_of(u)) {
+            const int slot = (e_base + 2 * n - 1) % SLOTS;
+            // from the first token that no row sees
+            const int from = visible_of(u.pos_last, u.s.kv_len, a.window, a.sinks).hi - u.tl.at(u.t_begin + n - 1) * kTok;
+            const bool ok = wait(sh, &sh.tail[slot], phase >> slot & 1u);
+            phase ^= 1u << slot;
+            if (ok) {
+              for (int h = 0; h < D / 64; ++h)
+                for (int i = from * 8 + lane; i < kTok * 8; i += 32)
+                  *(reinterpret_cast<uint4*>(generic + (ring - smem) + slot * C::kTileBytes + h * kTok * 128) + i) = make_uint4(0, 0, 0, 0);
+              fence_proxy_async_smem();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.full[slot]);
+            if (!ok) return false;
+          }
+          e_base += 2 * n;
+          return true;
+        });
       } else {
         // ------------------------------------------------------------------ 8-bit codes -> fp16
         // A warp takes 16 rows of a half tile, a quarter of it 4 neighbouring chunks of two rows that differ in bits 0 and 2: then
@@ -629,22 +919,26 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
           from[i] = swizzled<(D < 128 ? 64 : 128)>(0, kTok, r, c);
           to[i] = h * kTok * 128 + r * 128 + (((2 * (lane & 3)) ^ (r & 7)) << 4);
         }
+        int e_base = 0;
+        walk([&](const Unit& u, int64_t) {
+        const int n = u.n, blk_hi = visible_of(u.pos_last, u.s.kv_len, a.window, a.sinks).hi;
         bool ok = true;
-        for (int e = 0; e < 2 * n && ok; ++e) {
-          const int slot = e % SLOTS;
+        for (int i = 0; i < 2 * n && ok; ++i) {
+          const int e = e_base + i, slot = e % SLOTS;
           if (e >= SLOTS) ok = wait(sh, &sh.empty[slot], (e / SLOTS - 1) & 1);
-          const int seen = is_v(e) ? blk_l.hi - tl.at(t_begin + tile_of(e)) * kTok : kTok;  // tokens that some row sees
+          const bool is_v = i > 0 && ((i & 1) == 0 || i == 2 * n - 1);
+          const int j = !is_v ? (i + 1) / 2 : i == 2 * n - 1 ? n - 1 : i / 2 - 1;           // its token tile
+          const int seen = is_v ? blk_hi - u.tl.at(u.t_begin + j) * kTok : kTok;            // tokens that some row sees
 #pragma unroll 1
           for (int half = 0; half < 2; ++half) {
-            const int x = 2 * e + half, buf = x % C::kRaw;
-            ok = ok && wait(sh, &sh.raw_full[buf], (x / C::kRaw) & 1);
+            const int x = 2 * (e_base / 2 + j) + half, buf = (is_v ? C::kRawSide : 0) + x % C::kRawSide;
+            ok = ok && wait(sh, &sh.raw_full[buf], (x / C::kRawSide) & 1);
             if (!ok) break;
             const uint8_t* src = generic + (raw - smem) + buf * C::kRawBytes;
             uint8_t* dst = generic + (ring - smem) + slot * C::kTileBytes + half * 64 * 128;
             uint4 w[kPer];
 #pragma unroll
             for (int i = 0; i < kPer; ++i) w[i] = *reinterpret_cast<const uint4*>(src + from[i]);
-            mbar_arrive(&sh.raw_empty[buf]);
             if (seen < kTok) {
 #pragma unroll
               for (int i = 0; i < kPer; ++i)
@@ -662,81 +956,98 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
             }
             fence_proxy_async_smem();
             mbar_arrive(&sh.full[slot]);
+            mbar_arrive(&sh.raw_empty[buf]);  // not before the stores, which wait for the loads' values: the next copy overwrites them
           }
         }
+        e_base += 2 * n;
+        return ok;
+        });
       }
     }
   }
   __syncwarp();
+  tc_fence_before();
   __syncthreads();
-  if (splits > 1) cluster_sync();
   if (warp == 9) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }
-  if (warp < 8 && (TILES == 1 || splits > 1)) {
-    // join the blocks of the cluster and, with one row tile, their lanes: a warp per row
-    constexpr int kSets = TILES == 2 ? 1 : 2;
-    for (int r = rank * 8 + warp; r < row_end - row0; r += splits * 8) {
-      float mx = -INFINITY, sum = 0.f, o[D / 32];
+}
+
+// Joins the parts of the units that the cuts met: a block per record and eight rows, a warp per row.
+template <int D, int BITS, int TILES>
+__global__ void __launch_bounds__(256) k_attend_many_join(const AttendParams a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const PartRecord rec = *(reinterpret_cast<const PartRecord*>(a.part) + blockIdx.x);
+  if (!rec.valid) return;
+  const int lane = threadIdx.x & 31, r = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const SeqRows s = seq_rows(a.c, rec.b);
+  const int gr = rec.qb * TILES * kRows + r;
+  if (gr >= s.n * a.group) return;
+  constexpr int E = D / 32;
+  const int64_t row = (int64_t)r * (D + 4);
+  auto part = [&](int c) { return part_of(a, c, c == (int)blockIdx.x ? 1 : 0, D, TILES) + row; };
+  float mx = -INFINITY;
+  for (int c = blockIdx.x + lane; c <= rec.last; c += 32) mx = fmaxf(mx, part(c)[D]);
+  mx = warp_max(mx);
+  float l = 0.f, o[E];
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
-      for (int c = 0; c < splits * kSets; ++c) mx = fmaxf(mx, ld_cluster_f32(smem + C::kMax + (c % kSets * kRows + r) * 4, c / kSets));
-      for (int c = 0; c < splits * kSets; ++c) {
-        const int at = c % kSets * kRows + r, from = c / kSets;
-        const float mc = ld_cluster_f32(smem + C::kMax + at * 4, from);
-        const float f = mc == mx ? 1.f : exp2_fast(mc - mx);
-        sum = fmaf(ld_cluster_f32(smem + C::kSum + at * 4, from), f, sum);
+  for (int i = 0; i < E; ++i) o[i] = 0.f;
+#pragma unroll 4
+  for (int c = blockIdx.x; c <= rec.last; ++c) {
+    const float* q = part(c);
+    const float2 ml = *reinterpret_cast<const float2*>(q + D);
+    const float f = ml.x == mx ? 1.f : exp2_fast(ml.x - mx);
+    l = fmaf(ml.y, f, l);
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i)
-          o[i] = fmaf(ld_cluster_f32(smem + (at * C::kPartRow + lane * (D / 32) + i) * 4, from), f, o[i]);
-      }
-      const int gr = row0 + r;
-      float odd = sum * 0.f;
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) odd = fmaf(o[i], 0.f, odd);
-      if (__any_sync(0xffffffffu, odd != 0.f)) {
-        attend_row<D, BITS>(a, b, s, gr / a.group, kvh * a.group + gr % a.group, lane);
-        continue;
-      }
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      uint16_t* dst = a.out + row_offset(a, s.first, kvh, gr, a.o_token, a.o_head) + lane * (D / 32);
-#pragma unroll
-      for (int i = 0; i < D / 32; i += 2) *reinterpret_cast<uint32_t*>(dst + i) = sum == 0.f ? 0u : pack_bf16(o[i] * inv, o[i + 1] * inv);
+    for (int i = 0; i < E; i += 2) {
+      const float2 v = *reinterpret_cast<const float2*>(q + lane * E + i);
+      o[i] = fmaf(v.x, f, o[i]);
+      o[i + 1] = fmaf(v.y, f, o[i + 1]);
     }
   }
-  if (splits > 1) {
-    __syncwarp();
-    cluster_sync();  // no block leaves while another reads its shared memory
+  float odd = l * 0.f;
+#pragma unroll
+  for (int i = 0; i < E; ++i) odd = fmaf(o[i], 0.f, odd);
+  if (__any_sync(0xffffffffu, odd != 0.f)) {
+    attend_row<D, BITS>(a, rec.b, s, gr / a.group, rec.kvh * a.group + gr % a.group, lane);
+    return;
   }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  uint16_t* dst = a.out + row_offset(a, s.first, rec.kvh, gr, a.o_token, a.o_head) + lane * E;
+#pragma unroll
+  for (int i = 0; i < E; i += 2) *reinterpret_cast<uint32_t*>(dst + i) = l == 0.f ? 0u : pack_bf16(o[i] * inv, o[i + 1] * inv);
+}
+
+// Bytes of workspace: where the longest lengths that the sizes allow would give each block more than the least share.
+template <int D, int TILES>
+int64_t many_bytes(const AttendParams& a) {
+  const int64_t blocks = ((int64_t)a.part_rows + TILES * kRows - 1) / (TILES * kRows) * a.c.n_kv_heads * a.c.batch;
+  int64_t tokens = (int64_t)a.c.max_pages << a.c.page_shift;
+  if (a.window > 0) tokens = std::min<int64_t>(tokens, (int64_t)a.window + TILES * kRows / a.group + a.sinks + 2 * kTok);
+  if (blocks * (tokens / kTok + 1 + kUnitCost) < (int64_t)kMinShare * kSms) return 0;
+  return kRecordBytes + 2 * kSms * part_floats(D, TILES) * 4;
 }
 
 template <int D, int BITS, int TILES>
-cudaError_t launch(const AttendParams& a, cudaStream_t st) {
+cudaError_t launch(AttendParams a, cudaStream_t st) {
   using C = Cfg<D, BITS, TILES>;
   PageMaps maps;
   if (make_page_maps(a.c, D, BITS, std::min(a.c.page_size, BITS == 16 ? kTok : kTok / 2), &maps)) return cudaErrorInvalidValue;
   auto* f = k_attend_many<D, BITS, TILES>;
   static std::atomic<uint64_t> prepared{0};
-  const cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(f), C::kBytes, &prepared);
+  cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(f), C::kBytes, &prepared);
   if (e != cudaSuccess) return e;
-  const int64_t rows = (int64_t)a.c.max_q * a.group;
-  const int64_t q_blocks = (rows + TILES * kRows - 1) / (TILES * kRows);
-  const int64_t blocks = q_blocks * a.c.n_kv_heads * a.c.batch;
-  int64_t tokens = (int64_t)a.c.max_pages << a.c.page_shift;
-  if (a.window > 0) tokens = std::min<int64_t>(tokens, (int64_t)a.window + TILES * kRows / a.group + a.sinks + 2 * kTok);
-  // Few rows: the tokens are split until there are blocks for every SM; several sequences, whose lengths may differ, until
-  // each SM has about three.
-  const int64_t want = a.c.batch > 1 && TILES == 1 ? 3 * kSms : kSms;
-  int splits = 1;
-  while (splits < 8 && 2 * splits * blocks <= want && splits * 8 * kTok <= tokens) splits *= 2;
-  if (splits * q_blocks * a.c.n_kv_heads > 0x7fffffff || rows > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  return launch_cluster(f, dim3((unsigned)(splits * q_blocks * a.c.n_kv_heads), a.c.batch), C::kThreads, C::kBytes, splits, st, a, maps, (int)q_blocks, splits);
+  const int64_t bytes = many_bytes<D, TILES>(a);
+  if (bytes == 0 || bytes > a.part_bytes) a.part = nullptr;
+  e = launch_cluster(f, dim3(kSms), C::kThreads, C::kBytes, 1, st, a, maps);
+  if (e != cudaSuccess || !a.part) return e;
+  return launch_after(k_attend_many_join<D, BITS, TILES>, dim3(kSms, TILES * kRows / 8), 256, st, a);
 }
 
 template <int D, int BITS>
 cudaError_t launch_rows(const AttendParams& a, cudaStream_t st) {
-  return (int64_t)a.c.max_q * a.group <= kRows ? launch<D, BITS, 1>(a, st) : launch<D, BITS, 2>(a, st);
+  return a.part_rows <= kRows ? launch<D, BITS, 1>(a, st) : launch<D, BITS, 2>(a, st);
 }
 
 }  // namespace
@@ -744,6 +1055,11 @@ cudaError_t launch_rows(const AttendParams& a, cudaStream_t st) {
 cudaError_t launch_attend_many(const AttendParams& a, int head_dim, int kv_bits, cudaStream_t st) {
   if (head_dim == 128) return kv_bits == 16 ? launch_rows<128, 16>(a, st) : launch_rows<128, 8>(a, st);
   return kv_bits == 16 ? launch_rows<64, 16>(a, st) : launch_rows<64, 8>(a, st);
+}
+
+int64_t attend_many_bytes(const AttendParams& a, int head_dim) {
+  if (head_dim == 128) return a.part_rows <= kRows ? many_bytes<128, 1>(a) : many_bytes<128, 2>(a);
+  return a.part_rows <= kRows ? many_bytes<64, 1>(a) : many_bytes<64, 2>(a);
 }
 
 }  // namespace clo

@@ -456,6 +456,78 @@ def test_attention_scale_strides_stream_and_untouched_rows(clo):
         assert bool((wide[c.total:] == 7.0).all()) and bool((wide[..., d:] == 7.0).all())
 
 
+def dense_on_device(c, q, window=0, sinks=0):
+    """Attention of a Case in fp64 on the device, a (sequence, kv head) at a time: for sizes beyond the loops of paged_ref."""
+    out = torch.zeros(q.shape, dtype=torch.float64, device="cuda")
+    spread, reach = torch.zeros_like(out), torch.zeros(*q.shape[:2], 1, dtype=torch.float64, device="cuda")
+    group, d = q.shape[1] // c.hkv, c.d
+    vals = [v.cuda() if s is None else v.cuda() * s.double().cuda()[:, :, None, None] for v, s in zip(c.pages.val, c.scales)]
+    qd = q.double().cuda()
+    for b, (first, n, kv) in enumerate(c.seqs):
+        if n == 0:
+            continue
+        ids = c.table[b, :-(-kv // c.page)].long().cuda()
+        j = torch.arange(kv, device="cuda")
+        p = torch.arange(kv - n, kv, device="cuda")[:, None]
+        see = j <= p
+        if window:
+            see &= (j > p - window) | (j < sinks)
+        for h in range(c.hkv):
+            k, v = (x[ids, h].reshape(-1, d)[:kv] for x in vals)
+            for g in range(group):
+                x = qd[first:first + n, h * group + g]
+                w = torch.softmax((x @ k.T / math.sqrt(d)).masked_fill(~see, -math.inf), -1)
+                out[first:first + n, h * group + g] = w @ v
+                spread[first:first + n, h * group + g] = w @ v.abs()
+                reach[first:first + n, h * group + g] = ((x.abs() @ k.abs().T) * see).amax(-1, keepdim=True) / math.sqrt(d)
+    return out.cpu(), spread.cpu(), reach.cpu()
+
+
+# Sizes at which the units of rows are more than the SMs (several to a block), are cut between blocks, or are split over
+# blocks and joined; lengths of everything from one token on.
+LARGE = [
+    # seqs, hkv, group, d, page, bits, window, sinks
+    ([(n, n + 7 * n % 90) for n in range(33, 63)], 6, 3, 64, 32, 16, 0, 0),
+    ([(n, n + 7 * n % 90) for n in range(33, 63)], 6, 3, 64, 32, 8, 0, 0),
+    ([(n, n + 300) for n in range(100, 126)], 7, 2, 128, 64, 16, 0, 0),
+    ([(n, n + 300) for n in range(100, 126)], 7, 2, 128, 64, 8, 0, 0),
+    ([(700, 900), (1, 3000), (300, 300), (0, 50), (1500, 4000)], 4, 4, 128, 64, 16, 0, 0),
+    ([(700, 900), (1, 3000), (300, 300), (0, 50), (1500, 4000)], 4, 4, 128, 64, 8, 0, 0),
+    ([(700, 900), (64, 3000), (300, 300), (1500, 4000)], 4, 4, 64, 16, 8, 400, 20),
+    ([(700, 900), (64, 3000), (300, 300), (1500, 4000)], 4, 4, 64, 16, 16, 400, 20),
+    ([(20, 21000)], 8, 4, 128, 64, 16, 0, 0),
+    ([(20, 21000)], 8, 4, 128, 64, 8, 0, 0),
+    ([(30, 20000), (5, 700), (17, 9000)], 8, 4, 64, 128, 8, 0, 0),
+    ([(30, 20000), (5, 700), (17, 9000)], 8, 4, 64, 128, 16, 0, 0),
+    ([(200, 9000), (130, 130)], 8, 8, 128, 32, 8, 0, 0),
+    ([(200, 9000), (130, 130)], 8, 8, 128, 32, 16, 3000, 100),
+    ([(1, 40000)], 3, 5, 128, 64, 8, 0, 0),
+    ([(1, 40000), (1, 20)], 2, 16, 128, 64, 16, 0, 0),
+    ([(3, 30000), (2, 1)], 4, 4, 64, 16, 16, 0, 0),
+    ([(1, 5 + 37 * i) for i in range(70)], 4, 4, 128, 32, 8, 0, 0),
+]
+
+
+@pytest.mark.parametrize("case", range(len(LARGE)))
+def test_attention_at_sizes_that_share_the_gpu(clo, case):
+    seqs, hkv, group, d, page, bits, window, sinks = LARGE[case]
+    seqs = [(n, max(n, kv)) for n, kv in seqs]
+    c = Case(clo, seqs, hkv, d, page, bits, seed=200 + case)
+    c.device()
+    q = bf16(rand(300 + case, c.total, hkv * group, d) * 2)
+    want, spread, reach = dense_on_device(c, q, window, sinks)
+    bound = ref.attention_bound(want, spread, reach, d, bits)
+    check(c.attend(q, window, sinks), want, bound)
+    # without a workspace (one that is too small is none), and again with one that holds garbage
+    check(c.attend(q, window, sinks, workspace=torch.empty(16, dtype=torch.uint8, device="cuda")), want, bound, "no workspace")
+    size = c.cache.attention_workspace(hkv * group, len(seqs), c.total, c.tab.shape[1], c.max_q, window, sinks)
+    work = torch.full((size + 64,), 0xff, dtype=torch.uint8, device="cuda")
+    first = c.attend(q, window, sinks, workspace=work)
+    check(first, want, bound, "given workspace")
+    assert bool((work[size:] == 0xff).all()), "written past the workspace"
+    assert torch.equal(first, c.attend(q, window, sinks, workspace=work)), "two runs differ"
+
+
 def test_attention_offsets_past_32_bits(clo):
     # pages whose element offsets pass 2^32: few tokens, far apart
     d, page, hkv = 128, 128, 1
