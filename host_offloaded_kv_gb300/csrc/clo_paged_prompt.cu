@@ -38,7 +38,7 @@ namespace {
 constexpr int kTok = 128;    // tokens per tile
 constexpr int kRows = 128;   // rows per row tile
 constexpr float kGrow = 8.f;
-constexpr int kUnitCost = 2;   // what a unit costs beside its token tiles, in tiles
+constexpr int kUnitCost = 4;   // what a unit costs beside its token tiles, in tiles (11,000 cycles of 2,800)
 constexpr int kMinShare = 8;   // no cuts below this share per block: joining costs about as much as four tiles
 
 // ---------------------------------------------------------------------------- tcgen05
@@ -172,6 +172,27 @@ __device__ __forceinline__ bool wait(S& sh, uint64_t* bar, uint32_t parity) {
   }
   return false;
 }
+
+// Steps a pointer through a unit's rows, head by head and token by token.
+template <typename T>
+struct RowPtr {
+  T* p;
+  int h, group;
+  int64_t head, wrap;
+  __device__ __forceinline__ RowPtr(const AttendParams& a, T* base, int first, int kvh, int row, int64_t stride_token, int64_t stride_head) {
+    group = a.group;
+    head = stride_head;
+    wrap = stride_token - (int64_t)(group - 1) * stride_head;
+    const int t = token_of_row(a, row);
+    h = row - t * group;
+    p = base + (int64_t)(first + t) * stride_token + (int64_t)(kvh * group + h) * stride_head;
+  }
+  __device__ __forceinline__ void next() {
+    const bool last = ++h == group;
+    p += last ? wrap : head;
+    if (last) h = 0;
+  }
+};
 
 // A unit and the block's part of it.
 struct Unit {
@@ -470,16 +491,19 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
     // largest finite element into [2^14, 2^15).
     if (n > 0) asm volatile("bar.sync 1, 256;" ::: "memory");  // both lanes have left the last unit's Q
     if (n > 0 && ok) {
-      constexpr int kLanes = D / 8, kStepRows = 256 / kLanes, kIters = TILES * kRows / kStepRows;
-      const int c = tid % kLanes;
-#pragma unroll 1
+      // a thread takes one 16-byte chunk of kIters rows that follow one another
+      constexpr int kLanes = D / 8, kIters = TILES * kRows * kLanes / 256;
+      const int c = tid % kLanes, r0 = tid / kLanes * kIters;
+      RowPtr<const uint16_t> src(a, a.q + c * 8, s.first, kvh, row0 + r0, a.q_token, a.q_head);
+      uint8_t* const to = generic + (r0 / kRows * C::kQBytes + c / 8 * kRows * 128 + r0 % kRows * 128);
+#pragma unroll 2
       for (int i = 0; i < kIters; ++i) {
-        const int r = i * kStepRows + tid / kLanes, gr = row0 + r;
-        uint8_t* to = generic + (swizzled<128>(q_smem + r / kRows * C::kQBytes, kRows, r % kRows, c) - smem);
-        if (gr < rows)
-          cp_async16(to, a.q + row_offset(a, s.first, kvh, gr, a.q_token, a.q_head) + c * 8);
+        uint4* at = reinterpret_cast<uint4*>(to + i * 128 + ((c ^ (r0 + i)) & 7) * 16);
+        if (row0 + r0 + i < rows)
+          cp_async16(at, src.p);
         else
-          *reinterpret_cast<uint4*>(to) = make_uint4(0, 0, 0, 0);
+          *at = make_uint4(0, 0, 0, 0);
+        src.next();
       }
       cp_async_commit();
       cp_async_wait<0>();
@@ -487,8 +511,8 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
         __syncwarp();
 #pragma unroll 1
         for (int i = 0; i < kIters; ++i) {
-          const int r = i * kStepRows + tid / kLanes;
-          uint4* at = reinterpret_cast<uint4*>(generic + (swizzled<128>(q_smem + r / kRows * C::kQBytes, kRows, r % kRows, c) - smem));
+          const int r = r0 + i;
+          uint4* at = reinterpret_cast<uint4*>(to + i * 128 + ((c ^ r) & 7) * 16);
           float x[8], mx = 0.f;
           unpack8(*at, x);
 #pragma unroll
@@ -693,12 +717,14 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
         if (full) {
           __syncwarp();
           constexpr int kLanes = D / 8;
+          const int r0 = (warp & 3) * 32 + lane / kLanes * kLanes, c = lane % kLanes;  // kLanes rows that follow one another
+          const uint8_t* from = generic + (my_tile * C::kQBytes + c / 8 * kRows * 128 + r0 * 128);
+          RowPtr<uint16_t> dst(a, a.out + c * 8, s.first, kvh, row0 + my_tile * kRows + r0, a.o_token, a.o_head);
 #pragma unroll 2
           for (int i = 0; i < kLanes; ++i) {
-            const int r = (warp & 3) * 32 + i * (32 / kLanes) + lane / kLanes, gr = row0 + my_tile * kRows + r;
-            if (gr < rows)
-              *(reinterpret_cast<uint4*>(a.out + row_offset(a, s.first, kvh, gr, a.o_token, a.o_head)) + lane % kLanes) =
-                  *reinterpret_cast<const uint4*>(generic + (swizzled<128>(q_smem + my_tile * C::kQBytes, kRows, r, lane % kLanes) - smem));
+            if (row0 + my_tile * kRows + r0 + i < rows)
+              *reinterpret_cast<uint4*>(dst.p) = *reinterpret_cast<const uint4*>(from + i * 128 + ((c ^ (r0 + i)) & 7) * 16);
+            dst.next();
           }
           __syncwarp();
           unsigned again = __ballot_sync(0xffffffffu, row_ok && odd != 0.f);
