@@ -2,6 +2,8 @@
 
 * ``_lib/libclo.so``       the CUDA library behind the C ABI (``include/clo.h``),
                              compiled for sm_103a only;
+* ``_lib/_clo_torch-<torch version>.so``  the compiled part of the Python binding, for
+                             torch tensors (host C++ only; left out where torch is missing);
 * ``synth/libclo_synth.so`` the seeded input generator (plain C).
 
 Each translation unit is compiled in parallel and relinked only when a source
@@ -14,12 +16,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIBDIR = os.path.join(PKG, "_lib")
 CLO_LIB = os.path.join(LIBDIR, "libclo.so")
+TORCH_SRC = os.path.join(CSRC, "clo_torch.cpp")
 SYNTH_SRC = os.path.join(PKG, "synth", "synth.c")
 SYNTH_LIB = os.path.join(PKG, "synth", "libclo_synth.so")
 
@@ -91,6 +95,35 @@ def build_clo(force: bool = False, extra_flags=None) -> str:
     return CLO_LIB
 
 
+def torch_lib(version: str) -> str:
+    """The binding's file for a torch version (its C++ interface changes with it)."""
+    return os.path.join(LIBDIR, f"_clo_torch-{version}.so")
+
+
+def build_torch(force: bool = False) -> str | None:
+    """The binding for torch tensors; None where torch is not installed.  Needs libclo.so."""
+    try:
+        import torch
+    except ImportError:
+        return None
+    root = os.path.dirname(torch.__file__)
+    target = torch_lib(torch.__version__)
+    if not (force or _stale(target, [TORCH_SRC, CLO_LIB, os.path.join(ROOT, "include", "clo.h")])):
+        return target
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(cuda, "include"), os.path.join(ROOT, "include")]
+    lib = os.path.join(root, "lib")
+    tmp = target + ".tmp"
+    _run_parallel([[os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+                    f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", TORCH_SRC, "-o", tmp,
+                    *(f"-I{d}" for d in inc), f"-L{lib}", "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda",
+                    "-lc10", f"-Wl,-rpath,{lib}", f"-L{LIBDIR}", "-lclo", "-Wl,-rpath,$ORIGIN"]])
+    os.replace(tmp, target)
+    return target
+
+
 def build_all(force: bool = False) -> None:
     build_synth(force)
     build_clo(force)
+    build_torch(force)

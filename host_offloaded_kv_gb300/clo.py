@@ -1,7 +1,8 @@
 """Python binding of the CLO C ABI (``include/clo.h``): argument marshalling only.
 
 The functions carry the C names; every step of the decode path runs in the CUDA
-library ``_lib/libclo.so``.  There is no fallback: if the library is missing or
+library ``_lib/libclo.so``.  The calls on a paged cache, made once per layer and step, are
+marshalled by a compiled module beside it.  There is no fallback: if the library is missing or
 fails to load, every call raises.
 """
 from __future__ import annotations
@@ -327,86 +328,29 @@ def clo_rope_plan_init(cfg: clo_rope_config | None = None, **fields) -> clo_rope
 _ROPE_FIELDS = {n for n, _ in clo_rope_config._fields_}
 
 
-# The calls below run once per layer and step, so their checks are straight-line: what is right costs a few attribute
-# reads, what is wrong is named by the slower functions.  torch is imported with the first of them.
-torch = None
-_BF16 = _INT32 = _INT64 = None
-_byref = ctypes.byref
+_torch_binding = None
 
 
-def _load_torch() -> None:
-    global torch, _BF16, _INT32, _INT64
-    import torch as module
+def _fast():
+    """The compiled binding for torch tensors (csrc/clo_torch.cpp): checks, new outputs, marshalling."""
+    global _torch_binding
+    if _torch_binding is None:
+        import importlib.machinery
+        import importlib.util
 
-    module.cuda.current_device()  # raises where there is no GPU
-    load_library()
-    torch, _BF16, _INT32, _INT64 = module, module.bfloat16, module.int32, module.int64
+        import torch
 
+        from ._build import torch_lib
 
-def _device_of(t, name: str) -> int:
-    """Index of the current device, after checking that t is a tensor on it."""
-    if torch is None:
-        import torch as module
-
-        if not isinstance(t, module.Tensor) or not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        _load_torch()
-    dev = torch._C._cuda_getDevice()
-    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
-        _tensor_fault(t, name, dev, None)
-    return dev
-
-
-def _tensor_fault(t, name: str, dev: int, dtype) -> None:
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on {t.device}, not on the current device")
-    if dtype is not None and t.dtype is not dtype:
-        raise ValueError(f"{name} has dtype {t.dtype}; expected {dtype}")
-
-
-def _rows(t, name: str, dev: int, shape) -> clo_rows:
-    """A bf16 [n_tokens][n_heads][head_dim] tensor (any strides but the last) as the library takes it."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not _BF16 or t.get_device() != dev:
-        _tensor_fault(t, name, dev, _BF16)
-    if t.shape != shape or len(shape) != 3:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}; expected {tuple(shape) if len(shape) == 3 else '[n_tokens][n_heads][head_dim]'}")
-    st, sh, sd = t.stride()
-    if sd != 1 and shape[2] > 1:
-        raise ValueError(f"{name} must be contiguous along head_dim")
-    return clo_rows(t.data_ptr(), st, sh)
-
-
-def _new_rows(like):
-    """New rows of the shape of `like`, and as the library takes them."""
-    t = torch.empty_like(like)
-    st, sh, sd = t.stride()
-    if sd != 1:  # the layout of a transposed view
-        t = torch.empty(like.shape, dtype=_BF16, device=like.device)
-        st, sh, _ = t.stride()
-    return t, clo_rows(t.data_ptr(), st, sh)
-
-
-def _refuse_folded(t, name: str) -> None:
-    """Refuses an output whose rows lie on one another (expanded tensors)."""
-    if any(st == 0 and n > 1 for st, n in zip(t.stride(), t.shape)):
-        raise ValueError(f"{name} is written and must not be an expanded tensor")
-
-
-def _index(t, name: str, dev: int, dtype, numel: int):
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev:
-        _tensor_fault(t, name, dev, dtype)
-    if t.numel() != numel or not t.is_contiguous():
-        raise ValueError(f"{name} has shape {tuple(t.shape)}; expected a contiguous vector of {numel}")
-    return t.data_ptr()
-
-
-def _stream_of(stream, dev: int):
-    """A stream's handle; None is torch's current stream, an integer is passed through."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
-    return stream if isinstance(stream, int) else stream.cuda_stream
+        load_library()
+        path = torch_lib(torch.__version__)
+        if not os.path.exists(path):
+            raise RuntimeError(f"binding {path} is missing; build it with __graft_entry__.build()")
+        loader = importlib.machinery.ExtensionFileLoader("_clo_torch", path)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_clo_torch", loader))
+        loader.exec_module(module)
+        _torch_binding = module
+    return _torch_binding
 
 
 def clo_rope(plan: clo_rope_plan, x, positions, out=None, transpose: bool = False, stream=None):
@@ -414,23 +358,10 @@ def clo_rope(plan: clo_rope_plan, x, positions, out=None, transpose: bool = Fals
 
     out: rows of the same shape, x itself for in place, or None for new ones.  transpose applies the
     transposed rotation, which takes the gradient of the output to that of x.  Returns out."""
-    dev = _device_of(x, "x")
-    shape = x.shape
-    xr = _rows(x, "x", dev, shape)
-    n, h, d = shape
-    if out is None:
-        out, yr = _new_rows(x)
-    else:
-        _refuse_folded(out, "out")
-        yr = _rows(out, "out", dev, shape)
-    status = _lib.clo_rope(_byref(plan), _byref(xr), _byref(yr), _index(positions, "positions", dev, _INT64, n), n, h, d,
-                           1 if transpose else 0, _stream_of(stream, dev))
-    if status:
-        _check(status, "clo_rope")
-    return out
-
-
-_WORKSPACE_TOKENS = 2048  # a workspace for shorter tables would gain nothing that it costs
+    r = (_torch_binding or _fast()).rope(ctypes.addressof(plan), x, positions, out, transpose, stream)
+    if type(r) is int:
+        _check(r, "clo_rope")
+    return r
 
 
 class PagedCache:
@@ -446,9 +377,17 @@ class PagedCache:
     torch's current stream."""
 
     def __init__(self, k_pages, v_pages, k_scales=None, v_scales=None):
-        load_library()
-        self.device = _device_of(k_pages, "k_pages")
-        _device_of(v_pages, "v_pages")
+        import torch
+
+        for name, t in (("k_pages", k_pages), ("v_pages", v_pages), ("k_scales", k_scales), ("v_scales", v_scales)):
+            if name.endswith("scales") and t is None:
+                continue
+            if not isinstance(t, torch.Tensor) or not t.is_cuda:
+                raise ValueError(f"{name} must be a CUDA tensor")
+            if t.get_device() != torch.cuda.current_device():
+                raise ValueError(f"{name} is on {t.device}, not on the current device")
+        _fast()
+        self.device = k_pages.get_device()
         if k_pages.dtype not in (torch.bfloat16, torch.float8_e4m3fn) or v_pages.dtype is not k_pages.dtype:
             raise ValueError(f"pages have dtypes {k_pages.dtype}, {v_pages.dtype}; expected bfloat16 or float8_e4m3fn for both")
         if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
@@ -462,7 +401,6 @@ class PagedCache:
             if (t is None) != (bits == 16):
                 raise ValueError("8-bit pages come with k_scales and v_scales, bf16 pages without")
             if t is not None:
-                _device_of(t, name)
                 if t.dtype is not torch.float32 or tuple(t.shape) != (n, h) or not t.is_contiguous():
                     raise ValueError(f"{name} must be a contiguous fp32 tensor of shape {(n, h)}")
         self.k_pages, self.v_pages, self.k_scales, self.v_scales = k_pages, v_pages, k_scales, v_scales
@@ -471,14 +409,15 @@ class PagedCache:
                                   None if v_scales is None else v_scales.data_ptr(), n, *k_pages.stride()[:3],
                                   *v_pages.stride()[:3], h, d, s, bits)
         self._ref = ctypes.byref(self._c)
+        self._address = ctypes.addressof(self._c)
 
     @classmethod
     def create(cls, n_pages: int, n_kv_heads: int, page_size: int, head_dim: int, kv_bits: int = 16, device=None):
         """A cache of new pages (their contents are undefined until they are appended to)."""
         if kv_bits not in (16, 8):
             raise ValueError("kv_bits must be 16 or 8")
-        if torch is None:
-            _load_torch()
+        import torch
+
         device = torch.device("cuda", torch.cuda.current_device()) if device is None else device
         shape = (n_pages, n_kv_heads, page_size, head_dim)
         if kv_bits == 16:
@@ -486,120 +425,42 @@ class PagedCache:
         return cls(*(torch.empty(shape, dtype=torch.float8_e4m3fn, device=device) for _ in range(2)),
                    *(torch.ones((n_pages, n_kv_heads), dtype=torch.float32, device=device) for _ in range(2)))
 
-    def _batch(self, dev, q_starts, kv_lens, block_table, total: int, max_q) -> clo_paged_batch:
-        if dev != self.device:
-            raise ValueError(f"the cache is on device {self.device}, the call's rows on {dev}")
-        if not isinstance(block_table, torch.Tensor) or block_table.dtype is not _INT32 or block_table.get_device() != dev:
-            _tensor_fault(block_table, "block_table", dev, _INT32)
-        if block_table.dim() != 2:
-            raise ValueError(f"block_table has shape {tuple(block_table.shape)}; expected [batch][max_pages]")
-        batch, width = block_table.shape
-        stride, inner = block_table.stride()
-        if inner != 1 and width > 1:
-            raise ValueError("block_table must have contiguous rows")
-        return clo_paged_batch(_index(q_starts, "q_starts", dev, _INT32, batch + 1), _index(kv_lens, "kv_lens", dev, _INT32, batch),
-                               block_table.data_ptr(), stride, width, batch, total, total if max_q is None else max_q)
-
     def append(self, k, v, q_starts, kv_lens, block_table, rope: clo_rope_plan | None = None, positions=None, q=None,
                q_out=None, max_q=None, stream=None):
         """clo_paged_append: k, v bf16 [total][n_kv_heads][head_dim] into the pages, k rotated by rope; with
         q, returns the rotated queries (q_out, or new rows)."""
-        dev = _device_of(k, "k")
-        total = k.shape[0]
-        shape = (total, self.n_kv_heads, self.head_dim)
-        kr = _rows(k, "k", dev, shape)
-        vr = _rows(v, "v", dev, shape)
-        b = self._batch(dev, q_starts, kv_lens, block_table, total, max_q)
-        qr = yr = None
-        heads = 0
-        if q is not None:
-            shape = q.shape
-            qr = _byref(_rows(q, "q", dev, shape))
-            heads = shape[1]
-            if shape[0] != total or shape[2] != self.head_dim:
-                raise ValueError(f"q has shape {tuple(shape)}; expected [{total}][n_q_heads][{self.head_dim}]")
-            if q_out is None:
-                q_out, yr = _new_rows(q)
-            else:
-                _refuse_folded(q_out, "q_out")
-                yr = _rows(q_out, "q_out", dev, shape)
-            yr = _byref(yr)
-        elif q_out is not None:
-            raise ValueError("q_out without q")
-        status = _lib.clo_paged_append(
-            self._ref, _byref(b), None if rope is None else _byref(rope),
-            None if positions is None else _index(positions, "positions", dev, _INT64, total), _byref(kr), _byref(vr),
-            qr, yr, heads, _stream_of(stream, dev))
-        if status:
-            _check(status, "clo_paged_append")
-        return q_out
+        r = _torch_binding.append(self._address, self.device, k, v, q_starts, kv_lens, block_table,
+                                  0 if rope is None else ctypes.addressof(rope), positions, q, q_out, max_q, stream)
+        if type(r) is int:
+            _check(r, "clo_paged_append")
+        return r
 
     def read(self, q_starts, kv_lens, block_table, total: int, k_out=None, v_out=None, max_q=None, stream=None):
         """clo_paged_read: the batch's last tokens as bf16 (k, v), each [total][n_kv_heads][head_dim]."""
-        dev = _device_of(kv_lens, "kv_lens")
-        shape = (total, self.n_kv_heads, self.head_dim)
-        if k_out is None:
-            k_out = torch.empty(shape, dtype=_BF16, device=kv_lens.device)
-            kr = clo_rows(k_out.data_ptr(), shape[1] * shape[2], shape[2])
-        else:
-            _refuse_folded(k_out, "k_out")
-            kr = _rows(k_out, "k_out", dev, shape)
-        if v_out is None:
-            v_out, vr = _new_rows(k_out)
-        else:
-            _refuse_folded(v_out, "v_out")
-            vr = _rows(v_out, "v_out", dev, shape)
-        b = self._batch(dev, q_starts, kv_lens, block_table, total, max_q)
-        status = _lib.clo_paged_read(self._ref, _byref(b), _byref(kr), _byref(vr), _stream_of(stream, dev))
-        if status:
-            _check(status, "clo_paged_read")
-        return k_out, v_out
-
-    def _workspace(self, b: clo_paged_batch, heads: int, window: int, sinks: int) -> int:
-        size = ctypes.c_int64()
-        _check(_lib.clo_paged_attention_workspace(self._ref, ctypes.byref(b), heads, window, sinks, ctypes.byref(size)),
-               "clo_paged_attention_workspace")
-        return size.value
+        r = _torch_binding.read(self._address, self.device, q_starts, kv_lens, block_table, total, k_out, v_out, max_q, stream)
+        if type(r) is int:
+            _check(r, "clo_paged_read")
+        return r
 
     def attention_workspace(self, n_q_heads: int, batch: int, total: int, max_pages: int, max_q=None, window: int = 0,
                             sinks: int = 0) -> int:
         """Bytes of workspace that attention of these sizes uses (0: none)."""
         b = clo_paged_batch(1 << 20, 1 << 20, 1 << 20, max_pages, max_pages, batch, total, total if max_q is None else max_q)
-        return self._workspace(b, n_q_heads, window, sinks)
+        size = ctypes.c_int64()
+        _check(_lib.clo_paged_attention_workspace(self._ref, ctypes.byref(b), n_q_heads, window, sinks, ctypes.byref(size)),
+               "clo_paged_attention_workspace")
+        return size.value
 
     def attention(self, q, q_starts, kv_lens, block_table, out=None, max_q=None, softmax_scale: float = 0.0, window: int = 0,
                   sinks: int = 0, workspace=None, stream=None):
         """clo_paged_attention: q bf16 [total][n_q_heads][head_dim] over the pages; returns out (or new rows).
 
         workspace: uint8 tensor of attention_workspace() bytes, or None: allocated where the sizes ask for one."""
-        dev = _device_of(q, "q")
-        shape = q.shape
-        qr = _rows(q, "q", dev, shape)
-        total, heads, d = shape
-        if d != self.head_dim:
-            raise ValueError(f"q has head_dim {d}; the cache has {self.head_dim}")
-        if out is None:
-            out, orow = _new_rows(q)
-        else:
-            _refuse_folded(out, "out")
-            orow = _rows(out, "out", dev, shape)
-        b = self._batch(dev, q_starts, kv_lens, block_table, total, max_q)
-        work, size = None, 0
-        if workspace is None and (total >= 512 or b.max_pages * self.page_size >= _WORKSPACE_TOKENS):
-            size = self._workspace(b, heads, window, sinks)
-            if size:
-                workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
-                if stream is not None:  # not the allocator's stream: it has to know who uses the memory
-                    handle = _stream_of(stream, dev)
-                    workspace.record_stream(torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev))
-        if workspace is not None:
-            size = workspace.numel()
-            work = _index(workspace, "workspace", dev, torch.uint8, size)
-        status = _lib.clo_paged_attention(self._ref, _byref(b), _byref(qr), _byref(orow), heads, softmax_scale, window, sinks, work,
-                                          size, _stream_of(stream, dev))
-        if status:
-            _check(status, "clo_paged_attention")
-        return out
+        r = _torch_binding.attention(self._address, self.device, q, q_starts, kv_lens, block_table, out, max_q, softmax_scale,
+                                     window, sinks, workspace, stream)
+        if type(r) is int:
+            _check(r, "clo_paged_attention")
+        return r
 
 
 def clo_paged_attention_workspace(cache: PagedCache, *args, **kwargs) -> int:
