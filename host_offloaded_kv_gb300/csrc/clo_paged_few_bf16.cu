@@ -6,9 +6,9 @@ namespace clo {
 cudaError_t launch_attend_few_bf16(const AttendParams& a, int head_dim, cudaStream_t st) { return few<16>(a, head_dim, nullptr, st); }
 
 int64_t attend_few_bf16_bytes(const AttendParams& a, int head_dim) {
-  FewPlan p{};
-  few<16>(a, head_dim, &p, nullptr);
-  return p.bytes;
+  int64_t bytes = 0;
+  few<16>(a, head_dim, &bytes, nullptr);
+  return bytes;
 }
 
 }  // namespace clo

@@ -254,11 +254,6 @@ __device__ __forceinline__ int64_t seq_cost(const AttendParams& a, const SeqRows
   }
   return c;
 }
-__device__ __forceinline__ int64_t warp_sum64(int64_t v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
 __device__ __forceinline__ SeqRows shfl_seq(const SeqRows& s, int from) {
   SeqRows r;
   r.first = __shfl_sync(0xffffffffu, s.first, from);
@@ -359,20 +354,6 @@ __device__ void find_share(const AttendParams& a, int lane, S& sh) {
       if (total * (blockIdx.x + 1) / gridDim.x == share) return;
     }
   }
-}
-
-// Workspace: a record per block, then two parts per block (slot 0: a unit that it ends or passes through, slot 1: one that it begins),
-// each [row][D elements, maximum, sum, -, -].
-struct PartRecord {
-  int valid, b, qb, kvh;
-  int last;  // the unit's parts are this block's slot 1 and slot 0 of the following ones up to `last`
-  int pad[3];
-};
-constexpr int kRecordBytes = 8192;
-static_assert(kSms * sizeof(PartRecord) <= kRecordBytes, "records fit");
-__host__ __device__ constexpr int64_t part_floats(int d, int tiles) { return (int64_t)tiles * kRows * (d + 4); }
-__device__ __forceinline__ float* part_of(const AttendParams& a, int block, int slot, int d, int tiles) {
-  return a.part + kRecordBytes / 4 + (2 * (int64_t)block + slot) * part_floats(d, tiles);
 }
 
 template <int D, int BITS, int TILES>
@@ -481,11 +462,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
       record.b = u.b;
       record.qb = u.qb;
       record.kvh = kvh;
-      const int64_t end = base + u.all + kUnitCost;
-      int c = (int)min(end * gridDim.x / sh.total, (int64_t)gridDim.x - 1);
-      while (sh.total * c / gridDim.x >= end) --c;
-      while (sh.total * (c + 1) / gridDim.x < end) ++c;
-      record.last = c;
+      record.last = last_block(sh.total, gridDim.x, base + u.all + kUnitCost);
     }
     // Q rows into operand tiles, D / 8 threads per row.  8-bit pages: fp16, each row scaled by a power of two that puts its
     // largest finite element into [2^14, 2^15).
@@ -676,7 +653,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
         const float inv = full ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
         float* part = nullptr;
         if (!full) {
-          part = part_of(a, blockIdx.x, u.t_begin == 0 ? 1 : 0, D, TILES) + (int64_t)(my_tile * kRows + (tid & 127)) * (D + 4);
+          part = part_of(a, blockIdx.x, u.t_begin == 0 ? 1 : 0, TILES * kRows, D) + (int64_t)(my_tile * kRows + (tid & 127)) * (D + 4);
           *reinterpret_cast<float2*>(part + D) = make_float2(ref, l);
         }
         float odd = l * 0.f;  // NaN if anything in the row is no finite number
@@ -1012,7 +989,7 @@ __global__ void __launch_bounds__(256) k_attend_many_join(const AttendParams a) 
   if (gr >= s.n * a.group) return;
   constexpr int E = D / 32;
   const int64_t row = (int64_t)r * (D + 4);
-  auto part = [&](int c) { return part_of(a, c, c == (int)blockIdx.x ? 1 : 0, D, TILES) + row; };
+  auto part = [&](int c) { return part_of(a, c, c == (int)blockIdx.x ? 1 : 0, TILES * kRows, D) + row; };
   float mx = -INFINITY;
   for (int c = blockIdx.x + lane; c <= rec.last; c += 32) mx = fmaxf(mx, part(c)[D]);
   mx = warp_max(mx);
@@ -1052,7 +1029,7 @@ int64_t many_bytes(const AttendParams& a) {
   int64_t tokens = (int64_t)a.c.max_pages << a.c.page_shift;
   if (a.window > 0) tokens = std::min<int64_t>(tokens, (int64_t)a.window + TILES * kRows / a.group + a.sinks + 2 * kTok);
   if (blocks * (tokens / kTok + 1 + kUnitCost) < (int64_t)kMinShare * kSms) return 0;
-  return kRecordBytes + 2 * kSms * part_floats(D, TILES) * 4;
+  return part_bytes(kSms, TILES * kRows, D);
 }
 
 template <int D, int BITS, int TILES>
@@ -1066,7 +1043,8 @@ cudaError_t launch(AttendParams a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int64_t bytes = many_bytes<D, TILES>(a);
   if (bytes == 0 || bytes > a.part_bytes) a.part = nullptr;
-  e = launch_cluster(f, dim3(kSms), C::kThreads, C::kBytes, 1, st, a, maps);
+  f<<<kSms, C::kThreads, C::kBytes, st>>>(a, maps);
+  e = cudaGetLastError();
   if (e != cudaSuccess || !a.part) return e;
   return launch_after(k_attend_many_join<D, BITS, TILES>, dim3(kSms, TILES * kRows / 8), 256, st, a);
 }
