@@ -161,8 +161,10 @@ __device__ __forceinline__ void rotate_heads(const Rope& r, const uint64_t* s_tu
   }
 }
 
-// Rounds of heads per warp: many for long calls, where the sines count, few for short ones, where the latency does.
-constexpr int kLongIters = 8, kShortIters = 2;
+// Rounds of heads per warp: many for long calls, where the sines count, few for short ones, where the latency does, and no more
+// than the heads fill.  8192 tokens of 128-element heads, us with 8 / 4 / 2 rounds: 8 heads (floor 5.0) 11.0 / - / 7.5, 16 heads (9.9)
+// 13.0 / 10.7 / -, 40 heads (24.7) 33.6 / 30.4 / -; 2000 tokens, 32 heads (4.8) 6.3 / 7.1 / -.
+constexpr int kLongIters = 8, kMidIters = 4, kShortIters = 2;
 constexpr int64_t kLongTokens = 8 * 152;  // a warp per SM and slot of eight
 template <int D>
 __host__ __device__ constexpr int heads_per_warp(int iters) { return iters * 32 / (D / 16); }
@@ -578,13 +580,14 @@ extern "C" CLO_API clo_status clo_rope(const clo_rope_plan* plan, const clo_rows
   Rope r{*plan, transpose != 0};
   const bool vec = !rows_fault(x, true) && !rows_fault(y, true) && plan->rot_dim % 16 == 0 && (head_dim == 64 || head_dim == 128);
   if (vec) {
-    const int iters = n_tokens >= kLongTokens ? kLongIters : kShortIters;
-    const int per = iters * 32 / (head_dim / 16);  // heads per warp
+    const int rows = 32 / (head_dim / 16);  // heads per round
+    const int iters = n_tokens < kLongTokens || n_heads <= kShortIters * rows ? kShortIters : n_heads % (kLongIters * rows) ? kMidIters : kLongIters;
+    const int per = iters * rows;  // heads per warp
     const int chunks = (n_heads + per - 1) / per;
     const int64_t blocks = (n_tokens * chunks + kWarps - 1) / kWarps;
     if (blocks > 0x7fffffff) return paged_fail(CLO_ERR_INVALID, "%s: too many rows for one call", who);
-    auto* f = head_dim == 128 ? (iters == kLongIters ? k_rope<128, kLongIters> : k_rope<128, kShortIters>)
-                              : (iters == kLongIters ? k_rope<64, kLongIters> : k_rope<64, kShortIters>);
+    auto* f = head_dim == 128 ? (iters == kLongIters ? k_rope<128, kLongIters> : iters == kMidIters ? k_rope<128, kMidIters> : k_rope<128, kShortIters>)
+                              : (iters == kLongIters ? k_rope<64, kLongIters> : iters == kMidIters ? k_rope<64, kMidIters> : k_rope<64, kShortIters>);
     f<<<(unsigned)blocks, kThreads, 0, st>>>(r, rows_of(x), rows_of(y), positions, n_tokens, n_heads, chunks);
   } else {
     const int64_t pairs = n_tokens * n_heads * (head_dim - plan->rot_dim / 2);
