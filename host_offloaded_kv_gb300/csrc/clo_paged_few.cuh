@@ -173,9 +173,9 @@ __global__ void __launch_bounds__(kThreads) k_attend_few(const AttendParams a, c
 
   FewShare share{0, 1, 0, (int)blockIdx.x, (int)blockIdx.y};
   if (a.part) share = few_share(a, TOK, lane);
-  PartRecord record{};
   const bool by_unit = (int64_t)p.batch * p.n_kv_heads <= kWave;  // where a unit's record stands
   PartRecord* const records = reinterpret_cast<PartRecord*>(a.part);
+  if (tid == 0 && a.part && !by_unit) records[blockIdx.x].valid = 0;
   int st = 0;          // next stage, and its barrier's phase
   uint32_t phase = 0;
   int kvh = share.kvh, b = share.b;
@@ -210,10 +210,9 @@ __global__ void __launch_bounds__(kThreads) k_attend_few(const AttendParams a, c
       next(end);
       continue;
     }
-    if (a.part && t_begin == 0) {
+    if (tid == 0 && a.part && t_begin == 0) {
       const PartRecord r{!full, b, 0, kvh, full ? 0 : (int)((end - 1) / (share.last - share.first)), (int)blockIdx.x};
-      if (!by_unit && !full) record = r;
-      if (by_unit && tid == 0) records[b * p.n_kv_heads + kvh] = r;
+      if (by_unit || !full) records[by_unit ? b * p.n_kv_heads + kvh : blockIdx.x] = r;
     }
     constexpr int stride = kWarps;
     const int k0 = t_begin + warp, n_tiles = t_begin + n;
@@ -590,7 +589,6 @@ __global__ void __launch_bounds__(kThreads) k_attend_few(const AttendParams a, c
     if (tid == 0) s_odd = 0;
     __syncthreads();
   }
-  if (tid == 0 && a.part && !by_unit) records[blockIdx.x] = record;
 }
 
 // Joins the parts of the units that the cuts met: a block per record and row, D / 4 threads per slice of the parts.

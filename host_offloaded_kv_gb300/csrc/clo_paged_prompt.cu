@@ -39,7 +39,9 @@ constexpr int kTok = 128;    // tokens per tile
 constexpr int kRows = 128;   // rows per row tile
 constexpr float kGrow = 8.f;
 constexpr int kUnitCost = 4;   // what a unit costs beside its token tiles, in tiles (11,000 cycles of 2,800)
-constexpr int kMinShare = 8;   // no cuts below this share per block: joining costs about as much as four tiles
+// Least share where units are cut: joining costs about as much as four tiles.  Calls too small for all SMs cut only where a unit is
+// twice as long, into fewer shares; otherwise units stay whole, spread over the SMs.
+constexpr int kMinShare = 8;
 
 // ---------------------------------------------------------------------------- tcgen05
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -144,7 +146,7 @@ struct Cfg {
 template <int META, int TILES>
 struct Shared {
   uint64_t full[8], empty[8];      // operand tiles: filled (TMA or converters), products done
-  uint64_t tail[8], q_ready;       // bf16: a V tile whose end is yet to be cleared; Q
+  uint64_t tail[8], q_ready[2];      // bf16: a V tile whose end is yet to be cleared; Q
   uint64_t raw_full[12], raw_empty[12];  // 8-bit pages: halves of tiles on their way
   uint64_t s_full[2], p_half[2], p_ready[2];  // per lane: scores; weights of the first 64 tokens, of all
   uint64_t meta[META];
@@ -154,6 +156,8 @@ struct Shared {
   int failed;
   int64_t first, last, total;      // the block's share of the units' costs, [first, last) of total
   int64_t base;                    // where the first unit of the share begins
+  PartRecord record;               // of the unit that the share leaves unfinished
+  int blocks, cuts;                // blocks that take a share; whether units are cut
   int start[3];                    // that unit: sequence, block of rows, kv head
   float join_m[TILES == 1 ? kRows : 1], join_l[TILES == 1 ? kRows : 1];  // lane 1's maxima and sums
   int8_t q_exp[2][kRows];          // 8-bit pages: q rows are scaled by 2^-q_exp
@@ -242,7 +246,7 @@ __device__ __forceinline__ bool next_unit(const AttendParams& a, Unit* u) {
 
 // Cost of a sequence's units for one kv head: by one lane, or by a warp's lanes over its blocks of rows.
 template <int TILES>
-__device__ __forceinline__ int64_t seq_cost(const AttendParams& a, const SeqRows& s, int lane, int lanes) {
+__device__ __forceinline__ int64_t seq_cost(const AttendParams& a, const SeqRows& s, int lane, int lanes, int* most) {
   Unit u;
   u.s = s;
   u.rows = s.n * a.group;
@@ -251,6 +255,7 @@ __device__ __forceinline__ int64_t seq_cost(const AttendParams& a, const SeqRows
   for (u.qb = lane; u.qb < blocks; u.qb += lanes) {
     set_rows<TILES>(a, &u);
     c += u.all + kUnitCost;
+    *most = max(*most, u.all + kUnitCost);
   }
   return c;
 }
@@ -269,6 +274,7 @@ __device__ void find_share(const AttendParams& a, int lane, S& sh) {
   const PagedParams& p = a.c;
   const int heads = p.n_kv_heads;
   int64_t total = 0, share = 0;
+  int most = 0;  // the largest unit's cost
   // pass 0 adds everything up, pass 1 stops at the sequence that holds the share's begin
   for (int pass = 0; pass < 2; ++pass) {
     int64_t before = 0;
@@ -281,11 +287,11 @@ __device__ void find_share(const AttendParams& a, int lane, S& sh) {
       int64_t cost = 0;  // of this lane's sequence
       if (many) {
         for (int i = 0; i < count; ++i) {
-          const int64_t x = warp_sum64(seq_cost<TILES>(a, shfl_seq(mine, i), lane, 32));
+          const int64_t x = warp_sum64(seq_cost<TILES>(a, shfl_seq(mine, i), lane, 32, &most));
           if (lane == i) cost = x;
         }
       } else {
-        cost = seq_cost<TILES>(a, mine, 0, 1);
+        cost = seq_cost<TILES>(a, mine, 0, 1, &most);
       }
       cost *= heads;
       if (pass == 0) {
@@ -343,15 +349,21 @@ __device__ void find_share(const AttendParams& a, int lane, S& sh) {
       }
     }
     if (pass == 0) {
-      share = total * blockIdx.x / gridDim.x;
+      most = __reduce_max_sync(0xffffffffu, most);
+      const bool large = total >= (int64_t)kMinShare * gridDim.x, cuts = a.part && (large || most >= 2 * kMinShare);
+      const int blocks = cuts && !large ? max((int)(total / kMinShare), 1) : (int)gridDim.x;
+      share = total * min((int)blockIdx.x, blocks) / blocks;
+      const int64_t last = total * min((int)blockIdx.x + 1, blocks) / blocks;
       if (lane == 0) {
         sh.first = share;
-        sh.last = total * (blockIdx.x + 1) / gridDim.x;
+        sh.last = last;
         sh.total = total;
         sh.base = total;  // an empty share finds nothing
+        sh.blocks = blocks;
+        sh.cuts = cuts;
       }
       __syncwarp();
-      if (total * (blockIdx.x + 1) / gridDim.x == share) return;
+      if (last == share) return;
     }
   }
 }
@@ -386,7 +398,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
       mbar_init(&sh.p_half[i], 128);
       mbar_init(&sh.p_ready[i], 128);
     }
-    mbar_init(&sh.q_ready, 256);
+    for (int i = 0; i < TILES; ++i) mbar_init(&sh.q_ready[i], 256 / TILES);
     for (int i = 0; i < kMeta; ++i) mbar_init(&sh.meta[i], 1);
     sh.failed = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -405,7 +417,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
   constexpr uint32_t kS[2] = {0, 128}, kO[2] = {256, 384};
 
   // The block's walk over its units; every role takes it by itself.  `visit` is called with each unit that the block has a part of.
-  const bool cuts = a.part != nullptr && sh.total >= (int64_t)kMinShare * gridDim.x;
+  const bool cuts = sh.cuts;
   auto walk = [&](auto&& visit) {
     int64_t base = sh.base;
     const int64_t first = sh.first, last = sh.last;
@@ -452,25 +464,21 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
     uint32_t q_phase = 0, s_phase = 0;
     int tiles_done = 0;
     bool ok = true;
-    PartRecord record{};
+    if (tid == 0) sh.record.valid = 0;
     walk([&](const Unit& u, int64_t base) {
     const SeqRows& s = u.s;
     const int n = u.n, row0 = u.row0, rows = u.rows, kvh = u.kvh, mine = count_of(t, n);
     const bool full = n == u.all;
-    if (!full && u.t_begin == 0) {
-      record.valid = 1;
-      record.b = u.b;
-      record.qb = u.qb;
-      record.kvh = kvh;
-      record.last = last_block(sh.total, gridDim.x, base + u.all + kUnitCost);
-    }
+    if (tid == 0 && !full && u.t_begin == 0) sh.record = {1, u.b, u.qb, kvh, last_block(sh.total, sh.blocks, base + u.all + kUnitCost), (int)blockIdx.x};
     // Q rows into operand tiles, D / 8 threads per row.  8-bit pages: fp16, each row scaled by a power of two that puts its
     // largest finite element into [2^14, 2^15).
-    if (n > 0) asm volatile("bar.sync 1, 256;" ::: "memory");  // both lanes have left the last unit's Q
+    // Two row tiles: each lane loads its own, so that it need not wait for the other's end.
+    constexpr int kLoaders = TILES == 2 ? 128 : 256;
+    if (n > 0) asm volatile("bar.sync %0, %1;" ::"r"(1 + my_tile), "n"(kLoaders) : "memory");  // all have left the last unit's Q
     if (n > 0 && ok) {
       // a thread takes one 16-byte chunk of kIters rows that follow one another
-      constexpr int kLanes = D / 8, kIters = TILES * kRows * kLanes / 256;
-      const int c = tid % kLanes, r0 = tid / kLanes * kIters;
+      constexpr int kLanes = D / 8, kIters = kRows * kLanes / kLoaders;
+      const int c = tid % kLanes, r0 = my_tile * kRows + tid % kLoaders / kLanes * kIters;
       RowPtr<const uint16_t> src(a, a.q + c * 8, s.first, kvh, row0 + r0, a.q_token, a.q_head);
       uint8_t* const to = generic + (r0 / kRows * C::kQBytes + c / 8 * kRows * 128 + r0 % kRows * 128);
 #pragma unroll 2
@@ -503,13 +511,13 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
         }
       }
       fence_proxy_async_smem();
-      mbar_arrive(&sh.q_ready);
+      mbar_arrive(&sh.q_ready[my_tile]);
     }
     float ref = -INFINITY, l = 0.f;
     const int my_row = row0 + my_tile * kRows + (tid & 127);
     const bool row_ok = my_row < rows;
     if (n > 0) {
-      ok = ok && __all_sync(0xffffffffu, wait(sh, &sh.q_ready, q_phase));
+      ok = ok && __all_sync(0xffffffffu, wait(sh, &sh.q_ready[my_tile], q_phase));
       q_phase ^= 1u;
     }
     const float fac = BITS == 8 ? a.scale_log2 * __uint_as_float((uint32_t)(127 + sh.q_exp[my_tile][tid & 127]) << 23) : a.scale_log2;
@@ -637,7 +645,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
           sh.join_l[tid & 127] = l;
           tc_fence_before();
         }
-        asm volatile("bar.sync 2, 256;" ::: "memory");
+        asm volatile("bar.sync 3, 256;" ::: "memory");
         tc_fence_after();
       }
       if (TILES == 2 || t == 0) {
@@ -716,7 +724,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
     }
     return true;
     });
-    if (tid == 0 && a.part) *(reinterpret_cast<PartRecord*>(a.part) + blockIdx.x) = record;
+    if (tid == 0 && a.part) *(reinterpret_cast<PartRecord*>(a.part) + blockIdx.x) = sh.record;
   } else {
     if (warp == 8 || warp == 11) {
       // ---------------------------------------------------------------------- TMA: K and page data; V
@@ -837,18 +845,19 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
       walk([&](const Unit& u, int64_t) {
         const int n = u.n;
         if (n == 0) return true;
-        bool ok = wait(sh, &sh.q_ready, q_phase);
-        q_phase ^= 1u;
+        bool ok = true;
         for (int t = 0; t < 2 && ok; ++t) {
+          if (TILES == 2 || t == 0) ok = wait(sh, &sh.q_ready[t], q_phase);
           if (count_of(t, n) == 0) break;
           const int e = e_base + at_k(first_of(t));
-          ok = ready(e);
+          ok = ok && ready(e);
           if (!ok) break;
           tc_fence_after();
           score(t, e % SLOTS);
           tc_commit(&sh.s_full[t], leader);
           if (TILES == 1 || t == 1) tc_commit(&sh.empty[e % SLOTS], leader);
         }
+        q_phase ^= 1u;
         // V of tile j and K of the lane's next tile; looked at ahead of time, between two products' issue, where a wait
         // costs nothing
         bool ahead = false;
@@ -1022,13 +1031,14 @@ __global__ void __launch_bounds__(256) k_attend_many_join(const AttendParams a) 
   for (int i = 0; i < E; i += 2) *reinterpret_cast<uint32_t*>(dst + i) = l == 0.f ? 0u : pack_bf16(o[i] * inv, o[i + 1] * inv);
 }
 
-// Bytes of workspace: where the longest lengths that the sizes allow would give each block more than the least share.
+// Bytes of workspace: where the longest lengths that the sizes allow would have units cut.
 template <int D, int TILES>
 int64_t many_bytes(const AttendParams& a) {
   const int64_t blocks = ((int64_t)a.part_rows + TILES * kRows - 1) / (TILES * kRows) * a.c.n_kv_heads * a.c.batch;
   int64_t tokens = (int64_t)a.c.max_pages << a.c.page_shift;
   if (a.window > 0) tokens = std::min<int64_t>(tokens, (int64_t)a.window + TILES * kRows / a.group + a.sinks + 2 * kTok);
-  if (blocks * (tokens / kTok + 1 + kUnitCost) < (int64_t)kMinShare * kSms) return 0;
+  const int64_t most = tokens / kTok + 1 + kUnitCost;
+  if (most < 2 * kMinShare && blocks * most < (int64_t)kMinShare * kSms) return 0;
   return part_bytes(kSms, TILES * kRows, D);
 }
 
