@@ -13,7 +13,6 @@
 
 namespace clo {
 
-constexpr float kE4m3Max = 448.f;
 constexpr int kMinScaleExp = -64;
 constexpr float kMinScale = 1e-30f;   // smallest page scale that a reader uses
 constexpr int kMaxGroup = 16;         // query heads per kv head
@@ -246,29 +245,10 @@ __device__ __forceinline__ bool mbar_wait_limited(uint64_t* bar, uint32_t parity
   return false;
 }
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ float ld_cluster_f32(uint32_t smem_addr, uint32_t rank) {
-  float v;
-  asm volatile(
-      "{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
-      : "=f"(v)
-      : "r"(smem_addr), "r"(rank)
-      : "memory");
-  return v;
-}
-
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-
 
 }  // namespace clo

@@ -98,8 +98,8 @@ __device__ __forceinline__ TileList tiles_of(int pos_first, int pos_last, int kv
 constexpr int kSms = 152;  // GB300
 
 // ---------------------------------------------------------------------------- equal shares
-// All units' tiles of tokens, each unit with a constant cost beside them, lie end to end; block i of n takes [total i / n,
-// total (i + 1) / n).  A unit that a cut meets leaves one part per block in the caller's workspace: a record per block, then two
+// All units' tiles of tokens, each unit with a constant cost beside them, lie end to end and are cut into equal shares, one to a
+// block.  A unit that a cut meets leaves one part per block in the caller's workspace: a record per block, then two
 // parts per block (slot 1: of a unit that it begins, slot 0: of one that it ends or passes through), each [row][D elements, maximum,
 // sum, -, -].
 struct PartRecord {
@@ -116,20 +116,13 @@ inline int64_t part_bytes(int blocks, int rows, int d) { return kRecordBytes + 2
 __device__ __forceinline__ float* part_of(const AttendParams& a, int block, int slot, int rows, int d) {
   return a.part + kRecordBytes / 4 + (2 * (int64_t)block + slot) * rows * (d + 4);
 }
-// The block whose share holds the cost before `end`.
-__device__ __forceinline__ int last_block(int64_t total, int blocks, int64_t end) {
-  int c = (int)min(end * blocks / total, (int64_t)blocks - 1);
-  while (total * c / blocks >= end) --c;
-  while (total * (c + 1) / blocks < end) ++c;
-  return c;
-}
 __device__ __forceinline__ int64_t warp_sum64(int64_t v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 
-// Sets a kernel's shared-memory size and cluster limit, once per device (`prepared`: a bit each).
+// Sets a kernel's shared-memory size, once per device (`prepared`: a bit each).
 cudaError_t prepare_kernel(const void* f, int smem, std::atomic<uint64_t>* prepared);
 
 // A launch that may begin while the stream's previous kernel drains; the kernel waits for it (griddepcontrol.wait).

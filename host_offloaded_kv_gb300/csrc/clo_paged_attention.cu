@@ -44,7 +44,6 @@ cudaError_t prepare_kernel(const void* f, int smem, std::atomic<uint64_t>* prepa
   const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
   if (prepared->load(std::memory_order_acquire) & bit) return cudaSuccess;
   e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e == cudaSuccess) prepared->fetch_or(bit, std::memory_order_release);
   return e;
 }

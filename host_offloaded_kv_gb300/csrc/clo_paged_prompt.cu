@@ -259,6 +259,13 @@ __device__ __forceinline__ int64_t seq_cost(const AttendParams& a, const SeqRows
   }
   return c;
 }
+// The block whose share holds the cost before `end`, where block i of n takes [total i / n, total (i + 1) / n).
+__device__ __forceinline__ int last_block(int64_t total, int blocks, int64_t end) {
+  int c = (int)min(end * blocks / total, (int64_t)blocks - 1);
+  while (total * c / blocks >= end) --c;
+  while (total * (c + 1) / blocks < end) ++c;
+  return c;
+}
 __device__ __forceinline__ SeqRows shfl_seq(const SeqRows& s, int from) {
   SeqRows r;
   r.first = __shfl_sync(0xffffffffu, s.first, from);

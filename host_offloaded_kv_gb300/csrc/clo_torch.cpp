@@ -63,15 +63,42 @@ void shape_is(const at::Tensor& t, const char* name, int64_t a, int64_t b, int64
            (long long)a, (long long)b, (long long)c);
 }
 
-at::Tensor new_rows(int64_t a, int64_t b, int64_t c, int dev, clo_rows* r) {
-  at::Tensor t = at::detail::empty_cuda({a, b, c}, at::kBFloat16, c10::Device(c10::kCUDA, dev), std::nullopt);
-  *r = clo_rows{t.data_ptr(), b * c, c};
+template <typename T>
+T* address(PyObject* o) {
+  void* p = PyLong_AsVoidPtr(o);
+  if (!p && PyErr_Occurred()) throw Raised{};
+  return static_cast<T*>(p);
+}
+
+// None: torch's current stream; an integer: a handle; else an object with one.
+void* stream_of(PyObject* o, int dev) {
+  if (o == Py_None) return c10::cuda::getCurrentCUDAStream(dev).stream();
+  if (PyLong_Check(o)) return address<void>(o);
+  PyObject* h = PyObject_GetAttrString(o, "cuda_stream");
+  if (!h) throw Raised{};
+  void* p = PyLong_AsVoidPtr(h);
+  Py_DECREF(h);
+  if (!p && PyErr_Occurred()) throw Raised{};
+  return p;
+}
+
+// New memory of the current stream's allocator, for work on the caller's `stream`: a stream that the caller names may be another
+// than the current one, and then the allocator has to know who uses the memory.
+at::Tensor new_tensor(at::IntArrayRef size, at::ScalarType type, int dev, PyObject* stream) {
+  at::Tensor t = at::detail::empty_cuda(size, type, c10::Device(c10::kCUDA, dev), std::nullopt);
+  if (stream != Py_None)
+    c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(),
+                                                  c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(stream_of(stream, dev)), dev));
   return t;
 }
 
 // The caller's output, or new rows for None.
-at::Tensor output(PyObject* o, const char* name, int dev, int64_t a, int64_t b, int64_t c, clo_rows* r) {
-  if (o == Py_None) return new_rows(a, b, c, dev, r);
+at::Tensor output(PyObject* o, const char* name, int dev, int64_t a, int64_t b, int64_t c, clo_rows* r, PyObject* stream) {
+  if (o == Py_None) {
+    at::Tensor t = new_tensor({a, b, c}, at::kBFloat16, dev, stream);
+    *r = clo_rows{t.data_ptr(), b * c, c};
+    return t;
+  }
   const at::Tensor& t = rows(o, name, dev, r);
   shape_is(t, name, a, b, c);
   for (int i = 0; i < 3; ++i)
@@ -98,25 +125,6 @@ int32_t small(PyObject* o, const char* name) {
   const int64_t v = integer(o, name);
   if (v < INT32_MIN || v > INT32_MAX) refuse("%s is out of range", name);
   return (int32_t)v;
-}
-
-template <typename T>
-T* address(PyObject* o) {
-  void* p = PyLong_AsVoidPtr(o);
-  if (!p && PyErr_Occurred()) throw Raised{};
-  return static_cast<T*>(p);
-}
-
-// None: torch's current stream; an integer: a handle; else an object with one.
-void* stream_of(PyObject* o, int dev) {
-  if (o == Py_None) return c10::cuda::getCurrentCUDAStream(dev).stream();
-  if (PyLong_Check(o)) return address<void>(o);
-  PyObject* h = PyObject_GetAttrString(o, "cuda_stream");
-  if (!h) throw Raised{};
-  void* p = PyLong_AsVoidPtr(h);
-  Py_DECREF(h);
-  if (!p && PyErr_Occurred()) throw Raised{};
-  return p;
 }
 
 clo_paged_batch batch_of(PyObject* q_starts, PyObject* kv_lens, PyObject* table, int64_t total, PyObject* max_q, int dev, int cache_dev) {
@@ -163,7 +171,7 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t tokens = t.size(0), heads = t.size(1), d = t.size(2);
     if (heads > INT32_MAX || d > INT32_MAX) refuse("x is too large");
     const int64_t* pos = vector_of<int64_t>(a[2], "positions", dev, at::kLong, tokens);
-    at::Tensor out = output(a[3], "out", dev, tokens, heads, d, &y);
+    at::Tensor out = output(a[3], "out", dev, tokens, heads, d, &y, a[5]);
     const clo_status st = clo_rope(address<const clo_rope_plan>(a[0]), &x, &y, pos, tokens, (int32_t)heads, (int32_t)d, PyObject_IsTrue(a[4]),
                                    stream_of(a[5], dev));
     return st ? PyLong_FromLong(st) : THPVariable_Wrap(out);
@@ -189,7 +197,7 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (qt.size(1) > INT32_MAX) refuse("q is too large");
       heads = (int32_t)qt.size(1);
       shape_is(qt, "q", total, heads, c->head_dim);
-      out = output(a[10], "q_out", dev, total, heads, c->head_dim, &y);
+      out = output(a[10], "q_out", dev, total, heads, c->head_dim, &y, a[12]);
     } else if (a[10] != Py_None) {
       refuse("q_out without q");
     }
@@ -210,8 +218,8 @@ PyObject* read(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t total = integer(a[5], "total");
     if (total < 0) refuse("total must not be negative");
     clo_rows k, v;
-    at::Tensor kt = output(a[6], "k_out", dev, total, c->n_kv_heads, c->head_dim, &k);
-    at::Tensor vt = output(a[7], "v_out", dev, total, c->n_kv_heads, c->head_dim, &v);
+    at::Tensor kt = output(a[6], "k_out", dev, total, c->n_kv_heads, c->head_dim, &k, a[9]);
+    at::Tensor vt = output(a[7], "v_out", dev, total, c->n_kv_heads, c->head_dim, &v, a[9]);
     const clo_paged_batch b = batch_of(a[2], a[3], a[4], total, a[8], dev, small(a[1], "device"));
     const clo_status st = clo_paged_read(c, &b, &k, &v, stream_of(a[9], dev));
     if (st) return PyLong_FromLong(st);
@@ -235,7 +243,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (qt.size(2) != c->head_dim) refuse("q has head_dim %lld; the cache has %d", (long long)qt.size(2), c->head_dim);
     if (heads > INT32_MAX) refuse("q is too large");
     const clo_paged_batch b = batch_of(a[3], a[4], a[5], total, a[7], dev, small(a[1], "device"));
-    at::Tensor out = output(a[6], "out", dev, total, heads, c->head_dim, &o);
+    at::Tensor out = output(a[6], "out", dev, total, heads, c->head_dim, &o, a[12]);
     const double scale = PyFloat_AsDouble(a[8]);
     if (scale == -1.0 && PyErr_Occurred()) throw Raised{};
     const int32_t window = small(a[9], "window"), sinks = small(a[10], "sinks");
@@ -251,11 +259,8 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     } else {
       if (const clo_status st = clo_paged_attention_workspace(c, &b, (int32_t)heads, window, sinks, &bytes)) return PyLong_FromLong(st);
       if (bytes) {
-        own = at::detail::empty_cuda({bytes}, at::kByte, c10::Device(c10::kCUDA, dev), std::nullopt);
+        own = new_tensor({bytes}, at::kByte, dev, a[12]);
         work = own.data_ptr();
-        // a stream that is not the allocator's: it has to know who uses the memory
-        if (a[12] != Py_None)
-          c10::cuda::CUDACachingAllocator::recordStream(own.storage().data_ptr(), c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(stream), dev));
       }
     }
     const clo_status st = clo_paged_attention(c, &b, &q, &o, (int32_t)heads, (float)scale, window, sinks, work, bytes, stream);

@@ -505,6 +505,16 @@ LARGE = [
     ([(1, 40000), (1, 20)], 2, 16, 128, 64, 16, 0, 0),
     ([(3, 30000), (2, 1)], 4, 4, 64, 16, 16, 0, 0),
     ([(1, 5 + 37 * i) for i in range(70)], 4, 4, 128, 32, 8, 0, 0),
+    # more sequences than a warp looks over at once, most short, some without rows, one long
+    ([(i % 7 and 1, 1 + 13 * i % 97) for i in range(150)] + [(1, 6000)] + [(2, 3 + 5 * i) for i in range(150)], 2, 2, 128, 16, 16, 0, 0),
+    ([(i % 7 and 1, 1 + 13 * i % 97) for i in range(150)] + [(1, 12000)] + [(2, 3 + 5 * i) for i in range(150)], 2, 2, 128, 16, 8, 0, 0),
+    # as many units as fill the GPU, ragged
+    ([(1, 200 + 450 * i) for i in range(20)], 8, 2, 128, 64, 16, 0, 0),
+    ([(1, 200 + 450 * i) for i in range(20)], 8, 1, 64, 64, 8, 2500, 7),
+    # few units of many rows, long enough to be cut all the same
+    ([(30, 2500), (25, 40), (0, 9)], 3, 3, 128, 64, 16, 0, 0),
+    ([(30, 2500), (25, 40), (0, 9)], 3, 3, 128, 64, 8, 0, 0),
+    ([(90, 3100)], 1, 4, 64, 16, 16, 0, 0),
 ]
 
 
@@ -526,6 +536,31 @@ def test_attention_at_sizes_that_share_the_gpu(clo, case):
     check(first, want, bound, "given workspace")
     assert bool((work[size:] == 0xff).all()), "written past the workspace"
     assert torch.equal(first, c.attend(q, window, sinks, workspace=work)), "two runs differ"
+
+
+def test_calls_on_named_streams_at_once(clo):
+    """Two streams that the caller names, work of both in flight, outputs and workspaces of the current stream's allocator, whose
+    freed memory the current stream overwrites at once."""
+    cases, want = [], []
+    for seed, seqs in ((31, [(1, 20000), (1, 700)]), (32, [(40, 9000), (2, 30)])):
+        c = Case(clo, seqs, 4, 128, 64, 16, seed=seed)
+        c.device()
+        q = bf16(rand(seed, c.total, 16, 128)).cuda()
+        assert c.cache.attention_workspace(16, len(seqs), c.total, c.tab.shape[1], c.max_q) > 0
+        cases.append((c, q, torch.cuda.Stream()))
+        want.append(c.cache.attention(q, c.starts, c.lens, c.tab, max_q=c.max_q).cpu())
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, (c, q, s) in enumerate(cases):
+            got[i].append(c.cache.attention(q, c.starts, c.lens, c.tab, max_q=c.max_q, stream=s))
+            c.cache.attention(q, c.starts, c.lens, c.tab, max_q=c.max_q, stream=s)  # dropped before it has run
+            torch.full((1 << 20,), -1, dtype=torch.int32, device="cuda")
+            torch.full((c.total, 16, 128), 3.0, dtype=BF16, device="cuda")
+    torch.cuda.synchronize()
+    for i in range(2):
+        for o in got[i]:
+            assert torch.equal(o.cpu(), want[i])
 
 
 def test_attention_offsets_past_32_bits(clo):

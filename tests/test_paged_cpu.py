@@ -137,6 +137,31 @@ def test_paged_calls_refuse(clo, call):
         assert run(b=_batch(clo, **b)) == clo.CLO_OK  # nothing to do, nothing launched
 
 
+def test_attention_workspace_sizes(clo):
+    lib = clo.load_library()
+
+    def size(hq=32, window=0, sinks=0, **b):
+        out = ctypes.c_int64(-1)
+        batch = _batch(clo, **dict(dict(batch=1, total_q=1, max_q=1, max_pages=4096, table_stride=4096), **b))
+        rc = lib.clo_paged_attention_workspace(ctypes.byref(_cache(clo)), ctypes.byref(batch), hq, window, sinks, ctypes.byref(out))
+        assert rc == clo.CLO_OK
+        return out.value
+
+    for long in (dict(), dict(batch=600, total_q=600), dict(total_q=300, max_q=300), dict(total_q=300, max_q=9)):
+        assert size(**long) > 0 and size(**long) % 16 == 0
+        # sequences that the table or a window keeps short need none
+        assert size(**dict(long, max_pages=1)) == 0
+        assert size(window=16, **dict(long, batch=1)) == 0
+    # the size goes by the sizes, not by the lengths that the call meets
+    assert size(max_pages=4096) == size(max_pages=1 << 20)
+    assert size(batch=0) == size(total_q=0) == size(max_q=0) == 0
+    batch, out = _batch(clo), ctypes.c_int64(-1)
+    for args in ((0, 0, 0), (3, 0, 0), (4, -1, 0), (4, 0, -1)):
+        rc = lib.clo_paged_attention_workspace(ctypes.byref(_cache(clo)), ctypes.byref(batch), *args, ctypes.byref(out))
+        assert rc == clo.CLO_ERR_INVALID and clo.clo_last_error().startswith("clo_paged_attention_workspace"), args
+    assert lib.clo_paged_attention_workspace(ctypes.byref(_cache(clo)), ctypes.byref(batch), 4, 0, 0, None) == clo.CLO_ERR_INVALID
+
+
 def test_binding_refuses_host_tensors(clo):
     x = torch.zeros((2, 4, 64), dtype=torch.bfloat16)
     plan = clo.clo_rope_plan_init(rot_dim=64)
