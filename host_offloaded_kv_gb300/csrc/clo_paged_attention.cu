@@ -87,7 +87,8 @@ static const char* attend_params(const clo_paged_cache* cache, const clo_paged_b
   return nullptr;
 }
 
-// Up to this many rows per kv head go to the decode kernel, more to the tcgen05 kernel.
+// Up to this many rows per kv head go to the decode kernel, more to the tcgen05 kernel.  (32 rows there, four fragments wide:
+// 193 us for 132 at 16 sequences of 8 tokens by 4 heads over 8000 to 16,000 tokens of bf16, 178 for 123 with 8-bit pages.)
 constexpr int kFewRows = 16;
 
 extern "C" CLO_API clo_status clo_paged_attention_workspace(const clo_paged_cache* cache, const clo_paged_batch* batch, int32_t n_q_heads,
