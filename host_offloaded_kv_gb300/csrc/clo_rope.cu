@@ -125,8 +125,8 @@ struct Rows {
 // ---------------------------------------------------------------------------- rows of one token
 // A warp takes one token and up to ITERS rounds of its heads: the cosines and sines of a lane's unit are computed
 // once for all of them.
-template <int D, int ITERS>
-__device__ __forceinline__ void rotate_heads(const Rope& r, const uint64_t* s_turn, const Rows& x, const Rows& y, int64_t token, int64_t pos,
+template <int D, int ITERS, typename F>
+__device__ __forceinline__ void rotate_heads(const Rope& r, const uint64_t* s_turn, const Rows& x, const Rows& y, int64_t token, F&& position,
                                              int head0, int n_heads, int lane) {
   constexpr int kLanes = D / 16, kRows = 32 / kLanes;
   const Unit<D> u = unit_of_lane<D>(r, s_turn, lane % kLanes);
@@ -141,6 +141,8 @@ __device__ __forceinline__ void rotate_heads(const Rope& r, const uint64_t* s_tu
       vb[i] = *reinterpret_cast<const uint4*>(src + (int64_t)h * x.head + u.b);
     }
   }
+  int64_t pos;
+  if (!position(&pos)) return;
   CosSin c;
   if (u.rotate) c = cos_sin_of<D>(u, pos, r.transpose);
 #pragma unroll
@@ -170,14 +172,18 @@ template <int D>
 __host__ __device__ constexpr int heads_per_warp(int iters) { return iters * 32 / (D / 16); }
 
 template <int D, int ITERS>
-__global__ void __launch_bounds__(kThreads) k_rope(const Rope r, const Rows x, const Rows y, const int64_t* __restrict__ positions,
+__global__ void __launch_bounds__(kThreads, ITERS == kLongIters ? 2 : ITERS == kMidIters ? 3 : 4) k_rope(const Rope r, const Rows x, const Rows y, const int64_t* __restrict__ positions,
                                                    int64_t n_tokens, int n_heads, int chunks) {
   __shared__ __align__(16) uint64_t s_turn[CLO_ROPE_MAX_PAIRS];
   stage_turns(r, s_turn);
   const int64_t job = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
   const int64_t t = job / chunks;
   if (t >= n_tokens) return;
-  rotate_heads<D, ITERS>(r, s_turn, x, y, t, positions[t], (int)(job % chunks) * heads_per_warp<D>(ITERS), n_heads, threadIdx.x & 31);
+  auto position = [&](int64_t* pos) {
+    *pos = positions[t];
+    return true;
+  };
+  rotate_heads<D, ITERS>(r, s_turn, x, y, t, position, (int)(job % chunks) * heads_per_warp<D>(ITERS), n_heads, threadIdx.x & 31);
 }
 
 // Any strides, alignment, rot_dim and head_dim: one pair, or one copied element, per thread and step.
@@ -383,11 +389,15 @@ __global__ void __launch_bounds__(kThreads) k_paged_append(const AppendParams a)
   const int64_t job = (int64_t)((int)blockIdx.x - a.kv_blocks) * kWarps + warp;
   const int64_t t = job / a.q_chunks;
   if (t >= a.c.total_q) return;
-  const int b = seq_of_row(a.c, (int)t, lane);
-  if (b >= a.c.batch) return;
-  const SeqRows s = seq_rows(a.c, b);
-  const int64_t pos = a.positions ? __ldg(a.positions + t) : (int64_t)s.pos0 + (t - s.first);
-  rotate_heads<D, kIters>(a.rope, s_turn, a.q, a.q_out, t, pos, (int)(job % a.q_chunks) * heads_per_warp<D>(kIters), a.n_q_heads, lane);
+  // the row's sequence is looked up while its elements are on their way
+  auto position = [&](int64_t* pos) {
+    const int b = seq_of_row(a.c, (int)t, lane);
+    if (b >= a.c.batch) return false;
+    const SeqRows s = seq_rows(a.c, b);
+    *pos = a.positions ? __ldg(a.positions + t) : (int64_t)s.pos0 + (t - s.first);
+    return true;
+  };
+  rotate_heads<D, kIters>(a.rope, s_turn, a.q, a.q_out, t, position, (int)(job % a.q_chunks) * heads_per_warp<D>(kIters), a.n_q_heads, lane);
 }
 
 // ---------------------------------------------------------------------------- read-back
@@ -396,14 +406,12 @@ struct ReadParams {
   Rows out[2];
 };
 
-// A warp per row of the batch and side; 8 elements per lane and step.
+// A warp per row of the batch, K then V; 8 elements per lane and step.
 template <int D, int BITS>
 __global__ void __launch_bounds__(kThreads) k_paged_read(const ReadParams a) {
   const PagedParams& p = a.c;
   const int lane = threadIdx.x & 31;
-  const int64_t job = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int64_t t = job >> 1;
-  const int side = (int)(job & 1);
+  const int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (t >= p.total_q) return;
   const int b = seq_of_row(p, (int)t, lane);
   if (b >= p.batch) return;
@@ -411,33 +419,53 @@ __global__ void __launch_bounds__(kThreads) k_paged_read(const ReadParams a) {
   if (t - s.first >= s.n) return;
   const int64_t pos = (int64_t)s.pos0 + (t - s.first);
   const int page = pos < 0 || pos >= kMaxPagedTokens ? -1 : page_of(p, b, (int)(pos >> p.page_shift));
-  const PagedSide& sd = p.side[side];
-  const Rows& out = a.out[side];
-  uint16_t* dst = out.p + t * out.token;
   const int slot = (int)(pos & (p.page_size - 1));
   constexpr int kVecs = D / 8;
-#pragma unroll 4
-  for (int v = lane; v < p.n_kv_heads * kVecs; v += 32) {
-    const int h = v / kVecs, e = v % kVecs * 8;
-    uint4 w = make_uint4(0, 0, 0, 0);
-    if (page >= 0) {
-      const char* src = sd.pages + ((int64_t)page * sd.stride_page + (int64_t)h * sd.stride_head + (int64_t)slot * sd.stride_token + e) * (BITS / 8);
-      if (BITS == 16) {
-        w = __ldg(reinterpret_cast<const uint4*>(src));
-      } else {
-        const uint2 c = __ldg(reinterpret_cast<const uint2*>(src));
-        const float scale = fmaxf(__ldg(sd.scales + (int64_t)page * p.n_kv_heads + h), kMinScale);
-        float x[8];
+  const int n = p.n_kv_heads * kVecs;
+  constexpr int kBatch = 8;  // loads in flight per lane
+  for (int v0 = lane; v0 < 2 * n; v0 += 32 * kBatch) {
+    uint4 w[kBatch];
+    float scale[kBatch];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 d = e4m3_to_f32x2(((i < 2 ? c.x : c.y) >> (16 * (i & 1))) & 0xffffu);
-          x[2 * i] = d.x * scale;
-          x[2 * i + 1] = d.y * scale;
+    for (int i = 0; i < kBatch; ++i) {
+      const int v = v0 + 32 * i;
+      const bool second = v >= n;
+      const PagedSide& sd = p.side[second];
+      const int h = (second ? v - n : v) / kVecs, e = v % kVecs * 8;
+      w[i] = make_uint4(0, 0, 0, 0);
+      scale[i] = 1.f;
+      if (v < 2 * n && page >= 0) {
+        const char* src = sd.pages + ((int64_t)page * sd.stride_page + (int64_t)h * sd.stride_head + (int64_t)slot * sd.stride_token + e) * (BITS / 8);
+        if (BITS == 16) {
+          w[i] = __ldg(reinterpret_cast<const uint4*>(src));
+        } else {
+          const uint2 c = __ldg(reinterpret_cast<const uint2*>(src));
+          w[i].x = c.x;
+          w[i].y = c.y;
+          scale[i] = __ldg(sd.scales + (int64_t)page * p.n_kv_heads + h);
         }
-        w = pack8(x);
       }
     }
-    *reinterpret_cast<uint4*>(dst + (int64_t)h * out.head + e) = w;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int v = v0 + 32 * i;
+      if (v >= 2 * n) break;
+      const bool second = v >= n;
+      const Rows& out = a.out[second];
+      const int h = (second ? v - n : v) / kVecs, e = v % kVecs * 8;
+      if (BITS == 8) {
+        const float f = fmaxf(scale[i], kMinScale);
+        float x[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 d = e4m3_to_f32x2(((k < 2 ? w[i].x : w[i].y) >> (16 * (k & 1))) & 0xffffu);
+          x[2 * k] = d.x * f;
+          x[2 * k + 1] = d.y * f;
+        }
+        w[i] = pack8(x);
+      }
+      *reinterpret_cast<uint4*>(out.p + t * out.token + (int64_t)h * out.head + e) = w[i];
+    }
   }
 }
 
@@ -677,7 +705,7 @@ extern "C" CLO_API clo_status clo_paged_read(const clo_paged_cache* cache, const
   a.out[0] = rows_of(k_out);
   a.out[1] = rows_of(v_out);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const unsigned blocks = (unsigned)((2 * (int64_t)a.c.total_q + kWarps - 1) / kWarps);
+  const unsigned blocks = (unsigned)((a.c.total_q + kWarps - 1) / kWarps);
   if (cache->head_dim == 128) {
     if (cache->kv_bits == 16) k_paged_read<128, 16><<<blocks, kThreads, 0, st>>>(a);
     else k_paged_read<128, 8><<<blocks, kThreads, 0, st>>>(a);
