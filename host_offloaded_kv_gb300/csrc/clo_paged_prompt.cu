@@ -26,6 +26,10 @@
 // A masked weight is zero, but zero times NaN is not.  V behind the last visible token (a page's end, where memory may never
 // have been written) is cleared in the operand tile; rows that end with an infinity or NaN all the same, because V has one
 // where they do not look, or where they do, are computed again one by one.
+//
+// 8192 tokens, 32 over 8 heads of 128, causal, bf16: 403 to 411 us, 1.35 PFLOP/s, 70 % of a library product's rate: a token tile takes
+// both lanes 2770 cycles, of which the products 2048, and the diagonal's tiles count half.  2048 tokens over 32,768 of 8-bit
+// pages: 840 us, 1.27 PFLOP/s; there the softmax and the conversions share the issue slots (3700 cycles a tile).
 #include <cuda_runtime.h>
 
 #include <algorithm>
