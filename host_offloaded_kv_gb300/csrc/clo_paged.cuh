@@ -199,6 +199,9 @@ __device__ __forceinline__ uint32_t elect_one() {
   return r;
 }
 
+// Fetches a kernel parameter's tensor map ahead of its first use.
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) { asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory"); }
+
 // One box to shared memory; pages outside the map read as zeros.  The instruction takes its operands from uniform registers: lanes that
 // issue boxes of their own run one after the other, some 180 cycles each, so one thread issues all of a tile's.
 __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int element, int slot, int head, int page, uint32_t bar) {

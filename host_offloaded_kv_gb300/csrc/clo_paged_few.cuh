@@ -73,8 +73,9 @@ __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b
 // there are more.  Measured, whole against cut, us: 64 units of up to 12 tiles 6.5 / 11.8, 8 of 32 tiles 12.6 / 8.4; 256 units of
 // 10 to 19 tiles 8.3 / 14.2, of 63 to 125 tiles 36.6 / 40.6, of 32 to 500 tiles 103 / 94 (8-bit pages, 16 to 250 tiles: 80 / 59).
 constexpr int kWholeFew = 24, kWholeMany = 128;
-constexpr int kFewCost = 4;              // what a unit costs beside its tiles, in tiles
-constexpr int kFewShare = 8 + kFewCost;  // least share of a block: two tiles a warp
+// What a unit costs beside its tiles, in tiles, and the least share of a block.  Cost 4 / 14 / 20, us: 61 windows of 4096 tokens of
+// 8-bit pages 96.0 / 87.8 / 87.5, 32 sequences to 8000 tokens 59.5 / 53.8 / 54.0 (bf16: 94.2 / 91.1 / 91.3).
+constexpr int kFewCost = 14, kFewShare = 14;
 
 // A block's share, and the unit that it begins in.
 struct FewShare {
@@ -166,6 +167,10 @@ __global__ void __launch_bounds__(kThreads) k_attend_few(const AttendParams a, c
   const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t ring = smem + warp * kStages * kStageBytes;
   uint8_t* const generic = smem_raw + (smem - smem_u32(smem_raw));
+  FewShare share{0, 1, 0, (int)blockIdx.x, (int)blockIdx.y};
+  if (a.part) share = few_share(a, TOK, lane);
+  int kvh = share.kvh, b = share.b;
+  SeqRows s = seq_rows(p, b);
   if (tid == 0) s_odd = s_dead = 0;
   if (lane == 0) {
 #pragma unroll
@@ -175,27 +180,26 @@ __global__ void __launch_bounds__(kThreads) k_attend_few(const AttendParams a, c
   }
   __syncthreads();
 
-  FewShare share{0, 1, 0, (int)blockIdx.x, (int)blockIdx.y};
-  if (a.part) share = few_share(a, TOK, lane);
   const bool by_unit = (int64_t)p.batch * p.n_kv_heads <= kWave;  // where a unit's record stands
   PartRecord* const records = reinterpret_cast<PartRecord*>(a.part);
   if (tid == 0 && a.part && !by_unit) records[blockIdx.x].valid = 0;
   int st = 0;          // next stage, and its barrier's phase
   uint32_t phase = 0;
-  int kvh = share.kvh, b = share.b;
   int64_t base = share.first < share.last ? share.base : share.last;
+  auto next_seq = [&]() {
+    if (++b < p.batch) s = seq_rows(p, b);
+  };
   auto next = [&](int64_t end) {
     base = end;
     if (++kvh == p.n_kv_heads) {
       kvh = 0;
-      ++b;
+      next_seq();
     }
   };
   while (base < share.last && b < p.batch) {
-    const SeqRows s = seq_rows(p, b);
     const int rows = s.n * a.group;
     if (rows == 0) {
-      ++b;
+      next_seq();
       continue;
     }
     const TileList tl = tiles_of(s.pos0, s.pos0 + s.n - 1, s.kv_len, a.window, a.sinks, TOK);

@@ -394,6 +394,10 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
   const uint32_t q_smem = smem, ring = smem + TILES * C::kQBytes, raw = ring + SLOTS * C::kTileBytes;
   uint8_t* const generic = smem_raw + (smem - smem_u32(smem_raw));
 
+  if (tid == 32) {
+    prefetch_map(&maps.side[0]);
+    prefetch_map(&maps.side[1]);
+  }
   if (tid == 0) {
     for (int i = 0; i < 8; ++i) {
       mbar_init(&sh.full[i], BITS == 16 ? 1 : 2 * 128);
