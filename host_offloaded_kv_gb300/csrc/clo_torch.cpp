@@ -86,9 +86,11 @@ void* stream_of(PyObject* o, int dev) {
 // than the current one, and then the allocator has to know who uses the memory.
 at::Tensor new_tensor(at::IntArrayRef size, at::ScalarType type, int dev, PyObject* stream) {
   at::Tensor t = at::detail::empty_cuda(size, type, c10::Device(c10::kCUDA, dev), std::nullopt);
-  if (stream != Py_None)
-    c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(),
-                                                  c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(stream_of(stream, dev)), dev));
+  if (stream != Py_None) {
+    cudaStream_t st = static_cast<cudaStream_t>(stream_of(stream, dev));
+    if (st == cudaStreamLegacy) st = nullptr;  // the same stream by its other name
+    c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), c10::cuda::getStreamFromExternal(st, dev));
+  }
   return t;
 }
 

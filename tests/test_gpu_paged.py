@@ -563,6 +563,25 @@ def test_calls_on_named_streams_at_once(clo):
             assert torch.equal(o.cpu(), want[i])
 
 
+def test_streams_by_handle(clo):
+    # the default stream, its other name, the thread's own, one of torch's as a number and as an object
+    c = Case(clo, [(1, 9000)], 2, 64, 32, 16, seed=41)
+    c.device()
+    q = bf16(rand(41, c.total, 8, 64)).cuda()
+    plan = clo.clo_rope_plan_init(rot_dim=64)
+    pos = torch.tensor([70000], dtype=torch.int64, device="cuda")
+    want = c.attend(q).cpu(), clo.clo_rope(plan, q, pos).cpu()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (0, 1, 2, side.cuda_stream, side):
+        got = (c.cache.attention(q, c.starts, c.lens, c.tab, max_q=c.max_q, stream=stream), clo.clo_rope(plan, q, pos, stream=stream))
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert torch.equal(g.cpu(), w)
+    del got, g
+    torch.cuda.synchronize()
+
+
 def test_attention_offsets_past_32_bits(clo):
     # pages whose element offsets pass 2^32: few tokens, far apart
     d, page, hkv = 128, 128, 1
