@@ -80,17 +80,28 @@ __device__ __forceinline__ int seq_of_row(const PagedParams& p, int t, int lane)
   return b;
 }
 
-// cos and sin of position * turn: the product modulo 2^64 is the angle as a fraction of a turn, so far
-// positions lose nothing.  Its upper 32 bits, as half turns in [-1, 1), go through one rounding to fp32.
+// cos and sin of position * turn: the product modulo 2^64 is the angle as a fraction of a turn, so far positions lose nothing.
+// Its upper 32 bits go to the nearest quarter turn in integers; the rest, r in [-1/4, 1/4] half turns, is off by 2^-27 at most
+// after one rounding to fp32 (the whole angle would be by 2^-25, and more 8-bit codes would differ from an exact rotation's).
+// There Taylor's series of sin(pi r) to r^9 and of cos(pi r) to r^10 leave less than 2^-28; results are off by 7.5e-8 at most.
 __device__ __forceinline__ float2 rope_cos_sin(int64_t pos, uint64_t turn, float magnitude) {
   const uint32_t lo = (uint32_t)turn, hi = (uint32_t)(turn >> 32);
   const uint32_t plo = (uint32_t)pos, phi = (uint32_t)((uint64_t)pos >> 32);
   const uint32_t frac = __umulhi(plo, lo) + plo * hi + phi * lo;
-  float2 r;
-  sincospif((float)(int32_t)frac * 4.656612873077393e-10f, &r.y, &r.x);
-  r.x *= magnitude;
-  r.y *= magnitude;
-  return r;
+  const uint32_t quarter = (frac + 0x20000000u) >> 30;
+  const float r = (float)(int32_t)(frac - (quarter << 30)) * 4.656612873077393e-10f, r2 = r * r;
+  constexpr double kPi = 3.14159265358979323846, kPi2 = kPi * kPi, kPi4 = kPi2 * kPi2;
+  constexpr float kPiHi = (float)kPi, kPiLo = (float)(kPi - (double)kPiHi);
+  float p = fmaf((float)(kPi4 * kPi4 * kPi / 362880.0), r2, (float)(-kPi4 * kPi2 * kPi / 5040.0));
+  p = fmaf(fmaf(p, r2, (float)(kPi4 * kPi / 120.0)), r2, (float)(-kPi2 * kPi / 6.0));
+  const float s = fmaf(r, kPiHi, r * fmaf(p, r2, kPiLo));
+  float c = fmaf((float)(-kPi4 * kPi4 * kPi2 / 3628800.0), r2, (float)(kPi4 * kPi4 / 40320.0));
+  c = fmaf(fmaf(c, r2, (float)(-kPi4 * kPi2 / 720.0)), r2, (float)(kPi4 / 24.0));
+  c = fmaf(fmaf(c, r2, (float)(-kPi2 / 2.0)), r2, 1.f);
+  float2 y = quarter & 1u ? make_float2(s, c) : make_float2(c, s);
+  y.x *= (quarter + 1u) & 2u ? -magnitude : magnitude;
+  y.y *= quarter & 2u ? -magnitude : magnitude;
+  return y;
 }
 
 __device__ __forceinline__ void unpack8(const uint4 v, float* x) {
