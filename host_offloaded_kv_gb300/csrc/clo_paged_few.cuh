@@ -70,12 +70,13 @@ __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b
 }
 
 // Longest units, in tiles, that are left whole (no shares to find, no join): where there are fewer units than SMs, and where
-// there are more.  Measured, whole against cut, us: 64 units of up to 12 tiles 6.5 / 11.8, 8 of 32 tiles 12.6 / 8.4; 256 units of
+// there are more.  Measured, whole against cut, us: 64 units of up to 12 tiles 6.5 / 11.8, 8 of 32 tiles 12.6 / 7.6; 256 units of
 // 10 to 19 tiles 8.3 / 14.2, of 63 to 125 tiles 36.6 / 40.6, of 32 to 500 tiles 103 / 94 (8-bit pages, 16 to 250 tiles: 80 / 59).
 constexpr int kWholeFew = 24, kWholeMany = 128;
 // What a unit costs beside its tiles, in tiles, and the least share of a block.  Cost 4 / 14 / 20, us: 61 windows of 4096 tokens of
 // 8-bit pages 96.0 / 87.8 / 87.5, 32 sequences to 8000 tokens 59.5 / 53.8 / 54.0 (bf16: 94.2 / 91.1 / 91.3).
-constexpr int kFewCost = 14, kFewShare = 14;
+// Share 14 / 8 / 5, us: one sequence of 512 tokens 8.8 / 7.6 / 7.4, of 2000 9.3 / 8.6 / 9.0, of 8000 of 8-bit pages 12.4 / 11.2 / 11.1.
+constexpr int kFewCost = 14, kFewShare = 8;
 
 // A block's share, and the unit that it begins in.
 struct FewShare {

@@ -433,7 +433,7 @@ typedef struct clo_paged_batch {
  * max |x| <= 448 * 2^e over the finite new values of the page and head; a page that holds earlier
  * tokens gets the larger of this and its scale, and where that grows the earlier tokens' codes are
  * rescaled (exact unless they fall below 2^-6 * scale).  Infinities become +-448 * scale, NaN stays.
- * A page may be written for one sequence only in a call.  Rows on 16-byte boundaries, strides multiples of 8
+ * A call may write a page for one sequence and at one place of its table only.  Rows on 16-byte boundaries, strides multiples of 8
  * elements, rot_dim a multiple of 16.
  * Errors: CLO_ERR_INVALID, CLO_ERR_CUDA. */
 CLO_API clo_status clo_paged_append(const clo_paged_cache* cache, const clo_paged_batch* batch, const clo_rope_plan* plan,
