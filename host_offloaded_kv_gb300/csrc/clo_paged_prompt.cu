@@ -43,9 +43,10 @@ constexpr int kTok = 128;    // tokens per tile
 constexpr int kRows = 128;   // rows per row tile
 constexpr float kGrow = 8.f;
 constexpr int kUnitCost = 4;   // what a unit costs beside its token tiles, in tiles (11,000 cycles of 2,800)
-// Least share where units are cut: joining costs about as much as four tiles.  Calls too small for all SMs cut only where a unit is
-// twice as long, into fewer shares; otherwise units stay whole, spread over the SMs.
-constexpr int kMinShare = 8;
+// Units are cut where every block's share is kMinShare or more, as joining costs about as much as four tiles; in smaller calls only where a
+// unit costs twice that, into shares of kLongShare, and otherwise units stay whole, spread over the SMs.  Shares of 8 / 5, us: 30 rows
+// over 2000 tokens 19.8 / 17.5, of 8-bit pages 24.3 / 20.7; cutting down to 5 everywhere: a prompt of 600 tokens 17.7 / 20.7.
+constexpr int kMinShare = 8, kLongShare = 5;
 
 // ---------------------------------------------------------------------------- tcgen05
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -362,7 +363,7 @@ __device__ void find_share(const AttendParams& a, int lane, S& sh) {
     if (pass == 0) {
       most = __reduce_max_sync(0xffffffffu, most);
       const bool large = total >= (int64_t)kMinShare * gridDim.x, cuts = a.part && (large || most >= 2 * kMinShare);
-      const int blocks = cuts && !large ? max((int)(total / kMinShare), 1) : (int)gridDim.x;
+      const int blocks = cuts && !large ? min(max((int)(total / kLongShare), 1), (int)gridDim.x) : (int)gridDim.x;
       share = total * min((int)blockIdx.x, blocks) / blocks;
       const int64_t last = total * min((int)blockIdx.x + 1, blocks) / blocks;
       if (lane == 0) {
