@@ -654,9 +654,10 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
       }
       tc_fence_after();
       if (!ok) l = __int_as_float(0x7fffffff);
-      if (TILES == 1) {
-        // lane 1's sums join lane 0's: its accumulator lies in the same TMEM rows
-        if (TILES == 1 && t == 1) {
+      if (TILES == 1 && n > 0) {
+        // Lane 1's sums join lane 0's: its accumulator lies in the same TMEM rows.  Barrier 1 at the begin of the next unit with tiles
+        // holds lane 1 back until lane 0 has read them; a unit without tiles has neither that barrier nor sums.
+        if (t == 1) {
           sh.join_m[tid & 127] = ref;
           sh.join_l[tid & 127] = l;
           tc_fence_before();
