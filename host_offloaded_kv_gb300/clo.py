@@ -373,8 +373,10 @@ class PagedCache:
 
     The calls take the batch as q_starts int32 [batch + 1], kv_lens int32 [batch] (the call's tokens included)
     and block_table int32 [batch][max_pages]; max_q is the most rows that a sequence has (default: all
-    rows of the call, which is right for one sequence; a step of single tokens passes 1).  stream None is
-    torch's current stream."""
+    rows of the call, which is right for one sequence; a step of single tokens passes 1).
+
+    stream None is torch's current stream; otherwise a torch stream or a handle.  New outputs belong to the stream of the
+    call, as under ``torch.cuda.stream``: another stream that uses them waits for it first."""
 
     def __init__(self, k_pages, v_pages, k_scales=None, v_scales=None):
         import torch

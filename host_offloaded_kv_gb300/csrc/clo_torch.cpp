@@ -8,6 +8,7 @@
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -82,22 +83,25 @@ void* stream_of(PyObject* o, int dev) {
   return p;
 }
 
-// New memory of the current stream's allocator, for work on the caller's `stream`: a stream that the caller names may be another
-// than the current one, and then the allocator has to know who uses the memory.
-at::Tensor new_tensor(at::IntArrayRef size, at::ScalarType type, int dev, PyObject* stream) {
-  at::Tensor t = at::detail::empty_cuda(size, type, c10::Device(c10::kCUDA, dev), std::nullopt);
-  if (stream != Py_None) {
-    cudaStream_t st = static_cast<cudaStream_t>(stream_of(stream, dev));
-    if (st == cudaStreamLegacy) st = nullptr;  // the same stream by its other name
-    c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), c10::cuda::getStreamFromExternal(st, dev));
-  }
+// New memory for work on the caller's stream.  A stream that the caller names has its own, as under torch.cuda.stream: what the current
+// stream has freed may still be in use there, and the named stream does not wait for it.  `returned`: the caller gets the memory and may
+// go on to use it on the current stream, so the allocator is told of that one too.
+at::Tensor new_tensor(at::IntArrayRef size, at::ScalarType type, int dev, PyObject* stream, bool returned) {
+  const c10::Device device(c10::kCUDA, dev);
+  if (stream == Py_None) return at::detail::empty_cuda(size, type, device, std::nullopt);
+  cudaStream_t st = static_cast<cudaStream_t>(stream_of(stream, dev));
+  if (st == cudaStreamLegacy) st = nullptr;  // the same stream by its other name
+  const c10::cuda::CUDAStream current = c10::cuda::getCurrentCUDAStream(dev);
+  const c10::cuda::CUDAStreamGuard guard(st ? c10::cuda::getStreamFromExternal(st, dev) : c10::cuda::getDefaultCUDAStream(dev));
+  at::Tensor t = at::detail::empty_cuda(size, type, device, std::nullopt);
+  if (returned && current.stream() != st) c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), current);
   return t;
 }
 
 // The caller's output, or new rows for None.
 at::Tensor output(PyObject* o, const char* name, int dev, int64_t a, int64_t b, int64_t c, clo_rows* r, PyObject* stream) {
   if (o == Py_None) {
-    at::Tensor t = new_tensor({a, b, c}, at::kBFloat16, dev, stream);
+    at::Tensor t = new_tensor({a, b, c}, at::kBFloat16, dev, stream, true);
     *r = clo_rows{t.data_ptr(), b * c, c};
     return t;
   }
@@ -261,7 +265,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     } else {
       if (const clo_status st = clo_paged_attention_workspace(c, &b, (int32_t)heads, window, sinks, &bytes)) return PyLong_FromLong(st);
       if (bytes) {
-        own = new_tensor({bytes}, at::kByte, dev, a[12]);
+        own = new_tensor({bytes}, at::kByte, dev, a[12], false);
         work = own.data_ptr();
       }
     }

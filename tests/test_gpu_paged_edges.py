@@ -48,3 +48,62 @@ def test_units_without_tokens_between_others_in_one_block(clo, bits, rows, d):
     check(whole, want, bound, "no workspace")
     for _ in range(40):
         assert torch.equal(c.attend(q), first) and torch.equal(c.attend(q, workspace=none), whole)
+
+
+# --------------------------------------------------------------------------------------------- streams
+def stream_of_memory(address):
+    """The stream that torch's allocator took this memory for."""
+    for seg in torch.cuda.memory_snapshot():
+        if seg["address"] <= address < seg["address"] + seg["total_size"]:
+            return seg["stream"]
+
+
+def test_new_memory_belongs_to_the_named_stream(clo):
+    # what the current stream has just freed may still be written there: a call on another stream must not get it
+    n, h, d = 4096, 8, 128
+    plan = clo.clo_rope_plan_init(rot_dim=d)
+    x = bf16(rand(71, n, h, d)).cuda()
+    pos = torch.arange(n, device="cuda")
+    c = Case(clo, [(1, 20000)], 2, 64, 64, 16, seed=72)
+    c.device()
+    q = bf16(rand(73, 1, 8, 64)).cuda()
+    want = clo.clo_rope(plan, x, pos).cpu(), c.attend(q).cpu()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (side, side.cuda_stream):
+        old = torch.empty_like(x)
+        freed = old.data_ptr()
+        del old
+        got = clo.clo_rope(plan, x, pos, stream=stream)
+        assert got.data_ptr() != freed and stream_of_memory(got.data_ptr()) == side.cuda_stream
+        k, v = c.cache.read(c.starts, c.lens, c.tab, 1, stream=stream)
+        assert stream_of_memory(k.data_ptr()) == stream_of_memory(v.data_ptr()) == side.cuda_stream
+        out = c.attend(q, stream=stream)
+        assert stream_of_memory(out.data_ptr()) == side.cuda_stream
+        torch.cuda.synchronize()
+        assert torch.equal(got.cpu(), want[0]) and torch.equal(out.cpu(), want[1])
+        del got, k, v, out
+    torch.cuda.synchronize()
+    # the default stream by either name, from another current stream
+    with torch.cuda.stream(side):
+        for stream in (0, 1, torch.cuda.default_stream()):
+            assert stream_of_memory(clo.clo_rope(plan, x, pos, stream=stream).data_ptr()) == 0
+        assert stream_of_memory(clo.clo_rope(plan, x, pos).data_ptr()) == side.cuda_stream
+    torch.cuda.synchronize()
+
+
+def test_workspace_belongs_to_the_named_stream(clo):
+    c = Case(clo, [(1, 30000)], 2, 64, 64, 16, seed=74)
+    c.device()
+    q = bf16(rand(75, 1, 8, 64)).cuda()
+    want = c.attend(q)
+    size = c.cache.attention_workspace(8, 1, 1, c.tab.shape[1], 1)
+    assert size > 0
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    held = lambda: sum(s["total_size"] for s in torch.cuda.memory_snapshot() if s["stream"] == side.cuda_stream)  # noqa: E731
+    out, before = torch.empty_like(want), held()
+    c.attend(q, out=out, stream=side)
+    torch.cuda.synchronize()
+    assert held() >= before + size
+    assert torch.equal(out, want)
