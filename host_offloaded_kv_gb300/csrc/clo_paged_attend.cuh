@@ -51,6 +51,14 @@ __device__ void attend_row(const AttendParams& a, int b, const SeqRows& s, int r
   for (int i = 0; i < E; ++i) o[lane * E + i] = (uint16_t)pack_bf16(l == 0.f ? 0.f : acc[i] / l, 0.f);
 }
 
+// What becomes of a row's sums.  lost: a wait for a copy or product gave up, so they mean nothing, and the row is NaN whatever else holds
+// (computing it again would hide that memory or the launch is broken).  spoilt: V had an infinity or NaN that the row does not see.
+enum class RowEnd { store, nan, again };
+__host__ __device__ constexpr RowEnd row_end(bool lost, bool spoilt) { return lost ? RowEnd::nan : spoilt ? RowEnd::again : RowEnd::store; }
+// The same as a part's mark, for the kernel that joins the parts.
+constexpr float kPartSpoilt = 1.f, kPartLost = 2.f;
+__host__ __device__ constexpr float part_mark(RowEnd e) { return e == RowEnd::nan ? kPartLost : e == RowEnd::again ? kPartSpoilt : 0.f; }
+
 // Shared-memory address of 16-byte chunk `chunk` of row `row` in a tile of `rows` rows as TMA's swizzle left it.
 template <int SPAN>
 __device__ __forceinline__ uint32_t swizzled(uint32_t base, int rows, int row, int chunk) {
@@ -101,7 +109,7 @@ constexpr int kSms = 152;  // GB300
 // All units' tiles of tokens, each unit with a constant cost beside them, lie end to end and are cut into equal shares, one to a
 // block.  A unit that a cut meets leaves one part per block in the caller's workspace: a record per block, then two
 // parts per block (slot 1: of a unit that it begins, slot 0: of one that it ends or passes through), each [row][D elements, maximum,
-// sum, -, -].
+// sum, mark, -].
 struct PartRecord {
   int valid, b, qb, kvh;
   int last;  // the unit's parts are this block's slot 1 and slot 0 of the following ones up to `last`

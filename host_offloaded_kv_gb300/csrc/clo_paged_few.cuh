@@ -578,9 +578,8 @@ __global__ void __launch_bounds__(kThreads) k_attend_few(const AttendParams a, c
         const int r = e / (D / 4), q4 = e % (D / 4) * 4;
         *reinterpret_cast<float4*>(dst + r * (D + 4) + q4) = *reinterpret_cast<const float4*>(part + r * (D + 4) + q4);
       }
-      // maximum, sum, whether V held an infinity or NaN that only some rows see
-      if (tid < rows) *reinterpret_cast<float4*>(dst + tid * (D + 4) + D) = make_float4(s_cm[tid], s_cl[tid], s_odd ? 1.f : 0.f, 0.f);
-    } else if (!s_odd) {
+      if (tid < rows) *reinterpret_cast<float4*>(dst + tid * (D + 4) + D) = make_float4(s_cm[tid], s_cl[tid], part_mark(row_end(s_dead, s_odd)), 0.f);
+    } else if (row_end(s_dead, s_odd) != RowEnd::again) {  // a lost copy has made the sums NaN
       for (int e = tid; e < rows * (D / 2); e += kThreads) {
         const int r = e / (D / 2), d2 = e % (D / 2) * 2;
         const float sum = s_cl[r], inv = 1.f / sum;
@@ -618,7 +617,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_attend_join(const AttendParams
   if (r >= s.n * a.group || !rec.valid) return;
   const int64_t row = (int64_t)r * (D + 4);
   float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-  bool odd = false;
+  bool odd = false, lost = false;
 #pragma unroll 4
   for (int c = rec.own + slice; c <= rec.last; c += kSlices) {
     const float* q = part_of(a, c, c == rec.own ? 1 : 0, a.part_rows, D) + row;
@@ -626,7 +625,8 @@ __global__ void __launch_bounds__(kJoinThreads) k_attend_join(const AttendParams
     const float mn = fmaxf(m, t.x);
     const float keep = m == mn ? 1.f : exp2_fast(m - mn), f = t.x == mn ? 1.f : exp2_fast(t.x - mn);
     m = mn;
-    odd |= t.z != 0.f;
+    odd |= t.z == kPartSpoilt;
+    lost |= t.z == kPartLost;
     l = l * keep + t.y * f;
     o[0] = o[0] * keep + v.x * f;
     o[1] = o[1] * keep + v.y * f;
@@ -638,7 +638,8 @@ __global__ void __launch_bounds__(kJoinThreads) k_attend_join(const AttendParams
     s_m[slice] = m;
     s_l[slice] = l;
   }
-  if (__syncthreads_or(odd)) {
+  const bool any_odd = __syncthreads_or(odd), any_lost = __syncthreads_or(lost);
+  if (row_end(any_lost, any_odd) == RowEnd::again) {  // (a lost part's sum is NaN)
     if (threadIdx.x < 32) attend_row<D, BITS>(a, b, s, r / a.group, kvh * a.group + r % a.group, threadIdx.x);
     return;
   }

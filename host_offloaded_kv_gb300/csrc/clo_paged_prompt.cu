@@ -653,7 +653,6 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
         s_phase ^= 1u;
       }
       tc_fence_after();
-      if (!ok) l = __int_as_float(0x7fffffff);
       if (TILES == 1 && n > 0) {
         // Lane 1's sums join lane 0's: its accumulator lies in the same TMEM rows.  Barrier 1 at the begin of the next unit with tiles
         // holds lane 1 back until lane 0 has read them; a unit without tiles has neither that barrier nor sums.
@@ -675,11 +674,14 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
           l = l * f0 + sh.join_l[tid & 127] * f1;
           ref = mx;
         }
+        // a wait gave up anywhere in the block: this unit's rows and the rest of the share are NaN
+        const bool lost = *reinterpret_cast<volatile int*>(&sh.failed) != 0;
+        if (lost) l = __int_as_float(0x7fffffff);
         const float inv = full ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
         float* part = nullptr;
         if (!full) {
           part = part_of(a, blockIdx.x, u.t_begin == 0 ? 1 : 0, TILES * kRows, D) + (int64_t)(my_tile * kRows + (tid & 127)) * (D + 4);
-          *reinterpret_cast<float2*>(part + D) = make_float2(ref, l);
+          *reinterpret_cast<float4*>(part + D) = make_float4(ref, l, part_mark(row_end(lost, false)), 0.f);
         }
         float odd = l * 0.f;  // NaN if anything in the row is no finite number
 #pragma unroll 1
@@ -729,7 +731,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
             dst.next();
           }
           __syncwarp();
-          unsigned again = __ballot_sync(0xffffffffu, row_ok && odd != 0.f);
+          unsigned again = __ballot_sync(0xffffffffu, row_ok && row_end(lost, odd != 0.f) == RowEnd::again);
           for (; again; again &= again - 1) {
             const int gr = row0 + my_tile * kRows + (warp & 3) * 32 + __ffs(again) - 1;
             attend_row<D, BITS>(a, u.b, s, gr / a.group, kvh * a.group + gr % a.group, lane);
@@ -1020,12 +1022,14 @@ __global__ void __launch_bounds__(256) k_attend_many_join(const AttendParams a) 
   for (int c = blockIdx.x + lane; c <= rec.last; c += 32) mx = fmaxf(mx, part(c)[D]);
   mx = warp_max(mx);
   float l = 0.f, o[E];
+  bool lost = false;
 #pragma unroll
   for (int i = 0; i < E; ++i) o[i] = 0.f;
 #pragma unroll 4
   for (int c = blockIdx.x; c <= rec.last; ++c) {
     const float* q = part(c);
-    const float2 ml = *reinterpret_cast<const float2*>(q + D);
+    const float4 ml = *reinterpret_cast<const float4*>(q + D);
+    lost |= ml.z == kPartLost;
     const float f = ml.x == mx ? 1.f : exp2_fast(ml.x - mx);
     l = fmaf(ml.y, f, l);
 #pragma unroll
@@ -1038,7 +1042,7 @@ __global__ void __launch_bounds__(256) k_attend_many_join(const AttendParams a) 
   float odd = l * 0.f;
 #pragma unroll
   for (int i = 0; i < E; ++i) odd = fmaf(o[i], 0.f, odd);
-  if (__any_sync(0xffffffffu, odd != 0.f)) {
+  if (row_end(lost, __any_sync(0xffffffffu, odd != 0.f)) == RowEnd::again) {  // (a lost part's sum is NaN)
     attend_row<D, BITS>(a, rec.b, s, gr / a.group, rec.kvh * a.group + gr % a.group, lane);
     return;
   }

@@ -462,6 +462,8 @@ CLO_API clo_status clo_paged_read(const clo_paged_cache* cache, const clo_paged_
  * workspace: device memory, 16-byte aligned, of the size that clo_paged_attention_workspace gives (it may
  * hold anything, and is free again when the call's work is done); calls that may overlap need one each.
  * NULL or less than that: the call works without, on fewer SMs (it matters for few long sequences).
+ * Waits for copies and products inside the kernels are limited to two seconds.  Where one gives up (it takes a defect to get
+ * there), the rows that its block had left are NaN; no status tells.
  * Errors: CLO_ERR_INVALID, CLO_ERR_CUDA. */
 CLO_API clo_status clo_paged_attention(const clo_paged_cache* cache, const clo_paged_batch* batch, const clo_rows* q,
                                        const clo_rows* out, int32_t n_q_heads, float softmax_scale, int32_t window,

@@ -193,3 +193,34 @@ def test_reference_rounding_is_the_formats():
     x = x.clamp(-448, 448)
     near = (fin[None, :] - x[:, None]).abs().min(1)[0]
     assert torch.equal((ref.round_e4m3(x) - x).abs(), near)
+
+
+def test_a_lost_copy_is_never_hidden(tmp_path):
+    # rows of a unit whose wait gave up are NaN, also where V would have them computed again; parts carry that to the join
+    from host_offloaded_kv_gb300 import _build
+
+    src = tmp_path / "row_end.cu"
+    src.write_text('''#include <cstdio>
+#include "clo_paged_attend.cuh"
+using namespace clo;
+int main() {
+  for (int i = 0; i < 4; ++i) {
+    const RowEnd e = row_end(i & 2, i & 1);
+    const float mark = part_mark(e);
+    printf("%d %d %d ", (int)(e == RowEnd::nan), (int)(e == RowEnd::again), (int)(row_end(mark == kPartLost, mark == kPartSpoilt) == e));
+  }
+}
+''')
+    exe = str(tmp_path / "row_end")
+    csrc = os.path.join(ROOT, "host_offloaded_kv_gb300", "csrc")
+    subprocess.run([_build._nvcc(), "-std=c++17", "-gencode", "arch=compute_103a,code=sm_103a", "-I", csrc, "-I", os.path.join(ROOT, "include"),
+                    str(src), "-o", exe], check=True)
+    got = subprocess.run([exe], capture_output=True, text=True, check=True).stdout.split()
+    assert got == "0 0 1  0 1 1  1 0 1  1 0 1".split()
+    # every place that computes rows again asks row_end first
+    for name in ("clo_paged_few.cuh", "clo_paged_prompt.cu"):
+        text = open(os.path.join(csrc, name)).read()
+        calls = [m for m in range(len(text)) if text.startswith("attend_row<", m)]
+        assert len(calls) == 2
+        for at in calls:
+            assert "row_end(" in text[at - 1500:at], f"{name}: a row is computed again unasked"
