@@ -55,8 +55,8 @@ __device__ void attend_row(const AttendParams& a, int b, const SeqRows& s, int r
 // (computing it again would hide that memory or the launch is broken).  spoilt: V had an infinity or NaN that the row does not see.
 enum class RowEnd { store, nan, again };
 __host__ __device__ constexpr RowEnd row_end(bool lost, bool spoilt) { return lost ? RowEnd::nan : spoilt ? RowEnd::again : RowEnd::store; }
-// The same as a part's mark, for the kernel that joins the parts.
-constexpr float kPartSpoilt = 1.f, kPartLost = 2.f;
+// The same as a part's mark, for the kernel that joins the parts; kPartSeen: no finite number, and rightly.
+constexpr float kPartSpoilt = 1.f, kPartLost = 2.f, kPartSeen = 3.f;
 __host__ __device__ constexpr float part_mark(RowEnd e) { return e == RowEnd::nan ? kPartLost : e == RowEnd::again ? kPartSpoilt : 0.f; }
 
 // Shared-memory address of 16-byte chunk `chunk` of row `row` in a tile of `rows` rows as TMA's swizzle left it.
@@ -101,6 +101,72 @@ __device__ __forceinline__ TileList tiles_of(int pos_first, int pos_last, int kv
   t.first = max(a.lo / tokens, t.sink_tiles);
   t.rest = max((z.hi + tokens - 1) / tokens - t.first, 0);
   return t;
+}
+
+// Which of a warp's rows have to be computed again, of those (`want`, a lane each, at position `pos`) whose sums over the tiles [k0, k1)
+// of `tl` are no finite numbers.  What a row sees may make it so, and stays: only where V has an infinity or NaN in a token of the tiles that
+// the row does not see (zero times it is NaN), or where what it sees can pass fp32's range in the unnormalised sums alone
+// (weights up to 2^15, 2^30 tokens: values from 2^80 on, scales below 2^-80), the row's sums are wrong.  So they are where an infinity
+// had a weight too small for fp32: a NaN (`nan`) without one in V.  One look over V, up to eight loads of a warp in flight.
+template <int D, int BITS>
+__device__ __forceinline__ bool spoilt_rows(const AttendParams& a, int b, int kvh, const SeqRows& s, const TileList& tl, int k0, int k1, int tokens, int hi,
+                                            bool want, int pos, bool nan, int lane) {
+  const PagedParams& p = a.c;
+  const PagedSide& sd = p.side[1];
+  constexpr int kLanes = D * BITS / 64, kPer = 32 / kLanes;  // lanes of a row (8 bytes each), rows of a load
+  constexpr int kBatch = 16 / kPer < 8 ? 16 / kPer : 8;  // loads in flight
+  constexpr uint32_t kRow = kLanes == 32 ? 0xffffffffu : (1u << kLanes) - 1u;
+  bool spoilt = false, saw_nan = false, saw_inf = false;
+  const int groups = k1 * (tokens / 16);
+  for (int g0 = k0 * (tokens / 16); g0 < groups; g0 += 32) {
+    auto first_of = [&](int g) { return tl.at(g * 16 / tokens) * tokens + g * 16 % tokens; };
+    const int mine = g0 + lane < groups ? page_of(p, b, first_of(g0 + lane) >> p.page_shift) : -1;
+    for (int g = g0; g < min(g0 + 32, groups); ++g) {
+      const int page = __shfl_sync(0xffffffffu, mine, g - g0), j0 = first_of(g);
+      if (page < 0 || j0 >= hi) continue;
+      const char* src = sd.pages + ((int64_t)page * sd.stride_page + (int64_t)kvh * sd.stride_head) * (BITS / 8) + lane % kLanes * 8;
+      const bool small_scale = BITS == 8 && !(sd.scales[(int64_t)page * p.n_kv_heads + kvh] >= 0x1p-80f);
+#pragma unroll 1
+      for (int i0 = 0; i0 < 16; i0 += kPer * kBatch) {
+        uint2 w[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int j = j0 + i0 + i * kPer + lane / kLanes;
+          w[i] = j < hi ? __ldg(reinterpret_cast<const uint2*>(src + (int64_t)(j & (p.page_size - 1)) * sd.stride_token * (BITS / 8))) : make_uint2(0u, 0u);
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          bool is_nan = false, is_inf = false, large = small_scale;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t x = k ? w[i].y : w[i].x;
+            if (BITS == 8) {
+              is_nan |= __vcmpeq4(x & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0;
+            } else {
+              const uint32_t lo = x & 0x7fffu, up = x >> 16 & 0x7fffu;
+              is_nan |= max(lo, up) > 0x7f80u;
+              is_inf |= lo == 0x7f80u || up == 0x7f80u;
+              large |= (lo >= (127u + 80u) << 7 && lo < 0x7f80u) || (up >= (127u + 80u) << 7 && up < 0x7f80u);
+            }
+          }
+          const uint32_t nans = __ballot_sync(0xffffffffu, is_nan), infs = __ballot_sync(0xffffffffu, is_inf), larges = __ballot_sync(0xffffffffu, large);
+          if (!(nans | infs | larges)) continue;
+#pragma unroll 1
+          for (int r = 0; r < kPer; ++r) {
+            const int j = j0 + i0 + i * kPer + r;
+            if (j >= hi) break;
+            const bool n = nans >> (r * kLanes) & kRow, f = infs >> (r * kLanes) & kRow, l = larges >> (r * kLanes) & kRow;
+            const bool see = j <= pos && j < s.kv_len && (a.window == 0 || j > pos - a.window || j < a.sinks);
+            spoilt |= see ? l : n || f;
+            saw_nan |= see && n;
+            saw_inf |= see && f;
+          }
+        }
+      }
+      if (!__any_sync(0xffffffffu, want && !spoilt)) return want;
+    }
+  }
+  return want && (spoilt || (nan && saw_inf && !saw_nan));
 }
 
 constexpr int kSms = 152;  // GB300

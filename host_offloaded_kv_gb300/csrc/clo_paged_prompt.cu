@@ -24,8 +24,8 @@
 // the largest so far; exact in the end, as sum and accumulator share the reference).
 //
 // A masked weight is zero, but zero times NaN is not.  V behind the last visible token (a page's end, where memory may never
-// have been written) is cleared in the operand tile; rows that end with an infinity or NaN all the same, because V has one
-// where they do not look, or where they do, are computed again one by one.
+// have been written) is cleared in the operand tile.  Rows that end with an infinity or NaN all the same are computed again, one
+// by one, if V has one where they do not look (spoilt_rows looks V over once); what comes from tokens that they see stays.
 //
 // 8192 tokens, 32 over 8 heads of 128, causal, bf16: 403 to 411 us, 1.35 PFLOP/s, 70 % of a library product's rate: a token tile takes
 // both lanes 2770 cycles, of which the products 2048, and the diagonal's tiles count half.  2048 tokens over 32,768 of 8-bit
@@ -159,6 +159,7 @@ struct Shared {
   uint32_t there[META];
   uint32_t tmem;
   int failed;
+  int odd;                         // a row of the block ended as no finite number
   int64_t first, last, total;      // the block's share of the units' costs, [first, last) of total
   int64_t base;                    // where the first unit of the share begins
   PartRecord record;               // of the unit that the share leaves unfinished
@@ -380,6 +381,85 @@ __device__ void find_share(const AttendParams& a, int lane, S& sh) {
   }
 }
 
+// The block's walk over its units; every role takes it by itself.  `visit` is called with each unit that the block has a part of.
+template <int TILES, typename S, typename F>
+__device__ __forceinline__ void walk_units(const AttendParams& a, const S& sh, bool cuts, F&& visit) {
+  int64_t base = sh.base;
+  const int64_t first = sh.first, last = sh.last;
+  if (base >= last) return;
+  Unit u;
+  set_seq<TILES>(a, sh.start[0], &u);
+  u.qb = sh.start[1];
+  u.kvh = sh.start[2];
+  set_rows<TILES>(a, &u);
+  while (true) {
+    const int64_t end = base + u.all + kUnitCost;
+    bool part = base >= first;  // the unit begins in the share: whole units, and those without a token, go by that alone
+    u.t_begin = 0;
+    u.n = u.all;
+    if (cuts && u.all > 0) {
+      u.t_begin = base >= first ? 0 : max((int)(first - base) - kUnitCost, 0);
+      u.n = (end <= last ? u.all : max((int)(last - base) - kUnitCost, 0)) - u.t_begin;
+      part = u.n > 0;
+    }
+    if (part && !visit(u, base)) return;
+    base = end;
+    if (base >= last || !next_unit<TILES>(a, &u)) return;
+  }
+}
+
+// Rows that ended as no finite numbers: rightly, or to be computed again?  At the block's end, over its units once more and out of line, so
+// that the tiles' loops keep their registers (among them it cost 2 to 3 % with 8-bit pages).  A prompt of 8192 tokens, 8 over 2 heads, with
+// a NaN in one head's first V: 1.0 ms for 0.13 without; every such row computed again took 100 ms.
+template <int D, int BITS, int TILES, typename S>
+__device__ __noinline__ void look_again(const AttendParams a, const S& sh) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  walk_units<TILES>(a, sh, sh.cuts, [&](const Unit& u, int64_t) {
+    const bool full = u.n == u.all;
+    for (int r0 = warp * 32; r0 < TILES * kRows && u.row0 + r0 < u.rows; r0 += blockDim.x) {
+      const int row = u.row0 + r0 + lane;
+      bool spoilt = false, nan = false;
+      float* part = nullptr;
+      if (row < u.rows) {
+        if (full) {
+          const uint16_t* o = a.out + row_offset(a, u.s.first, u.kvh, row, a.o_token, a.o_head);
+#pragma unroll 1
+          for (int e = 0; e < D; e += 8) {
+            float y[8];
+            unpack8(*reinterpret_cast<const uint4*>(o + e), y);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              nan |= isnan(y[k]);
+              spoilt |= !isfinite(y[k]);
+            }
+          }
+        } else {
+          part = part_of(a, blockIdx.x, u.t_begin == 0 ? 1 : 0, TILES * kRows, D) + (int64_t)(r0 + lane) * (D + 4);
+          spoilt = !isfinite(part[D + 1]);
+#pragma unroll 1
+          for (int e = 0; e < D; ++e) {
+            nan |= isnan(part[e]);
+            spoilt |= !isfinite(part[e]);
+          }
+        }
+      }
+      if (!__any_sync(0xffffffffu, spoilt)) continue;
+      if (spoilt && !full) part[D + 2] = kPartSeen;
+      spoilt = spoilt_rows<D, BITS>(a, u.b, u.kvh, u.s, u.tl, u.t_begin, u.t_begin + u.n, kTok, visible_of(u.pos_last, u.s.kv_len, a.window, a.sinks).hi,
+                                    spoilt, u.s.pos0 + token_of_row(a, min(row, u.rows - 1)), nan, lane);
+      if (!full) {
+        if (spoilt) part[D + 2] = kPartSpoilt;
+        continue;
+      }
+      for (unsigned again = __ballot_sync(0xffffffffu, row_end(sh.failed != 0, spoilt) == RowEnd::again); again; again &= again - 1) {
+        const int gr = u.row0 + r0 + __ffs(again) - 1;
+        attend_row<D, BITS>(a, u.b, u.s, gr / a.group, u.kvh * a.group + gr % a.group, lane);
+      }
+    }
+    return true;
+  });
+}
+
 template <int D, int BITS, int TILES>
 __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_many(const AttendParams a, const __grid_constant__ PageMaps maps) {
   using C = Cfg<D, BITS, TILES>;
@@ -416,7 +496,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
     }
     for (int i = 0; i < TILES; ++i) mbar_init(&sh.q_ready[i], 256 / TILES);
     for (int i = 0; i < kMeta; ++i) mbar_init(&sh.meta[i], 1);
-    sh.failed = 0;
+    sh.failed = sh.odd = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
@@ -432,32 +512,8 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
   const uint32_t tmem = sh.tmem;
   constexpr uint32_t kS[2] = {0, 128}, kO[2] = {256, 384};
 
-  // The block's walk over its units; every role takes it by itself.  `visit` is called with each unit that the block has a part of.
   const bool cuts = sh.cuts;
-  auto walk = [&](auto&& visit) {
-    int64_t base = sh.base;
-    const int64_t first = sh.first, last = sh.last;
-    if (base >= last) return;
-    Unit u;
-    set_seq<TILES>(a, sh.start[0], &u);
-    u.qb = sh.start[1];
-    u.kvh = sh.start[2];
-    set_rows<TILES>(a, &u);
-    while (true) {
-      const int64_t end = base + u.all + kUnitCost;
-      bool part = base >= first;  // the unit begins in the share: whole units, and those without a token, go by that alone
-      u.t_begin = 0;
-      u.n = u.all;
-      if (cuts && u.all > 0) {
-        u.t_begin = base >= first ? 0 : max((int)(first - base) - kUnitCost, 0);
-        u.n = (end <= last ? u.all : max((int)(last - base) - kUnitCost, 0)) - u.t_begin;
-        part = u.n > 0;
-      }
-      if (part && !visit(u, base)) return;
-      base = end;
-      if (base >= last || !next_unit<TILES>(a, &u)) return;
-    }
-  };
+  auto walk = [&](auto&& visit) { walk_units<TILES>(a, sh, cuts, visit); };
 
   // Operand tiles of a unit in ring order: e = 0 is K(0), e = 2 j + 1 is K(j + 1), e = 2 j + 2 is V(j), without K(n); the ring's count
   // runs on from unit to unit.  Lane t takes token tiles first_of(t), + kStep, ...
@@ -703,6 +759,8 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
           }
           if (!full) {
 #pragma unroll
+            for (int i = 0; i < 32; ++i) odd = fmaf(__uint_as_float(o[i]), 0.f, odd);
+#pragma unroll
             for (int i = 0; i < 32; i += 4) *reinterpret_cast<uint4*>(part + 32 * c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
           } else {
             // through the row tile's Q, which is done with, so that rows leave in whole lines
@@ -718,6 +776,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
             }
           }
         }
+        if (__any_sync(0xffffffffu, row_ok && odd != 0.f) && lane == 0) sh.odd = 1;
         if (full) {
           __syncwarp();
           constexpr int kLanes = D / 8;
@@ -730,11 +789,14 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
               *reinterpret_cast<uint4*>(dst.p) = *reinterpret_cast<const uint4*>(from + i * 128 + ((c ^ (r0 + i)) & 7) * 16);
             dst.next();
           }
-          __syncwarp();
-          unsigned again = __ballot_sync(0xffffffffu, row_ok && row_end(lost, odd != 0.f) == RowEnd::again);
-          for (; again; again &= again - 1) {
-            const int gr = row0 + my_tile * kRows + (warp & 3) * 32 + __ffs(again) - 1;
-            attend_row<D, BITS>(a, u.b, s, gr / a.group, kvh * a.group + gr % a.group, lane);
+          if (BITS == 8) {
+            // a sum of weights past fp32's range (scales near 2^-100)
+            __syncwarp();
+            unsigned again = __ballot_sync(0xffffffffu, row_ok && row_end(lost, l == INFINITY) == RowEnd::again);
+            for (; again; again &= again - 1) {
+              const int gr = row0 + my_tile * kRows + (warp & 3) * 32 + __ffs(again) - 1;
+              attend_row<D, BITS>(a, u.b, s, gr / a.group, kvh * a.group + gr % a.group, lane);
+            }
           }
         }
       }
@@ -1003,6 +1065,8 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }
+
+  if (sh.odd != 0 && sh.failed == 0) look_again<D, BITS, TILES>(a, sh);
 }
 
 // Joins the parts of the units that the cuts met: a block per record and eight rows, a warp per row.
@@ -1022,7 +1086,7 @@ __global__ void __launch_bounds__(256) k_attend_many_join(const AttendParams a) 
   for (int c = blockIdx.x + lane; c <= rec.last; c += 32) mx = fmaxf(mx, part(c)[D]);
   mx = warp_max(mx);
   float l = 0.f, o[E];
-  bool lost = false;
+  bool lost = false, spoilt = false, seen = false;
 #pragma unroll
   for (int i = 0; i < E; ++i) o[i] = 0.f;
 #pragma unroll 4
@@ -1030,6 +1094,8 @@ __global__ void __launch_bounds__(256) k_attend_many_join(const AttendParams a) 
     const float* q = part(c);
     const float4 ml = *reinterpret_cast<const float4*>(q + D);
     lost |= ml.z == kPartLost;
+    spoilt |= ml.z == kPartSpoilt;
+    seen |= ml.z == kPartSeen;
     const float f = ml.x == mx ? 1.f : exp2_fast(ml.x - mx);
     l = fmaf(ml.y, f, l);
 #pragma unroll
@@ -1042,11 +1108,24 @@ __global__ void __launch_bounds__(256) k_attend_many_join(const AttendParams a) 
   float odd = l * 0.f;
 #pragma unroll
   for (int i = 0; i < E; ++i) odd = fmaf(o[i], 0.f, odd);
-  if (row_end(lost, __any_sync(0xffffffffu, odd != 0.f)) == RowEnd::again) {  // (a lost part's sum is NaN)
-    attend_row<D, BITS>(a, rec.b, s, gr / a.group, rec.kvh * a.group + gr % a.group, lane);
-    return;
-  }
   const float inv = l == 0.f ? 0.f : 1.f / l;
+  if (__any_sync(0xffffffffu, odd != 0.f)) {
+    // no part says so: the join itself passed fp32's range; NaN out of parts without one: an infinity met a weight of zero, or its opposite
+    bool nan = false, had_nan = false;
+#pragma unroll
+    for (int i = 0; i < E; ++i) nan |= isnan(o[i] * inv);
+    for (int c = blockIdx.x; c <= rec.last; ++c) {
+      const float* q = part(c);
+      had_nan |= isnan(q[D + 1]);
+#pragma unroll
+      for (int i = 0; i < E; ++i) had_nan |= isnan(q[lane * E + i]);
+    }
+    spoilt |= !seen || (__any_sync(0xffffffffu, nan) && !__any_sync(0xffffffffu, had_nan));
+    if (row_end(lost, spoilt) == RowEnd::again) {
+      attend_row<D, BITS>(a, rec.b, s, gr / a.group, rec.kvh * a.group + gr % a.group, lane);
+      return;
+    }
+  }
   uint16_t* dst = a.out + row_offset(a, s.first, rec.kvh, gr, a.o_token, a.o_head) + lane * E;
 #pragma unroll
   for (int i = 0; i < E; i += 2) *reinterpret_cast<uint32_t*>(dst + i) = l == 0.f ? 0u : pack_bf16(o[i] * inv, o[i + 1] * inv);

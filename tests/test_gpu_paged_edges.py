@@ -1,4 +1,6 @@
 """Edges of the calls over HBM pages on the GPU: what padded batches, other streams, odd bounds and extreme values meet."""
+import math
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -107,3 +109,112 @@ def test_workspace_belongs_to_the_named_stream(clo):
     torch.cuda.synchronize()
     assert held() >= before + size
     assert torch.equal(out, want)
+
+
+# --------------------------------------------------------------------------------------------- V that is not finite
+def put_v(c, marks):
+    """V of (sequence, kv head, token, element) set to a value, on the CPU side of a Case (before device())."""
+    for b, h, j, e, value in marks:
+        page = int(c.table[b, j // c.page])
+        for t in (c.codes[1], c.pages.val[1]):
+            if t.dtype is torch.float8_e4m3fn:
+                t.view(torch.uint8)[page, h, j % c.page, e] = 0x7f
+            else:
+                t[page, h, j % c.page, e] = value
+
+
+def with_marks(c, q, marks, window=0, sinks=0):
+    """(want, bound): the fp64 attention with V zero at the marks, then each mark's value where a row sees it."""
+    vals = c.pages.val[1].clone()
+    for b, h, j, e, _ in marks:
+        c.pages.val[1][int(c.table[b, j // c.page]), h, j % c.page, e] = 0.0
+    want, spread, reach = dense(c, q, window, sinks)
+    c.pages.val[1] = vals
+    group = q.shape[1] // c.hkv
+    add = torch.zeros_like(want)
+    for b, h, j, e, value in marks:
+        first, n, kv = c.seqs[b]
+        pos = torch.arange(kv - n, kv)
+        see = (pos >= j) & ((pos - window < j) | (j < sinks) if window else True)
+        add[first:first + n, h * group:(h + 1) * group, e] += torch.where(see, value, 0.0)[:, None]
+    return want + add, ref.attention_bound(want, spread, reach, c.d, c.bits)
+
+
+NAN, INF = float("nan"), float("inf")
+SPOILT = [
+    # seqs, hkv, group, d, page, window, sinks, marks (8-bit pages: all NaN)
+    ([(1300, 1300)], 2, 4, 128, 64, 0, 0, [(0, 0, 0, 5, NAN), (0, 1, 300, 9, INF), (0, 1, 1000, 9, -INF), (0, 1, 1001, 70, -INF)]),
+    ([(1300, 1300)], 2, 4, 64, 16, 0, 0, [(0, 0, 1299, 63, NAN), (0, 1, 640, 0, NAN), (0, 1, 641, 0, INF)]),
+    ([(900, 1500), (20, 20)], 2, 4, 128, 32, 300, 5, [(0, 0, 2, 1, NAN), (0, 0, 6, 2, NAN), (0, 1, 700, 3, INF), (1, 1, 19, 4, NAN)]),
+    # one row tile, units cut between blocks and joined
+    ([(40, 9000)], 2, 2, 128, 64, 0, 0, [(0, 0, 100, 7, NAN), (0, 1, 8999, 8, INF), (0, 1, 8970, 9, NAN)]),
+    ([(40, 9000)], 2, 2, 64, 128, 2000, 3, [(0, 0, 6990, 7, NAN), (0, 0, 1, 8, INF), (0, 1, 4, 9, NAN)]),
+    # two row tiles, joined
+    ([(200, 6000)], 2, 3, 128, 16, 0, 0, [(0, 0, 0, 127, NAN), (0, 1, 5900, 3, NAN)]),
+]
+
+
+@pytest.mark.parametrize("bits", [16, 8])
+@pytest.mark.parametrize("case", range(len(SPOILT)))
+def test_rows_are_not_finite_where_they_see_it(clo, case, bits):
+    seqs, hkv, group, d, page, window, sinks, marks = SPOILT[case]
+    if bits == 8:
+        marks = [(b, h, j, e, NAN) for b, h, j, e, _ in marks]
+    c = Case(clo, seqs, hkv, d, page, bits, seed=80 + case)
+    put_v(c, marks)
+    c.device()
+    q = bf16(rand(81 + case, c.total, hkv * group, d))
+    want, bound = with_marks(c, q, marks, window, sinks)
+    check(c.attend(q, window, sinks), want, bound)
+    check(c.attend(q, window, sinks, workspace=torch.empty(16, dtype=torch.uint8, device="cuda")), want, bound, "no workspace")
+
+
+@pytest.mark.parametrize("rows,kv", [(300, 300), (40, 5000)])
+def test_large_values_and_infinities_of_no_weight(clo, rows, kv):
+    # values whose weighted sum passes fp32's range before it is divided by the weights' sum, and an infinity of a weight below fp32's
+    # normal range (2^-134 of the row's largest), whose product with it is an infinity all the same
+    d = 128
+    c = Case(clo, [(rows, kv)], 1, d, 64, 16, seed=91)
+    for t in (c.codes[0], c.pages.val[0]):
+        t[..., 0] = 0.0
+    put_v(c, [(0, 0, j, 3, 2.0 ** 119) for j in range(kv)] + [(0, 0, 5, 4, INF)])
+    page = int(c.table[0, 0])
+    for t in (c.codes[0], c.pages.val[0]):
+        t[page, 0, 5] = 0.0
+        t[page, 0, 5, 0] = -64.0
+        t[page, 0, 6:7, 0] = 64.0
+    c.device()
+    q = bf16(rand(92, rows, 2, d) * 0.01)
+    q[..., 0] = bf16(torch.tensor(134 * math.log(2) / 128 * math.sqrt(d)))
+    got = c.attend(q)[..., :5].cpu().double()
+    pos = torch.arange(kv - rows, kv)
+    late = pos >= 6
+    # channel 3: the weighted mean of equal values; weights are rounded to bf16 above and not below the line
+    assert ((got[late][..., 3] / 2.0 ** 119 - 1).abs() <= 2 * 2.0 ** -8).all()
+    assert (got[late][..., 4] == INF).all()
+
+
+@pytest.mark.parametrize("bits", [16, 8])
+@pytest.mark.parametrize("value", [NAN, INF])
+def test_one_value_that_is_not_finite_does_not_stall_a_prompt(clo, bits, value):
+    if bits == 8 and value == INF:
+        pytest.skip("8-bit pages hold no infinity")
+    times = []
+    for marks in ([], [(0, 0, 0, 5, value)]):
+        c = Case(clo, [(8192, 8192)], 2, 128, 64, bits, seed=95)
+        put_v(c, marks)
+        c.device()
+        q = bf16(rand(96, 8192, 8, 128)).cuda()
+        out = c.attend(q)
+        assert bool(torch.isfinite(out).all()) == (not marks)
+        runs = []
+        for _ in range(5):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            c.attend(q, out=out)
+            b.record()
+            b.synchronize()
+            runs.append(a.elapsed_time(b))
+        times.append(min(runs))
+    print(f"{times[0] * 1e3:.0f} us, with it {times[1] * 1e3:.0f} us")
+    assert times[1] < 20 * times[0]  # row by row it would be hundreds of times

@@ -221,6 +221,6 @@ int main() {
     for name in ("clo_paged_few.cuh", "clo_paged_prompt.cu"):
         text = open(os.path.join(csrc, name)).read()
         calls = [m for m in range(len(text)) if text.startswith("attend_row<", m)]
-        assert len(calls) == 2
+        assert len(calls) >= 2
         for at in calls:
             assert "row_end(" in text[at - 1500:at], f"{name}: a row is computed again unasked"
