@@ -200,6 +200,7 @@ __global__ void __launch_bounds__(kThreads) k_attend_few(const AttendParams a, c
   while (base < share.last && b < p.batch) {
     const int rows = s.n * a.group;
     if (rows == 0) {
+      if (!a.part) break;  // whole units have a block each: the next sequence's is not this one's
       next_seq();
       continue;
     }

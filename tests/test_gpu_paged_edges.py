@@ -218,3 +218,50 @@ def test_one_value_that_is_not_finite_does_not_stall_a_prompt(clo, bits, value):
         times.append(min(runs))
     print(f"{times[0] * 1e3:.0f} us, with it {times[1] * 1e3:.0f} us")
     assert times[1] < 20 * times[0]  # row by row it would be hundreds of times
+
+
+# --------------------------------------------------------------------------------------------- padded decode batches
+def best_time(call, n=5):
+    runs = []
+    for _ in range(n):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        call()
+        b.record()
+        b.synchronize()
+        runs.append(a.elapsed_time(b))
+    return min(runs)
+
+
+@pytest.mark.parametrize("bits", [16, 8])
+def test_sequences_without_rows_cost_no_work(clo, bits):
+    # inactive slots of a decode batch in front of an active one, whole units (no workspace): each read the active one's pages
+    none = torch.empty(16, dtype=torch.uint8, device="cuda")
+    times, q = [], bf16(rand(101, 1, 8, 128)).cuda()
+    for slots in (0, 600):
+        c = Case(clo, [(0, 0)] * slots + [(1, 20000)], 2, 128, 64, bits, seed=100)
+        c.device()
+        got = c.attend(q, workspace=none)
+        want, spread, reach = dense(c, q.cpu())
+        check(got, want, ref.attention_bound(want, spread, reach, 128, bits))
+        times.append(best_time(lambda: c.attend(q, workspace=none)))
+    print(f"{times[0] * 1e3:.0f} us, with 600 inactive slots {times[1] * 1e3:.0f} us")
+    assert times[1] < 2 * times[0]  # 601 times the bytes otherwise
+
+
+@pytest.mark.parametrize("d,bits", [(128, 16), (64, 8)])
+def test_decode_batches_of_any_pattern_of_rows(clo, d, bits):
+    # sequences without rows first, last and between, with and without tokens, beside longer ones; whole units and shares
+    for seed in range(6):
+        pick = torch.randint(0, 4, (40,), generator=torch.Generator().manual_seed(seed)).tolist()
+        seqs = [[(0, 0), (0, 70), (1, 300 + 97 * i), (2, 1 + 5 * i)][k] for i, k in enumerate(pick)]
+        if not any(n for n, _ in seqs):
+            continue
+        seqs = [(n, max(n, kv)) for n, kv in seqs]
+        c = Case(clo, seqs, 2, d, 32, bits, seed=seed)
+        c.device()
+        q = bf16(rand(110 + seed, c.total, 6, d))
+        want, spread, reach = dense(c, q)
+        bound = ref.attention_bound(want, spread, reach, d, bits)
+        check(c.attend(q), want, bound)
+        check(c.attend(q, workspace=torch.empty(16, dtype=torch.uint8, device="cuda")), want, bound, "no workspace")
