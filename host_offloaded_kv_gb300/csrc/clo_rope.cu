@@ -399,6 +399,7 @@ __global__ void __launch_bounds__(kThreads) k_paged_append(const AppendParams a)
     const int b = seq_of_row(a.c, (int)t, lane);
     if (b >= a.c.batch) return false;
     const SeqRows s = seq_rows(a.c, b);
+    if (t - s.first >= s.n) return false;  // beyond max_q: left out, as its key is
     *pos = a.positions ? __ldg(a.positions + t) : (int64_t)s.pos0 + (t - s.first);
     return true;
   };

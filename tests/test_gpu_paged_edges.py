@@ -265,3 +265,33 @@ def test_decode_batches_of_any_pattern_of_rows(clo, d, bits):
         bound = ref.attention_bound(want, spread, reach, d, bits)
         check(c.attend(q), want, bound)
         check(c.attend(q, workspace=torch.empty(16, dtype=torch.uint8, device="cuda")), want, bound, "no workspace")
+
+
+# --------------------------------------------------------------------------------------------- rows beyond max_q
+@pytest.mark.parametrize("bits", [16, 8])
+def test_rows_beyond_max_q_are_left_out_by_every_call(clo, bits):
+    # of sequences with 9, 2 and 6 rows, the first 4 rows at most; keys, queries, read-back and attention agree on it
+    d, hkv, hq, most = 64, 2, 4, 4
+    seqs = [(9, 40), (2, 2), (6, 6)]
+    c = Case(clo, seqs, hkv, d, 16, bits, seed=120)
+    cache = c.device()
+    before = [p.clone() for p in (cache.k_pages, cache.v_pages)]
+    plan = clo.clo_rope_plan_init(rot_dim=d)
+    k, q = bf16(rand(121, c.total, hkv, d)).cuda(), bf16(rand(122, c.total, hq, d)).cuda()
+    mark = lambda h: torch.full((c.total, h, d), 7.0, dtype=BF16, device="cuda")  # noqa: E731
+    q_out, k_out, v_out, out = mark(hq), mark(hkv), mark(hkv), mark(hq)
+    cache.append(k, k, c.starts, c.lens, c.tab, rope=plan, q=q, q_out=q_out, max_q=most)
+    cache.read(c.starts, c.lens, c.tab, c.total, k_out=k_out, v_out=v_out, max_q=most)
+    cache.attention(q, c.starts, c.lens, c.tab, out=out, max_q=most)
+    left = torch.cat([torch.arange(n) >= most for n, _ in seqs]).cuda()
+    for t in (q_out, k_out, v_out, out):
+        assert bool((t[left] == 7.0).all()) and not bool((t[~left] == 7.0).all(-1).any())
+    pos = torch.cat([torch.arange(kv - n, kv) for n, kv in seqs])
+    want = clo.clo_rope(plan, q, pos.cuda())
+    assert torch.equal(q_out[~left], want[~left])
+    for pages, old in zip((cache.k_pages, cache.v_pages), before):
+        for first, n, kv in c.seqs:
+            for i in range(most, n):
+                j, b = kv - n + i, [s[0] for s in c.seqs].index(first)
+                page = int(c.table[b, j // 16])
+                assert torch.equal(pages.view(torch.uint8)[page, :, j % 16], old.view(torch.uint8)[page, :, j % 16])
