@@ -36,6 +36,11 @@ constexpr int kStages = 2;
 constexpr int kFewSmem = kWarps * kStages * kStageBytes + 1024;
 constexpr int kWave = 2 * kSms;  // blocks: two to an SM
 
+// 8-bit pages: weights up to 2^14 (fp16 then holds them down to 2^-38 of the largest) are divided by their page's V scale, which may be as
+// small as 1e-30, before they are summed.  The sums are kept 2^7 smaller, so that two million such weights stay in fp32's range; the
+// reciprocal of the largest scale, 2^-135 then, still has 14 bits.
+constexpr float kSumDown = 0x1p-7f;
+
 template <int D, int BITS>
 struct Tile {
   static constexpr int kRowBytes = D * BITS / 8;
@@ -154,7 +159,7 @@ template <int D, int BITS, int NT>
 __global__ void __launch_bounds__(kThreads) k_attend_few(const AttendParams a, const __grid_constant__ PageMaps maps) {
   using T = Tile<D, BITS>;
   constexpr int TOK = T::kTokens, KM = T::kM, KD = D / 16, ROWS = 8 * NT;
-  constexpr float kOff = BITS == 16 ? 0.f : 14.f;  // weights up to 2^14: fp16 holds them down to 2^-38 of the largest
+  constexpr float kOff = BITS == 16 ? 0.f : 14.f, kDown = BITS == 16 ? 1.f : kSumDown;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t s_full[kWarps][kStages];
   __shared__ __align__(16) float s_scale[kWarps][kStages][2][4];
@@ -408,7 +413,7 @@ __global__ void __launch_bounds__(kThreads) k_attend_few(const AttendParams a, c
           ks = fmaxf(s_scale[warp][st][0][mt], kMinScale);
           const float vs = fmaxf(s_scale[warp][st][1][mt], kMinScale);
           lvs = __log2f(vs);
-          inv_vs[mt] = __frcp_rn(vs);
+          inv_vs[mt] = __frcp_rn(vs) * kDown;
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -583,7 +588,7 @@ __global__ void __launch_bounds__(kThreads) k_attend_few(const AttendParams a, c
     } else if (row_end(s_dead, s_odd) != RowEnd::again) {  // a lost copy has made the sums NaN
       for (int e = tid; e < rows * (D / 2); e += kThreads) {
         const int r = e / (D / 2), d2 = e % (D / 2) * 2;
-        const float sum = s_cl[r], inv = 1.f / sum;
+        const float sum = s_cl[r], inv = 1.f / sum * kDown;
         const float2 o = *reinterpret_cast<const float2*>(part + r * (D + 4) + d2);
         *reinterpret_cast<uint32_t*>(a.out + row_offset(a, s.first, kvh, r, a.o_token, a.o_head) + d2) = sum == 0.f ? 0u : pack_bf16(o.x * inv, o.y * inv);
       }
@@ -656,7 +661,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_attend_join(const AttendParams
     l += s_l[i] * f;
     o[0] += s_o[i][d] * f;
   }
-  a.out[row_offset(a, s.first, kvh, r, a.o_token, a.o_head) + d] = (uint16_t)pack_bf16(l == 0.f ? 0.f : o[0] / l, 0.f);
+  a.out[row_offset(a, s.first, kvh, r, a.o_token, a.o_head) + d] = (uint16_t)pack_bf16(l == 0.f ? 0.f : o[0] / l * (BITS == 16 ? 1.f : kSumDown), 0.f);
 }
 
 // Bytes of workspace: none where no unit can be long, or no unit so long that its block would outlast the others by much.

@@ -295,3 +295,44 @@ def test_rows_beyond_max_q_are_left_out_by_every_call(clo, bits):
                 j, b = kv - n + i, [s[0] for s in c.seqs].index(first)
                 page = int(c.table[b, j // 16])
                 assert torch.equal(pages.view(torch.uint8)[page, :, j % 16], old.view(torch.uint8)[page, :, j % 16])
+
+
+# --------------------------------------------------------------------------------------------- scales at the ends of their range
+@pytest.mark.parametrize("power", [1e-30, 2.0 ** -64, 3e33])
+@pytest.mark.parametrize("seqs", [[(1, 60000), (1, 25000)], [(1, 30000), (2, 700)] + [(1, 24000)] * 38])
+def test_decode_with_scales_at_the_ends_of_their_range(clo, seqs, power):
+    # weights that are nearly equal over many tokens, divided by such scales, sum up to 1e34 times the tokens
+    c = Case(clo, seqs, 2, 64, 128, 8, seed=130)
+    c.scales[1] = (c.scales[1] * (64 if power > 1e-30 else 0) * power).clamp(min=1e-30)
+    c.pages.scale[1] = c.scales[1].double()
+    c.device()
+    q = bf16(rand(131, c.total, 8, 64) * 1e-3)
+    want, spread, reach = dense(c, q)
+    assert float(want.abs().max()) < 3e38
+    unit = float(want.abs().max())  # (the bound's floor of 1e-30 is about values near one)
+    bound = ref.attention_bound(want / unit, spread / unit, reach, 64, 8)
+    check(c.attend(q).double() / unit, want / unit, bound)
+    check(c.attend(q, workspace=torch.empty(16, dtype=torch.uint8, device="cuda")).double() / unit, want / unit, bound, "no workspace")
+
+
+def test_prompt_with_scales_at_the_end_of_their_range(clo):
+    # weights of up to 2^15 (the running maximum lags by up to 2^8) over scales of 1e-30: a whole unit's sum passes fp32's range
+    rows, kv, d = 200, 20000, 64
+    c = Case(clo, [(rows, kv)], 1, d, 64, 8, seed=133)
+    c.scales[1] = torch.full_like(c.scales[1], 1e-30)
+    c.scales[0] = torch.full_like(c.scales[0], 2.0 ** -8)
+    for t in (c.codes[0], c.pages.val[0]):
+        t.view(torch.uint8).zero_() if t.dtype is torch.float8_e4m3fn else t.zero_()
+    for j in range(256, kv):
+        page = int(c.table[0, j // 64])
+        c.codes[0].view(torch.uint8)[page, 0, j % 64, 0] = 0x7e  # 448
+        c.pages.val[0][page, 0, j % 64, 0] = 448.0
+    c.pages.scale = [s.double() for s in c.scales]
+    c.device()
+    q = torch.zeros(rows, 2, d, dtype=BF16)
+    q[..., 0] = bf16(torch.tensor(7.5 * math.log(2) * math.sqrt(d) / 1.75))
+    want, spread, reach = dense(c, q)
+    unit = float(want.abs().max())
+    bound = ref.attention_bound(want / unit, spread / unit, reach, d, 8)
+    for work in (None, torch.empty(16, dtype=torch.uint8, device="cuda")):
+        check(c.attend(q, workspace=work).double() / unit, want / unit, bound)
