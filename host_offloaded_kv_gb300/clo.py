@@ -357,7 +357,8 @@ def clo_rope(plan: clo_rope_plan, x, positions, out=None, transpose: bool = Fals
     """Rotates bf16 rows [n_tokens][n_heads][head_dim] by int64 positions [n_tokens] (see include/clo.h).
 
     out: rows of the same shape, x itself for in place, or None for new ones.  transpose applies the
-    transposed rotation, which takes the gradient of the output to that of x.  Returns out."""
+    transposed rotation, which takes the gradient of the output to that of x: the call itself is not recorded by autograd,
+    and refuses an x that requires a gradient while gradients are recorded.  Returns out."""
     r = (_torch_binding or _fast()).rope(ctypes.addressof(plan), x, positions, out, transpose, stream)
     if type(r) is int:
         _check(r, "clo_rope")
@@ -376,7 +377,9 @@ class PagedCache:
     rows of the call, which is right for one sequence; a step of single tokens passes 1).
 
     stream None is torch's current stream; otherwise a torch stream or a handle.  New outputs belong to the stream of the
-    call, as under ``torch.cuda.stream``: another stream that uses them waits for it first."""
+    call, as under ``torch.cuda.stream``: another stream that uses them waits for it first.
+
+    Autograd records none of the calls; rows that require a gradient are refused while it records."""
 
     def __init__(self, k_pages, v_pages, k_scales=None, v_scales=None):
         import torch
@@ -388,6 +391,8 @@ class PagedCache:
                 raise ValueError(f"{name} must be a CUDA tensor")
             if t.get_device() != torch.cuda.current_device():
                 raise ValueError(f"{name} is on {t.device}, not on the current device")
+            if t.requires_grad:
+                raise ValueError(f"{name} requires a gradient, which the calls do not record")
         _fast()
         self.device = k_pages.get_device()
         if k_pages.dtype not in (torch.bfloat16, torch.float8_e4m3fn) or v_pages.dtype is not k_pages.dtype:

@@ -6,6 +6,7 @@
 #include <Python.h>
 
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
@@ -47,11 +48,14 @@ const at::Tensor& tensor_on(PyObject* o, const char* name, int dev, at::ScalarTy
   return t;
 }
 
-// A bf16 [n_tokens][n_heads][head_dim] tensor, any strides but the last.
+// A bf16 [n_tokens][n_heads][head_dim] tensor, any strides but the last.  None of the calls is recorded by autograd: a tensor whose
+// gradient would get lost in one is refused.
 clo_rows rows_of(const at::Tensor& t) { return clo_rows{t.data_ptr(), t.stride(0), t.stride(1)}; }
 
 const at::Tensor& rows(PyObject* o, const char* name, int dev, clo_rows* r) {
   const at::Tensor& t = tensor_on(o, name, dev, at::kBFloat16);
+  if (t.requires_grad() && c10::GradMode::is_enabled())
+    refuse("%s requires a gradient, which the call does not record: detach it, or call under torch.no_grad()", name);
   if (t.dim() != 3) refuse("%s must have the shape [n_tokens][n_heads][head_dim]", name);
   if (t.stride(2) != 1 && t.size(2) > 1) refuse("%s must be contiguous along head_dim", name);
   *r = rows_of(t);

@@ -336,3 +336,36 @@ def test_prompt_with_scales_at_the_end_of_their_range(clo):
     bound = ref.attention_bound(want / unit, spread / unit, reach, d, 8)
     for work in (None, torch.empty(16, dtype=torch.uint8, device="cuda")):
         check(c.attend(q, workspace=work).double() / unit, want / unit, bound)
+
+
+# --------------------------------------------------------------------------------------------- autograd
+def test_rows_that_require_a_gradient_are_refused_while_it_is_recorded(clo):
+    n, h, d = 5, 2, 64
+    plan, pos = clo.clo_rope_plan_init(rot_dim=d), torch.arange(n, device="cuda")
+    x = bf16(rand(141, n, h, d)).cuda()
+    g = x.clone().requires_grad_()
+    c = Case(clo, [(n, n)], h, d, 16, 16, seed=142)
+    cache = c.device()
+    at = (c.starts, c.lens, c.tab)
+    calls = [lambda t: clo.clo_rope(plan, t, pos), lambda t: clo.clo_rope(plan, x, pos, out=t), lambda t: cache.append(t, x, *at),
+             lambda t: cache.append(x, t, *at), lambda t: cache.append(x, x, *at, rope=plan, q=t),
+             lambda t: cache.append(x, x, *at, rope=plan, q=x, q_out=t), lambda t: cache.read(*at, n, k_out=t),
+             lambda t: cache.read(*at, n, v_out=t), lambda t: cache.attention(t, *at), lambda t: cache.attention(x, *at, out=t)]
+    for call in calls:
+        for t in (g, g * 2):  # a leaf, and what was computed from one
+            with pytest.raises(ValueError, match="gradient"):
+                call(t)
+    with pytest.raises(ValueError, match="gradient"):
+        clo.PagedCache(cache.k_pages.clone().requires_grad_(), cache.v_pages)
+    want = clo.clo_rope(plan, x, pos)
+    with torch.no_grad():
+        for call in calls:
+            call(g.clone())
+        assert torch.equal(clo.clo_rope(plan, g, pos), want)
+    with torch.inference_mode():
+        y = clo.clo_rope(plan, g, pos)
+        assert torch.equal(y, want)
+        cache.append(y, y, *at, rope=plan, q=y, q_out=y)
+        cache.attention(y, *at, out=torch.empty_like(y))
+    assert torch.equal(clo.clo_rope(plan, g.detach(), pos), want)
+    assert not want.requires_grad
