@@ -410,7 +410,7 @@ class PagedCache:
             if t is not None:
                 if t.dtype is not torch.float32 or tuple(t.shape) != (n, h) or not t.is_contiguous():
                     raise ValueError(f"{name} must be a contiguous fp32 tensor of shape {(n, h)}")
-        self.k_pages, self.v_pages, self.k_scales, self.v_scales = k_pages, v_pages, k_scales, v_scales
+        self.k_pages, self.v_pages, self.k_scales, self.v_scales = self._tensors = k_pages, v_pages, k_scales, v_scales
         self.n_pages, self.n_kv_heads, self.page_size, self.head_dim, self.kv_bits = n, h, s, d, bits
         self._c = clo_paged_cache(k_pages.data_ptr(), v_pages.data_ptr(), None if k_scales is None else k_scales.data_ptr(),
                                   None if v_scales is None else v_scales.data_ptr(), n, *k_pages.stride()[:3],
@@ -437,7 +437,7 @@ class PagedCache:
         """clo_paged_append: k, v bf16 [total][n_kv_heads][head_dim] into the pages, k rotated by rope; with
         q, returns the rotated queries (q_out, or new rows)."""
         r = _torch_binding.append(self._address, self.device, k, v, q_starts, kv_lens, block_table,
-                                  0 if rope is None else ctypes.addressof(rope), positions, q, q_out, max_q, stream)
+                                  0 if rope is None else ctypes.addressof(rope), positions, q, q_out, max_q, stream, self._tensors)
         if type(r) is int:
             _check(r, "clo_paged_append")
         return r

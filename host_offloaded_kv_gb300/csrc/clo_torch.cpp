@@ -116,6 +116,13 @@ at::Tensor output(PyObject* o, const char* name, int dev, int64_t a, int64_t b, 
   return t;
 }
 
+// Tells autograd that a tensor of the caller's was written, as torch's own in-place operations do (None: there is no such tensor).
+void written(PyObject* o) {
+  if (o == Py_None) return;
+  const at::Tensor& t = THPVariable_Unpack(o);
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 template <typename T>
 const T* vector_of(PyObject* o, const char* name, int dev, at::ScalarType type, int64_t n) {
   const at::Tensor& t = tensor_on(o, name, dev, type);
@@ -184,13 +191,15 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     at::Tensor out = output(a[3], "out", dev, tokens, heads, d, &y, a[5]);
     const clo_status st = clo_rope(address<const clo_rope_plan>(a[0]), &x, &y, pos, tokens, (int32_t)heads, (int32_t)d, PyObject_IsTrue(a[4]),
                                    stream_of(a[5], dev));
-    return st ? PyLong_FromLong(st) : THPVariable_Wrap(out);
+    if (st) return PyLong_FromLong(st);
+    written(a[3]);
+    return THPVariable_Wrap(out);
   });
 }
 
-// cache, cache device, k, v, q_starts, kv_lens, block_table, plan (0: none), positions, q, q_out, max_q, stream
+// cache, cache device, k, v, q_starts, kv_lens, block_table, plan (0: none), positions, q, q_out, max_q, stream, the cache's tensors (a tuple)
 PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 13, [&]() -> PyObject* {
+  return guarded(n, 14, [&]() -> PyObject* {
     const clo_paged_cache* c = address<const clo_paged_cache>(a[0]);
     const int dev = device_of(cuda_tensor(a[2], "k"), "k");
     clo_rows k, v, q{}, y{};
@@ -215,6 +224,8 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const clo_status st = clo_paged_append(c, &b, address<const clo_rope_plan>(a[7]), pos, &k, &v, with_q ? &q : nullptr, with_q ? &y : nullptr, heads,
                                            stream_of(a[12], dev));
     if (st) return PyLong_FromLong(st);
+    for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(a[13]); ++i) written(PyTuple_GET_ITEM(a[13], i));
+    written(a[10]);
     if (with_q) return THPVariable_Wrap(out);
     Py_RETURN_NONE;
   });
@@ -233,6 +244,8 @@ PyObject* read(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const clo_paged_batch b = batch_of(a[2], a[3], a[4], total, a[8], dev, small(a[1], "device"));
     const clo_status st = clo_paged_read(c, &b, &k, &v, stream_of(a[9], dev));
     if (st) return PyLong_FromLong(st);
+    written(a[6]);
+    written(a[7]);
     PyObject* kw = THPVariable_Wrap(kt);
     PyObject* vw = THPVariable_Wrap(vt);
     PyObject* pair = kw && vw ? PyTuple_Pack(2, kw, vw) : nullptr;
@@ -274,7 +287,10 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
       }
     }
     const clo_status st = clo_paged_attention(c, &b, &q, &o, (int32_t)heads, (float)scale, window, sinks, work, bytes, stream);
-    return st ? PyLong_FromLong(st) : THPVariable_Wrap(out);
+    if (st) return PyLong_FromLong(st);
+    written(a[6]);
+    written(a[11]);
+    return THPVariable_Wrap(out);
   });
 }
 

@@ -369,3 +369,41 @@ def test_rows_that_require_a_gradient_are_refused_while_it_is_recorded(clo):
         cache.attention(y, *at, out=torch.empty_like(y))
     assert torch.equal(clo.clo_rope(plan, g.detach(), pos), want)
     assert not want.requires_grad
+
+
+@pytest.mark.parametrize("bits", [16, 8])
+def test_what_a_call_writes_gets_a_new_version(clo, bits):
+    n, h, d = 5, 2, 64
+    plan, pos = clo.clo_rope_plan_init(rot_dim=d), torch.arange(n, device="cuda")
+    x = bf16(rand(151, n, h, d)).cuda()
+    c = Case(clo, [(n, n)], h, d, 16, bits, seed=152)
+    cache = c.device()
+    at = (c.starts, c.lens, c.tab)
+    out = [torch.empty_like(x) for _ in range(5)]
+    work = torch.empty(1 << 16, dtype=torch.uint8, device="cuda")
+    pages = [t for t in (cache.k_pages, cache.v_pages, cache.k_scales, cache.v_scales) if t is not None]
+    read = [x, pos, *at]
+    now = lambda ts: [t._version for t in ts]  # noqa: E731
+
+    def raises(call, ts):
+        old, kept = now(ts), now(read)
+        call()
+        assert all(a > b for a, b in zip(now(ts), old)) and now(read) == kept
+
+    raises(lambda: clo.clo_rope(plan, x, pos, out=out[0]), [out[0]])
+    raises(lambda: cache.append(x, x, *at, rope=plan, q=x, q_out=out[1]), pages + [out[1]])
+    raises(lambda: cache.read(*at, n, k_out=out[2], v_out=out[3]), out[2:4])
+    raises(lambda: cache.attention(x, *at, out=out[4], workspace=work), [out[4], work])
+    old = now(pages)
+    cache.read(*at, n), cache.attention(x, *at)
+    with pytest.raises(ValueError):
+        cache.append(x, x[:2], *at)
+    assert now(pages) == old
+    # autograd notices that what it saved was overwritten
+    w = torch.ones_like(x, requires_grad=True)
+    y = (w * out[0]).sum()
+    clo.clo_rope(plan, x, pos, out=out[0])
+    with pytest.raises(RuntimeError, match="inplace"):
+        y.backward()
+    with torch.inference_mode():  # tensors without a version
+        clo.clo_rope(plan, x, pos, out=torch.empty_like(x))
