@@ -21,6 +21,19 @@ namespace {
 
 struct Raised {};  // a Python error is set
 
+// Other Python threads run while this one allocates or launches: both can wait (for the driver, for room in the launch queue).
+struct WithoutGil {
+  PyThreadState* state = PyEval_SaveThread();
+  WithoutGil() = default;
+  WithoutGil(const WithoutGil&) = delete;
+  ~WithoutGil() { PyEval_RestoreThread(state); }
+};
+template <typename F>
+auto without_gil(F&& f) {
+  WithoutGil released;
+  return f();
+}
+
 [[noreturn]] void refuse(const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);
@@ -92,9 +105,10 @@ void* stream_of(PyObject* o, int dev) {
 // go on to use it on the current stream, so the allocator is told of that one too.
 at::Tensor new_tensor(at::IntArrayRef size, at::ScalarType type, int dev, PyObject* stream, bool returned) {
   const c10::Device device(c10::kCUDA, dev);
-  if (stream == Py_None) return at::detail::empty_cuda(size, type, device, std::nullopt);
+  if (stream == Py_None) return without_gil([&] { return at::detail::empty_cuda(size, type, device, std::nullopt); });
   cudaStream_t st = static_cast<cudaStream_t>(stream_of(stream, dev));
   if (st == cudaStreamLegacy) st = nullptr;  // the same stream by its other name
+  WithoutGil released;
   const c10::cuda::CUDAStream current = c10::cuda::getCurrentCUDAStream(dev);
   const c10::cuda::CUDAStreamGuard guard(st ? c10::cuda::getStreamFromExternal(st, dev) : c10::cuda::getDefaultCUDAStream(dev));
   at::Tensor t = at::detail::empty_cuda(size, type, device, std::nullopt);
@@ -189,8 +203,10 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (heads > INT32_MAX || d > INT32_MAX) refuse("x is too large");
     const int64_t* pos = vector_of<int64_t>(a[2], "positions", dev, at::kLong, tokens);
     at::Tensor out = output(a[3], "out", dev, tokens, heads, d, &y, a[5]);
-    const clo_status st = clo_rope(address<const clo_rope_plan>(a[0]), &x, &y, pos, tokens, (int32_t)heads, (int32_t)d, PyObject_IsTrue(a[4]),
-                                   stream_of(a[5], dev));
+    const clo_rope_plan* plan = address<const clo_rope_plan>(a[0]);
+    const int transpose = PyObject_IsTrue(a[4]);
+    void* stream = stream_of(a[5], dev);
+    const clo_status st = without_gil([&] { return clo_rope(plan, &x, &y, pos, tokens, (int32_t)heads, (int32_t)d, transpose, stream); });
     if (st) return PyLong_FromLong(st);
     written(a[3]);
     return THPVariable_Wrap(out);
@@ -221,8 +237,10 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
       refuse("q_out without q");
     }
     const bool with_q = a[9] != Py_None;
-    const clo_status st = clo_paged_append(c, &b, address<const clo_rope_plan>(a[7]), pos, &k, &v, with_q ? &q : nullptr, with_q ? &y : nullptr, heads,
-                                           stream_of(a[12], dev));
+    const clo_rope_plan* plan = address<const clo_rope_plan>(a[7]);
+    void* stream = stream_of(a[12], dev);
+    const clo_status st =
+        without_gil([&] { return clo_paged_append(c, &b, plan, pos, &k, &v, with_q ? &q : nullptr, with_q ? &y : nullptr, heads, stream); });
     if (st) return PyLong_FromLong(st);
     for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(a[13]); ++i) written(PyTuple_GET_ITEM(a[13], i));
     written(a[10]);
@@ -242,7 +260,8 @@ PyObject* read(PyObject*, PyObject* const* a, Py_ssize_t n) {
     at::Tensor kt = output(a[6], "k_out", dev, total, c->n_kv_heads, c->head_dim, &k, a[9]);
     at::Tensor vt = output(a[7], "v_out", dev, total, c->n_kv_heads, c->head_dim, &v, a[9]);
     const clo_paged_batch b = batch_of(a[2], a[3], a[4], total, a[8], dev, small(a[1], "device"));
-    const clo_status st = clo_paged_read(c, &b, &k, &v, stream_of(a[9], dev));
+    void* stream = stream_of(a[9], dev);
+    const clo_status st = without_gil([&] { return clo_paged_read(c, &b, &k, &v, stream); });
     if (st) return PyLong_FromLong(st);
     written(a[6]);
     written(a[7]);
@@ -286,7 +305,8 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
         work = own.data_ptr();
       }
     }
-    const clo_status st = clo_paged_attention(c, &b, &q, &o, (int32_t)heads, (float)scale, window, sinks, work, bytes, stream);
+    const clo_status st =
+        without_gil([&] { return clo_paged_attention(c, &b, &q, &o, (int32_t)heads, (float)scale, window, sinks, work, bytes, stream); });
     if (st) return PyLong_FromLong(st);
     written(a[6]);
     written(a[11]);

@@ -407,3 +407,38 @@ def test_what_a_call_writes_gets_a_new_version(clo, bits):
         y.backward()
     with torch.inference_mode():  # tensors without a version
         clo.clo_rope(plan, x, pos, out=torch.empty_like(x))
+
+
+# --------------------------------------------------------------------------------------------- threads
+def test_other_threads_run_while_a_launch_waits(clo):
+    # the launch queue is full behind 0.6 s of other work: a call waits for room, and a second thread goes on
+    import threading
+    import time
+
+    x = bf16(rand(161, 1, 1, 64)).cuda()
+    plan, pos, out = clo.clo_rope_plan_init(rot_dim=64), torch.zeros(1, dtype=torch.int64, device="cuda"), torch.empty_like(x)
+    clo.clo_rope(plan, x, pos, out=out)
+    torch.cuda.synchronize()
+    longest, done = [0.0], threading.Event()
+
+    def tick():
+        last = time.perf_counter()
+        while not done.is_set():
+            time.sleep(0.001)
+            now = time.perf_counter()
+            longest[0], last = max(longest[0], now - last), now
+
+    thread = threading.Thread(target=tick)
+    thread.start()
+    try:
+        t0 = time.perf_counter()
+        torch.cuda._sleep(1_200_000_000)
+        for _ in range(5000):
+            clo.clo_rope(plan, x, pos, out=out)
+        took = time.perf_counter() - t0
+        torch.cuda.synchronize()
+    finally:
+        done.set()
+        thread.join()
+    assert took > 0.3, "the queue was not full"
+    assert longest[0] < 0.2, f"the second thread stood still for {longest[0]:.2f} s"
