@@ -205,6 +205,7 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     at::Tensor out = output(a[3], "out", dev, tokens, heads, d, &y, a[5]);
     const clo_rope_plan* plan = address<const clo_rope_plan>(a[0]);
     const int transpose = PyObject_IsTrue(a[4]);
+    if (transpose < 0) throw Raised{};
     void* stream = stream_of(a[5], dev);
     const clo_status st = without_gil([&] { return clo_rope(plan, &x, &y, pos, tokens, (int32_t)heads, (int32_t)d, transpose, stream); });
     if (st) return PyLong_FromLong(st);

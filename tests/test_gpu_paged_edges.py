@@ -442,3 +442,22 @@ def test_other_threads_run_while_a_launch_waits(clo):
         thread.join()
     assert took > 0.3, "the queue was not full"
     assert longest[0] < 0.2, f"the second thread stood still for {longest[0]:.2f} s"
+
+
+def test_arguments_of_no_truth_or_kind_are_refused(clo):
+    x = bf16(rand(171, 2, 2, 64)).cuda()
+    plan, pos = clo.clo_rope_plan_init(rot_dim=64), torch.zeros(2, dtype=torch.int64, device="cuda")
+    out = torch.zeros_like(x)
+    with pytest.raises(RuntimeError, match="ambiguous"):  # the error of the truth value itself
+        clo.clo_rope(plan, x, pos, out=out, transpose=torch.ones(2))
+    torch.cuda.synchronize()
+    assert not out.any()  # refused before the launch
+    for bad in (dict(stream="side"), dict(stream=object()), dict(stream=1.5)):
+        with pytest.raises((AttributeError, TypeError, ValueError)):
+            clo.clo_rope(plan, x, pos, out=out, **bad)
+    c = Case(clo, [(2, 2)], 2, 64, 16, 16, seed=172)
+    cache = c.device()
+    at = (c.starts, c.lens, c.tab)
+    for bad in (dict(max_q=1.5), dict(max_q="1"), dict(window=None), dict(sinks=1 << 40), dict(softmax_scale="x"), dict(workspace=x)):
+        with pytest.raises((TypeError, ValueError)):
+            cache.attention(x, *at, **bad)
