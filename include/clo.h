@@ -381,8 +381,9 @@ CLO_API clo_status clo_rope_plan_init(const clo_rope_config* cfg, clo_rope_plan*
  * other elements are copied.  transpose != 0 applies magnitude * R(position)^T: the gradient
  * of the call.  x and y may be the same rows (same strides); other overlap is not allowed.
  * positions: int64 [n_tokens], any value.  head_dim: even, rot_dim <= head_dim <= 1024.
- * n_tokens or n_heads 0: nothing to do.  Any strides and 2-byte alignment are taken; rows
- * on 16-byte boundaries with rot_dim and head_dim multiples of 16 move in 16-byte words.
+ * n_tokens or n_heads 0: nothing to do.  Any strides and 2-byte alignment are taken.  Rows on
+ * 16-byte boundaries (strides multiples of 8 elements) of 64 or 128 elements with rot_dim a
+ * multiple of 16 move in 16-byte words; all others go pair by pair, at about a sixth of the rate.
  * Errors: CLO_ERR_INVALID, CLO_ERR_CUDA. */
 CLO_API clo_status clo_rope(const clo_rope_plan* plan, const clo_rows* x, const clo_rows* y, const int64_t* positions,
                             int64_t n_tokens, int32_t n_heads, int32_t head_dim, int32_t transpose, void* stream);
