@@ -461,3 +461,96 @@ def test_arguments_of_no_truth_or_kind_are_refused(clo):
     for bad in (dict(max_q=1.5), dict(max_q="1"), dict(window=None), dict(sinks=1 << 40), dict(softmax_scale="x"), dict(workspace=x)):
         with pytest.raises((TypeError, ValueError)):
             cache.attention(x, *at, **bad)
+
+
+# --------------------------------------------------------------------------------------------- rotation at any position
+def rotated_exactly(plan, x, pos):
+    """fp64 rotation by the plan's own turns, position * turn modulo one turn in integers, and what fp32 may be off by: cosine and sine
+    by 7.5e-8, and two roundings of a product and a sum (2^-24 each)."""
+    import numpy as np
+
+    half = plan.rot_dim // 2
+    turn = np.array(plan.turn[:half], dtype=np.uint64)
+    with np.errstate(over="ignore"):
+        frac = pos.numpy().astype(np.uint64)[:, None] * turn
+    angle = torch.from_numpy(frac.astype(np.float64)) * (2 * math.pi / 2.0 ** 64)
+    c, s = (torch.cos(angle) * plan.magnitude)[:, None], (torch.sin(angle) * plan.magnitude)[:, None]
+    y, off = x.double().clone(), torch.zeros(x.shape, dtype=torch.float64)
+    ia = torch.arange(half) * 2 if plan.interleaved else torch.arange(half)
+    ib = ia + 1 if plan.interleaved else ia + half
+    p, q = x.double()[..., ia], x.double()[..., ib]
+    y[..., ia], y[..., ib] = p * c - q * s, q * c + p * s
+    off[..., ia] = off[..., ib] = (7.5e-8 + 2 * 2.0 ** -24) * plan.magnitude * (p.abs() + q.abs())
+    return y, off
+
+
+def rounded_once(got, want, off):
+    """got is want, off by at most `off`, rounded to bf16: within half a step of want, where off reaches the next value too."""
+    got = got.cpu().double()
+    e = torch.frexp(torch.maximum(got.abs(), want.abs()))[1]
+    half_step = torch.ldexp(torch.ones_like(want), e - 9)  # 8 significant bits
+    over = (got - want).abs() / (half_step + off)
+    assert float(over.max()) <= 1.0, f"{float(over.max()):.6f} of the bound"
+
+
+POSITIONS = [(0, 1 << 20), (1 << 31, 1 << 33), (1 << 33, 1 << 45), (1 << 45, (1 << 63) - 1), (-(1 << 62), 0)]
+
+
+@pytest.mark.parametrize("lo,hi", POSITIONS)
+@pytest.mark.parametrize("d,rot,interleaved", [(128, 128, False), (64, 64, True), (128, 48, True), (96, 96, False), (64, 20, False)])
+def test_rope_rounds_once_at_any_position(clo, lo, hi, d, rot, interleaved):
+    n, h = 2000, 4
+    gen = torch.Generator().manual_seed(d + rot)
+    pos = torch.randint(lo, hi, (n,), generator=gen)
+    plan = clo.clo_rope_plan_init(rot_dim=rot, interleaved=interleaved, theta=500000.0, scaling="yarn", factor=16.0, original_max=32768)
+    x = bf16(rand(181, n, h, d))
+    rounded_once(clo.clo_rope(plan, x.cuda(), pos.cuda()), *rotated_exactly(plan, x, pos))
+
+
+@pytest.mark.parametrize("lo,hi", POSITIONS)
+def test_append_rounds_once_at_any_position(clo, lo, hi):
+    n, hkv, hq, d = 700, 2, 4, 128
+    pos = torch.randint(lo, hi, (n,), generator=torch.Generator().manual_seed(182))
+    plan = clo.clo_rope_plan_init(rot_dim=d)
+    c = Case(clo, [(n, n)], hkv, d, 64, 16, seed=183)
+    cache = c.device()
+    k, q = bf16(rand(184, n, hkv, d)), bf16(rand(185, n, hq, d))
+    got = cache.append(k.cuda(), k.cuda(), c.starts, c.lens, c.tab, rope=plan, positions=pos.cuda(), q=q.cuda())
+    rounded_once(got, *rotated_exactly(plan, q, pos))
+    rounded_once(cache.read(c.starts, c.lens, c.tab, n)[0], *rotated_exactly(plan, k, pos))
+
+
+# --------------------------------------------------------------------------------------------- many sequences, C names
+@pytest.mark.parametrize("bits", [16, 8])
+def test_thousands_of_sequences_under_the_c_names(clo, bits):
+    # sequences with 0 to 2 rows, in every block of the lookups, through the functions that carry the C names
+    pick = torch.randint(0, 3, (3000,), generator=torch.Generator().manual_seed(190)).tolist()
+    seqs = [(n, n + 11 * i % 30) for i, n in enumerate(pick)]
+    hkv, hq, d = 2, 4, 64
+    c = Case(clo, seqs, hkv, d, 16, bits, seed=191, width=2)
+    cache = c.device()
+    plan = clo.clo_rope_plan_init(rot_dim=d)
+    k, v, q = bf16(rand(192, c.total, hkv, d)), bf16(rand(193, c.total, hkv, d)), bf16(rand(194, c.total, hq, d))
+    pos = torch.cat([torch.arange(kv - n, kv) for n, kv in seqs])
+    at = (c.starts, c.lens, c.tab)
+    qr = clo.clo_paged_append(cache, k.cuda(), v.cuda(), *at, rope=plan, q=q.cuda(), max_q=2)
+    assert torch.equal(qr, clo.clo_rope(plan, q.cuda(), pos.cuda()))
+    gk, gv = clo.clo_paged_read(cache, *at, c.total, max_q=2)
+    kr = clo.clo_rope(plan, k.cuda(), pos.cuda())
+    if bits == 16:
+        assert torch.equal(gk, kr) and torch.equal(gv, v.cuda())
+    else:  # a code's half step (2^-4 of the value, 2^-10 of the scale at the least) and kr's own rounding
+        for got, x, side in ((gk, kr, 0), (gv, v.cuda(), 1)):
+            scale = (cache.k_scales, cache.v_scales)[side]
+            page = torch.cat([c.table[b, (torch.arange(kv - n, kv) // 16)].long() for b, (n, kv) in enumerate(seqs)]).cuda()
+            bound = (2.0 ** -4 + 2.0 ** -7) * x.double().abs() + 2.0 ** -10 * scale[page].double()[:, :, None]
+            check(got, x.double().cpu(), bound.cpu())
+    # the pages as they are now, for the reference
+    for side, (p, s) in enumerate(((cache.k_pages, cache.k_scales), (cache.v_pages, cache.v_scales))):
+        c.pages.val[side] = p.cpu().double() if s is None else ref.e4m3_values(p.contiguous().view(torch.uint8).cpu())
+        c.scales[side] = None if s is None else s.cpu()
+    want, spread, reach = dense(c, qr.cpu())
+    bound = ref.attention_bound(want, spread, reach, d, bits)
+    check(clo.clo_paged_attention(cache, qr, *at, max_q=2), want, bound)
+    size = clo.clo_paged_attention_workspace(cache, hq, len(seqs), c.total, c.tab.shape[1], 2)
+    assert size == cache.attention_workspace(hq, len(seqs), c.total, c.tab.shape[1], 2)
