@@ -310,6 +310,10 @@ def clo_rope_config_default() -> clo_rope_config:
 def clo_rope_plan_init(cfg: clo_rope_config | None = None, **fields) -> clo_rope_plan:
     """Plan of a rotation: from a config, or from its fields (scaling by name: "none", "linear",
     "bands", "yarn").  The plan holds plain values and may serve any number of calls."""
+    if cfg is not None and fields:
+        raise TypeError("a config and its fields exclude each other")
+    if cfg is not None and not isinstance(cfg, clo_rope_config):
+        raise TypeError(f"cfg must be a clo_rope_config, not {type(cfg).__name__}")
     if cfg is None:
         cfg = clo_rope_config_default()
         for name, value in fields.items():
@@ -326,6 +330,12 @@ def clo_rope_plan_init(cfg: clo_rope_config | None = None, **fields) -> clo_rope
 
 
 _ROPE_FIELDS = {n for n, _ in clo_rope_config._fields_}
+
+
+def _plan_address(plan) -> int:
+    if not isinstance(plan, clo_rope_plan):
+        raise TypeError(f"the plan of a rotation must be a clo_rope_plan, not {type(plan).__name__}")
+    return ctypes.addressof(plan)
 
 
 _torch_binding = None
@@ -359,7 +369,7 @@ def clo_rope(plan: clo_rope_plan, x, positions, out=None, transpose: bool = Fals
     out: rows of the same shape, x itself for in place, or None for new ones.  transpose applies the
     transposed rotation, which takes the gradient of the output to that of x: the call itself is not recorded by autograd,
     and refuses an x that requires a gradient while gradients are recorded.  Returns out."""
-    r = (_torch_binding or _fast()).rope(ctypes.addressof(plan), x, positions, out, transpose, stream)
+    r = (_torch_binding or _fast()).rope(_plan_address(plan), x, positions, out, transpose, stream)
     if type(r) is int:
         _check(r, "clo_rope")
     return r
@@ -437,7 +447,7 @@ class PagedCache:
         """clo_paged_append: k, v bf16 [total][n_kv_heads][head_dim] into the pages, k rotated by rope; with
         q, returns the rotated queries (q_out, or new rows)."""
         r = _torch_binding.append(self._address, self.device, k, v, q_starts, kv_lens, block_table,
-                                  0 if rope is None else ctypes.addressof(rope), positions, q, q_out, max_q, stream, self._tensors)
+                                  0 if rope is None else _plan_address(rope), positions, q, q_out, max_q, stream, self._tensors)
         if type(r) is int:
             _check(r, "clo_paged_append")
         return r

@@ -224,3 +224,18 @@ int main() {
         assert len(calls) >= 2
         for at in calls:
             assert "row_end(" in text[at - 1500:at], f"{name}: a row is computed again unasked"
+
+
+def test_plans_and_configs_are_what_they_say(clo):
+    cfg = clo.clo_rope_config_default()
+    cfg.rot_dim = 64
+    plan = clo.clo_rope_plan_init(cfg)
+    assert plan.rot_dim == 64
+    with pytest.raises(TypeError, match="exclude"):  # one of them would be ignored
+        clo.clo_rope_plan_init(cfg, rot_dim=32)
+    with pytest.raises(TypeError, match="clo_rope_config"):
+        clo.clo_rope_plan_init(plan)
+    x, pos = torch.zeros((2, 4, 64), dtype=torch.bfloat16), torch.zeros(2, dtype=torch.int64)
+    for bad in (cfg, None, 64):  # a config is shorter than the plan that the call reads
+        with pytest.raises(TypeError, match="clo_rope_plan"):
+            clo.clo_rope(bad, x, pos)
