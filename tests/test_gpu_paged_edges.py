@@ -554,3 +554,25 @@ def test_thousands_of_sequences_under_the_c_names(clo, bits):
     check(clo.clo_paged_attention(cache, qr, *at, max_q=2), want, bound)
     size = clo.clo_paged_attention_workspace(cache, hq, len(seqs), c.total, c.tab.shape[1], 2)
     assert size == cache.attention_workspace(hq, len(seqs), c.total, c.tab.shape[1], 2)
+
+
+def test_capture_on_a_named_stream(clo):
+    # the capturing stream named in the call (outputs and workspace from the graph's memory), replayed with other inputs beside eager calls
+    c = Case(clo, [(1, 9000), (1, 300)], 2, 128, 64, 8, seed=201)
+    c.device()
+    plan = clo.clo_rope_plan_init(rot_dim=128)
+    q, pos = bf16(rand(202, 2, 8, 128)).cuda(), torch.tensor([8999, 299], device="cuda")
+    assert c.cache.attention_workspace(8, 2, 2, c.tab.shape[1], 1) > 0
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        out = c.attend(clo.clo_rope(plan, q, pos, stream=side), stream=side)
+    for i in range(3):
+        q.copy_(bf16(rand(203 + i, 2, 8, 128)))
+        eager = [c.attend(clo.clo_rope(plan, q, pos)) for _ in range(3)]
+        graph.replay()
+        eager += [c.attend(clo.clo_rope(plan, q, pos)) for _ in range(3)]
+        torch.cuda.synchronize()
+        for e in eager:
+            assert torch.equal(out, e)
