@@ -21,9 +21,9 @@ namespace {
 // join through distributed shared memory were slower: 12 us for 6 at 8 x 200 tokens, and 16 blocks of a cluster find room only 7
 // times on the SMs.)
 //
-// 8 sequences of 32,768 tokens of bf16, 32 over 8 heads of 128: 163 us, 6.6 TB/s, 97 % of a copy's rate; of 8-bit pages 89 us,
-// 6.0 TB/s, where the conversions of the codes take issue slots too.  One token over 64 tokens: 3.7 us, a launch and four loads
-// that wait for each other (lengths, page, K, V).
+// 8 sequences of 32,768 tokens of bf16, 32 over 8 heads of 128: 162 to 166 us, 6.6 TB/s, 97 % of a copy's rate; of 8-bit pages 89 us,
+// 6.0 TB/s, where the conversions of the codes take issue slots too.  One token over 64 tokens, in a graph: 3.5 us, a launch and four
+// loads that wait for each other (lengths, page, K, V).
 constexpr int kStageBytes = 8192;
 
 constexpr int kWarps = 4;

@@ -27,9 +27,9 @@
 // have been written) is cleared in the operand tile.  Rows that end with an infinity or NaN all the same are computed again, one
 // by one, if V has one where they do not look (spoilt_rows looks V over once); what comes from tokens that they see stays.
 //
-// 8192 tokens, 32 over 8 heads of 128, causal, bf16: 403 to 411 us, 1.35 PFLOP/s, 70 % of a library product's rate: a token tile takes
+// 8192 tokens, 32 over 8 heads of 128, causal, bf16: 404 to 416 us, 1.34 PFLOP/s, 70 % of a library product's rate: a token tile takes
 // both lanes 2770 cycles, of which the products 2048, and the diagonal's tiles count half.  2048 tokens over 32,768 of 8-bit
-// pages: 840 us, 1.27 PFLOP/s; there the softmax and the conversions share the issue slots (3700 cycles a tile).
+// pages: 848 us, 1.26 PFLOP/s; there the softmax and the conversions share the issue slots (3700 cycles a tile).
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -7,10 +7,10 @@
 // head's rest behind rot_dim: 16 adjacent ones, copied).  d / 16 lanes cover a row, so that a lane keeps
 // its unit while its warp walks over rows.
 //
-// Measured: 8192 tokens of 32 heads of 128, 23.0 us, 5.8 TB/s (86 % of a copy's rate); 30,000 tokens 73 us, 99 %; one token 2.3 us.
-// Append with queries: about 11,000 tokens, 8-bit pages, 32 over 8 heads, 80 us, 4.9 TB/s (registers hold two blocks to an SM: a page's
-// rows stay in them until its scale is known); 64 single tokens, bf16, 8.0 us.  Read-back of 8 x 8192 tokens: bf16 80 us, 6.7 TB/s,
-// 8-bit pages 68 us, 5.9 TB/s.
+// Measured: 8192 tokens of 32 heads of 128, 24.9 us, 5.4 TB/s (80 % of a copy's rate); 30,000 tokens 75 us, 96 %; one token 2.2 us in a
+// graph.  Append with queries, 32 over 8 heads: 11,000 tokens, bf16 pages 52 us, 5.2 TB/s, 8-bit pages 54 us, 4.6 TB/s (registers hold two
+// blocks to an SM: a page's rows stay in them until its scale is known); 64 single tokens, in a graph, 3.8 and 4.5 us.  Read-back of
+// 8 x 8192 tokens: bf16 82 us, 6.5 TB/s, 8-bit pages 70 us, 5.8 TB/s.
 #include <cuda_runtime.h>
 
 #include <algorithm>
