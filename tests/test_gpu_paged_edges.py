@@ -576,3 +576,69 @@ def test_capture_on_a_named_stream(clo):
         torch.cuda.synchronize()
         for e in eager:
             assert torch.equal(out, e)
+
+
+# --------------------------------------------------------------------------------------------- lengths past the table, expanded inputs
+@pytest.mark.parametrize("bits", [16, 8])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (10, 4), (10, 0), (700, 100), (1 << 30, 1 << 30)])
+@pytest.mark.parametrize("seqs", [[(3, 1000), (1, 33), (2, 40)], [(40, 1000), (20, 700), (33, 60)]])
+def test_lengths_past_the_table(clo, seqs, window, sinks, bits):
+    # the table holds 48 tokens of each sequence: rows behind them see what is there, or nothing
+    c = Case(clo, seqs, 2, 64, 16, bits, seed=211, width=3)
+    c.device()
+    q = bf16(rand(212, c.total, 6, 64))
+    c.compare(c.attend(q, window, sinks), q, window, sinks)
+
+
+@pytest.mark.parametrize("bits", [16, 8])
+def test_inputs_expanded_over_heads_and_tokens(clo, bits):
+    hkv, hq, d = 2, 8, 128
+    for seqs in ([(1, 90), (2, 33)], [(40, 90), (5, 33)]):
+        c = Case(clo, seqs, hkv, d, 32, bits, seed=221)
+        cache = c.device()
+        plan = clo.clo_rope_plan_init(rot_dim=d)
+        k1, q1 = bf16(rand(222, c.total, 1, d)).cuda(), bf16(rand(223, 1, hq, d)).cuda()
+        k, q = k1.expand(c.total, hkv, d), q1.expand(c.total, hq, d)  # strides of zero
+        pos = torch.cat([torch.arange(kv - n, kv) for n, kv in seqs]).cuda()
+        assert torch.equal(clo.clo_rope(plan, q, pos), clo.clo_rope(plan, q.contiguous(), pos))
+        qr = cache.append(k, k, c.starts, c.lens, c.tab, rope=plan, q=q, max_q=c.max_q)
+        assert torch.equal(qr, clo.clo_rope(plan, q.contiguous(), pos))
+        gk, gv = cache.read(c.starts, c.lens, c.tab, c.total)
+        twin = Case(clo, seqs, hkv, d, 32, bits, seed=221)
+        other = twin.device()
+        other.append(k.contiguous(), k.contiguous(), c.starts, c.lens, c.tab, rope=plan, max_q=c.max_q)
+        for a, b in zip((gk, gv), other.read(c.starts, c.lens, c.tab, c.total)):
+            assert torch.equal(a, b)
+        assert torch.equal(c.attend(q), c.attend(q.contiguous()))
+
+
+@pytest.mark.parametrize("bits", [16, 8])
+def test_empty_batches_tables_and_strided_read_back(clo, bits):
+    d, hkv = 64, 2
+    c = Case(clo, [(3, 20), (1, 7)], hkv, d, 16, bits, seed=231)
+    cache = c.device()
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    rows = lambda n, h: bf16(rand(232, n, h, d)).cuda()  # noqa: E731
+    plan = clo.clo_rope_plan_init(rot_dim=d)
+    # no sequence; sequences without a row
+    for starts, lens in ((i32(0), i32()), (i32(0, 0, 0), i32(5, 0))):
+        table = torch.zeros(len(lens), 2, dtype=torch.int32, device="cuda")
+        assert cache.append(rows(0, hkv), rows(0, hkv), starts, lens, table, rope=plan, q=rows(0, 4)).shape == (0, 4, d)
+        assert cache.attention(rows(0, 4), starts, lens, table).shape == (0, 4, d)
+        assert [t.shape for t in cache.read(starts, lens, table, 0)] == [(0, hkv, d)] * 2
+    # a table without pages: nothing is written, read as zeros, attended to
+    before = [t.clone() for t in cache._tensors if t is not None]
+    for n in (1, 30):
+        at = i32(0, n), i32(n), torch.zeros(1, 0, dtype=torch.int32, device="cuda")
+        qr = cache.append(rows(n, hkv), rows(n, hkv), *at, rope=plan, q=rows(n, 4))
+        assert torch.equal(qr, clo.clo_rope(plan, rows(n, 4), torch.arange(n, device="cuda")))
+        assert not cache.attention(rows(n, 4), *at).any() and not any(t.any() for t in cache.read(*at, n))
+    for a, b in zip(before, (t for t in cache._tensors if t is not None)):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    # into wider rows, heads outermost, the rest left alone
+    want = cache.read(c.starts, c.lens, c.tab, c.total)
+    wide = torch.full((c.total, hkv, d + 8), 7.0, dtype=BF16, device="cuda")
+    outer = torch.full((hkv, c.total + 1, d), 7.0, dtype=BF16, device="cuda")
+    cache.read(c.starts, c.lens, c.tab, c.total, k_out=wide[..., :d], v_out=outer.transpose(0, 1)[:c.total])
+    assert torch.equal(wide[..., :d], want[0]) and bool((wide[..., d:] == 7.0).all())
+    assert torch.equal(outer.transpose(0, 1)[:c.total], want[1]) and bool((outer[:, c.total] == 7.0).all())
