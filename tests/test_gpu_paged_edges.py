@@ -642,3 +642,30 @@ def test_empty_batches_tables_and_strided_read_back(clo, bits):
     cache.read(c.starts, c.lens, c.tab, c.total, k_out=wide[..., :d], v_out=outer.transpose(0, 1)[:c.total])
     assert torch.equal(wide[..., :d], want[0]) and bool((wide[..., d:] == 7.0).all())
     assert torch.equal(outer.transpose(0, 1)[:c.total], want[1]) and bool((outer[:, c.total] == 7.0).all())
+
+
+@pytest.mark.parametrize("group", [2, 16])
+def test_the_most_sequences_that_a_call_takes(clo, group):
+    # 65,535 sequences of two tokens, both the call's: 4 rows per kv head, or 32 (the prompt kernel)
+    batch, d, scale = 65535, 64, 0.2
+    cache = clo.PagedCache.create(batch, 1, 16, d)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    table = torch.randperm(batch, generator=torch.Generator().manual_seed(1)).to(torch.int32).cuda().view(batch, 1)
+    starts, lens = torch.arange(0, 2 * batch + 1, 2, **i32), torch.full((batch,), 2, **i32)
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    new = lambda h: torch.randn((2 * batch, h, d), generator=gen, device="cuda").to(BF16)  # noqa: E731
+    k, v, q = new(1), new(1), new(group)
+    times = [best_time(lambda: cache.append(k, v, starts, lens, table, max_q=2), 3)]
+    gk, gv = cache.read(starts, lens, table, 2 * batch, max_q=2)
+    assert torch.equal(gk, k) and torch.equal(gv, v)
+    out = cache.attention(q, starts, lens, table, max_q=2, softmax_scale=scale)
+    times.append(best_time(lambda: cache.attention(q, starts, lens, table, out=out, max_q=2, softmax_scale=scale), 3))
+    print(f"append {times[0]:.2f} ms, attention {times[1]:.2f} ms")
+    kd, vd, qd = (t.double().view(batch, 2, -1, d) for t in (k, v, q))
+    sc = torch.einsum("bqhd,bkd->bqhk", qd, kd[:, :, 0]) * scale
+    sc[:, 0, :, 1] = -math.inf
+    w = torch.softmax(sc, -1)
+    want, spread = torch.einsum("bqhk,bkd->bqhd", w, vd[:, :, 0]), torch.einsum("bqhk,bkd->bqhd", w, vd[:, :, 0].abs())
+    reach = (torch.einsum("bqhd,bkd->bqhk", qd.abs(), kd[:, :, 0].abs()) * scale).amax(-1, keepdim=True)
+    bound = ref.attention_bound(want, spread, reach, d, 16).view(2 * batch, group, d)
+    check(out, want.view(2 * batch, group, d).cpu(), bound.cpu())
