@@ -24,7 +24,9 @@ CLO_DEC_HIT, CLO_DEC_MISS, CLO_DEC_PERSIST = 0, 1, 2
 STEP_HIST = 4096
 CLO_SET_DROP_FLAG_LAYER, CLO_SET_WAIT_TIMEOUT_NS = 1, 2
 CLO_ROPE_SCALING = {"none": 0, "linear": 1, "bands": 2, "yarn": 3}
+CLO_ROPE_ORDER = {"sections": 0, "cycled": 1}
 CLO_ROPE_MAX_PAIRS = 64
+CLO_ROPE_MAX_AXES = 4
 
 _STATUS_NAMES = {0: "CLO_OK", 1: "CLO_ERR_INVALID", 2: "CLO_ERR_OOM", 3: "CLO_ERR_CUDA", 4: "CLO_ERR_TIMEOUT",
                  5: "CLO_ERR_STATE", 6: "CLO_ERR_CAPACITY", 7: "CLO_ERR_DEVICE"}
@@ -93,6 +95,10 @@ class clo_rope_config(ctypes.Structure):
         ("beta_slow", ctypes.c_double),
         ("original_max", ctypes.c_int64),
         ("magnitude", ctypes.c_double),
+        ("n_axes", ctypes.c_int32),
+        ("axis_pairs", ctypes.c_int32 * CLO_ROPE_MAX_AXES),
+        ("axis_order", ctypes.c_int32),
+        ("axis_own_freqs", ctypes.c_int32),
     ]
 
 
@@ -103,6 +109,8 @@ class clo_rope_plan(ctypes.Structure):
         ("rot_dim", ctypes.c_int32),
         ("interleaved", ctypes.c_int32),
         ("ready", ctypes.c_int32),
+        ("axis", ctypes.c_uint8 * CLO_ROPE_MAX_PAIRS),
+        ("n_axes", ctypes.c_int32),
     ]
 
 
@@ -309,7 +317,10 @@ def clo_rope_config_default() -> clo_rope_config:
 
 def clo_rope_plan_init(cfg: clo_rope_config | None = None, **fields) -> clo_rope_plan:
     """Plan of a rotation: from a config, or from its fields (scaling by name: "none", "linear",
-    "bands", "yarn").  The plan holds plain values and may serve any number of calls."""
+    "bands", "yarn").  The plan holds plain values and may serve any number of calls.
+
+    axis_pairs: the pairs of each axis where tokens have positions on several, for example (16, 24, 24) for time,
+    height and width; axis_order by name: "sections", "cycled".  Such a plan takes positions [n_axes][n_tokens]."""
     if cfg is not None and fields:
         raise TypeError("a config and its fields exclude each other")
     if cfg is not None and not isinstance(cfg, clo_rope_config):
@@ -323,7 +334,19 @@ def clo_rope_plan_init(cfg: clo_rope_config | None = None, **fields) -> clo_rope
                 if value not in CLO_ROPE_SCALING:
                     raise ValueError(f"unknown scaling {value!r}; known: {sorted(CLO_ROPE_SCALING)}")
                 value = CLO_ROPE_SCALING[value]
-            setattr(cfg, name, int(value) if name == "interleaved" else value)
+            if name == "axis_order" and isinstance(value, str):
+                if value not in CLO_ROPE_ORDER:
+                    raise ValueError(f"unknown axis_order {value!r}; known: {sorted(CLO_ROPE_ORDER)}")
+                value = CLO_ROPE_ORDER[value]
+            if name == "axis_pairs":
+                value = tuple(value)
+                if not 1 <= len(value) <= CLO_ROPE_MAX_AXES:
+                    raise ValueError(f"axis_pairs has {len(value)} axes; 1 .. {CLO_ROPE_MAX_AXES} are possible")
+                if fields.get("n_axes", len(value)) != len(value):
+                    raise ValueError("n_axes is not the length of axis_pairs")
+                cfg.n_axes = len(value)
+                value = (ctypes.c_int32 * CLO_ROPE_MAX_AXES)(*value)
+            setattr(cfg, name, int(value) if name in ("interleaved", "axis_own_freqs") else value)
     plan = clo_rope_plan()
     _check(load_library().clo_rope_plan_init(ctypes.byref(cfg), ctypes.byref(plan)), "clo_rope_plan_init")
     return plan
@@ -364,7 +387,8 @@ def _fast():
 
 
 def clo_rope(plan: clo_rope_plan, x, positions, out=None, transpose: bool = False, stream=None):
-    """Rotates bf16 rows [n_tokens][n_heads][head_dim] by int64 positions [n_tokens] (see include/clo.h).
+    """Rotates bf16 rows [n_tokens][n_heads][head_dim] by int64 positions [n_tokens] (see include/clo.h), or
+    [n_axes][n_tokens] where the plan has several axes.
 
     out: rows of the same shape, x itself for in place, or None for new ones.  transpose applies the
     transposed rotation, which takes the gradient of the output to that of x: the call itself is not recorded by autograd,

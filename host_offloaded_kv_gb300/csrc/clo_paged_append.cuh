@@ -1,0 +1,234 @@
+// Paged append with the rotation on the way: the kernel and its launch, instantiated by the pages' type.  One pass over the rows, bounded
+// by HBM traffic (large calls) or by one launch and two or three dependent loads (single-token steps).
+//
+// Measured with queries, 32 over 8 heads: 11,000 tokens, bf16 pages 52 us, 5.2 TB/s, 8-bit pages 54 us, 4.6 TB/s (registers hold two
+// blocks to an SM: a page's rows stay in them until its scale is known); 64 single tokens, in a graph, 3.8 and 4.5 us.
+#pragma once
+
+#include "clo_rope.cuh"
+
+namespace clo {
+
+struct AppendParams {
+  PagedParams c;
+  Rows in[2];  // k, v
+  Rows q, q_out;
+  const int64_t* positions;
+  int32_t n_q_heads;   // 0: no queries
+  int32_t q_chunks;    // warps per query token
+  int32_t items;       // upper bound of (sequence, touched page) pairs
+  int32_t kv_blocks;   // blocks that write pages; the others rotate queries
+  Rope rope;
+};
+
+// A call's launch, by the pages' type.
+void launch_append_bf16(const AppendParams& a, int head_dim, int64_t blocks, int per, cudaStream_t st);
+void launch_append_e4m3(const AppendParams& a, int head_dim, int64_t blocks, int per, cudaStream_t st);
+
+namespace {
+
+// ---------------------------------------------------------------------------- paged append
+
+// The item-th (sequence, touched page) of the batch, by the whole warp; false past the last one.
+__device__ __forceinline__ bool item_of(const PagedParams& p, int item, int lane, int* seq, int* logical, SeqRows* rows) {
+  int before = 0;
+  for (int c = 0; c < p.batch; c += 32) {
+    int pages = 0;
+    SeqRows s;
+    if (c + lane < p.batch) {
+      s = seq_rows(p, c + lane);
+      if (s.n > 0) {
+        // positions [pos0, pos0 + n) clipped to [0, capacity)
+        const int lo = max(s.pos0, 0), hi = min((int64_t)s.pos0 + s.n, (int64_t)p.max_pages << p.page_shift);
+        if (hi > lo) pages = ((hi - 1) >> p.page_shift) - (lo >> p.page_shift) + 1;
+      }
+    }
+    int incl = pages;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const unsigned m = __ballot_sync(0xffffffffu, before + incl > item);
+    if (m) {
+      const int l = __ffs(m) - 1;
+      const int b = c + l;
+      const int skip = item - before - (__shfl_sync(0xffffffffu, incl, l) - __shfl_sync(0xffffffffu, pages, l));
+      *seq = b;
+      *rows = seq_rows(p, b);
+      *logical = (max(rows->pos0, 0) >> p.page_shift) + skip;
+      return true;
+    }
+    before += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  return false;
+}
+
+// One job: (touched page, kv head, K or V), by kPer warps.  A lane holds kUnits units (16 elements of a row each) in registers from
+// the load to the store, so that rows are read and rotated once also where the page's scale comes in between; kPer warps
+// hold the most rows that a page can get from the call.
+constexpr int kUnits = 4;
+
+template <int D, int BITS, int kPer, bool AXES>
+__device__ __forceinline__ void write_page(const AppendParams& a, const uint64_t* s_turn, int item, int head, int side, int part, int lane, float* s_red,
+                                           int group) {
+  const PagedParams& p = a.c;
+  int b, logical;
+  SeqRows s;
+  if (!item_of(p, item, lane, &b, &logical, &s)) return;
+  const int page = page_of(p, b, logical);
+  if (page < 0) return;
+  constexpr int kLanes = D / 16, kRows = 32 / kLanes;
+  const int base = logical << p.page_shift;             // position of slot 0
+  const int lo = max(max(s.pos0, 0), base), hi = min(s.pos0 + s.n, base + p.page_size);
+  const PagedSide& sd = p.side[side];
+  const Rows& in = a.in[side];
+  Unit<D> u = unit_of_lane<D, AXES>(a.rope, s_turn, lane % kLanes);
+  const bool rotate = side == 0 && u.rotate;
+  if (side == 1) {
+    u.a = (lane % kLanes) * 16;
+    u.b = u.a + 8;
+  }
+  char* dst0 = sd.pages + ((int64_t)page * sd.stride_page + (int64_t)head * sd.stride_head) * (BITS / 8);
+  const int first = lo + part * kRows + lane / kLanes;  // this lane's rows: first, + kPer * kRows, ...
+
+  uint4 va[kUnits], vb[kUnits];
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    const int pos = first + i * kPer * kRows;
+    if (pos < hi) {
+      const uint16_t* src = in.p + (int64_t)(s.first + (pos - s.pos0)) * in.token + (int64_t)head * in.head;
+      va[i] = __ldg(reinterpret_cast<const uint4*>(src + u.a));
+      vb[i] = __ldg(reinterpret_cast<const uint4*>(src + u.b));
+    }
+  }
+  float f[kUnits][16], amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    const int pos = first + i * kPer * kRows;
+    if (pos < hi) {
+      unpack8(va[i], f[i]);
+      unpack8(vb[i], f[i] + 8);
+      if (rotate) {
+        const int64_t row = s.first + (pos - s.pos0);
+        Place where{pos, nullptr, 0};
+        if (AXES && a.positions)
+          where = {0, a.positions + row, a.c.total_q};
+        else if (a.positions)
+          where.pos = __ldg(a.positions + row);
+        rotate_unit<D>(u, cos_sin_of<D, AXES>(u, where, 0), f[i]);
+      }
+      if (BITS == 16) {
+        char* dst = dst0 + (int64_t)(pos - base) * sd.stride_token * 2;
+        *reinterpret_cast<uint4*>(dst + u.a * 2) = pack8(f[i]);
+        *reinterpret_cast<uint4*>(dst + u.b * 2) = pack8(f[i] + 8);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const float m = fabsf(f[i][k]);
+          amax = fmaxf(amax, m < INFINITY ? m : 0.f);
+        }
+      }
+    }
+  }
+  if (BITS == 16) return;
+  amax = warp_max(amax);
+  if (kPer > 1) {
+    if (lane == 0) s_red[group * kPer + part] = amax;
+    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(kPer * 32) : "memory");
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) amax = fmaxf(amax, s_red[group * kPer + i]);
+  }
+  // smallest e with amax <= 1.75 * 2^(8 + e), from the bits of amax
+  const int bits = __float_as_int(amax);
+  int e = (bits >> 23) - 127 - 8 + ((bits & 0x7fffff) > 0x600000 ? 1 : 0);
+  e = max(e, kMinScaleExp);
+  float scale = __int_as_float((e + 127) << 23);
+  float* sp = sd.scales + (int64_t)page * p.n_kv_heads + head;
+  if (lo > base) {
+    const float old = *sp;
+    if (old >= scale) {  // a scale that is no number is replaced
+      scale = old;
+    } else if (old > 0.f) {
+      const float f = old / scale;
+      for (int v = part * 32 + lane; v < (lo - base) * (D / 8); v += kPer * 32) {
+        uint2* c = reinterpret_cast<uint2*>(dst0 + (int64_t)(v / (D / 8)) * sd.stride_token + v % (D / 8) * 8);
+        const uint2 w = *c;
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 d = e4m3_to_f32x2(((i < 2 ? w.x : w.y) >> (16 * (i & 1))) & 0xffffu);
+          x[2 * i] = d.x * f;
+          x[2 * i + 1] = d.y * f;
+        }
+        *c = pack8_e4m3(x);
+      }
+    }
+  }
+  const float inv = 1.f / scale;
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    const int pos = first + i * kPer * kRows;
+    if (pos < hi) {
+#pragma unroll
+      for (int k = 0; k < 16; ++k) f[i][k] *= inv;
+      char* dst = dst0 + (int64_t)(pos - base) * sd.stride_token;
+      *reinterpret_cast<uint2*>(dst + u.a) = pack8_e4m3(f[i]);
+      *reinterpret_cast<uint2*>(dst + u.b) = pack8_e4m3(f[i] + 8);
+    }
+  }
+  // every warp has read the old scale
+  if (kPer > 1) asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(kPer * 32) : "memory");
+  __syncwarp();
+  if (part == 0 && lane == 0) *sp = scale;
+}
+
+template <int D, int BITS, int kPer, bool AXES>
+__global__ void __launch_bounds__(kThreads) k_paged_append(const AppendParams a) {
+  __shared__ __align__(16) uint64_t s_turn[kTurns<AXES>];
+  __shared__ float s_red[kWarps];
+  stage_turns<AXES>(a.rope, s_turn);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if ((int)blockIdx.x < a.kv_blocks) {
+    const int64_t job = (int64_t)blockIdx.x * (kWarps / kPer) + warp / kPer;
+    const int heads = a.c.n_kv_heads;
+    const int64_t item = job / (2 * heads);
+    if (item >= a.items) return;
+    write_page<D, BITS, kPer, AXES>(a, s_turn, (int)item, (int)(job % heads), (int)(job / heads & 1), warp % kPer, lane, s_red, warp / kPer);
+    return;
+  }
+  constexpr int kIters = kPer == 1 ? kShortIters : kLongIters;
+  const int64_t job = (int64_t)((int)blockIdx.x - a.kv_blocks) * kWarps + warp;
+  const int64_t t = job / a.q_chunks;
+  if (t >= a.c.total_q) return;
+  // the row's sequence is looked up while its elements are on their way
+  auto position = [&](Place* where) {
+    const int b = seq_of_row(a.c, (int)t, lane);
+    if (b >= a.c.batch) return false;
+    const SeqRows s = seq_rows(a.c, b);
+    if (t - s.first >= s.n) return false;  // beyond max_q: left out, as its key is
+    *where = {(int64_t)s.pos0 + (t - s.first), nullptr, 0};
+    if (AXES && a.positions)
+      *where = {0, a.positions + t, a.c.total_q};
+    else if (a.positions)
+      where->pos = __ldg(a.positions + t);
+    return true;
+  };
+  rotate_heads<D, kIters, AXES>(a.rope, s_turn, a.q, a.q_out, t, position, (int)(job % a.q_chunks) * heads_per_warp<D>(kIters), a.n_q_heads, lane);
+}
+
+template <int BITS>
+void launch_append_bits(const AppendParams& a, int head_dim, int64_t blocks, int per, cudaStream_t st) {
+  auto launch = [&](auto* one, auto* two, auto* four, auto* eight) { (per == 1 ? one : per == 2 ? two : per == 4 ? four : eight)<<<(unsigned)blocks, kThreads, 0, st>>>(a); };
+  if (a.rope.plan.n_axes > 1) {
+    if (head_dim == 128) launch(k_paged_append<128, BITS, 1, true>, k_paged_append<128, BITS, 2, true>, k_paged_append<128, BITS, 4, true>, k_paged_append<128, BITS, 8, true>);
+    else launch(k_paged_append<64, BITS, 1, true>, k_paged_append<64, BITS, 2, true>, k_paged_append<64, BITS, 4, true>, k_paged_append<64, BITS, 8, true>);
+  } else {
+    if (head_dim == 128) launch(k_paged_append<128, BITS, 1, false>, k_paged_append<128, BITS, 2, false>, k_paged_append<128, BITS, 4, false>, k_paged_append<128, BITS, 8, false>);
+    else launch(k_paged_append<64, BITS, 1, false>, k_paged_append<64, BITS, 2, false>, k_paged_append<64, BITS, 4, false>, k_paged_append<64, BITS, 8, false>);
+  }
+}
+
+}  // namespace
+
+}  // namespace clo

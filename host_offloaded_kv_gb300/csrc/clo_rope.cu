@@ -1,16 +1,8 @@
-// Rotary positions (clo_rope), paged append with the rotation on the way (clo_paged_append) and the
-// read-back (clo_paged_read): one pass over the rows each, bounded by HBM traffic (large calls) or by
-// one launch and two or three dependent loads (single-token steps).
-//
-// The unit of work is 16 elements of one head's row: the two 8-element vectors whose elements pair up
-// (half layout: elements [8u, 8u + 8) and the same offset by rot_dim / 2; interleaved: 16 adjacent ones; a
-// head's rest behind rot_dim: 16 adjacent ones, copied).  d / 16 lanes cover a row, so that a lane keeps
-// its unit while its warp walks over rows.
+// Rotary positions (clo_rope) and the read-back of pages (clo_paged_read): one pass over the rows each, bounded by HBM
+// traffic (large calls) or by one launch and two or three dependent loads (single-token steps).
 //
 // Measured: 8192 tokens of 32 heads of 128, 24.9 us, 5.4 TB/s (80 % of a copy's rate); 30,000 tokens 75 us, 96 %; one token 2.2 us in a
-// graph.  Append with queries, 32 over 8 heads: 11,000 tokens, bf16 pages 52 us, 5.2 TB/s, 8-bit pages 54 us, 4.6 TB/s (registers hold two
-// blocks to an SM: a page's rows stay in them until its scale is known); 64 single tokens, in a graph, 3.8 and 4.5 us.  Read-back of
-// 8 x 8192 tokens: bf16 82 us, 6.5 TB/s, 8-bit pages 70 us, 5.8 TB/s.
+// graph.  Read-back of 8 x 8192 tokens: bf16 82 us, 6.5 TB/s, 8-bit pages 70 us, 5.8 TB/s.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -18,9 +10,10 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <type_traits>
 
 #include "clo.h"
-#include "clo_paged.cuh"
+#include "clo_rope.cuh"
 
 namespace clo {
 
@@ -39,156 +32,22 @@ clo_status paged_fail(clo_status st, const char* fmt, ...) {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-
-struct Rope {
-  clo_rope_plan plan;  // rot_dim 0: copy
-  int transpose;
-};
-
-// What a lane knows about its 16-element unit.
-template <int D>
-struct Unit {
-  int a, b;       // element offsets of the two vectors
-  bool rotate, interleaved;
-  uint64_t turn[8];
-  float magnitude;
-};
-
-// The plan's turns in shared memory: lanes read their units' with wide loads, where the parameter space would serve one address at a time.
-__device__ __forceinline__ void stage_turns(const Rope& r, uint64_t* s_turn) {
-  if (threadIdx.x < CLO_ROPE_MAX_PAIRS) s_turn[threadIdx.x] = r.plan.turn[threadIdx.x];
-  __syncthreads();
-}
-
-template <int D>
-__device__ __forceinline__ Unit<D> unit_of_lane(const Rope& r, const uint64_t* s_turn, int u) {
-  Unit<D> x;
-  const int rot = r.plan.rot_dim;
-  x.rotate = u * 16 < rot;
-  x.interleaved = r.plan.interleaved != 0;
-  x.magnitude = r.plan.magnitude;
-  if (x.rotate && !x.interleaved) {
-    x.a = u * 8;
-    x.b = rot / 2 + u * 8;
-  } else {
-    x.a = u * 16;
-    x.b = u * 16 + 8;
-  }
-  if (x.rotate) {
-#pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-      const ulonglong2 t = *reinterpret_cast<const ulonglong2*>(s_turn + u * 8 + i);
-      x.turn[i] = t.x;
-      x.turn[i + 1] = t.y;
-    }
-  }
-  return x;
-}
-
-struct CosSin {
-  float2 v[8];
-};
-
-template <int D>
-__device__ __forceinline__ CosSin cos_sin_of(const Unit<D>& u, int64_t pos, int transpose) {
-  CosSin c;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    c.v[i] = rope_cos_sin(pos, u.turn[i], u.magnitude);
-    if (transpose) c.v[i].y = -c.v[i].y;
-  }
-  return c;
-}
-
-// Rotates a unit: x[0..8) are the elements at a, x[8..16) those at b.
-template <int D>
-__device__ __forceinline__ void rotate_unit(const Unit<D>& u, const CosSin& c, float* x) {
-  if (u.interleaved) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float p = x[2 * i], q = x[2 * i + 1];
-      x[2 * i] = fmaf(p, c.v[i].x, -q * c.v[i].y);
-      x[2 * i + 1] = fmaf(q, c.v[i].x, p * c.v[i].y);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float p = x[i], q = x[8 + i];
-      x[i] = fmaf(p, c.v[i].x, -q * c.v[i].y);
-      x[8 + i] = fmaf(q, c.v[i].x, p * c.v[i].y);
-    }
-  }
-}
-
-struct Rows {
-  uint16_t* p;
-  int64_t token, head;
-};
-
-// ---------------------------------------------------------------------------- rows of one token
-// A warp takes one token and up to ITERS rounds of its heads: the cosines and sines of a lane's unit are computed
-// once for all of them.
-template <int D, int ITERS, typename F>
-__device__ __forceinline__ void rotate_heads(const Rope& r, const uint64_t* s_turn, const Rows& x, const Rows& y, int64_t token, F&& position,
-                                             int head0, int n_heads, int lane) {
-  constexpr int kLanes = D / 16, kRows = 32 / kLanes;
-  const Unit<D> u = unit_of_lane<D>(r, s_turn, lane % kLanes);
-  const uint16_t* src = x.p + token * x.token;
-  uint16_t* dst = y.p + token * y.token;
-  uint4 va[ITERS], vb[ITERS];
-#pragma unroll
-  for (int i = 0; i < ITERS; ++i) {
-    const int h = head0 + i * kRows + lane / kLanes;
-    if (h < n_heads) {
-      va[i] = *reinterpret_cast<const uint4*>(src + (int64_t)h * x.head + u.a);
-      vb[i] = *reinterpret_cast<const uint4*>(src + (int64_t)h * x.head + u.b);
-    }
-  }
-  int64_t pos;
-  if (!position(&pos)) return;
-  CosSin c;
-  if (u.rotate) c = cos_sin_of<D>(u, pos, r.transpose);
-#pragma unroll
-  for (int i = 0; i < ITERS; ++i) {
-    const int h = head0 + i * kRows + lane / kLanes;
-    if (h < n_heads) {
-      if (u.rotate) {
-        float f[16];
-        unpack8(va[i], f);
-        unpack8(vb[i], f + 8);
-        rotate_unit<D>(u, c, f);
-        va[i] = pack8(f);
-        vb[i] = pack8(f + 8);
-      }
-      *reinterpret_cast<uint4*>(dst + (int64_t)h * y.head + u.a) = va[i];
-      *reinterpret_cast<uint4*>(dst + (int64_t)h * y.head + u.b) = vb[i];
-    }
-  }
-}
-
-// Rounds of heads per warp: many for long calls, where the sines count, few for short ones, where the latency does, and no more
-// than the heads fill.  8192 tokens of 128-element heads, us with 8 / 4 / 2 rounds: 8 heads (floor 5.0) 11.0 / - / 7.5, 16 heads (9.9)
-// 13.0 / 10.7 / -, 40 heads (24.7) 33.6 / 30.4 / -; 2000 tokens, 32 heads (4.8) 6.3 / 7.1 / -.
-constexpr int kLongIters = 8, kMidIters = 4, kShortIters = 2;
-constexpr int64_t kLongTokens = 8 * 152;  // a warp per SM and slot of eight
-template <int D>
-__host__ __device__ constexpr int heads_per_warp(int iters) { return iters * 32 / (D / 16); }
-
-template <int D, int ITERS>
+template <int D, int ITERS, bool AXES>
 __global__ void __launch_bounds__(kThreads, ITERS == kLongIters ? 2 : ITERS == kMidIters ? 3 : 4) k_rope(const Rope r, const Rows x, const Rows y, const int64_t* __restrict__ positions,
                                                    int64_t n_tokens, int n_heads, int chunks) {
-  __shared__ __align__(16) uint64_t s_turn[CLO_ROPE_MAX_PAIRS];
-  stage_turns(r, s_turn);
+  __shared__ __align__(16) uint64_t s_turn[kTurns<AXES>];
+  stage_turns<AXES>(r, s_turn);
   const int64_t job = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
   const int64_t t = job / chunks;
   if (t >= n_tokens) return;
-  auto position = [&](int64_t* pos) {
-    *pos = positions[t];
+  auto position = [&](Place* where) {
+    if (AXES)
+      *where = {0, positions + t, n_tokens};
+    else
+      where->pos = positions[t];
     return true;
   };
-  rotate_heads<D, ITERS>(r, s_turn, x, y, t, position, (int)(job % chunks) * heads_per_warp<D>(ITERS), n_heads, threadIdx.x & 31);
+  rotate_heads<D, ITERS, AXES>(r, s_turn, x, y, t, position, (int)(job % chunks) * heads_per_warp<D>(ITERS), n_heads, threadIdx.x & 31);
 }
 
 // Any strides, alignment, rot_dim and head_dim: one pair, or one copied element, per thread and step.
@@ -207,204 +66,13 @@ __global__ void __launch_bounds__(kThreads) k_rope_any(const Rope r, const Rows 
       continue;
     }
     const int a = r.plan.interleaved ? 2 * i : i, b = r.plan.interleaved ? 2 * i + 1 : i + half;
-    float2 c = rope_cos_sin(positions[t], r.plan.turn[i], r.plan.magnitude);
+    const int64_t at = r.plan.n_axes > 1 ? r.plan.axis[i] * n_tokens + t : t;
+    float2 c = rope_cos_sin(positions[at], r.plan.turn[i], r.plan.magnitude);
     if (r.transpose) c.y = -c.y;
     const float p = bf16_bits_to_f32(src[a]), q = bf16_bits_to_f32(src[b]);
     dst[a] = (uint16_t)pack_bf16(fmaf(p, c.x, -q * c.y), 0.f);
     dst[b] = (uint16_t)pack_bf16(fmaf(q, c.x, p * c.y), 0.f);
   }
-}
-
-// ---------------------------------------------------------------------------- paged append
-struct AppendParams {
-  PagedParams c;
-  Rows in[2];  // k, v
-  Rows q, q_out;
-  const int64_t* positions;
-  int32_t n_q_heads;   // 0: no queries
-  int32_t q_chunks;    // warps per query token
-  int32_t items;       // upper bound of (sequence, touched page) pairs
-  int32_t kv_blocks;   // blocks that write pages; the others rotate queries
-  Rope rope;
-};
-
-// The item-th (sequence, touched page) of the batch, by the whole warp; false past the last one.
-__device__ __forceinline__ bool item_of(const PagedParams& p, int item, int lane, int* seq, int* logical, SeqRows* rows) {
-  int before = 0;
-  for (int c = 0; c < p.batch; c += 32) {
-    int pages = 0;
-    SeqRows s;
-    if (c + lane < p.batch) {
-      s = seq_rows(p, c + lane);
-      if (s.n > 0) {
-        // positions [pos0, pos0 + n) clipped to [0, capacity)
-        const int lo = max(s.pos0, 0), hi = min((int64_t)s.pos0 + s.n, (int64_t)p.max_pages << p.page_shift);
-        if (hi > lo) pages = ((hi - 1) >> p.page_shift) - (lo >> p.page_shift) + 1;
-      }
-    }
-    int incl = pages;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
-    }
-    const unsigned m = __ballot_sync(0xffffffffu, before + incl > item);
-    if (m) {
-      const int l = __ffs(m) - 1;
-      const int b = c + l;
-      const int skip = item - before - (__shfl_sync(0xffffffffu, incl, l) - __shfl_sync(0xffffffffu, pages, l));
-      *seq = b;
-      *rows = seq_rows(p, b);
-      *logical = (max(rows->pos0, 0) >> p.page_shift) + skip;
-      return true;
-    }
-    before += __shfl_sync(0xffffffffu, incl, 31);
-  }
-  return false;
-}
-
-// One job: (touched page, kv head, K or V), by kPer warps.  A lane holds kUnits units (16 elements of a row each) in registers from
-// the load to the store, so that rows are read and rotated once also where the page's scale comes in between; kPer warps
-// hold the most rows that a page can get from the call.
-constexpr int kUnits = 4;
-
-template <int D, int BITS, int kPer>
-__device__ __forceinline__ void write_page(const AppendParams& a, const uint64_t* s_turn, int item, int head, int side, int part, int lane, float* s_red,
-                                           int group) {
-  const PagedParams& p = a.c;
-  int b, logical;
-  SeqRows s;
-  if (!item_of(p, item, lane, &b, &logical, &s)) return;
-  const int page = page_of(p, b, logical);
-  if (page < 0) return;
-  constexpr int kLanes = D / 16, kRows = 32 / kLanes;
-  const int base = logical << p.page_shift;             // position of slot 0
-  const int lo = max(max(s.pos0, 0), base), hi = min(s.pos0 + s.n, base + p.page_size);
-  const PagedSide& sd = p.side[side];
-  const Rows& in = a.in[side];
-  Unit<D> u = unit_of_lane<D>(a.rope, s_turn, lane % kLanes);
-  const bool rotate = side == 0 && u.rotate;
-  if (side == 1) {
-    u.a = (lane % kLanes) * 16;
-    u.b = u.a + 8;
-  }
-  char* dst0 = sd.pages + ((int64_t)page * sd.stride_page + (int64_t)head * sd.stride_head) * (BITS / 8);
-  const int first = lo + part * kRows + lane / kLanes;  // this lane's rows: first, + kPer * kRows, ...
-
-  uint4 va[kUnits], vb[kUnits];
-#pragma unroll
-  for (int i = 0; i < kUnits; ++i) {
-    const int pos = first + i * kPer * kRows;
-    if (pos < hi) {
-      const uint16_t* src = in.p + (int64_t)(s.first + (pos - s.pos0)) * in.token + (int64_t)head * in.head;
-      va[i] = __ldg(reinterpret_cast<const uint4*>(src + u.a));
-      vb[i] = __ldg(reinterpret_cast<const uint4*>(src + u.b));
-    }
-  }
-  float f[kUnits][16], amax = 0.f;
-#pragma unroll
-  for (int i = 0; i < kUnits; ++i) {
-    const int pos = first + i * kPer * kRows;
-    if (pos < hi) {
-      unpack8(va[i], f[i]);
-      unpack8(vb[i], f[i] + 8);
-      if (rotate) {
-        const int64_t at = a.positions ? __ldg(a.positions + s.first + (pos - s.pos0)) : pos;
-        rotate_unit<D>(u, cos_sin_of<D>(u, at, 0), f[i]);
-      }
-      if (BITS == 16) {
-        char* dst = dst0 + (int64_t)(pos - base) * sd.stride_token * 2;
-        *reinterpret_cast<uint4*>(dst + u.a * 2) = pack8(f[i]);
-        *reinterpret_cast<uint4*>(dst + u.b * 2) = pack8(f[i] + 8);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const float m = fabsf(f[i][k]);
-          amax = fmaxf(amax, m < INFINITY ? m : 0.f);
-        }
-      }
-    }
-  }
-  if (BITS == 16) return;
-  amax = warp_max(amax);
-  if (kPer > 1) {
-    if (lane == 0) s_red[group * kPer + part] = amax;
-    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(kPer * 32) : "memory");
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) amax = fmaxf(amax, s_red[group * kPer + i]);
-  }
-  // smallest e with amax <= 1.75 * 2^(8 + e), from the bits of amax
-  const int bits = __float_as_int(amax);
-  int e = (bits >> 23) - 127 - 8 + ((bits & 0x7fffff) > 0x600000 ? 1 : 0);
-  e = max(e, kMinScaleExp);
-  float scale = __int_as_float((e + 127) << 23);
-  float* sp = sd.scales + (int64_t)page * p.n_kv_heads + head;
-  if (lo > base) {
-    const float old = *sp;
-    if (old >= scale) {  // a scale that is no number is replaced
-      scale = old;
-    } else if (old > 0.f) {
-      const float f = old / scale;
-      for (int v = part * 32 + lane; v < (lo - base) * (D / 8); v += kPer * 32) {
-        uint2* c = reinterpret_cast<uint2*>(dst0 + (int64_t)(v / (D / 8)) * sd.stride_token + v % (D / 8) * 8);
-        const uint2 w = *c;
-        float x[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 d = e4m3_to_f32x2(((i < 2 ? w.x : w.y) >> (16 * (i & 1))) & 0xffffu);
-          x[2 * i] = d.x * f;
-          x[2 * i + 1] = d.y * f;
-        }
-        *c = pack8_e4m3(x);
-      }
-    }
-  }
-  const float inv = 1.f / scale;
-#pragma unroll
-  for (int i = 0; i < kUnits; ++i) {
-    const int pos = first + i * kPer * kRows;
-    if (pos < hi) {
-#pragma unroll
-      for (int k = 0; k < 16; ++k) f[i][k] *= inv;
-      char* dst = dst0 + (int64_t)(pos - base) * sd.stride_token;
-      *reinterpret_cast<uint2*>(dst + u.a) = pack8_e4m3(f[i]);
-      *reinterpret_cast<uint2*>(dst + u.b) = pack8_e4m3(f[i] + 8);
-    }
-  }
-  // every warp has read the old scale
-  if (kPer > 1) asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(kPer * 32) : "memory");
-  __syncwarp();
-  if (part == 0 && lane == 0) *sp = scale;
-}
-
-template <int D, int BITS, int kPer>
-__global__ void __launch_bounds__(kThreads) k_paged_append(const AppendParams a) {
-  __shared__ __align__(16) uint64_t s_turn[CLO_ROPE_MAX_PAIRS];
-  __shared__ float s_red[kWarps];
-  stage_turns(a.rope, s_turn);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if ((int)blockIdx.x < a.kv_blocks) {
-    const int64_t job = (int64_t)blockIdx.x * (kWarps / kPer) + warp / kPer;
-    const int heads = a.c.n_kv_heads;
-    const int64_t item = job / (2 * heads);
-    if (item >= a.items) return;
-    write_page<D, BITS, kPer>(a, s_turn, (int)item, (int)(job % heads), (int)(job / heads & 1), warp % kPer, lane, s_red, warp / kPer);
-    return;
-  }
-  constexpr int kIters = kPer == 1 ? kShortIters : kLongIters;
-  const int64_t job = (int64_t)((int)blockIdx.x - a.kv_blocks) * kWarps + warp;
-  const int64_t t = job / a.q_chunks;
-  if (t >= a.c.total_q) return;
-  // the row's sequence is looked up while its elements are on their way
-  auto position = [&](int64_t* pos) {
-    const int b = seq_of_row(a.c, (int)t, lane);
-    if (b >= a.c.batch) return false;
-    const SeqRows s = seq_rows(a.c, b);
-    if (t - s.first >= s.n) return false;  // beyond max_q: left out, as its key is
-    *pos = a.positions ? __ldg(a.positions + t) : (int64_t)s.pos0 + (t - s.first);
-    return true;
-  };
-  rotate_heads<D, kIters>(a.rope, s_turn, a.q, a.q_out, t, position, (int)(job % a.q_chunks) * heads_per_warp<D>(kIters), a.n_q_heads, lane);
 }
 
 // ---------------------------------------------------------------------------- read-back
@@ -475,19 +143,6 @@ __global__ void __launch_bounds__(kThreads) k_paged_read(const ReadParams a) {
     }
   }
 }
-
-// ---------------------------------------------------------------------------- arguments
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-const char* rows_fault(const clo_rows* r, bool vectors) {
-  if (!r || !r->ptr) return "null pointer";
-  if (reinterpret_cast<uintptr_t>(r->ptr) & 1u) return "rows must be 2-byte aligned";
-  if (vectors && (!aligned16(r->ptr) || r->stride_token % 8 || r->stride_head % 8))
-    return "rows must lie on 16-byte boundaries (strides multiples of 8 elements)";
-  return nullptr;
-}
-
-Rows rows_of(const clo_rows* r) { return Rows{static_cast<uint16_t*>(r->ptr), r->stride_token, r->stride_head}; }
 
 }  // namespace
 
@@ -564,36 +219,63 @@ extern "C" CLO_API clo_status clo_rope_plan_init(const clo_rope_config* c, clo_r
     return paged_fail(CLO_ERR_INVALID, "%s: need low_freq < high_freq", who);
   if (c->scaling == CLO_ROPE_YARN && !(c->beta_slow > 0.0 && c->beta_fast > c->beta_slow && std::isfinite(c->beta_fast)))
     return paged_fail(CLO_ERR_INVALID, "%s: need beta_fast > beta_slow > 0", who);
+  if (c->n_axes < 0 || c->n_axes > CLO_ROPE_MAX_AXES) return paged_fail(CLO_ERR_INVALID, "%s: n_axes must be 0 .. %d", who, CLO_ROPE_MAX_AXES);
+  const int axes = c->n_axes > 1 ? c->n_axes : 1;
+  if (axes > 1) {
+    int64_t sum = 0;
+    for (int a = 0; a < axes; ++a) {
+      if (c->axis_pairs[a] < 1) return paged_fail(CLO_ERR_INVALID, "%s: axis_pairs must be 1 or more for each axis", who);
+      sum += c->axis_pairs[a];
+    }
+    if (sum != rot / 2) return paged_fail(CLO_ERR_INVALID, "%s: axis_pairs must add up to rot_dim / 2", who);
+    if (c->axis_order != CLO_ROPE_SECTIONS && c->axis_order != CLO_ROPE_CYCLED)
+      return paged_fail(CLO_ERR_INVALID, "%s: unknown axis_order %d", who, c->axis_order);
+  }
   const double two_pi = 6.283185307179586476925;
   memset(plan, 0, sizeof *plan);
-  double lo = 0.0, hi = 0.0;
-  if (c->scaling == CLO_ROPE_YARN) {
-    auto pair_of = [&](double n) { return rot * std::log((double)c->original_max / (n * two_pi)) / (2.0 * std::log(c->theta)); };
-    lo = std::fmax(0.0, std::floor(pair_of(c->beta_fast)));
-    hi = std::fmin(rot - 1.0, std::ceil(pair_of(c->beta_slow)));
-  }
-  for (int i = 0; i < rot / 2; ++i) {
-    double f = std::pow(c->theta, -2.0 * i / rot);
+  int used[CLO_ROPE_MAX_AXES] = {0, 0, 0, 0}, turn = 0;
+  for (int p = 0; p < rot / 2; ++p) {
+    int axis = 0;
+    if (axes > 1 && c->axis_order == CLO_ROPE_SECTIONS) {
+      while (used[axis] == c->axis_pairs[axis]) ++axis;
+    } else if (axes > 1) {
+      while (used[turn % axes] == c->axis_pairs[turn % axes]) ++turn;
+      axis = turn++ % axes;
+    }
+    // the pair's index, and the dimensions that its series runs over
+    const bool own = axes > 1 && c->axis_own_freqs != 0;
+    const int i = own ? used[axis] : p, n = own ? 2 * c->axis_pairs[axis] : rot;
+    ++used[axis];
+    plan->axis[p] = (uint8_t)axis;
+    double f = std::pow(c->theta, -2.0 * i / n);
     double keep = 1.0;  // share of the unscaled frequency
     if (c->scaling == CLO_ROPE_LINEAR) keep = 0.0;
     if (c->scaling == CLO_ROPE_BANDS) keep = ((double)c->original_max * f / two_pi - c->low_freq) / (c->high_freq - c->low_freq);
-    if (c->scaling == CLO_ROPE_YARN) keep = 1.0 - std::fmin(1.0, std::fmax(0.0, (i - lo) / std::fmax(hi - lo, 1e-3)));
+    if (c->scaling == CLO_ROPE_YARN) {
+      auto pair_of = [&](double turns) { return n * std::log((double)c->original_max / (turns * two_pi)) / (2.0 * std::log(c->theta)); };
+      const double lo = std::fmax(0.0, std::floor(pair_of(c->beta_fast))), hi = std::fmin(n - 1.0, std::ceil(pair_of(c->beta_slow)));
+      keep = 1.0 - std::fmin(1.0, std::fmax(0.0, (i - lo) / std::fmax(hi - lo, 1e-3)));
+    }
     keep = std::fmin(1.0, std::fmax(0.0, keep));
     f = keep * f + (1.0 - keep) * f / c->factor;
     // f <= 1 radian per position, so the fraction of a turn is below 1/6
-    plan->turn[i] = (uint64_t)std::llrint(std::ldexp(f / two_pi, 62)) << 2;
+    plan->turn[p] = (uint64_t)std::llrint(std::ldexp(f / two_pi, 62)) << 2;
   }
   plan->magnitude = c->magnitude > 0.0 ? (float)c->magnitude
                     : c->scaling == CLO_ROPE_YARN ? (float)(0.1 * std::log(c->factor) + 1.0) : 1.f;
   plan->rot_dim = rot;
   plan->interleaved = c->interleaved != 0;
+  plan->n_axes = axes;
   plan->ready = 1;
   return CLO_OK;
 }
 
-static const char* plan_fault(const clo_rope_plan* p, int head_dim) {
+const char* clo::plan_fault(const clo_rope_plan* p, int head_dim) {
   if (!p) return "null plan";
-  if (p->ready != 1 || p->rot_dim < 2 || p->rot_dim % 2 || p->rot_dim > 2 * CLO_ROPE_MAX_PAIRS) return "plan not set by clo_rope_plan_init";
+  if (p->ready != 1 || p->rot_dim < 2 || p->rot_dim % 2 || p->rot_dim > 2 * CLO_ROPE_MAX_PAIRS || p->n_axes < 1 || p->n_axes > CLO_ROPE_MAX_AXES)
+    return "plan not set by clo_rope_plan_init";
+  for (int i = 0; p->n_axes > 1 && i < p->rot_dim / 2; ++i)  // the kernels read a position of each pair's axis
+    if (p->axis[i] >= p->n_axes) return "plan not set by clo_rope_plan_init";
   if (p->rot_dim > head_dim) return "rot_dim is larger than head_dim";
   return nullptr;
 }
@@ -621,80 +303,20 @@ extern "C" CLO_API clo_status clo_rope(const clo_rope_plan* plan, const clo_rows
     const int chunks = (n_heads + per - 1) / per;
     const int64_t blocks = (n_tokens * chunks + kWarps - 1) / kWarps;
     if (blocks > 0x7fffffff) return paged_fail(CLO_ERR_INVALID, "%s: too many rows for one call", who);
-    auto* f = head_dim == 128 ? (iters == kLongIters ? k_rope<128, kLongIters> : iters == kMidIters ? k_rope<128, kMidIters> : k_rope<128, kShortIters>)
-                              : (iters == kLongIters ? k_rope<64, kLongIters> : iters == kMidIters ? k_rope<64, kMidIters> : k_rope<64, kShortIters>);
+    auto kernel = [&](auto d, auto axes) {
+      constexpr int D = decltype(d)::value;
+      constexpr bool AXES = decltype(axes)::value;
+      return iters == kLongIters ? k_rope<D, kLongIters, AXES> : iters == kMidIters ? k_rope<D, kMidIters, AXES> : k_rope<D, kShortIters, AXES>;
+    };
+    using D128 = std::integral_constant<int, 128>;
+    using D64 = std::integral_constant<int, 64>;
+    auto* f = plan->n_axes > 1 ? (head_dim == 128 ? kernel(D128{}, std::true_type{}) : kernel(D64{}, std::true_type{}))
+                               : (head_dim == 128 ? kernel(D128{}, std::false_type{}) : kernel(D64{}, std::false_type{}));
     f<<<(unsigned)blocks, kThreads, 0, st>>>(r, rows_of(x), rows_of(y), positions, n_tokens, n_heads, chunks);
   } else {
     const int64_t pairs = n_tokens * n_heads * (head_dim - plan->rot_dim / 2);
     const int64_t blocks = (pairs + kThreads - 1) / kThreads;
     k_rope_any<<<(unsigned)(blocks < 65536 ? blocks : 65536), kThreads, 0, st>>>(r, rows_of(x), rows_of(y), positions, n_tokens, n_heads, head_dim);
-  }
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return paged_fail(CLO_ERR_CUDA, "%s: launch: %s", who, cudaGetErrorString(e));
-  return CLO_OK;
-}
-
-template <int D, int BITS>
-static void launch_append(const AppendParams& a, int64_t blocks, int per, cudaStream_t st) {
-  auto* f = per == 1 ? k_paged_append<D, BITS, 1> : per == 2 ? k_paged_append<D, BITS, 2> : per == 4 ? k_paged_append<D, BITS, 4> : k_paged_append<D, BITS, 8>;
-  f<<<(unsigned)blocks, kThreads, 0, st>>>(a);
-}
-
-extern "C" CLO_API clo_status clo_paged_append(const clo_paged_cache* cache, const clo_paged_batch* batch, const clo_rope_plan* plan,
-                                               const int64_t* positions, const clo_rows* k, const clo_rows* v, const clo_rows* q,
-                                               const clo_rows* q_out, int32_t n_q_heads, void* stream) {
-  const char* who = "clo_paged_append";
-  AppendParams a{};
-  if (const char* f = paged_params(cache, batch, &a.c)) return paged_fail(CLO_ERR_INVALID, "%s: %s", who, f);
-  if (plan) {
-    if (const char* f = plan_fault(plan, cache->head_dim)) return paged_fail(CLO_ERR_INVALID, "%s: %s", who, f);
-    if (plan->rot_dim % 16) return paged_fail(CLO_ERR_INVALID, "%s: rot_dim must be a multiple of 16 (rotate with clo_rope and append without a plan)", who);
-  }
-  if (!q != !q_out) return paged_fail(CLO_ERR_INVALID, "%s: q and q_out come together", who);
-  if (q && (n_q_heads < 1 || n_q_heads > 65535)) return paged_fail(CLO_ERR_INVALID, "%s: n_q_heads must be 1 .. 65535", who);
-  if (q && !plan) return paged_fail(CLO_ERR_INVALID, "%s: q without a plan", who);
-  if (reinterpret_cast<uintptr_t>(positions) & 7u) return paged_fail(CLO_ERR_INVALID, "%s: positions must be 8-byte aligned int64", who);
-  if (batch->batch == 0 || batch->total_q == 0 || a.c.max_q == 0) return CLO_OK;
-  for (const clo_rows* r : {k, v})
-    if (const char* f = rows_fault(r, true)) return paged_fail(CLO_ERR_INVALID, "%s: k, v: %s", who, f);
-  if (q)
-    for (const clo_rows* r : {q, q_out})
-      if (const char* f = rows_fault(r, true)) return paged_fail(CLO_ERR_INVALID, "%s: q, q_out: %s", who, f);
-  if (q && q->ptr == q_out->ptr && (q->stride_token != q_out->stride_token || q->stride_head != q_out->stride_head))
-    return paged_fail(CLO_ERR_INVALID, "%s: q and q_out may be the same rows only with the same strides", who);
-  a.in[0] = rows_of(k);
-  a.in[1] = rows_of(v);
-  a.positions = positions;
-  if (plan) a.rope.plan = *plan;
-  // A sequence with n rows touches at most (n - 1) / page_size + 2 pages, and no more than n.
-  const int64_t t = a.c.total_q;
-  int64_t items = t / a.c.page_size + 2 * (int64_t)a.c.batch;
-  if (items > t) items = t;
-  a.items = (int32_t)items;
-  // Warps per job: as many as hold the most rows that a page can get (a single token: one).
-  const int rows = std::min(a.c.page_size, a.c.max_q), units = rows * (cache->head_dim / 16);
-  const int per = units <= 32 * kUnits ? 1 : units <= 64 * kUnits ? 2 : units <= 128 * kUnits ? 4 : 8;
-  const int64_t jobs = items * 2 * a.c.n_kv_heads;
-  const int64_t kv_blocks = (jobs * per + kWarps - 1) / kWarps;
-  int64_t q_blocks = 0;
-  if (q) {
-    const int heads = (per == 1 ? kShortIters : kLongIters) * 32 / (cache->head_dim / 16);  // per warp
-    a.q = rows_of(q);
-    a.q_out = rows_of(q_out);
-    a.n_q_heads = n_q_heads;
-    a.q_chunks = (n_q_heads + heads - 1) / heads;
-    q_blocks = (t * a.q_chunks + kWarps - 1) / kWarps;
-  }
-  if (kv_blocks + q_blocks > 0x7fffffff) return paged_fail(CLO_ERR_INVALID, "%s: too many rows for one call", who);
-  a.kv_blocks = (int32_t)kv_blocks;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int64_t blocks = kv_blocks + q_blocks;
-  if (cache->head_dim == 128) {
-    if (cache->kv_bits == 16) launch_append<128, 16>(a, blocks, per, st);
-    else launch_append<128, 8>(a, blocks, per, st);
-  } else {
-    if (cache->kv_bits == 16) launch_append<64, 16>(a, blocks, per, st);
-    else launch_append<64, 8>(a, blocks, per, st);
   }
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return paged_fail(CLO_ERR_CUDA, "%s: launch: %s", who, cudaGetErrorString(e));

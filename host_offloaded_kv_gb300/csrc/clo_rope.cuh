@@ -1,0 +1,192 @@
+// Device parts of the rotation by positions, shared by clo_rope and clo_paged_append.
+//
+// The unit of work is 16 elements of one head's row: the two 8-element vectors whose elements pair up
+// (half layout: elements [8u, 8u + 8) and the same offset by rot_dim / 2; interleaved: 16 adjacent ones; a
+// head's rest behind rot_dim: 16 adjacent ones, copied).  d / 16 lanes cover a row, so that a lane keeps
+// its unit while its warp walks over rows.
+#pragma once
+
+#include <stddef.h>
+
+#include "clo_paged.cuh"
+
+namespace clo {
+
+struct Rope {
+  clo_rope_plan plan;  // rot_dim 0: copy
+  int transpose;
+};
+
+struct Rows {
+  uint16_t* p;
+  int64_t token, head;
+};
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+
+
+// What a lane knows about its 16-element unit.
+template <int D>
+struct Unit {
+  int a, b;       // element offsets of the two vectors
+  bool rotate, interleaved;
+  uint64_t turn[8];
+  uint64_t axes;  // AXES: a byte per pair
+  float magnitude;
+};
+
+// The plan's turns in shared memory: lanes read their units' with wide loads, where the parameter space would serve one address at a time.
+// AXES: behind them the axes of each unit's eight pairs, a byte each.
+template <bool AXES>
+constexpr int kTurns = CLO_ROPE_MAX_PAIRS + (AXES ? CLO_ROPE_MAX_PAIRS / 8 : 0);
+static_assert(offsetof(clo_rope_plan, axis) % 8 == 0, "the axes are read by eight");
+template <bool AXES>
+__device__ __forceinline__ void stage_turns(const Rope& r, uint64_t* s_turn) {
+  if (threadIdx.x < CLO_ROPE_MAX_PAIRS) s_turn[threadIdx.x] = r.plan.turn[threadIdx.x];
+  if (AXES && threadIdx.x < CLO_ROPE_MAX_PAIRS / 8) s_turn[CLO_ROPE_MAX_PAIRS + threadIdx.x] = reinterpret_cast<const uint64_t*>(r.plan.axis)[threadIdx.x];
+  __syncthreads();
+}
+
+// Where a row stands: at `pos` on every axis, or (AXES) at at[axis * stride].
+struct Place {
+  int64_t pos;
+  const int64_t* at;
+  int64_t stride;
+};
+
+template <int D, bool AXES>
+__device__ __forceinline__ Unit<D> unit_of_lane(const Rope& r, const uint64_t* s_turn, int u) {
+  Unit<D> x;
+  const int rot = r.plan.rot_dim;
+  x.rotate = u * 16 < rot;
+  x.interleaved = r.plan.interleaved != 0;
+  x.magnitude = r.plan.magnitude;
+  if (x.rotate && !x.interleaved) {
+    x.a = u * 8;
+    x.b = rot / 2 + u * 8;
+  } else {
+    x.a = u * 16;
+    x.b = u * 16 + 8;
+  }
+  if (x.rotate) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      const ulonglong2 t = *reinterpret_cast<const ulonglong2*>(s_turn + u * 8 + i);
+      x.turn[i] = t.x;
+      x.turn[i + 1] = t.y;
+    }
+    if (AXES) x.axes = s_turn[CLO_ROPE_MAX_PAIRS + u];
+  }
+  return x;
+}
+
+struct CosSin {
+  float2 v[8];
+};
+
+template <int D, bool AXES>
+__device__ __forceinline__ CosSin cos_sin_of(const Unit<D>& u, const Place& where, int transpose) {
+  CosSin c;
+  int64_t pos[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) pos[i] = AXES && where.at ? __ldg(where.at + (int64_t)((u.axes >> (8 * i)) & 0xffu) * where.stride) : where.pos;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    c.v[i] = rope_cos_sin(pos[i], u.turn[i], u.magnitude);
+    if (transpose) c.v[i].y = -c.v[i].y;
+  }
+  return c;
+}
+
+// Rotates a unit: x[0..8) are the elements at a, x[8..16) those at b.
+template <int D>
+__device__ __forceinline__ void rotate_unit(const Unit<D>& u, const CosSin& c, float* x) {
+  if (u.interleaved) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float p = x[2 * i], q = x[2 * i + 1];
+      x[2 * i] = fmaf(p, c.v[i].x, -q * c.v[i].y);
+      x[2 * i + 1] = fmaf(q, c.v[i].x, p * c.v[i].y);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float p = x[i], q = x[8 + i];
+      x[i] = fmaf(p, c.v[i].x, -q * c.v[i].y);
+      x[8 + i] = fmaf(q, c.v[i].x, p * c.v[i].y);
+    }
+  }
+}
+
+
+// ---------------------------------------------------------------------------- rows of one token
+// A warp takes one token and up to ITERS rounds of its heads: the cosines and sines of a lane's unit are computed
+// once for all of them.
+template <int D, int ITERS, bool AXES, typename F>
+__device__ __forceinline__ void rotate_heads(const Rope& r, const uint64_t* s_turn, const Rows& x, const Rows& y, int64_t token, F&& position,
+                                             int head0, int n_heads, int lane) {
+  constexpr int kLanes = D / 16, kRows = 32 / kLanes;
+  const Unit<D> u = unit_of_lane<D, AXES>(r, s_turn, lane % kLanes);
+  const uint16_t* src = x.p + token * x.token;
+  uint16_t* dst = y.p + token * y.token;
+  uint4 va[ITERS], vb[ITERS];
+#pragma unroll
+  for (int i = 0; i < ITERS; ++i) {
+    const int h = head0 + i * kRows + lane / kLanes;
+    if (h < n_heads) {
+      va[i] = *reinterpret_cast<const uint4*>(src + (int64_t)h * x.head + u.a);
+      vb[i] = *reinterpret_cast<const uint4*>(src + (int64_t)h * x.head + u.b);
+    }
+  }
+  Place where;
+  if (!position(&where)) return;
+  CosSin c;
+  if (u.rotate) c = cos_sin_of<D, AXES>(u, where, r.transpose);
+#pragma unroll
+  for (int i = 0; i < ITERS; ++i) {
+    const int h = head0 + i * kRows + lane / kLanes;
+    if (h < n_heads) {
+      if (u.rotate) {
+        float f[16];
+        unpack8(va[i], f);
+        unpack8(vb[i], f + 8);
+        rotate_unit<D>(u, c, f);
+        va[i] = pack8(f);
+        vb[i] = pack8(f + 8);
+      }
+      *reinterpret_cast<uint4*>(dst + (int64_t)h * y.head + u.a) = va[i];
+      *reinterpret_cast<uint4*>(dst + (int64_t)h * y.head + u.b) = vb[i];
+    }
+  }
+}
+
+// Rounds of heads per warp: many for long calls, where the sines count, few for short ones, where the latency does, and no more
+// than the heads fill.  8192 tokens of 128-element heads, us with 8 / 4 / 2 rounds: 8 heads (floor 5.0) 11.0 / - / 7.5, 16 heads (9.9)
+// 13.0 / 10.7 / -, 40 heads (24.7) 33.6 / 30.4 / -; 2000 tokens, 32 heads (4.8) 6.3 / 7.1 / -.
+constexpr int kLongIters = 8, kMidIters = 4, kShortIters = 2;
+constexpr int64_t kLongTokens = 8 * 152;  // a warp per SM and slot of eight
+template <int D>
+__host__ __device__ constexpr int heads_per_warp(int iters) { return iters * 32 / (D / 16); }
+
+}  // namespace
+
+// ---------------------------------------------------------------------------- arguments
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+inline const char* rows_fault(const clo_rows* r, bool vectors) {
+  if (!r || !r->ptr) return "null pointer";
+  if (reinterpret_cast<uintptr_t>(r->ptr) & 1u) return "rows must be 2-byte aligned";
+  if (vectors && (!aligned16(r->ptr) || r->stride_token % 8 || r->stride_head % 8))
+    return "rows must lie on 16-byte boundaries (strides multiples of 8 elements)";
+  return nullptr;
+}
+
+inline Rows rows_of(const clo_rows* r) { return Rows{static_cast<uint16_t*>(r->ptr), r->stride_token, r->stride_head}; }
+
+// What is wrong with a plan, or null.
+const char* plan_fault(const clo_rope_plan* p, int head_dim);
+
+}  // namespace clo

@@ -144,6 +144,15 @@ const T* vector_of(PyObject* o, const char* name, int dev, at::ScalarType type, 
   return static_cast<const T*>(t.data_ptr());
 }
 
+// Positions of n rows: [n], or [n_axes][n] for a plan of several axes.
+const int64_t* positions_of(PyObject* o, const clo_rope_plan* plan, int dev, int64_t n) {
+  if (!plan || plan->n_axes < 2) return vector_of<int64_t>(o, "positions", dev, at::kLong, n);
+  const at::Tensor& t = tensor_on(o, "positions", dev, at::kLong);
+  if (t.dim() != 2 || t.size(0) != plan->n_axes || t.size(1) != n || !t.is_contiguous())
+    refuse("positions must be a contiguous tensor of the shape [%d][%lld], a row per axis", (int)plan->n_axes, (long long)n);
+  return static_cast<const int64_t*>(t.data_ptr());
+}
+
 int64_t integer(PyObject* o, const char* name) {
   const long long v = PyLong_AsLongLong(o);
   if (v == -1 && PyErr_Occurred()) {
@@ -201,9 +210,9 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor& t = rows(a[1], "x", dev, &x);
     const int64_t tokens = t.size(0), heads = t.size(1), d = t.size(2);
     if (heads > INT32_MAX || d > INT32_MAX) refuse("x is too large");
-    const int64_t* pos = vector_of<int64_t>(a[2], "positions", dev, at::kLong, tokens);
-    at::Tensor out = output(a[3], "out", dev, tokens, heads, d, &y, a[5]);
     const clo_rope_plan* plan = address<const clo_rope_plan>(a[0]);
+    const int64_t* pos = positions_of(a[2], plan, dev, tokens);
+    at::Tensor out = output(a[3], "out", dev, tokens, heads, d, &y, a[5]);
     const int transpose = PyObject_IsTrue(a[4]);
     if (transpose < 0) throw Raised{};
     void* stream = stream_of(a[5], dev);
@@ -225,7 +234,8 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     shape_is(kt, "k", total, c->n_kv_heads, c->head_dim);
     shape_is(rows(a[3], "v", dev, &v), "v", total, c->n_kv_heads, c->head_dim);
     const clo_paged_batch b = batch_of(a[4], a[5], a[6], total, a[11], dev, small(a[1], "device"));
-    const int64_t* pos = a[8] == Py_None ? nullptr : vector_of<int64_t>(a[8], "positions", dev, at::kLong, total);
+    const clo_rope_plan* plan = address<const clo_rope_plan>(a[7]);
+    const int64_t* pos = a[8] == Py_None ? nullptr : positions_of(a[8], plan, dev, total);
     at::Tensor out;
     int32_t heads = 0;
     if (a[9] != Py_None) {
@@ -238,7 +248,6 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
       refuse("q_out without q");
     }
     const bool with_q = a[9] != Py_None;
-    const clo_rope_plan* plan = address<const clo_rope_plan>(a[7]);
     void* stream = stream_of(a[12], dev);
     const clo_status st =
         without_gil([&] { return clo_paged_append(c, &b, plan, pos, &k, &v, with_q ? &q : nullptr, with_q ? &y : nullptr, heads, stream); });

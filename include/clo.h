@@ -337,7 +337,9 @@ typedef struct clo_rows {
 } clo_rows;
 
 enum { CLO_ROPE_NONE = 0, CLO_ROPE_LINEAR = 1, CLO_ROPE_BANDS = 2, CLO_ROPE_YARN = 3 };
+enum { CLO_ROPE_SECTIONS = 0, CLO_ROPE_CYCLED = 1 };
 #define CLO_ROPE_MAX_PAIRS 64
+#define CLO_ROPE_MAX_AXES 4
 
 /* Rotary positions: pair i of the first rot_dim elements of a head is rotated by the angle
  * position * f_i, f_i = theta^(-2i / rot_dim) before scaling; the rest is copied.
@@ -349,7 +351,13 @@ enum { CLO_ROPE_NONE = 0, CLO_ROPE_LINEAR = 1, CLO_ROPE_BANDS = 2, CLO_ROPE_YARN
  *           CLO_ROPE_YARN    pair indices lo = max(0, floor(c(beta_fast))), hi = min(rot_dim - 1,
  *                            ceil(c(beta_slow))), c(n) = rot_dim ln(original_max / (2 pi n)) / (2 ln theta);
  *                            w = 1 - clamp((i - lo) / max(hi - lo, 0.001), 0, 1), as above;
- *                            magnitude 0.1 ln(factor) + 1 unless given. */
+ *                            magnitude 0.1 ln(factor) + 1 unless given.
+ * Several axes (time, height, width of images and video): a token has a position on each of n_axes axes, and pair i
+ * turns by the one of its axis. Axis a has axis_pairs[a] pairs (all of them: rot_dim / 2):
+ *   axis_order CLO_ROPE_SECTIONS  the first axis_pairs[0] pairs, then the next axis' ...
+ *              CLO_ROPE_CYCLED    in turns, axis 0, 1, .., 0, 1, .. without those whose pairs are used up
+ * The frequencies are those of the pairs' indices over rot_dim as above, or, with axis_own_freqs, each axis' own series: the
+ * axis' j-th pair has index j and rot_dim = 2 * axis_pairs[a] in the formulas above. */
 typedef struct clo_rope_config {
   int32_t rot_dim;     /* even, 2 .. 2 * CLO_ROPE_MAX_PAIRS */
   int32_t interleaved; /* nonzero: pairs (2i, 2i + 1); 0: pairs (i, i + rot_dim / 2) */
@@ -360,6 +368,10 @@ typedef struct clo_rope_config {
   double beta_fast, beta_slow; /* yarn: fast > slow > 0; default 32, 1 */
   int64_t original_max;        /* bands, yarn: original context length, >= 1 */
   double magnitude;            /* factor on the rotated elements; 0 (default) = by the scaling */
+  int32_t n_axes;              /* 0 and 1 (default): one axis, the fields below have no effect; up to CLO_ROPE_MAX_AXES */
+  int32_t axis_pairs[CLO_ROPE_MAX_AXES]; /* each >= 1 */
+  int32_t axis_order;          /* CLO_ROPE_SECTIONS (default), CLO_ROPE_CYCLED */
+  int32_t axis_own_freqs;      /* nonzero: a series of frequencies for each axis */
 } clo_rope_config;
 
 /* What the kernels take (plain values, kept by the caller; fill it with clo_rope_plan_init):
@@ -371,6 +383,8 @@ typedef struct clo_rope_plan {
   int32_t rot_dim;
   int32_t interleaved;
   int32_t ready; /* set by clo_rope_plan_init */
+  uint8_t axis[CLO_ROPE_MAX_PAIRS]; /* of each pair */
+  int32_t n_axes;
 } clo_rope_plan;
 
 CLO_API void clo_rope_config_default(clo_rope_config* cfg);
@@ -380,7 +394,7 @@ CLO_API clo_status clo_rope_plan_init(const clo_rope_config* cfg, clo_rope_plan*
 /* y = magnitude * R(position) x on the rotated elements, rounded once from fp32 to bf16; the
  * other elements are copied.  transpose != 0 applies magnitude * R(position)^T: the gradient
  * of the call.  x and y may be the same rows (same strides); other overlap is not allowed.
- * positions: int64 [n_tokens], any value.  head_dim: even, rot_dim <= head_dim <= 1024.
+ * positions: int64 [n_tokens] ([n_axes][n_tokens] for a plan of several axes), any value.  head_dim: even, rot_dim <= head_dim <= 1024.
  * n_tokens or n_heads 0: nothing to do.  Any strides and 2-byte alignment are taken.  Rows on
  * 16-byte boundaries (strides multiples of 8 elements) of 64 or 128 elements with rot_dim a
  * multiple of 16 move in 16-byte words; all others go pair by pair, at about a sixth of the rate.
@@ -427,8 +441,8 @@ typedef struct clo_paged_batch {
 } clo_paged_batch;
 
 /* Append: writes the rows of k and v ([total_q][n_kv_heads][head_dim]) to their slots, k rotated by plan
- * (NULL: as it is) at `positions` (int64 [total_q]; NULL: the rows' positions in the cache), rounded once
- * from fp32.  With q and q_out ([total_q][n_q_heads][head_dim], both or neither; in place allowed), q is
+ * (NULL: as it is) at `positions` (int64 [total_q], or [n_axes][total_q] for a plan of several axes; NULL: the rows' positions
+ * in the cache, on every axis), rounded once from fp32.  With q and q_out ([total_q][n_q_heads][head_dim], both or neither; in place allowed), q is
  * rotated into q_out in the same launch.  Slots other than the new tokens' are left as they are, but:
  * kv_bits 8: a page whose slot 0 is written gets the scale 2^e, e >= -64 the smallest with
  * max |x| <= 448 * 2^e over the finite new values of the page and head; a page that holds earlier
