@@ -122,7 +122,8 @@ class clo_paged_cache(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("k_pages", "v_pages", "k_scales", "v_scales")] + \
         [(n, ctypes.c_int64) for n in ("n_pages", "k_stride_page", "k_stride_head", "k_stride_token", "v_stride_page",
                                        "v_stride_head", "v_stride_token")] + \
-        [(n, ctypes.c_int32) for n in ("n_kv_heads", "head_dim", "page_size", "kv_bits")]
+        [(n, ctypes.c_int32) for n in ("n_kv_heads", "head_dim", "page_size", "kv_bits")] + \
+        [(n, ctypes.c_void_p) for n in ("k_group_scales", "v_group_scales")]
 
 
 class clo_paged_batch(ctypes.Structure):
@@ -406,6 +407,9 @@ class PagedCache:
     multiples of 16 bytes with head_dim contiguous (pages laid out token by token: pass
     ``pages.transpose(1, 2)``).  8-bit pages come with contiguous fp32 scales [n_pages][n_kv_heads].
 
+    4-bit pages: uint8 [n_pages][n_kv_heads][page_size][head_dim / 2], two codes to a byte, with the same scales and contiguous
+    float8_e4m3fn group scales [n_pages][n_kv_heads][page_size][head_dim / 16], one per 16 elements of a row.
+
     The calls take the batch as q_starts int32 [batch + 1], kv_lens int32 [batch] (the call's tokens included)
     and block_table int32 [batch][max_pages]; max_q is the most rows that a sequence has (default: all
     rows of the call, which is right for one sequence; a step of single tokens passes 1).
@@ -415,10 +419,11 @@ class PagedCache:
 
     Autograd records none of the calls; rows that require a gradient are refused while it records."""
 
-    def __init__(self, k_pages, v_pages, k_scales=None, v_scales=None):
+    def __init__(self, k_pages, v_pages, k_scales=None, v_scales=None, k_group_scales=None, v_group_scales=None):
         import torch
 
-        for name, t in (("k_pages", k_pages), ("v_pages", v_pages), ("k_scales", k_scales), ("v_scales", v_scales)):
+        for name, t in (("k_pages", k_pages), ("v_pages", v_pages), ("k_scales", k_scales), ("v_scales", v_scales),
+                        ("k_group_scales", k_group_scales), ("v_group_scales", v_group_scales)):
             if name.endswith("scales") and t is None:
                 continue
             if not isinstance(t, torch.Tensor) or not t.is_cuda:
@@ -429,42 +434,60 @@ class PagedCache:
                 raise ValueError(f"{name} requires a gradient, which the calls do not record")
         _fast()
         self.device = k_pages.get_device()
-        if k_pages.dtype not in (torch.bfloat16, torch.float8_e4m3fn) or v_pages.dtype is not k_pages.dtype:
-            raise ValueError(f"pages have dtypes {k_pages.dtype}, {v_pages.dtype}; expected bfloat16 or float8_e4m3fn for both")
+        if k_pages.dtype not in (torch.bfloat16, torch.float8_e4m3fn, torch.uint8) or v_pages.dtype is not k_pages.dtype:
+            raise ValueError(f"pages have dtypes {k_pages.dtype}, {v_pages.dtype}; expected bfloat16, float8_e4m3fn or uint8 (4-bit codes) for both")
         if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
             raise ValueError(f"pages have shapes {tuple(k_pages.shape)}, {tuple(v_pages.shape)}; expected "
-                             "[n_pages][n_kv_heads][page_size][head_dim] for both")
+                             "[n_pages][n_kv_heads][page_size][head_dim] for both (4-bit pages: head_dim / 2)")
         if k_pages.stride(3) != 1 or v_pages.stride(3) != 1:
             raise ValueError("pages must be contiguous along head_dim")
         n, h, s, d = k_pages.shape
-        bits = 16 if k_pages.dtype is torch.bfloat16 else 8
+        bits = 16 if k_pages.dtype is torch.bfloat16 else 8 if k_pages.dtype is torch.float8_e4m3fn else 4
+        per = 2 if bits == 4 else 1  # elements to one of the tensor's
+        d *= per
         for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
             if (t is None) != (bits == 16):
-                raise ValueError("8-bit pages come with k_scales and v_scales, bf16 pages without")
+                raise ValueError("8-bit and 4-bit pages come with k_scales and v_scales, bf16 pages without")
             if t is not None:
                 if t.dtype is not torch.float32 or tuple(t.shape) != (n, h) or not t.is_contiguous():
                     raise ValueError(f"{name} must be a contiguous fp32 tensor of shape {(n, h)}")
-        self.k_pages, self.v_pages, self.k_scales, self.v_scales = self._tensors = k_pages, v_pages, k_scales, v_scales
+        for name, t in (("k_group_scales", k_group_scales), ("v_group_scales", v_group_scales)):
+            if (t is None) != (bits != 4):
+                raise ValueError("4-bit pages come with k_group_scales and v_group_scales, others without")
+            if t is not None:
+                if t.dtype is not torch.float8_e4m3fn or tuple(t.shape) != (n, h, s, d // 16) or not t.is_contiguous():
+                    raise ValueError(f"{name} must be a contiguous float8_e4m3fn tensor of shape {(n, h, s, d // 16)}")
+        self.k_pages, self.v_pages, self.k_scales, self.v_scales, self.k_group_scales, self.v_group_scales = self._tensors = (
+            k_pages, v_pages, k_scales, v_scales, k_group_scales, v_group_scales)
         self.n_pages, self.n_kv_heads, self.page_size, self.head_dim, self.kv_bits = n, h, s, d, bits
         self._c = clo_paged_cache(k_pages.data_ptr(), v_pages.data_ptr(), None if k_scales is None else k_scales.data_ptr(),
-                                  None if v_scales is None else v_scales.data_ptr(), n, *k_pages.stride()[:3],
-                                  *v_pages.stride()[:3], h, d, s, bits)
+                                  None if v_scales is None else v_scales.data_ptr(), n, *(per * x for x in k_pages.stride()[:3]),
+                                  *(per * x for x in v_pages.stride()[:3]), h, d, s, bits,
+                                  None if k_group_scales is None else k_group_scales.data_ptr(),
+                                  None if v_group_scales is None else v_group_scales.data_ptr())
         self._ref = ctypes.byref(self._c)
         self._address = ctypes.addressof(self._c)
 
     @classmethod
-    def create(cls, n_pages: int, n_kv_heads: int, page_size: int, head_dim: int, kv_bits: int = 16, device=None):
-        """A cache of new pages (their contents are undefined until they are appended to)."""
-        if kv_bits not in (16, 8):
-            raise ValueError("kv_bits must be 16 or 8")
+    def create(cls, n_pages: int, n_kv_heads: int, page_size: int, head_dim: int, kv_bits: int = 16, device=None, group=None):
+        """A cache of new pages (their contents are undefined until they are appended to).
+
+        group: the elements that share a scale, to be stated with kv_bits 4 (16 is what the calls read and write)."""
+        if kv_bits not in (16, 8, 4):
+            raise ValueError("kv_bits must be 16, 8 or 4")
+        if (group != 16) if kv_bits == 4 else (group is not None):
+            raise ValueError("kv_bits 4 comes with group=16, the elements that share a scale; other kv_bits without a group")
         import torch
 
         device = torch.device("cuda", torch.cuda.current_device()) if device is None else device
         shape = (n_pages, n_kv_heads, page_size, head_dim)
         if kv_bits == 16:
             return cls(*(torch.empty(shape, dtype=torch.bfloat16, device=device) for _ in range(2)))
-        return cls(*(torch.empty(shape, dtype=torch.float8_e4m3fn, device=device) for _ in range(2)),
-                   *(torch.ones((n_pages, n_kv_heads), dtype=torch.float32, device=device) for _ in range(2)))
+        scales = [torch.ones((n_pages, n_kv_heads), dtype=torch.float32, device=device) for _ in range(2)]
+        if kv_bits == 8:
+            return cls(*(torch.empty(shape, dtype=torch.float8_e4m3fn, device=device) for _ in range(2)), *scales)
+        return cls(*(torch.empty((*shape[:3], head_dim // 2), dtype=torch.uint8, device=device) for _ in range(2)), *scales,
+                   *(torch.empty((*shape[:3], head_dim // 16), dtype=torch.float8_e4m3fn, device=device) for _ in range(2)))
 
     def append(self, k, v, q_starts, kv_lens, block_table, rope: clo_rope_plan | None = None, positions=None, q=None,
                q_out=None, max_q=None, stream=None):

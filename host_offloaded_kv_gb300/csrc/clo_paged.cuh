@@ -18,10 +18,11 @@ constexpr float kMinScale = 1e-30f;   // smallest page scale that a reader uses
 constexpr int kMaxGroup = 16;         // query heads per kv head
 constexpr int64_t kMaxPagedTokens = int64_t(1) << 30;
 
-// One of K or V: pages, scales (8-bit pages) and strides in elements.
+// One of K or V: pages, scales (8-bit and 4-bit pages), group scales (4-bit pages) and strides in elements.
 struct PagedSide {
   char* pages;
   float* scales;
+  uint8_t* groups;
   int64_t stride_page, stride_head, stride_token;
 };
 
@@ -151,6 +152,35 @@ __device__ __forceinline__ float2 e4m3_to_f32x2(uint32_t two) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
+// Eight 4-bit codes as four fp16 pairs, in order (exact).
+__device__ __forceinline__ void e2m1_to_f16x8(uint32_t eight, uint32_t* h) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(eight));
+}
+// Eight 4-bit codes: nearest, ties to even, beyond +-6 (infinities too) to +-6.
+__device__ __forceinline__ uint32_t pack8_e2m1(const float* x) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tcvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\tmov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(r)
+      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
+  return r;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// 4-bit pages: offset of the group scales of a page's and head's slot.
+template <int D>
+__device__ __forceinline__ int64_t groups_at(const PagedParams& p, int page, int head, int slot) {
+  return (((int64_t)page * p.n_kv_heads + head) * p.page_size + slot) * (D / 16);
+}
+// Two group scales next to each other as fp32.
+__device__ __forceinline__ float2 group_scales(const uint8_t* two) { return e4m3_to_f32x2(*reinterpret_cast<const uint16_t*>(two)); }
+
 // A sequence's visible tokens for a row at position `pos` are [0, sink_end) and [lo, hi).
 struct Visible {
   int sink_end, lo, hi;
@@ -196,7 +226,7 @@ clo_status paged_fail(clo_status st, const char* fmt, ...);
 
 // ---------------------------------------------------------------------------- TMA
 // Tensor maps of K and V as [page][head][slot][element] with boxes of `rows` slots and one swizzle span (128
-// bytes, or the whole row where that is 64) of elements.
+// bytes, or the whole row where that is less) of elements.
 struct PageMaps {
   CUtensorMap side[2];
 };
@@ -220,6 +250,15 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, in
       "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
       "l"(map), "r"(element), "r"(slot), "r"(head), "r"(page), "r"(bar)
       : "memory");
+}
+
+// Group scales of a page's and head's `slots` slots from `slot` on (both multiples of 16) to shared memory.  Runs of 64 bytes are too
+// short for boxes, which want 128-byte boundaries there.
+template <int D>
+__device__ __forceinline__ void copy_groups(uint32_t dst, const PagedParams& p, const PagedSide& sd, int page, int head, int slot, int slots, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(sd.groups + groups_at<D>(p, page, head, slot)),
+               "r"(slots * (D / 16)), "r"(bar)
+               : "memory");
 }
 
 __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {

@@ -54,7 +54,7 @@ extern "C" CLO_API clo_status clo_paged_append(const clo_paged_cache* cache, con
   a.kv_blocks = (int32_t)kv_blocks;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int64_t blocks = kv_blocks + q_blocks;
-  (cache->kv_bits == 16 ? launch_append_bf16 : launch_append_e4m3)(a, cache->head_dim, blocks, per, st);
+  (cache->kv_bits == 16 ? launch_append_bf16 : cache->kv_bits == 8 ? launch_append_e4m3 : launch_append_e2m1)(a, cache->head_dim, blocks, per, st);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return paged_fail(CLO_ERR_CUDA, "%s: launch: %s", who, cudaGetErrorString(e));
   return CLO_OK;

@@ -24,6 +24,7 @@ struct AppendParams {
 // A call's launch, by the pages' type.
 void launch_append_bf16(const AppendParams& a, int head_dim, int64_t blocks, int per, cudaStream_t st);
 void launch_append_e4m3(const AppendParams& a, int head_dim, int64_t blocks, int per, cudaStream_t st);
+void launch_append_e2m1(const AppendParams& a, int head_dim, int64_t blocks, int per, cudaStream_t st);
 
 namespace {
 
@@ -64,6 +65,112 @@ __device__ __forceinline__ bool item_of(const PagedParams& p, int item, int lane
   return false;
 }
 
+// ---- 4-bit pages.  A group is 16 neighbouring elements, that is two 8-element vectors, of two lanes where a rotated row pairs up its halves.
+
+// Where the other vectors of the groups of this lane's vectors are: the lane, and which of its two.
+template <int D>
+struct Partners {
+  int lane_a, lane_b;
+  bool second_a, second_b;
+};
+template <int D>
+__device__ __forceinline__ Partners<D> partners_of(bool halves, int rot_dim, int lane) {
+  constexpr int kLanes = D / 16;
+  const int u = lane % kLanes, row = lane - u, n = halves ? rot_dim / 16 : 0;  // rotating units of a row in the half layout
+  auto owner = [&](int vec, bool* second) {
+    *second = vec < 2 * n ? vec >= n : vec & 1;
+    return row + (vec < 2 * n ? (vec >= n ? vec - n : vec) : vec >> 1);
+  };
+  Partners<D> w;
+  w.lane_a = owner((u < n ? u : 2 * u) ^ 1, &w.second_a);
+  w.lane_b = owner((u < n ? n + u : 2 * u + 1) ^ 1, &w.second_b);
+  return w;
+}
+
+// Codes and group scales of a unit's two vectors.
+struct Codes4 {
+  uint32_t a, b, scale_a, scale_b;
+  bool near;  // what fp32's rotation left open: a code or a scale lies within its error of a border
+};
+
+// e4m3 code of the scale of a group whose largest |x|, over the page's scale, has these bits (infinity: the largest scale; NaN: NaN).
+__device__ __forceinline__ uint32_t group_scale_of(uint32_t bits) {
+  if (bits >= 0x7f800000u) return bits == 0x7f800000u ? 0x7eu : 0x7fu;
+  return pack_e4m3(__fdiv_rn(__uint_as_float(bits), 6.f), 0.f);
+}
+
+// x: a unit's values; inv: one over the page's scale (a power of two).  All lanes of the warp take part.
+template <int D>
+__device__ __forceinline__ Codes4 encode_unit(const float* x, float inv, bool rotated, const Partners<D>& with) {
+  float y[16], err[8];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) y[k] = x[k] * inv;
+  // |x - exact| <= 2^-21 (|p| + |q|) over the rotated pair p, q: sine and cosine are off by 7.5e-8, three roundings of 2^-24 follow, and the
+  // unrotated pair's |p| + |q| is at most sqrt(2) times the rotated one's.  Twice the pair's larger element is as good a bound and needs no
+  // pairing: here the larger of the unit's whole, which only flags a little more.
+  float top = 0.f;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) top = fmaxf(top, fabsf(y[k]));
+  const float off = rotated && top < INFINITY ? top * 0x1p-20f : 0.f;
+  (void)err;
+  uint32_t key[2] = {0u, 0u};
+#pragma unroll
+  for (int k = 0; k < 16; ++k) key[k / 8] = max(key[k / 8], __float_as_uint(y[k]) & 0x7fffffffu);
+  Codes4 c;
+  c.near = false;
+  uint32_t code[2];
+#pragma unroll
+  for (int v = 0; v < 2; ++v) {
+    const int from = v ? with.lane_b : with.lane_a;
+    const bool second = v ? with.second_b : with.second_a;
+    const uint32_t ka = __shfl_sync(0xffffffffu, key[0], from), kb = __shfl_sync(0xffffffffu, key[1], from);
+    const float other_off = __shfl_sync(0xffffffffu, off, from);
+    const uint32_t all = max(key[v], second ? kb : ka);
+    const uint32_t scale = group_scale_of(all);
+    if (rotated && all < 0x7f800000u) {
+      const float m = __uint_as_float(all), o = fmaxf(off, other_off);
+      c.near |= group_scale_of(__float_as_uint(m + o)) != scale || group_scale_of(__float_as_uint(fmaxf(m - o, 0.f))) != scale;
+    }
+    // x / scale, rounded once: a product with the rounded reciprocal and one correction by the exact remainder
+    const float s = e4m3_to_f32x2(scale).x, r = s > 0.f ? 1.f / s : 0.f;
+    float q[8], lo[8], hi[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float z = y[8 * v + k], t = z * r;
+      q[k] = fabsf(t) < INFINITY ? fmaf(fmaf(-t, s, z), r, t) : t;
+      lo[k] = q[k] - off * r;
+      hi[k] = q[k] + off * r;
+    }
+    code[v] = pack8_e2m1(q);
+    if (rotated) c.near |= pack8_e2m1(lo) != code[v] || pack8_e2m1(hi) != code[v];
+    if (v) c.scale_b = scale;
+    else c.scale_a = scale;
+  }
+  c.a = code[0];
+  c.b = code[1];
+  return c;
+}
+
+// The rotated values of a unit from an exact angle, in fp64, rounded to the odd one of the two nearest fp32 numbers: such a value lies on the
+// same side of every border between codes as the exact one, as borders have fewer bits.
+template <int D, bool AXES>
+__device__ __noinline__ void rotate_exactly(const Unit<D>& u, const Place& where, const uint16_t* src, float* x) {
+  auto odd = [](double v) {
+    const float f = __double2float_rz(v);
+    return (double)f == v ? f : __uint_as_float(__float_as_uint(f) | 1u);
+  };
+#pragma unroll 1
+  for (int i = 0; i < 8; ++i) {
+    const int64_t pos = AXES && where.at ? __ldg(where.at + (int64_t)((u.axes >> (8 * i)) & 0xffu) * where.stride) : where.pos;
+    const int ip = u.interleaved ? 2 * i : i, iq = u.interleaved ? 2 * i + 1 : 8 + i;  // in the unit
+    const double p = bf16_bits_to_f32(src[(ip < 8 ? u.a : u.b - 8) + ip]), q = bf16_bits_to_f32(src[(iq < 8 ? u.a : u.b - 8) + iq]);
+    double s, c;
+    sincospi((double)(int64_t)((uint64_t)pos * u.turn[i]) * 0x1p-63, &s, &c);
+    x[ip] = odd((p * c - q * s) * (double)u.magnitude);
+    x[iq] = odd((q * c + p * s) * (double)u.magnitude);
+  }
+}
+
 // One job: (touched page, kv head, K or V), by kPer warps.  A lane holds kUnits units (16 elements of a row each) in registers from
 // the load to the store, so that rows are read and rotated once also where the page's scale comes in between; kPer warps
 // hold the most rows that a page can get from the call.
@@ -89,7 +196,7 @@ __device__ __forceinline__ void write_page(const AppendParams& a, const uint64_t
     u.a = (lane % kLanes) * 16;
     u.b = u.a + 8;
   }
-  char* dst0 = sd.pages + ((int64_t)page * sd.stride_page + (int64_t)head * sd.stride_head) * (BITS / 8);
+  char* dst0 = sd.pages + ((int64_t)page * sd.stride_page + (int64_t)head * sd.stride_head) * BITS / 8;
   const int first = lo + part * kRows + lane / kLanes;  // this lane's rows: first, + kPer * kRows, ...
 
   uint4 va[kUnits], vb[kUnits];
@@ -139,9 +246,10 @@ __device__ __forceinline__ void write_page(const AppendParams& a, const uint64_t
 #pragma unroll
     for (int i = 0; i < kPer; ++i) amax = fmaxf(amax, s_red[group * kPer + i]);
   }
-  // smallest e with amax <= 1.75 * 2^(8 + e), from the bits of amax
+  // smallest e with amax <= 448 * 2^e (8 bits: 1.75 * 2^8) or 2688 * 2^e (4 bits: 1.3125 * 2^11), from the bits of amax
+  constexpr int kTopExp = BITS == 8 ? 8 : 11, kTopMantissa = BITS == 8 ? 0x600000 : 0x280000;
   const int bits = __float_as_int(amax);
-  int e = (bits >> 23) - 127 - 8 + ((bits & 0x7fffff) > 0x600000 ? 1 : 0);
+  int e = (bits >> 23) - 127 - kTopExp + ((bits & 0x7fffff) > kTopMantissa ? 1 : 0);
   e = max(e, kMinScaleExp);
   float scale = __int_as_float((e + 127) << 23);
   float* sp = sd.scales + (int64_t)page * p.n_kv_heads + head;
@@ -151,7 +259,16 @@ __device__ __forceinline__ void write_page(const AppendParams& a, const uint64_t
       scale = old;
     } else if (old > 0.f) {
       const float f = old / scale;
-      for (int v = part * 32 + lane; v < (lo - base) * (D / 8); v += kPer * 32) {
+      if (BITS == 4) {
+        // the earlier tokens' group scales, four at a time (a row's are one or two words)
+        uint32_t* const words = reinterpret_cast<uint32_t*>(sd.groups + groups_at<D>(p, page, head, 0));
+        for (int v = part * 32 + lane; v < (lo - base) * (D / 64); v += kPer * 32) {
+          const uint32_t w = words[v];
+          const float2 x = e4m3_to_f32x2(w & 0xffffu), y = e4m3_to_f32x2(w >> 16);
+          words[v] = pack_e4m3(x.x * f, x.y * f) | pack_e4m3(y.x * f, y.y * f) << 16;
+        }
+      }
+      for (int v = part * 32 + lane; BITS == 8 && v < (lo - base) * (D / 8); v += kPer * 32) {
         uint2* c = reinterpret_cast<uint2*>(dst0 + (int64_t)(v / (D / 8)) * sd.stride_token + v % (D / 8) * 8);
         const uint2 w = *c;
         float x[8];
@@ -166,8 +283,50 @@ __device__ __forceinline__ void write_page(const AppendParams& a, const uint64_t
     }
   }
   const float inv = 1.f / scale;
+  if constexpr (BITS == 4) {
+    const Partners<D> with = partners_of<D>(rotate && !u.interleaved, a.rope.plan.rot_dim, lane);
+    uint8_t* const groups = sd.groups + groups_at<D>(p, page, head, 0);
+#pragma unroll 1
+    for (int i = 0; i < kUnits && lo + part * kRows + i * kPer * kRows < hi; ++i) {
+      const int pos = first + i * kPer * kRows;
+      float x[16];
 #pragma unroll
-  for (int i = 0; i < kUnits; ++i) {
+      for (int n = 0; n < kUnits; ++n)
+        if (n == i) {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) x[k] = f[n][k];
+        }
+      if (pos >= hi) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) x[k] = 0.f;
+      }
+      Codes4 c = encode_unit<D>(x, inv, rotate && pos < hi, with);
+      if (__any_sync(0xffffffffu, c.near)) {
+        if (c.near) {
+          const int64_t row = s.first + (pos - s.pos0);
+          Place where{pos, nullptr, 0};
+          if (AXES && a.positions)
+            where = {0, a.positions + row, a.c.total_q};
+          else if (a.positions)
+            where.pos = __ldg(a.positions + row);
+          const uint16_t* src = in.p + row * in.token + (int64_t)head * in.head;
+          rotate_exactly<D, AXES>(u, where, src, x);
+        }
+        c = encode_unit<D>(x, inv, false, with);
+      }
+      if (pos < hi) {
+        char* dst = dst0 + (int64_t)(pos - base) * sd.stride_token / 2;
+        *reinterpret_cast<uint32_t*>(dst + u.a / 2) = c.a;
+        *reinterpret_cast<uint32_t*>(dst + u.b / 2) = c.b;
+        // the vector with the group's first elements writes its scale
+        uint8_t* const g = groups + (pos - base) * (D / 16);
+        if (u.a % 16 == 0) g[u.a / 16] = (uint8_t)c.scale_a;
+        if (u.b % 16 == 0) g[u.b / 16] = (uint8_t)c.scale_b;
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; BITS == 8 && i < kUnits; ++i) {
     const int pos = first + i * kPer * kRows;
     if (pos < hi) {
 #pragma unroll

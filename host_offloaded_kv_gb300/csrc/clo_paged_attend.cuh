@@ -26,6 +26,12 @@ __device__ void attend_row(const AttendParams& a, int b, const SeqRows& s, int r
     const PagedSide& sd = p.side[side];
     const int64_t at = (int64_t)page * sd.stride_page + (int64_t)kvh * sd.stride_head + (int64_t)slot * sd.stride_token + e;
     if (BITS == 16) return bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(sd.pages)[at]);
+    if (BITS == 4) {
+      uint32_t h[4];
+      e2m1_to_f16x8(reinterpret_cast<const uint8_t*>(sd.pages)[at >> 1] >> (e & 1 ? 4 : 0), h);
+      const float g = e4m3_to_f32x2(sd.groups[groups_at<D>(p, page, kvh, slot) + e / 16]).x;
+      return __half22float2(*reinterpret_cast<const __half2*>(h)).x * g * fmaxf(sd.scales[(int64_t)page * p.n_kv_heads + kvh], kMinScale);
+    }
     return e4m3_to_f32x2(reinterpret_cast<const uint8_t*>(sd.pages)[at]).x *
            fmaxf(sd.scales[(int64_t)page * p.n_kv_heads + kvh], kMinScale);
   };
@@ -64,7 +70,7 @@ template <int SPAN>
 __device__ __forceinline__ uint32_t swizzled(uint32_t base, int rows, int row, int chunk) {
   constexpr int kChunks = SPAN / 16;
   const int c = chunk % kChunks;
-  const int x = SPAN == 128 ? c ^ (row & 7) : c ^ ((row >> 1) & 3);
+  const int x = SPAN == 128 ? c ^ (row & 7) : SPAN == 64 ? c ^ ((row >> 1) & 3) : c ^ ((row >> 2) & 1);
   return base + chunk / kChunks * rows * SPAN + row * SPAN + x * 16;
 }
 
@@ -74,6 +80,9 @@ __device__ __forceinline__ bool not_finite2(uint32_t x) {
   constexpr uint32_t E = BITS == 16 ? 0x7f80u : 0x7c00u;
   return (x & E) == E || ((x >> 16) & E) == E;
 }
+
+// True if one of four e4m3 codes is NaN (0x7f or 0xff).
+__device__ __forceinline__ bool e4m3_nan4(uint32_t x) { return __vcmpeq4(x & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0; }
 
 template <int BITS>
 __device__ __forceinline__ bool not_finite16(const uint4 w) {
@@ -113,7 +122,7 @@ __device__ __forceinline__ bool spoilt_rows(const AttendParams& a, int b, int kv
                                             bool want, int pos, bool nan, int lane) {
   const PagedParams& p = a.c;
   const PagedSide& sd = p.side[1];
-  constexpr int kLanes = D * BITS / 64, kPer = 32 / kLanes;  // lanes of a row (8 bytes each), rows of a load
+  constexpr int kLanes = D * BITS / 64, kPer = 32 / kLanes;  // lanes of a row (8 bytes each), rows of a load; 4-bit pages have no use of these
   constexpr int kBatch = 16 / kPer < 8 ? 16 / kPer : 8;  // loads in flight
   constexpr uint32_t kRow = kLanes == 32 ? 0xffffffffu : (1u << kLanes) - 1u;
   bool spoilt = false, saw_nan = false, saw_inf = false;
@@ -124,6 +133,28 @@ __device__ __forceinline__ bool spoilt_rows(const AttendParams& a, int b, int kv
     for (int g = g0; g < min(g0 + 32, groups); ++g) {
       const int page = __shfl_sync(0xffffffffu, mine, g - g0), j0 = first_of(g);
       if (page < 0 || j0 >= hi) continue;
+      if constexpr (BITS == 4) {
+        // codes are finite: a lane per token looks at its group scales
+        const int64_t at = groups_at<D>(p, page, kvh, (j0 + (lane & 15)) & (p.page_size - 1));
+        uint32_t w[2] = {0u, 0u};
+        if (j0 + (lane & 15) < hi) {
+          w[0] = __ldg(reinterpret_cast<const uint32_t*>(sd.groups + at));
+          if (D == 128) w[1] = __ldg(reinterpret_cast<const uint32_t*>(sd.groups + at + 4));
+        }
+        const uint32_t nans = __ballot_sync(0xffffffffu, e4m3_nan4(w[0]) || e4m3_nan4(w[1])) & 0xffffu;
+        const bool large = !(sd.scales[(int64_t)page * p.n_kv_heads + kvh] >= 0x1p-80f);
+        if (nans || large) {
+#pragma unroll 1
+          for (int r = 0; r < 16 && j0 + r < hi; ++r) {
+            const int j = j0 + r;
+            const bool n = nans >> r & 1u, see = j <= pos && j < s.kv_len && (a.window == 0 || j > pos - a.window || j < a.sinks);
+            spoilt |= see ? large : n;
+            saw_nan |= see && n;
+          }
+        }
+        if (!__any_sync(0xffffffffu, want && !spoilt)) return want;
+        continue;
+      }
       const char* src = sd.pages + ((int64_t)page * sd.stride_page + (int64_t)kvh * sd.stride_head) * (BITS / 8) + lane % kLanes * 8;
       const bool small_scale = BITS == 8 && !(sd.scales[(int64_t)page * p.n_kv_heads + kvh] >= 0x1p-80f);
 #pragma unroll 1
@@ -216,6 +247,8 @@ cudaError_t launch_after(void (*f)(Params...), dim3 grid, int threads, cudaStrea
 
 cudaError_t launch_attend_few_bf16(const AttendParams& a, int head_dim, cudaStream_t st);
 cudaError_t launch_attend_few_e4m3(const AttendParams& a, int head_dim, cudaStream_t st);
+cudaError_t launch_attend_few_e2m1(const AttendParams& a, int head_dim, cudaStream_t st);
+int64_t attend_few_e2m1_bytes(const AttendParams& a, int head_dim);
 int64_t attend_few_bf16_bytes(const AttendParams& a, int head_dim);
 int64_t attend_few_e4m3_bytes(const AttendParams& a, int head_dim);
 cudaError_t launch_attend_many(const AttendParams& a, int head_dim, int kv_bits, cudaStream_t st);

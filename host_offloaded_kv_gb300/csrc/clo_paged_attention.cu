@@ -51,14 +51,15 @@ cudaError_t prepare_kernel(const void* f, int smem, std::atomic<uint64_t>* prepa
 const char* make_page_maps(const PagedParams& c, int head_dim, int kv_bits, int rows, PageMaps* maps) {
   EncodeFn encode = tensor_map_encoder();
   if (!encode) return "no tensor map encoder in the driver";
-  const int bytes = kv_bits / 8, span = std::min(head_dim * bytes, 128);
+  const int unit = kv_bits == 16 ? 2 : 1, row = head_dim * kv_bits / 8, span = std::min(row, 128);  // bytes
   for (int s = 0; s < 2; ++s) {
     const PagedSide& sd = c.side[s];
-    const cuuint64_t dims[4] = {(cuuint64_t)head_dim, (cuuint64_t)c.page_size, (cuuint64_t)c.n_kv_heads, (cuuint64_t)c.n_pages};
-    const cuuint64_t strides[3] = {(cuuint64_t)sd.stride_token * bytes, (cuuint64_t)sd.stride_head * bytes, (cuuint64_t)sd.stride_page * bytes};
-    const cuuint32_t box[4] = {(cuuint32_t)(span / bytes), (cuuint32_t)rows, 1, 1}, step[4] = {1, 1, 1, 1};
-    const CUresult r = encode(&maps->side[s], bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, sd.pages, dims, strides,
-                              box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, span == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+    const cuuint64_t dims[4] = {(cuuint64_t)(row / unit), (cuuint64_t)c.page_size, (cuuint64_t)c.n_kv_heads, (cuuint64_t)c.n_pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)sd.stride_token * kv_bits / 8, (cuuint64_t)sd.stride_head * kv_bits / 8, (cuuint64_t)sd.stride_page * kv_bits / 8};
+    const cuuint32_t box[4] = {(cuuint32_t)(span / unit), (cuuint32_t)rows, 1, 1}, step[4] = {1, 1, 1, 1};
+    const CUresult r = encode(&maps->side[s], unit == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, sd.pages, dims, strides,
+                              box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              span == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : span == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return "the driver refused a tensor map of the pages";
   }
@@ -102,7 +103,7 @@ extern "C" CLO_API clo_status clo_paged_attention_workspace(const clo_paged_cach
   if (a.part_rows > kFewRows)
     *bytes = attend_many_bytes(a, cache->head_dim);
   else
-    *bytes = cache->kv_bits == 16 ? attend_few_bf16_bytes(a, cache->head_dim) : attend_few_e4m3_bytes(a, cache->head_dim);
+    *bytes = (cache->kv_bits == 16 ? attend_few_bf16_bytes : cache->kv_bits == 8 ? attend_few_e4m3_bytes : attend_few_e2m1_bytes)(a, cache->head_dim);
   return CLO_OK;
 }
 
@@ -136,7 +137,7 @@ extern "C" CLO_API clo_status clo_paged_attention(const clo_paged_cache* cache, 
   if (a.part_rows > kFewRows)
     e = launch_attend_many(a, cache->head_dim, cache->kv_bits, st);
   else
-    e = cache->kv_bits == 16 ? launch_attend_few_bf16(a, cache->head_dim, st) : launch_attend_few_e4m3(a, cache->head_dim, st);
+    e = (cache->kv_bits == 16 ? launch_attend_few_bf16 : cache->kv_bits == 8 ? launch_attend_few_e4m3 : launch_attend_few_e2m1)(a, cache->head_dim, st);
   if (e != cudaSuccess) return paged_fail(CLO_ERR_CUDA, "%s: launch: %s", who, cudaGetErrorString(e));
   return CLO_OK;
 }

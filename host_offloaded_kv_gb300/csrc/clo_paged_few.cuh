@@ -14,7 +14,7 @@ namespace {
 // with movmatrix.
 //
 // Each warp owns a ring of kStages 8 KB stages (16 tokens of bf16 K and V rows of 128, 64 tokens of 8-bit rows of 64) that it
-// fills with TMA boxes, so no warp waits for another before a unit's end, where they join through shared memory.
+// fills with TMA boxes (4-bit pages: 64 tokens and their group scales), so no warp waits for another before a unit's end, where they join through shared memory.
 //
 // All units' tiles are cut into equal shares, one per block of a single wave, so that ragged batches load the SMs alike and one
 // long sequence fills the GPU; a second kernel joins what the cuts met.  Without a workspace units stay whole.  (Clusters that
@@ -33,7 +33,6 @@ constexpr int kThreads = kWarps * 32;
 // bf16 166 us for 163, one sequence of 524,288 tokens of 8-bit pages 173 us for 165, 64 sequences of 64-element heads 27 us for 22.
 // Three blocks with 8-bit pages: 170 us and more for 165.
 constexpr int kStages = 2;
-constexpr int kFewSmem = kWarps * kStages * kStageBytes + 1024;
 constexpr int kWave = 2 * kSms;  // blocks: two to an SM
 
 // 8-bit pages: weights up to 2^14 (fp16 then holds them down to 2^-38 of the largest) are divided by their page's V scale, which may be as
@@ -46,9 +45,12 @@ struct Tile {
   static constexpr int kRowBytes = D * BITS / 8;
   static constexpr int kSpan = kRowBytes < 128 ? kRowBytes : 128;  // bytes of a row in one swizzled block
   static constexpr int kSpans = kRowBytes / kSpan;
-  static constexpr int kTokens = kStageBytes / (2 * kRowBytes);
+  static constexpr int kTokens = BITS == 4 ? 64 : kStageBytes / (2 * kRowBytes);
   static constexpr int kM = kTokens / 16;
   static constexpr int kSideBytes = kTokens * kRowBytes;
+  static constexpr int kGroupBytes = BITS == 4 ? kTokens * (D / 16) : 0;  // group scales, of K and then of V, behind the codes
+  static constexpr int kStage = 2 * (kSideBytes + kGroupBytes);
+  static constexpr int kSmem = kWarps * kStages * kStage + 1024;
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t* r) {
@@ -56,6 +58,16 @@ __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t* r) {
 }
 __device__ __forceinline__ void ldsm4_trans(uint32_t addr, uint32_t* r) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+// One, two or four words at once.
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t* w) {
+  if constexpr (N == 4)
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr) : "memory");
+  else if constexpr (N == 2)
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr) : "memory");
+  else
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(addr) : "memory");
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
@@ -171,7 +183,7 @@ __global__ void __launch_bounds__(kThreads) k_attend_few(const AttendParams a, c
   const PagedParams& p = a.c;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, g = lane >> 2, t4 = lane & 3;
   const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t ring = smem + warp * kStages * kStageBytes;
+  const uint32_t ring = smem + warp * kStages * T::kStage;
   uint8_t* const generic = smem_raw + (smem - smem_u32(smem_raw));
   FewShare share{0, 1, 0, (int)blockIdx.x, (int)blockIdx.y};
   if (a.part) share = few_share(a, TOK, lane);
@@ -238,20 +250,20 @@ __global__ void __launch_bounds__(kThreads) k_attend_few(const AttendParams a, c
     };
     auto issue = [&](int k, int page, int st) {
       const unsigned there = __ballot_sync(0xffffffffu, page >= 0);
-      if (BITS == 8 && page >= 0) {  // lanes below KM
+      if (BITS != 16 && page >= 0) {  // lanes below KM
         const int64_t at = (int64_t)page * p.n_kv_heads + kvh;
 #pragma unroll
         for (int side = 0; side < 2; ++side)
           asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(&s_scale[warp][st][side][lane])), "l"(p.side[side].scales + at) : "memory");
       }
       const int box = min(p.page_size, TOK), first = tl.at(k) * TOK;
-      const uint32_t dst = ring + st * kStageBytes, bar = smem_u32(&s_full[warp][st]);
+      const uint32_t dst = ring + st * T::kStage, bar = smem_u32(&s_full[warp][st]);
       int id[KM];
 #pragma unroll
       for (int g = 0; g < KM; ++g) id[g] = __shfl_sync(0xffffffffu, page, g);
       if (elect_one()) {
         s_there[warp][st] = there;
-        mbar_arrive_expect_tx(&s_full[warp][st], kStageBytes);
+        mbar_arrive_expect_tx(&s_full[warp][st], 2 * T::kSideBytes + 2 * __popc(there) * (BITS == 4 ? D : 0));
 #pragma unroll
         for (int g = 0; g < KM; ++g)
           if (g * 16 % box == 0) {
@@ -261,10 +273,16 @@ __global__ void __launch_bounds__(kThreads) k_attend_few(const AttendParams a, c
               for (int h = 0; h < T::kSpans; ++h)
                 tma_box(dst + side * T::kSideBytes + h * TOK * T::kSpan + g * 16 * T::kSpan, &maps.side[side], h * (T::kSpan * 8 / BITS),
                         (first + g * 16) & (p.page_size - 1), kvh, id[g], bar);
+            if constexpr (BITS == 4) {
+#pragma unroll
+              for (int side = 0; side < 2; ++side)  // of a page that is not there: what the stage held, which no row sees
+                if (id[g] >= 0)
+                  copy_groups<D>(dst + 2 * T::kSideBytes + side * T::kGroupBytes + g * 16 * (D / 16), p, p.side[side], id[g], kvh, (first + g * 16) & (p.page_size - 1), box, bar);
+            }
           }
       }
       __syncwarp();
-      if (BITS == 8) cp_async_commit();
+      if (BITS != 16) cp_async_commit();
     };
 
     const bool dead = __any_sync(0xffffffffu, s_dead != 0);  // a copy was lost: the rest of the share is NaN
@@ -274,13 +292,13 @@ __global__ void __launch_bounds__(kThreads) k_attend_few(const AttendParams a, c
 #pragma unroll
     for (int i = 0; i < kStages; ++i) {
       if (k0 + i * stride < n_tiles && !dead) issue(k0 + i * stride, page_next[i], st + i < kStages ? st + i : st + i - kStages);
-      else if (BITS == 8) cp_async_commit();
+      else if (BITS != 16) cp_async_commit();
     }
     int page_ahead = page_for(k0 + kStages * stride);
 
     // Q^T fragments: column (row of the unit) nt * 8 + g.  bf16: elements kk * 16 + 2 t4 + {0, 1} and + 8.  8-bit pages: the lane's
-    // four codes of a 16-element chunk are neighbours, so elements kk * 16 + 4 t4 + {0, 1} and {2, 3}; q in fp16, scaled by
-    // a power of two that puts the row's largest finite element into [2^14, 2^15).
+    // four codes of a 16-element chunk are neighbours, so elements kk * 16 + 4 t4 + {0, 1} and {2, 3}; 4-bit pages: its eight codes of 32
+    // elements, shared by two products; q in fp16, scaled by a power of two that puts the row's largest finite element into [2^14, 2^15).
     uint32_t qf[NT][KD][2];
     float fac[NT][2];
 #pragma unroll
@@ -299,7 +317,7 @@ __global__ void __launch_bounds__(kThreads) k_attend_few(const AttendParams a, c
         float mx = 0.f;
 #pragma unroll
         for (int kk = 0; kk < KD; ++kk) {
-          raw[kk] = r < rows ? *reinterpret_cast<const uint2*>(qp + kk * 16 + 4 * t4) : make_uint2(0u, 0u);
+          raw[kk] = r < rows ? *reinterpret_cast<const uint2*>(qp + (BITS == 4 ? kk / 2 * 32 + 8 * t4 + kk % 2 * 4 : kk * 16 + 4 * t4)) : make_uint2(0u, 0u);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const uint32_t w = i < 2 ? raw[kk].x : raw[kk].y;
@@ -340,14 +358,14 @@ __global__ void __launch_bounds__(kThreads) k_attend_few(const AttendParams a, c
     bool odd = false, ok = !dead;
 
     for (int k = k0; k < n_tiles && ok; k += stride) {
-      if (BITS == 8) cp_async_wait<kStages - 1>();
+      if (BITS != 16) cp_async_wait<kStages - 1>();
       __syncwarp();
       ok = mbar_wait_limited(&s_full[warp][st], phase);
       if (!__all_sync(0xffffffffu, ok)) {
         ok = false;
         break;
       }
-      const uint32_t kb = ring + st * kStageBytes, vb = kb + T::kSideBytes;
+      const uint32_t kb = ring + st * T::kStage, vb = kb + T::kSideBytes;
       const int j0 = tl.at(k) * TOK;
       const uint32_t there = s_there[warp][st];
       // every row sees the whole tile
@@ -355,7 +373,21 @@ __global__ void __launch_bounds__(kThreads) k_attend_few(const AttendParams a, c
       // is looked over for the same reason.
       const bool whole = there == (1u << KM) - 1u && j0 + TOK <= va.hi && (j0 >= vz.lo || j0 + TOK <= (a.window > 0 ? a.sinks : 0));
 
-      if (!whole) {
+      if (BITS == 4 && !whole) {
+        // codes are finite: clearing a token's group scales clears its V
+        constexpr int kWords = D / 64;
+#pragma unroll 1
+        for (int i = lane; i < TOK * kWords; i += 32) {
+          const int r = i / kWords, j = j0 + r;
+          const bool any = (there >> (r >> 4) & 1u) && j < vz.hi && (j >= va.lo || j < (a.window > 0 ? a.sinks : 0));
+          uint32_t* at = reinterpret_cast<uint32_t*>(generic + (vb - smem) + T::kSideBytes + T::kGroupBytes) + i;
+          if (!any)
+            *at = 0u;
+          else if (s.n > 1)
+            odd |= e4m3_nan4(*at);
+        }
+        __syncwarp();
+      } else if (!whole) {
         constexpr int kChunks = T::kRowBytes / 16;
 #pragma unroll 1
         for (int i = lane; i < TOK * kChunks; i += 32) {
@@ -385,6 +417,35 @@ __global__ void __launch_bounds__(kThreads) k_attend_few(const AttendParams a, c
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) mma16816<BITS>(sc[mt][nt], f, qf[nt][kk][0], qf[nt][kk][1]);
           }
+        } else if (BITS == 4) {
+          // A lane holds eight codes of 32 elements of tokens g and g + 8 (the pairs of two products) and the scale of the group they are in.
+          const uint32_t gs = kb + 2 * T::kSideBytes + (mt * 16 + g) * (D / 16), pick = t4 < 2 ? 0x2200u : 0x3311u;
+          uint32_t sw[2][D / 64];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) lds_words<D / 64>(gs + h * 8 * (D / 16), sw[h]);
+#pragma unroll
+          for (int c = 0; c < D / 32; c += 2) {
+            uint32_t r[4], sg[2][2];  // [token g, g + 8][chunk]: the scale, twice
+            ldsm4(swizzled<T::kSpan>(kb, TOK, mt * 16 + (lane & 15), c + (lane >> 4)), r);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) e4m3_to_f16x4(__byte_perm(sw[h][c / 2], 0u, pick), &sg[h][0], &sg[h][1]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              uint32_t x[2][4];
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                e2m1_to_f16x8(r[2 * i + h], x[h]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[h][e] = mul_f16x2(x[h][e], sg[h][i]);
+              }
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const uint32_t f[4] = {x[0][2 * j], x[1][2 * j], x[0][2 * j + 1], x[1][2 * j + 1]};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) mma16816<BITS>(sc[mt][nt], f, qf[nt][2 * (c + i) + j][0], qf[nt][2 * (c + i) + j][1]);
+              }
+            }
+          }
         } else {
 #pragma unroll
           for (int kk = 0; kk < KD; kk += 2) {
@@ -409,7 +470,7 @@ __global__ void __launch_bounds__(kThreads) k_attend_few(const AttendParams a, c
       for (int mt = 0; mt < KM; ++mt) {
         float ks = 1.f, lvs = 0.f;
         inv_vs[mt] = 1.f;
-        if (BITS == 8) {
+        if (BITS != 16) {
           ks = fmaxf(s_scale[warp][st][0][mt], kMinScale);
           const float vs = fmaxf(s_scale[warp][st][1][mt], kMinScale);
           lvs = __log2f(vs);
@@ -420,7 +481,7 @@ __global__ void __launch_bounds__(kThreads) k_attend_few(const AttendParams a, c
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float f = fac[nt][i & 1] * ks;
-            sc[mt][nt][i] = BITS == 8 ? fmaf(sc[mt][nt][i], f, lvs) : sc[mt][nt][i] * f;
+            sc[mt][nt][i] = BITS != 16 ? fmaf(sc[mt][nt][i], f, lvs) : sc[mt][nt][i] * f;
             if (!whole) {
               const int j = j0 + mt * 16 + g + (i >> 1) * 8;
               const int pos = s.pos0 + token_of_row(a, nt * 8 + 2 * t4 + (i & 1));
@@ -462,7 +523,7 @@ __global__ void __launch_bounds__(kThreads) k_attend_few(const AttendParams a, c
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             w[i] = exp2_fast(sc[mt][nt][i] - ref[i & 1]);
-            l[nt][i & 1] = BITS == 8 ? fmaf(w[i], inv_vs[mt], l[nt][i & 1]) : l[nt][i & 1] + w[i];
+            l[nt][i & 1] = BITS != 16 ? fmaf(w[i], inv_vs[mt], l[nt][i & 1]) : l[nt][i & 1] + w[i];
           }
           // weights in the products' type: bf16 next to bf16 V, fp16 next to 8-bit V (three bits more, and V is exact in it)
 #pragma unroll
@@ -482,6 +543,40 @@ __global__ void __launch_bounds__(kThreads) k_attend_few(const AttendParams a, c
             ldsm4_trans(swizzled<T::kSpan>(vb, TOK, mt * 16 + (lane & 7) + (lane >> 4) * 8, dt * 2 + (lane >> 3 & 1)), f);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) mma16816<BITS>(acc[dt][nt], f, pf[mt][nt][0], pf[mt][nt][1]);
+          }
+        } else if (BITS == 4) {
+          // A lane holds elements 4 g .. 4 g + 3 of 32, of tokens 2 t4 and 2 t4 + 1 (r[0]) and of those 8 on (r[1]); pairs of tokens are what
+          // a product takes, so the halves change places: rows g and g + 8 of two products.
+          const uint32_t gs = vb + T::kSideBytes + T::kGroupBytes + (mt * 16 + 2 * t4) * (D / 16), pick = g < 4 ? 0x6240u : 0x7351u;
+          uint32_t sw[2][2 * (D / 64)];  // [tokens 2 t4.., 2 t4 + 8..][token, word]
+#pragma unroll
+          for (int h = 0; h < 2; ++h) lds_words<2 * (D / 64)>(gs + h * 8 * (D / 16), sw[h]);
+#pragma unroll
+          for (int c = 0; c < D / 32; c += 2) {
+            uint32_t r[4], sg[2][2];  // [tokens][chunk]: both tokens' scales
+            ldsm4_trans(swizzled<T::kSpan>(vb, TOK, mt * 16 + (lane & 15), c + (lane >> 4)), r);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) e4m3_to_f16x4(__byte_perm(sw[h][c / 2], sw[h][D / 64 + c / 2], pick), &sg[h][0], &sg[h][1]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              uint32_t x[2][4];
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                uint32_t y[4];
+                e2m1_to_f16x8(r[2 * i + h], y);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  x[h][2 * e] = mul_f16x2(__byte_perm(y[e], y[e + 2], 0x5410), sg[h][i]);
+                  x[h][2 * e + 1] = mul_f16x2(__byte_perm(y[e], y[e + 2], 0x7632), sg[h][i]);
+                }
+              }
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const uint32_t f[4] = {x[0][2 * j], x[0][2 * j + 1], x[1][2 * j], x[1][2 * j + 1]};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) mma16816<BITS>(acc[2 * (c + i) + j][nt], f, pf[mt][nt][0], pf[mt][nt][1]);
+              }
+            }
           }
         } else {
           // two 16-element chunks per load; a lane's pairs of elements 2 g, 2 g + 1 of two tokens become rows g and g + 8
@@ -508,7 +603,7 @@ __global__ void __launch_bounds__(kThreads) k_attend_few(const AttendParams a, c
         fence_proxy_async_smem();
         issue(kn, page_ahead, st);
         page_ahead = page_for(kn + stride);
-      } else if (BITS == 8) {
+      } else if (BITS != 16) {
         cp_async_commit();
       }
       if (++st == kStages) {
@@ -516,7 +611,7 @@ __global__ void __launch_bounds__(kThreads) k_attend_few(const AttendParams a, c
         phase ^= 1u;
       }
     }
-    if (BITS == 8) cp_async_wait<0>();
+    if (BITS != 16) cp_async_wait<0>();
     // A wait that gave up (a copy lost): the rows become NaN.  The copies in flight get the same limit again.
     if (!ok) {
       if (!dead)
@@ -530,7 +625,7 @@ __global__ void __launch_bounds__(kThreads) k_attend_few(const AttendParams a, c
 
     // Join the warps: every warp's accumulator in its own ring.
     float* part = reinterpret_cast<float*>(generic);
-    constexpr int kPart = kStages * kStageBytes / 4;
+    constexpr int kPart = kStages * T::kStage / 4;
     static_assert(ROWS * (D + 4) <= kPart, "a warp's accumulator fits its ring");
     if (__any_sync(0xffffffffu, odd) && lane == 0) s_odd = 1;
     __syncwarp();
@@ -551,7 +646,7 @@ __global__ void __launch_bounds__(kThreads) k_attend_few(const AttendParams a, c
         for (int dt = 0; dt < KD; ++dt)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const int e = dt * 16 + (BITS == 16 ? g + 8 * h : 2 * g + h);
+            const int e = BITS == 4 ? dt / 2 * 32 + 4 * g + dt % 2 * 2 + h : dt * 16 + (BITS == 16 ? g + 8 * h : 2 * g + h);
             part[warp * kPart + r * (D + 4) + e] = acc[dt][nt][i + 2 * h];
           }
       }
@@ -687,9 +782,9 @@ cudaError_t few_rows(AttendParams a, int64_t* bytes, cudaStream_t st) {
   if (make_page_maps(a.c, D, BITS, std::min(a.c.page_size, T::kTokens), &maps)) return cudaErrorInvalidValue;
   auto* f = k_attend_few<D, BITS, NT>;
   static std::atomic<uint64_t> prepared{0};
-  cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(f), kFewSmem, &prepared);
+  cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(f), T::kSmem, &prepared);
   if (e != cudaSuccess) return e;
-  f<<<a.part ? dim3(kWave) : dim3(a.c.batch, a.c.n_kv_heads), kThreads, kFewSmem, st>>>(a, maps);
+  f<<<a.part ? dim3(kWave) : dim3(a.c.batch, a.c.n_kv_heads), kThreads, T::kSmem, st>>>(a, maps);
   e = cudaGetLastError();
   if (e != cudaSuccess || !a.part) return e;
   const int64_t units = (int64_t)a.c.batch * a.c.n_kv_heads;

@@ -18,7 +18,7 @@
 //   warps 8, 11      TMA of K and of V: pages -> ring of operand tiles, K(0) K(1) V(0) K(2) V(1) ...
 //   warp 9           MMA issue: P V of a token tile, then S of the lane's next one, the lanes in turn
 //   warp 10          bf16 pages: V behind the last token that any row sees is cleared
-//   warps 12-15      8-bit pages only: codes -> fp16 operand tiles
+//   warps 12-15      8-bit and 4-bit pages: codes -> fp16 operand tiles (4-bit: times their groups' scales, exact)
 //
 // The accumulator is rescaled only when a row's maximum has grown by more than 2^8 (weights stay below 2^8 times
 // the largest so far; exact in the end, as sum and accumulator share the reference).
@@ -140,9 +140,10 @@ struct Cfg {
   static constexpr int kQBytes = kRows * D * 2;
   // operand tiles of the ring, and 8-bit tiles on their way into it: what fits next to Q
   static constexpr int kSlots = BITS == 16 ? (D == 64 ? 8 : TILES == 2 ? 4 : 5) : (D == 64 ? 6 : 4);
-  static constexpr int kRawSide = BITS == 16 ? 0 : D == 64 ? 6 : TILES == 2 ? 2 : 3;  // halves of 64 tokens, for K and for V
+  static constexpr int kRawSide = BITS == 16 ? 0 : D == 64 ? 6 : BITS == 8 ? (TILES == 2 ? 2 : 3) : (TILES == 2 ? 3 : 6);  // halves of 64 tokens, for K and for V
   static constexpr int kRaw = 2 * kRawSide;
-  static constexpr int kRawBytes = BITS == 16 ? 0 : kTok * D / 2;
+  static constexpr int kRawCodes = BITS == 16 ? 0 : kTok / 2 * D * BITS / 8;
+  static constexpr int kRawBytes = kRawCodes + (BITS == 4 ? kTok / 2 * (D / 16) : 0);  // 4-bit pages: group scales behind the codes
   static constexpr int kMeta = D == 64 ? 16 : 8;  // token tiles whose page data is kept: more than the ring runs ahead
   static constexpr int kThreads = BITS == 16 ? 384 : 512;
   static constexpr int kBytes = TILES * kQBytes + kSlots * kTileBytes + kRaw * kRawBytes + 1024;
@@ -564,7 +565,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
       }
       cp_async_commit();
       cp_async_wait<0>();
-      if (BITS == 8) {
+      if (BITS != 16) {
         __syncwarp();
 #pragma unroll 1
         for (int i = 0; i < kIters; ++i) {
@@ -592,7 +593,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
       ok = ok && __all_sync(0xffffffffu, wait(sh, &sh.q_ready[my_tile], q_phase));
       q_phase ^= 1u;
     }
-    const float fac = BITS == 8 ? a.scale_log2 * __uint_as_float((uint32_t)(127 + sh.q_exp[my_tile][tid & 127]) << 23) : a.scale_log2;
+    const float fac = BITS != 16 ? a.scale_log2 * __uint_as_float((uint32_t)(127 + sh.q_exp[my_tile][tid & 127]) << 23) : a.scale_log2;
     {
       // the tile's first and last row bound what "every row sees" means; rows past the end follow the last one
       const int rf = min(row0 + my_tile * kRows, rows - 1), rl = min(row0 + my_tile * kRows + kRows - 1, rows - 1);
@@ -641,7 +642,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
           for (int k = 0; k < 16; k += 2)
 #pragma unroll
             for (int h = 0; h < 4; ++h) m4[h] = fmaxf(m4[h], fmaxf(__uint_as_float(x[16 * h + k]), __uint_as_float(x[16 * h + k + 1])));
-          if (BITS == 8) {
+          if (BITS != 16) {
 #pragma unroll
             for (int h = 0; h < 4; ++h) m4[h] = fmaf(m4[h], fmaxf(sh.scale[slot][0][4 * half + h] * fac, 1e-37f), sh.scale[slot][1][4 * half + h]);
           }
@@ -675,7 +676,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
           for (int h = 0; h < 4; ++h) {
             // 16 tokens: one page, one set of scales
             const int at = 4 * half + h;
-            const float mul = BITS == 8 ? fmaxf(sh.scale[slot][0][at] * fac, 1e-37f) : fac, add = BITS == 8 ? sh.scale[slot][1][at] + sub : sub;
+            const float mul = BITS != 16 ? fmaxf(sh.scale[slot][0][at] * fac, 1e-37f) : fac, add = BITS != 16 ? sh.scale[slot][1][at] + sub : sub;
             const uint64_t mul2 = pack2(mul, mul), add_2 = pack2(add, add);
 #pragma unroll
             for (int k = 0; k < 16; k += 2) {
@@ -686,9 +687,9 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
               // weights in the products' type: bf16 next to bf16 V, fp16 next to 8-bit V
               w[8 * h + k / 2] = BITS == 16 ? pack_bf16(y.x, y.y) : pack_f16(y.x, y.y);
             }
-            if (BITS == 8 || h == 3) {
+            if (BITS != 16 || h == 3) {
               const float2 q = unpack2(add2(sum2[0], sum2[1]));
-              l = BITS == 8 ? fmaf(q.x + q.y, sh.scale[slot][2][at], l) : l + (q.x + q.y);
+              l = BITS != 16 ? fmaf(q.x + q.y, sh.scale[slot][2][at], l) : l + (q.x + q.y);
               sum2[0] = sum2[1] = 0;
             }
           }
@@ -789,7 +790,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
               *reinterpret_cast<uint4*>(dst.p) = *reinterpret_cast<const uint4*>(from + i * 128 + ((c ^ (r0 + i)) & 7) * 16);
             dst.next();
           }
-          if (BITS == 8) {
+          if (BITS != 16) {
             // a sum of weights past fp32's range (scales near 2^-100)
             __syncwarp();
             unsigned again = __ballot_sync(0xffffffffu, row_ok && row_end(lost, l == INFINITY) == RowEnd::again);
@@ -810,7 +811,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
     if (warp == 8 || warp == 11) {
       // ---------------------------------------------------------------------- TMA: K and page data; V
       const int side = warp == 8 ? 0 : 1;
-      constexpr int kSpan = BITS == 16 ? 128 : (D < 128 ? D : 128);  // bytes of a page row in one box
+      constexpr int kSpan = D * BITS / 8 < 128 ? D * BITS / 8 : 128;  // bytes of a page row in one box
       constexpr int kBoxSpans = D * BITS / 8 / kSpan;
       // The ring of operand tiles (16 bits), or the side's own ring of half tiles.  Two warps may fill one ring in turns only if it holds
       // three elements or more: the parity of an earlier use than the one waited for must not be met (K jumps three places from
@@ -832,7 +833,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
       };
       auto scales_of = [&](int page) {
         float2 sc = make_float2(1.f, 1.f);
-        if (BITS == 8 && side == 0 && page >= 0) {
+        if (BITS != 16 && side == 0 && page >= 0) {
           const int64_t at = (int64_t)page * p.n_kv_heads + kvh;
           sc = make_float2(__ldg(p.side[0].scales + at), __ldg(p.side[1].scales + at));
         }
@@ -863,13 +864,24 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
           if (elect_one()) {
             const uint32_t dst = BITS == 16 ? ring + buf * C::kTileBytes : raw + buf * C::kRawBytes, bar = smem_u32(full);
             const int slot0 = u.tl.at(u.t_begin + j) * kTok + h * kPartTok;
-            mbar_arrive_expect_tx(full, BITS == 16 ? C::kTileBytes : C::kRawBytes);
+            int groups = 0;  // bytes of group scales that are there; the others are zeros, as codes of a page that is not there
+            if (BITS == 4) {
+#pragma unroll
+              for (int g = 0; g < kPartTok / 16; ++g) {
+                groups += id[g] >= 0 ? D : 0;
+                if (id[g] < 0)
+                  for (int i = 0; i < D; i += 16) *reinterpret_cast<uint4*>(generic + (raw - smem) + buf * C::kRawBytes + C::kRawCodes + g * D + i) = make_uint4(0, 0, 0, 0);
+              }
+            }
+            mbar_arrive_expect_tx(full, BITS == 16 ? C::kTileBytes : C::kRawCodes + groups);
 #pragma unroll
             for (int g = 0; g < kPartTok / 16; ++g)
               if (g * 16 % box == 0) {
 #pragma unroll
                 for (int w = 0; w < kBoxSpans; ++w)
                   tma_box(dst + g * 16 * kSpan + w * kTok * kSpan, &maps.side[side], w * (kSpan * 8 / BITS), (slot0 + g * 16) & (p.page_size - 1), kvh, id[g], bar);
+                if (BITS == 4 && id[g] >= 0)
+                  copy_groups<D>(dst + C::kRawCodes + g * 16 * (D / 16), p, p.side[side], id[g], kvh, (slot0 + g * 16) & (p.page_size - 1), box, bar);
               }
           }
           __syncwarp();
@@ -878,7 +890,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
           const int slot = (tiles_done + j) % kMeta;
           const unsigned there = __ballot_sync(0xffffffffu, page0 >= 0) >> (8 * q) & 0xffu;
           if (lane == 0) sh.there[slot] = there;
-          if (BITS == 8 && lane >> 3 == q) {
+          if (BITS != 16 && lane >> 3 == q) {
             const float vs = fmaxf(scale0.y, kMinScale);
             sh.scale[slot][0][lane & 7] = fmaxf(scale0.x, kMinScale);
             sh.scale[slot][1][lane & 7] = __log2f(vs);
@@ -1000,17 +1012,28 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
           return true;
         });
       } else {
-        // ------------------------------------------------------------------ 8-bit codes -> fp16
-        // A warp takes 16 rows of a half tile, a quarter of it 4 neighbouring chunks of two rows that differ in bits 0 and 2: then
-        // neither the reads nor the writes of the swizzled tiles meet in a bank.
-        constexpr int kHalves = D / 64, kPer = 2 * kHalves;  // 16-byte chunks of codes per thread and half tile
-        const int w4 = warp - 12, pair = lane >> 3, r8 = lane & 4 ? pair ^ 5 : pair;
-        uint32_t from[kPer], to[kPer];  // offsets in the half tile and in the operand tile's half
+        // ------------------------------------------------------------------ codes -> fp16
+        // 8-bit pages: a warp takes 16 rows of a half tile, a quarter of it 4 neighbouring chunks of two rows that differ in bits 0 and 2: then
+        // neither the reads nor the writes of the swizzled tiles meet in a bank.  4-bit pages: a quarter takes one chunk (32 elements) of eight rows
+        // that follow one another, which has the same effect.
+        constexpr int kHalves = D / 64, kPer = BITS == 8 ? 2 * kHalves : kHalves;  // 16-byte chunks of codes per thread and half tile
+        const int w4 = warp - 12, pair = lane >> 3, r8 = BITS == 4 ? lane & 7 : lane & 4 ? pair ^ 5 : pair;
+        // row in the half tile
+        auto row_of = [&](int i) { return w4 * 16 + (BITS == 8 ? i / kHalves : D == 128 ? i : lane >> 4) * 8 + r8; };
+        uint32_t from[kPer], to[kPer], scales[kPer];  // offsets in the half tile, in the operand tile's half, and of the group scales
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-          const int r = w4 * 16 + i / kHalves * 8 + r8, h = i % kHalves, c = h * 4 + (lane & 3);
-          from[i] = swizzled<(D < 128 ? 64 : 128)>(0, kTok, r, c);
-          to[i] = h * kTok * 128 + r * 128 + (((2 * (lane & 3)) ^ (r & 7)) << 4);
+          const int r = row_of(i);
+          if (BITS == 8) {
+            const int h = i % kHalves, c = h * 4 + (lane & 3);
+            from[i] = swizzled<(D < 128 ? 64 : 128)>(0, kTok, r, c);
+            to[i] = h * kTok * 128 + r * 128 + (((2 * (lane & 3)) ^ (r & 7)) << 4);
+          } else {
+            const int c = pair & (D / 32 - 1);
+            from[i] = swizzled<(D / 2)>(0, kTok, r, c);
+            to[i] = c / 2 * kTok * 128 + r * 128 + (((c & 1) * 4 ^ (r & 7)) << 4);
+            scales[i] = C::kRawCodes + r * (D / 16) + 2 * c;
+          }
         }
         int e_base = 0;
         walk([&](const Unit& u, int64_t) {
@@ -1032,13 +1055,32 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
             uint4 w[kPer];
 #pragma unroll
             for (int i = 0; i < kPer; ++i) w[i] = *reinterpret_cast<const uint4*>(src + from[i]);
+            uint32_t two[kPer];  // 4-bit pages: the scales of a chunk's two groups
+            if (BITS == 4) {
+#pragma unroll
+              for (int i = 0; i < kPer; ++i) two[i] = *reinterpret_cast<const uint16_t*>(src + scales[i]);
+            }
             if (seen < kTok) {
 #pragma unroll
               for (int i = 0; i < kPer; ++i)
-                if (half * 64 + w4 * 16 + i / kHalves * 8 + r8 >= seen) w[i] = make_uint4(0, 0, 0, 0);
+                if (half * 64 + row_of(i) >= seen) {
+                  w[i] = make_uint4(0, 0, 0, 0);
+                  two[i] = 0;
+                }
             }
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
+              if (BITS == 4) {
+                const uint32_t sc = e4m3_to_f16x2(two[i]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const uint32_t sg = __byte_perm(sc, 0u, k < 2 ? 0x1010 : 0x3232);
+                  uint32_t y[4];
+                  e2m1_to_f16x8(k == 0 ? w[i].x : k == 1 ? w[i].y : k == 2 ? w[i].z : w[i].w, y);
+                  *reinterpret_cast<uint4*>(dst + (to[i] ^ (16 * k))) = make_uint4(mul_f16x2(y[0], sg), mul_f16x2(y[1], sg), mul_f16x2(y[2], sg), mul_f16x2(y[3], sg));
+                }
+                continue;
+              }
               uint4 lo, hi;
               e4m3_to_f16x4(w[i].x, &lo.x, &lo.y);
               e4m3_to_f16x4(w[i].y, &lo.z, &lo.w);
@@ -1167,8 +1209,8 @@ cudaError_t launch_rows(const AttendParams& a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_attend_many(const AttendParams& a, int head_dim, int kv_bits, cudaStream_t st) {
-  if (head_dim == 128) return kv_bits == 16 ? launch_rows<128, 16>(a, st) : launch_rows<128, 8>(a, st);
-  return kv_bits == 16 ? launch_rows<64, 16>(a, st) : launch_rows<64, 8>(a, st);
+  if (head_dim == 128) return kv_bits == 16 ? launch_rows<128, 16>(a, st) : kv_bits == 8 ? launch_rows<128, 8>(a, st) : launch_rows<128, 4>(a, st);
+  return kv_bits == 16 ? launch_rows<64, 16>(a, st) : kv_bits == 8 ? launch_rows<64, 8>(a, st) : launch_rows<64, 4>(a, st);
 }
 
 int64_t attend_many_bytes(const AttendParams& a, int head_dim) {

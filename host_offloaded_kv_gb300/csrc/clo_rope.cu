@@ -110,9 +110,13 @@ __global__ void __launch_bounds__(kThreads) k_paged_read(const ReadParams a) {
       w[i] = make_uint4(0, 0, 0, 0);
       scale[i] = 1.f;
       if (v < 2 * n && page >= 0) {
-        const char* src = sd.pages + ((int64_t)page * sd.stride_page + (int64_t)h * sd.stride_head + (int64_t)slot * sd.stride_token + e) * (BITS / 8);
+        const char* src = sd.pages + ((int64_t)page * sd.stride_page + (int64_t)h * sd.stride_head + (int64_t)slot * sd.stride_token + e) * BITS / 8;
         if (BITS == 16) {
           w[i] = __ldg(reinterpret_cast<const uint4*>(src));
+        } else if (BITS == 4) {
+          w[i].x = __ldg(reinterpret_cast<const uint32_t*>(src));
+          w[i].y = __ldg(sd.groups + groups_at<D>(p, page, h, slot) + e / 16);
+          scale[i] = __ldg(sd.scales + (int64_t)page * p.n_kv_heads + h);
         } else {
           const uint2 c = __ldg(reinterpret_cast<const uint2*>(src));
           w[i].x = c.x;
@@ -138,6 +142,19 @@ __global__ void __launch_bounds__(kThreads) k_paged_read(const ReadParams a) {
           x[2 * k + 1] = d.y * f;
         }
         w[i] = pack8(x);
+      } else if (BITS == 4) {
+        // the group's scale first: the product of two fp32 numbers of a few bits is exact, and so is that with a power of two
+        const float f = e4m3_to_f32x2(w[i].y).x * fmaxf(scale[i], kMinScale);
+        uint32_t half[4];
+        e2m1_to_f16x8(w[i].x, half);
+        float x[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 d = __half22float2(*reinterpret_cast<const __half2*>(&half[k]));
+          x[2 * k] = d.x * f;
+          x[2 * k + 1] = d.y * f;
+        }
+        w[i] = pack8(x);
       }
       *reinterpret_cast<uint4*>(out.p + t * out.token + (int64_t)h * out.head + e) = w[i];
     }
@@ -151,7 +168,7 @@ const char* paged_params(const clo_paged_cache* c, const clo_paged_batch* b, Pag
   if (!c || !b) return "null pointer";
   if (!c->k_pages || !c->v_pages) return "null pages";
   if (c->head_dim != 64 && c->head_dim != 128) return "head_dim must be 64 or 128";
-  if (c->kv_bits != 16 && c->kv_bits != 8) return "kv_bits must be 16 or 8";
+  if (c->kv_bits != 16 && c->kv_bits != 8 && c->kv_bits != 4) return "kv_bits must be 16, 8 or 4";
   if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128)
     return "page_size must be 16, 32, 64 or 128";
   if (c->n_kv_heads < 1 || c->n_kv_heads > 65535) return "n_kv_heads must be 1 .. 65535";
@@ -159,10 +176,12 @@ const char* paged_params(const clo_paged_cache* c, const clo_paged_batch* b, Pag
   const int64_t per16 = 128 / c->kv_bits;
   const int64_t strides[6] = {c->k_stride_page, c->k_stride_head, c->k_stride_token, c->v_stride_page, c->v_stride_head, c->v_stride_token};
   for (int64_t s : strides)
-    if (s <= 0 || s % per16 || s * (c->kv_bits / 8) >= (int64_t(1) << 40)) return "page strides must be positive multiples of 16 bytes, below 2^40 bytes";
+    if (s <= 0 || s % per16 || s >= (int64_t(8) << 40) / c->kv_bits) return "page strides must be positive multiples of 16 bytes, below 2^40 bytes";
   if (!aligned16(c->k_pages) || !aligned16(c->v_pages)) return "pages must be 16-byte aligned";
-  if (c->kv_bits == 8 && (!c->k_scales || !c->v_scales || (reinterpret_cast<uintptr_t>(c->k_scales) & 3u) || (reinterpret_cast<uintptr_t>(c->v_scales) & 3u)))
-    return "8-bit pages need 4-byte aligned scales";
+  if (c->kv_bits != 16 && (!c->k_scales || !c->v_scales || (reinterpret_cast<uintptr_t>(c->k_scales) & 3u) || (reinterpret_cast<uintptr_t>(c->v_scales) & 3u)))
+    return "8-bit and 4-bit pages need 4-byte aligned scales";
+  if (c->kv_bits == 4 && (!c->k_group_scales || !c->v_group_scales || !aligned16(c->k_group_scales) || !aligned16(c->v_group_scales)))
+    return "4-bit pages need 16-byte aligned group scales";
   if (b->batch < 0 || b->batch > 65535) return "batch must be 0 .. 65535";
   if (b->total_q < 0 || b->total_q > kMaxPagedTokens || b->max_q < 0) return "total_q must be 0 .. 2^30, max_q not negative";
   if (b->max_pages < 0 || (int64_t)b->max_pages * c->page_size >= kMaxPagedTokens) return "max_pages * page_size must be below 2^30";
@@ -171,8 +190,8 @@ const char* paged_params(const clo_paged_cache* c, const clo_paged_batch* b, Pag
     if ((reinterpret_cast<uintptr_t>(b->q_starts) | reinterpret_cast<uintptr_t>(b->kv_lens) | reinterpret_cast<uintptr_t>(b->block_table)) & 3u)
       return "the batch's arrays must be 4-byte aligned";
   }
-  p->side[0] = PagedSide{static_cast<char*>(c->k_pages), c->k_scales, c->k_stride_page, c->k_stride_head, c->k_stride_token};
-  p->side[1] = PagedSide{static_cast<char*>(c->v_pages), c->v_scales, c->v_stride_page, c->v_stride_head, c->v_stride_token};
+  p->side[0] = PagedSide{static_cast<char*>(c->k_pages), c->k_scales, static_cast<uint8_t*>(c->k_group_scales), c->k_stride_page, c->k_stride_head, c->k_stride_token};
+  p->side[1] = PagedSide{static_cast<char*>(c->v_pages), c->v_scales, static_cast<uint8_t*>(c->v_group_scales), c->v_stride_page, c->v_stride_head, c->v_stride_token};
   p->q_starts = b->q_starts;
   p->kv_lens = b->kv_lens;
   p->table = b->block_table;
@@ -337,10 +356,12 @@ extern "C" CLO_API clo_status clo_paged_read(const clo_paged_cache* cache, const
   const unsigned blocks = (unsigned)((a.c.total_q + kWarps - 1) / kWarps);
   if (cache->head_dim == 128) {
     if (cache->kv_bits == 16) k_paged_read<128, 16><<<blocks, kThreads, 0, st>>>(a);
-    else k_paged_read<128, 8><<<blocks, kThreads, 0, st>>>(a);
+    else if (cache->kv_bits == 8) k_paged_read<128, 8><<<blocks, kThreads, 0, st>>>(a);
+    else k_paged_read<128, 4><<<blocks, kThreads, 0, st>>>(a);
   } else {
     if (cache->kv_bits == 16) k_paged_read<64, 16><<<blocks, kThreads, 0, st>>>(a);
-    else k_paged_read<64, 8><<<blocks, kThreads, 0, st>>>(a);
+    else if (cache->kv_bits == 8) k_paged_read<64, 8><<<blocks, kThreads, 0, st>>>(a);
+    else k_paged_read<64, 4><<<blocks, kThreads, 0, st>>>(a);
   }
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return paged_fail(CLO_ERR_CUDA, "%s: launch: %s", who, cudaGetErrorString(e));

@@ -408,11 +408,15 @@ CLO_API clo_status clo_rope(const clo_rope_plan* plan, const clo_rows* x, const 
  * and kv head, separate for K and V.  The scales that clo_paged_append writes are powers
  * of two, so values are exact in bf16; clo_paged_attention and clo_paged_read take any positive
  * finite scales (below 1e-30: taken as 1e-30).
- * Base addresses on 16-byte boundaries, strides multiples of 16 bytes and > 0. */
+ * kv_bits 4: codes of a sign, two exponent bits and one of mantissa (0, 1/2, 1, 3/2, 2, 3, 4, 6 and their negatives; bit 3 is the sign),
+ * two to a byte, element 2i in the low half of byte i, with an e4m3 scale for each 16 neighbouring elements of a row:
+ * value = code * group scale * scale[p][h], scale[p][h] as for kv_bits 8. A group scale of NaN makes its 16 values NaN. The group
+ * scales of page p, head h, slot t are the head_dim / 16 bytes at ((p * n_kv_heads + h) * page_size + t) * head_dim / 16.
+ * Base addresses (pages, group scales) on 16-byte boundaries, strides multiples of 16 bytes and > 0. */
 typedef struct clo_paged_cache {
   void* k_pages;
   void* v_pages;
-  float* k_scales; /* fp32 [n_pages][n_kv_heads], contiguous; kv_bits 8 only */
+  float* k_scales; /* fp32 [n_pages][n_kv_heads], contiguous; kv_bits 8 and 4 */
   float* v_scales;
   int64_t n_pages; /* 1 .. 2^31 - 1 */
   int64_t k_stride_page, k_stride_head, k_stride_token; /* elements */
@@ -420,7 +424,9 @@ typedef struct clo_paged_cache {
   int32_t n_kv_heads;
   int32_t head_dim;  /* 64 or 128 */
   int32_t page_size; /* tokens: 16, 32, 64 or 128 */
-  int32_t kv_bits;   /* 16 or 8 */
+  int32_t kv_bits;   /* 16, 8 or 4 */
+  void* k_group_scales; /* e4m3 [n_pages][n_kv_heads][page_size][head_dim / 16], contiguous; kv_bits 4 only */
+  void* v_group_scales;
 } clo_paged_cache;
 
 /* A ragged batch: sequence b has kv_lens[b] tokens in the cache, the call's own included, and its
@@ -448,6 +454,10 @@ typedef struct clo_paged_batch {
  * max |x| <= 448 * 2^e over the finite new values of the page and head; a page that holds earlier
  * tokens gets the larger of this and its scale, and where that grows the earlier tokens' codes are
  * rescaled (exact unless they fall below 2^-6 * scale).  Infinities become +-448 * scale, NaN stays.
+ * kv_bits 4: the page's scale likewise, with max |x| <= 2688 * 2^e (6 * 448), where it grows the earlier tokens' group scales are rescaled (exact
+ * unless they fall below 2^-6). A group's scale is the nearest e4m3 value to max |x| / (6 * 2^e) over its 16 elements, a code the
+ * nearest to x / (group scale * 2^e), both with ties to even and of the exactly rotated x. A group with an infinity gets the
+ * largest scale (448), where infinities are +-6; one with a NaN is NaN.
  * A call may write a page for one sequence and at one place of its table only.  Rows on 16-byte boundaries, strides multiples of 8
  * elements, rot_dim a multiple of 16.
  * Errors: CLO_ERR_INVALID, CLO_ERR_CUDA. */
@@ -455,7 +465,7 @@ CLO_API clo_status clo_paged_append(const clo_paged_cache* cache, const clo_page
                                     const int64_t* positions, const clo_rows* k, const clo_rows* v, const clo_rows* q,
                                     const clo_rows* q_out, int32_t n_q_heads, void* stream);
 
-/* Read back: the batch's rows as bf16 (code * scale, rounded once) into k_out and v_out
+/* Read back: the batch's rows as bf16 (codes times their scales, rounded once) into k_out and v_out
  * [total_q][n_kv_heads][head_dim]; rows as for clo_paged_append.  A whole sequence is read with
  * q_starts = {0, n}, kv_lens = {n}, and goes to the host pool with clo_append_kv(..., src_is_device = 1).
  * Errors: CLO_ERR_INVALID, CLO_ERR_CUDA. */
@@ -465,7 +475,7 @@ CLO_API clo_status clo_paged_read(const clo_paged_cache* cache, const clo_paged_
 /* Attention of the batch's query rows over the cache:
  *   out = sum_j p_j V_j, p = softmax over the visible j of softmax_scale * q . K_j,
  * q and out bf16 [total_q][n_q_heads][head_dim]; scores, maxima and sums in fp32, weights rounded to
- * the type of the product (bf16 for bf16 pages, fp16 for 8-bit pages), out rounded once.
+ * the type of the product (bf16 for bf16 pages, fp16 for 8-bit and 4-bit pages), out rounded once.
  * Token j is visible to the row at position p iff j <= p, j < kv_lens[b], its page is there, and
  * window == 0 or j > p - window or j < sinks: the last `window` tokens (the row's own included) and
  * the first `sinks`.  Rows that see no token, or whose scores are all -infinity, are zeros; what an
