@@ -252,13 +252,11 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, in
       : "memory");
 }
 
-// Group scales of a page's and head's `slots` slots from `slot` on (both multiples of 16) to shared memory.  Runs of 64 bytes are too
-// short for boxes, which want 128-byte boundaries there.
+// 16 bytes of group scales (a lane's share of a tile's) to shared memory, zeros for a page that is not there.  The scales of 16 tokens are
+// 64 or 128 bytes: copies by the TMA unit, one or two per page, held the unit up more than these do the lanes.
 template <int D>
-__device__ __forceinline__ void copy_groups(uint32_t dst, const PagedParams& p, const PagedSide& sd, int page, int head, int slot, int slots, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(sd.groups + groups_at<D>(p, page, head, slot)),
-               "r"(slots * (D / 16)), "r"(bar)
-               : "memory");
+__device__ __forceinline__ void copy_groups(uint32_t dst, const PagedParams& p, const uint8_t* groups, int page, int head, int slot) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(groups + groups_at<D>(p, max(page, 0), head, slot)), "r"(page >= 0 ? 16 : 0) : "memory");
 }
 
 __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {

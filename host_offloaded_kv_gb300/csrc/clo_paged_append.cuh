@@ -154,14 +154,14 @@ __device__ __forceinline__ Codes4 encode_unit(const float* x, float inv, bool ro
 // The rotated values of a unit from an exact angle, in fp64, rounded to the odd one of the two nearest fp32 numbers: such a value lies on the
 // same side of every border between codes as the exact one, as borders have fewer bits.
 template <int D, bool AXES>
-__device__ __noinline__ void rotate_exactly(const Unit<D>& u, const Place& where, const uint16_t* src, float* x) {
+__device__ __noinline__ void rotate_exactly(const Unit<D>& u, const Place<AXES>& where, const uint16_t* src, float* x) {
   auto odd = [](double v) {
     const float f = __double2float_rz(v);
     return (double)f == v ? f : __uint_as_float(__float_as_uint(f) | 1u);
   };
 #pragma unroll 1
   for (int i = 0; i < 8; ++i) {
-    const int64_t pos = AXES && where.at ? __ldg(where.at + (int64_t)((u.axes >> (8 * i)) & 0xffu) * where.stride) : where.pos;
+    const int64_t pos = where.on(AXES ? u.axes >> (8 * i) & 0xffu : 0);
     const int ip = u.interleaved ? 2 * i : i, iq = u.interleaved ? 2 * i + 1 : 8 + i;  // in the unit
     const double p = bf16_bits_to_f32(src[(ip < 8 ? u.a : u.b - 8) + ip]), q = bf16_bits_to_f32(src[(iq < 8 ? u.a : u.b - 8) + iq]);
     double s, c;
@@ -217,13 +217,7 @@ __device__ __forceinline__ void write_page(const AppendParams& a, const uint64_t
       unpack8(va[i], f[i]);
       unpack8(vb[i], f[i] + 8);
       if (rotate) {
-        const int64_t row = s.first + (pos - s.pos0);
-        Place where{pos, nullptr, 0};
-        if (AXES && a.positions)
-          where = {0, a.positions + row, a.c.total_q};
-        else if (a.positions)
-          where.pos = __ldg(a.positions + row);
-        rotate_unit<D>(u, cos_sin_of<D, AXES>(u, where, 0), f[i]);
+        rotate_unit<D>(u, cos_sin_of<D, AXES>(u, place_of<AXES>(a.positions, s.first + (pos - s.pos0), p.total_q, pos), 0), f[i]);
       }
       if (BITS == 16) {
         char* dst = dst0 + (int64_t)(pos - base) * sd.stride_token * 2;
@@ -304,13 +298,7 @@ __device__ __forceinline__ void write_page(const AppendParams& a, const uint64_t
       if (__any_sync(0xffffffffu, c.near)) {
         if (c.near) {
           const int64_t row = s.first + (pos - s.pos0);
-          Place where{pos, nullptr, 0};
-          if (AXES && a.positions)
-            where = {0, a.positions + row, a.c.total_q};
-          else if (a.positions)
-            where.pos = __ldg(a.positions + row);
-          const uint16_t* src = in.p + row * in.token + (int64_t)head * in.head;
-          rotate_exactly<D, AXES>(u, where, src, x);
+          rotate_exactly<D, AXES>(u, place_of<AXES>(a.positions, row, p.total_q, pos), in.p + row * in.token + (int64_t)head * in.head, x);
         }
         c = encode_unit<D>(x, inv, false, with);
       }
@@ -361,16 +349,12 @@ __global__ void __launch_bounds__(kThreads) k_paged_append(const AppendParams a)
   const int64_t t = job / a.q_chunks;
   if (t >= a.c.total_q) return;
   // the row's sequence is looked up while its elements are on their way
-  auto position = [&](Place* where) {
+  auto position = [&](Place<AXES>* where) {
     const int b = seq_of_row(a.c, (int)t, lane);
     if (b >= a.c.batch) return false;
     const SeqRows s = seq_rows(a.c, b);
     if (t - s.first >= s.n) return false;  // beyond max_q: left out, as its key is
-    *where = {(int64_t)s.pos0 + (t - s.first), nullptr, 0};
-    if (AXES && a.positions)
-      *where = {0, a.positions + t, a.c.total_q};
-    else if (a.positions)
-      where->pos = __ldg(a.positions + t);
+    *where = place_of<AXES>(a.positions, t, a.c.total_q, (int64_t)s.pos0 + (t - s.first));
     return true;
   };
   rotate_heads<D, kIters, AXES>(a.rope, s_turn, a.q, a.q_out, t, position, (int)(job % a.q_chunks) * heads_per_warp<D>(kIters), a.n_q_heads, lane);

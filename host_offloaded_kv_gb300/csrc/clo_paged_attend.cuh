@@ -213,8 +213,8 @@ struct PartRecord {
   int own;   // this block
   int pad[2];
 };
-constexpr int kRecordBytes = 16384;
-constexpr int kMostBlocks = 2 * kSms;
+constexpr int kRecordBytes = 20480;
+constexpr int kMostBlocks = 4 * kSms;
 static_assert(kMostBlocks * sizeof(PartRecord) <= kRecordBytes, "records fit");
 
 inline int64_t part_bytes(int blocks, int rows, int d) { return kRecordBytes + 2 * (int64_t)blocks * rows * (d + 4) * 4; }

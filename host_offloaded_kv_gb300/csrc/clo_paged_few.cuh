@@ -33,7 +33,12 @@ constexpr int kThreads = kWarps * 32;
 // bf16 166 us for 163, one sequence of 524,288 tokens of 8-bit pages 173 us for 165, 64 sequences of 64-element heads 27 us for 22.
 // Three blocks with 8-bit pages: 170 us and more for 165.
 constexpr int kStages = 2;
-constexpr int kWave = 2 * kSms;  // blocks: two to an SM
+
+// Blocks to an SM.
+template <int D, int BITS, int NT>
+constexpr int kPerSm = BITS == 4 && !(D == 128 && NT == 2) ? 3 : 2;
+template <int D, int BITS, int NT>
+constexpr int kWave = kPerSm<D, BITS, NT> * kSms;
 
 // 8-bit pages: weights up to 2^14 (fp16 then holds them down to 2^-38 of the largest) are divided by their page's V scale, which may be as
 // small as 1e-30, before they are summed.  The sums are kept 2^7 smaller, so that two million such weights stay in fp32's range; the
@@ -84,6 +89,15 @@ __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// c / x for positive x, without a branch and into the subnormal numbers: the hardware's reciprocal (off by one unit in the last place) flushes
+// those of x above 2^126.
+__device__ __forceinline__ float reciprocal(float x, float c) {
+  const float k = x >= 0x1p64f ? 0x1p-32f : 1.f;
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * k));
+  return r * (k * c);
 }
 
 // Longest units, in tiles, that are left whole (no shares to find, no join): where there are fewer units than SMs, and where
@@ -168,7 +182,7 @@ __device__ __forceinline__ FewShare few_share(const AttendParams& a, int tokens,
 }
 
 template <int D, int BITS, int NT>
-__global__ void __launch_bounds__(kThreads) k_attend_few(const AttendParams a, const __grid_constant__ PageMaps maps) {
+__global__ void __launch_bounds__(kThreads, kPerSm<D, BITS, NT>) k_attend_few(const AttendParams a, const __grid_constant__ PageMaps maps) {
   using T = Tile<D, BITS>;
   constexpr int TOK = T::kTokens, KM = T::kM, KD = D / 16, ROWS = 8 * NT;
   constexpr float kOff = BITS == 16 ? 0.f : 14.f, kDown = BITS == 16 ? 1.f : kSumDown;
@@ -198,7 +212,7 @@ __global__ void __launch_bounds__(kThreads) k_attend_few(const AttendParams a, c
   }
   __syncthreads();
 
-  const bool by_unit = (int64_t)p.batch * p.n_kv_heads <= kWave;  // where a unit's record stands
+  const bool by_unit = (int64_t)p.batch * p.n_kv_heads <= kWave<D, BITS, NT>;  // where a unit's record stands
   PartRecord* const records = reinterpret_cast<PartRecord*>(a.part);
   if (tid == 0 && a.part && !by_unit) records[blockIdx.x].valid = 0;
   int st = 0;          // next stage, and its barrier's phase
@@ -261,25 +275,32 @@ __global__ void __launch_bounds__(kThreads) k_attend_few(const AttendParams a, c
       int id[KM];
 #pragma unroll
       for (int g = 0; g < KM; ++g) id[g] = __shfl_sync(0xffffffffu, page, g);
+      if constexpr (BITS == 4) {
+        // group scales, 16 bytes a lane: of both sides at once where half the lanes hold a side's
+        constexpr int kLanes = T::kGroupBytes / 16, kLaneTokens = TOK / kLanes;
+        const int l = lane % kLanes, mine = __shfl_sync(0xffffffffu, page, l * kLaneTokens / 16), slot = (first + l * kLaneTokens) & (p.page_size - 1);
+#pragma unroll
+        for (int side = lane / kLanes; side < 2; side += 32 / kLanes)
+          copy_groups<D>(dst + 2 * T::kSideBytes + side * T::kGroupBytes + l * 16, p, side ? p.side[1].groups : p.side[0].groups, mine, kvh, slot);
+      }
       if (elect_one()) {
         s_there[warp][st] = there;
-        mbar_arrive_expect_tx(&s_full[warp][st], 2 * T::kSideBytes + 2 * __popc(there) * (BITS == 4 ? D : 0));
+        mbar_arrive_expect_tx(&s_full[warp][st], 2 * T::kSideBytes);
+        auto fetch = [&](int g, int page) {
+          const int slot = (first + g * 16) & (p.page_size - 1);
 #pragma unroll
-        for (int g = 0; g < KM; ++g)
-          if (g * 16 % box == 0) {
+          for (int side = 0; side < 2; ++side)
 #pragma unroll
-            for (int side = 0; side < 2; ++side)
+            for (int h = 0; h < T::kSpans; ++h)
+              tma_box(dst + side * T::kSideBytes + h * TOK * T::kSpan + g * 16 * T::kSpan, &maps.side[side], h * (T::kSpan * 8 / BITS), slot, kvh, page, bar);
+        };
+        if (BITS == 4 && box == TOK) {
+          fetch(0, id[0]);
+        } else {
 #pragma unroll
-              for (int h = 0; h < T::kSpans; ++h)
-                tma_box(dst + side * T::kSideBytes + h * TOK * T::kSpan + g * 16 * T::kSpan, &maps.side[side], h * (T::kSpan * 8 / BITS),
-                        (first + g * 16) & (p.page_size - 1), kvh, id[g], bar);
-            if constexpr (BITS == 4) {
-#pragma unroll
-              for (int side = 0; side < 2; ++side)  // of a page that is not there: what the stage held, which no row sees
-                if (id[g] >= 0)
-                  copy_groups<D>(dst + 2 * T::kSideBytes + side * T::kGroupBytes + g * 16 * (D / 16), p, p.side[side], id[g], kvh, (first + g * 16) & (p.page_size - 1), box, bar);
-            }
-          }
+          for (int g = 0; g < KM; ++g)
+            if ((g * 16 & (box - 1)) == 0) fetch(g, id[g]);
+        }
       }
       __syncwarp();
       if (BITS != 16) cp_async_commit();
@@ -402,6 +423,13 @@ __global__ void __launch_bounds__(kThreads) k_attend_few(const AttendParams a, c
         __syncwarp();
       }
 
+      float my_ks = 1.f, my_lvs = 0.f, my_inv = 1.f;  // 4-bit pages: a lane per 16 tokens
+      if (BITS == 4) {
+        my_ks = fmaxf(s_scale[warp][st][0][lane & (KM - 1)], kMinScale);
+        const float vs = fmaxf(s_scale[warp][st][1][lane & (KM - 1)], kMinScale);
+        my_lvs = __log2f(vs);
+        my_inv = reciprocal(vs, kDown);
+      }
       float sc[KM][NT][4];
 #pragma unroll
       for (int mt = 0; mt < KM; ++mt) {
@@ -463,14 +491,24 @@ __global__ void __launch_bounds__(kThreads) k_attend_few(const AttendParams a, c
         }
       }
 
-      // Scores in log2 units.  8-bit pages: the page's V scale joins the exponent, so that the weights times the codes keep the
+      // Scores in log2 units.  8-bit and 4-bit pages: the page's V scale joins the exponent, so that the weights times the codes keep the
       // accumulator in range, and leaves the sum by its reciprocal.
+      auto hide = [&](int mt, int nt, int i) {
+        const int j = j0 + mt * 16 + g + (i >> 1) * 8;
+        const int pos = s.pos0 + token_of_row(a, nt * 8 + 2 * t4 + (i & 1));
+        const bool see = (there >> mt & 1u) && j <= pos && j < s.kv_len && (a.window == 0 || j > pos - a.window || j < a.sinks);
+        if (!see) sc[mt][nt][i] = -INFINITY;
+      };
       float inv_vs[KM];
 #pragma unroll
       for (int mt = 0; mt < KM; ++mt) {
         float ks = 1.f, lvs = 0.f;
         inv_vs[mt] = 1.f;
-        if (BITS != 16) {
+        if (BITS == 4) {
+          ks = __shfl_sync(0xffffffffu, my_ks, mt);
+          lvs = __shfl_sync(0xffffffffu, my_lvs, mt);
+          inv_vs[mt] = __shfl_sync(0xffffffffu, my_inv, mt);
+        } else if (BITS != 16) {
           ks = fmaxf(s_scale[warp][st][0][mt], kMinScale);
           const float vs = fmaxf(s_scale[warp][st][1][mt], kMinScale);
           lvs = __log2f(vs);
@@ -482,13 +520,16 @@ __global__ void __launch_bounds__(kThreads) k_attend_few(const AttendParams a, c
           for (int i = 0; i < 4; ++i) {
             const float f = fac[nt][i & 1] * ks;
             sc[mt][nt][i] = BITS != 16 ? fmaf(sc[mt][nt][i], f, lvs) : sc[mt][nt][i] * f;
-            if (!whole) {
-              const int j = j0 + mt * 16 + g + (i >> 1) * 8;
-              const int pos = s.pos0 + token_of_row(a, nt * 8 + 2 * t4 + (i & 1));
-              const bool see = (there >> mt & 1u) && j <= pos && j < s.kv_len && (a.window == 0 || j > pos - a.window || j < a.sinks);
-              if (!see) sc[mt][nt][i] = -INFINITY;
-            }
+            if (BITS != 4 && !whole) hide(mt, nt, i);
           }
+      }
+      if (BITS == 4 && !whole) {  // (in the loop above: a branch for each score)
+#pragma unroll
+        for (int mt = 0; mt < KM; ++mt)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) hide(mt, nt, i);
       }
       uint32_t pf[KM][NT][2];
 #pragma unroll
@@ -702,7 +743,7 @@ __global__ void __launch_bounds__(kThreads) k_attend_few(const AttendParams a, c
 
 // Joins the parts of the units that the cuts met: a block per record and row, D / 4 threads per slice of the parts.
 constexpr int kJoinThreads = 256;
-template <int D, int BITS>
+template <int D, int BITS, int NT>
 __global__ void __launch_bounds__(kJoinThreads) k_attend_join(const AttendParams a) {
   constexpr int kLanes = D / 4, kSlices = kJoinThreads / kLanes;
   __shared__ __align__(16) float s_o[kSlices][D];
@@ -711,7 +752,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_attend_join(const AttendParams
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const PartRecord rec = reinterpret_cast<const PartRecord*>(a.part)[blockIdx.x];
   // by unit: nobody writes the record of a unit without rows
-  const bool by_unit = (int64_t)a.c.batch * a.c.n_kv_heads <= kWave;
+  const bool by_unit = (int64_t)a.c.batch * a.c.n_kv_heads <= kWave<D, BITS, NT>;
   const int b = by_unit ? blockIdx.x / a.c.n_kv_heads : rec.b, kvh = by_unit ? blockIdx.x % a.c.n_kv_heads : rec.kvh;
   if (!by_unit && !rec.valid) return;
   const SeqRows s = seq_rows(a.c, b);
@@ -766,7 +807,7 @@ int64_t few_bytes(const AttendParams& a) {
   int64_t tokens = (int64_t)a.c.max_pages << a.c.page_shift;
   if (a.window > 0) tokens = std::min<int64_t>(tokens, (int64_t)a.window + a.c.max_q + a.sinks + 2 * T::kTokens);
   const int64_t whole = (int64_t)a.c.batch * a.c.n_kv_heads >= kSms ? kWholeMany : kWholeFew;
-  return tokens <= whole * T::kTokens ? 0 : part_bytes(kWave, a.part_rows, D);
+  return tokens <= whole * T::kTokens ? 0 : part_bytes(kWave<D, BITS, NT>, a.part_rows, D);
 }
 
 template <int D, int BITS, int NT>
@@ -784,11 +825,11 @@ cudaError_t few_rows(AttendParams a, int64_t* bytes, cudaStream_t st) {
   static std::atomic<uint64_t> prepared{0};
   cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(f), T::kSmem, &prepared);
   if (e != cudaSuccess) return e;
-  f<<<a.part ? dim3(kWave) : dim3(a.c.batch, a.c.n_kv_heads), kThreads, T::kSmem, st>>>(a, maps);
+  f<<<a.part ? dim3(kWave<D, BITS, NT>) : dim3(a.c.batch, a.c.n_kv_heads), kThreads, T::kSmem, st>>>(a, maps);
   e = cudaGetLastError();
   if (e != cudaSuccess || !a.part) return e;
   const int64_t units = (int64_t)a.c.batch * a.c.n_kv_heads;
-  return launch_after(k_attend_join<D, BITS>, dim3(std::min<int64_t>(units, kWave), a.part_rows), kJoinThreads, st, a);
+  return launch_after(k_attend_join<D, BITS, NT>, dim3(std::min<int64_t>(units, kWave<D, BITS, NT>), a.part_rows), kJoinThreads, st, a);
 }
 
 // Runs the call, or (bytes) says what workspace it takes.

@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
       mbar_init(&sh.tail[i], 1);
     }
     for (int i = 0; i < 12; ++i) {
-      mbar_init(&sh.raw_full[i], 1);
+      mbar_init(&sh.raw_full[i], BITS == 4 ? 1 + 32 : 1);
       mbar_init(&sh.raw_empty[i], 128);
     }
     for (int i = 0; i < 2; ++i) {
@@ -861,27 +861,24 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
           if (use > 0) ok = wait(sh, empty, (use - 1) & 1);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
+          if constexpr (BITS == 4) {
+            // group scales, 16 bytes a lane, which arrives when they have landed
+            constexpr int kLanes = kPartTok * (D / 16) / 16, kLaneTokens = kPartTok / kLanes;
+            const int l = lane % kLanes, page = __shfl_sync(0xffffffffu, page0, 8 * q + h * (kPartTok / 16) + l * kLaneTokens / 16);
+            const int slot = (u.tl.at(u.t_begin + j) * kTok + h * kPartTok + l * kLaneTokens) & (p.page_size - 1);
+            if (lane < kLanes) copy_groups<D>(raw + buf * C::kRawBytes + C::kRawCodes + l * 16, p, side ? p.side[1].groups : p.side[0].groups, page, kvh, slot);
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(full)) : "memory");
+          }
           if (elect_one()) {
             const uint32_t dst = BITS == 16 ? ring + buf * C::kTileBytes : raw + buf * C::kRawBytes, bar = smem_u32(full);
             const int slot0 = u.tl.at(u.t_begin + j) * kTok + h * kPartTok;
-            int groups = 0;  // bytes of group scales that are there; the others are zeros, as codes of a page that is not there
-            if (BITS == 4) {
-#pragma unroll
-              for (int g = 0; g < kPartTok / 16; ++g) {
-                groups += id[g] >= 0 ? D : 0;
-                if (id[g] < 0)
-                  for (int i = 0; i < D; i += 16) *reinterpret_cast<uint4*>(generic + (raw - smem) + buf * C::kRawBytes + C::kRawCodes + g * D + i) = make_uint4(0, 0, 0, 0);
-              }
-            }
-            mbar_arrive_expect_tx(full, BITS == 16 ? C::kTileBytes : C::kRawCodes + groups);
+            mbar_arrive_expect_tx(full, BITS == 16 ? C::kTileBytes : C::kRawCodes);
 #pragma unroll
             for (int g = 0; g < kPartTok / 16; ++g)
-              if (g * 16 % box == 0) {
+              if ((g * 16 & (box - 1)) == 0) {
 #pragma unroll
                 for (int w = 0; w < kBoxSpans; ++w)
                   tma_box(dst + g * 16 * kSpan + w * kTok * kSpan, &maps.side[side], w * (kSpan * 8 / BITS), (slot0 + g * 16) & (p.page_size - 1), kvh, id[g], bar);
-                if (BITS == 4 && id[g] >= 0)
-                  copy_groups<D>(dst + C::kRawCodes + g * 16 * (D / 16), p, p.side[side], id[g], kvh, (slot0 + g * 16) & (p.page_size - 1), box, bar);
               }
           }
           __syncwarp();
@@ -904,6 +901,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
       tiles_done += n;
       return ok;
       });
+      if (BITS == 4) cp_async_wait<0>();
       if (!ok) {  // copies in flight land before the block leaves
         for (int i = 0; i < kBuf; ++i)
           for (int ph = 0; ph < 2; ++ph) mbar_wait_limited(BITS == 16 ? &sh.full[i] : &sh.raw_full[side * kBuf + i], ph);

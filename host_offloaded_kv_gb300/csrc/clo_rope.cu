@@ -40,11 +40,8 @@ __global__ void __launch_bounds__(kThreads, ITERS == kLongIters ? 2 : ITERS == k
   const int64_t job = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
   const int64_t t = job / chunks;
   if (t >= n_tokens) return;
-  auto position = [&](Place* where) {
-    if (AXES)
-      *where = {0, positions + t, n_tokens};
-    else
-      where->pos = positions[t];
+  auto position = [&](Place<AXES>* where) {
+    *where = place_of<AXES>(positions, t, n_tokens, 0);
     return true;
   };
   rotate_heads<D, ITERS, AXES>(r, s_turn, x, y, t, position, (int)(job % chunks) * heads_per_warp<D>(ITERS), n_heads, threadIdx.x & 31);

@@ -50,12 +50,27 @@ __device__ __forceinline__ void stage_turns(const Rope& r, uint64_t* s_turn) {
   __syncthreads();
 }
 
-// Where a row stands: at `pos` on every axis, or (AXES) at at[axis * stride].
+// Where a row stands: at `pos` on every axis, or at at[axis * stride].
+template <bool AXES>
 struct Place {
+  int64_t pos;
+  __device__ __forceinline__ int64_t on(uint64_t) const { return pos; }
+};
+template <>
+struct Place<true> {
   int64_t pos;
   const int64_t* at;
   int64_t stride;
+  __device__ __forceinline__ int64_t on(uint64_t axis) const { return at ? __ldg(at + (int64_t)axis * stride) : pos; }
 };
+// Row `row` of a call's positions (null: it stands at `pos`), `n` rows in all.
+template <bool AXES>
+__device__ __forceinline__ Place<AXES> place_of(const int64_t* positions, int64_t row, int64_t n, int64_t pos) {
+  if constexpr (AXES)
+    return {pos, positions ? positions + row : nullptr, n};
+  else
+    return {positions ? __ldg(positions + row) : pos};
+}
 
 template <int D, bool AXES>
 __device__ __forceinline__ Unit<D> unit_of_lane(const Rope& r, const uint64_t* s_turn, int u) {
@@ -88,14 +103,11 @@ struct CosSin {
 };
 
 template <int D, bool AXES>
-__device__ __forceinline__ CosSin cos_sin_of(const Unit<D>& u, const Place& where, int transpose) {
+__device__ __forceinline__ CosSin cos_sin_of(const Unit<D>& u, const Place<AXES>& where, int transpose) {
   CosSin c;
-  int64_t pos[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) pos[i] = AXES && where.at ? __ldg(where.at + (int64_t)((u.axes >> (8 * i)) & 0xffu) * where.stride) : where.pos;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    c.v[i] = rope_cos_sin(pos[i], u.turn[i], u.magnitude);
+    c.v[i] = rope_cos_sin(where.on(AXES ? u.axes >> (8 * i) & 0xffu : 0), u.turn[i], u.magnitude);
     if (transpose) c.v[i].y = -c.v[i].y;
   }
   return c;
@@ -141,7 +153,7 @@ __device__ __forceinline__ void rotate_heads(const Rope& r, const uint64_t* s_tu
       vb[i] = *reinterpret_cast<const uint4*>(src + (int64_t)h * x.head + u.b);
     }
   }
-  Place where;
+  Place<AXES> where;
   if (!position(&where)) return;
   CosSin c;
   if (u.rotate) c = cos_sin_of<D, AXES>(u, where, r.transpose);
