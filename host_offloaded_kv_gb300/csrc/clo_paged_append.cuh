@@ -5,7 +5,10 @@
 // blocks to an SM: a page's rows stay in them until its scale is known); 64 single tokens, in a graph, 3.8 and 4.5 us.
 #pragma once
 
+#include <type_traits>
+
 #include "clo_rope.cuh"
+#include "clo_rotate_exact.cuh"
 
 namespace clo {
 
@@ -87,62 +90,86 @@ __device__ __forceinline__ Partners<D> partners_of(bool halves, int rot_dim, int
   return w;
 }
 
+constexpr float kRotationError = 3.2e-7f;
+
 // Codes and group scales of a unit's two vectors.
 struct Codes4 {
   uint32_t a, b, scale_a, scale_b;
-  bool near;  // what fp32's rotation left open: a code or a scale lies within its error of a border
+  uint32_t open;  // what fp32's rotation left open, a bit per pair: a code or a scale lies within its error of a border
 };
+
+// x / d for a divisor whose rounded reciprocal r is given: one correction by the exact remainder rounds the quotient correctly
+// (Markstein's method), so that quotients on a border between two codes stay there.
+__device__ __forceinline__ float quotient(float x, float d, float r) {
+  const float t = x * r;
+  return fmaf(fmaf(-t, d, x), r, t);
+}
 
 // e4m3 code of the scale of a group whose largest |x|, over the page's scale, has these bits (infinity: the largest scale; NaN: NaN).
 __device__ __forceinline__ uint32_t group_scale_of(uint32_t bits) {
   if (bits >= 0x7f800000u) return bits == 0x7f800000u ? 0x7eu : 0x7fu;
-  return pack_e4m3(__fdiv_rn(__uint_as_float(bits), 6.f), 0.f);
+  return pack_e4m3(quotient(__uint_as_float(bits), 6.f, 1.f / 6.f), 0.f);
 }
 
-// x: a unit's values; inv: one over the page's scale (a power of two).  All lanes of the warp take part.
-template <int D>
-__device__ __forceinline__ Codes4 encode_unit(const float* x, float inv, bool rotated, const Partners<D>& with) {
-  float y[16], err[8];
-#pragma unroll
-  for (int k = 0; k < 16; ++k) y[k] = x[k] * inv;
-  // |x - exact| <= 2^-21 (|p| + |q|) over the rotated pair p, q: sine and cosine are off by 7.5e-8, three roundings of 2^-24 follow, and the
-  // unrotated pair's |p| + |q| is at most sqrt(2) times the rotated one's.  Twice the pair's larger element is as good a bound and needs no
-  // pairing: here the larger of the unit's whole, which only flags a little more.
-  float top = 0.f;
-#pragma unroll
-  for (int k = 0; k < 16; ++k) top = fmaxf(top, fabsf(y[k]));
-  const float off = rotated && top < INFINITY ? top * 0x1p-20f : 0.f;
-  (void)err;
+// x: a unit's values; inv: one over the page's scale (a power of two); rotated: x carries fp32's errors (ROTATED false: no lane's does).  All
+// lanes of the warp take part.
+template <int D, bool ROTATED>
+__device__ __forceinline__ Codes4 encode_unit(const float* x, float inv, bool rotated, bool interleaved, const Partners<D>& with) {
+  float y[16];
   uint32_t key[2] = {0u, 0u};
 #pragma unroll
-  for (int k = 0; k < 16; ++k) key[k / 8] = max(key[k / 8], __float_as_uint(y[k]) & 0x7fffffffu);
+  for (int k = 0; k < 16; ++k) {
+    y[k] = x[k] * inv;
+    key[k / 8] = max(key[k / 8], __float_as_uint(y[k]) & 0x7fffffffu);
+  }
+  // |x - exact| <= 3.2e-7 (|x| + |y|) over the rotated pair x, y: sine and cosine are off by 7.5e-8 of the unrotated pair's |p| + |q|, which is
+  // at most sqrt(2) times |x| + |y|; the products and the sum round by 2^-24 of |q| and of |x|, the magnitude by 2^-24 of both.
+  float off[8], most = 0.f;
+#pragma unroll
+  for (int i = 0; ROTATED && i < 8; ++i) {
+    const float o = (interleaved ? fabsf(y[2 * i]) + fabsf(y[2 * i + 1]) : fabsf(y[i]) + fabsf(y[8 + i])) * kRotationError;
+    off[i] = rotated && o < INFINITY ? o : 0.f;
+    most = fmaxf(most, off[i]);
+  }
   Codes4 c;
-  c.near = false;
+  c.open = 0;
   uint32_t code[2];
 #pragma unroll
   for (int v = 0; v < 2; ++v) {
     const int from = v ? with.lane_b : with.lane_a;
     const bool second = v ? with.second_b : with.second_a;
     const uint32_t ka = __shfl_sync(0xffffffffu, key[0], from), kb = __shfl_sync(0xffffffffu, key[1], from);
-    const float other_off = __shfl_sync(0xffffffffu, off, from);
+    const float o = ROTATED ? fmaxf(most, __shfl_sync(0xffffffffu, most, from)) : 0.f;
     const uint32_t all = max(key[v], second ? kb : ka);
-    const uint32_t scale = group_scale_of(all);
-    if (rotated && all < 0x7f800000u) {
-      const float m = __uint_as_float(all), o = fmaxf(off, other_off);
-      c.near |= group_scale_of(__float_as_uint(m + o)) != scale || group_scale_of(__float_as_uint(fmaxf(m - o, 0.f))) != scale;
+    const float m = __uint_as_float(all);
+    const uint32_t scale = group_scale_of(o > 0.f ? __float_as_uint(m + o) : all);
+    if (o > 0.f && all < 0x7f800000u && group_scale_of(__float_as_uint(fmaxf(m - o, 0.f))) != scale) c.open = 0xffu;
+    const float s = e4m3_to_f32x2(scale).x;
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+    r = s > 0.f ? r : 0.f;
+    if (all >= 0x7f800000u) {  // infinities: +-6 times the largest scale
+#pragma unroll
+      for (int k = 0; k < 8; ++k) y[8 * v + k] = fminf(fmaxf(y[8 * v + k], -1e30f), 1e30f);
     }
-    // x / scale, rounded once: a product with the rounded reciprocal and one correction by the exact remainder
-    const float s = e4m3_to_f32x2(scale).x, r = s > 0.f ? 1.f / s : 0.f;
-    float q[8], lo[8], hi[8];
+    float lo[8], hi[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const float z = y[8 * v + k], t = z * r;
-      q[k] = fabsf(t) < INFINITY ? fmaf(fmaf(-t, s, z), r, t) : t;
-      lo[k] = q[k] - off * r;
-      hi[k] = q[k] + off * r;
+      lo[k] = quotient(y[8 * v + k], s, r);
+      if (ROTATED) {
+        const float e = (interleaved ? off[4 * v + k / 2] : off[k]) * r;
+        hi[k] = lo[k] + e;
+        lo[k] -= e;
+      }
     }
-    code[v] = pack8_e2m1(q);
-    if (rotated) c.near |= pack8_e2m1(lo) != code[v] || pack8_e2m1(hi) != code[v];
+    code[v] = pack8_e2m1(lo);
+    // a nibble for each element; halves: element k of either vector is of pair k; neighbours: elements 2 i, 2 i + 1 of vector v of pair 4 v + i
+    uint32_t d = ROTATED ? code[v] ^ pack8_e2m1(hi) : 0u;
+    if (d != 0 && s > 0.f && rotated) {  // (zeros differ in sign)
+      d = (d | d >> 1 | d >> 2 | d >> 3) & 0x11111111u;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) c.open |= (d >> (4 * k) & 1u) << (interleaved ? 4 * v + k / 2 : k);
+    }
     if (v) c.scale_b = scale;
     else c.scale_a = scale;
   }
@@ -151,24 +178,11 @@ __device__ __forceinline__ Codes4 encode_unit(const float* x, float inv, bool ro
   return c;
 }
 
-// The rotated values of a unit from an exact angle, in fp64, rounded to the odd one of the two nearest fp32 numbers: such a value lies on the
-// same side of every border between codes as the exact one, as borders have fewer bits.
-template <int D, bool AXES>
-__device__ __noinline__ void rotate_exactly(const Unit<D>& u, const Place<AXES>& where, const uint16_t* src, float* x) {
-  auto odd = [](double v) {
-    const float f = __double2float_rz(v);
-    return (double)f == v ? f : __uint_as_float(__float_as_uint(f) | 1u);
-  };
-#pragma unroll 1
-  for (int i = 0; i < 8; ++i) {
-    const int64_t pos = where.on(AXES ? u.axes >> (8 * i) & 0xffu : 0);
-    const int ip = u.interleaved ? 2 * i : i, iq = u.interleaved ? 2 * i + 1 : 8 + i;  // in the unit
-    const double p = bf16_bits_to_f32(src[(ip < 8 ? u.a : u.b - 8) + ip]), q = bf16_bits_to_f32(src[(iq < 8 ? u.a : u.b - 8) + iq]);
-    double s, c;
-    sincospi((double)(int64_t)((uint64_t)pos * u.turn[i]) * 0x1p-63, &s, &c);
-    x[ip] = odd((p * c - q * s) * (double)u.magnitude);
-    x[iq] = odd((q * c + p * s) * (double)u.magnitude);
-  }
+// One pair in integers (clo_rotate_exact.cuh), out of line.
+__device__ __noinline__ float2 rotate_exactly(uint32_t p, uint32_t q, uint64_t angle, float magnitude) {
+  float2 r;
+  rotate_exact((uint16_t)p, (uint16_t)q, angle, magnitude, &r.x, &r.y);
+  return r;
 }
 
 // One job: (touched page, kv head, K or V), by kPer warps.  A lane holds kUnits units (16 elements of a row each) in registers from
@@ -217,7 +231,7 @@ __device__ __forceinline__ void write_page(const AppendParams& a, const uint64_t
       unpack8(va[i], f[i]);
       unpack8(vb[i], f[i] + 8);
       if (rotate) {
-        rotate_unit<D>(u, cos_sin_of<D, AXES>(u, place_of<AXES>(a.positions, s.first + (pos - s.pos0), p.total_q, pos), 0), f[i]);
+        rotate_unit<D>(u, cos_sin_of<D, AXES>(u, place_of<AXES>(a.rope, a.positions, s.first + (pos - s.pos0), p.total_q, pos), 0), f[i]);
       }
       if (BITS == 16) {
         char* dst = dst0 + (int64_t)(pos - base) * sd.stride_token * 2;
@@ -280,38 +294,63 @@ __device__ __forceinline__ void write_page(const AppendParams& a, const uint64_t
   if constexpr (BITS == 4) {
     const Partners<D> with = partners_of<D>(rotate && !u.interleaved, a.rope.plan.rot_dim, lane);
     uint8_t* const groups = sd.groups + groups_at<D>(p, page, head, 0);
+    // One copy of the code for all units: several did not fit the instruction cache (11,000 tokens with queries 144 us for 96).
+    auto encode_rows = [&](auto turned) {
+      constexpr bool kTurned = decltype(turned)::value;
 #pragma unroll 1
-    for (int i = 0; i < kUnits && lo + part * kRows + i * kPer * kRows < hi; ++i) {
-      const int pos = first + i * kPer * kRows;
-      float x[16];
+      for (int i = 0; i < kUnits && lo + part * kRows + i * kPer * kRows < hi; ++i) {
+        const int pos = first + i * kPer * kRows;
+        float x[16];
 #pragma unroll
-      for (int n = 0; n < kUnits; ++n)
-        if (n == i) {
+        for (int k = 0; k < 16; ++k) {
+          x[k] = f[0][k];
 #pragma unroll
-          for (int k = 0; k < 16; ++k) x[k] = f[n][k];
+          for (int n = 1; n < kUnits; ++n) x[k] = i == n ? f[n][k] : x[k];
+          x[k] = pos < hi ? x[k] : 0.f;
         }
-      if (pos >= hi) {
-#pragma unroll
-        for (int k = 0; k < 16; ++k) x[k] = 0.f;
-      }
-      Codes4 c = encode_unit<D>(x, inv, rotate && pos < hi, with);
-      if (__any_sync(0xffffffffu, c.near)) {
-        if (c.near) {
+        Codes4 c;
+#pragma unroll 1
+        for (bool again = false;; again = true) {
+          c = encode_unit<D, kTurned>(x, inv, rotate && !again, u.interleaved, with);
+          if (!kTurned || again || !__any_sync(0xffffffffu, c.open != 0)) break;
+          // what fp32 left open: those pairs once more, exactly
           const int64_t row = s.first + (pos - s.pos0);
-          rotate_exactly<D, AXES>(u, place_of<AXES>(a.positions, row, p.total_q, pos), in.p + row * in.token + (int64_t)head * in.head, x);
+          const uint16_t* src = in.p + row * in.token + (int64_t)head * in.head;
+#pragma unroll 1
+          for (; c.open; c.open &= c.open - 1) {
+            const int n = __ffs(c.open) - 1, unit = lane % kLanes;
+            const int ep = u.interleaved ? u.a + 2 * n : u.a + n, eq = u.interleaved ? ep + 1 : u.b + n;
+            const uint64_t axis = AXES ? s_turn[CLO_ROPE_MAX_PAIRS + unit] >> (8 * n) & 0xffu : 0;
+            const int64_t at = a.positions ? __ldg(a.positions + axis * p.total_q + row) : pos;
+            const float2 y = rotate_exactly(src[ep], src[eq], (uint64_t)at * s_turn[unit * 8 + n], u.magnitude);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              if (k != n) continue;
+              if (u.interleaved) {
+                x[2 * k] = y.x;
+                x[2 * k + 1] = y.y;
+              } else {
+                x[k] = y.x;
+                x[8 + k] = y.y;
+              }
+            }
+          }
         }
-        c = encode_unit<D>(x, inv, false, with);
+        if (pos < hi) {
+          char* dst = dst0 + (int64_t)(pos - base) * sd.stride_token / 2;
+          *reinterpret_cast<uint32_t*>(dst + u.a / 2) = c.a;
+          *reinterpret_cast<uint32_t*>(dst + u.b / 2) = c.b;
+          // the vector with the group's first elements writes its scale
+          uint8_t* const g = groups + (pos - base) * (D / 16);
+          if (u.a % 16 == 0) g[u.a / 16] = (uint8_t)c.scale_a;
+          if (u.b % 16 == 0) g[u.b / 16] = (uint8_t)c.scale_b;
+        }
       }
-      if (pos < hi) {
-        char* dst = dst0 + (int64_t)(pos - base) * sd.stride_token / 2;
-        *reinterpret_cast<uint32_t*>(dst + u.a / 2) = c.a;
-        *reinterpret_cast<uint32_t*>(dst + u.b / 2) = c.b;
-        // the vector with the group's first elements writes its scale
-        uint8_t* const g = groups + (pos - base) * (D / 16);
-        if (u.a % 16 == 0) g[u.a / 16] = (uint8_t)c.scale_a;
-        if (u.b % 16 == 0) g[u.b / 16] = (uint8_t)c.scale_b;
-      }
-    }
+    };
+    if (side == 0 && a.rope.plan.rot_dim > 0)
+      encode_rows(std::true_type{});
+    else
+      encode_rows(std::false_type{});
   }
 #pragma unroll
   for (int i = 0; BITS == 8 && i < kUnits; ++i) {
@@ -331,7 +370,7 @@ __device__ __forceinline__ void write_page(const AppendParams& a, const uint64_t
 }
 
 template <int D, int BITS, int kPer, bool AXES>
-__global__ void __launch_bounds__(kThreads) k_paged_append(const AppendParams a) {
+__global__ void __launch_bounds__(kThreads, BITS == 4 || AXES ? 2 : 1) k_paged_append(const AppendParams a) {
   __shared__ __align__(16) uint64_t s_turn[kTurns<AXES>];
   __shared__ float s_red[kWarps];
   stage_turns<AXES>(a.rope, s_turn);
@@ -354,7 +393,7 @@ __global__ void __launch_bounds__(kThreads) k_paged_append(const AppendParams a)
     if (b >= a.c.batch) return false;
     const SeqRows s = seq_rows(a.c, b);
     if (t - s.first >= s.n) return false;  // beyond max_q: left out, as its key is
-    *where = place_of<AXES>(a.positions, t, a.c.total_q, (int64_t)s.pos0 + (t - s.first));
+    *where = place_of<AXES>(a.rope, a.positions, t, a.c.total_q, (int64_t)s.pos0 + (t - s.first));
     return true;
   };
   rotate_heads<D, kIters, AXES>(a.rope, s_turn, a.q, a.q_out, t, position, (int)(job % a.q_chunks) * heads_per_warp<D>(kIters), a.n_q_heads, lane);

@@ -41,7 +41,7 @@ __global__ void __launch_bounds__(kThreads, ITERS == kLongIters ? 2 : ITERS == k
   const int64_t t = job / chunks;
   if (t >= n_tokens) return;
   auto position = [&](Place<AXES>* where) {
-    *where = place_of<AXES>(positions, t, n_tokens, 0);
+    *where = place_of<AXES>(r, positions, t, n_tokens, 0);
     return true;
   };
   rotate_heads<D, ITERS, AXES>(r, s_turn, x, y, t, position, (int)(job % chunks) * heads_per_warp<D>(ITERS), n_heads, threadIdx.x & 31);
@@ -107,13 +107,9 @@ __global__ void __launch_bounds__(kThreads) k_paged_read(const ReadParams a) {
       w[i] = make_uint4(0, 0, 0, 0);
       scale[i] = 1.f;
       if (v < 2 * n && page >= 0) {
-        const char* src = sd.pages + ((int64_t)page * sd.stride_page + (int64_t)h * sd.stride_head + (int64_t)slot * sd.stride_token + e) * BITS / 8;
+        const char* src = sd.pages + ((int64_t)page * sd.stride_page + (int64_t)h * sd.stride_head + (int64_t)slot * sd.stride_token + e) * (BITS / 8);
         if (BITS == 16) {
           w[i] = __ldg(reinterpret_cast<const uint4*>(src));
-        } else if (BITS == 4) {
-          w[i].x = __ldg(reinterpret_cast<const uint32_t*>(src));
-          w[i].y = __ldg(sd.groups + groups_at<D>(p, page, h, slot) + e / 16);
-          scale[i] = __ldg(sd.scales + (int64_t)page * p.n_kv_heads + h);
         } else {
           const uint2 c = __ldg(reinterpret_cast<const uint2*>(src));
           w[i].x = c.x;
@@ -139,21 +135,69 @@ __global__ void __launch_bounds__(kThreads) k_paged_read(const ReadParams a) {
           x[2 * k + 1] = d.y * f;
         }
         w[i] = pack8(x);
-      } else if (BITS == 4) {
-        // the group's scale first: the product of two fp32 numbers of a few bits is exact, and so is that with a power of two
-        const float f = e4m3_to_f32x2(w[i].y).x * fmaxf(scale[i], kMinScale);
-        uint32_t half[4];
-        e2m1_to_f16x8(w[i].x, half);
-        float x[8];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 d = __half22float2(*reinterpret_cast<const __half2*>(&half[k]));
-          x[2 * k] = d.x * f;
-          x[2 * k + 1] = d.y * f;
-        }
-        w[i] = pack8(x);
       }
       *reinterpret_cast<uint4*>(out.p + t * out.token + (int64_t)h * out.head + e) = w[i];
+    }
+  }
+}
+
+// 4-bit pages: a group of 16 elements per lane and step.
+template <int D>
+__global__ void __launch_bounds__(kThreads) k_paged_read4(const ReadParams a) {
+  const PagedParams& p = a.c;
+  const int lane = threadIdx.x & 31;
+  const int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (t >= p.total_q) return;
+  const int b = seq_of_row(p, (int)t, lane);
+  if (b >= p.batch) return;
+  const SeqRows s = seq_rows(p, b);
+  if (t - s.first >= s.n) return;
+  const int64_t pos = (int64_t)s.pos0 + (t - s.first);
+  const int page = pos < 0 || pos >= kMaxPagedTokens ? -1 : page_of(p, b, (int)(pos >> p.page_shift));
+  const int slot = (int)(pos & (p.page_size - 1));
+  constexpr int kGroups = D / 16, kBatch = 4;
+  const int n = p.n_kv_heads * kGroups;
+#pragma unroll
+  for (int side = 0; side < 2; ++side) {
+    const PagedSide& sd = p.side[side];
+    const Rows& out = a.out[side];
+    for (int v0 = lane; v0 < n; v0 += 32 * kBatch) {
+      uint2 w[kBatch];
+      uint32_t group[kBatch];
+      float scale[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int v = v0 + 32 * i, h = v / kGroups, g = v % kGroups;
+        w[i] = make_uint2(0u, 0u);
+        group[i] = 0u;
+        scale[i] = 1.f;
+        if (v < n && page >= 0) {
+          w[i] = __ldg(reinterpret_cast<const uint2*>(sd.pages + ((int64_t)page * sd.stride_page + (int64_t)h * sd.stride_head + (int64_t)slot * sd.stride_token + g * 16) / 2));
+          group[i] = __ldg(sd.groups + groups_at<D>(p, page, h, slot) + g);
+          scale[i] = __ldg(sd.scales + (int64_t)page * p.n_kv_heads + h);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int v = v0 + 32 * i, h = v / kGroups, g = v % kGroups;
+        if (v >= n) break;
+        // the product of two numbers of a few bits and a power of two is exact
+        const float f = e4m3_to_f32x2(group[i]).x * fmaxf(scale[i], kMinScale);
+        uint16_t* dst = out.p + t * out.token + (int64_t)h * out.head + g * 16;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t c[4];
+          e2m1_to_f16x8(half ? w[i].y : w[i].x, c);
+          float x[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 d = __half22float2(*reinterpret_cast<const __half2*>(&c[k]));
+            x[2 * k] = d.x * f;
+            x[2 * k + 1] = d.y * f;
+          }
+          *reinterpret_cast<uint4*>(dst + 8 * half) = pack8(x);
+        }
+      }
     }
   }
 }
@@ -354,11 +398,11 @@ extern "C" CLO_API clo_status clo_paged_read(const clo_paged_cache* cache, const
   if (cache->head_dim == 128) {
     if (cache->kv_bits == 16) k_paged_read<128, 16><<<blocks, kThreads, 0, st>>>(a);
     else if (cache->kv_bits == 8) k_paged_read<128, 8><<<blocks, kThreads, 0, st>>>(a);
-    else k_paged_read<128, 4><<<blocks, kThreads, 0, st>>>(a);
+    else k_paged_read4<128><<<blocks, kThreads, 0, st>>>(a);
   } else {
     if (cache->kv_bits == 16) k_paged_read<64, 16><<<blocks, kThreads, 0, st>>>(a);
     else if (cache->kv_bits == 8) k_paged_read<64, 8><<<blocks, kThreads, 0, st>>>(a);
-    else k_paged_read<64, 4><<<blocks, kThreads, 0, st>>>(a);
+    else k_paged_read4<64><<<blocks, kThreads, 0, st>>>(a);
   }
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return paged_fail(CLO_ERR_CUDA, "%s: launch: %s", who, cudaGetErrorString(e));

@@ -50,26 +50,31 @@ __device__ __forceinline__ void stage_turns(const Rope& r, uint64_t* s_turn) {
   __syncthreads();
 }
 
-// Where a row stands: at `pos` on every axis, or at at[axis * stride].
+// Where a row stands, on every axis alike or on each.
 template <bool AXES>
 struct Place {
   int64_t pos;
-  __device__ __forceinline__ int64_t on(uint64_t) const { return pos; }
+  __device__ __forceinline__ int64_t on(uint32_t) const { return pos; }
 };
 template <>
 struct Place<true> {
-  int64_t pos;
-  const int64_t* at;
-  int64_t stride;
-  __device__ __forceinline__ int64_t on(uint64_t axis) const { return at ? __ldg(at + (int64_t)axis * stride) : pos; }
+  int64_t pos[CLO_ROPE_MAX_AXES];
+  __device__ __forceinline__ int64_t on(uint32_t axis) const {
+    const int64_t lo = axis & 1 ? pos[1] : pos[0], hi = axis & 1 ? pos[3] : pos[2];
+    return axis & 2 ? hi : lo;
+  }
 };
 // Row `row` of a call's positions (null: it stands at `pos`), `n` rows in all.
 template <bool AXES>
-__device__ __forceinline__ Place<AXES> place_of(const int64_t* positions, int64_t row, int64_t n, int64_t pos) {
-  if constexpr (AXES)
-    return {pos, positions ? positions + row : nullptr, n};
-  else
-    return {positions ? __ldg(positions + row) : pos};
+__device__ __forceinline__ Place<AXES> place_of(const Rope& r, const int64_t* positions, int64_t row, int64_t n, int64_t pos) {
+  Place<AXES> w;
+  if constexpr (AXES) {
+#pragma unroll
+    for (int a = 0; a < CLO_ROPE_MAX_AXES; ++a) w.pos[a] = positions && a < r.plan.n_axes ? __ldg(positions + a * n + row) : pos;
+  } else {
+    w.pos = positions ? __ldg(positions + row) : pos;
+  }
+  return w;
 }
 
 template <int D, bool AXES>
@@ -107,7 +112,7 @@ __device__ __forceinline__ CosSin cos_sin_of(const Unit<D>& u, const Place<AXES>
   CosSin c;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    c.v[i] = rope_cos_sin(where.on(AXES ? u.axes >> (8 * i) & 0xffu : 0), u.turn[i], u.magnitude);
+    c.v[i] = rope_cos_sin(where.on(AXES ? (uint32_t)(u.axes >> (8 * i)) : 0u), u.turn[i], u.magnitude);
     if (transpose) c.v[i].y = -c.v[i].y;
   }
   return c;

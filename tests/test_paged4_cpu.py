@@ -1,5 +1,6 @@
 """4-bit pages without a GPU: refusals of the C calls and of the binding, the reference's rounding."""
 import ctypes
+import os
 import random
 import re
 import subprocess
@@ -92,6 +93,49 @@ def test_reference_rounding():
     assert torch.equal(ref4.codes_of(ref4.bytes_of(-ref4.LEVELS)), -ref4.LEVELS)
     for a, e in ((0.0, -64), (2688.0, 0), (2688.0001, 1), (1.0, -11), (2.0 ** -100, -64), (5.25, -9)):
         assert ref4.needed_scale(a) == 2.0 ** e
+
+
+def test_pairs_are_rotated_in_integers_to_2_to_the_minus_48(tmp_path):
+    # against 64-bit-mantissa arithmetic: angles of every size, exponents 50 apart, zeros, magnitudes; rounded to the odd neighbour
+    from host_offloaded_kv_gb300 import _build
+
+    src = tmp_path / "exact.cu"
+    src.write_text(r'''
+#include <cstdio>
+#include <random>
+#include "clo_rotate_exact.cuh"
+using namespace clo;
+static float of(uint16_t x) { const uint32_t b = (uint32_t)x << 16; float f; memcpy(&f, &b, 4); return f; }
+int main() {
+  std::mt19937_64 g(1);
+  const long double turn = 6.283185307179586476925286766559005768L / 18446744073709551616.0L;
+  long bad = 0, even = 0;
+  for (int i = 0; i < 1000000; ++i) {
+    uint64_t a = g();
+    if (i % 5 == 0) a >>= g() % 60;
+    if (i % 7 == 0) a = (a & 3) << 62;
+    uint16_t p = (g() & 0x807f) | (100 + g() % 50) << 7, q = (g() & 0x807f) | (100 + g() % 50) << 7;
+    if (i % 11 == 0) p = 0;
+    if (i % 13 == 0) q &= 0x8000;
+    const float m = i % 3 == 0 ? 1.f : 1.f + (g() % 1000) / 777.f;
+    float x[2];
+    rotate_exact(p, q, a, m, &x[0], &x[1]);
+    const long double s = sinl((int64_t)a * turn), c = cosl((int64_t)a * turn), P = of(p), Q = of(q);
+    const long double want[2] = {(P * c - Q * s) * m, (Q * c + P * s) * m}, slack = ldexpl(fmaxl(fabsl(P), fabsl(Q)) * m, -48);
+    for (int k = 0; k < 2; ++k) {
+      bad += !(want[k] >= nextafterf(x[k], -INFINITY) - slack && want[k] <= nextafterf(x[k], INFINITY) + slack);
+      uint32_t b;
+      memcpy(&b, &x[k], 4);
+      even += !(b & 1) && fabsl(want[k] - x[k]) > slack;
+    }
+  }
+  printf("%ld %ld\n", bad, even);
+}
+''')
+    exe = str(src)[:-3]
+    subprocess.run([_build._nvcc(), "-std=c++17", "-gencode", "arch=compute_103a,code=sm_103a", "-I", os.path.join(base.ROOT, "host_offloaded_kv_gb300", "csrc"),
+                    str(src), "-o", exe], check=True)
+    assert subprocess.run([exe], capture_output=True, text=True, check=True).stdout.split() == ["0", "0"]
 
 
 SHAPES = [(d, 4, tiles) for d in (64, 128) for tiles in (1, 2)]
