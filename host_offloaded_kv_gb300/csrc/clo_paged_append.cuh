@@ -370,7 +370,7 @@ __device__ __forceinline__ void write_page(const AppendParams& a, const uint64_t
 }
 
 template <int D, int BITS, int kPer, bool AXES>
-__global__ void __launch_bounds__(kThreads, BITS == 4 || AXES ? 2 : 1) k_paged_append(const AppendParams a) {
+__global__ void __launch_bounds__(kThreads, 2) k_paged_append(const AppendParams a) {
   __shared__ __align__(16) uint64_t s_turn[kTurns<AXES>];
   __shared__ float s_red[kWarps];
   stage_turns<AXES>(a.rope, s_turn);

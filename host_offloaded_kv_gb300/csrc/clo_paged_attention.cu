@@ -90,7 +90,7 @@ static const char* attend_params(const clo_paged_cache* cache, const clo_paged_b
 
 // Up to this many rows per kv head go to the decode kernel, more to the tcgen05 kernel.  (32 rows there, four fragments wide:
 // 193 us for 132 at 16 sequences of 8 tokens by 4 heads over 8000 to 16,000 tokens of bf16, 178 for 123 with 8-bit pages.)
-constexpr int kFewRows = 16;
+constexpr int few_rows_of(const clo_paged_cache* c) { return c->kv_bits == 4 && c->head_dim == 64 ? 24 : 16; }
 
 extern "C" CLO_API clo_status clo_paged_attention_workspace(const clo_paged_cache* cache, const clo_paged_batch* batch, int32_t n_q_heads,
                                                             int32_t window, int32_t sinks, int64_t* bytes) {
@@ -100,7 +100,7 @@ extern "C" CLO_API clo_status clo_paged_attention_workspace(const clo_paged_cach
   *bytes = 0;
   if (const char* f = attend_params(cache, batch, n_q_heads, window, sinks, &a)) return paged_fail(CLO_ERR_INVALID, "%s: %s", who, f);
   if (a.c.batch == 0 || a.c.total_q == 0 || a.c.max_q == 0) return CLO_OK;
-  if (a.part_rows > kFewRows)
+  if (a.part_rows > few_rows_of(cache))
     *bytes = attend_many_bytes(a, cache->head_dim);
   else
     *bytes = (cache->kv_bits == 16 ? attend_few_bf16_bytes : cache->kv_bits == 8 ? attend_few_e4m3_bytes : attend_few_e2m1_bytes)(a, cache->head_dim);
@@ -134,7 +134,7 @@ extern "C" CLO_API clo_status clo_paged_attention(const clo_paged_cache* cache, 
   a.part_bytes = workspace ? workspace_bytes : 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if (a.part_rows > kFewRows)
+  if (a.part_rows > few_rows_of(cache))
     e = launch_attend_many(a, cache->head_dim, cache->kv_bits, st);
   else
     e = (cache->kv_bits == 16 ? launch_attend_few_bf16 : cache->kv_bits == 8 ? launch_attend_few_e4m3 : launch_attend_few_e2m1)(a, cache->head_dim, st);

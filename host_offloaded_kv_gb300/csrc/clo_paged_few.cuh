@@ -36,7 +36,7 @@ constexpr int kStages = 2;
 
 // Blocks to an SM.
 template <int D, int BITS, int NT>
-constexpr int kPerSm = BITS == 4 && !(D == 128 && NT == 2) ? 3 : 2;
+constexpr int kPerSm = BITS == 4 && !(D == 128 && NT == 2) && NT < 3 ? 3 : 2;
 template <int D, int BITS, int NT>
 constexpr int kWave = kPerSm<D, BITS, NT> * kSms;
 
@@ -836,6 +836,9 @@ cudaError_t few_rows(AttendParams a, int64_t* bytes, cudaStream_t st) {
 template <int BITS>
 cudaError_t few(const AttendParams& a, int head_dim, int64_t* bytes, cudaStream_t st) {
   if (head_dim == 128) return a.part_rows <= 8 ? few_rows<128, BITS, 1>(a, bytes, st) : few_rows<128, BITS, 2>(a, bytes, st);
+  if constexpr (BITS == 4) {
+    if (a.part_rows > 16) return few_rows<64, BITS, 3>(a, bytes, st);
+  }
   return a.part_rows <= 8 ? few_rows<64, BITS, 1>(a, bytes, st) : few_rows<64, BITS, 2>(a, bytes, st);
 }
 
