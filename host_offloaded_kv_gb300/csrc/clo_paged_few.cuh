@@ -103,11 +103,19 @@ __device__ __forceinline__ float reciprocal(float x, float c) {
 // Longest units, in tiles, that are left whole (no shares to find, no join): where there are fewer units than SMs, and where
 // there are more.  Measured, whole against cut, us: 64 units of up to 12 tiles 6.5 / 11.8, 8 of 32 tiles 12.6 / 7.6; 256 units of
 // 10 to 19 tiles 8.3 / 14.2, of 63 to 125 tiles 36.6 / 40.6, of 32 to 500 tiles 103 / 94 (8-bit pages, 16 to 250 tiles: 80 / 59).
-constexpr int kWholeFew = 24, kWholeMany = 128;
+// 4-bit pages, whose tiles hold 64 tokens and take longer, whole / cut: 8 sequences of 600 tokens, 8 heads 10.5 / 12.4, one of 2000 - / 12.4; 32 of
+// 2500 30.9 / 37.5, 32 to 8000 72.6 / 49.6, 61 windows of 4096 80.4 / 74.1.
+template <int BITS>
+constexpr int kWholeFew = BITS == 4 ? 12 : 24;
+template <int BITS>
+constexpr int kWholeMany = BITS == 4 ? 48 : 128;
 // What a unit costs beside its tiles, in tiles, and the least share of a block.  Cost 4 / 14 / 20, us: 61 windows of 4096 tokens of
 // 8-bit pages 96.0 / 87.8 / 87.5, 32 sequences to 8000 tokens 59.5 / 53.8 / 54.0 (bf16: 94.2 / 91.1 / 91.3).
 // Share 14 / 8 / 5, us: one sequence of 512 tokens 8.8 / 7.6 / 7.4, of 2000 9.3 / 8.6 / 9.0, of 8000 of 8-bit pages 12.4 / 11.2 / 11.1.
-constexpr int kFewCost = 14, kFewShare = 8;
+// 4-bit pages, share 8 / 4: one sequence of 8000 tokens 14.5 / 13.3; the cost makes no difference there (4, 8, 14, 22: 80.6 to 81.1 for the windows).
+constexpr int kFewCost = 14;
+template <int BITS>
+constexpr int kFewShare = BITS == 4 ? 4 : 8;
 
 // A block's share, and the unit that it begins in.
 struct FewShare {
@@ -117,6 +125,7 @@ struct FewShare {
 };
 
 // By every warp of the block.  Lanes take four sequences each.
+template <int BITS>
 __device__ __forceinline__ FewShare few_share(const AttendParams& a, int tokens, int lane) {
   const PagedParams& p = a.c;
   constexpr int kPer = 4;
@@ -144,7 +153,7 @@ __device__ __forceinline__ FewShare few_share(const AttendParams& a, int tokens,
     total += warp_sum64(mine);
   }
   total *= p.n_kv_heads;
-  const int64_t share = max((total + gridDim.x - 1) / gridDim.x, (int64_t)kFewShare);
+  const int64_t share = max((total + gridDim.x - 1) / gridDim.x, (int64_t)kFewShare<BITS>);
   f.first = min(total, share * blockIdx.x);
   f.last = min(total, f.first + share);
   if (f.first >= f.last) return f;
@@ -200,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm<D, BITS, NT>) k_attend_few(co
   const uint32_t ring = smem + warp * kStages * T::kStage;
   uint8_t* const generic = smem_raw + (smem - smem_u32(smem_raw));
   FewShare share{0, 1, 0, (int)blockIdx.x, (int)blockIdx.y};
-  if (a.part) share = few_share(a, TOK, lane);
+  if (a.part) share = few_share<BITS>(a, TOK, lane);
   int kvh = share.kvh, b = share.b;
   SeqRows s = seq_rows(p, b);
   if (tid == 0) s_odd = s_dead = 0;
@@ -806,7 +815,7 @@ int64_t few_bytes(const AttendParams& a) {
   using T = Tile<D, BITS>;
   int64_t tokens = (int64_t)a.c.max_pages << a.c.page_shift;
   if (a.window > 0) tokens = std::min<int64_t>(tokens, (int64_t)a.window + a.c.max_q + a.sinks + 2 * T::kTokens);
-  const int64_t whole = (int64_t)a.c.batch * a.c.n_kv_heads >= kSms ? kWholeMany : kWholeFew;
+  const int64_t whole = (int64_t)a.c.batch * a.c.n_kv_heads >= kSms ? kWholeMany<BITS> : kWholeFew<BITS>;
   return tokens <= whole * T::kTokens ? 0 : part_bytes(kWave<D, BITS, NT>, a.part_rows, D);
 }
 
