@@ -22,7 +22,9 @@ namespace {
 // times on the SMs.)
 //
 // 8 sequences of 32,768 tokens of bf16, 32 over 8 heads of 128: 162 to 166 us, 6.6 TB/s, 97 % of a copy's rate; of 8-bit pages 89 us,
-// 6.0 TB/s, where the conversions of the codes take issue slots too.  One token over 64 tokens, in a graph: 3.5 us, a launch and four
+// 6.0 TB/s, where the conversions of the codes take issue slots too; of 4-bit pages 70 us, 4.3 TB/s: 320 instructions for 16 tokens of K and
+// V, 80 of them conversions, 64 products with the groups' scales and 40 that bring two tokens' values together, issue in 58 % of the
+// cycles (the copies alone take 50 us).  One token over 64 tokens, in a graph: 3.5 us, a launch and four
 // loads that wait for each other (lengths, page, K, V).
 constexpr int kStageBytes = 8192;
 
@@ -34,7 +36,8 @@ constexpr int kThreads = kWarps * 32;
 // Three blocks with 8-bit pages: 170 us and more for 165.
 constexpr int kStages = 2;
 
-// Blocks to an SM.
+// Blocks to an SM.  4-bit pages: conversions, scales and products take more issue slots than the memory takes time, so more warps are wanted:
+// 8 x 32,768 tokens, us: two blocks 76, three 70.  Four with one stage to a warp, K and V refilled apart, 74; with tiles of 32 tokens 84.
 template <int D, int BITS, int NT>
 constexpr int kPerSm = BITS == 4 && !(D == 128 && NT == 2) && NT < 3 ? 3 : 2;
 template <int D, int BITS, int NT>

@@ -29,7 +29,7 @@
 //
 // 8192 tokens, 32 over 8 heads of 128, causal, bf16: 404 to 416 us, 1.34 PFLOP/s, 70 % of a library product's rate: a token tile takes
 // both lanes 2770 cycles, of which the products 2048, and the diagonal's tiles count half.  2048 tokens over 32,768 of 8-bit
-// pages: 848 us, 1.26 PFLOP/s; there the softmax and the conversions share the issue slots (3700 cycles a tile).
+// pages: 830 us, 1.28 PFLOP/s; there the softmax and the conversions share the issue slots (3600 cycles a tile); of 4-bit pages 889 us.
 #include <cuda_runtime.h>
 
 #include <algorithm>
