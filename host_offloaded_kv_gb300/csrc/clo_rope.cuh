@@ -118,6 +118,28 @@ __device__ __forceinline__ CosSin cos_sin_of(const Unit<D>& u, const Place<AXES>
   return c;
 }
 
+// The same for a warp whose lanes all stand at one place: the lanes that share a unit compute a pair or two each and hand them around.
+template <int D, bool AXES>
+__device__ __forceinline__ CosSin cos_sin_shared(const Rope& r, const uint64_t* s_turn, const Place<AXES>& where, int lane) {
+  constexpr int kLanes = D / 16, kShare = 32 / kLanes, kOwn = 8 / kShare;
+  const int u = lane % kLanes, first = lane / kLanes;
+  float2 own[kOwn];
+#pragma unroll
+  for (int j = 0; j < kOwn; ++j) {
+    const int i = first + j * kShare;
+    const uint32_t axis = AXES ? (uint32_t)(s_turn[CLO_ROPE_MAX_PAIRS + u] >> (8 * i)) : 0u;
+    own[j] = rope_cos_sin(where.on(axis), s_turn[u * 8 + i], r.plan.magnitude);
+    if (r.transpose) own[j].y = -own[j].y;
+  }
+  CosSin c;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    c.v[i].x = __shfl_sync(0xffffffffu, own[i / kShare].x, u + i % kShare * kLanes);
+    c.v[i].y = __shfl_sync(0xffffffffu, own[i / kShare].y, u + i % kShare * kLanes);
+  }
+  return c;
+}
+
 // Rotates a unit: x[0..8) are the elements at a, x[8..16) those at b.
 template <int D>
 __device__ __forceinline__ void rotate_unit(const Unit<D>& u, const CosSin& c, float* x) {
@@ -160,8 +182,7 @@ __device__ __forceinline__ void rotate_heads(const Rope& r, const uint64_t* s_tu
   }
   Place<AXES> where;
   if (!position(&where)) return;
-  CosSin c;
-  if (u.rotate) c = cos_sin_of<D, AXES>(u, where, r.transpose);
+  const CosSin c = cos_sin_shared<D, AXES>(r, s_turn, where, lane);
 #pragma unroll
   for (int i = 0; i < ITERS; ++i) {
     const int h = head0 + i * kRows + lane / kLanes;

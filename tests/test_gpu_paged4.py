@@ -493,3 +493,103 @@ def test_what_an_append_writes_gets_a_new_version(clo):
     assert [t._version for t in pages] == now
     with pytest.raises(ValueError, match="gradient"):
         cache.attention(x.clone().requires_grad_(), c.starts, c.lens, c.tab)
+
+
+# --------------------------------------------------------------------------------------------- rows at which one kernel gives way to another
+ROWS = [
+    # seqs, hkv, group, d, page, window, sinks: 17 to 24 rows per kv head of 64 and of 128, 25, and both sides of 8 and 16
+    ([(6, 500), (1, 40), (3, 7), (0, 20)], 2, 4, 64, 16, 0, 0),
+    ([(7, 900), (5, 64), (7, 7)], 1, 3, 64, 64, 100, 5),
+    ([(3, 333), (2, 2)], 2, 8, 64, 128, 0, 0),
+    ([(24, 700), (17, 20), (1, 1)], 2, 1, 64, 32, 0, 0),
+    ([(25, 700), (17, 20), (1, 1)], 2, 1, 64, 32, 64, 3),
+    ([(6, 500), (1, 40), (3, 7), (0, 20)], 2, 4, 128, 16, 0, 0),
+    ([(8, 300), (1, 9)], 2, 1, 128, 64, 0, 0),
+    ([(9, 300), (1, 9)], 2, 1, 64, 64, 0, 0),
+    ([(16, 300), (1, 9)], 1, 1, 128, 32, 0, 0),
+    # long enough to be cut between blocks
+    ([(6, 20000), (4, 900), (2, 3)], 2, 4, 64, 64, 0, 0),
+    ([(7, 3 + 150 * i) for i in range(40)], 4, 3, 64, 16, 0, 0),
+]
+
+
+@pytest.mark.parametrize("case", range(len(ROWS)))
+def test_attention_at_every_width_of_rows(clo, case):
+    seqs, hkv, group, d, page, window, sinks = ROWS[case]
+    c = Case(clo, [(min(n, kv), kv) for n, kv in seqs], hkv, d, page, seed=400 + case)
+    c.device()
+    q = bf16(rand(401 + case, c.total, hkv * group, d))
+    want, spread, reach = dense_on_device(c, q, window, sinks)
+    bound = limit(c.pages4, c.seqs, want, spread, reach, d)
+    first = c.attend(q, window, sinks)
+    check(first, want, bound)
+    check(c.attend(q, window, sinks, workspace=torch.empty(16, dtype=torch.uint8, device="cuda")), want, bound, "no workspace")
+    work = torch.full((c.cache.attention_workspace(hkv * group, len(seqs), c.total, c.table.shape[1], max_q=c.max_q, window=window, sinks=sinks),), 0xff,
+                      dtype=torch.uint8, device="cuda")
+    assert torch.equal(c.attend(q, window, sinks, workspace=work), first)  # whatever the workspace held
+
+
+def test_queries_that_are_not_finite_spoil_their_own_rows(clo):
+    for rows in (1, 5, 40):
+        c = Case(clo, [(rows, 150), (rows, 90)], 2, 64, 32, seed=420 + rows)
+        c.device()
+        q = bf16(rand(421, c.total, 4, 64))
+        clean = c.attend(q)
+        q[0, 1, 3], q[rows, 2, 60] = NAN, INF
+        got = c.attend(q)
+        same_rows = torch.ones(c.total, 4, dtype=torch.bool)
+        same_rows[0, 1] = same_rows[rows, 2] = False
+        assert torch.isnan(got[0, 1]).all()
+        assert torch.equal(got.cpu()[same_rows], clean.cpu()[same_rows])
+
+
+def test_strided_rows_in_a_wider_buffer(clo):
+    # q, out, k, v and the read-back inside wider buffers; what lies between them is left as it was
+    d, hkv, group, page = 64, 2, 3, 16
+    c = Case(clo, [(5, 37), (1, 20)], hkv, d, page, seed=430)
+    cache = c.device()
+    wide = lambda h, fill: torch.full((c.total + 1, h + 2, d + 8), fill, dtype=BF16, device="cuda")  # noqa: E731
+    q, out = wide(hkv * group, 0.5), wide(hkv * group, 7.0)
+    src = bf16(rand(431, c.total, hkv * group, d))
+    q[:c.total, 1:-1, 8:] = src.cuda()
+    cache.attention(q[:c.total, 1:-1, 8:], c.starts, c.lens, c.tab, out=out[:c.total, 1:-1, 8:], max_q=5)
+    c.compare(out[:c.total, 1:-1, 8:], src)
+    keep = torch.ones(out.shape, dtype=torch.bool)
+    keep[:c.total, 1:-1, 8:] = False
+    assert bool((out.cpu()[keep] == 7.0).all())
+    k, v = wide(hkv, 0.25), wide(hkv, 0.25)
+    x = bf16(rand(432, c.total, hkv, d))
+    k[:c.total, 1:-1, 8:] = x.cuda()
+    v[:c.total, 1:-1, 8:] = x.cuda() * 2
+    cache.append(k[:c.total, 1:-1, 8:], v[:c.total, 1:-1, 8:], c.starts, c.lens, c.tab, max_q=5)
+    for side in range(2):
+        c.pages4.append(side, x.double() * (1 + side), c.seqs, c.table)
+    same(cache, c.pages4)
+    ko, vo = wide(hkv, 3.0), wide(hkv, 3.0)
+    cache.read(c.starts, c.lens, c.tab, c.total, k_out=ko[:c.total, 1:-1, 8:], v_out=vo[:c.total, 1:-1, 8:])
+    a, b = cache.read(c.starts, c.lens, c.tab, c.total)
+    keep = torch.ones(ko.shape, dtype=torch.bool)
+    keep[:c.total, 1:-1, 8:] = False
+    for o, want in ((ko, a), (vo, b)):
+        assert torch.equal(o[:c.total, 1:-1, 8:], want) and bool((o.cpu()[keep] == 3.0).all())
+
+
+def test_thousands_of_sequences(clo):
+    # single tokens and pairs of 2000 sequences under the C names, some without rows, some without tokens
+    d, page, hkv, group = 64, 16, 1, 2
+    seqs = [((i % 3), 0 if i % 50 == 0 else (i % 3) + i % 30) for i in range(2000)]
+    seqs = [(min(n, kv), kv) for n, kv in seqs]
+    c = Case(clo, seqs, hkv, d, page, seed=440)
+    cache = c.device()
+    x = bf16(rand(441, c.total, hkv, d))
+    clo.clo_paged_append(cache, x.cuda(), x.cuda(), c.starts, c.lens, c.tab, max_q=2)
+    for side in range(2):
+        c.pages4.append(side, x.double(), c.seqs, c.table)
+    same(cache, c.pages4)
+    k, _ = clo.clo_paged_read(cache, c.starts, c.lens, c.tab, c.total, max_q=2)
+    q = bf16(rand(442, c.total, hkv * group, d))
+    want, spread, reach = ref.attention(c.pages, q, c.seqs, c.table, group)
+    check(clo.clo_paged_attention(cache, q.cuda(), c.starts, c.lens, c.tab, max_q=2), want, limit(c.pages4, c.seqs, want, spread, reach, d))
+    vals = c.pages.val[0]
+    want = torch.stack([vals[int(c.table[b, (kv - n + i) // page]), :, (kv - n + i) % page] for b, (_, n, kv) in enumerate(c.seqs) for i in range(n)])
+    assert torch.equal(k.cpu().double(), want)
