@@ -1,8 +1,8 @@
 // Rotary positions (clo_rope) and the read-back of pages (clo_paged_read): one pass over the rows each, bounded by HBM
 // traffic (large calls) or by one launch and two or three dependent loads (single-token steps).
 //
-// Measured: 8192 tokens of 32 heads of 128, 24.9 us, 5.4 TB/s (80 % of a copy's rate); 30,000 tokens 75 us, 96 %; one token 2.2 us in a
-// graph; with three axes 26.7 us.  Read-back of 8 x 8192 tokens: bf16 82 us, 6.5 TB/s, 8-bit pages 70 us, 5.8 TB/s; of 10,800 tokens of 4-bit pages
+// Measured: 8192 tokens of 32 heads of 128, on one axis or three, 24.1 us, 5.6 TB/s (82 % of a copy's rate); 30,000 tokens 74 us, 97 %; one
+// token 2.2 us in a graph.  Read-back of 8 x 8192 tokens: bf16 82 us, 6.5 TB/s, 8-bit pages 70 us, 5.8 TB/s; of 10,800 tokens of 4-bit pages
 // 18.5 us, 3.0 TB/s.
 #include <cuda_runtime.h>
 
@@ -34,7 +34,7 @@ clo_status paged_fail(clo_status st, const char* fmt, ...) {
 namespace {
 
 template <int D, int ITERS, bool AXES>
-__global__ void __launch_bounds__(kThreads, ITERS == kLongIters ? 2 : ITERS == kMidIters ? 3 : 4) k_rope(const Rope r, const Rows x, const Rows y, const int64_t* __restrict__ positions,
+__global__ void __launch_bounds__(kThreads, ITERS == kMidIters ? 3 : 4) k_rope(const Rope r, const Rows x, const Rows y, const int64_t* __restrict__ positions,
                                                    int64_t n_tokens, int n_heads, int chunks) {
   __shared__ __align__(16) uint64_t s_turn[kTurns<AXES>];
   stage_turns<AXES>(r, s_turn);
@@ -359,7 +359,7 @@ extern "C" CLO_API clo_status clo_rope(const clo_rope_plan* plan, const clo_rows
   const bool vec = !rows_fault(x, true) && !rows_fault(y, true) && plan->rot_dim % 16 == 0 && (head_dim == 64 || head_dim == 128);
   if (vec) {
     const int rows = 32 / (head_dim / 16);  // heads per round
-    const int iters = n_tokens < kLongTokens || n_heads <= kShortIters * rows ? kShortIters : n_heads % (kLongIters * rows) ? kMidIters : kLongIters;
+    const int iters = n_tokens < kLongTokens || n_heads <= kShortIters * rows ? kShortIters : kMidIters;
     const int per = iters * rows;  // heads per warp
     const int chunks = (n_heads + per - 1) / per;
     const int64_t blocks = (n_tokens * chunks + kWarps - 1) / kWarps;
@@ -367,7 +367,7 @@ extern "C" CLO_API clo_status clo_rope(const clo_rope_plan* plan, const clo_rows
     auto kernel = [&](auto d, auto axes) {
       constexpr int D = decltype(d)::value;
       constexpr bool AXES = decltype(axes)::value;
-      return iters == kLongIters ? k_rope<D, kLongIters, AXES> : iters == kMidIters ? k_rope<D, kMidIters, AXES> : k_rope<D, kShortIters, AXES>;
+      return iters == kMidIters ? k_rope<D, kMidIters, AXES> : k_rope<D, kShortIters, AXES>;
     };
     using D128 = std::integral_constant<int, 128>;
     using D64 = std::integral_constant<int, 64>;

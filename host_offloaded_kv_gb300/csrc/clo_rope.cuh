@@ -160,7 +160,6 @@ __device__ __forceinline__ void rotate_unit(const Unit<D>& u, const CosSin& c, f
   }
 }
 
-
 // ---------------------------------------------------------------------------- rows of one token
 // A warp takes one token and up to ITERS rounds of its heads: the cosines and sines of a lane's unit are computed
 // once for all of them.
@@ -201,9 +200,10 @@ __device__ __forceinline__ void rotate_heads(const Rope& r, const uint64_t* s_tu
   }
 }
 
-// Rounds of heads per warp: many for long calls, where the sines count, few for short ones, where the latency does, and no more
-// than the heads fill.  8192 tokens of 128-element heads, us with 8 / 4 / 2 rounds: 8 heads (floor 5.0) 11.0 / - / 7.5, 16 heads (9.9)
-// 13.0 / 10.7 / -, 40 heads (24.7) 33.6 / 30.4 / -; 2000 tokens, 32 heads (4.8) 6.3 / 7.1 / -.
+// Rounds of heads per warp: more for long calls, where the sines count, few for short ones, where the latency does, and no more than the
+// heads fill.  8192 tokens of 128-element heads, us with 8 / 4 / 2 rounds: 32 heads (floor 19.8) 24.7 / 24.0 / 24.7, 40 heads (24.7)
+// 28.8 / 28.8 / 29.1; 30,000 tokens of 32 heads (72.4) 74.7 / 73.8 / 75.9.  (Before lanes shared the sines, eight were best for 32 heads.)  The
+// append's queries take eight, beside pages that are written by whole warps.
 constexpr int kLongIters = 8, kMidIters = 4, kShortIters = 2;
 constexpr int64_t kLongTokens = 8 * 152;  // a warp per SM and slot of eight
 template <int D>
