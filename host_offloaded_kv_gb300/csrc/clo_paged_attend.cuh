@@ -252,6 +252,8 @@ int64_t attend_few_e2m1_bytes(const AttendParams& a, int head_dim);
 int64_t attend_few_bf16_bytes(const AttendParams& a, int head_dim);
 int64_t attend_few_e4m3_bytes(const AttendParams& a, int head_dim);
 cudaError_t launch_attend_many(const AttendParams& a, int head_dim, int kv_bits, cudaStream_t st);
+cudaError_t launch_attend_many_e4m3(const AttendParams& a, int head_dim, cudaStream_t st);
+cudaError_t launch_attend_many_e2m1(const AttendParams& a, int head_dim, cudaStream_t st);
 int64_t attend_many_bytes(const AttendParams& a, int head_dim);
 
 }  // namespace clo

@@ -29,7 +29,7 @@
 //
 // 8192 tokens, 32 over 8 heads of 128, causal, bf16: 404 to 416 us, 1.34 PFLOP/s, 70 % of a library product's rate: a token tile takes
 // both lanes 2770 cycles, of which the products 2048, and the diagonal's tiles count half.  2048 tokens over 32,768 of 8-bit
-// pages: 830 us, 1.28 PFLOP/s; there the softmax and the conversions share the issue slots (3600 cycles a tile); of 4-bit pages 889 us.
+// pages: 785 us, 1.36 PFLOP/s; there the softmax and the conversions share the issue slots (3400 cycles a tile); of 4-bit pages 806 us.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -461,10 +461,13 @@ __device__ __noinline__ void look_again(const AttendParams a, const S& sh) {
   });
 }
 
-template <int D, int BITS, int TILES>
+// SETS: page scales of half a tile, that is the pages that 64 tokens lie in (8-bit and 4-bit pages; 1 with pages of 64 tokens or more).  The softmax
+// takes them as few times as that: with pages of 64, one set against four, 2048 tokens over 32,768 of 8-bit pages 784 / 830 us, of 4-bit
+// pages 805 / 891.  Deciding it while the kernel runs cost more than it gave (876, and 472 for 425 with pages of 32).
+template <int D, int BITS, int TILES, int SETS>
 __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_many(const AttendParams a, const __grid_constant__ PageMaps maps) {
   using C = Cfg<D, BITS, TILES>;
-  constexpr int SLOTS = C::kSlots;
+  constexpr int SLOTS = C::kSlots, kSet = 4 / SETS;  // 16-token groups to a set
   extern __shared__ uint8_t smem_raw[];
   constexpr int kMeta = C::kMeta;
   __shared__ __align__(16) Shared<kMeta, TILES> sh;
@@ -642,11 +645,14 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
           for (int k = 0; k < 16; k += 2)
 #pragma unroll
             for (int h = 0; h < 4; ++h) m4[h] = fmaxf(m4[h], fmaxf(__uint_as_float(x[16 * h + k]), __uint_as_float(x[16 * h + k + 1])));
-          if (BITS != 16) {
 #pragma unroll
-            for (int h = 0; h < 4; ++h) m4[h] = fmaf(m4[h], fmaxf(sh.scale[slot][0][4 * half + h] * fac, 1e-37f), sh.scale[slot][1][4 * half + h]);
+          for (int h = 0; h < 4; h += kSet) {
+            float top = m4[h];
+#pragma unroll
+            for (int i = 1; i < kSet; ++i) top = fmaxf(top, m4[h + i]);
+            if (BITS != 16) top = fmaf(top, fmaxf(sh.scale[slot][0][4 * half + h] * fac, 1e-37f), sh.scale[slot][1][4 * half + h]);
+            mx = fmaxf(mx, top);
           }
-          mx = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
         }
         if (BITS == 16) mx *= fac;
         if (!whole) tc_wait_st();
@@ -671,13 +677,15 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
           uint32_t w[32];
-          uint64_t sum2[2] = {0, 0};
+          uint64_t sum2[2] = {0, 0}, mul2 = pack2(fac, fac), add_2 = pack2(sub, sub);
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
-            // 16 tokens: one page, one set of scales
             const int at = 4 * half + h;
-            const float mul = BITS != 16 ? fmaxf(sh.scale[slot][0][at] * fac, 1e-37f) : fac, add = BITS != 16 ? sh.scale[slot][1][at] + sub : sub;
-            const uint64_t mul2 = pack2(mul, mul), add_2 = pack2(add, add);
+            if (BITS != 16 && h % kSet == 0) {  // another page's scales
+              const float mul = fmaxf(sh.scale[slot][0][at] * fac, 1e-37f), add = sh.scale[slot][1][at] + sub;
+              mul2 = pack2(mul, mul);
+              add_2 = pack2(add, add);
+            }
 #pragma unroll
             for (int k = 0; k < 16; k += 2) {
               float2 y = unpack2(fma2(pack2(__uint_as_float(x[16 * h + k]), __uint_as_float(x[16 * h + k + 1])), mul2, add_2));
@@ -687,7 +695,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, TILES>::kThreads, 1) k_attend_man
               // weights in the products' type: bf16 next to bf16 V, fp16 next to 8-bit V
               w[8 * h + k / 2] = BITS == 16 ? pack_bf16(y.x, y.y) : pack_f16(y.x, y.y);
             }
-            if (BITS != 16 || h == 3) {
+            if ((h + 1) % kSet == 0) {
               const float2 q = unpack2(add2(sum2[0], sum2[1]));
               l = BITS != 16 ? fmaf(q.x + q.y, sh.scale[slot][2][at], l) : l + (q.x + q.y);
               sum2[0] = sum2[1] = 0;
@@ -1182,12 +1190,12 @@ int64_t many_bytes(const AttendParams& a) {
   return part_bytes(kSms, TILES * kRows, D);
 }
 
-template <int D, int BITS, int TILES>
+template <int D, int BITS, int TILES, int SETS>
 cudaError_t launch(AttendParams a, cudaStream_t st) {
   using C = Cfg<D, BITS, TILES>;
   PageMaps maps;
   if (make_page_maps(a.c, D, BITS, std::min(a.c.page_size, BITS == 16 ? kTok : kTok / 2), &maps)) return cudaErrorInvalidValue;
-  auto* f = k_attend_many<D, BITS, TILES>;
+  auto* f = k_attend_many<D, BITS, TILES, SETS>;
   static std::atomic<uint64_t> prepared{0};
   cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(f), C::kBytes, &prepared);
   if (e != cudaSuccess) return e;
@@ -1199,21 +1207,40 @@ cudaError_t launch(AttendParams a, cudaStream_t st) {
   return launch_after(k_attend_many_join<D, BITS, TILES>, dim3(kSms, TILES * kRows / 8), 256, st, a);
 }
 
-template <int D, int BITS>
+template <int D, int BITS, int SETS>
 cudaError_t launch_rows(const AttendParams& a, cudaStream_t st) {
-  return a.part_rows <= kRows ? launch<D, BITS, 1>(a, st) : launch<D, BITS, 2>(a, st);
+  return a.part_rows <= kRows ? launch<D, BITS, 1, SETS>(a, st) : launch<D, BITS, 2, SETS>(a, st);
+}
+template <int D, int BITS>
+cudaError_t launch_sets(const AttendParams& a, cudaStream_t st) {
+  if constexpr (BITS != 16) {
+    if (a.c.page_size == 16) return launch_rows<D, BITS, 4>(a, st);
+    if (a.c.page_size == 32) return launch_rows<D, BITS, 2>(a, st);
+  }
+  return launch_rows<D, BITS, 1>(a, st);
+}
+template <int BITS>
+cudaError_t launch_bits(const AttendParams& a, int head_dim, cudaStream_t st) {
+  return head_dim == 128 ? launch_sets<128, BITS>(a, st) : launch_sets<64, BITS>(a, st);
 }
 
 }  // namespace
 
+// The coded pages' kernels are compiled by files of their own, which name their bits and include this one.
+#if defined(CLO_PROMPT_BITS) && CLO_PROMPT_BITS == 8
+cudaError_t launch_attend_many_e4m3(const AttendParams& a, int head_dim, cudaStream_t st) { return launch_bits<8>(a, head_dim, st); }
+#elif defined(CLO_PROMPT_BITS)
+cudaError_t launch_attend_many_e2m1(const AttendParams& a, int head_dim, cudaStream_t st) { return launch_bits<4>(a, head_dim, st); }
+#else
 cudaError_t launch_attend_many(const AttendParams& a, int head_dim, int kv_bits, cudaStream_t st) {
-  if (head_dim == 128) return kv_bits == 16 ? launch_rows<128, 16>(a, st) : kv_bits == 8 ? launch_rows<128, 8>(a, st) : launch_rows<128, 4>(a, st);
-  return kv_bits == 16 ? launch_rows<64, 16>(a, st) : kv_bits == 8 ? launch_rows<64, 8>(a, st) : launch_rows<64, 4>(a, st);
+  return kv_bits == 16 ? launch_bits<16>(a, head_dim, st) : kv_bits == 8 ? launch_attend_many_e4m3(a, head_dim, st) : launch_attend_many_e2m1(a, head_dim, st);
 }
 
 int64_t attend_many_bytes(const AttendParams& a, int head_dim) {
   if (head_dim == 128) return a.part_rows <= kRows ? many_bytes<128, 1>(a) : many_bytes<128, 2>(a);
   return a.part_rows <= kRows ? many_bytes<64, 1>(a) : many_bytes<64, 2>(a);
 }
+
+#endif
 
 }  // namespace clo
