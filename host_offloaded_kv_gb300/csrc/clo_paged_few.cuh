@@ -23,8 +23,7 @@ namespace {
 //
 // 8 sequences of 32,768 tokens of bf16, 32 over 8 heads of 128: 162 to 166 us, 6.6 TB/s, 97 % of a copy's rate; of 8-bit pages 89 us,
 // 6.0 TB/s, where the conversions of the codes take issue slots too; of 4-bit pages 70 us, 4.3 TB/s: 320 instructions for 16 tokens of K and
-// V, 80 of them conversions, 64 products with the groups' scales and 40 that bring two tokens' values together, issue in 58 % of the
-// cycles (the copies alone take 50 us).  One token over 64 tokens, in a graph: 3.5 us, a launch and four
+// V, of which 80 conversions, 64 products with the groups' scales and 40 permutes take two cycles each, bound it (the copies alone: 50 us).  One token over 64 tokens, in a graph: 3.5 us, a launch and four
 // loads that wait for each other (lengths, page, K, V).
 constexpr int kStageBytes = 8192;
 
