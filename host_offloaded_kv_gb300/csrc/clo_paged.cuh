@@ -178,8 +178,6 @@ template <int D>
 __device__ __forceinline__ int64_t groups_at(const PagedParams& p, int page, int head, int slot) {
   return (((int64_t)page * p.n_kv_heads + head) * p.page_size + slot) * (D / 16);
 }
-// Two group scales next to each other as fp32.
-__device__ __forceinline__ float2 group_scales(const uint8_t* two) { return e4m3_to_f32x2(*reinterpret_cast<const uint16_t*>(two)); }
 
 // A sequence's visible tokens for a row at position `pos` are [0, sink_end) and [lo, hi).
 struct Visible {

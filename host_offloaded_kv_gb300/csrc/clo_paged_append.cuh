@@ -100,8 +100,8 @@ struct Codes4 {
   uint32_t open;  // what fp32's rotation left open, a bit per pair: a code or a scale lies within its error of a border
 };
 
-// x / d for a divisor whose rounded reciprocal r is given: one correction by the exact remainder rounds the quotient correctly
-// (Markstein's method), so that quotients on a border between two codes stay there.
+// x / d for a divisor whose reciprocal r is given: one correction by the exact remainder (Markstein's method).  It rounds the quotient correctly
+// where r is the rounded reciprocal; with an r that is a unit off, quotients of few bits, as on a border between two codes, still come out exactly.
 __device__ __forceinline__ float quotient(float x, float d, float r) {
   const float t = x * r;
   return fmaf(fmaf(-t, d, x), r, t);

@@ -434,8 +434,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm<D, BITS, NT>) k_attend_few(co
         __syncwarp();
       }
 
-      float my_ks = 1.f, my_lvs = 0.f, my_inv = 1.f;  // 4-bit pages: a lane per 16 tokens
-      if (BITS == 4) {
+      float my_ks = 1.f, my_lvs = 0.f, my_inv = 1.f;  // page scales: a lane per 16 tokens
+      if (BITS != 16) {
         my_ks = fmaxf(s_scale[warp][st][0][lane & (KM - 1)], kMinScale);
         const float vs = fmaxf(s_scale[warp][st][1][lane & (KM - 1)], kMinScale);
         my_lvs = __log2f(vs);
@@ -515,15 +515,10 @@ __global__ void __launch_bounds__(kThreads, kPerSm<D, BITS, NT>) k_attend_few(co
       for (int mt = 0; mt < KM; ++mt) {
         float ks = 1.f, lvs = 0.f;
         inv_vs[mt] = 1.f;
-        if (BITS == 4) {
+        if (BITS != 16) {
           ks = __shfl_sync(0xffffffffu, my_ks, mt);
           lvs = __shfl_sync(0xffffffffu, my_lvs, mt);
           inv_vs[mt] = __shfl_sync(0xffffffffu, my_inv, mt);
-        } else if (BITS != 16) {
-          ks = fmaxf(s_scale[warp][st][0][mt], kMinScale);
-          const float vs = fmaxf(s_scale[warp][st][1][mt], kMinScale);
-          lvs = __log2f(vs);
-          inv_vs[mt] = __frcp_rn(vs) * kDown;
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -531,10 +526,10 @@ __global__ void __launch_bounds__(kThreads, kPerSm<D, BITS, NT>) k_attend_few(co
           for (int i = 0; i < 4; ++i) {
             const float f = fac[nt][i & 1] * ks;
             sc[mt][nt][i] = BITS != 16 ? fmaf(sc[mt][nt][i], f, lvs) : sc[mt][nt][i] * f;
-            if (BITS != 4 && !whole) hide(mt, nt, i);
+            if (BITS == 16 && !whole) hide(mt, nt, i);
           }
       }
-      if (BITS == 4 && !whole) {  // (in the loop above: a branch for each score)
+      if (BITS != 16 && !whole) {  // (in the loop above: a branch for each score; 8-bit pages, 524,288 tokens: 168 us for 166)
 #pragma unroll
         for (int mt = 0; mt < KM; ++mt)
 #pragma unroll
