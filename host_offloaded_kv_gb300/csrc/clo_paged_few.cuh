@@ -803,7 +803,8 @@ __global__ void __launch_bounds__(kJoinThreads) k_attend_join(const AttendParams
     l += s_l[i] * f;
     o[0] += s_o[i][d] * f;
   }
-  a.out[row_offset(a, s.first, kvh, r, a.o_token, a.o_head) + d] = (uint16_t)pack_bf16(l == 0.f ? 0.f : o[0] / l * (BITS == 16 ? 1.f : kSumDown), 0.f);
+  // (o / l alone is 2^7 times the result, past fp32's range for outputs above 2^121)
+  a.out[row_offset(a, s.first, kvh, r, a.o_token, a.o_head) + d] = (uint16_t)pack_bf16(l == 0.f ? 0.f : o[0] * (BITS == 16 ? 1.f : kSumDown) / l, 0.f);
 }
 
 // Bytes of workspace: none where no unit can be long, or no unit so long that its block would outlast the others by much.

@@ -1,0 +1,46 @@
+"""4-bit pages on the GPU where ranges and borders end."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import paged4_ref as ref4  # noqa: E402
+from test_gpu_paged import BF16, rand  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def clo():
+    from host_offloaded_kv_gb300 import clo as m
+
+    m.load_library()
+    return m
+
+
+def i32(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def e4m3(t):
+    return t.float().to(torch.float8_e4m3fn).cuda()
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("rows,tokens", [(1, 60000), (1, 300), (200, 3000)])
+def test_outputs_near_the_end_of_bf16(clo, bits, rows, tokens):
+    # every V is 1.5 * 2^e, so every output is: finite whether units are cut and joined or stay whole.  Weights are rounded to fp16 for the
+    # product and not for the sum (2^-11), sums to fp32 (below 2^-14 for so many equal terms), the output to bf16 (2^-8)
+    hkv, group, d, page = 2, 4, 64, 64
+    n = -(-tokens // page)
+    for e in (120, 124, 126):
+        if bits == 8:
+            pages = [torch.zeros(n, hkv, page, d), torch.full((n, hkv, page, d), 1.5)]
+            cache = clo.PagedCache(*(p.to(torch.float8_e4m3fn).cuda() for p in pages), torch.ones(n, hkv).cuda(), torch.full((n, hkv), 2.0 ** e).cuda())
+        else:
+            codes = [ref4.bytes_of(torch.full((n, hkv, page, d), x, dtype=torch.float64)).cuda() for x in (0.0, 6.0)]
+            cache = clo.PagedCache(*codes, torch.ones(n, hkv).cuda(), torch.full((n, hkv), 2.0 ** (e - 2)).cuda(), *(e4m3(torch.ones(n, hkv, page, d // 16)) for _ in range(2)))
+        q = rand(1, rows, hkv * group, d).to(BF16).cuda()
+        for work in (None, torch.empty(16, dtype=torch.uint8, device="cuda")):
+            got = cache.attention(q, i32([0, rows]), i32([tokens]), torch.arange(n, dtype=torch.int32, device="cuda")[None], max_q=rows, workspace=work).double()
+            off = float((got / (1.5 * 2.0 ** e) - 1).abs().max())
+            assert off <= 2.0 ** -8 + 2.0 ** -11 + 2.0 ** -14, (e, work is None, off)
