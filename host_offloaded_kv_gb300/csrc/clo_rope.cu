@@ -182,8 +182,9 @@ __global__ void __launch_bounds__(kThreads) k_paged_read4(const ReadParams a) {
       for (int i = 0; i < kBatch; ++i) {
         const int v = v0 + 32 * i, h = v / kGroups, g = v % kGroups;
         if (v >= n) break;
-        // the product of two numbers of a few bits and a power of two is exact
-        const float f = e4m3_to_f32x2(group[i]).x * fmaxf(scale[i], kMinScale);
+        // a code times its group's scale is exact and below 2^12; the page's scale comes last, as group scale times page scale may pass fp32's
+        // range where the code is zero or a half.  Powers of two leave the product exact, other scales round it to fp32.
+        const float f = e4m3_to_f32x2(group[i]).x, page_scale = fmaxf(scale[i], kMinScale);
         uint16_t* dst = out.p + t * out.token + (int64_t)h * out.head + g * 16;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -193,8 +194,8 @@ __global__ void __launch_bounds__(kThreads) k_paged_read4(const ReadParams a) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const float2 d = __half22float2(*reinterpret_cast<const __half2*>(&c[k]));
-            x[2 * k] = d.x * f;
-            x[2 * k + 1] = d.y * f;
+            x[2 * k] = d.x * f * page_scale;
+            x[2 * k + 1] = d.y * f * page_scale;
           }
           *reinterpret_cast<uint4*>(dst + 8 * half) = pack8(x);
         }

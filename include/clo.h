@@ -465,8 +465,8 @@ CLO_API clo_status clo_paged_append(const clo_paged_cache* cache, const clo_page
                                     const int64_t* positions, const clo_rows* k, const clo_rows* v, const clo_rows* q,
                                     const clo_rows* q_out, int32_t n_q_heads, void* stream);
 
-/* Read back: the batch's rows as bf16 (codes times their scales, rounded once) into k_out and v_out
- * [total_q][n_kv_heads][head_dim]; rows as for clo_paged_append.  A whole sequence is read with
+/* Read back: the batch's rows as bf16 (codes times their scales, rounded once; by way of fp32 where a scale is no power of two)
+ * into k_out and v_out [total_q][n_kv_heads][head_dim]; rows as for clo_paged_append.  A whole sequence is read with
  * q_starts = {0, n}, kv_lens = {n}, and goes to the host pool with clo_append_kv(..., src_is_device = 1).
  * Errors: CLO_ERR_INVALID, CLO_ERR_CUDA. */
 CLO_API clo_status clo_paged_read(const clo_paged_cache* cache, const clo_paged_batch* batch, const clo_rows* k_out,

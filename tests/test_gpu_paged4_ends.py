@@ -44,3 +44,19 @@ def test_outputs_near_the_end_of_bf16(clo, bits, rows, tokens):
             got = cache.attention(q, i32([0, rows]), i32([tokens]), torch.arange(n, dtype=torch.int32, device="cuda")[None], max_q=rows, workspace=work).double()
             off = float((got / (1.5 * 2.0 ** e) - 1).abs().max())
             assert off <= 2.0 ** -8 + 2.0 ** -11 + 2.0 ** -14, (e, work is None, off)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_read_back_of_large_scales(clo, d):
+    # group scale times page scale lies past fp32's range, code times both does not
+    hkv, page = 3, 16
+    gen = torch.Generator().manual_seed(d)
+    code = torch.tensor([0.0, 0.5, -0.5, -0.0], dtype=torch.float64)[torch.randint(0, 4, (2, hkv, page, d), generator=gen)]
+    group = torch.full((2, hkv, page, d // 16), 448.0, dtype=torch.float64)
+    scale = torch.full((2, hkv), 1.0, dtype=torch.float64) * 2.0 ** 120
+    cache = clo.PagedCache(*(ref4.bytes_of(code).cuda() for _ in range(2)), *(scale.float().cuda() for _ in range(2)), *(e4m3(group) for _ in range(2)))
+    k, v = cache.read(i32([0, 2 * page]), i32([2 * page]), i32([[1, 0]]), 2 * page)
+    want = ref4.values(code, group, scale)[[1, 0]].transpose(1, 2).reshape(2 * page, hkv, d)
+    assert torch.isfinite(want).all() and float(want.abs().max()) < 2.0 ** 128
+    for got in (k, v):
+        assert torch.equal(got.cpu().double(), want)
