@@ -93,6 +93,8 @@ __device__ __forceinline__ Partners<D> partners_of(bool halves, int rot_dim, int
 }
 
 constexpr float kRotationError = 3.2e-7f;
+// The same of a job's largest element, which is no smaller than the other one of its pair, and what the products with it round.
+constexpr float kMaxError = 2.f * kRotationError + 0x1p-23f;
 
 // Codes and group scales of a unit's two vectors.
 struct Codes4 {
@@ -249,18 +251,51 @@ __device__ __forceinline__ void write_page(const AppendParams& a, const uint64_t
     }
   }
   if (BITS == 16) return;
-  amax = warp_max(amax);
-  if (kPer > 1) {
-    if (lane == 0) s_red[group * kPer + part] = amax;
-    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(kPer * 32) : "memory");
+  // the job's largest, of its warps' lanes
+  auto over_warps = [&](float m) {
+    m = warp_max(m);
+    if (kPer > 1) {
+      if (lane == 0) s_red[group * kPer + part] = m;
+      asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(kPer * 32) : "memory");
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) amax = fmaxf(amax, s_red[group * kPer + i]);
+      for (int i = 0; i < kPer; ++i) m = fmaxf(m, s_red[group * kPer + i]);
+    }
+    return m;
+  };
+  // smallest e >= kMinScaleExp with m <= 448 * 2^e (8 bits: 1.75 * 2^8) or 2688 * 2^e (4 bits: 1.3125 * 2^11), from the bits of m
+  auto exponent_of = [](float m) {
+    constexpr int kTopExp = BITS == 8 ? 8 : 11, kTopMantissa = BITS == 8 ? 0x600000 : 0x280000;
+    const int bits = __float_as_int(m);
+    return max((bits >> 23) - 127 - kTopExp + ((bits & 0x7fffff) > kTopMantissa ? 1 : 0), kMinScaleExp);
+  };
+  // Pair n of the lane's unit of a row, in integers.
+  auto exact_pair = [&](int pos, int n) {
+    const int64_t row = s.first + (pos - s.pos0);
+    const uint16_t* src = in.p + row * in.token + (int64_t)head * in.head;
+    const int unit = lane % kLanes, ep = u.interleaved ? u.a + 2 * n : u.a + n, eq = u.interleaved ? ep + 1 : u.b + n;
+    const uint64_t axis = AXES ? s_turn[CLO_ROPE_MAX_PAIRS + unit] >> (8 * n) & 0xffu : 0;
+    const int64_t at = a.positions ? __ldg(a.positions + axis * p.total_q + row) : pos;
+    return rotate_exactly(src[ep], src[eq], (uint64_t)at * s_turn[unit * 8 + n], u.magnitude);
+  };
+  const float mine = amax;
+  amax = over_warps(amax);
+  int e = exponent_of(amax);
+  if (BITS == 4 && side == 0 && a.rope.plan.rot_dim > 0 && exponent_of(amax * (1.f - kMaxError)) != exponent_of(amax * (1.f + kMaxError))) {
+    // fp32 leaves the page's scale open: the largest element once more, exactly
+    float m = rotate ? 0.f : mine;
+#pragma unroll 1
+    for (int i = 0; rotate && i < kUnits * 8; ++i) {
+      const int pos = first + (i >> 3) * kPer * kRows;
+      if (pos >= hi) break;
+      const float2 y = exact_pair(pos, i & 7);
+      const float x0 = fabsf(y.x), x1 = fabsf(y.y);
+      m = fmaxf(m, fmaxf(x0 < INFINITY ? x0 : 0.f, x1 < INFINITY ? x1 : 0.f));
+    }
+    // every warp has read the first sums
+    if (kPer > 1) asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(kPer * 32) : "memory");
+    __syncwarp();
+    e = exponent_of(over_warps(m));
   }
-  // smallest e with amax <= 448 * 2^e (8 bits: 1.75 * 2^8) or 2688 * 2^e (4 bits: 1.3125 * 2^11), from the bits of amax
-  constexpr int kTopExp = BITS == 8 ? 8 : 11, kTopMantissa = BITS == 8 ? 0x600000 : 0x280000;
-  const int bits = __float_as_int(amax);
-  int e = (bits >> 23) - 127 - kTopExp + ((bits & 0x7fffff) > kTopMantissa ? 1 : 0);
-  e = max(e, kMinScaleExp);
   float scale = __int_as_float((e + 127) << 23);
   float* sp = sd.scales + (int64_t)page * p.n_kv_heads + head;
   if (lo > base) {
@@ -316,15 +351,10 @@ __device__ __forceinline__ void write_page(const AppendParams& a, const uint64_t
           c = encode_unit<D, kTurned>(x, inv, rotate && !again, u.interleaved, with);
           if (!kTurned || again || !__any_sync(0xffffffffu, c.open != 0)) break;
           // what fp32 left open: those pairs once more, exactly
-          const int64_t row = s.first + (pos - s.pos0);
-          const uint16_t* src = in.p + row * in.token + (int64_t)head * in.head;
 #pragma unroll 1
           for (; c.open; c.open &= c.open - 1) {
-            const int n = __ffs(c.open) - 1, unit = lane % kLanes;
-            const int ep = u.interleaved ? u.a + 2 * n : u.a + n, eq = u.interleaved ? ep + 1 : u.b + n;
-            const uint64_t axis = AXES ? s_turn[CLO_ROPE_MAX_PAIRS + unit] >> (8 * n) & 0xffu : 0;
-            const int64_t at = a.positions ? __ldg(a.positions + axis * p.total_q + row) : pos;
-            const float2 y = rotate_exactly(src[ep], src[eq], (uint64_t)at * s_turn[unit * 8 + n], u.magnitude);
+            const int n = __ffs(c.open) - 1;
+            const float2 y = exact_pair(pos, n);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
               if (k != n) continue;

@@ -456,7 +456,7 @@ typedef struct clo_paged_batch {
  * rescaled (exact unless they fall below 2^-6 * scale).  Infinities become +-448 * scale, NaN stays.
  * kv_bits 4: the page's scale likewise, with max |x| <= 2688 * 2^e (6 * 448), where it grows the earlier tokens' group scales are rescaled (exact
  * unless they fall below 2^-6). A group's scale is the nearest e4m3 value to max |x| / (6 * 2^e) over its 16 elements, a code the
- * nearest to x / (group scale * 2^e), both with ties to even and of the exactly rotated x. A group with an infinity gets the
+ * nearest to x / (group scale * 2^e), with ties to even. All three are those of the exactly rotated x. A group with an infinity gets the
  * largest scale (448), where infinities are +-6; one with a NaN is NaN.
  * A call may write a page for one sequence and at one place of its table only.  Rows on 16-byte boundaries, strides multiples of 8
  * elements, rot_dim a multiple of 16.

@@ -1,4 +1,6 @@
 """4-bit pages on the GPU where ranges and borders end."""
+import math
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -60,3 +62,37 @@ def test_read_back_of_large_scales(clo, d):
     assert torch.isfinite(want).all() and float(want.abs().max()) < 2.0 ** 128
     for got in (k, v):
         assert torch.equal(got.cpu().double(), want)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("page", [16, 128])
+def test_page_scales_are_those_of_the_exact_rotation(clo, page, interleaved):
+    # The largest key of a page lies within 2^-24 of 2688 * 2^e: the factor on the rotated elements is chosen to put it there.  Pair 0 turns by
+    # one radian per position; a page of 128 is shared out to several warps, and the key stands in its last row.
+    trials, d, hkv = 300, 64, 1
+    gen = torch.Generator().manual_seed(page + interleaved)
+    cache = clo.PagedCache.create(trials, hkv, page, d, kv_bits=4, group=16)
+    want = torch.zeros(trials, dtype=torch.float64)
+    a, b = (0, 1) if interleaved else (0, 32)
+    done = 0
+    while done < trials:
+        p, q = (float(x) for x in torch.randn(2, generator=gen).to(BF16))
+        pos = int(torch.randint(0, 2000, (1,), generator=gen))
+        s, c = math.sin(pos), math.cos(pos)
+        x, y = abs(p * c - q * s), abs(q * c + p * s)
+        if x < 0.1 or x < 1.1 * y:
+            continue
+        e = math.ceil(math.log2(x / 2688.0))
+        magnitude = float(torch.tensor(2688.0 * 2.0 ** e / x, dtype=torch.float32))
+        off = magnitude * x / (2688.0 * 2.0 ** e) - 1.0
+        if abs(off) < 1e-12:  # what 64 bits do not decide
+            continue
+        rows = torch.zeros(page, hkv, d, dtype=BF16)
+        rows[-1, 0, a], rows[-1, 0, b] = p, q
+        plan = clo.clo_rope_plan_init(rot_dim=d, interleaved=interleaved, magnitude=magnitude)
+        where = torch.full((page,), pos, dtype=torch.int64).cuda()
+        cache.append(rows.cuda(), torch.zeros_like(rows).cuda(), i32([0, page]), i32([page]), i32([[done]]), rope=plan, positions=where)
+        want[done] = 2.0 ** (e + (off > 0))
+        done += 1
+    got = cache.k_scales[:, 0].cpu().double()
+    assert torch.equal(got, want), f"{int((got != want).sum())} of {trials} scales"
