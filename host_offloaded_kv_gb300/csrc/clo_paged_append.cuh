@@ -92,9 +92,8 @@ __device__ __forceinline__ Partners<D> partners_of(bool halves, int rot_dim, int
   return w;
 }
 
-constexpr float kRotationError = 3.2e-7f;
-// The same of a job's largest element, which is no smaller than the other one of its pair, and what the products with it round.
-constexpr float kMaxError = 2.f * kRotationError + 0x1p-23f;
+// The error (clo_rotate_exact.cuh) of a job's largest element, which is no smaller than the other one of its pair, and what the products with it round.
+constexpr float kMaxError = 4.06e-7f + 1.13e-7f + 0x1p-23f;
 
 // Codes and group scales of a unit's two vectors.
 struct Codes4 {
@@ -115,10 +114,10 @@ __device__ __forceinline__ uint32_t group_scale_of(uint32_t bits) {
   return pack_e4m3(quotient(__uint_as_float(bits), 6.f, 1.f / 6.f), 0.f);
 }
 
-// x: a unit's values; inv: one over the page's scale (a power of two); rotated: x carries fp32's errors (ROTATED false: no lane's does).  All
-// lanes of the warp take part.
+// x: a unit's values; inv: one over the page's scale (a power of two); rotated: x carries fp32's errors (ROTATED false: no lane's does); one: the
+// rotation's magnitude is 1.  All lanes of the warp take part.
 template <int D, bool ROTATED>
-__device__ __forceinline__ Codes4 encode_unit(const float* x, float inv, bool rotated, bool interleaved, const Partners<D>& with) {
+__device__ __forceinline__ Codes4 encode_unit(const float* x, float inv, bool rotated, bool one, bool interleaved, const Partners<D>& with) {
   float y[16];
   uint32_t key[2] = {0u, 0u};
 #pragma unroll
@@ -126,12 +125,10 @@ __device__ __forceinline__ Codes4 encode_unit(const float* x, float inv, bool ro
     y[k] = x[k] * inv;
     key[k / 8] = max(key[k / 8], __float_as_uint(y[k]) & 0x7fffffffu);
   }
-  // |x - exact| <= 3.2e-7 (|x| + |y|) over the rotated pair x, y: sine and cosine are off by 7.5e-8 of the unrotated pair's |p| + |q|, which is
-  // at most sqrt(2) times |x| + |y|; the products and the sum round by 2^-24 of |q| and of |x|, the magnitude by 2^-24 of both.
   float off[8], most = 0.f;
 #pragma unroll
   for (int i = 0; ROTATED && i < 8; ++i) {
-    const float o = (interleaved ? fabsf(y[2 * i]) + fabsf(y[2 * i + 1]) : fabsf(y[i]) + fabsf(y[8 + i])) * kRotationError;
+    const float o = interleaved ? rotation_error(y[2 * i], y[2 * i + 1], one) : rotation_error(y[i], y[8 + i], one);
     off[i] = rotated && o < INFINITY ? o : 0.f;
     most = fmaxf(most, off[i]);
   }
@@ -348,7 +345,7 @@ __device__ __forceinline__ void write_page(const AppendParams& a, const uint64_t
         Codes4 c;
 #pragma unroll 1
         for (bool again = false;; again = true) {
-          c = encode_unit<D, kTurned>(x, inv, rotate && !again, u.interleaved, with);
+          c = encode_unit<D, kTurned>(x, inv, rotate && !again, u.magnitude == 1.f, u.interleaved, with);
           if (!kTurned || again || !__any_sync(0xffffffffu, c.open != 0)) break;
           // what fp32 left open: those pairs once more, exactly
 #pragma unroll 1

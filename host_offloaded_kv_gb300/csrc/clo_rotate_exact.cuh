@@ -9,6 +9,16 @@
 
 namespace clo {
 
+// What an element of a pair that fp32 rotated to x, y may be off by, with what the quotient by a group's scale and the ends of the interval round; one:
+// the magnitude is 1.  Of the pair's length r = sqrt(x^2 + y^2): sine and cosine are off by 7.5e-8 of |p| + |q| <= sqrt(2) r (p, q: the unrotated pair
+// times the magnitude), the product of q and the sine rounds by 2^-24 of r at most, and so do the two products with the magnitude together.  Of the
+// element: the sum, the quotient and the interval's end round by 2^-24 each.  1.66e-7 r (2.26e-7 r) and 1.79e-7 of the larger element a, with
+// r <= a + b / 2 for the smaller one b.
+__host__ __device__ inline float rotation_error(float x, float y, bool one) {
+  const float a = fmaxf(fabsf(x), fabsf(y)), b = fminf(fabsf(x), fabsf(y));
+  return fmaf(a, one ? 3.46e-7f : 4.06e-7f, b * (one ? 0.83e-7f : 1.13e-7f));
+}
+
 // The upper half of a 128-bit product.
 __host__ __device__ inline int64_t mul_high(int64_t a, int64_t b) {
 #ifdef __CUDA_ARCH__

@@ -96,3 +96,41 @@ def test_page_scales_are_those_of_the_exact_rotation(clo, page, interleaved):
         done += 1
     got = cache.k_scales[:, 0].cpu().double()
     assert torch.equal(got, want), f"{int((got != want).sum())} of {trials} scales"
+
+
+@pytest.mark.parametrize("page", [16, 64])
+def test_codes_at_borders_are_those_of_the_exact_rotation(clo, page):
+    # A key within 2^-24 of the border between two codes, by the choice of the factor as above.  Pair 1 does not turn (its frequency is nearly zero):
+    # its first element is the group's largest and takes the page's scale and the group's far from their own borders.
+    trials, d, rot = 400, 64, 16
+    gen = torch.Generator().manual_seed(page)
+    cache = clo.PagedCache.create(trials, 1, page, d, kv_bits=4, group=16)
+    want, got_at = torch.zeros(trials, dtype=torch.float64), []
+    done = 0
+    while done < trials:
+        p, q = (float(x) for x in torch.randn(2, generator=gen).to(BF16))
+        pos = int(torch.randint(0, 2000, (1,), generator=gen))
+        x, y = p * math.cos(pos) - q * math.sin(pos), q * math.cos(pos) + p * math.sin(pos)
+        border = (0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0)[done % 7]
+        # group scale 1 and page scale 2^e: the key at border * 2^e, the largest element at about 6 * 2^e, the other one of the pair below it
+        if abs(x) < 0.01 or abs(y) * border >= 5.9 * abs(x):
+            continue
+        e = math.floor(math.log2(abs(x) / border)) + 1
+        magnitude = float(torch.tensor(border * 2.0 ** e / abs(x), dtype=torch.float32))
+        off = magnitude * abs(x) / (border * 2.0 ** e) - 1.0
+        if abs(off) < 1e-12:
+            continue
+        row = torch.zeros(1, 1, d, dtype=BF16)
+        row[0, 0, 0], row[0, 0, 8], row[0, 0, 1] = p, q, float(torch.tensor(6.0 * 2.0 ** e / magnitude).to(BF16))
+        row[0, 0, 32] = 2000.0 * 2.0 ** e  # not rotated: the page's largest, which makes its scale 2^e
+        plan = clo.clo_rope_plan_init(rot_dim=rot, theta=1e300, magnitude=magnitude)
+        cache.append(row.cuda(), torch.zeros_like(row).cuda(), i32([0, 1]), i32([1]), i32([[done]]), rope=plan, positions=torch.tensor([pos]).cuda())
+        lo = max(v for v in ref4.LEVELS.tolist() if v < border)
+        hi = min(v for v in ref4.LEVELS.tolist() if v > border)
+        want[done] = math.copysign(hi if off > 0 else lo, x) * 2.0 ** e
+        got_at.append(2.0 ** e)
+        done += 1
+    now = ref4.of_cache(cache)
+    scale = torch.tensor(got_at, dtype=torch.float64)
+    assert torch.equal(now.scale[0][:, 0], scale) and torch.equal(now.group[0][:, 0, 0, 0], torch.ones(trials, dtype=torch.float64))
+    assert torch.equal(now.code[0][:, 0, 0, 0] * scale, want)
