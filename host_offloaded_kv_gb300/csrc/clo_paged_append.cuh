@@ -165,9 +165,9 @@ __device__ __forceinline__ Codes4 encode_unit(const float* x, float inv, bool ro
     }
     code[v] = pack8_e2m1(lo);
     // a nibble for each element; halves: element k of either vector is of pair k; neighbours: elements 2 i, 2 i + 1 of vector v of pair 4 v + i
-    uint32_t d = ROTATED ? code[v] ^ pack8_e2m1(hi) : 0u;
-    if (d != 0 && s > 0.f && rotated) {  // (zeros differ in sign)
-      d = (d | d >> 1 | d >> 2 | d >> 3) & 0x11111111u;
+    const uint32_t top = ROTATED ? pack8_e2m1(hi) : code[v];
+    if (top != code[v] && rotated) {
+      const uint32_t d = codes_differ(&code[v], top);
 #pragma unroll
       for (int k = 0; k < 8; ++k) c.open |= (d >> (4 * k) & 1u) << (interleaved ? 4 * v + k / 2 : k);
     }

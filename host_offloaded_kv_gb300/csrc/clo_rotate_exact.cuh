@@ -19,6 +19,15 @@ __host__ __device__ inline float rotation_error(float x, float y, bool one) {
   return fmaf(a, one ? 3.46e-7f : 4.06e-7f, b * (one ? 0.83e-7f : 1.13e-7f));
 }
 
+// The elements whose 4-bit codes differ between the two ends of an interval, a bit per nibble (bit 4 k).  Zeros of either sign are one value; where
+// the ends have both, the code becomes that of a positive zero.
+__host__ __device__ inline uint32_t codes_differ(uint32_t* low, uint32_t high) {
+  const uint32_t d = *low ^ high, any = *low | high;
+  const uint32_t held = (any | any >> 1 | any >> 2) & 0x11111111u;  // not zero at both ends
+  *low &= ~((d & ~(held << 3)) & 0x88888888u);
+  return (d | d >> 1 | d >> 2 | d >> 3) & held;
+}
+
 // The upper half of a 128-bit product.
 __host__ __device__ inline int64_t mul_high(int64_t a, int64_t b) {
 #ifdef __CUDA_ARCH__

@@ -39,3 +39,26 @@ def test_error_of_a_rotated_element_counts_every_rounding(tmp_path):
             # sines, product with q, sums with the magnitude; then the sum, the quotient by the group's scale, an end of the interval
             need = (7.5e-8 * math.sqrt(2.0) + u + magnitude) * r + 3 * u * max(x, y)
             assert float(got[2 * i + k]) >= need * (1 + 1e-5), (x, y, k)  # (products of two of the errors: far below 1e-5 of one)
+
+
+def test_zeros_of_either_sign_are_one_code(tmp_path):
+    # every pair of codes in every place, between neighbours of which some differ
+    got = compiled(tmp_path, r'''
+int main() {
+  for (int k = 0; k < 8; ++k)
+    for (unsigned lo = 0; lo < 16; ++lo)
+      for (unsigned hi = 0; hi < 16; ++hi) {
+        const uint32_t rest = 0x1908a3f0u & ~(15u << 4 * k);
+        uint32_t low = rest | lo << 4 * k;
+        const uint32_t d = codes_differ(&low, rest | hi << 4 * k);
+        printf("%u %u %d ", d, low >> 4 * k & 15u, (low & ~(15u << 4 * k)) == rest);
+      }
+}
+''')
+    at = iter(map(int, got))
+    for k in range(8):
+        for lo in range(16):
+            for hi in range(16):
+                zeros = lo & 7 == 0 and hi & 7 == 0
+                want = 0 if lo == hi or zeros else 1 << 4 * k
+                assert (next(at), next(at), next(at)) == (want, 0 if zeros and lo != hi else lo, 1), (k, lo, hi)
