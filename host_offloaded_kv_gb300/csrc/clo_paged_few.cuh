@@ -2,6 +2,7 @@
 #pragma once
 
 #include <algorithm>
+#include <type_traits>
 
 #include "clo_paged_attend.cuh"
 
@@ -41,6 +42,14 @@ template <int D, int BITS, int NT>
 constexpr int kPerSm = BITS == 4 && !(D == 128 && NT == 2) && NT < 3 ? 3 : 2;
 template <int D, int BITS, int NT>
 constexpr int kWave = kPerSm<D, BITS, NT> * kSms;
+// Calls whose units stay whole have a block each, in as many waves as the residency makes.  Bounded to 168 registers, three blocks are faster where
+// they save a wave and slower where they do not, 8 kv heads, us (bf16, heads of 128, 4 rows; 12 rows; 8-bit pages, heads of 64, 12 rows):
+//   two blocks / three   45 sequences of 1200 tokens 46.7 / 36.9; 128 of 300 46.5 / 44.5; 39 of 300 13.9 / 9.2
+//                        64 of 1200 52.7 / 58.2; 64 of 1000 51.6 / 65.6; 64 of 300 15.0 / 16.5
+// Where two blocks leave the compiler below that count by itself (one fragment of rows over 8-bit pages or with heads of 64), three run anyway.
+template <int D, int BITS, int NT>
+constexpr bool kThirdBlock = BITS != 4 && (NT > 1 || (D == 128 && BITS == 16));
+constexpr bool third_block_pays(int64_t units) { return (units + 3 * kSms - 1) / (3 * kSms) < (units + 2 * kSms - 1) / (2 * kSms); }
 
 // 8-bit pages: weights up to 2^14 (fp16 then holds them down to 2^-38 of the largest) are divided by their page's V scale, which may be as
 // small as 1e-30, before they are summed.  The sums are kept 2^7 smaller, so that two million such weights stay in fp32's range; the
@@ -192,8 +201,8 @@ __device__ __forceinline__ FewShare few_share(const AttendParams& a, int tokens,
   return f;
 }
 
-template <int D, int BITS, int NT>
-__global__ void __launch_bounds__(kThreads, kPerSm<D, BITS, NT>) k_attend_few(const AttendParams a, const __grid_constant__ PageMaps maps) {
+template <int D, int BITS, int NT, int PER_SM>
+__global__ void __launch_bounds__(kThreads, PER_SM) k_attend_few(const AttendParams a, const __grid_constant__ PageMaps maps) {
   using T = Tile<D, BITS>;
   constexpr int TOK = T::kTokens, KM = T::kM, KD = D / 16, ROWS = 8 * NT;
   constexpr float kOff = BITS == 16 ? 0.f : 14.f, kDown = BITS == 16 ? 1.f : kSumDown;
@@ -828,14 +837,20 @@ cudaError_t few_rows(AttendParams a, int64_t* bytes, cudaStream_t st) {
   if (need == 0 || need > a.part_bytes) a.part = nullptr;
   PageMaps maps;
   if (make_page_maps(a.c, D, BITS, std::min(a.c.page_size, T::kTokens), &maps)) return cudaErrorInvalidValue;
-  auto* f = k_attend_few<D, BITS, NT>;
-  static std::atomic<uint64_t> prepared{0};
-  cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(f), T::kSmem, &prepared);
-  if (e != cudaSuccess) return e;
-  f<<<a.part ? dim3(kWave<D, BITS, NT>) : dim3(a.c.batch, a.c.n_kv_heads), kThreads, T::kSmem, st>>>(a, maps);
-  e = cudaGetLastError();
-  if (e != cudaSuccess || !a.part) return e;
   const int64_t units = (int64_t)a.c.batch * a.c.n_kv_heads;
+  auto run = [&](auto per_sm) {
+    auto* f = k_attend_few<D, BITS, NT, decltype(per_sm)::value>;
+    static std::atomic<uint64_t> prepared{0};
+    const cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(f), T::kSmem, &prepared);
+    if (e != cudaSuccess) return e;
+    f<<<a.part ? dim3(kWave<D, BITS, NT>) : dim3(a.c.batch, a.c.n_kv_heads), kThreads, T::kSmem, st>>>(a, maps);
+    return cudaGetLastError();
+  };
+  if constexpr (kThirdBlock<D, BITS, NT>) {
+    if (!a.part && third_block_pays(units)) return run(std::integral_constant<int, 3>{});
+  }
+  const cudaError_t e = run(std::integral_constant<int, kPerSm<D, BITS, NT>>{});
+  if (e != cudaSuccess || !a.part) return e;
   return launch_after(k_attend_join<D, BITS, NT>, dim3(std::min<int64_t>(units, kWave<D, BITS, NT>), a.part_rows), kJoinThreads, st, a);
 }
 
