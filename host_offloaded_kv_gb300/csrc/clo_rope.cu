@@ -233,8 +233,10 @@ const char* paged_params(const clo_paged_cache* c, const clo_paged_batch* b, Pag
     if ((reinterpret_cast<uintptr_t>(b->q_starts) | reinterpret_cast<uintptr_t>(b->kv_lens) | reinterpret_cast<uintptr_t>(b->block_table)) & 3u)
       return "the batch's arrays must be 4-byte aligned";
   }
-  p->side[0] = PagedSide{static_cast<char*>(c->k_pages), c->k_scales, static_cast<uint8_t*>(c->k_group_scales), c->k_stride_page, c->k_stride_head, c->k_stride_token};
-  p->side[1] = PagedSide{static_cast<char*>(c->v_pages), c->v_scales, static_cast<uint8_t*>(c->v_group_scales), c->v_stride_page, c->v_stride_head, c->v_stride_token};
+  // (callers of other pages may have been compiled before the struct had these fields)
+  void* const groups[2] = {c->kv_bits == 4 ? c->k_group_scales : nullptr, c->kv_bits == 4 ? c->v_group_scales : nullptr};
+  p->side[0] = PagedSide{static_cast<char*>(c->k_pages), c->k_scales, static_cast<uint8_t*>(groups[0]), c->k_stride_page, c->k_stride_head, c->k_stride_token};
+  p->side[1] = PagedSide{static_cast<char*>(c->v_pages), c->v_scales, static_cast<uint8_t*>(groups[1]), c->v_stride_page, c->v_stride_head, c->v_stride_token};
   p->q_starts = b->q_starts;
   p->kv_lens = b->kv_lens;
   p->table = b->block_table;

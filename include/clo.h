@@ -29,6 +29,9 @@
  *   - Device pointers passed in stay owned by the caller; the library owns all
  *     memory it allocates (pinned host pool, HBM buffers) and frees it in
  *     clo_destroy().
+ *   - Structs grow at their ends (clo_rope_config and clo_rope_plan with several
+ *     axes, clo_paged_cache with 4-bit pages): callers are compiled against the
+ *     header of the library that they load.
  *   - Device-side failures (a ready-flag wait that ran out of time, an internal
  *     bounds check) are latched in a device error word and reported by the next
  *     call that synchronises with the stream: clo_sync(), clo_stats(), a
