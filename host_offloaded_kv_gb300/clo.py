@@ -472,7 +472,8 @@ class PagedCache:
     def create(cls, n_pages: int, n_kv_heads: int, page_size: int, head_dim: int, kv_bits: int = 16, device=None, group=None):
         """A cache of new pages (their contents are undefined until they are appended to).
 
-        group: the elements that share a scale, to be stated with kv_bits 4 (16 is what the calls read and write)."""
+        group: the elements that share a scale, to be stated with kv_bits 4 (16 is what the calls read and write; a caller
+        who means groups of another size, or codes without them, is refused)."""
         if kv_bits not in (16, 8, 4):
             raise ValueError("kv_bits must be 16, 8 or 4")
         if (group != 16) if kv_bits == 4 else (group is not None):

@@ -1,10 +1,11 @@
 // Paged append with the rotation on the way: the kernel and its launch, instantiated by the pages' type.  One pass over the rows, bounded
 // by HBM traffic (large calls) or by one launch and two or three dependent loads (single-token steps).
 //
-// Measured with queries, 32 over 8 heads: 11,000 tokens, bf16 pages 52 us, 5.2 TB/s, 8-bit pages 54 us, 4.6 TB/s (registers hold two
-// blocks to an SM: a page's rows stay in them until its scale is known); 64 single tokens, in a graph, 3.8 and 4.5 us.
-// 4-bit pages, 10,800 tokens at positions on three axes: 96 us with queries, 75 without, 41 without rotation (8-bit pages 74, 39, 37); 64 single
-// tokens 8.2 us for 6.3, and 8 us more where a pair is left open (rotate_exactly), one call in three or four.
+// Measured with queries, 32 over 8 heads: 11,000 tokens, bf16 pages 52 us, 5.2 TB/s, 8-bit pages 53 us, 4.6 TB/s (registers hold two
+// blocks to an SM: a page's rows stay in them until its scale is known); 64 single tokens, in a graph, 3.9 and 4.5 us.
+// One sequence of 10,800 tokens at positions on three axes, in a graph, with queries / without / without rotation, us: bf16 55.6 / 31.7 / 20.6, 8-bit
+// pages 56.2 / 33.3 / 21.2, 4-bit pages 73.6 / 59.4 / 33.2, where instructions bound it and 128 registers hold not all: 100 to 172 bytes a thread spill.
+// 64 single tokens of 4-bit pages 5.8 us, and 8 us more where a pair is left open (rotate_exactly), one call in three or four.
 #pragma once
 
 #include <type_traits>
@@ -328,7 +329,7 @@ __device__ __forceinline__ void write_page(const AppendParams& a, const uint64_t
   if constexpr (BITS == 4) {
     const Partners<D> with = partners_of<D>(rotate && !u.interleaved, a.rope.plan.rot_dim, lane);
     uint8_t* const groups = sd.groups + groups_at<D>(p, page, head, 0);
-    // One copy of the code for all units: several did not fit the instruction cache (11,000 tokens with queries 144 us for 96).
+    // One copy of the code for all units: several did not fit the instruction cache (13,600 tokens with queries 144 us for 96).
     auto encode_rows = [&](auto turned) {
       constexpr bool kTurned = decltype(turned)::value;
 #pragma unroll 1

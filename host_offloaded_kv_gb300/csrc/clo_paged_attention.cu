@@ -90,6 +90,9 @@ static const char* attend_params(const clo_paged_cache* cache, const clo_paged_b
 
 // Up to this many rows per kv head go to the decode kernel, more to the tcgen05 kernel.  (32 rows there, four fragments wide:
 // 193 us for 132 at 16 sequences of 8 tokens by 4 heads over 8000 to 16,000 tokens of bf16, 178 for 123 with 8-bit pages.)
+// 4-bit pages, decode kernel / tcgen05 kernel, us: 24 rows of 64, 16 sequences to 16,000 tokens 48.8 / 78.0, 4 of 1000 13.0 / 17.2, 32 of 2000
+// 24.1 / 53.7, one of 100,000 34.9 / 62.5.  Wider rows gain there too and are not taken yet: 24 rows of 128 72.6 / 97.7 (with spills), 15.7 / 20.5,
+// 40.1 / 67.3, 54.9 / 78.1; 32 rows of 64 59.3 / 78.3, 14.8 / 17.1, 29.2 / 53.8, 42.0 / 63.0.
 constexpr int few_rows_of(const clo_paged_cache* c) { return c->kv_bits == 4 && c->head_dim == 64 ? 24 : 16; }
 
 extern "C" CLO_API clo_status clo_paged_attention_workspace(const clo_paged_cache* cache, const clo_paged_batch* batch, int32_t n_q_heads,

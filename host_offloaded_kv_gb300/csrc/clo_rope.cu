@@ -1,9 +1,9 @@
 // Rotary positions (clo_rope) and the read-back of pages (clo_paged_read): one pass over the rows each, bounded by HBM
 // traffic (large calls) or by one launch and two or three dependent loads (single-token steps).
 //
-// Measured: 8192 tokens of 32 heads of 128, on one axis or three, 24.1 us, 5.6 TB/s (82 % of a copy's rate); 30,000 tokens 74 us, 97 %; one
-// token 2.2 us in a graph.  Read-back of 8 x 8192 tokens: bf16 82 us, 6.5 TB/s, 8-bit pages 70 us, 5.8 TB/s; of 10,800 tokens of 4-bit pages
-// 18.5 us, 3.0 TB/s.
+// Measured: 8192 tokens of 32 heads of 128, on one axis or three, 23.1 to 24.4 us, 5.5 to 5.8 TB/s (81 to 86 % of a copy's rate); 30,000 tokens
+// 74 us, 97 %; one token 2.0 us in a graph.  Read-back of 8 x 8192 tokens: bf16 82 us, 6.5 TB/s, 8-bit pages 70 us, 5.8 TB/s; of 13,751 tokens of
+// 4-bit pages 18.5 us, 3.9 TB/s.
 #include <cuda_runtime.h>
 
 #include <algorithm>
